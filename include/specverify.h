@@ -8,7 +8,12 @@
  *   - spec_verify_greedy: the argmax-match variant;
  *   - spec_verify_tree_greedy: greedy verification of a draft tree;
  *   - kv_commit_rollback: commit of the accepted provisional KV slots into a
- *     paged cache and release of the provisional blocks.
+ *     paged cache and release of the provisional blocks;
+ * and what a verifier with an 8-bit paged cache needs around that step:
+ *   - kv_q8_append, kv_q8_attention: the cache in e4m3 with a scale for each
+ *     block of tokens and head, and the attention of the provisional tokens;
+ *   - kv_reserve, kv_fork, kv_free: blocks for new tokens, rows that share
+ *     their prefix with another row, and their release.
  *
  * Sources (page title, section):
  *   [L] aiengineeringfromscratch.com, "Speculative decoding and EAGLE-3":
@@ -95,7 +100,10 @@ extern "C" {
                                     arrival of batch row b is withheld) and
                                     SPECVERIFY_IDLE_NS (the producers' idle limit, default
                                     2 s), read at every verify launch */
-#define SPEC_DERR_BAD_SLOT 128   /* kv: a slot_map entry of a kept position outside [0, K] */
+#define SPEC_DERR_BAD_SLOT 128   /* kv: a slot_map entry of a kept position outside [0, K], or a
+                                    row of kv_fork / kv_free out of range or listed twice */
+#define SPEC_DERR_VALUE 256      /* kv_q8_append: a NaN (stored as 0) or an infinity (stored as the
+                                    largest finite number) in k or v */
 
 /* ---- per-row diagnostic bits written to row_info[b] (optional) ---- */
 #define SPEC_ROW_ACCEPT_REFINED 1 /* an accept test fell inside the fp32 error bound and was
@@ -365,6 +373,122 @@ int kv_commit_inplace(int32_t* block_table, int32_t* seq_lens, const int32_t* nu
 int kv_evict_provisional(int32_t* block_table, int32_t* seq_lens, int num_blocks,
                          int block_size, int B, int K, int max_blocks, int32_t* free_stack,
                          int32_t* free_top, int32_t* status, void* stream);
+
+/*
+ * kv_q8_append - writes tokens to the 8-bit paged cache of one layer.
+ *
+ *   k, v         [B, T, num_kv_heads, head_dim] dtype (SPEC_BF16 or SPEC_F32), 16-byte aligned
+ *   kv_pool      [num_blocks][num_layers][2][num_kv_heads][block_size][head_dim] e4m3 codes
+ *                (plane 0 keys, plane 1 values), 16-byte aligned; head_dim a multiple of 16
+ *   kv_scales    [num_blocks][num_layers][2][num_kv_heads] float: a number is code * scale
+ *   block_table  [B, max_blocks] int32; the entries that hold positions
+ *                L_b .. L_b + n_b - 1 must be valid (kv_reserve)
+ *   seq_lens     [B] int32: L_b, not changed (kv_commit_inplace sets the new length)
+ *   num_new      optional [B] int32: n_b in [0, T]; null: T
+ *   layer        in [0, num_layers)
+ * Token t of row b goes to position L_b + t. For each block that the new tokens
+ * touch, each plane and head: s_new = 2^e with the smallest e >= -100 such that the
+ * largest magnitude of the block's new tokens is <= 448 * 2^e; the block's scale
+ * becomes s_new, or max(s_new, its old scale) when it keeps tokens before L_b; new
+ * codes are e4m3(x / scale), to nearest even; kept codes are rewritten for a scale
+ * that grew. What lay at or after L_b in a block is dropped, scale included when
+ * nothing lies before L_b, so rejected tokens leave no trace in a block of their own.
+ * Appending the same tokens again gives the same bytes. Blocks are written by one
+ * holder only: kv_fork copies the block that a row will write to.
+ * Device errors (in *err_flag, when given): SPEC_DERR_BAD_LENGTH (a negative length,
+ * n_b outside [0, T], beyond max_blocks: that row is not written),
+ * SPEC_DERR_BAD_BLOCK (an id out of range: that block is not written), SPEC_DERR_VALUE.
+ */
+int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* kv_scales,
+                 const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
+                 int num_blocks, int num_layers, int layer, int num_kv_heads, int head_dim,
+                 int block_size, int B, int T, int max_blocks, void* stream, int32_t* err_flag);
+
+/*
+ * kv_q8_attention - attention of every row's newest tokens over its 8-bit paged
+ * cache: a verification step's T = K + 1 provisional tokens, or T = 1.
+ *
+ *   q, out       [B, T, num_q_heads, head_dim] dtype, 16-byte aligned; query t of row b
+ *                is position L_b + t. Query head i reads kv head i / (num_q_heads /
+ *                num_kv_heads). 1 <= T <= 32, head_dim a multiple of 16 up to 256
+ *   kv_pool, kv_scales, block_table, num_new, layer: as kv_q8_append, which must have
+ *                written the new tokens; seq_lens L_b counts the tokens before them
+ *   tree_mask    optional [B, T] uint32, the ancestor-only mask of a draft tree ([G]): bit s
+ *                of tree_mask[b][t] lets query t see position L_b + s (its own slot included);
+ *                positions before L_b are seen by all. Null: query t sees j <= L_b + t
+ *   window       0, or w >= 1: query t sees only j > L_b + t - w, and the first `sinks`
+ *                positions. Not together with tree_mask (SPEC_ENOTSUP)
+ *   softmax_scale  > 0: out = sum_j softmax_j(softmax_scale * q . k_j) v_j over the keys seen
+ *   workspace    kv_q8_attention_workspace_bytes bytes, 256-byte aligned, no initialisation;
+ *                calls that share one must be ordered on the device
+ * A query that sees no key gets zeros, as do queries t >= n_b. A query that sees a
+ * token whose block id is out of range, and every query of a row whose lengths are
+ * invalid, gets NaN, and the bit is set in *err_flag. Scores, maxima and sums are
+ * fp32. With bf16 queries, head_dim 64 or 128 and blocks of 8, 16, 32, 64 tokens or a
+ * multiple of 128, the products run on the tensor cores: queries enter as two e4m3
+ * terms (exact for numbers down to 2^-10 of their row's largest), probabilities as
+ * three e5m2 terms (9 bits). Everything else runs in fp32.
+ */
+int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
+                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
+                    const uint32_t* tree_mask, void* out, float softmax_scale, int window,
+                    int sinks, int num_blocks, int num_layers, int layer, int num_q_heads,
+                    int num_kv_heads, int head_dim, int block_size, int B, int T, int max_blocks,
+                    void* workspace, size_t workspace_bytes, void* stream, int32_t* err_flag);
+
+/* kv_q8_attention_workspace_bytes - size of the workspace of kv_q8_attention (it does
+ * not depend on B or on the lengths); 0 for arguments that the call rejects. */
+size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads, int head_dim);
+
+/*
+ * kv_reserve - blocks for new tokens: entries ceil(L_b / bs) .. ceil((L_b + n_b) / bs) - 1
+ * of every row that are -1 take ids from the top of the free stack (rows ascending,
+ * entries ascending); entries that hold a block keep it. seq_lens is not changed.
+ * The layout is kv_commit_inplace's, which frees what a step leaves unused.
+ *   num_new optional [B] int32; null: n for every row. status REQUIRED [1] int32: 0, or the
+ *   bits that stopped the call (then nothing changed): SPEC_DERR_BAD_LENGTH (negative,
+ *   or beyond max_blocks), SPEC_DERR_BAD_BLOCK (an entry or a popped id out of range),
+ *   SPEC_DERR_NO_SPACE. B <= 8192 (SPEC_ENOTSUP).
+ */
+int kv_reserve(int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new, int n,
+               int num_blocks, int block_size, int B, int max_blocks, const int32_t* free_stack,
+               int32_t* free_top, int32_t* status, void* stream);
+
+/*
+ * kv_fork - rows that continue another row's committed tokens.
+ *
+ *   src_rows, dst_rows [n] int32: pair i makes row dst_rows[i] (length 0, entries
+ *                -1) a copy of row src_rows[i]. Parents may repeat; children must be
+ *                distinct and no parent of the call
+ *   extra_refs   [num_blocks] int32: holders of each block beyond the first; 0 for blocks
+ *                that were never shared, so the commit calls need not know it
+ *   kv_pool      planes of block_size * token_bytes bytes, `planes` of them per block:
+ *                num_layers * 2 * num_kv_heads planes of head_dim bytes a token for the 8-bit
+ *                cache, num_layers * 2 planes of num_kv_heads * head_dim * kv_elem_bytes for
+ *                kv_commit_rollback's. token_bytes a multiple of 16
+ *   kv_scales    optional [num_blocks][planes] float, copied with the block
+ * Full blocks are shared (extra_refs + 1); a partly filled tail block is copied, its
+ * L % bs tokens only, into a block from the top of the free stack (in the order of
+ * the pairs). Provisional blocks past L are not forked. status as in kv_reserve, all
+ * or nothing; SPEC_DERR_BAD_SLOT: a row out of range, a child listed twice or
+ * listed as a parent; SPEC_DERR_BAD_LENGTH: a child whose length is not 0.
+ * n <= 8192.
+ */
+int kv_fork(int32_t* block_table, int32_t* seq_lens, int32_t* extra_refs, const int32_t* src_rows,
+            const int32_t* dst_rows, int n, void* kv_pool, int planes, int token_bytes,
+            float* kv_scales, int num_blocks, int block_size, int B, int max_blocks,
+            int32_t* free_stack, int32_t* free_top, int32_t* status, void* stream);
+
+/*
+ * kv_free - releases rows: every block of the n listed rows loses one holder, blocks
+ * without any are pushed on the free stack (in the order in which the call first
+ * lists them), the rows' entries become -1 and their lengths 0. status as in
+ * kv_reserve, all or nothing; SPEC_DERR_BAD_BLOCK: an id out of range, a block listed
+ * more often than it is held, or a stack that would overflow. n <= 8192.
+ */
+int kv_free(int32_t* block_table, int32_t* seq_lens, int32_t* extra_refs, const int32_t* rows,
+            int n, int num_blocks, int B, int max_blocks, int32_t* free_stack, int32_t* free_top,
+            int32_t* status, void* stream);
 
 /*
  * spec_selftest_ex2 - diagnostic: the maximum relative error of the hardware

@@ -10,6 +10,9 @@ The entry points carry the C names:
   spec_verify_greedy(...)   argmax-match verification
   spec_verify_tree_greedy(...)  argmax-match verification of a draft tree
   kv_commit_rollback(...)   commit accepted provisional KV slots, free provisional blocks
+  kv_q8_append(...)         tokens into the 8-bit paged cache (e4m3, a scale per block and head)
+  kv_q8_attention(...)      attention of the provisional tokens over that cache
+  kv_reserve, kv_fork, kv_free   blocks for new tokens, shared prefixes, release
 See include/specverify.h for layouts, ownership and error behaviour.
 """
 from __future__ import annotations
@@ -26,6 +29,7 @@ SPEC_DERR_TOKEN, SPEC_DERR_LOGITS = 1, 2
 SPEC_DERR_BAD_ACCEPT, SPEC_DERR_BAD_LENGTH, SPEC_DERR_NO_SPACE, SPEC_DERR_BAD_BLOCK = 4, 8, 16, 32
 SPEC_DERR_TIMEOUT = 64
 SPEC_DERR_BAD_SLOT = 128
+SPEC_DERR_VALUE = 256
 SPEC_ROW_ACCEPT_REFINED, SPEC_ROW_SAMPLE_REFINED = 1, 2
 SPEC_ROW_UNCERTIFIED, SPEC_ROW_ZERO_RESIDUAL = 4, 8
 
@@ -33,7 +37,8 @@ EXPORTED = ("spec_verify_sample", "spec_verify_greedy", "spec_verify_workspace_b
             "kv_commit_rollback", "spec_selftest_ex2", "spec_status_string", "spec_version",
             "spec_verify_greedy_noalloc", "spec_verify_greedy_noalloc_max_bytes",
             "kv_commit_inplace", "kv_evict_provisional", "spec_verify_tree_greedy",
-            "spec_filter_thresholds")
+            "spec_filter_thresholds", "kv_q8_append", "kv_q8_attention",
+            "kv_q8_attention_workspace_bytes", "kv_reserve", "kv_fork", "kv_free")
 
 _lib = None
 
@@ -79,6 +84,19 @@ def lib() -> ctypes.CDLL:
         L.kv_commit_rollback.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P, P, P,
                                          P]
         L.kv_commit_rollback.restype = I
+        L.kv_q8_append.argtypes = [P, P, I, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, P]
+        L.kv_q8_append.restype = I
+        L.kv_q8_attention.argtypes = [P, I, P, P, P, P, P, P, P, F, I, I, I, I, I, I, I, I, I, I,
+                                      I, I, P, Z, P, P]
+        L.kv_q8_attention.restype = I
+        L.kv_q8_attention_workspace_bytes.argtypes = [I, I, I, I]
+        L.kv_q8_attention_workspace_bytes.restype = Z
+        L.kv_reserve.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P]
+        L.kv_reserve.restype = I
+        L.kv_fork.argtypes = [P, P, P, P, P, I, P, I, I, P, I, I, I, I, P, P, P, P]
+        L.kv_fork.restype = I
+        L.kv_free.argtypes = [P, P, P, P, I, I, I, I, P, P, P, P]
+        L.kv_free.restype = I
         L.spec_selftest_ex2.argtypes = [F, F, P, P]
         L.spec_selftest_ex2.restype = I
         L.spec_status_string.argtypes = [I]
@@ -353,6 +371,190 @@ def kv_commit_rollback(block_table, seq_lens, num_accepted, prov_blocks, kv_pool
         _ptr(free_top), _ptr(status), _stream(stream), _ptr(slot_map))
     if st != SPEC_OK:
         raise SpecError("kv_commit_rollback", st)
+
+
+def _q8_pool(kv_pool, kv_scales):
+    """Checks the 8-bit pool and its scales; returns the pool's shape."""
+    import torch
+    _check(kv_pool, "kv_pool", 6)
+    _check(kv_scales, "kv_scales", 4, torch.float32)
+    if kv_pool.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"kv_pool must be float8_e4m3fn (or its uint8 bytes), got {kv_pool.dtype}")
+    if kv_pool.shape[2] != 2 or kv_scales.shape != kv_pool.shape[:4]:
+        raise ValueError("kv_pool must be [num_blocks, layers, 2, kv_heads, block_size, head_dim] "
+                         "and kv_scales [num_blocks, layers, 2, kv_heads]")
+    return kv_pool.shape
+
+
+def _rows(B, **named):
+    """Checks optional int32 [B] tensors."""
+    import torch
+    for name, t in named.items():
+        if t is not None:
+            _check(t, name, 1, torch.int32)
+            if t.shape[0] != B:
+                raise ValueError(f"{name} must have {B} entries, got {t.shape[0]}")
+
+
+def _one_word(**named):
+    import torch
+    for name, t in named.items():
+        if t is not None:
+            _check(t, name, 1, torch.int32)
+            if t.shape[0] < 1:
+                raise ValueError(f"{name} must have an entry")
+
+
+def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int = 0,
+                 num_new=None, stream=None, err_flag=None) -> None:
+    """Writes k, v [B, T, kv_heads, head_dim] (bf16 or fp32) to positions seq_lens[b] ... of the
+    8-bit cache's `layer`: kv_pool [num_blocks, layers, 2, kv_heads, block_size, head_dim]
+    float8_e4m3fn, kv_scales [num_blocks, layers, 2, kv_heads]. num_new: optional int32 [B]."""
+    import torch
+    NB, NL, _, H, bs, D = _q8_pool(kv_pool, kv_scales)
+    _check(k, "k", 4)
+    _check(v, "v", 4, k.dtype)
+    _check(block_table, "block_table", 2, torch.int32)
+    B, T, kh, kd = k.shape
+    if v.shape != k.shape or (kh, kd) != (H, D) or block_table.shape[0] != B:
+        raise ValueError(f"k and v must be [B, T, {H}, {D}] and block_table [B, max_blocks]")
+    _rows(B, seq_lens=seq_lens, num_new=num_new)
+    _one_word(err_flag=err_flag)
+    st = lib().kv_q8_append(
+        _ptr(k), _ptr(v), _dtype_code(k), _ptr(kv_pool), _ptr(kv_scales), _ptr(block_table),
+        _ptr(seq_lens), _ptr(num_new), NB, NL, layer, H, D, bs, B, T, block_table.shape[1],
+        _stream(stream), _ptr(err_flag))
+    if st != SPEC_OK:
+        raise SpecError("kv_q8_append", st)
+
+
+def kv_q8_attention_workspace_bytes(T: int, num_q_heads: int, num_kv_heads: int,
+                                    head_dim: int) -> int:
+    """Device workspace bytes of kv_q8_attention (0: the call would be rejected)."""
+    return int(lib().kv_q8_attention_workspace_bytes(T, num_q_heads, num_kv_heads, head_dim))
+
+
+_attn_workspaces = {}
+
+
+def _attn_workspace(need, device, stream):
+    """A cached workspace of the attention, one per device and stream: calls on one stream are
+    ordered, calls on two may overlap."""
+    import torch
+    key = (device, stream.cuda_stream)
+    ws = _attn_workspaces.get(key)
+    if ws is None or ws.numel() < need + 256:
+        if ws is not None:
+            ws.record_stream(stream)  # its last call may still be running
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
+        _attn_workspaces[key] = ws
+    return ws
+
+
+def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer: int = 0,
+                    softmax_scale: float | None = None, window: int = 0, sinks: int = 0,
+                    num_new=None, tree_mask=None, workspace=None, stream=None,
+                    err_flag=None) -> None:
+    """Attention of q [B, T, q_heads, head_dim] (positions seq_lens[b] + t) over the 8-bit cache
+    (layout as kv_q8_append) into out, same shape and dtype (bf16 or fp32). softmax_scale defaults
+    to head_dim ** -0.5; window / sinks: sliding window and always-visible first positions;
+    tree_mask: optional int32 [B, T], bit s of entry t lets query t see position seq_lens[b] + s."""
+    import torch
+    NB, NL, _, H, bs, D = _q8_pool(kv_pool, kv_scales)
+    _check(q, "q", 4)
+    _check(out, "out", 4, q.dtype)
+    _check(block_table, "block_table", 2, torch.int32)
+    B, T, Hq, qd = q.shape
+    if out.shape != q.shape or qd != D or block_table.shape[0] != B:
+        raise ValueError(f"q and out must be [B, T, q_heads, {D}] and block_table [B, max_blocks]")
+    _rows(B, seq_lens=seq_lens, num_new=num_new)
+    _one_word(err_flag=err_flag)
+    if tree_mask is not None:
+        _check(tree_mask, "tree_mask", 2, torch.int32)
+        if tuple(tree_mask.shape) != (B, T):
+            raise ValueError(f"tree_mask must be [{B}, {T}], got {tuple(tree_mask.shape)}")
+    if workspace is None:
+        need = kv_q8_attention_workspace_bytes(T, Hq, H, D)
+        # an unsupported shape: the library call itself reports why
+        stream = stream or torch.cuda.current_stream()
+        workspace = _attn_workspace(need, q.device, stream) if need else None
+    if workspace is None:
+        wsp, wsn = ctypes.c_void_p(0), 0
+    else:
+        off = (-workspace.data_ptr()) % 256
+        wsp, wsn = ctypes.c_void_p(workspace.data_ptr() + off), max(0, workspace.numel() - off)
+    st = lib().kv_q8_attention(
+        _ptr(q), _dtype_code(q), _ptr(kv_pool), _ptr(kv_scales), _ptr(block_table),
+        _ptr(seq_lens), _ptr(num_new), _ptr(tree_mask), _ptr(out),
+        D ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, NB, NL, layer, Hq,
+        H, D, bs, B, T, block_table.shape[1], wsp, wsn, _stream(stream), _ptr(err_flag))
+    if st != SPEC_OK:
+        raise SpecError("kv_q8_attention", st)
+
+
+def kv_reserve(block_table, seq_lens, free_stack, free_top, status, *, n: int, block_size: int,
+               num_blocks: int, num_new=None, stream=None) -> None:
+    """Blocks for n (or num_new[b]) tokens past seq_lens[b]; status receives 0 or error bits."""
+    import torch
+    _check(block_table, "block_table", 2, torch.int32)
+    B, MB = block_table.shape
+    _rows(B, seq_lens=seq_lens, num_new=num_new)
+    _rows(num_blocks, free_stack=free_stack)
+    _one_word(free_top=free_top, status=status)
+    st = lib().kv_reserve(_ptr(block_table), _ptr(seq_lens), _ptr(num_new), n, num_blocks,
+                          block_size, B, MB, _ptr(free_stack), _ptr(free_top), _ptr(status),
+                          _stream(stream))
+    if st != SPEC_OK:
+        raise SpecError("kv_reserve", st)
+
+
+def kv_fork(block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, free_stack, free_top,
+            status, *, block_size: int, kv_scales=None, stream=None) -> None:
+    """Rows dst_rows[i] become copies of rows src_rows[i]: full blocks shared, tail blocks copied.
+    kv_pool: the 8-bit pool with kv_scales, or kv_commit_rollback's [num_blocks, layers, 2,
+    block_size, kv_heads, head_dim] pool without."""
+    import torch
+    _check(block_table, "block_table", 2, torch.int32)
+    B, MB = block_table.shape
+    _rows(B, seq_lens=seq_lens)
+    if kv_scales is not None:
+        NB, NL, _, H, bs, D = _q8_pool(kv_pool, kv_scales)
+        planes, token = NL * 2 * H, D
+    else:
+        _check(kv_pool, "kv_pool", 6)
+        NB, NL, two, bs, H, D = kv_pool.shape
+        if two != 2:
+            raise ValueError("kv_pool must be [num_blocks, layers, 2, block_size, heads, head_dim]")
+        planes, token = NL * 2, H * D * kv_pool.element_size()
+    if bs != block_size:
+        raise ValueError(f"kv_pool holds blocks of {bs} tokens, not {block_size}")
+    _check(src_rows, "src_rows", 1, torch.int32)
+    _rows(src_rows.shape[0], dst_rows=dst_rows)
+    _rows(NB, extra_refs=extra_refs, free_stack=free_stack)
+    _one_word(free_top=free_top, status=status)
+    st = lib().kv_fork(_ptr(block_table), _ptr(seq_lens), _ptr(extra_refs), _ptr(src_rows),
+                       _ptr(dst_rows), src_rows.shape[0], _ptr(kv_pool), planes, token,
+                       _ptr(kv_scales), NB, block_size, B, MB, _ptr(free_stack), _ptr(free_top),
+                       _ptr(status), _stream(stream))
+    if st != SPEC_OK:
+        raise SpecError("kv_fork", st)
+
+
+def kv_free(block_table, seq_lens, extra_refs, rows, free_stack, free_top, status, *,
+            num_blocks: int, stream=None) -> None:
+    """Releases the listed rows; blocks that no other row holds go back on the free stack."""
+    import torch
+    _check(block_table, "block_table", 2, torch.int32)
+    B, MB = block_table.shape
+    _rows(B, seq_lens=seq_lens)
+    _check(rows, "rows", 1, torch.int32)
+    _rows(num_blocks, extra_refs=extra_refs, free_stack=free_stack)
+    _one_word(free_top=free_top, status=status)
+    st = lib().kv_free(_ptr(block_table), _ptr(seq_lens), _ptr(extra_refs), _ptr(rows),
+                       rows.shape[0], num_blocks, B, MB, _ptr(free_stack), _ptr(free_top),
+                       _ptr(status), _stream(stream))
+    if st != SPEC_OK:
+        raise SpecError("kv_free", st)
 
 
 def spec_selftest_ex2(lo: float, hi: float, *, stream=None) -> float:

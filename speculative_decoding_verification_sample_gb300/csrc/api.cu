@@ -180,4 +180,120 @@ int kv_evict_provisional(int32_t* block_table, int32_t* seq_lens, int num_blocks
                      free_stack, free_top, status, stream);
 }
 
+// Positions of a row fit 2^30, so that sums of a few of them fit an int.
+static bool bad_table(int num_blocks, int block_size, int B, int max_blocks) {
+  return num_blocks < 1 || block_size < 1 || B < 1 || max_blocks < 1 ||
+         int64_t(max_blocks) * block_size > (int64_t(1) << 30) ||
+         int64_t(B) * max_blocks > INT32_MAX / 2;
+}
+
+constexpr int kMaxPageRows = 8192;  // rows or pairs of one call of the block operators
+
+int kv_reserve(int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new, int n,
+               int num_blocks, int block_size, int B, int max_blocks, const int32_t* free_stack,
+               int32_t* free_top, int32_t* status, void* stream) {
+  if (!block_table || !seq_lens || !free_stack || !free_top || !status) return SPEC_EINVAL;
+  if (bad_table(num_blocks, block_size, B, max_blocks) || (!num_new && n < 0)) return SPEC_EINVAL;
+  if (B > kMaxPageRows) return SPEC_ENOTSUP;
+  sv::KvReserveLaunch k{block_table, seq_lens, num_new, n, num_blocks, block_size, B, max_blocks,
+                        free_stack, free_top, status, stream};
+  return sv::launch_kv_reserve(k);
+}
+
+int kv_fork(int32_t* block_table, int32_t* seq_lens, int32_t* extra_refs, const int32_t* src_rows,
+            const int32_t* dst_rows, int n, void* kv_pool, int planes, int token_bytes,
+            float* kv_scales, int num_blocks, int block_size, int B, int max_blocks,
+            int32_t* free_stack, int32_t* free_top, int32_t* status, void* stream) {
+  if (!block_table || !seq_lens || !extra_refs || !src_rows || !dst_rows || !kv_pool ||
+      !free_stack || !free_top || !status)
+    return SPEC_EINVAL;
+  if (bad_table(num_blocks, block_size, B, max_blocks) || n < 1 || planes < 1 || token_bytes < 1)
+    return SPEC_EINVAL;
+  if (n > kMaxPageRows || int64_t(n) * max_blocks > INT32_MAX / 2) return SPEC_ENOTSUP;
+  // a CTA addresses its planes' words with 32 bits
+  if (token_bytes % 16 != 0 || !aligned16(kv_pool) || int64_t(block_size) * token_bytes > (1 << 27))
+    return SPEC_ENOTSUP;
+  sv::KvForkLaunch k{block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, kv_scales,
+                     planes, token_bytes, num_blocks, block_size, B, max_blocks, n, free_stack,
+                     free_top, status, stream};
+  return sv::launch_kv_fork(k);
+}
+
+int kv_free(int32_t* block_table, int32_t* seq_lens, int32_t* extra_refs, const int32_t* rows,
+            int n, int num_blocks, int B, int max_blocks, int32_t* free_stack, int32_t* free_top,
+            int32_t* status, void* stream) {
+  if (!block_table || !seq_lens || !extra_refs || !rows || !free_stack || !free_top || !status)
+    return SPEC_EINVAL;
+  if (bad_table(num_blocks, 1, B, max_blocks) || n < 1) return SPEC_EINVAL;
+  if (n > kMaxPageRows || int64_t(n) * max_blocks > INT32_MAX / 2) return SPEC_ENOTSUP;
+  sv::KvFreeLaunch k{block_table, seq_lens, extra_refs, rows, num_blocks, B, max_blocks, n,
+                     free_stack, free_top, status, stream};
+  return sv::launch_kv_free(k);
+}
+
+static int check_q8_pool(const void* pool, const float* scales, int num_blocks, int num_layers,
+                         int layer, int num_kv_heads, int head_dim, int block_size, int B,
+                         int max_blocks) {
+  if (!pool || !scales) return SPEC_EINVAL;
+  if (bad_table(num_blocks, block_size, B, max_blocks) || num_layers < 1 || layer < 0 ||
+      layer >= num_layers || num_kv_heads < 1 || head_dim < 1)
+    return SPEC_EINVAL;
+  if (head_dim % 16 != 0 || !aligned16(pool)) return SPEC_ENOTSUP;
+  if (int64_t(num_layers) * 2 * num_kv_heads > INT32_MAX ||
+      int64_t(block_size) * head_dim > INT32_MAX / 4)
+    return SPEC_ENOTSUP;
+  return SPEC_OK;
+}
+
+int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* kv_scales,
+                 const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
+                 int num_blocks, int num_layers, int layer, int num_kv_heads, int head_dim,
+                 int block_size, int B, int T, int max_blocks, void* stream, int32_t* err_flag) {
+  if (!k || !v || !block_table || !seq_lens || elem_bytes(dtype) == 0 || T < 1)
+    return SPEC_EINVAL;
+  const int st = check_q8_pool(kv_pool, kv_scales, num_blocks, num_layers, layer, num_kv_heads,
+                               head_dim, block_size, B, max_blocks);
+  if (st != SPEC_OK) return st;
+  if (T > (1 << 30) - 2 * block_size) return SPEC_EINVAL;
+  if (!aligned16(k) || !aligned16(v)) return SPEC_ENOTSUP;
+  sv::Q8AppendLaunch a{k, v, dtype, kv_pool, kv_scales, block_table, seq_lens, num_new,
+                       num_blocks, num_layers, layer, num_kv_heads, head_dim, block_size, B, T,
+                       max_blocks, stream, err_flag};
+  return sv::launch_kv_q8_append(a);
+}
+
+size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (T < 1 || T > 32 || num_kv_heads < 1 || num_q_heads < num_kv_heads ||
+      num_q_heads % num_kv_heads != 0 || head_dim < 16 || head_dim > 256 || head_dim % 16 != 0)
+    return 0;
+  return sv::kv_q8_attention_workspace(T, num_q_heads / num_kv_heads, head_dim);
+}
+
+int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
+                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
+                    const uint32_t* tree_mask, void* out, float softmax_scale, int window,
+                    int sinks, int num_blocks, int num_layers, int layer, int num_q_heads,
+                    int num_kv_heads, int head_dim, int block_size, int B, int T, int max_blocks,
+                    void* workspace, size_t workspace_bytes, void* stream, int32_t* err_flag) {
+  if (!q || !out || !block_table || !seq_lens || elem_bytes(dtype) == 0) return SPEC_EINVAL;
+  if (!(softmax_scale > 0.0f) || std::isinf(softmax_scale) || window < 0 || sinks < 0 ||
+      (sinks > 0 && window == 0))
+    return SPEC_EINVAL;
+  const int st = check_q8_pool(kv_pool, kv_scales, num_blocks, num_layers, layer, num_kv_heads,
+                               head_dim, block_size, B, max_blocks);
+  if (st != SPEC_OK) return st;
+  if (T < 1 || num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0) return SPEC_EINVAL;
+  if (tree_mask && window > 0) return SPEC_ENOTSUP;
+  const size_t need = kv_q8_attention_workspace_bytes(T, num_q_heads, num_kv_heads, head_dim);
+  if (need == 0 || int64_t(T) * num_q_heads > (1 << 20)) return SPEC_ENOTSUP;
+  if (!aligned16(q) || !aligned16(out)) return SPEC_ENOTSUP;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)
+    return SPEC_EINVAL;
+  sv::Q8AttnLaunch a{q, dtype, kv_pool, kv_scales, block_table, seq_lens, num_new, tree_mask, out,
+                     softmax_scale, window, sinks, num_blocks, num_layers, layer, num_kv_heads,
+                     num_q_heads / num_kv_heads, head_dim, block_size, B, T, max_blocks, workspace,
+                     stream, err_flag};
+  return sv::launch_kv_q8_attention(a);
+}
+
 }  // extern "C"

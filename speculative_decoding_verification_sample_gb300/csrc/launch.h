@@ -1,6 +1,7 @@
 // Host-side launch descriptors shared by the C-ABI layer (api.cu) and the
 // kernel translation units. Plain structs of pointers and sizes.
 #pragma once
+#include <cstddef>
 #include <cstdint>
 
 namespace sv {
@@ -81,6 +82,83 @@ struct FilterLaunch {
   int32_t* err;
   void* stream;
 };
+
+struct KvReserveLaunch {
+  int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* num_new;  // null: n for every row
+  int n, num_blocks, block_size, B, max_blocks;
+  const int32_t* free_stack;
+  int32_t* free_top;
+  int32_t* status;
+  void* stream;
+};
+
+struct KvForkLaunch {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* extra_refs;
+  const int32_t* src_rows;
+  const int32_t* dst_rows;
+  void* kv_pool;
+  float* kv_scales;  // null: the pool has none
+  int planes, token_bytes, num_blocks, block_size, B, max_blocks, n;
+  int32_t* free_stack;
+  int32_t* free_top;
+  int32_t* status;
+  void* stream;
+};
+
+struct KvFreeLaunch {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* extra_refs;
+  const int32_t* rows;
+  int num_blocks, B, max_blocks, n;
+  int32_t* free_stack;
+  int32_t* free_top;
+  int32_t* status;
+  void* stream;
+};
+
+struct Q8AppendLaunch {
+  const void* k;
+  const void* v;
+  int dtype;
+  void* pool;
+  float* scales;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* num_new;  // null: T
+  int num_blocks, num_layers, layer, H, D, bs, B, T, max_blocks;
+  void* stream;
+  int32_t* err;
+};
+
+struct Q8AttnLaunch {
+  const void* q;
+  int dtype;
+  const void* pool;
+  const float* scales;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* num_new;     // null: T
+  const uint32_t* tree_mask;  // null: a chain
+  void* out;
+  float softmax_scale;
+  int window, sinks;
+  int num_blocks, num_layers, layer, H, G, D, bs, B, T, max_blocks;
+  void* workspace;
+  void* stream;
+  int32_t* err;
+};
+
+int launch_kv_reserve(const KvReserveLaunch& k);
+int launch_kv_fork(const KvForkLaunch& k);
+int launch_kv_free(const KvFreeLaunch& k);
+int launch_kv_q8_append(const Q8AppendLaunch& k);
+int launch_kv_q8_attention(const Q8AttnLaunch& k);
+size_t kv_q8_attention_workspace(int T, int G, int D);
 
 int launch_verify_sample(const SampleLaunch& s);
 int launch_filter(const FilterLaunch& f);
