@@ -1,0 +1,377 @@
+"""kv_q8_append and kv_q8_attention against the fp64 oracle."""
+import numpy as np
+import pytest
+
+from gpu_helpers import gpu_lib
+from oracle import q8
+from q8_helpers import (as_int32, bf16_values, cache, dev_pool, dev_scales, i32, poison_tails,
+                        table, tree_masks)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ append
+def _append_case(seed, *, lengths, T, H, D, bs, dtype, num_new=None, layers=2, layer=1):
+    import torch
+    rng = np.random.default_rng(seed)
+    B = len(lengths)
+    n = [T] * B if num_new is None else num_new
+    bt, _, nb = table(rng, [a + b for a, b in zip(lengths, n)], bs)
+    pool, scales = cache(rng, nb, layers, H, bs, D)
+    # magnitudes over several binades, so that some blocks' scales grow and some do not
+    k, v = (rng.normal(0, 1, (B, T, H, D)) * 2.0 ** rng.integers(-6, 7, (B, T, H, 1))
+            for _ in range(2))
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    k, v = (torch.from_numpy(x.astype(np.float32)).to(t) for x in (k, v))
+    return dict(k=k, v=v, pool=pool, scales=scales, bt=bt, sl=np.array(lengths),
+                nn=None if num_new is None else np.array(num_new), layer=layer)
+
+
+def _append_gpu(sv, c, stream=None):
+    import torch
+    pool, scales = dev_pool(c["pool"]), dev_scales(c["scales"])
+    err = i32([0])
+    sv.kv_q8_append(c["k"].cuda(), c["v"].cuda(), pool, scales, i32(c["bt"]), i32(c["sl"]),
+                    layer=c["layer"], num_new=None if c["nn"] is None else i32(c["nn"]),
+                    err_flag=err)
+    torch.cuda.synchronize()
+    return pool.view(torch.uint8).cpu().numpy(), scales.double().cpu().numpy(), int(err.item())
+
+
+def _append_same(sv, c):
+    want = q8.append(c["k"].double().numpy(), c["v"].double().numpy(), c["pool"], c["scales"],
+                     c["bt"], c["sl"], c["nn"], layer=c["layer"])
+    got = _append_gpu(sv, c)
+    assert got[2] == want[2]
+    assert np.array_equal(got[1], want[1])
+    assert np.array_equal(got[0], want[0])
+    return want
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H,D,bs", [(1, 2, 128, 16), (5, 8, 128, 16), (3, 1, 64, 32),
+                                      (70, 2, 64, 16), (40, 3, 256, 64), (9, 2, 80, 1),
+                                      (17, 1, 16, 24), (200, 1, 128, 128)])
+def test_append_matches_oracle(dtype, T, H, D, bs):
+    lengths = [0, 1, bs - 1, bs, bs + 1, 3 * bs + bs // 2, 7]
+    _append_same(gpu_lib(), _append_case(T * bs, lengths=lengths, T=T, H=H, D=D, bs=bs,
+                                         dtype=dtype))
+
+
+def test_append_ragged_and_empty_rows():
+    c = _append_case(3, lengths=[0, 5, 16, 31, 100], T=33, H=2, D=128, bs=16, dtype="bf16",
+                     num_new=[0, 33, 1, 0, 17])
+    _append_same(gpu_lib(), c)
+
+
+def test_append_zeros_extremes_and_subnormals():
+    import torch
+    c = _append_case(4, lengths=[0, 3, 16], T=4, H=2, D=64, bs=16, dtype="fp32")
+    c["k"][0] = 0
+    c["k"][1, :, 0] *= 1e-44      # below the smallest scale
+    c["k"][1, :, 1] = 3.3e38
+    c["v"][2, 0, 0, 0] = 448.0
+    c["v"][2, 0, 1] = torch.linspace(-1, 1, 64) * 2.0 ** -120
+    _append_same(gpu_lib(), c)
+
+
+def test_append_reports_what_it_cannot_store():
+    sv = gpu_lib()
+    c = _append_case(5, lengths=[2, 20, 0], T=5, H=2, D=64, bs=16, dtype="bf16")
+    c["k"][0, 1, 0, 3] = float("nan")
+    c["v"][1, 2, 1, 7] = float("inf")
+    c["v"][2, 0, 0, 0] = -float("inf")
+    assert _append_same(sv, c)[2] == 256
+    c = _append_case(6, lengths=[2, 20, 0, 6, 7], T=5, H=2, D=64, bs=16, dtype="bf16",
+                     num_new=[5, 5, 5, 6, 5])
+    c["bt"][1, 1] = len(c["pool"])
+    c["bt"][4, 0] = -1
+    c["sl"][2] = -1
+    assert _append_same(sv, c)[2] == 32 | 8
+    c = _append_case(7, lengths=[40], T=5, H=1, D=64, bs=16, dtype="bf16")
+    c["sl"][0] = 44   # 49 tokens in 3 blocks of 16
+    assert _append_same(sv, c)[2] == 8
+
+
+def test_append_twice_changes_nothing():
+    sv = gpu_lib()
+    c = _append_case(8, lengths=[3, 18], T=6, H=2, D=128, bs=16, dtype="bf16")
+    pool, scales, _ = _append_gpu(sv, c)
+    c2 = dict(c, pool=pool, scales=scales)
+    again = _append_gpu(sv, c2)
+    assert np.array_equal(again[0], pool) and np.array_equal(again[1], scales)
+
+
+# ------------------------------------------------------------------ attention
+def _attn_case(seed, *, lengths, T, Hq, H, D, bs, num_new=None, tree=False, dtype="bf16", layers=2,
+               layer=1, qscale=1.0, spread=1):
+    rng = np.random.default_rng(seed)
+    B = len(lengths)
+    n = [T] * B if num_new is None else num_new
+    ends = [a + b for a, b in zip(lengths, n)]
+    bt, _, nb = table(rng, ends, bs)
+    pool, scales = cache(rng, nb, layers, H, bs, D, spread)
+    pool = poison_tails(pool, bt, ends, bs)
+    q = rng.normal(0, qscale, (B, T, Hq, D))
+    q = bf16_values(q) if dtype == "bf16" else q.astype(np.float32).astype(np.float64)
+    return dict(q=q, pool=pool, scales=scales, bt=bt, sl=np.array(lengths),
+                nn=None if num_new is None else np.array(num_new), layer=layer, dtype=dtype,
+                tree=tree_masks(rng, B, T) if tree else None)
+
+
+def _attn_gpu(sv, c, **kw):
+    import torch
+    dt = torch.bfloat16 if c["dtype"] == "bf16" else torch.float32
+    q = torch.from_numpy(c["q"]).to(dt).cuda()
+    out = torch.full_like(q, 7.0)
+    err = i32([0])
+    sv.kv_q8_attention(q, dev_pool(c["pool"]), dev_scales(c["scales"]), i32(c["bt"]), i32(c["sl"]),
+                       out, layer=c["layer"], num_new=None if c["nn"] is None else i32(c["nn"]),
+                       tree_mask=None if c["tree"] is None else i32(as_int32(c["tree"])),
+                       err_flag=err, **kw)
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy(), int(err.item())
+
+
+def _bound(c, want, spread, reach, D):
+    """What the arithmetic may be off by.
+
+    A score carries D fp32 products and sums (2^-24 each relative to sum |q_d k_d|, `reach`),
+    counted 16-fold for the accumulation order and width of the matrix units, and an fp32
+    exponential: the weight's relative error is e = 16 D 2^-24 reach + 2^-20, in the weight and
+    in the sum. bf16: a weight is held in 9 bits (2^-9 of it; 2^-16 of the largest for the
+    smallest ones) and the output rounded to 8 (2^-8 of it). fp32: 2^-24, and fp32 sums.
+    """
+    e = 2 * (16 * D * 2.0 ** -24 * reach + 2.0 ** -20)
+    n = c["bt"].shape[1] * c["pool"].shape[4]
+    if c["dtype"] == "bf16":
+        return (2.0 ** -9 + e) * spread + 2.0 ** -8 * np.abs(want) + n * 2.0 ** -22 * spread + 1e-30
+    return (e + 64 * 2.0 ** -24) * spread + 2.0 ** -23 * np.abs(want) + 1e-30
+
+
+def _attn_same(sv, c, kw=None, oracle_kw=None):
+    kw = kw or {}
+    got, err = _attn_gpu(sv, c, **kw)
+    want, spread, reach = q8.attention(c["q"], c["pool"], c["scales"], c["bt"], c["sl"], c["nn"],
+                                       layer=c["layer"], tree_mask=c["tree"], **kw)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    ok = ~np.isnan(want)
+    off = np.abs(got - want)[ok]
+    lim = _bound(c, want, spread, reach, c["q"].shape[-1])[ok]
+    worst = float(np.max(off / lim)) if off.size else 0.0
+    assert worst <= 1.0, worst
+    return err
+
+
+LENGTHS = [0, 1, 15, 16, 123, 127, 128, 129, 300]
+
+
+@pytest.mark.parametrize("T,Hq,H,D,bs", [
+    (1, 4, 1, 128, 16), (5, 8, 2, 128, 16), (1, 1, 1, 128, 16), (3, 12, 4, 128, 32),
+    (7, 8, 1, 128, 64), (32, 4, 1, 128, 16), (16, 16, 2, 128, 128), (2, 7, 1, 128, 8),
+    (5, 8, 2, 64, 16), (1, 8, 1, 64, 32), (32, 12, 1, 64, 64), (4, 2, 1, 128, 256),
+    (1, 2, 1, 80, 16), (5, 4, 2, 256, 16), (3, 2, 2, 16, 24), (2, 2, 1, 128, 1),
+])
+def test_attention_matches_oracle(T, Hq, H, D, bs):
+    c = _attn_case(T * D + bs, lengths=LENGTHS, T=T, Hq=Hq, H=H, D=D, bs=bs)
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+@pytest.mark.parametrize("T,Hq,H,D,bs", [(1, 4, 1, 128, 16), (5, 4, 2, 64, 16), (9, 3, 1, 48, 5)])
+def test_attention_fp32(T, Hq, H, D, bs):
+    c = _attn_case(T * D + bs, lengths=LENGTHS, T=T, Hq=Hq, H=H, D=D, bs=bs, dtype="fp32")
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+@pytest.mark.parametrize("D,bs", [(128, 16), (64, 32), (96, 16)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (37, 4), (128, 0), (129, 200), (250, 37),
+                                          (5000, 3)])
+def test_attention_window_and_sinks(D, bs, window, sinks):
+    c = _attn_case(window + D, lengths=[0, 1, 60, 129, 401, 700, 1023], T=6, Hq=4, H=1, D=D, bs=bs)
+    assert _attn_same(gpu_lib(), c, dict(window=window, sinks=sinks)) == 0
+
+
+@pytest.mark.parametrize("T,G,D,bs", [(15, 4, 128, 16), (32, 2, 128, 64), (9, 1, 64, 16),
+                                      (5, 2, 32, 16)])
+def test_attention_tree(T, G, D, bs):
+    c = _attn_case(T, lengths=[0, 3, 120, 128, 250], T=T, Hq=2 * G, H=2, D=D, bs=bs, tree=True)
+    assert _attn_same(gpu_lib(), c) == 0
+    c["tree"][:, 1] = 0   # with no committed token: a query that sees nothing
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+def test_attention_ragged_rows():
+    c = _attn_case(11, lengths=[0, 40, 128, 0, 77], T=6, Hq=8, H=2, D=128, bs=16,
+                   num_new=[0, 6, 1, 3, 0])
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+def test_attention_many_rows_and_splits():
+    """More items than CTAs, lengths from one token to thousands: items that begin and end
+    anywhere in a CTA's share."""
+    rng = np.random.default_rng(12)
+    lengths = [int(x) for x in rng.integers(0, 200, 150)] + [2500, 0, 1]
+    c = _attn_case(12, lengths=lengths, T=2, Hq=8, H=4, D=128, bs=16, layers=1, layer=0)
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+def test_attention_long_row():
+    c = _attn_case(13, lengths=[20000], T=3, Hq=2, H=1, D=128, bs=16, layers=1, layer=0)
+    assert _attn_same(gpu_lib(), c) == 0
+    c = _attn_case(14, lengths=[20000, 17], T=2, Hq=8, H=1, D=64, bs=64, layers=1, layer=0)
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+@pytest.mark.parametrize("D", [128, 64, 96])
+def test_attention_peaked_scores(D):
+    """Scores over hundreds of binades: later keys far above the first tiles' maximum and far
+    below it, scales that differ by 2^24 from block to block."""
+    c = _attn_case(15 + D, lengths=[600, 900], T=4, Hq=4, H=1, D=D, bs=16, qscale=6.0, spread=12)
+    c["scales"][:, :, 0] = np.minimum(c["scales"][:, :, 0], 2.0 ** -3)
+    # the row's keys grow along the sequence
+    for b in range(2):
+        held = c["bt"][b][c["bt"][b] >= 0]
+        c["scales"][held, :, 0] = 2.0 ** np.linspace(-12, -3, len(held)).round()[:, None, None]
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+def test_attention_softmax_scale_and_small_queries():
+    sv = gpu_lib()
+    c = _attn_case(16, lengths=[200, 50], T=2, Hq=4, H=1, D=128, bs=16)
+    assert _attn_same(sv, c, dict(softmax_scale=0.5)) == 0
+    c["q"] *= 2.0 ** -40
+    c["q"][0, 0, 0] = 0.0
+    c["q"][1, 1, 2, 5:] *= 2.0 ** -30   # numbers far below their row's largest
+    assert _attn_same(sv, c) == 0
+
+
+def test_attention_zero_scales():
+    c = _attn_case(17, lengths=[200, 50], T=2, Hq=4, H=1, D=128, bs=16)
+    c["scales"][:, :, 1] = 0.0
+    assert _attn_same(gpu_lib(), c) == 0
+    c["scales"][:, :, 0] = 2.0 ** -100
+    assert _attn_same(gpu_lib(), c) == 0
+
+
+@pytest.mark.parametrize("D", [128, 96])
+def test_attention_nan_queries_stay_in_their_row(D):
+    c = _attn_case(18, lengths=[140, 50], T=3, Hq=4, H=1, D=D, bs=16)
+    c["q"][0, 1, 2, 7] = np.nan
+    got, err = _attn_gpu(gpu_lib(), c)
+    c["q"][0, 1, 2, 7] = 0.0
+    want, spread, reach = q8.attention(c["q"], c["pool"], c["scales"], c["bt"], c["sl"], None,
+                                       layer=c["layer"])
+    bad = np.zeros(got.shape, bool)
+    bad[0, 1, 2] = True
+    assert err == 0 and np.array_equal(np.isnan(got), bad)
+    assert np.all(np.abs(got - want)[~bad] <= _bound(c, want, spread, reach, D)[~bad])
+
+
+@pytest.mark.parametrize("D", [128, 64, 96])
+def test_attention_bad_blocks_and_lengths(D):
+    sv = gpu_lib()
+    c = _attn_case(19, lengths=[300, 300, 10, 60, 5], T=3, Hq=4, H=2, D=D, bs=16,
+                   num_new=[3, 3, 3, 4, 3])
+    c["bt"][0, 3] = -1
+    c["bt"][1, 0] = len(c["pool"]) + 5
+    c["sl"][2] = -4
+    assert _attn_same(sv, c) == 32 | 8
+    # a bad block outside every window is not touched
+    c = _attn_case(20, lengths=[600, 600], T=3, Hq=4, H=2, D=D, bs=16)
+    c["bt"][0, 10] = -1
+    assert _attn_same(sv, c, dict(window=100, sinks=4)) == 0
+
+
+def test_attention_runs_on_the_given_stream_and_repeats():
+    """Two streams at once, each with the workspace of its own; the same bits every time."""
+    import torch
+    sv = gpu_lib()
+    c = _attn_case(21, lengths=[3000, 700, 90], T=5, Hq=8, H=2, D=128, bs=16)
+    q = torch.from_numpy(c["q"]).bfloat16().cuda()
+    args = (dev_pool(c["pool"]), dev_scales(c["scales"]), i32(c["bt"]), i32(c["sl"]))
+    first = torch.empty_like(q)
+    sv.kv_q8_attention(q, *args, first, layer=1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(q) for _ in range(10)] for _ in streams]
+    for i in range(10):
+        for s, o in zip(streams, outs):
+            sv.kv_q8_attention(q, *args, o[i], layer=1, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        for x in o:
+            assert torch.equal(x, first)
+
+
+def test_append_then_attend_in_a_graph():
+    """The pair captured once and replayed on new tokens and lengths."""
+    import torch
+    sv = gpu_lib()
+    c = _attn_case(22, lengths=[40, 130], T=3, Hq=4, H=2, D=128, bs=16)
+    rng = np.random.default_rng(22)
+    q = torch.from_numpy(c["q"]).bfloat16().cuda()
+    k, v = (torch.empty((2, 3, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pool, scales = dev_pool(c["pool"]), dev_scales(c["scales"])
+    bt, sl, out = i32(c["bt"]), i32(c["sl"]), torch.empty_like(q)
+
+    def step():
+        sv.kv_q8_append(k, v, pool, scales, bt, sl, layer=1)
+        sv.kv_q8_attention(q, pool, scales, bt, sl, out, layer=1)
+
+    k.zero_(), v.zero_()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for shift in (0, -7, -40):
+        pool.copy_(dev_pool(c["pool"]))
+        scales.copy_(dev_scales(c["scales"]))
+        kv = [bf16_values(rng.normal(0, 1, (2, 3, 2, 128))) for _ in range(2)]
+        k.copy_(torch.from_numpy(kv[0]).bfloat16())
+        v.copy_(torch.from_numpy(kv[1]).bfloat16())
+        L = c["sl"] + shift
+        sl.copy_(i32(L))
+        graph.replay()
+        torch.cuda.synchronize()
+        p2, s2, _ = q8.append(kv[0], kv[1], c["pool"], c["scales"], c["bt"], L, layer=1)
+        assert np.array_equal(pool.view(torch.uint8).cpu().numpy(), p2)
+        want, spread, reach = q8.attention(c["q"], p2, s2, c["bt"], L, layer=1)
+        off = np.abs(out.double().cpu().numpy() - want)
+        assert np.all(off <= _bound(c, want, spread, reach, 128))
+
+
+def test_binding_refuses():
+    import torch
+    sv = gpu_lib()
+    c = _attn_case(23, lengths=[20], T=2, Hq=4, H=2, D=64, bs=16)
+    q = torch.zeros((1, 2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    pool, scales, bt, sl = dev_pool(c["pool"]), dev_scales(c["scales"]), i32(c["bt"]), i32(c["sl"])
+    out = torch.empty_like(q)
+    ok = dict(q=q, kv_pool=pool, kv_scales=scales, block_table=bt, seq_lens=sl, out=out)
+    sv.kv_q8_attention(**ok)
+    for err, change in [
+        (TypeError, dict(q=q.half(), out=out.half())), (TypeError, dict(kv_pool=pool.to(torch.bfloat16))),
+        (TypeError, dict(kv_scales=scales.double())), (ValueError, dict(kv_scales=scales[:-1])),
+        (ValueError, dict(out=out[:, :1].contiguous())), (TypeError, dict(out=out.float())),
+        (ValueError, dict(q=q.transpose(1, 2))), (ValueError, dict(seq_lens=i32([1, 2]))),
+        (TypeError, dict(seq_lens=sl.long())), (ValueError, dict(block_table=bt.repeat(2, 1))),
+        (ValueError, dict(tree_mask=i32([[1]]))), (ValueError, dict(num_new=i32([1, 1]))),
+        (sv.SpecError, dict(layer=2)), (sv.SpecError, dict(sinks=3)),
+        (sv.SpecError, dict(softmax_scale=0.0)),
+        (sv.SpecError, dict(workspace=torch.empty(300, dtype=torch.uint8, device="cuda"))),
+        (sv.SpecError, dict(q=q[:, :, :3].contiguous(), out=out[:, :, :3].contiguous())),
+    ]:
+        with pytest.raises(err):
+            sv.kv_q8_attention(**{**ok, **change})
+    kv = torch.zeros((1, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    ok = dict(k=kv, v=kv, kv_pool=pool, kv_scales=scales, block_table=bt, seq_lens=sl)
+    sv.kv_q8_append(**ok)
+    for err, change in [(TypeError, dict(v=kv.float())), (ValueError, dict(v=kv[:, :1].contiguous())),
+                        (TypeError, dict(k=kv.half(), v=kv.half())), (sv.SpecError, dict(layer=-1)),
+                        (ValueError, dict(k=kv[..., :32].contiguous(), v=kv[..., :32].contiguous()))]:
+        with pytest.raises(err):
+            sv.kv_q8_append(**{**ok, **change})
+    torch.cuda.synchronize()
