@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(const AttnArgs a)
           float f[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) f[q] = 0.0f;
-          if (pos < g.s.end) {
+          if (needed(g.s, pos, 1)) {
             const int id = a.bt[int64_t(g.b) * a.MB + pos / a.bs];
             if (id >= 0 && id < a.NB) {
               const int64_t unit = int64_t(plane) * a.H + g.h;
@@ -299,22 +299,30 @@ int launch_kv_q8_attention(const Q8AttnLaunch& k) {
   a.planes_per_block = k.num_layers * 2 * k.H;
   const int sms = sm_count();
   if (sms == 0) return SPEC_ECUDA;
-  a.rows_per_block = kAnyRows;
-  a.RB = (a.R + kAnyRows - 1) / kAnyRows;
-  const size_t smem = any_smem(k.D);
-  auto kern = k.dtype == SPEC_F32 ? attn_any_kernel<float> : attn_any_kernel<__nv_bfloat16>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
-      cudaSuccess)
-    return SPEC_ECUDA;
-  int nc = 2 * sms < kAttnMaxCtas ? 2 * sms : kAttnMaxCtas;
+  const int64_t planes = int64_t(k.num_blocks) * a.planes_per_block;
+  const bool tc = attn_tc_takes(k.dtype, k.D, k.bs, planes);
+  a.rows_per_block = tc ? attn_tc_rows(a.R) : kAnyRows;
+  a.RB = (a.R + a.rows_per_block - 1) / a.rows_per_block;
   uint8_t* ws = static_cast<uint8_t*>(k.workspace);
   a.parts = reinterpret_cast<float*>(ws);
   ws += up256(size_t(2) * kAttnMaxCtas * a.rows_per_block * k.D * sizeof(float));
   a.stats = reinterpret_cast<float2*>(ws);
   ws += up256(size_t(2) * kAttnMaxCtas * a.rows_per_block * sizeof(float2));
   a.joins = reinterpret_cast<int4*>(ws);
-  cudaStream_t st = static_cast<cudaStream_t>(k.stream);
-  if (launch_pdl(kern, dim3(nc), dim3(kAnyThreads), smem, st, a) != SPEC_OK) return SPEC_ECUDA;
+  int nc = 2 * sms < kAttnMaxCtas ? 2 * sms : kAttnMaxCtas;
+  if (tc) {
+    const int st = launch_attn_tc(a, k.pool, planes, sms, kAttnMaxCtas, &nc, k.stream);
+    if (st != SPEC_OK) return st;
+  } else {
+    const size_t smem = any_smem(k.D);
+    auto kern = k.dtype == SPEC_F32 ? attn_any_kernel<float> : attn_any_kernel<__nv_bfloat16>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+        cudaSuccess)
+      return SPEC_ECUDA;
+    const int st = launch_pdl(kern, dim3(nc), dim3(kAnyThreads), smem,
+                              static_cast<cudaStream_t>(k.stream), a);
+    if (st != SPEC_OK) return st;
+  }
   return launch_attn_join(a, nc, k.dtype, k.stream);
 }
 

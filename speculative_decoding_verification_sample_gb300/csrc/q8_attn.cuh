@@ -52,6 +52,7 @@ struct AttnArgs {
 
 struct RowSpan {
   int L, n, end;           // committed and new tokens; end = L + n
+  int lo, sink_end;        // some query may see positions [0, sink_end) and [lo, end) only
   int sink_tiles, win_tile;  // tiles [0, sink_tiles) and [win_tile, ...)
   int tiles;
   bool bad;
@@ -62,6 +63,7 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
   s.L = a.sl[b];
   s.n = a.nn ? a.nn[b] : a.T;
   s.bad = s.L < 0 || s.n < 0 || s.n > a.T || int64_t(s.L) + s.n > int64_t(a.MB) * a.bs;
+  s.lo = s.sink_end = 0;
   if (s.bad || s.n == 0) {
     s.end = s.tiles = s.sink_tiles = s.win_tile = 0;
     return s;
@@ -71,8 +73,10 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
   s.sink_tiles = 0;
   s.win_tile = 0;
   if (a.window > 0 && s.L >= a.window) {
-    s.win_tile = (s.L - a.window + 1) / kAttnTile;
-    s.sink_tiles = (min(a.sinks, s.end) + kAttnTile - 1) / kAttnTile;
+    s.lo = s.L - a.window + 1;
+    s.sink_end = min(a.sinks, s.end);
+    s.win_tile = s.lo / kAttnTile;
+    s.sink_tiles = (s.sink_end + kAttnTile - 1) / kAttnTile;
     if (s.sink_tiles >= s.win_tile) s.sink_tiles = s.win_tile = 0;
   }
   s.tiles = s.sink_tiles + all - s.win_tile;
@@ -81,6 +85,12 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
 
 __device__ __forceinline__ int tile_start(const RowSpan& s, int k) {
   return (k < s.sink_tiles ? k : k - s.sink_tiles + s.win_tile) * kAttnTile;
+}
+
+// May a query of the row see a position of [p, p + n)? Blocks for which this is
+// false are not read (a caller with a window may have freed them).
+__device__ __forceinline__ bool needed(const RowSpan& s, int p, int n) {
+  return p < s.end && (p + n > s.lo || p < s.sink_end);
 }
 
 // Does query t see key j (t < n, j < end)?
@@ -220,6 +230,13 @@ __device__ __forceinline__ void write_join(const AttnArgs& a, const AttnPlan& p,
   }
   a.joins[c] = j;
 }
+
+// The tensor-core kernel (kv_q8_attention_tc.cu): whether it takes a call, its
+// rows per block, and its launch, which sets `nc` to the number of CTAs.
+bool attn_tc_takes(int dtype, int D, int bs, int64_t planes);
+int attn_tc_rows(int R);
+int launch_attn_tc(const AttnArgs& a, const void* pool_base, int64_t planes, int sms, int max_ctas,
+                   int* nc, void* stream);
 
 int launch_attn_join(const AttnArgs& a, int nc, int dtype, void* stream);
 
