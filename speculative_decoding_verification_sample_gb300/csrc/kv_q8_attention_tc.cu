@@ -16,11 +16,12 @@
 // into three e5m2 terms of at most 3 bits, exactly; e5m2 is the upper byte of
 // fp16, so a term is a byte of the fp16 number and the rest one subtraction.
 // 9 bits leave the bf16 output's own rounding the larger error; e5m2's 32
-// binades hold probabilities down to 2^-22 of the first tile's largest.
-//   Softmax: the running maximum of a row is only moved when a score exceeds it by
-// 2^8 (or a V scale the reference scale by 2): then O and l are rescaled once;
-// otherwise a tile costs no reduction over its keys. l stays per thread (one key
-// of every tile) until the item ends.
+// binades hold what a key contributes (probability times V scale) down to 2^-22 of
+// the row's reference.
+//   Softmax: a row's reference m is the largest z_j + log2(V scale of j) (rounded up
+// to a binade) of the first tile, and is only moved when a later one exceeds it by
+// 8: then O and l are rescaled once; otherwise a tile costs no reduction over its
+// keys. l stays per thread (one key of every tile) until the item ends.
 //
 // Roles: warps 0-3 softmax (thread = key of the tile), warp 4 TMA, warp 5 MMA.
 // K and V tiles share one ring of slots, released separately. Two CTAs per SM
@@ -46,9 +47,9 @@ constexpr int kTcSoftmax = 128;             // threads of the softmax warps
 constexpr int kTcThreads = kTcSoftmax + 64;
 constexpr int kTcScaleRing = 8;             // tiles whose scales are held
 constexpr int kTcMaxPages = 16;             // blocks of one tile
-constexpr float kTcUnset = -1e30f;          // maximum of a row that has seen no key
-constexpr float kTcSlack = 8.0f;            // binades by which scores may exceed the maximum
-constexpr float kTcLift = 64.0f;            // p = 1 enters as 2^6: 2^6 2^8 2 <= 2^15 in e5m2
+constexpr float kTcUnset = -1e30f;          // reference of a row that has seen no key
+constexpr float kTcSlack = 8.0f;            // binades by which keys may exceed the reference
+constexpr float kTcLift = 64.0f;            // 1 enters as 2^6: 2^6 2^8 < 2^16, e5m2's range
 constexpr int kTcSmem = 107 * 1024;         // dynamic, of one CTA: two per SM
 
 template <int NR, int D>
@@ -73,12 +74,12 @@ struct TcShared {
   int abort;
   float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
   float row_c[NR];     // query row's scale * softmax_scale * log2(e)
-  float row_m[NR];     // maximum
-  float row_a[NR];     // rescale factor, then 1 / sum
+  float row_m[NR];     // reference of the exponentials
+  float row_a[NR];     // rescale factor, then that of the output
   int row_t[NR];       // query (T for rows that do not exist)
   uint32_t row_mask[NR];
   float part[4][NR];   // the warps' maxima, then sums
-  float part_v[4];
+  int part_v[4];
 };
 
 // Bounded wait. Once one has given up, every wait returns at once: the roles
@@ -108,6 +109,13 @@ __device__ __forceinline__ bool bar_softmax_or(bool x) {
       : "r"(uint32_t(x))
       : "memory");
   return r != 0;
+}
+
+// The smallest e in [-100, 100] with |x| <= 2^e (100 for larger ones).
+__device__ __forceinline__ int scale_binade(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  const int e = int(u >> 23) - 127 + ((u & 0x7fffffu) != 0);
+  return max(-100, min(100, e));
 }
 
 // Maximum over the warp of floats without NaN: as integers in float order.
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       float l[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-      float vref = 0.0f;
+      int vref = 0;
 
       for (int k = g.t0; k < g.t1; ++k, ++j) {
         const int p0 = tile_start(g.s, k), pos = p0 + tid;
@@ -356,7 +364,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         tc_wait(&sh.full[vslot], (vi / NS) & 1, &sh.abort, a.err);
         tc_fence_after();
         const float vs = sh.vs[j % kTcScaleRing][tid / bs];
-        const float ks = vs == vs ? sh.ks[j % kTcScaleRing][tid / bs] : vs;
+        const float ks =
+            fabsf(vs) <= FLT_MAX ? sh.ks[j % kTcScaleRing][tid / bs] : __uint_as_float(0x7fc00000u);
         float z[NR];
 #pragma unroll
         for (int r = 0; r < NR; r += 8) {
@@ -384,22 +393,26 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
         }
-        bool over = vs > 2.0f * vref;
+        if (k == g.t0) {
+          // V scales are taken relative to this tile's largest, a power of two
+          const int x = __reduce_max_sync(0xffffffffu, scale_binade(vs));
+          if (lane == 0) sh.part_v[warp] = x;
+          bar_softmax();
+          vref = max(max(sh.part_v[0], sh.part_v[1]), max(sh.part_v[2], sh.part_v[3]));
+        }
+        const float vr = vs * q8_pow2(-vref);
+        const float lv = float(scale_binade(vr));  // vr <= 2^lv
+        bool over = k == g.t0;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) over = over || z[r] > sh.row_m[r] + kTcSlack;
-        if (bar_softmax_or(over || k == g.t0)) {
-          // move the maxima (and V's reference scale) to this tile's
+        for (int r = 0; r < NR; ++r) over = over || z[r] - sh.row_m[r] > kTcSlack - lv;
+        if (bar_softmax_or(over)) {
+          // move the references to this tile's maxima
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const float x = warp_max(z[r] == z[r] ? z[r] : -INFINITY);
+            const float x = warp_max(z[r] == z[r] ? z[r] + lv : -INFINITY);
             if (lane == (r & 31)) sh.part[warp][r] = x;
           }
-          const float xv = warp_max(vs == vs ? vs : 0.0f);
-          if (lane == 0) sh.part_v[warp] = xv;
           bar_softmax();
-          const float v_old = vref;
-          vref = fmaxf(fmaxf(fmaxf(sh.part_v[0], sh.part_v[1]), fmaxf(sh.part_v[2], sh.part_v[3])),
-                       fmaxf(vref, 7.5e-37f));
           for (int r = tid; r < NR; r += kTcSoftmax) {
             const float old = sh.row_m[r];
             const float m = fmaxf(fmaxf(fmaxf(sh.part[0][r], sh.part[1][r]),
@@ -411,7 +424,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int r = 0; r < NR; ++r) l[r] *= sh.row_a[r];
           if (k > g.t0) {
-            const float va = v_old / vref;
             tc_wait(&sh.pv_done, (j - 1) & 1, &sh.abort, a.err);
             tc_fence_after();
 #pragma unroll
@@ -420,14 +432,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
               tmem_ld8(o_addr + r, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] *= sh.row_a[r + x] * va;
+              for (int x = 0; x < 8; ++x) o[x] *= sh.row_a[r + x];
               tmem_st8(o_addr + r, o);
             }
             tmem_wait_st();
           }
         }
         if (j > 0) tc_wait(&sh.pv_done, (j - 1) & 1, &sh.abort, a.err);  // P may be replaced
-        const float lift = vs / vref * kTcLift;
+        const float lift = vr * kTcLift;
 #pragma unroll
         for (int r0 = 0; r0 < NR; r0 += 16) {
           uint32_t t0[4], t1[4], t2[4];
@@ -491,15 +503,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
       for (int r = tid; r < NR; r += kTcSoftmax) {
         const float sum = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
-        sh.row_a[r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        // A part is left with its sum in [1, 2): references of parts differ by their V
+        // scales, so a sum by itself may be as far from 1 as those.
+        const int e = sum > 0.0f && sum <= FLT_MAX ? int(__float_as_uint(sum) >> 23) - 127 : 0;
+        sh.row_a[r] = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : q8_pow2(-e);
         if (!whole && r < rows)
           a.stats[slot * a.rows_per_block + r] =
-              make_float2(sh.row_m[r] == kTcUnset ? -INFINITY : sh.row_m[r], sum);
+              make_float2(sum == 0.0f ? -INFINITY : sh.row_m[r] + float(e), sum * q8_pow2(-e));
       }
       bar_softmax();
       tc_wait(&sh.pv_done, (j - 1) & 1, &sh.abort, a.err);
       tc_fence_after();
-      const float unlift = vref / kTcLift;
+      const float unlift = q8_pow2(vref) / kTcLift;
 #pragma unroll 1
       for (int r0 = 0; r0 < NR; r0 += 8) {
         float o[8];
@@ -510,12 +525,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           for (int x = 0; x < 8; ++x) {
             const int r = r0 + x;
             if (r < rows) {
-              const float v = o[x] * unlift;
+              const float v = o[x] * sh.row_a[r] * unlift;
               if (whole) {
                 const int row = g.rb * a.rows_per_block + r, t = sh.row_t[r];
                 static_cast<__nv_bfloat16*>(
                     a.out)[((int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G)) * D +
-                           tid] = __float2bfloat16(v * sh.row_a[r]);
+                           tid] = __float2bfloat16(v);
               } else {
                 a.parts[(slot * a.rows_per_block + r) * D + tid] = v;
               }
