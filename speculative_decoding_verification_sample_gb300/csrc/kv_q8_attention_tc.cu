@@ -23,9 +23,10 @@
 // 8: then O and l are rescaled once; otherwise a tile costs no reduction over its
 // keys. l stays per thread (one key of every tile) until the item ends.
 //
-// Roles: warps 0-3 softmax (thread = key of the tile), warp 4 TMA, warp 5 MMA.
-// K and V tiles share one ring of slots, released separately. Two CTAs per SM
-// hide each other's latencies.
+// Roles: one or two groups of 4 softmax warps (thread = key of the tile, each group
+// its own query rows), a TMA warp, an MMA warp and a warp that prepares the next
+// item's queries. K and V tiles share one ring of slots, released separately. Two
+// CTAs per SM hide each other's latencies.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,11 +44,9 @@
 
 namespace sv {
 
-constexpr int kTcSoftmax = 128;             // threads of the softmax warps
-constexpr int kTcThreads = kTcSoftmax + 64;
 constexpr int kTcScaleRing = 8;             // tiles whose scales are held
 constexpr int kTcMaxPages = 16;             // blocks of one tile
-constexpr float kTcUnset = -1e30f;          // reference of a row that has seen no key
+constexpr float kTcUnset = 1e30f;           // minus the reference of a row that has seen no key
 constexpr float kTcSlack = 8.0f;            // binades by which keys may exceed the reference
 constexpr float kTcLift = 64.0f;            // 1 enters as 2^6: 2^6 2^8 < 2^16, e5m2's range
 constexpr int kTcSmem = 107 * 1024;         // dynamic, of one CTA: two per SM
@@ -55,31 +54,54 @@ constexpr int kTcSmem = 107 * 1024;         // dynamic, of one CTA: two per SM
 template <int NR, int D>
 struct TcShape {
   static constexpr int NO = (NR + 15) / 16 * 16;
+  static constexpr int kGroups = NR > 8 ? 2 : 1;           // softmax groups
+  static constexpr int W = NR / kGroups;                   // rows of a group
+  static constexpr int kSoftmax = 128 * kGroups;
+  static constexpr int kThreads = kSoftmax + 96;
   static constexpr int kSlot = kAttnTile * D;
   static constexpr int kQ = 2 * NR * D;
   static constexpr int kP = 3 * NO * kAttnTile;
-  static constexpr int kFit = (kTcSmem - kQ - kP - 1024) / kSlot;
+  static constexpr int kQBufs = NR <= 48 ? 2 : 1;          // two where four slots still fit
+  static constexpr int kPBufs = 1;
+  static constexpr int kFit = (kTcSmem - kQBufs * kQ - kPBufs * kP - 1024) / kSlot;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   static constexpr int kSBufs = 4 * NR + NO <= 256 ? 2 : 1;
   static constexpr int kCols = kSBufs * 2 * NR + NO;
   static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
-  static constexpr size_t kBytes = size_t(kSlots) * kSlot + kQ + kP + 1024;
+  static constexpr size_t kBytes = size_t(kSlots) * kSlot + kQBufs * kQ + kPBufs * kP + 1024;
   static_assert(kCols <= 256 && kSlots >= 3, "two CTAs per SM");
+  static_assert(size_t(kP) >= (kThreads + 1) * 8, "the plan's sums lie there first");
 };
 
-template <int NR>
+// A ring of N slots or buffers: the place of the next use and the phase it is in.
+template <int N>
+struct TcRing {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+template <int NR, int QB>
 struct TcShared {
-  uint64_t full[8], empty[8], s_full[2], s_empty[2], p_full, pv_done, q_full;
+  alignas(16) float row_c[QB][NR];  // query row's scale * softmax_scale * log2(e)
+  alignas(16) float row_nm[NR];    // minus the reference of the exponentials
+  alignas(16) float row_a[NR];     // rescale factor, then that of the output
+  alignas(16) float part[4][NR];   // the warps' maxima, then sums
+  Segment seg[QB];                 // the items that the queries belong to
+  int64_t row_off[QB][NR];          // row of q and out, -1: none
+  int row_t[QB][NR];                // query (T for rows that do not exist)
+  uint32_t row_mask[QB][NR];
+  float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
+  int2 tile[kTcScaleRing];  // first position; whether every query sees every key
+  int part_v[2][4];
+  uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full[2], q_empty[2];
   uint32_t tmem;
   int abort;
-  float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
-  float row_c[NR];     // query row's scale * softmax_scale * log2(e)
-  float row_m[NR];     // reference of the exponentials
-  float row_a[NR];     // rescale factor, then that of the output
-  int row_t[NR];       // query (T for rows that do not exist)
-  uint32_t row_mask[NR];
-  float part[4][NR];   // the warps' maxima, then sums
-  int part_v[4];
 };
 
 // Bounded wait. Once one has given up, every wait returns at once: the roles
@@ -97,16 +119,17 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, int* abo
   if (err) atomicOr(err, SPEC_DERR_TIMEOUT);
 }
 
-__device__ __forceinline__ void bar_softmax() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
+// Barriers of one softmax group (ids 1 and 2).
+__device__ __forceinline__ void bar_group(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory");
 }
-__device__ __forceinline__ bool bar_softmax_or(bool x) {
+__device__ __forceinline__ bool bar_group_or(int group, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(uint32_t(x))
+      : "r"(group + 1), "r"(uint32_t(x))
       : "memory");
   return r != 0;
 }
@@ -118,47 +141,65 @@ __device__ __forceinline__ int scale_binade(float x) {
   return max(-100, min(100, e));
 }
 
-// Maximum over the warp of floats without NaN: as integers in float order.
-__device__ __forceinline__ float warp_max(float x) {
-  int i = __float_as_int(x);
-  i ^= (i >> 31) & 0x7fffffff;
-  i = __reduce_max_sync(0xffffffffu, i);
-  i ^= (i >> 31) & 0x7fffffff;
-  return __int_as_float(i);
+// Eight rows reduced over the warp's keys: lanes exchange halves of the rows until
+// each holds one (7 shuffles), then the four lanes of a row finish it. Lane i
+// returns row reduce8_row(i).
+__device__ __forceinline__ int reduce8_row(int lane) {
+  return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
+}
+template <class Op, class Map>
+__device__ __forceinline__ float reduce8(float* v, int lane, Op op, Map map) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = map(v[q]);
+#pragma unroll
+  for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int q = 0; q < n; ++q) {
+      const float give = up ? v[q] : v[q + n], keep = up ? v[q + n] : v[q];
+      v[q] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 template <int NR, int D>
-__global__ void __launch_bounds__(kTcThreads, 2)
+__global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     attn_tc_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map) {
   using S = TcShape<NR, D>;
-  constexpr int NS = S::kSlots, NO = S::NO, NB = S::kSBufs;
+  constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs, QB = S::kQBufs, PB = S::kPBufs;
+  constexpr int kTmaWarp = S::kSoftmax / 32, kMmaWarp = kTmaWarp + 1, kQWarp = kTmaWarp + 2;
   constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // TMA and operands: 128- or 64-byte swizzle
   extern __shared__ uint8_t raw_smem[];
-  __shared__ TcShared<NR> sh;
-  __shared__ int64_t prefix[kTcThreads + 1];
+  __shared__ TcShared<NR, QB> sh;
+  static_assert(sizeof(sh) + S::kBytes + 512 <= 113 * 1024, "two CTAs per SM");
   uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint8_t* q_s = sm + NS * S::kSlot;
-  uint8_t* p_s = q_s + S::kQ;
+  uint8_t* p_s = q_s + QB * S::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, nc = gridDim.x;
+  int64_t* prefix = reinterpret_cast<int64_t*>(p_s);  // before the first item only
 
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.full[i], 1 + 32);
+      mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    for (int i = 0; i < kTcScaleRing; ++i) mbar_init(&sh.scales_full[i], 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_empty[i], kTcSoftmax);
+      mbar_init(&sh.s_empty[i], S::kSoftmax);
+      mbar_init(&sh.p_full[i], S::kSoftmax);
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.q_full[i], 32);
+      mbar_init(&sh.q_empty[i], 1 + S::kSoftmax);
     }
-    mbar_init(&sh.p_full, kTcSoftmax);
-    mbar_init(&sh.pv_done, 1);
-    mbar_init(&sh.q_full, kTcSoftmax);
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, S::kAlloc);
     tmem_relinquish();
     if (lane == 0) tma_prefetch_map(&map);
@@ -174,379 +215,513 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   Segment g;
   if (work) g = find_segment(a, prefix, plan.u0, plan.u1);
   if (tid == 0) write_join(a, plan, work ? &g : nullptr, c);
-  const int bs = min(a.bs, kAttnTile);      // rows of one copy
-  const int pages = kAttnTile / bs;
+  __syncthreads();
+  const int tiles = int(plan.u1 - plan.u0);
+  auto last_of_cta = [&](const Segment& s) { return s.u + (s.t1 - s.t0) >= plan.u1; };
 
-  if (work && warp == 4) {
+  if (work && warp == kTmaWarp) {
     // ---------------------------------------------------------------- TMA
-    int i = 0, j = 0;  // ring position, tile
-    int id = -1;
-    auto page_id = [&](const Segment& s, int k) {
-      const int pos = tile_start(s.s, k) + lane * bs;
-      return lane < pages && needed(s.s, pos, bs) ? a.bt[int64_t(s.b) * a.MB + pos / a.bs] : -2;
+    const int bs = min(a.bs, kAttnTile);  // rows of one copy
+    const int pages = kAttnTile / bs;
+    auto page_id = [&](int k) {
+      const int pos = tile_start(g.s, k) + lane * bs;
+      return lane < pages && needed(g.s, pos, bs) ? a.bt[int64_t(g.b) * a.MB + pos / a.bs] : -2;
     };
-    id = page_id(g, g.t0);
-    for (;;) {
-      for (int k = g.t0; k < g.t1; ++k, ++j) {
-        const int cur = id;
-        const int pos = tile_start(g.s, k) + lane * bs;
-        if (k + 1 < g.t1) id = page_id(g, k + 1);  // in flight while this tile's slots are awaited
-        const bool ok = cur >= 0 && cur < a.NB;
-        if (cur != -2 && !ok && a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * uint32_t(bs) * D;
-        const int c1 = pos % a.bs;
-        const int plane = ok ? cur * a.planes_per_block + a.plane0 + g.h : 0;
-#pragma unroll
-        for (int v = 0; v < 2; ++v, ++i) {
-          const int slot = i % NS;
-          tc_wait(&sh.empty[slot], ((i / NS) & 1) ^ 1, &sh.abort, a.err);
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
-          __syncwarp();
-          if (ok)
-            tma_tile_3d(sm + slot * S::kSlot + lane * bs * D, &map, 0, c1, plane + v * a.H,
-                        &sh.full[slot]);
-          bool copying = false;
-          if (v == 1 && lane < pages) {
-            float* ks = &sh.ks[j % kTcScaleRing][lane];
-            float* vs = &sh.vs[j % kTcScaleRing][lane];
-            if (ok) {
-              const float* sp = a.scales + cur * a.block_scales + g.h;
-              cp_async4(ks, sp);
-              cp_async4(vs, sp + a.H);
-              copying = true;
-            } else {
-              // a block that cannot be read: NaN scores; one that is not needed: zeros
-              *ks = cur == -2 ? 0.0f : __uint_as_float(0x7fc00000u);
-              *vs = 0.0f;
-            }
-          }
-          if (copying) cp_async_arrive(&sh.full[slot]);
-          else mbar_arrive(&sh.full[slot]);
+    // Order of the copies: K_0, then K_(j+1) and V_j in turn, the order in which the
+    // products take them; a V tile loaded with its K tile would hold its slot for longer.
+    int k = g.t0, loads = 0;
+    TcRing<NS> ring;
+    TcRing<kTcScaleRing> sring;
+    int id = page_id(k), v_c1 = 0, v_plane = 0;  // V of the tile before
+    uint32_t v_ok = 0;
+    auto load = [&](uint32_t mask, int c1, int plane) {
+      tc_wait(&sh.empty[ring.at], ring.phase ^ 1, &sh.abort, a.err);
+      if (lane == 0)
+        mbar_arrive_expect_tx(&sh.full[ring.at], __popc(mask) * uint32_t(bs) * D);
+      __syncwarp();
+      if (mask >> lane & 1)
+        tma_tile_3d(sm + ring.at * S::kSlot + lane * bs * D, &map, 0, c1, plane,
+                    &sh.full[ring.at]);
+      ring.next();
+      ++loads;
+    };
+    for (int j = 0; j < tiles; ++j) {
+      const int cur = id;
+      const bool ok = cur >= 0 && cur < a.NB;
+      const int c1 = a.bs <= kAttnTile ? 0 : tile_start(g.s, k) % a.bs;
+      const int plane = ok ? cur * a.planes_per_block + a.plane0 + g.h : 0;
+      const float* sp = a.scales + (ok ? cur * a.block_scales : 0) + g.h;
+      const int p0 = tile_start(g.s, k);
+      const bool open = __all_sync(0xffffffffu, ok || lane >= pages) && tile_open(a, g.s, p0);
+      // with one query buffer an item's first scores wait for the outputs before them
+      const bool v_first = QB == 1 && k == g.t0;
+      if (++k == g.t1 && j + 1 < tiles) {
+        next_segment(a, g, plan.u1);
+        k = g.t0;
+      }
+      if (j + 1 < tiles) id = page_id(k);  // in flight while this tile's slots are awaited
+      if (cur != -2 && !ok && a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (j > 0 && v_first) load(v_ok, v_c1, v_plane);
+      load(mask, c1, plane);
+      bool copying = false;
+      if (lane < pages) {
+        float* ks = &sh.ks[sring.at][lane];
+        float* vs = &sh.vs[sring.at][lane];
+        if (ok) {
+          cp_async4(ks, sp);
+          cp_async4(vs, sp + a.H);
+          copying = true;
+        } else {
+          // a block that cannot be read: NaN scores; one that is not needed: zeros
+          *ks = cur == -2 ? 0.0f : __uint_as_float(0x7fc00000u);
+          *vs = 0.0f;
         }
       }
-      if (g.u + (g.t1 - g.t0) >= plan.u1) break;
-      next_segment(a, g, plan.u1);
-      id = page_id(g, g.t0);
+      if (lane == 31) sh.tile[sring.at] = make_int2(p0, open);  // pages <= 16: it copies nothing
+      if (copying) cp_async_arrive(&sh.scales_full[sring.at]);
+      else mbar_arrive(&sh.scales_full[sring.at]);
+      sring.next();
+      if (j > 0 && !v_first) load(v_ok, v_c1, v_plane);
+      v_ok = mask;
+      v_c1 = c1;
+      v_plane = plane + a.H;
     }
+    load(v_ok, v_c1, v_plane);
     // the copies land before the CTA may leave
-    for (int x = max(0, i - NS); x < i; ++x)
+    for (int x = max(0, loads - NS); x < loads; ++x)
       tc_wait(&sh.full[x % NS], (x / NS) & 1, &sh.abort, a.err);
-  } else if (work && warp == 5) {
+  } else if (work && warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
       constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, 2 * NR);
       constexpr uint32_t idesc_o = tc_idesc(0, 1, 1, 1, 128, NO);
-      const uint32_t ring = smem_u32(sm);
-      const uint64_t q_desc = tc_desc(smem_u32(q_s), 16, 8 * D, kSwz);
-      const uint64_t p_desc = tc_desc(smem_u32(p_s), 128, 2048, 0);
-      int j = 0, seg = 0;
-      auto scores = [&](int t, bool first) {
-        const int i = 2 * t, slot = i % NS, buf = t % NB;
-        if (first) tc_wait(&sh.q_full, seg & 1, &sh.abort, a.err);
-        tc_wait(&sh.full[slot], (i / NS) & 1, &sh.abort, a.err);
-        tc_wait(&sh.s_empty[buf], ((t / NB) & 1) ^ 1, &sh.abort, a.err);
+      const uint64_t slot0 = tc_desc(smem_u32(sm), 16, 8 * D, kSwz);
+      const uint64_t v_slot0 = tc_desc(smem_u32(sm), 0, 8 * D, kSwz);
+      const uint64_t q0 = tc_desc(smem_u32(q_s), 16, 8 * D, kSwz);
+      const uint64_t p0 = tc_desc(smem_u32(p_s), 128, 2048, 0);
+      int k = g.t0;  // tile of the next scores
+      TcRing<NS> ring;
+      TcRing<SB> sbuf;
+      TcRing<QB> qbuf;
+      TcRing<PB> pbuf;
+      auto scores = [&]() {
+        if (k == g.t0) tc_wait(&sh.q_full[qbuf.at], qbuf.phase, &sh.abort, a.err);
+        tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
+        tc_wait(&sh.s_empty[sbuf.at], sbuf.phase ^ 1, &sh.abort, a.err);
         tc_fence_after();
-        const uint64_t k_desc = tc_desc(ring + slot * S::kSlot, 16, 8 * D, kSwz);
+        const uint64_t k_desc = slot0 + ring.at * (S::kSlot / 16);
+        const uint64_t q_desc = q0 + qbuf.at * (S::kQ / 16);
 #pragma unroll
         for (int x = 0; x < D / 32; ++x)
-          tc_mma_f8(tmem + buf * 2 * NR, k_desc + 2 * x, q_desc + 2 * x, idesc_s, x > 0);
-        tc_commit(&sh.empty[slot]);
-        tc_commit(&sh.s_full[buf]);
+          tc_mma_f8(tmem + sbuf.at * 2 * NR, k_desc + 2 * x, q_desc + 2 * x, idesc_s, x > 0);
+        tc_commit(&sh.empty[ring.at]);
+        tc_commit(&sh.s_full[sbuf.at]);
+        ring.next();
+        sbuf.next();
+        if (++k == g.t1) {
+          tc_commit(&sh.q_empty[qbuf.at]);
+          if (!last_of_cta(g)) next_segment(a, g, plan.u1);
+          k = g.t0;
+          qbuf.next();
+        }
       };
-      auto outputs = [&](int t, bool first) {
-        const int i = 2 * t + 1, slot = i % NS;
-        tc_wait(&sh.full[slot], (i / NS) & 1, &sh.abort, a.err);
-        tc_wait(&sh.p_full, t & 1, &sh.abort, a.err);
+      auto outputs = [&](bool first) {
+        tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
+        tc_wait(&sh.p_full[pbuf.at], pbuf.phase, &sh.abort, a.err);
         tc_fence_after();
         // V as stored: D contiguous, groups of 8 keys 8 D bytes apart. With D = 64 the
         // second half of M repeats the first (offset 0) and is ignored.
-        const uint64_t v_desc = tc_desc(ring + slot * S::kSlot, 0, 8 * D, kSwz);
+        const uint64_t v_desc = v_slot0 + ring.at * (S::kSlot / 16);
+        const uint64_t p_desc = p0 + pbuf.at * (S::kP / 16);
 #pragma unroll
         for (int x = 0; x < kAttnTile / 32; ++x)
 #pragma unroll
           for (int m = 0; m < 3; ++m)
-            tc_mma_f8(tmem + NB * 2 * NR, v_desc + x * (32 * D / 16),
+            tc_mma_f8(tmem + SB * 2 * NR, v_desc + x * (32 * D / 16),
                       p_desc + (m * NO * kAttnTile + x * 512) / 16, idesc_o,
                       !(first && x == 0 && m == 0));
-        tc_commit(&sh.empty[slot]);
-        tc_commit(&sh.pv_done);
+        tc_commit(&sh.empty[ring.at]);
+        tc_commit(&sh.pv_done[pbuf.at]);
+        ring.next();
+        pbuf.next();
       };
-      for (;;) {
-        scores(j, true);
-        for (int k = g.t0; k < g.t1; ++k, ++j) {
-          if (k + 1 < g.t1) scores(j + 1, false);
-          outputs(j, k == g.t0);
-        }
-        ++seg;
-        if (g.u + (g.t1 - g.t0) >= plan.u1) break;
-        next_segment(a, g, plan.u1);
+      bool first = true;  // is tile j the first of its item?
+      scores();
+      for (int j = 0; j < tiles; ++j) {
+        // the order of the copies
+        const bool next_first = k == g.t0, v_first = QB == 1 && next_first;
+        if (j + 1 < tiles && !v_first) scores();
+        outputs(first);
+        if (j + 1 < tiles && v_first) scores();
+        first = next_first;
       }
     }
     __syncwarp();
-  } else if (work) {
-    // ---------------------------------------------------------------- softmax
-    const uint32_t lane_addr = tmem + (uint32_t(warp * 32) << 16);
-    const uint32_t o_addr = lane_addr + NB * 2 * NR;
-    int j = 0;
-    for (;;) {
-      // queries of this item -> two e4m3 terms each
-      bar_softmax();  // the previous item's rows are done with
-      constexpr int kPerRow = D / 8;  // threads of a row, eight numbers each
+  } else if (work && warp == kQWarp) {
+    // ---------------------------------------------------------------- queries
+    // of each item, as two e4m3 terms a number: kPerRow lanes a row, 8 numbers each
+    constexpr int kPerRow = D / 8, kRows = 32 / kPerRow;
+    const int d8 = lane % kPerRow;
+    TcRing<QB> qbuf;
+    for (;; qbuf.next()) {
+      const int qb = qbuf.at;
+      tc_wait(&sh.q_empty[qb], qbuf.phase ^ 1, &sh.abort, a.err);
+      uint8_t* qs = q_s + qb * S::kQ;
 #pragma unroll 1
-      for (int r0 = 0; r0 < NR; r0 += kTcSoftmax / kPerRow) {
-        const int r = r0 + tid / kPerRow, d8 = tid % kPerRow;
-        if (r < NR) {
-          const int row = g.rb * a.rows_per_block + r;
+      for (int r0 = 0; r0 < NR; r0 += 8) {
+        uint4 w[8 / kRows];
+        int64_t off[8 / kRows];
+        int t[8 / kRows];
+#pragma unroll
+        for (int x = 0; x < 8 / kRows; ++x) {
+          const int r = r0 + x * kRows + lane / kPerRow, row = g.rb * a.rows_per_block + r;
           const bool live = r < a.rows_per_block && row < a.R;
-          const int t = live ? row / a.G : a.T;
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          t[x] = live ? row / a.G : a.T;
+          off[x] = live ? (int64_t(g.b) * a.T + t[x]) * a.H * a.G + g.h * a.G + (row - t[x] * a.G)
+                        : -1;
+          w[x] = make_uint4(0u, 0u, 0u, 0u);
           if (live)
-            w = *reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(a.q) +
-                ((int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G)) * D + d8 * 8);
+            w[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                   off[x] * D + d8 * 8);
+        }
+#pragma unroll
+        for (int x = 0; x < 8 / kRows; ++x) {
+          const int r = r0 + x * kRows + lane / kPerRow;
           float f[8];
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
           uint32_t top = 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            f[2 * x] = __uint_as_float(u[x] << 16);
-            f[2 * x + 1] = __uint_as_float(u[x] & 0xffff0000u);
-            top = max(top, max((u[x] << 16) & 0x7fffffffu, u[x] & 0x7fff0000u));
+          for (int y = 0; y < 4; ++y) {
+            f[2 * y] = __uint_as_float(u[y] << 16);
+            f[2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
+            top = max(top, max((u[y] << 16) & 0x7fffffffu, u[y] & 0x7fff0000u));
           }
 #pragma unroll
           for (int o = kPerRow / 2; o > 0; o >>= 1)
-            top = max(top, __shfl_xor_sync(__activemask(), top, o));
-          // |x| 2^-e in [128, 256) at the largest; e also stays in range for bf16 subnormals
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // |f| 2^-e in [128, 256) at the largest; e stays in range for bf16 subnormals
           const int e = max(int(top >> 23) - 127 - 7, -110);
-          const float down = q8_pow2(-e > 120 ? 120 : -e);
-          const float up = q8_pow2(e);
+          const float down = q8_pow2(-e), up = q8_pow2(e);
           float lo[8];
           uint32_t hw[2], lw[2];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) f[x] *= down;
+          for (int y = 0; y < 8; ++y) f[y] *= down;
           hw[0] = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
           hw[1] = f32x4_to_e4m3(f[4], f[5], f[6], f[7]);
           e4m3x4_to_f32(hw[0], lo);
           e4m3x4_to_f32(hw[1], lo + 4);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) lo[x] = f[x] - lo[x];
+          for (int y = 0; y < 8; ++y) lo[y] = f[y] - lo[y];
           lw[0] = f32x4_to_e4m3(lo[0], lo[1], lo[2], lo[3]);
           lw[1] = f32x4_to_e4m3(lo[4], lo[5], lo[6], lo[7]);
-          auto put = [&](int rr, const uint32_t* x) {
-            const int sw = D == 128 ? rr & 7 : (rr >> 1) & 3;
-            const int chunk = (d8 >> 1) ^ sw;
-            *reinterpret_cast<uint2*>(q_s + rr * D + chunk * 16 + (d8 & 1) * 8) =
-                make_uint2(x[0], x[1]);
+          auto put = [&](int rr, const uint32_t* v) {
+            const int chunk = (d8 >> 1) ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
+            *reinterpret_cast<uint2*>(qs + rr * D + chunk * 16 + (d8 & 1) * 8) =
+                make_uint2(v[0], v[1]);
           };
           put(r, hw);
           put(NR + r, lw);
           if (d8 == 0) {
             // a row with an infinity or a NaN: its scores are NaN
-            sh.row_c[r] = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : up * a.scale_log2;
-            sh.row_m[r] = live ? kTcUnset : 0.0f;
-            sh.row_t[r] = t;
-            sh.row_mask[r] = a.tree && live ? a.tree[int64_t(g.b) * a.T + t] : 0u;
+            sh.row_c[qb][r] =
+                top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : up * a.scale_log2;
+            sh.row_t[qb][r] = t[x];
+            sh.row_off[qb][r] = off[x];
+            sh.row_mask[qb][r] =
+                a.tree && off[x] >= 0 ? a.tree[int64_t(g.b) * a.T + t[x]] : 0u;
           }
         }
       }
+      if (lane == 0) sh.seg[qb] = g;
       fence_async_smem();
-      mbar_arrive(&sh.q_full);
-      bar_softmax();
-      float l[NR];
+      mbar_arrive(&sh.q_full[qb]);
+      if (last_of_cta(g)) break;
+      next_segment(a, g, plan.u1);
+    }
+  } else if (work && warp < kTmaWarp) {
+    // ---------------------------------------------------------------- softmax
+    const int group = warp >> 2, gw = warp & 3, key = tid & 127;
+    const int col0 = group * S::W;        // this group's rows
+    constexpr int chunks = S::W / 8;      // eights of them
+    const uint32_t lane_addr = tmem + (uint32_t(gw * 32) << 16) + col0;
+    const uint32_t o_addr = lane_addr + SB * 2 * NR;
+    const int bsh = a.bs >= kAttnTile ? 7 : 31 - __clz(a.bs);
+    // tile's scales; its V slot in the ring (needed only where rows of V are cleared)
+    TcRing<kTcScaleRing> sring;
+    TcRing<SB> sbuf;
+    TcRing<PB> pbuf;
+    TcRing<QB> qbuf;
+    int j = 0;
+    auto wait_outputs = [&]() {  // of the latest tile whose P has been given
+      const int at = PB == 1 ? 0 : pbuf.at ^ 1;
+      tc_wait(&sh.pv_done[at], PB == 1 || pbuf.at == 0 ? pbuf.phase ^ 1 : pbuf.phase, &sh.abort,
+              a.err);
+      tc_fence_after();
+    };
+    for (;; qbuf.next()) {
+      const int qb = qbuf.at;
+      tc_wait(&sh.q_full[qb], qbuf.phase, &sh.abort, a.err);
+      const Segment& g = sh.seg[qb];  // read where it is needed: registers are scarce here
+      {
+        // V scales are taken relative to the first tile's largest, a power of two
+        tc_wait(&sh.scales_full[sring.at], sring.phase, &sh.abort, a.err);
+        const int x =
+            __reduce_max_sync(0xffffffffu, scale_binade(sh.vs[sring.at][key >> bsh]));
+        if (lane == 0) sh.part_v[group][gw] = x;
+        if (key < 8 * chunks)
+          sh.row_nm[col0 + key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
+        bar_group(group);
+      }
+      const int vref = max(max(sh.part_v[group][0], sh.part_v[group][1]),
+                           max(sh.part_v[group][2], sh.part_v[group][3]));
+      const float vdown = q8_pow2(-vref);
+      uint64_t l[S::W / 2];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-      int vref = 0;
+      for (int r = 0; r < S::W / 2; ++r) l[r] = 0;
 
-      for (int k = g.t0; k < g.t1; ++k, ++j) {
-        const int p0 = tile_start(g.s, k), pos = p0 + tid;
-        const int buf = j % NB, vi = 2 * j + 1, vslot = vi % NS;
-        tc_wait(&sh.s_full[buf], (j / NB) & 1, &sh.abort, a.err);
-        tc_wait(&sh.full[vslot], (vi / NS) & 1, &sh.abort, a.err);
-        tc_fence_after();
-        const float vs = sh.vs[j % kTcScaleRing][tid / bs];
-        const float ks =
-            fabsf(vs) <= FLT_MAX ? sh.ks[j % kTcScaleRing][tid / bs] : __uint_as_float(0x7fc00000u);
-        float z[NR];
-#pragma unroll
-        for (int r = 0; r < NR; r += 8) {
-          float lo[8];
-          tmem_ld8(lane_addr + buf * 2 * NR + r, z + r);
-          tmem_ld8(lane_addr + buf * 2 * NR + NR + r, lo);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 8; ++x) z[r + x] += lo[x];
-        }
-        tc_fence_before();
-        mbar_arrive(&sh.s_empty[buf]);
-#pragma unroll
-        for (int r = 0; r < NR; ++r) z[r] = z[r] * ks * sh.row_c[r];
-        bool keep = ks == ks;  // does the token's V row enter the product?
-        if (!tile_open(a, g.s, p0)) {
-          keep = keep && needed(g.s, pos, 1);
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (!sees(a, g.s, sh.row_mask[r], sh.row_t[r], pos)) z[r] = -INFINITY;
-        }
-        if (!keep) {
-          // what lies there is not a number of this row (and 0 * NaN is NaN)
-          uint4* v = reinterpret_cast<uint4*>(sm + vslot * S::kSlot + tid * D);
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (k == g.t0) {
-          // V scales are taken relative to this tile's largest, a power of two
-          const int x = __reduce_max_sync(0xffffffffu, scale_binade(vs));
-          if (lane == 0) sh.part_v[warp] = x;
-          bar_softmax();
-          vref = max(max(sh.part_v[0], sh.part_v[1]), max(sh.part_v[2], sh.part_v[3]));
-        }
-        const float vr = vs * q8_pow2(-vref);
+      const int t0 = g.t0, t1 = g.t1;
+      for (int k = t0; k < t1; ++k, ++j) {
+        tc_wait(&sh.scales_full[sring.at], sring.phase, &sh.abort, a.err);
+        const float vs = sh.vs[sring.at][key >> bsh];
+        float ks = sh.ks[sring.at][key >> bsh];
+        const int2 info = sh.tile[sring.at];
+        const bool open = info.y;
+        sring.next();
+        if (!(fabsf(vs) <= FLT_MAX)) ks = __uint_as_float(0x7fc00000u);
+        const float vr = vs * vdown;
         const float lv = float(scale_binade(vr));  // vr <= 2^lv
-        bool over = k == g.t0;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) over = over || z[r] - sh.row_m[r] > kTcSlack - lv;
-        if (bar_softmax_or(over)) {
-          // move the references to this tile's maxima
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const float x = warp_max(z[r] == z[r] ? z[r] + lv : -INFINITY);
-            if (lane == (r & 31)) sh.part[warp][r] = x;
+        const uint64_t ks2 = f2_pack(ks, ks);
+        uint32_t seen = ~0u;  // by each row of the group
+        if (!open) {
+          seen = 0;
+#pragma unroll 1
+          for (int r = 0; r < 8 * chunks; ++r)
+            seen |= uint32_t(sees(a, g.s, sh.row_mask[qb][col0 + r], sh.row_t[qb][col0 + r],
+                                  info.x + key))
+                    << r;
+        }
+        uint64_t y[S::W / 2];  // exponents relative to the references
+        tc_wait(&sh.s_full[sbuf.at], sbuf.phase, &sh.abort, a.err);
+        tc_fence_after();
+        const uint32_t s_addr = lane_addr + sbuf.at * 2 * NR;
+        // s k c (- m) of rows 8 x .. 8 x + 7; the scores come in two loads
+        auto load = [&](int x, float* hi, float* lo) {
+          tmem_ld8(s_addr + 8 * x, hi);
+          tmem_ld8(s_addr + NR + 8 * x, lo);
+        };
+        auto exponents = [&](int x, const float* hi, const float* lo, uint64_t* o, bool relative) {
+          const ulonglong2* cp = reinterpret_cast<const ulonglong2*>(&sh.row_c[qb][col0 + 8 * x]);
+          const ulonglong2* mp = reinterpret_cast<const ulonglong2*>(&sh.row_nm[col0 + 8 * x]);
+          const ulonglong2 c0 = cp[0], c1 = cp[1];
+          ulonglong2 m0 = make_ulonglong2(0, 0), m1 = m0;
+          if (relative) {
+            m0 = mp[0];
+            m1 = mp[1];
           }
-          bar_softmax();
-          for (int r = tid; r < NR; r += kTcSoftmax) {
-            const float old = sh.row_m[r];
+          const uint64_t cc[4] = {c0.x, c0.y, c1.x, c1.y}, mm[4] = {m0.x, m0.y, m1.x, m1.y};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t s2 = f2_add(f2_pack(hi[2 * q], hi[2 * q + 1]),
+                                       f2_pack(lo[2 * q], lo[2 * q + 1]));
+            o[q] = f2_fma(f2_mul(s2, ks2), cc[q], mm[q]);
+          }
+          if (!open) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float e0, e1;
+              f2_unpack(o[q], e0, e1);
+              if (!(seen >> (8 * x + 2 * q) & 1u)) e0 = -INFINITY;
+              if (!(seen >> (8 * x + 2 * q + 1) & 1u)) e1 = -INFINITY;
+              o[q] = f2_pack(e0, e1);
+            }
+          }
+        };
+        bool moved = false;
+        for (;;) {
+          if (k > t0 || moved) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < S::W / 8; x += 2) {  // two loads in flight
+              float h0[8], l0[8], h1[8], l1[8];
+              if (x < chunks) load(x, h0, l0);
+              if (x + 1 < chunks) load(x + 1, h1, l1);
+              tmem_wait_ld();
+              if (x < chunks) {
+                exponents(x, h0, l0, y + 4 * x, true);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  top = fmaxf(top, fmaxf(f2_lo(y[4 * x + q]), f2_hi(y[4 * x + q])));
+              }
+              if (x + 1 < chunks) {
+                exponents(x + 1, h1, l1, y + 4 * x + 4, true);
+#pragma unroll
+                for (int q = 4; q < 8; ++q)
+                  top = fmaxf(top, fmaxf(f2_lo(y[4 * x + q]), f2_hi(y[4 * x + q])));
+              }
+            }
+            if (moved || !bar_group_or(group, top > kTcSlack - lv)) break;
+          }
+          // move the references to this tile's maxima
+          moved = true;
+#pragma unroll 1
+          for (int x = 0; x < chunks; ++x) {
+            float hi[8], lo[8];
+            uint64_t z[4];
+            load(x, hi, lo);
+            tmem_wait_ld();
+            exponents(x, hi, lo, z, false);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f2_unpack(z[q], hi[2 * q], hi[2 * q + 1]);
+            // fmaxf drops a NaN score: it makes its row's sum NaN by itself
+            const float m = reduce8(hi, lane, [](float u, float v) { return fmaxf(u, v); },
+                                    [&](float v) { return v == v ? v + lv : -INFINITY; });
+            if ((lane & 3) == 0) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = m;
+          }
+          bar_group(group);
+          if (key < 8 * chunks) {
+            const int r = col0 + key;
+            const float old = -sh.row_nm[r];
             const float m = fmaxf(fmaxf(fmaxf(sh.part[0][r], sh.part[1][r]),
                                         fmaxf(sh.part[2][r], sh.part[3][r])), old);
-            sh.row_m[r] = m;
+            sh.row_nm[r] = -m;
             sh.row_a[r] = ex2_approx(old - m);
           }
-          bar_softmax();
+          bar_group(group);
 #pragma unroll
-          for (int r = 0; r < NR; ++r) l[r] *= sh.row_a[r];
-          if (k > g.t0) {
-            tc_wait(&sh.pv_done, (j - 1) & 1, &sh.abort, a.err);
-            tc_fence_after();
-#pragma unroll
-            for (int r = 0; r < NR; r += 8) {
+          for (int r = 0; r < S::W / 2; ++r)
+            l[r] = f2_mul(l[r], f2_pack(sh.row_a[col0 + 2 * r], sh.row_a[col0 + 2 * r + 1]));
+          if (k > t0) {
+            wait_outputs();  // of the tile before
+#pragma unroll 1
+            for (int x = 0; x < chunks; ++x) {
               float o[8];
-              tmem_ld8(o_addr + r, o);
+              tmem_ld8(o_addr + 8 * x, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] *= sh.row_a[r + x];
-              tmem_st8(o_addr + r, o);
+              for (int q = 0; q < 8; ++q) o[q] *= sh.row_a[col0 + 8 * x + q];
+              tmem_st8(o_addr + 8 * x, o);
             }
             tmem_wait_st();
           }
         }
-        if (j > 0) tc_wait(&sh.pv_done, (j - 1) & 1, &sh.abort, a.err);  // P may be replaced
-        const float lift = vr * kTcLift;
+        tc_fence_before();
+        mbar_arrive(&sh.s_empty[sbuf.at]);
+        sbuf.next();
+        tc_wait(&sh.pv_done[pbuf.at], pbuf.phase ^ 1, &sh.abort, a.err);  // P may be replaced
+        const uint64_t lift = f2_pack(vr * kTcLift, vr * kTcLift);
+        uint8_t* p_to = p_s + pbuf.at * S::kP + key * 16;
 #pragma unroll
-        for (int r0 = 0; r0 < NR; r0 += 16) {
-          uint32_t t0[4], t1[4], t2[4];
+        for (int x = 0; x < S::W / 8; ++x) {
+          if (x < chunks) {
+            uint32_t t[3][2];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = r0 + 4 * x;
-            if (r < NR) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t h[2];
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float p[2];
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                  const int rr = r + 2 * y + w;
-                  p[w] = ex2_approx(z[rr] - sh.row_m[rr]);
-                  l[rr] += p[w];
-                  p[w] *= lift;
-                }
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[y]) : "f"(p[1]), "f"(p[0]));
-                h[y] = (h[y] + 0x00020002u) & 0xfffcfffcu;  // 9 bits, half up
+              for (int w = 0; w < 2; ++w) {
+                const int i = 4 * x + 2 * q + w;
+                float e0, e1;
+                f2_unpack(y[i], e0, e1);
+                const uint64_t p = f2_pack(ex2_approx(e0), ex2_approx(e1));
+                l[i] = f2_add(l[i], p);
+                f2_unpack(f2_mul(p, lift), e0, e1);
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[w]) : "f"(e1), "f"(e0));
+                h[w] = (h[w] + 0x00020002u) & 0xfffcfffcu;  // 9 bits, half up
               }
               auto rest = [](uint32_t v) {
                 uint32_t o;
                 asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o) : "r"(v), "r"(v & 0xff00ff00u));
                 return o;
               };
-              t0[x] = __byte_perm(h[0], h[1], 0x7531);
+              t[0][q] = __byte_perm(h[0], h[1], 0x7531);
               h[0] = rest(h[0]);
               h[1] = rest(h[1]);
-              t1[x] = __byte_perm(h[0], h[1], 0x7531);
+              t[1][q] = __byte_perm(h[0], h[1], 0x7531);
               h[0] = rest(h[0]);
               h[1] = rest(h[1]);
-              t2[x] = __byte_perm(h[0], h[1], 0x7531);
+              t[2][q] = __byte_perm(h[0], h[1], 0x7531);
             }
+            const int col = col0 + 8 * x;
+            uint8_t* d = p_to + (col >> 4) * 2048 + (col & 8);
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+              *reinterpret_cast<uint2*>(d + m * NO * kAttnTile) = make_uint2(t[m][0], t[m][1]);
           }
-          uint8_t* d = p_s + (r0 / 16) * 2048 + tid * 16;
-          auto put = [&](uint8_t* to, const uint32_t* t) {
-            if (r0 + 16 <= NR) *reinterpret_cast<uint4*>(to) = make_uint4(t[0], t[1], t[2], t[3]);
-            else *reinterpret_cast<uint2*>(to) = make_uint2(t[0], t[1]);
-          };
-          put(d, t0);
-          put(d + NO * kAttnTile, t1);
-          put(d + 2 * NO * kAttnTile, t2);
+        }
+        if (!open && group == 0 && (!(ks == ks) || !needed(g.s, info.x + key, 1))) {
+          // what lies in this V row is not a number of the sequence (and 0 * NaN is NaN)
+          const bool k_after = j + 1 < tiles && !(QB == 1 && k + 1 == t1);
+          const int vi = 2 * j + (k_after ? 2 : 1);  // loads before it: 0 .. j or j + 1 of K
+          tc_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, a.err);
+          uint4* v = reinterpret_cast<uint4*>(sm + vi % NS * S::kSlot + key * D);
+#pragma unroll 1
+          for (int x = 0; x < D / 16; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();
         tc_fence_before();
-        mbar_arrive(&sh.p_full);
+        mbar_arrive(&sh.p_full[pbuf.at]);
+        pbuf.next();
       }
 
       // ------------------------------------------------------------ the item's end
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float x = l[r];
+      for (int x = 0; x < S::W / 8; ++x) {
+        if (x < chunks) {
+          float v[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == (r & 31)) sh.part[warp][r] = x;
+          for (int q = 0; q < 4; ++q) f2_unpack(l[4 * x + q], v[2 * q], v[2 * q + 1]);
+          const float sum = reduce8(v, lane, [](float u, float w) { return u + w; },
+                                    [](float u) { return u; });
+          if ((lane & 3) == 0) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = sum;
+        }
       }
-      bar_softmax();
+      bar_group(group);
       const bool whole = g.t0 == 0 && g.t1 == g.s.tiles;
       const int64_t slot = 2 * c + (g.u == plan.u0 ? 0 : 1);
-      const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
-      for (int r = tid; r < NR; r += kTcSoftmax) {
+      if (key < 8 * chunks) {
+        const int r = col0 + key;
         const float sum = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
         // A part is left with its sum in [1, 2): references of parts differ by their V
         // scales, so a sum by itself may be as far from 1 as those.
         const int e = sum > 0.0f && sum <= FLT_MAX ? int(__float_as_uint(sum) >> 23) - 127 : 0;
-        sh.row_a[r] = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : q8_pow2(-e);
-        if (!whole && r < rows)
-          a.stats[slot * a.rows_per_block + r] =
-              make_float2(sum == 0.0f ? -INFINITY : sh.row_m[r] + float(e), sum * q8_pow2(-e));
+        const float unlift = q8_pow2(vref) / kTcLift;
+        sh.row_a[r] = (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : q8_pow2(-e)) * unlift;
+        if (!whole && r < a.rows_per_block)
+          a.stats[slot * a.rows_per_block + r] = make_float2(
+              sum == 0.0f ? -INFINITY : -sh.row_nm[r] + float(e), sum * q8_pow2(-e));
       }
-      bar_softmax();
-      tc_wait(&sh.pv_done, (j - 1) & 1, &sh.abort, a.err);
-      tc_fence_after();
-      const float unlift = q8_pow2(vref) / kTcLift;
+      bar_group(group);
+      wait_outputs();
 #pragma unroll 1
-      for (int r0 = 0; r0 < NR; r0 += 8) {
+      for (int x = 0; x < chunks; ++x) {
         float o[8];
-        tmem_ld8(o_addr + r0, o);
+        tmem_ld8(o_addr + 8 * x, o);
         tmem_wait_ld();
-        if (D == 128 || tid < D) {
+        if (D == 128 || key < D) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int r = r0 + x;
-            if (r < rows) {
-              const float v = o[x] * sh.row_a[r] * unlift;
-              if (whole) {
-                const int row = g.rb * a.rows_per_block + r, t = sh.row_t[r];
-                static_cast<__nv_bfloat16*>(
-                    a.out)[((int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G)) * D +
-                           tid] = __float2bfloat16(v);
-              } else {
-                a.parts[(slot * a.rows_per_block + r) * D + tid] = v;
-              }
+          for (int q = 0; q < 8; ++q) {
+            const int r = col0 + 8 * x + q;
+            const int64_t off = sh.row_off[qb][r];
+            if (off >= 0) {
+              const float v = o[q] * sh.row_a[r];
+              if (whole) static_cast<__nv_bfloat16*>(a.out)[off * D + key] = __float2bfloat16(v);
+              else a.parts[(slot * a.rows_per_block + r) * D + key] = v;
             }
           }
         }
       }
-      tc_fence_before();  // the next item's products overwrite O after its q_full and p_full
-      if (g.u + (g.t1 - g.t0) >= plan.u1) break;
-      next_segment(a, g, plan.u1);
+      const bool last = last_of_cta(g);
+      tc_fence_before();  // the next item's products overwrite O after its p_full
+      mbar_arrive(&sh.q_empty[qb]);
+      if (last) break;
+      bar_group(group);  // row_a, row_nm, part: every thread is done with the item
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, S::kAlloc);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, S::kAlloc);
 }
 
 // ------------------------------------------------------------------ host
@@ -588,7 +763,7 @@ int launch_shape(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return SPEC_ECUDA;
-  return launch_pdl(kern, dim3(nc), dim3(kTcThreads), smem, st, a, map);
+  return launch_pdl(kern, dim3(nc), dim3(TcShape<NR, D>::kThreads), smem, st, a, map);
 }
 
 template <int D>
@@ -596,7 +771,6 @@ int launch_rows(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t 
   const int r = a.rows_per_block;
   if (r <= 8) return launch_shape<8, D>(a, map, nc, st);
   if (r <= 16) return launch_shape<16, D>(a, map, nc, st);
-  if (r <= 24) return launch_shape<24, D>(a, map, nc, st);
   if (r <= 32) return launch_shape<32, D>(a, map, nc, st);
   if (r <= 48) return launch_shape<48, D>(a, map, nc, st);
   return launch_shape<64, D>(a, map, nc, st);
