@@ -30,7 +30,7 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 template <class T>
 __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(const AttnArgs a) {
   extern __shared__ float sm[];
-  __shared__ int64_t prefix[kAnyThreads + 1];
+  __shared__ int64_t prefix[kAnyThreads + 1], warp_sum[kAnyThreads / 32];
   const int ld = a.D + 1;
   float* qs = sm;                    // [32][D]
   float* ks = qs + kAnyRows * a.D;   // [32][D + 1]
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(const AttnArgs a)
   pdl_trigger();
   pdl_wait();
   write_empty_rows<T>(a, c, nc);
-  const AttnPlan plan = attn_plan(a, prefix, nc, c);
+  const AttnPlan plan = attn_plan(a, prefix, warp_sum, nc, c);
   if (plan.u0 >= plan.u1) {
     if (tid == 0) write_join(a, plan, nullptr, c);
     return;

@@ -49,26 +49,49 @@ constexpr int kTcMaxPages = 16;             // blocks of one tile
 constexpr float kTcUnset = 1e30f;           // minus the reference of a row that has seen no key
 constexpr float kTcSlack = 8.0f;            // binades by which keys may exceed the reference
 constexpr float kTcLift = 64.0f;            // 1 enters as 2^6: 2^6 2^8 < 2^16, e5m2's range
-constexpr int kTcSmem = 107 * 1024;         // dynamic, of one CTA: two per SM
+constexpr int kTcSmem = 113 * 1024 - 512;   // of one CTA, two per SM
 
+template <int NR, int QB>
+struct TcShared {
+  alignas(16) float row_c[QB][NR];  // query row's scale * softmax_scale * log2(e)
+  alignas(16) float row_nm[NR];     // minus the reference of the exponentials
+  alignas(16) float row_a[NR];      // rescale factor, then that of the output
+  alignas(16) float part[4][NR];    // the warps' maxima, then sums
+  alignas(16) float zero[NR];
+  uint64_t row_to[NR];              // where the row's outputs go, 0: nowhere
+  Segment seg[QB];                  // the items that the queries belong to
+  int64_t row_off[QB][NR];          // row of q and out, -1: none
+  int row_t[QB][NR];                // query (T for rows that do not exist)
+  uint32_t row_mask[QB][NR];
+  alignas(16) float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
+  int2 tile[kTcScaleRing];  // first position; whether every query sees every key
+  uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full,
+      pv_done, q_full[2], q_empty[2];
+  int64_t warp_sum[12];
+  uint32_t tmem;
+  int abort;
+};
+
+// Softmax threads: one group of 128 (a thread a key) up to 24 rows, beyond that two
+// groups with half the rows each, as a thread holds an exponent and a sum per row.
 template <int NR, int D>
 struct TcShape {
   static constexpr int NO = (NR + 15) / 16 * 16;
-  static constexpr int kGroups = NR > 8 ? 2 : 1;           // softmax groups
-  static constexpr int W = NR / kGroups;                   // rows of a group
+  static constexpr int kGroups = NR > 24 ? 2 : 1;
   static constexpr int kSoftmax = 128 * kGroups;
-  static constexpr int kThreads = kSoftmax + 96;
+  static constexpr int kThreads = kSoftmax + 128;
+  static constexpr int W = NR / kGroups;                   // rows of a group
   static constexpr int kSlot = kAttnTile * D;
   static constexpr int kQ = 2 * NR * D;
   static constexpr int kP = 3 * NO * kAttnTile;
   static constexpr int kQBufs = NR <= 48 ? 2 : 1;          // two where four slots still fit
-  static constexpr int kPBufs = 1;
-  static constexpr int kFit = (kTcSmem - kQBufs * kQ - kPBufs * kP - 1024) / kSlot;
+  static constexpr int kSmall = kQBufs * kQ + kP + int(sizeof(TcShared<NR, kQBufs>));
+  static constexpr int kFit = (kTcSmem - kSmall) / kSlot;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   static constexpr int kSBufs = 4 * NR + NO <= 256 ? 2 : 1;
   static constexpr int kCols = kSBufs * 2 * NR + NO;
   static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
-  static constexpr size_t kBytes = size_t(kSlots) * kSlot + kQBufs * kQ + kPBufs * kP + 1024;
+  static constexpr size_t kBytes = size_t(kSlots) * kSlot + kSmall;
   static_assert(kCols <= 256 && kSlots >= 3, "two CTAs per SM");
   static_assert(size_t(kP) >= (kThreads + 1) * 8, "the plan's sums lie there first");
 };
@@ -84,24 +107,6 @@ struct TcRing {
       phase ^= 1;
     }
   }
-};
-
-template <int NR, int QB>
-struct TcShared {
-  alignas(16) float row_c[QB][NR];  // query row's scale * softmax_scale * log2(e)
-  alignas(16) float row_nm[NR];    // minus the reference of the exponentials
-  alignas(16) float row_a[NR];     // rescale factor, then that of the output
-  alignas(16) float part[4][NR];   // the warps' maxima, then sums
-  Segment seg[QB];                 // the items that the queries belong to
-  int64_t row_off[QB][NR];          // row of q and out, -1: none
-  int row_t[QB][NR];                // query (T for rows that do not exist)
-  uint32_t row_mask[QB][NR];
-  float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
-  int2 tile[kTcScaleRing];  // first position; whether every query sees every key
-  int part_v[2][4];
-  uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full[2], q_empty[2];
-  uint32_t tmem;
-  int abort;
 };
 
 // Bounded wait. Once one has given up, every wait returns at once: the roles
@@ -141,42 +146,145 @@ __device__ __forceinline__ int scale_binade(float x) {
   return max(-100, min(100, e));
 }
 
-// Eight rows reduced over the warp's keys: lanes exchange halves of the rows until
-// each holds one (7 shuffles), then the four lanes of a row finish it. Lane i
-// returns row reduce8_row(i).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// N times eight rows summed over the warp's keys: lanes exchange halves of the rows
+// until each holds one (7 shuffles), then the four lanes of a row finish it. Lane i
+// has row reduce8_row(i) of each eight in v[.][0].
 __device__ __forceinline__ int reduce8_row(int lane) {
   return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
 }
-template <class Op, class Map>
-__device__ __forceinline__ float reduce8(float* v, int lane, Op op, Map map) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) v[q] = map(v[q]);
+template <int N>
+__device__ __forceinline__ void reduce8(float (*v)[8], int lane) {
 #pragma unroll
   for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
-    for (int q = 0; q < n; ++q) {
-      const float give = up ? v[q] : v[q + n], keep = up ? v[q + n] : v[q];
-      v[q] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    for (int x = 0; x < N; ++x)
+#pragma unroll
+      for (int q = 0; q < n; ++q) {
+        const float give = up ? v[x][q] : v[x][q + n], keep = up ? v[x][q + n] : v[x][q];
+        v[x][q] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+  }
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int x = 0; x < N; ++x) v[x][0] += __shfl_xor_sync(0xffffffffu, v[x][0], o);
+}
+
+// Which of the rows [col0, col0 + w) of an item see position p, as bits. Rows are
+// ordered by query, so those of a chain are a range of them.
+__device__ __forceinline__ uint32_t seen_rows(const AttnArgs& a, const Segment& g,
+                                              const uint32_t* row_mask, const int* row_t, int p,
+                                              int col0, int w) {
+  const RowSpan& s = g.s;
+  if (p >= s.end) return 0u;
+  if (a.tree && p >= s.L) {
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int r = 0; r < w; ++r)
+      m |= uint32_t(row_t[col0 + r] < s.n && (row_mask[col0 + r] >> (p - s.L) & 1u)) << r;
+    return m;
+  }
+  const int first = max(0, p - s.L);
+  const int end = a.window == 0 || p < a.sinks ? s.n : max(0, min(s.n, p - s.L + a.window));
+  const int base = g.rb * a.rows_per_block + col0;
+  const int lo = max(0, first * a.G - base), hi = min(w, end * a.G - base);
+  if (hi <= lo) return 0u;
+  return (hi == 32 ? ~0u : (1u << hi) - 1u) & (~0u << lo);
+}
+
+// An item's queries as two e4m3 terms a number, by warp w of n: kPerRow lanes a row,
+// 8 numbers each; and what the softmax needs to know of the rows. One copy of the
+// code for its two callers, the next rows' loads in flight.
+template <int NR, int D, class Shared>
+__device__ __noinline__ void prepare_rows(const AttnArgs& a, Shared& sh, const Segment& g,
+                                          uint8_t* qs, int qb, int w, int n) {
+  constexpr int kPerRow = D / 8, kRows = 32 / kPerRow;
+  const int lane = threadIdx.x & 31, d8 = lane % kPerRow;
+  struct Row {
+    uint4 x;
+    int64_t off;
+    int t;
+  };
+  auto fetch = [&](int r) {
+    Row o;
+    const int row = g.rb * a.rows_per_block + r;
+    const bool live = r < a.rows_per_block && row < a.R;
+    o.t = live ? row / a.G : a.T;
+    o.off = live ? (int64_t(g.b) * a.T + o.t) * a.H * a.G + g.h * a.G + (row - o.t * a.G) : -1;
+    o.x = make_uint4(0u, 0u, 0u, 0u);
+    if (live)
+      o.x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + o.off * D +
+                                            d8 * 8);
+    return o;
+  };
+  int r = w * kRows + lane / kPerRow;
+  Row next = fetch(r);
+#pragma unroll 1
+  for (int i = w * kRows; i < NR; i += n * kRows) {
+    const Row o = next;
+    const int row = r;
+    r += n * kRows;
+    if (i + n * kRows < NR) next = fetch(r);
+    float f[8], lo[8];
+    const uint32_t u[4] = {o.x.x, o.x.y, o.x.z, o.x.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      f[2 * y] = __uint_as_float(u[y] << 16);
+      f[2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
+      top = max(top, max((u[y] << 16) & 0x7fffffffu, u[y] & 0x7fff0000u));
+    }
+#pragma unroll
+    for (int s = kPerRow / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+    // |f| 2^-e in [128, 256) at the largest; e stays in range for bf16 subnormals
+    const int e = max(int(top >> 23) - 127 - 7, -110);
+    const float down = q8_pow2(-e);
+    uint32_t hw[2], lw[2];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) f[y] *= down;
+    hw[0] = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
+    hw[1] = f32x4_to_e4m3(f[4], f[5], f[6], f[7]);
+    e4m3x4_to_f32(hw[0], lo);
+    e4m3x4_to_f32(hw[1], lo + 4);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) lo[y] = f[y] - lo[y];
+    lw[0] = f32x4_to_e4m3(lo[0], lo[1], lo[2], lo[3]);
+    lw[1] = f32x4_to_e4m3(lo[4], lo[5], lo[6], lo[7]);
+    auto put = [&](int rr, const uint32_t* v) {
+      const int chunk = (d8 >> 1) ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
+      *reinterpret_cast<uint2*>(qs + rr * D + chunk * 16 + (d8 & 1) * 8) = make_uint2(v[0], v[1]);
+    };
+    put(row, hw);
+    put(NR + row, lw);
+    if (d8 == 0) {
+      // a row with an infinity or a NaN: its scores are NaN
+      sh.row_c[qb][row] =
+          top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
+      sh.row_t[qb][row] = o.t;
+      sh.row_off[qb][row] = o.off;
+      sh.row_mask[qb][row] = a.tree && o.off >= 0 ? a.tree[int64_t(g.b) * a.T + o.t] : 0u;
     }
   }
-  v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
-  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 template <int NR, int D>
 __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     attn_tc_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map) {
   using S = TcShape<NR, D>;
-  constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs, QB = S::kQBufs, PB = S::kPBufs;
+  constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs, QB = S::kQBufs;
   constexpr int kTmaWarp = S::kSoftmax / 32, kMmaWarp = kTmaWarp + 1, kQWarp = kTmaWarp + 2;
   constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // TMA and operands: 128- or 64-byte swizzle
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ TcShared<NR, QB> sh;
-  static_assert(sizeof(sh) + S::kBytes + 512 <= 113 * 1024, "two CTAs per SM");
-  uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t sm[];  // ring, queries, P, the rest
   uint8_t* q_s = sm + NS * S::kSlot;
   uint8_t* p_s = q_s + QB * S::kQ;
+  TcShared<NR, QB>& sh = *reinterpret_cast<TcShared<NR, QB>*>(p_s + S::kP);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, nc = gridDim.x;
   int64_t* prefix = reinterpret_cast<int64_t*>(p_s);  // before the first item only
@@ -191,11 +299,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], S::kSoftmax);
-      mbar_init(&sh.p_full[i], S::kSoftmax);
-      mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.q_full[i], 32);
+      mbar_init(&sh.q_full[i], 64);
       mbar_init(&sh.q_empty[i], 1 + S::kSoftmax);
     }
+    mbar_init(&sh.p_full, S::kSoftmax);
+    mbar_init(&sh.pv_done, 1);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -204,19 +312,27 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     tmem_relinquish();
     if (lane == 0) tma_prefetch_map(&map);
   }
+  if (tid < NR) sh.zero[tid] = 0.0f;
+  if (tid < kTcScaleRing * kTcMaxPages) (&sh.vs[0][0])[tid] = 0.0f;  // pages that a tile does not have
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   pdl_wait();
   write_empty_rows<__nv_bfloat16>(a, c, nc);
-  const AttnPlan plan = attn_plan(a, prefix, nc, c);
+  const AttnPlan plan = attn_plan(a, prefix, sh.warp_sum, nc, c);
   const bool work = plan.u0 < plan.u1;
   Segment g;
   if (work) g = find_segment(a, prefix, plan.u0, plan.u1);
   if (tid == 0) write_join(a, plan, work ? &g : nullptr, c);
   __syncthreads();
   const int tiles = int(plan.u1 - plan.u0);
+  if (work && (warp < kTmaWarp || warp >= kQWarp)) {
+    // the first item's queries
+    prepare_rows<NR, D>(a, sh, g, q_s, 0, warp < kTmaWarp ? warp : warp - 2, S::kSoftmax / 32 + 2);
+    fence_async_smem();
+    asm volatile("bar.sync 3, %0;" ::"n"(S::kSoftmax + 64) : "memory");
+  }
   auto last_of_cta = [&](const Segment& s) { return s.u + (s.t1 - s.t0) >= plan.u1; };
 
   if (work && warp == kTmaWarp) {
@@ -304,9 +420,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       TcRing<NS> ring;
       TcRing<SB> sbuf;
       TcRing<QB> qbuf;
-      TcRing<PB> pbuf;
-      auto scores = [&]() {
-        if (k == g.t0) tc_wait(&sh.q_full[qbuf.at], qbuf.phase, &sh.abort, a.err);
+      uint32_t p_phase = 0;
+      auto scores = [&]() {  // returns whether the tile is its item's first
+        const bool first = k == g.t0;
+        if (first) tc_wait(&sh.q_full[qbuf.at], qbuf.phase, &sh.abort, a.err);
         tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
         tc_wait(&sh.s_empty[sbuf.at], sbuf.phase ^ 1, &sh.abort, a.err);
         tc_fence_after();
@@ -325,374 +442,289 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           k = g.t0;
           qbuf.next();
         }
+        return first;
       };
       auto outputs = [&](bool first) {
         tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
-        tc_wait(&sh.p_full[pbuf.at], pbuf.phase, &sh.abort, a.err);
+        tc_wait(&sh.p_full, p_phase, &sh.abort, a.err);
+        p_phase ^= 1;
         tc_fence_after();
         // V as stored: D contiguous, groups of 8 keys 8 D bytes apart. With D = 64 the
         // second half of M repeats the first (offset 0) and is ignored.
         const uint64_t v_desc = v_slot0 + ring.at * (S::kSlot / 16);
-        const uint64_t p_desc = p0 + pbuf.at * (S::kP / 16);
 #pragma unroll
         for (int x = 0; x < kAttnTile / 32; ++x)
 #pragma unroll
           for (int m = 0; m < 3; ++m)
             tc_mma_f8(tmem + SB * 2 * NR, v_desc + x * (32 * D / 16),
-                      p_desc + (m * NO * kAttnTile + x * 512) / 16, idesc_o,
+                      p0 + (m * NO * kAttnTile + x * 512) / 16, idesc_o,
                       !(first && x == 0 && m == 0));
         tc_commit(&sh.empty[ring.at]);
-        tc_commit(&sh.pv_done[pbuf.at]);
+        tc_commit(&sh.pv_done);
         ring.next();
-        pbuf.next();
       };
-      bool first = true;  // is tile j the first of its item?
-      scores();
+      bool first = scores();
       for (int j = 0; j < tiles; ++j) {
         // the order of the copies
-        const bool next_first = k == g.t0, v_first = QB == 1 && next_first;
-        if (j + 1 < tiles && !v_first) scores();
+        const bool v_first = QB == 1 && k == g.t0;
+        bool next = false;
+        if (j + 1 < tiles && !v_first) next = scores();
         outputs(first);
-        if (j + 1 < tiles && v_first) scores();
-        first = next_first;
+        if (j + 1 < tiles && v_first) next = scores();
+        first = next;
       }
     }
     __syncwarp();
-  } else if (work && warp == kQWarp) {
+  } else if (work && warp >= kQWarp) {
     // ---------------------------------------------------------------- queries
-    // of each item, as two e4m3 terms a number: kPerRow lanes a row, 8 numbers each
-    constexpr int kPerRow = D / 8, kRows = 32 / kPerRow;
-    const int d8 = lane % kPerRow;
+    // of the next item while this one is worked on; the first item's were taken by all
     TcRing<QB> qbuf;
-    for (;; qbuf.next()) {
+    for (bool first = true;; first = false) {
       const int qb = qbuf.at;
-      tc_wait(&sh.q_empty[qb], qbuf.phase ^ 1, &sh.abort, a.err);
-      uint8_t* qs = q_s + qb * S::kQ;
-#pragma unroll 1
-      for (int r0 = 0; r0 < NR; r0 += 8) {
-        uint4 w[8 / kRows];
-        int64_t off[8 / kRows];
-        int t[8 / kRows];
-#pragma unroll
-        for (int x = 0; x < 8 / kRows; ++x) {
-          const int r = r0 + x * kRows + lane / kPerRow, row = g.rb * a.rows_per_block + r;
-          const bool live = r < a.rows_per_block && row < a.R;
-          t[x] = live ? row / a.G : a.T;
-          off[x] = live ? (int64_t(g.b) * a.T + t[x]) * a.H * a.G + g.h * a.G + (row - t[x] * a.G)
-                        : -1;
-          w[x] = make_uint4(0u, 0u, 0u, 0u);
-          if (live)
-            w[x] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                   off[x] * D + d8 * 8);
-        }
-#pragma unroll
-        for (int x = 0; x < 8 / kRows; ++x) {
-          const int r = r0 + x * kRows + lane / kPerRow;
-          float f[8];
-          const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            f[2 * y] = __uint_as_float(u[y] << 16);
-            f[2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
-            top = max(top, max((u[y] << 16) & 0x7fffffffu, u[y] & 0x7fff0000u));
-          }
-#pragma unroll
-          for (int o = kPerRow / 2; o > 0; o >>= 1)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // |f| 2^-e in [128, 256) at the largest; e stays in range for bf16 subnormals
-          const int e = max(int(top >> 23) - 127 - 7, -110);
-          const float down = q8_pow2(-e), up = q8_pow2(e);
-          float lo[8];
-          uint32_t hw[2], lw[2];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) f[y] *= down;
-          hw[0] = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
-          hw[1] = f32x4_to_e4m3(f[4], f[5], f[6], f[7]);
-          e4m3x4_to_f32(hw[0], lo);
-          e4m3x4_to_f32(hw[1], lo + 4);
-#pragma unroll
-          for (int y = 0; y < 8; ++y) lo[y] = f[y] - lo[y];
-          lw[0] = f32x4_to_e4m3(lo[0], lo[1], lo[2], lo[3]);
-          lw[1] = f32x4_to_e4m3(lo[4], lo[5], lo[6], lo[7]);
-          auto put = [&](int rr, const uint32_t* v) {
-            const int chunk = (d8 >> 1) ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
-            *reinterpret_cast<uint2*>(qs + rr * D + chunk * 16 + (d8 & 1) * 8) =
-                make_uint2(v[0], v[1]);
-          };
-          put(r, hw);
-          put(NR + r, lw);
-          if (d8 == 0) {
-            // a row with an infinity or a NaN: its scores are NaN
-            sh.row_c[qb][r] =
-                top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : up * a.scale_log2;
-            sh.row_t[qb][r] = t[x];
-            sh.row_off[qb][r] = off[x];
-            sh.row_mask[qb][r] =
-                a.tree && off[x] >= 0 ? a.tree[int64_t(g.b) * a.T + t[x]] : 0u;
-          }
-        }
+      if (!first) {
+        tc_wait(&sh.q_empty[qb], qbuf.phase ^ 1, &sh.abort, a.err);
+        prepare_rows<NR, D>(a, sh, g, q_s + qb * S::kQ, qb, warp - kQWarp, 2);
+        fence_async_smem();
       }
-      if (lane == 0) sh.seg[qb] = g;
-      fence_async_smem();
+      if (lane == 0 && warp == kQWarp) sh.seg[qb] = g;
       mbar_arrive(&sh.q_full[qb]);
+      qbuf.next();
       if (last_of_cta(g)) break;
       next_segment(a, g, plan.u1);
     }
   } else if (work && warp < kTmaWarp) {
     // ---------------------------------------------------------------- softmax
-    const int group = warp >> 2, gw = warp & 3, key = tid & 127;
-    const int col0 = group * S::W;        // this group's rows
-    constexpr int chunks = S::W / 8;      // eights of them
+    constexpr int W = S::W, chunks = W / 8;  // rows of a group, in eights
+    const int group = warp >> 2, gw = warp & 3, key = tid & 127, col0 = group * W;
+    float* const nm = sh.row_nm + col0;
+    float* const ra = sh.row_a + col0;
     const uint32_t lane_addr = tmem + (uint32_t(gw * 32) << 16) + col0;
     const uint32_t o_addr = lane_addr + SB * 2 * NR;
-    const int bsh = a.bs >= kAttnTile ? 7 : 31 - __clz(a.bs);
-    // tile's scales; its V slot in the ring (needed only where rows of V are cleared)
-    TcRing<kTcScaleRing> sring;
-    TcRing<SB> sbuf;
-    TcRing<PB> pbuf;
+    const int page = key >> (a.bs >= kAttnTile ? 7 : 31 - __clz(a.bs));
     TcRing<QB> qbuf;
-    int j = 0;
-    auto wait_outputs = [&]() {  // of the latest tile whose P has been given
-      const int at = PB == 1 ? 0 : pbuf.at ^ 1;
-      tc_wait(&sh.pv_done[at], PB == 1 || pbuf.at == 0 ? pbuf.phase ^ 1 : pbuf.phase, &sh.abort,
-              a.err);
-      tc_fence_after();
+    int j = 0;  // tile of the CTA
+    auto wait_outputs = [&]() {  // of the tile before
+      tc_wait(&sh.pv_done, (j & 1) ^ 1, &sh.abort, a.err);
     };
     for (;; qbuf.next()) {
       const int qb = qbuf.at;
       tc_wait(&sh.q_full[qb], qbuf.phase, &sh.abort, a.err);
       const Segment& g = sh.seg[qb];  // read where it is needed: registers are scarce here
+      const int j_first = j, j_end = j + (g.t1 - g.t0);
+      if (key < W) nm[key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
+      bar_group(group);
+      // V scales are taken relative to the first tile's largest, a power of two
+      int vref = 0;
+      tc_wait(&sh.scales_full[j % kTcScaleRing], j / kTcScaleRing & 1, &sh.abort, a.err);
       {
-        // V scales are taken relative to the first tile's largest, a power of two
-        tc_wait(&sh.scales_full[sring.at], sring.phase, &sh.abort, a.err);
-        const int x =
-            __reduce_max_sync(0xffffffffu, scale_binade(sh.vs[sring.at][key >> bsh]));
-        if (lane == 0) sh.part_v[group][gw] = x;
-        if (key < 8 * chunks)
-          sh.row_nm[col0 + key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
-        bar_group(group);
-      }
-      const int vref = max(max(sh.part_v[group][0], sh.part_v[group][1]),
-                           max(sh.part_v[group][2], sh.part_v[group][3]));
-      const float vdown = q8_pow2(-vref);
-      uint64_t l[S::W / 2];
+        float x = 0.0f;
 #pragma unroll
-      for (int r = 0; r < S::W / 2; ++r) l[r] = 0;
+        for (int i = 0; i < kTcMaxPages; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(&sh.vs[j % kTcScaleRing][i]);
+          x = fmaxf(fmaxf(x, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+        }
+        vref = scale_binade(x);
+      }
+      const float vdown = q8_pow2(-vref);
+      float2 l[W / 2];
+#pragma unroll
+      for (int r = 0; r < W / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
 
-      const int t0 = g.t0, t1 = g.t1;
-      for (int k = t0; k < t1; ++k, ++j) {
-        tc_wait(&sh.scales_full[sring.at], sring.phase, &sh.abort, a.err);
-        const float vs = sh.vs[sring.at][key >> bsh];
-        float ks = sh.ks[sring.at][key >> bsh];
-        const int2 info = sh.tile[sring.at];
+#pragma unroll 1
+      for (; j < j_end; ++j) {
+        const int se = j % kTcScaleRing, sb = SB == 2 ? j & 1 : 0;
+        tc_wait(&sh.scales_full[se], j / kTcScaleRing & 1, &sh.abort, a.err);
+        const float vs = sh.vs[se][page];
+        float ks = sh.ks[se][page];
+        const int2 info = sh.tile[se];
         const bool open = info.y;
-        sring.next();
         if (!(fabsf(vs) <= FLT_MAX)) ks = __uint_as_float(0x7fc00000u);
         const float vr = vs * vdown;
         const float lv = float(scale_binade(vr));  // vr <= 2^lv
-        const uint64_t ks2 = f2_pack(ks, ks);
-        uint32_t seen = ~0u;  // by each row of the group
-        if (!open) {
-          seen = 0;
-#pragma unroll 1
-          for (int r = 0; r < 8 * chunks; ++r)
-            seen |= uint32_t(sees(a, g.s, sh.row_mask[qb][col0 + r], sh.row_t[qb][col0 + r],
-                                  info.x + key))
-                    << r;
-        }
-        uint64_t y[S::W / 2];  // exponents relative to the references
-        tc_wait(&sh.s_full[sbuf.at], sbuf.phase, &sh.abort, a.err);
+        const float2 ks2 = make_float2(ks, ks);
+        const uint32_t seen = open ? ~0u : seen_rows(a, g, sh.row_mask[qb], sh.row_t[qb],
+                                                     info.x + key, col0, W);
+        float2 y[W / 2];  // exponents relative to the references
+        tc_wait(&sh.s_full[sb], (SB == 2 ? j >> 1 : j) & 1, &sh.abort, a.err);
         tc_fence_after();
-        const uint32_t s_addr = lane_addr + sbuf.at * 2 * NR;
-        // s k c (- m) of rows 8 x .. 8 x + 7; the scores come in two loads
-        auto load = [&](int x, float* hi, float* lo) {
-          tmem_ld8(s_addr + 8 * x, hi);
-          tmem_ld8(s_addr + NR + 8 * x, lo);
-        };
-        auto exponents = [&](int x, const float* hi, const float* lo, uint64_t* o, bool relative) {
-          const ulonglong2* cp = reinterpret_cast<const ulonglong2*>(&sh.row_c[qb][col0 + 8 * x]);
-          const ulonglong2* mp = reinterpret_cast<const ulonglong2*>(&sh.row_nm[col0 + 8 * x]);
-          const ulonglong2 c0 = cp[0], c1 = cp[1];
-          ulonglong2 m0 = make_ulonglong2(0, 0), m1 = m0;
-          if (relative) {
-            m0 = mp[0];
-            m1 = mp[1];
-          }
-          const uint64_t cc[4] = {c0.x, c0.y, c1.x, c1.y}, mm[4] = {m0.x, m0.y, m1.x, m1.y};
+        const uint32_t s_addr = lane_addr + sb * 2 * NR;
+        // s k c (- m) of all rows; the scores come in two terms
+        auto exponents = [&](const float* minus) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint64_t s2 = f2_add(f2_pack(hi[2 * q], hi[2 * q + 1]),
-                                       f2_pack(lo[2 * q], lo[2 * q + 1]));
-            o[q] = f2_fma(f2_mul(s2, ks2), cc[q], mm[q]);
+          for (int x = 0; x < chunks; x += 2) {  // two loads in flight
+            const int n = x + 1 < chunks ? 2 : 1;
+            float hi[16], lo[16];
+            tmem_ld8(s_addr + 8 * x, hi);
+            tmem_ld8(s_addr + NR + 8 * x, lo);
+            if (n == 2) {
+              tmem_ld8(s_addr + 8 * x + 8, hi + 8);
+              tmem_ld8(s_addr + NR + 8 * x + 8, lo + 8);
+            }
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 2 * n; ++q) {
+              const float4 c4 = *reinterpret_cast<const float4*>(&sh.row_c[qb][col0 + 8 * x + 4 * q]);
+              const float4 m4 = *reinterpret_cast<const float4*>(minus + 8 * x + 4 * q);
+              const float2 s0 = __fadd2_rn(make_float2(hi[4 * q], hi[4 * q + 1]),
+                                           make_float2(lo[4 * q], lo[4 * q + 1]));
+              const float2 s1 = __fadd2_rn(make_float2(hi[4 * q + 2], hi[4 * q + 3]),
+                                           make_float2(lo[4 * q + 2], lo[4 * q + 3]));
+              y[4 * x + 2 * q] = __ffma2_rn(__fmul2_rn(s0, ks2), make_float2(c4.x, c4.y),
+                                            make_float2(m4.x, m4.y));
+              y[4 * x + 2 * q + 1] = __ffma2_rn(__fmul2_rn(s1, ks2), make_float2(c4.z, c4.w),
+                                                make_float2(m4.z, m4.w));
+            }
           }
           if (!open) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float e0, e1;
-              f2_unpack(o[q], e0, e1);
-              if (!(seen >> (8 * x + 2 * q) & 1u)) e0 = -INFINITY;
-              if (!(seen >> (8 * x + 2 * q + 1) & 1u)) e1 = -INFINITY;
-              o[q] = f2_pack(e0, e1);
+            for (int i = 0; i < W / 2; ++i) {
+              if (!(seen >> (2 * i) & 1u)) y[i].x = -INFINITY;
+              if (!(seen >> (2 * i + 1) & 1u)) y[i].y = -INFINITY;
             }
           }
         };
-        bool moved = false;
+        // Usually one pass: relative to the references, none of which has to move. The
+        // first tile and one that exceeds them take the plain scores (again).
+        bool relative = j > j_first;
         for (;;) {
-          if (k > t0 || moved) {
-            float top = -INFINITY;
+          exponents(relative ? nm : sh.zero);
+          if (!relative) break;
+          float top = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < S::W / 8; x += 2) {  // two loads in flight
-              float h0[8], l0[8], h1[8], l1[8];
-              if (x < chunks) load(x, h0, l0);
-              if (x + 1 < chunks) load(x + 1, h1, l1);
-              tmem_wait_ld();
-              if (x < chunks) {
-                exponents(x, h0, l0, y + 4 * x, true);
+          for (int i = 0; i < W / 2; ++i) top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+          if (!bar_group_or(group, top > kTcSlack - lv)) break;
+          relative = false;
+        }
+        if (!relative) {
+          // move the references to this tile's maxima (a NaN score is passed over: it makes
+          // its row's sum NaN by itself)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                  top = fmaxf(top, fmaxf(f2_lo(y[4 * x + q]), f2_hi(y[4 * x + q])));
-              }
-              if (x + 1 < chunks) {
-                exponents(x + 1, h1, l1, y + 4 * x + 4, true);
-#pragma unroll
-                for (int q = 4; q < 8; ++q)
-                  top = fmaxf(top, fmaxf(f2_lo(y[4 * x + q]), f2_hi(y[4 * x + q])));
-              }
-            }
-            if (moved || !bar_group_or(group, top > kTcSlack - lv)) break;
-          }
-          // move the references to this tile's maxima
-          moved = true;
-#pragma unroll 1
-          for (int x = 0; x < chunks; ++x) {
-            float hi[8], lo[8];
-            uint64_t z[4];
-            load(x, hi, lo);
-            tmem_wait_ld();
-            exponents(x, hi, lo, z, false);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) f2_unpack(z[q], hi[2 * q], hi[2 * q + 1]);
-            // fmaxf drops a NaN score: it makes its row's sum NaN by itself
-            const float m = reduce8(hi, lane, [](float u, float v) { return fmaxf(u, v); },
-                                    [&](float v) { return v == v ? v + lv : -INFINITY; });
-            if ((lane & 3) == 0) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = m;
+          for (int i = 0; i < W / 2; ++i) {
+            const float m0 = warp_max(y[i].x + lv), m1 = warp_max(y[i].y + lv);
+            if (lane == i) *reinterpret_cast<float2*>(&sh.part[gw][col0 + 2 * i]) = make_float2(m0, m1);
           }
           bar_group(group);
-          if (key < 8 * chunks) {
-            const int r = col0 + key;
-            const float old = -sh.row_nm[r];
-            const float m = fmaxf(fmaxf(fmaxf(sh.part[0][r], sh.part[1][r]),
-                                        fmaxf(sh.part[2][r], sh.part[3][r])), old);
-            sh.row_nm[r] = -m;
-            sh.row_a[r] = ex2_approx(old - m);
+          if (key < W) {
+            const float* mp = sh.part[0] + col0 + key;
+            const float old = -nm[key];
+            const float m = fmaxf(fmaxf(fmaxf(mp[0], mp[NR]), fmaxf(mp[2 * NR], mp[3 * NR])), old);
+            nm[key] = -m;
+            ra[key] = ex2_approx(old - m);
           }
           bar_group(group);
 #pragma unroll
-          for (int r = 0; r < S::W / 2; ++r)
-            l[r] = f2_mul(l[r], f2_pack(sh.row_a[col0 + 2 * r], sh.row_a[col0 + 2 * r + 1]));
-          if (k > t0) {
-            wait_outputs();  // of the tile before
+          for (int i = 0; i < W / 2; ++i)
+            y[i] = __fadd2_rn(y[i], *reinterpret_cast<const float2*>(nm + 2 * i));
+          if (j > j_first) {
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i)
+              l[i] = __fmul2_rn(l[i], *reinterpret_cast<const float2*>(ra + 2 * i));
+            wait_outputs();
+            tc_fence_after();
 #pragma unroll 1
             for (int x = 0; x < chunks; ++x) {
               float o[8];
               tmem_ld8(o_addr + 8 * x, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] *= sh.row_a[col0 + 8 * x + q];
+              for (int q = 0; q < 8; ++q) o[q] *= ra[8 * x + q];
               tmem_st8(o_addr + 8 * x, o);
             }
             tmem_wait_st();
           }
         }
         tc_fence_before();
-        mbar_arrive(&sh.s_empty[sbuf.at]);
-        sbuf.next();
-        tc_wait(&sh.pv_done[pbuf.at], pbuf.phase ^ 1, &sh.abort, a.err);  // P may be replaced
-        const uint64_t lift = f2_pack(vr * kTcLift, vr * kTcLift);
-        uint8_t* p_to = p_s + pbuf.at * S::kP + key * 16;
+        mbar_arrive(&sh.s_empty[sb]);
+        wait_outputs();  // P may be replaced
+        const float2 lift = make_float2(vr * kTcLift, vr * kTcLift);
+        uint8_t* p_to = p_s + key * 16;
 #pragma unroll
-        for (int x = 0; x < S::W / 8; ++x) {
-          if (x < chunks) {
-            uint32_t t[3][2];
+        for (int x = 0; x < chunks; ++x) {
+          uint32_t t[3][2];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t h[2];
+          for (int q = 0; q < 2; ++q) {
+            uint32_t h[2];
 #pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const int i = 4 * x + 2 * q + w;
-                float e0, e1;
-                f2_unpack(y[i], e0, e1);
-                const uint64_t p = f2_pack(ex2_approx(e0), ex2_approx(e1));
-                l[i] = f2_add(l[i], p);
-                f2_unpack(f2_mul(p, lift), e0, e1);
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[w]) : "f"(e1), "f"(e0));
-                h[w] = (h[w] + 0x00020002u) & 0xfffcfffcu;  // 9 bits, half up
-              }
-              auto rest = [](uint32_t v) {
-                uint32_t o;
-                asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o) : "r"(v), "r"(v & 0xff00ff00u));
-                return o;
-              };
-              t[0][q] = __byte_perm(h[0], h[1], 0x7531);
-              h[0] = rest(h[0]);
-              h[1] = rest(h[1]);
-              t[1][q] = __byte_perm(h[0], h[1], 0x7531);
-              h[0] = rest(h[0]);
-              h[1] = rest(h[1]);
-              t[2][q] = __byte_perm(h[0], h[1], 0x7531);
+            for (int w = 0; w < 2; ++w) {
+              const int i = 4 * x + 2 * q + w;
+              const float2 p = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+              l[i] = __fadd2_rn(l[i], p);
+              const float2 v = __fmul2_rn(p, lift);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[w]) : "f"(v.y), "f"(v.x));
+              h[w] = (h[w] + 0x00020002u) & 0xfffcfffcu;  // 9 bits, half up
             }
-            const int col = col0 + 8 * x;
-            uint8_t* d = p_to + (col >> 4) * 2048 + (col & 8);
-#pragma unroll
-            for (int m = 0; m < 3; ++m)
-              *reinterpret_cast<uint2*>(d + m * NO * kAttnTile) = make_uint2(t[m][0], t[m][1]);
+            auto rest = [](uint32_t v) {
+              uint32_t o;
+              asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o) : "r"(v), "r"(v & 0xff00ff00u));
+              return o;
+            };
+            t[0][q] = __byte_perm(h[0], h[1], 0x7531);
+            h[0] = rest(h[0]);
+            h[1] = rest(h[1]);
+            t[1][q] = __byte_perm(h[0], h[1], 0x7531);
+            h[0] = rest(h[0]);
+            h[1] = rest(h[1]);
+            t[2][q] = __byte_perm(h[0], h[1], 0x7531);
           }
+          const int col = col0 + 8 * x;
+          uint8_t* d = p_to + (col >> 4) * 2048 + (col & 8);
+#pragma unroll
+          for (int m = 0; m < 3; ++m)
+            *reinterpret_cast<uint2*>(d + m * NO * kAttnTile) = make_uint2(t[m][0], t[m][1]);
         }
         if (!open && group == 0 && (!(ks == ks) || !needed(g.s, info.x + key, 1))) {
           // what lies in this V row is not a number of the sequence (and 0 * NaN is NaN)
-          const bool k_after = j + 1 < tiles && !(QB == 1 && k + 1 == t1);
+          const bool k_after = j + 1 < tiles && !(QB == 1 && j + 1 == j_end);
           const int vi = 2 * j + (k_after ? 2 : 1);  // loads before it: 0 .. j or j + 1 of K
           tc_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, a.err);
           uint4* v = reinterpret_cast<uint4*>(sm + vi % NS * S::kSlot + key * D);
 #pragma unroll 1
-          for (int x = 0; x < D / 16; ++x) v[x] = make_uint4(0u, 0u, 0u, 0u);
+          for (int x = 0; x < D / 16; ++x)  // the lanes start in different banks
+            v[(x + key) % (D / 16)] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_async_smem();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[pbuf.at]);
-        pbuf.next();
+        mbar_arrive(&sh.p_full);
       }
 
       // ------------------------------------------------------------ the item's end
+      {
+        float v[chunks][8];
 #pragma unroll
-      for (int x = 0; x < S::W / 8; ++x) {
-        if (x < chunks) {
-          float v[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) f2_unpack(l[4 * x + q], v[2 * q], v[2 * q + 1]);
-          const float sum = reduce8(v, lane, [](float u, float w) { return u + w; },
-                                    [](float u) { return u; });
-          if ((lane & 3) == 0) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = sum;
+        for (int i = 0; i < W / 2; ++i) {
+          v[i / 4][i % 4 * 2] = l[i].x;
+          v[i / 4][i % 4 * 2 + 1] = l[i].y;
         }
+        reduce8<chunks>(v, lane);
+        if ((lane & 3) == 0)
+#pragma unroll
+          for (int x = 0; x < chunks; ++x) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = v[x][0];
       }
       bar_group(group);
       const bool whole = g.t0 == 0 && g.t1 == g.s.tiles;
       const int64_t slot = 2 * c + (g.u == plan.u0 ? 0 : 1);
-      if (key < 8 * chunks) {
-        const int r = col0 + key;
-        const float sum = sh.part[0][r] + sh.part[1][r] + sh.part[2][r] + sh.part[3][r];
+      if (key < W) {
+        const float* mp = sh.part[0] + col0 + key;
+        const float sum = mp[0] + mp[NR] + mp[2 * NR] + mp[3 * NR];
         // A part is left with its sum in [1, 2): references of parts differ by their V
         // scales, so a sum by itself may be as far from 1 as those.
         const int e = sum > 0.0f && sum <= FLT_MAX ? int(__float_as_uint(sum) >> 23) - 127 : 0;
         const float unlift = q8_pow2(vref) / kTcLift;
-        sh.row_a[r] = (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : q8_pow2(-e)) * unlift;
-        if (!whole && r < a.rows_per_block)
-          a.stats[slot * a.rows_per_block + r] = make_float2(
-              sum == 0.0f ? -INFINITY : -sh.row_nm[r] + float(e), sum * q8_pow2(-e));
+        ra[key] = (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : q8_pow2(-e)) * unlift;
+        const int64_t off = sh.row_off[qb][col0 + key], part = slot * a.rows_per_block + col0 + key;
+        uint64_t to = 0;
+        if (off >= 0)
+          to = whole ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + off * D)
+                     : reinterpret_cast<uint64_t>(a.parts + part * D);
+        sh.row_to[col0 + key] = to;
+        if (!whole && off >= 0)
+          a.stats[part] = make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e),
+                                      sum * q8_pow2(-e));
       }
       bar_group(group);
       wait_outputs();
+      tc_fence_after();
+      const bool last = last_of_cta(g);
 #pragma unroll 1
       for (int x = 0; x < chunks; ++x) {
         float o[8];
@@ -701,17 +733,14 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         if (D == 128 || key < D) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const int r = col0 + 8 * x + q;
-            const int64_t off = sh.row_off[qb][r];
-            if (off >= 0) {
-              const float v = o[q] * sh.row_a[r];
-              if (whole) static_cast<__nv_bfloat16*>(a.out)[off * D + key] = __float2bfloat16(v);
-              else a.parts[(slot * a.rows_per_block + r) * D + key] = v;
-            }
+            const uint64_t to = sh.row_to[col0 + 8 * x + q];
+            const float v = o[q] * ra[8 * x + q];
+            if (to == 0) continue;
+            if (whole) reinterpret_cast<__nv_bfloat16*>(to)[key] = __float2bfloat16(v);
+            else reinterpret_cast<float*>(to)[key] = v;
           }
         }
       }
-      const bool last = last_of_cta(g);
       tc_fence_before();  // the next item's products overwrite O after its p_full
       mbar_arrive(&sh.q_empty[qb]);
       if (last) break;
@@ -771,6 +800,7 @@ int launch_rows(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t 
   const int r = a.rows_per_block;
   if (r <= 8) return launch_shape<8, D>(a, map, nc, st);
   if (r <= 16) return launch_shape<16, D>(a, map, nc, st);
+  if (r <= 24) return launch_shape<24, D>(a, map, nc, st);
   if (r <= 32) return launch_shape<32, D>(a, map, nc, st);
   if (r <= 48) return launch_shape<48, D>(a, map, nc, st);
   return launch_shape<64, D>(a, map, nc, st);

@@ -122,8 +122,10 @@ struct Segment {
   int64_t u;             // unit index of tile t0
 };
 
-// Every thread of the CTA; `prefix` holds blockDim.x + 1 tile counts in shared memory.
-__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix, int nc, int c) {
+// Every thread of the CTA; in shared memory `prefix` takes blockDim.x + 1 tile counts,
+// `warp_sum` one of each warp.
+__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix, int64_t* warp_sum,
+                                              int nc, int c) {
   const int per = (a.B + blockDim.x - 1) / blockDim.x;
   int64_t sum = 0;
   for (int i = 0; i < per; ++i) {
@@ -138,7 +140,6 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix
     const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  __shared__ int64_t warp_sum[32];
   if (lane == 31) warp_sum[threadIdx.x >> 5] = inc;
   __syncthreads();
   for (int w = 0; w < int(threadIdx.x >> 5); ++w) inc += warp_sum[w];
