@@ -373,36 +373,62 @@ def kv_commit_rollback(block_table, seq_lens, num_accepted, prov_blocks, kv_pool
         raise SpecError("kv_commit_rollback", st)
 
 
-def _q8_pool(kv_pool, kv_scales):
-    """Checks the 8-bit pool and its scales; returns the pool's shape."""
+# The calls below take a few microseconds on the device, so their arguments are checked with
+# few Python steps: _arg covers the usual case and leaves the message to _check.
+def _arg(t, name, ndim, dtype):
+    """The device pointer of a contiguous CUDA tensor of `ndim` dims and `dtype` (None: any)."""
+    try:
+        if t.is_cuda and (t.dtype is dtype or dtype is None) and t.ndim == ndim \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _check(t, name, ndim, dtype)
+    raise ValueError(f"{name} is not a usable tensor")
+
+
+def _vec(t, name, n):
+    """The pointer of an optional int32 [n] tensor."""
+    if t is None:
+        return None
     import torch
-    _check(kv_pool, "kv_pool", 6)
-    _check(kv_scales, "kv_scales", 4, torch.float32)
-    if kv_pool.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    p = _arg(t, name, 1, torch.int32)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    return p
+
+
+def _word(t, name):
+    """The pointer of an optional int32 tensor of at least one entry."""
+    if t is None:
+        return None
+    import torch
+    p = _arg(t, name, 1, torch.int32)
+    if t.shape[0] < 1:
+        raise ValueError(f"{name} must have an entry")
+    return p
+
+
+def _raw_stream(stream, device):
+    """cudaStream_t of `stream`, or of the current stream of the tensors' device."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _q8_pool(kv_pool, kv_scales):
+    """Checks the 8-bit pool and its scales; returns their pointers and the pool's shape."""
+    import torch
+    pool = _arg(kv_pool, "kv_pool", 6, None)
+    scales = _arg(kv_scales, "kv_scales", 4, torch.float32)
+    if kv_pool.dtype is not torch.float8_e4m3fn and kv_pool.dtype is not torch.uint8:
         raise TypeError(f"kv_pool must be float8_e4m3fn (or its uint8 bytes), got {kv_pool.dtype}")
-    if kv_pool.shape[2] != 2 or kv_scales.shape != kv_pool.shape[:4]:
+    shape = kv_pool.shape
+    if shape[2] != 2 or kv_scales.shape != shape[:4]:
         raise ValueError("kv_pool must be [num_blocks, layers, 2, kv_heads, block_size, head_dim] "
                          "and kv_scales [num_blocks, layers, 2, kv_heads]")
-    return kv_pool.shape
-
-
-def _rows(B, **named):
-    """Checks optional int32 [B] tensors."""
-    import torch
-    for name, t in named.items():
-        if t is not None:
-            _check(t, name, 1, torch.int32)
-            if t.shape[0] != B:
-                raise ValueError(f"{name} must have {B} entries, got {t.shape[0]}")
-
-
-def _one_word(**named):
-    import torch
-    for name, t in named.items():
-        if t is not None:
-            _check(t, name, 1, torch.int32)
-            if t.shape[0] < 1:
-                raise ValueError(f"{name} must have an entry")
+    return pool, scales, shape
 
 
 def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int = 0,
@@ -411,19 +437,18 @@ def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int 
     8-bit cache's `layer`: kv_pool [num_blocks, layers, 2, kv_heads, block_size, head_dim]
     float8_e4m3fn, kv_scales [num_blocks, layers, 2, kv_heads]. num_new: optional int32 [B]."""
     import torch
-    NB, NL, _, H, bs, D = _q8_pool(kv_pool, kv_scales)
-    _check(k, "k", 4)
-    _check(v, "v", 4, k.dtype)
-    _check(block_table, "block_table", 2, torch.int32)
+    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
+    kp = _arg(k, "k", 4, None)
+    vp = _arg(v, "v", 4, k.dtype)
+    bt = _arg(block_table, "block_table", 2, torch.int32)
     B, T, kh, kd = k.shape
-    if v.shape != k.shape or (kh, kd) != (H, D) or block_table.shape[0] != B:
+    rows, MB = block_table.shape
+    if v.shape != k.shape or kh != H or kd != D or rows != B:
         raise ValueError(f"k and v must be [B, T, {H}, {D}] and block_table [B, max_blocks]")
-    _rows(B, seq_lens=seq_lens, num_new=num_new)
-    _one_word(err_flag=err_flag)
-    st = lib().kv_q8_append(
-        _ptr(k), _ptr(v), _dtype_code(k), _ptr(kv_pool), _ptr(kv_scales), _ptr(block_table),
-        _ptr(seq_lens), _ptr(num_new), NB, NL, layer, H, D, bs, B, T, block_table.shape[1],
-        _stream(stream), _ptr(err_flag))
+    st = (_lib or lib()).kv_q8_append(
+        kp, vp, _dtype_code(k), pool, scales, bt, _vec(seq_lens, "seq_lens", B),
+        _vec(num_new, "num_new", B), NB, NL, layer, H, D, bs, B, T, MB,
+        _raw_stream(stream, k.device), _word(err_flag, "err_flag"))
     if st != SPEC_OK:
         raise SpecError("kv_q8_append", st)
 
@@ -437,17 +462,27 @@ def kv_q8_attention_workspace_bytes(T: int, num_q_heads: int, num_kv_heads: int,
 _attn_workspaces = {}
 
 
-def _attn_workspace(need, device, stream):
-    """A cached workspace of the attention, one per device and stream: calls on one stream are
-    ordered, calls on two may overlap."""
-    import torch
-    key = (device, stream.cuda_stream)
+def _attn_workspace(shape, device, raw, stream):
+    """(pointer, bytes) of a cached workspace, one per device and stream: calls on one stream
+    are ordered, calls on two may overlap."""
+    key = (shape, device.index, raw)
     ws = _attn_workspaces.get(key)
-    if ws is None or ws.numel() < need + 256:
-        if ws is not None:
-            ws.record_stream(stream)  # its last call may still be running
-        ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
-        _attn_workspaces[key] = ws
+    if ws is None:
+        import torch
+        need = kv_q8_attention_workspace_bytes(*shape)
+        if need == 0:
+            return None, 0  # an unsupported shape: the library call itself reports why
+        held = _attn_workspaces.get((device.index, raw))
+        if held is None or held.numel() < need + 256:
+            if held is not None:
+                # its last call may still be running
+                held.record_stream(stream or torch.cuda.current_stream(device))
+                for k in [k for k in _attn_workspaces if k[1:] == (device.index, raw)]:
+                    del _attn_workspaces[k]
+            held = torch.empty(need + 256, dtype=torch.uint8, device=device)
+            _attn_workspaces[(device.index, raw)] = held
+        off = (-held.data_ptr()) % 256
+        ws = _attn_workspaces[key] = held.data_ptr() + off, held.numel() - off
     return ws
 
 
@@ -458,36 +493,36 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
     """Attention of q [B, T, q_heads, head_dim] (positions seq_lens[b] + t) over the 8-bit cache
     (layout as kv_q8_append) into out, same shape and dtype (bf16 or fp32). softmax_scale defaults
     to head_dim ** -0.5; window / sinks: sliding window and always-visible first positions;
-    tree_mask: optional int32 [B, T], bit s of entry t lets query t see position seq_lens[b] + s."""
+    tree_mask: optional int32 [B, T], bit s of entry t lets query t see position seq_lens[b] + s.
+    workspace: a uint8 tensor of kv_q8_attention_workspace_bytes + 256; None: one that the
+    binding keeps for the stream."""
     import torch
-    NB, NL, _, H, bs, D = _q8_pool(kv_pool, kv_scales)
-    _check(q, "q", 4)
-    _check(out, "out", 4, q.dtype)
-    _check(block_table, "block_table", 2, torch.int32)
-    B, T, Hq, qd = q.shape
-    if out.shape != q.shape or qd != D or block_table.shape[0] != B:
+    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
+    qp = _arg(q, "q", 4, None)
+    op = _arg(out, "out", 4, q.dtype)
+    bt = _arg(block_table, "block_table", 2, torch.int32)
+    shape = q.shape
+    B, T, Hq, qd = shape
+    rows, MB = block_table.shape
+    if out.shape != shape or qd != D or rows != B:
         raise ValueError(f"q and out must be [B, T, q_heads, {D}] and block_table [B, max_blocks]")
-    _rows(B, seq_lens=seq_lens, num_new=num_new)
-    _one_word(err_flag=err_flag)
+    tm = None
     if tree_mask is not None:
-        _check(tree_mask, "tree_mask", 2, torch.int32)
+        tm = _arg(tree_mask, "tree_mask", 2, torch.int32)
         if tuple(tree_mask.shape) != (B, T):
             raise ValueError(f"tree_mask must be [{B}, {T}], got {tuple(tree_mask.shape)}")
+    device = q.device
+    raw = _raw_stream(stream, device)
     if workspace is None:
-        need = kv_q8_attention_workspace_bytes(T, Hq, H, D)
-        # an unsupported shape: the library call itself reports why
-        stream = stream or torch.cuda.current_stream()
-        workspace = _attn_workspace(need, q.device, stream) if need else None
-    if workspace is None:
-        wsp, wsn = ctypes.c_void_p(0), 0
+        wsp, wsn = _attn_workspace((T, Hq, H, D), device, raw, stream)
     else:
         off = (-workspace.data_ptr()) % 256
-        wsp, wsn = ctypes.c_void_p(workspace.data_ptr() + off), max(0, workspace.numel() - off)
-    st = lib().kv_q8_attention(
-        _ptr(q), _dtype_code(q), _ptr(kv_pool), _ptr(kv_scales), _ptr(block_table),
-        _ptr(seq_lens), _ptr(num_new), _ptr(tree_mask), _ptr(out),
-        D ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, NB, NL, layer, Hq,
-        H, D, bs, B, T, block_table.shape[1], wsp, wsn, _stream(stream), _ptr(err_flag))
+        wsp, wsn = workspace.data_ptr() + off, max(0, workspace.numel() - off)
+    st = (_lib or lib()).kv_q8_attention(
+        qp, _dtype_code(q), pool, scales, bt, _vec(seq_lens, "seq_lens", B),
+        _vec(num_new, "num_new", B), tm, op, D ** -0.5 if softmax_scale is None else softmax_scale,
+        window, sinks, NB, NL, layer, Hq, H, D, bs, B, T, MB, wsp, wsn, raw,
+        _word(err_flag, "err_flag"))
     if st != SPEC_OK:
         raise SpecError("kv_q8_attention", st)
 
@@ -496,14 +531,12 @@ def kv_reserve(block_table, seq_lens, free_stack, free_top, status, *, n: int, b
                num_blocks: int, num_new=None, stream=None) -> None:
     """Blocks for n (or num_new[b]) tokens past seq_lens[b]; status receives 0 or error bits."""
     import torch
-    _check(block_table, "block_table", 2, torch.int32)
+    bt = _arg(block_table, "block_table", 2, torch.int32)
     B, MB = block_table.shape
-    _rows(B, seq_lens=seq_lens, num_new=num_new)
-    _rows(num_blocks, free_stack=free_stack)
-    _one_word(free_top=free_top, status=status)
-    st = lib().kv_reserve(_ptr(block_table), _ptr(seq_lens), _ptr(num_new), n, num_blocks,
-                          block_size, B, MB, _ptr(free_stack), _ptr(free_top), _ptr(status),
-                          _stream(stream))
+    st = (_lib or lib()).kv_reserve(
+        bt, _vec(seq_lens, "seq_lens", B), _vec(num_new, "num_new", B), n, num_blocks, block_size,
+        B, MB, _vec(free_stack, "free_stack", num_blocks), _word(free_top, "free_top"),
+        _word(status, "status"), _raw_stream(stream, block_table.device))
     if st != SPEC_OK:
         raise SpecError("kv_reserve", st)
 
@@ -514,28 +547,26 @@ def kv_fork(block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, free
     kv_pool: the 8-bit pool with kv_scales, or kv_commit_rollback's [num_blocks, layers, 2,
     block_size, kv_heads, head_dim] pool without."""
     import torch
-    _check(block_table, "block_table", 2, torch.int32)
+    bt = _arg(block_table, "block_table", 2, torch.int32)
     B, MB = block_table.shape
-    _rows(B, seq_lens=seq_lens)
     if kv_scales is not None:
-        NB, NL, _, H, bs, D = _q8_pool(kv_pool, kv_scales)
+        pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
         planes, token = NL * 2 * H, D
     else:
-        _check(kv_pool, "kv_pool", 6)
+        pool, scales = _arg(kv_pool, "kv_pool", 6, None), None
         NB, NL, two, bs, H, D = kv_pool.shape
         if two != 2:
             raise ValueError("kv_pool must be [num_blocks, layers, 2, block_size, heads, head_dim]")
         planes, token = NL * 2, H * D * kv_pool.element_size()
     if bs != block_size:
         raise ValueError(f"kv_pool holds blocks of {bs} tokens, not {block_size}")
-    _check(src_rows, "src_rows", 1, torch.int32)
-    _rows(src_rows.shape[0], dst_rows=dst_rows)
-    _rows(NB, extra_refs=extra_refs, free_stack=free_stack)
-    _one_word(free_top=free_top, status=status)
-    st = lib().kv_fork(_ptr(block_table), _ptr(seq_lens), _ptr(extra_refs), _ptr(src_rows),
-                       _ptr(dst_rows), src_rows.shape[0], _ptr(kv_pool), planes, token,
-                       _ptr(kv_scales), NB, block_size, B, MB, _ptr(free_stack), _ptr(free_top),
-                       _ptr(status), _stream(stream))
+    src = _arg(src_rows, "src_rows", 1, torch.int32)
+    n = src_rows.shape[0]
+    st = (_lib or lib()).kv_fork(
+        bt, _vec(seq_lens, "seq_lens", B), _vec(extra_refs, "extra_refs", NB), src,
+        _vec(dst_rows, "dst_rows", n), n, pool, planes, token, scales, NB, block_size, B, MB,
+        _vec(free_stack, "free_stack", NB), _word(free_top, "free_top"), _word(status, "status"),
+        _raw_stream(stream, block_table.device))
     if st != SPEC_OK:
         raise SpecError("kv_fork", st)
 
@@ -544,15 +575,13 @@ def kv_free(block_table, seq_lens, extra_refs, rows, free_stack, free_top, statu
             num_blocks: int, stream=None) -> None:
     """Releases the listed rows; blocks that no other row holds go back on the free stack."""
     import torch
-    _check(block_table, "block_table", 2, torch.int32)
+    bt = _arg(block_table, "block_table", 2, torch.int32)
     B, MB = block_table.shape
-    _rows(B, seq_lens=seq_lens)
-    _check(rows, "rows", 1, torch.int32)
-    _rows(num_blocks, extra_refs=extra_refs, free_stack=free_stack)
-    _one_word(free_top=free_top, status=status)
-    st = lib().kv_free(_ptr(block_table), _ptr(seq_lens), _ptr(extra_refs), _ptr(rows),
-                       rows.shape[0], num_blocks, B, MB, _ptr(free_stack), _ptr(free_top),
-                       _ptr(status), _stream(stream))
+    st = (_lib or lib()).kv_free(
+        bt, _vec(seq_lens, "seq_lens", B), _vec(extra_refs, "extra_refs", num_blocks),
+        _arg(rows, "rows", 1, torch.int32), rows.shape[0], num_blocks, B, MB,
+        _vec(free_stack, "free_stack", num_blocks), _word(free_top, "free_top"),
+        _word(status, "status"), _raw_stream(stream, block_table.device))
     if st != SPEC_OK:
         raise SpecError("kv_free", st)
 

@@ -246,16 +246,26 @@ constexpr int kAttnMaxCtas = 512;  // bound of the work split, for the workspace
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
 size_t any_smem(int D) {
   return sizeof(float) * (size_t(kAnyRows) * D + kAnyKeys * (D + 1) + size_t(kAnyKeys) * D +
                           kAnyRows * 33);
+}
+
+template <class T>
+int launch_any(const AttnArgs& a, int nc, void* stream) {
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(attn_any_kernel<T>, any_smem(kAnyMaxD), done) != SPEC_OK) return SPEC_ECUDA;
+  return launch_pdl(attn_any_kernel<T>, dim3(nc), dim3(kAnyThreads), any_smem(a.D),
+                    static_cast<cudaStream_t>(stream), a);
 }
 
 }  // namespace
@@ -314,13 +324,8 @@ int launch_kv_q8_attention(const Q8AttnLaunch& k) {
     const int st = launch_attn_tc(a, k.pool, planes, sms, kAttnMaxCtas, &nc, k.stream);
     if (st != SPEC_OK) return st;
   } else {
-    const size_t smem = any_smem(k.D);
-    auto kern = k.dtype == SPEC_F32 ? attn_any_kernel<float> : attn_any_kernel<__nv_bfloat16>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
-        cudaSuccess)
-      return SPEC_ECUDA;
-    const int st = launch_pdl(kern, dim3(nc), dim3(kAnyThreads), smem,
-                              static_cast<cudaStream_t>(k.stream), a);
+    const int st = k.dtype == SPEC_F32 ? launch_any<float>(a, nc, k.stream)
+                                       : launch_any<__nv_bfloat16>(a, nc, k.stream);
     if (st != SPEC_OK) return st;
   }
   return launch_attn_join(a, nc, k.dtype, k.stream);

@@ -789,9 +789,8 @@ template <int NR, int D>
 int launch_shape(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t st) {
   auto kern = attn_tc_kernel<NR, D>;
   constexpr size_t smem = TcShape<NR, D>::kBytes;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
-      cudaSuccess)
-    return SPEC_ECUDA;
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(kern, smem, done) != SPEC_OK) return SPEC_ECUDA;
   return launch_pdl(kern, dim3(nc), dim3(TcShape<NR, D>::kThreads), smem, st, a, map);
 }
 

@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdlib>
 #include <mutex>
 
@@ -87,6 +88,21 @@ int launch_dataflow(Kern kern, const Args& args, size_t smem, cudaStream_t st) {
     if (g > 0 && g < grid) grid = g;
   }
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, args);
+}
+
+// Allows `kern` its dynamic shared memory, once per device (`done`: a word of the
+// caller's for that kernel), so that small calls do not pay for it every time.
+template <class Kern>
+int allow_smem(Kern kern, size_t smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ECUDA;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return SPEC_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+      cudaSuccess)
+    return SPEC_ECUDA;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return SPEC_OK;
 }
 
 }  // namespace sv
