@@ -14,13 +14,14 @@
 //            goes onto the stack, in the order in which it is first listed.
 //
 // Each call moves a few kilobytes of tables, so it is bound by the latency of
-// dependent global accesses, not by bandwidth: the planning runs as ONE cluster
-// of 8 CTAs x 1024 threads whose phases are separated by the hardware cluster
-// barrier (well under a microsecond) instead of launches. The entries of all
-// rows form one flat list (a prefix sum over the rows' spans, a binary search
-// back), so long and short rows balance; each CTA owns a contiguous part of
-// it and the parts' counts go through distributed shared memory, which makes
-// the order of pops and pushes a function of the inputs alone.
+// dependent global accesses and by launches, not by bandwidth. The entries of all
+// rows form one flat list (a prefix sum over the rows' spans, a binary search back),
+// so long and short rows balance; a thread holds 8 consecutive entries in registers
+// through all phases, and lists of up to 8192 are planned by one CTA, longer ones by
+// ONE cluster of 8 CTAs whose phases are separated by the hardware cluster barrier
+// instead of launches (a cluster costs about 3 us more to launch). Each CTA owns a
+// contiguous part of the list and the parts' counts go through distributed shared
+// memory, which makes the order of pops and pushes a function of the inputs alone.
 // All-or-nothing: nothing is written before every check has passed; what the
 // checks themselves write (claims in seq_lens, counts in extra_refs) is undone.
 #include <cooperative_groups.h>
@@ -39,15 +40,29 @@ namespace cg = cooperative_groups;
 
 constexpr int kPgThreads = 1024;
 constexpr int kPgCluster = 8;
+constexpr int kPgHeld = 8;        // entries that a thread holds
 constexpr int kPgMaxRows = 8192;  // rows (or pairs) of one call: the prefix sums lie in shared memory
 constexpr int kPgRowsPerThread = kPgMaxRows / kPgThreads;
 constexpr int kForkThreads = 256;
-constexpr int kForkPlanes = 8;  // planes of a tail block that one CTA copies
+constexpr int kForkPlanes = 8;    // planes of a tail block that one CTA copies
+constexpr int kForkWords = 4;     // 16-byte words that a thread of it has in flight
 
 struct PgShared {
   int prefix[kPgMaxRows + 1];  // flat index of each row's first entry
   int warp[kPgThreads / 32];
   int cnt, err;                // this CTA's share, read by the cluster
+};
+
+// The CTAs that plan together: C = 1 or kPgCluster.
+template <int C>
+struct PgTeam {
+  __device__ __forceinline__ static int rank() {
+    return C == 1 ? 0 : int(cg::this_cluster().block_rank());
+  }
+  __device__ __forceinline__ static void sync() {
+    if (C == 1) __syncthreads();
+    else cg::this_cluster().sync();
+  }
 };
 
 // Block-wide exclusive scan (kPgThreads threads); `total` is the block's sum.
@@ -87,17 +102,20 @@ __device__ void pg_publish(PgShared& sh, int cnt, int err) {
   __syncthreads();
 }
 
-// Cluster-wide: sum of the counts, union of the errors, sum over lower ranks.
+// Over the team: sum of the counts, union of the errors, sum over lower ranks.
 struct PgAll {
   int cnt, err, before;
 };
-__device__ PgAll pg_exchange(cg::cluster_group& cl, PgShared& sh, int cnt, int err) {
+template <int C>
+__device__ PgAll pg_exchange(PgShared& sh, int cnt, int err) {
   pg_publish(sh, cnt, err);
+  if (C == 1) return PgAll{sh.cnt, sh.err, 0};
+  cg::cluster_group cl = cg::this_cluster();
   cl.sync();
   PgAll r{0, 0, 0};
   const int me = cl.block_rank();
 #pragma unroll
-  for (int k = 0; k < kPgCluster; ++k) {
+  for (int k = 0; k < C; ++k) {
     const PgShared* o = cl.map_shared_rank(&sh, k);
     const int c = o->cnt;
     r.cnt += c;
@@ -107,6 +125,24 @@ __device__ PgAll pg_exchange(cg::cluster_group& cl, PgShared& sh, int cnt, int e
   cl.sync();  // the values may be replaced, or the CTA may leave
   return r;
 }
+
+// A CTA's part [e0, e1) of a flat list, in rounds of kPgThreads * kPgHeld entries;
+// thread t of a round has kPgHeld consecutive ones.
+template <int C>
+struct PgPart {
+  int e0, e1, rounds;
+  __device__ PgPart(int total) {
+    const int r = PgTeam<C>::rank();
+    e0 = int(int64_t(total) * r / C);
+    e1 = int(int64_t(total) * (r + 1) / C);
+    // the same for every CTA of the team: all of them run all rounds
+    rounds = ((total + C - 1) / C + kPgThreads * kPgHeld - 1) / (kPgThreads * kPgHeld);
+  }
+  __device__ __forceinline__ int at(int round, int k) const {
+    const int e = e0 + (round * kPgThreads + int(threadIdx.x)) * kPgHeld + k;
+    return e < e1 ? e : -1;
+  }
+};
 
 // prefix[] of n spans given by span(i); each thread takes consecutive rows.
 template <class F>
@@ -155,11 +191,9 @@ struct ReserveArgs {
   int32_t* status;
 };
 
-__global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
-    kv_reserve_kernel(const ReserveArgs a) {
-  __shared__ PgShared sh;
-  cg::cluster_group cl = cg::this_cluster();
-  const int tid = threadIdx.x, rank = cl.block_rank();
+template <int C>
+__device__ __forceinline__ void reserve_body(const ReserveArgs& a, PgShared& sh) {
+  const int tid = threadIdx.x, rank = PgTeam<C>::rank();
   pdl_trigger();
   pdl_wait();
   const int top = *a.ftop;
@@ -172,42 +206,57 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     }
     return pg_cdiv(L + n, a.bs) - pg_cdiv(L, a.bs);
   });
-  const int e0 = int(int64_t(total) * rank / kPgCluster);
-  const int e1 = int(int64_t(total) * (rank + 1) / kPgCluster);
-  auto slot = [&](int e) -> int32_t* {
-    const int b = pg_row(sh, a.B, e);
-    return a.bt + int64_t(b) * a.MB + pg_cdiv(a.sl[b], a.bs) + (e - sh.prefix[b]);
+  const PgPart<C> part(total);
+  int32_t* slot[kPgHeld];
+  int x[kPgHeld];
+  auto load = [&](int round) {  // entries of this thread, 0 where there is none
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k) {
+      const int e = part.at(round, k);
+      slot[k] = nullptr;
+      x[k] = 0;
+      if (e >= 0) {
+        const int b = pg_row(sh, a.B, e);
+        slot[k] = a.bt + int64_t(b) * a.MB + pg_cdiv(a.sl[b], a.bs) + (e - sh.prefix[b]);
+        x[k] = *slot[k];
+      }
+    }
   };
   int cnt = 0;
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int x = *slot(e);
-    cnt += x == -1;
-    if (x < -1 || x >= a.NB) err |= SPEC_DERR_BAD_BLOCK;
+  for (int r = 0; r < part.rounds; ++r) {
+    load(r);
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k) {
+      cnt += x[k] == -1;
+      if (x[k] < -1 || x[k] >= a.NB) err |= SPEC_DERR_BAD_BLOCK;
+    }
   }
-  PgAll all = pg_exchange(cl, sh, cnt, err);
+  PgAll all = pg_exchange<C>(sh, cnt, err);
   const int need = all.cnt, base = all.before;
   err = all.err;
   if (err == 0 && (top < 0 || top > a.NB || need > top)) err = SPEC_DERR_NO_SPACE;
   if (err == 0) {
     int pe = 0;
-    for (int i = rank * kPgThreads + tid; i < need; i += kPgCluster * kPgThreads) {
-      const int x = a.fs[top - 1 - i];
-      if (x < 0 || x >= a.NB) pe = SPEC_DERR_BAD_BLOCK;
+    for (int i = rank * kPgThreads + tid; i < need; i += C * kPgThreads) {
+      const int y = a.fs[top - 1 - i];
+      if (y < 0 || y >= a.NB) pe = SPEC_DERR_BAD_BLOCK;
     }
-    err = pg_exchange(cl, sh, 0, pe).err;
+    err = pg_exchange<C>(sh, 0, pe).err;
   }
   if (err != 0) {
     if (rank == 0 && tid == 0) *a.status = err;
     return;
   }
   int carry = base;
-  for (int f = e0; f < e1; f += kPgThreads) {  // uniform over the CTA: the scan synchronises
-    const int e = f + tid;
-    int32_t* p = e < e1 ? slot(e) : nullptr;
-    const bool want = p && *p == -1;
-    int sum;
-    const int r = carry + pg_scan(want, sh.warp, sum);
-    if (want) *p = a.fs[top - 1 - r];
+  for (int r = 0; r < part.rounds; ++r) {
+    if (part.rounds > 1) load(r);
+    int mine = 0, sum;
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k) mine += x[k] == -1;
+    int at = carry + pg_scan(mine, sh.warp, sum);
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k)
+      if (x[k] == -1) *slot[k] = a.fs[top - 1 - at++];
     carry += sum;
   }
   if (rank == 0 && tid == 0) {
@@ -216,11 +265,30 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
   }
 }
 
+__global__ void __launch_bounds__(kPgThreads) kv_reserve_kernel(const ReserveArgs a) {
+  __shared__ PgShared sh;
+  reserve_body<1>(a, sh);
+}
+__global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
+    kv_reserve_cluster_kernel(const ReserveArgs a) {
+  __shared__ PgShared sh;
+  reserve_body<kPgCluster>(a, sh);
+}
+
+// One CTA where it can hold `entries` (an upper bound), else a cluster.
+template <class Kern, class Args>
+int launch_plan(Kern one, Kern cluster, int64_t entries, const Args& a, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return entries <= kPgThreads * kPgHeld
+             ? launch_pdl(one, dim3(1), dim3(kPgThreads), 0, st, a)
+             : launch_pdl(cluster, dim3(kPgCluster), dim3(kPgThreads), 0, st, a);
+}
+
 int launch_kv_reserve(const KvReserveLaunch& k) {
   ReserveArgs a{k.block_table, k.seq_lens, k.num_new, k.n, k.num_blocks, k.block_size, k.B,
                 k.max_blocks, k.free_stack, k.free_top, k.status};
-  return launch_pdl(kv_reserve_kernel, dim3(kPgCluster), dim3(kPgThreads), 0,
-                    static_cast<cudaStream_t>(k.stream), a);
+  const int64_t row = k.num_new ? k.max_blocks : k.n / k.block_size + 1;
+  return launch_plan(kv_reserve_kernel, kv_reserve_cluster_kernel, k.B * row, a, k.stream);
 }
 
 // ------------------------------------------------------------------ fork
@@ -238,13 +306,13 @@ struct ForkArgs {
   int32_t* status;
 };
 
-__global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
-    kv_fork_plan_kernel(const ForkArgs a) {
-  __shared__ PgShared sh;
-  cg::cluster_group cl = cg::this_cluster();
-  const int tid = threadIdx.x, rank = cl.block_rank();
-  pdl_trigger();
+template <int C>
+__device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) {
+  const int tid = threadIdx.x, rank = PgTeam<C>::rank();
   pdl_wait();
+  // From here on the copies may start: they read the parents' tables and blocks,
+  // which this kernel does not change, and wait for it before they write.
+  pdl_trigger();
   const int top = *a.ftop;
   int err = 0;
   const int total = pg_prefix(sh, a.n, [&](int i) {
@@ -260,18 +328,29 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     }
     return pg_cdiv(L, a.bs);
   });
-  const int e0 = int(int64_t(total) * rank / kPgCluster);
-  const int e1 = int(int64_t(total) * (rank + 1) / kPgCluster);
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int i = pg_row(sh, a.n, e), j = e - sh.prefix[i];
-    const int x = a.bt[int64_t(a.src[i]) * a.MB + j];
-    if (x < 0 || x >= a.NB || a.bt[int64_t(a.dst[i]) * a.MB + j] != -1) err |= SPEC_DERR_BAD_BLOCK;
-  }
+  const PgPart<C> part(total);
+  int32_t* to[kPgHeld];  // the child's entry, null for the tail block
+  int x[kPgHeld];
+  int bad = 0;
+  auto load = [&](int round) {
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k) {
+      const int e = part.at(round, k);
+      to[k] = nullptr;
+      if (e >= 0) {
+        const int i = pg_row(sh, a.n, e), j = e - sh.prefix[i], s = a.src[i];
+        x[k] = a.bt[int64_t(s) * a.MB + j];
+        to[k] = a.bt + int64_t(a.dst[i]) * a.MB + j;
+        if (x[k] < 0 || x[k] >= a.NB || *to[k] != -1) bad = SPEC_DERR_BAD_BLOCK;
+        if ((j + 1) * int64_t(a.bs) > __ldcg(&a.sl[s])) to[k] = nullptr;
+      }
+    }
+  };
+  for (int r = 0; r < part.rounds; ++r) load(r);
+  err = pg_exchange<C>(sh, 0, err | bad).err;
   // tails: pairs with a partly filled block, ranked in the order of the pairs
   const int per = (a.n + kPgThreads - 1) / kPgThreads, i0 = tid * per;
   int mine = 0;
-  PgAll all = pg_exchange(cl, sh, 0, err);
-  err = all.err;
   if (err == 0)
     for (int i = i0; i < i0 + per && i < a.n; ++i) mine += a.sl[a.src[i]] % a.bs != 0;
   int tails;
@@ -284,8 +363,8 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     int pe = 0;
     if (rank == 0) {
       for (int k = tid; k < tails; k += kPgThreads) {
-        const int x = a.fs[top - 1 - k];
-        if (x < 0 || x >= a.NB) pe |= SPEC_DERR_BAD_BLOCK;
+        const int y = a.fs[top - 1 - k];
+        if (y < 0 || y >= a.NB) pe |= SPEC_DERR_BAD_BLOCK;
       }
       for (int i = i0; i < i0 + per && i < a.n; ++i)
         if (atomicExch(&a.sl[a.dst[i]], -1) != 0) pe |= SPEC_DERR_BAD_SLOT;
@@ -293,7 +372,7 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
       for (int i = i0; i < i0 + per && i < a.n; ++i)
         if (__ldcg(&a.sl[a.src[i]]) < 0) pe |= SPEC_DERR_BAD_SLOT;
     }
-    err = pg_exchange(cl, sh, 0, pe).err;
+    err = pg_exchange<C>(sh, 0, pe).err;
     if (err != 0 && rank == 0)
       for (int i = i0; i < i0 + per && i < a.n; ++i) a.sl[a.dst[i]] = 0;
   }
@@ -301,12 +380,14 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
     if (rank == 0 && tid == 0) *a.status = err;
     return;
   }
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int i = pg_row(sh, a.n, e), j = e - sh.prefix[i], s = a.src[i];
-    if ((j + 1) * int64_t(a.bs) > __ldcg(&a.sl[s])) continue;  // the tail block
-    const int x = a.bt[int64_t(s) * a.MB + j];
-    a.bt[int64_t(a.dst[i]) * a.MB + j] = x;
-    atomicAdd(&a.refs[x], 1);
+  for (int r = 0; r < part.rounds; ++r) {
+    if (part.rounds > 1) load(r);
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k)
+      if (to[k]) {
+        *to[k] = x[k];
+        atomicAdd(&a.refs[x[k]], 1);
+      }
   }
   if (rank == 0) {
     int r = at;
@@ -321,43 +402,68 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
   }
 }
 
+__global__ void __launch_bounds__(kPgThreads) kv_fork_plan_kernel(const ForkArgs a) {
+  __shared__ PgShared sh;
+  fork_plan_body<1>(a, sh);
+}
+__global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
+    kv_fork_plan_cluster_kernel(const ForkArgs a) {
+  __shared__ PgShared sh;
+  fork_plan_body<kPgCluster>(a, sh);
+}
+
 // The tail blocks' tokens and scales: CTA (chunk, pair) copies kForkPlanes
-// planes. Bound by memory: it reads and writes L % bs tokens of every plane.
+// planes. Bound by memory: it reads and writes L % bs tokens of every plane. Its
+// first loads do not wait for the plan, which changes neither the parents' rows nor
+// any block; they test what the plan has not yet vouched for.
 __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkArgs a) {
   pdl_trigger();
-  pdl_wait();  // the plan
-  if (*a.status != 0) return;
-  const int i = blockIdx.y, s = a.src[i], d = a.dst[i];
-  const int L = a.sl[s], off = L % a.bs;  // a parent's length does not change
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.sl[d] = L;
-  if (off == 0) return;
-  const int j = L / a.bs;
-  const int64_t x = a.bt[int64_t(s) * a.MB + j], y = a.bt[int64_t(d) * a.MB + j];
+  const int i = blockIdx.y, s = __ldcg(&a.src[i]), d = __ldcg(&a.dst[i]);
+  const int L = s >= 0 && s < a.B ? __ldcg(&a.sl[s]) : 0;
+  const int off = L > 0 && L <= int64_t(a.MB) * a.bs ? L % a.bs : 0;
+  const int j = off ? L / a.bs : 0;
+  const int64_t x = off ? __ldcg(&a.bt[int64_t(s) * a.MB + j]) : -1;
+  const bool some = x >= 0 && x < a.NB;
   const int p0 = blockIdx.x * kForkPlanes;
   const int np = min(kForkPlanes, a.planes - p0);
   const int64_t plane = int64_t(a.bs) * a.tb;
-  const uint8_t* from = a.pool + (x * a.planes + p0) * plane;
-  uint8_t* to = a.pool + (y * a.planes + p0) * plane;
   const int vec = off * (a.tb / 16);  // 16-byte words of a plane's tokens
-  const int total = np * vec;
-  constexpr int kUnroll = 4;
-  for (int g0 = threadIdx.x; g0 < total; g0 += kForkThreads * kUnroll) {
-    uint4 v[kUnroll];
-    int64_t o[kUnroll];
+  const int total = some ? np * vec : 0;
+  const uint8_t* from = a.pool + ((some ? x : 0) * a.planes + p0) * plane;
+  uint8_t* to = a.pool;
+  bool waited = false;
+  int64_t y = 0;
+  // until the plan is done and says that it has changed the tables
+  auto plan_ok = [&]() {
+    if (!waited) {
+      waited = true;
+      pdl_wait();
+      if (__ldcg(a.status) != 0) return false;
+      if (blockIdx.x == 0 && threadIdx.x == 0) a.sl[d] = L;
+      if (some) y = __ldcg(&a.bt[int64_t(d) * a.MB + j]);
+      to = a.pool + (y * a.planes + p0) * plane;
+    }
+    return true;
+  };
+  for (int g0 = threadIdx.x; g0 < total; g0 += kForkThreads * kForkWords) {
+    uint4 v[kForkWords];
+    int64_t o[kForkWords];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kForkWords; ++k) {
       const int g = g0 + k * kForkThreads;
       o[k] = -1;
       if (g < total) {
         const int p = g / vec;
         o[k] = p * plane + int64_t(g - p * vec) * 16;
-        v[k] = ldg_nc_v4(from + o[k]);
+        v[k] = __ldcg(reinterpret_cast<const uint4*>(from + o[k]));
       }
     }
+    if (!plan_ok()) return;
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k)
+    for (int k = 0; k < kForkWords; ++k)
       if (o[k] >= 0) *reinterpret_cast<uint4*>(to + o[k]) = v[k];
   }
+  if (!plan_ok() || !some) return;
   if (a.scales && threadIdx.x < np)
     a.scales[y * a.planes + p0 + threadIdx.x] = a.scales[x * a.planes + p0 + threadIdx.x];
 }
@@ -366,11 +472,12 @@ int launch_kv_fork(const KvForkLaunch& k) {
   ForkArgs a{k.block_table, k.seq_lens, k.extra_refs, k.src_rows, k.dst_rows,
              static_cast<uint8_t*>(k.kv_pool), k.kv_scales, k.num_blocks, k.block_size, k.B,
              k.max_blocks, k.n, k.planes, k.token_bytes, k.free_stack, k.free_top, k.status};
-  cudaStream_t st = static_cast<cudaStream_t>(k.stream);
-  if (launch_pdl(kv_fork_plan_kernel, dim3(kPgCluster), dim3(kPgThreads), 0, st, a) != SPEC_OK)
-    return SPEC_ECUDA;
+  const int st = launch_plan(kv_fork_plan_kernel, kv_fork_plan_cluster_kernel,
+                             int64_t(k.n) * k.max_blocks, a, k.stream);
+  if (st != SPEC_OK) return st;
   const int chunks = (k.planes + kForkPlanes - 1) / kForkPlanes;
-  return launch_pdl(kv_fork_copy_kernel, dim3(chunks, k.n), dim3(kForkThreads), 0, st, a);
+  return launch_pdl(kv_fork_copy_kernel, dim3(chunks, k.n), dim3(kForkThreads), 0,
+                    static_cast<cudaStream_t>(k.stream), a);
 }
 
 // ------------------------------------------------------------------ free
@@ -392,38 +499,60 @@ struct FreeArgs {
 //     (below -1, so never mistaken for a count);
 //   3 the entry whose index its block holds pushes it, ranked by a scan;
 //   4 that entry sets the count to 0; all entries are cleared.
-__global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
-    kv_free_kernel(const FreeArgs a) {
-  __shared__ PgShared sh;
-  cg::cluster_group cl = cg::this_cluster();
-  const int tid = threadIdx.x, rank = cl.block_rank();
+template <int C>
+__device__ __forceinline__ void free_body(const FreeArgs& a, PgShared& sh) {
+  const int tid = threadIdx.x, rank = PgTeam<C>::rank(), step = C * kPgThreads;
   pdl_trigger();
   pdl_wait();
   const int top = *a.ftop;
   const int E = a.n * a.MB;
-  const int e0 = int(int64_t(E) * rank / kPgCluster), e1 = int(int64_t(E) * (rank + 1) / kPgCluster);
-  const int step = kPgCluster * kPgThreads;
+  const PgPart<C> part(E);
   int err = 0;
   for (int i = rank * kPgThreads + tid; i < a.n; i += step) {
     const int r = a.rows[i];
     if (r < 0 || r >= a.B) err |= SPEC_DERR_BAD_SLOT;
     else if (a.sl[r] < 0) err |= SPEC_DERR_BAD_LENGTH;
   }
-  err = pg_exchange(cl, sh, 0, err).err;
+  err = pg_exchange<C>(sh, 0, err).err;
   if (err != 0) {
     if (rank == 0 && tid == 0) *a.status = err;
     return;
   }
+  int32_t* slot[kPgHeld];
+  int x[kPgHeld];  // block ids, -1: none
+  auto load = [&](int round) {
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k) {
+      const int e = part.at(round, k);
+      slot[k] = nullptr;
+      x[k] = -1;
+      if (e >= 0) {
+        const int i = e / a.MB;
+        slot[k] = a.bt + int64_t(a.rows[i]) * a.MB + (e - i * a.MB);
+        x[k] = *slot[k];
+      }
+    }
+  };
+  // calls f(entry's flat index, k) for every entry that holds a block
+  auto each = [&](auto f) {
+    for (int r = 0; r < part.rounds; ++r) {
+      if (part.rounds > 1) load(r);
+#pragma unroll
+      for (int k = 0; k < kPgHeld; ++k)
+        if (x[k] >= 0) f(part.at(r, k), k);
+    }
+  };
   // rows must be distinct: each is claimed by complementing its length
-  auto entry = [&](int e) -> int32_t* { return a.bt + int64_t(a.rows[e / a.MB]) * a.MB + e % a.MB; };
   for (int i = rank * kPgThreads + tid; i < a.n; i += step) {
     int32_t* p = &a.sl[a.rows[i]];
     const int L = *reinterpret_cast<volatile int32_t*>(p);
     if (L < 0 || atomicCAS(p, L, ~L) != L) err |= SPEC_DERR_BAD_SLOT;
   }
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int x = *entry(e);
-    if (x < -1 || x >= a.NB) err |= SPEC_DERR_BAD_BLOCK;
+  for (int r = 0; r < part.rounds; ++r) {
+    load(r);
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k)
+      if (x[k] < -1 || x[k] >= a.NB) err |= SPEC_DERR_BAD_BLOCK;
   }
   if (top < 0 || top > a.NB) err |= SPEC_DERR_BAD_BLOCK;
   auto unclaim = [&]() {  // only reached with every CTA past its claims
@@ -433,71 +562,80 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
       if (L < 0) atomicCAS(p, L, ~L);  // a row listed twice is undone once
     }
   };
-  err = pg_exchange(cl, sh, 0, err).err;
+  err = pg_exchange<C>(sh, 0, err).err;
   if (err != 0) {
     unclaim();
     if (rank == 0 && tid == 0) *a.status = err;
     return;
   }
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int x = *entry(e);
-    if (x >= 0) atomicSub(&a.refs[x], 1);
-  }
-  cl.sync();
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int x = *entry(e);
-    if (x >= 0 && __ldcg(&a.refs[x]) < -1) err |= SPEC_DERR_BAD_BLOCK;
-  }
+  each([&](int, int k) { atomicSub(&a.refs[x[k]], 1); });
+  PgTeam<C>::sync();
+  each([&](int, int k) {
+    if (__ldcg(&a.refs[x[k]]) < -1) err |= SPEC_DERR_BAD_BLOCK;
+  });
   auto give_back = [&]() {
-    for (int e = e0 + tid; e < e1; e += kPgThreads) {
-      const int x = *entry(e);
-      if (x >= 0) atomicAdd(&a.refs[x], 1);
-    }
+    each([&](int, int k) { atomicAdd(&a.refs[x[k]], 1); });
     unclaim();
     if (rank == 0 && tid == 0) *a.status = err;
   };
-  err = pg_exchange(cl, sh, 0, err).err;
+  err = pg_exchange<C>(sh, 0, err).err;
   if (err != 0) {
     give_back();
     return;
   }
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int x = *entry(e);
-    if (x >= 0 && __ldcg(&a.refs[x]) <= -1) atomicMin(&a.refs[x], e - E - 1);
-  }
-  cl.sync();
+  each([&](int e, int k) {
+    if (__ldcg(&a.refs[x[k]]) <= -1) atomicMin(&a.refs[x[k]], e - E - 1);
+  });
+  PgTeam<C>::sync();
   int cnt = 0;
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    const int x = *entry(e);
-    cnt += x >= 0 && __ldcg(&a.refs[x]) == e - E - 1;
+  uint32_t push = 0;  // this thread's entries that push, of the last round
+  int round = 0;
+  for (; round < part.rounds; ++round) {
+    if (part.rounds > 1) load(round);
+    push = 0;
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k)
+      if (x[k] >= 0 && __ldcg(&a.refs[x[k]]) == part.at(round, k) - E - 1) push |= 1u << k;
+    cnt += __popc(push);
   }
-  PgAll all = pg_exchange(cl, sh, cnt, 0);
+  PgAll all = pg_exchange<C>(sh, cnt, 0);
   if (all.cnt > a.NB - top) {  // some id would be held twice
-    for (int e = e0 + tid; e < e1; e += kPgThreads) {
-      const int x = *entry(e);
-      if (x >= 0 && __ldcg(&a.refs[x]) < -1) a.refs[x] = -1;
-    }
-    cl.sync();
+    each([&](int, int k) {
+      if (__ldcg(&a.refs[x[k]]) < -1) a.refs[x[k]] = -1;
+    });
+    PgTeam<C>::sync();
     err = SPEC_DERR_BAD_BLOCK;
     give_back();
     return;
   }
   int carry = top + all.before;
-  for (int f = e0; f < e1; f += kPgThreads) {
-    const int e = f + tid;
-    const int x = e < e1 ? *entry(e) : -1;
-    const bool push = x >= 0 && __ldcg(&a.refs[x]) == e - E - 1;
+  for (int r = 0; r < part.rounds; ++r) {
+    if (part.rounds > 1) {
+      load(r);
+      push = 0;
+#pragma unroll
+      for (int k = 0; k < kPgHeld; ++k)
+        if (x[k] >= 0 && __ldcg(&a.refs[x[k]]) == part.at(r, k) - E - 1) push |= 1u << k;
+    }
     int sum;
-    const int r = carry + pg_scan(push, sh.warp, sum);
-    if (push) a.fs[r] = x;
+    int at = carry + pg_scan(__popc(push), sh.warp, sum);
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k)
+      if (push >> k & 1u) a.fs[at++] = x[k];
     carry += sum;
   }
-  cl.sync();  // every entry has been compared before a count changes
-  for (int e = e0 + tid; e < e1; e += kPgThreads) {
-    int32_t* p = entry(e);
-    const int x = *p;
-    if (x >= 0 && __ldcg(&a.refs[x]) == e - E - 1) a.refs[x] = 0;
-    *p = -1;
+  PgTeam<C>::sync();  // every entry has been compared before a count changes
+  for (int r = 0; r < part.rounds; ++r) {
+    if (part.rounds > 1) load(r);
+#pragma unroll
+    for (int k = 0; k < kPgHeld; ++k) {
+      // with one round the comparison above still holds
+      const bool mine = part.rounds == 1
+                            ? (push >> k & 1u)
+                            : x[k] >= 0 && __ldcg(&a.refs[x[k]]) == part.at(r, k) - E - 1;
+      if (mine) a.refs[x[k]] = 0;
+      if (slot[k]) *slot[k] = -1;
+    }
   }
   for (int i = rank * kPgThreads + tid; i < a.n; i += step) a.sl[a.rows[i]] = 0;
   if (rank == 0 && tid == 0) {
@@ -506,11 +644,21 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
   }
 }
 
+__global__ void __launch_bounds__(kPgThreads) kv_free_kernel(const FreeArgs a) {
+  __shared__ PgShared sh;
+  free_body<1>(a, sh);
+}
+__global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
+    kv_free_cluster_kernel(const FreeArgs a) {
+  __shared__ PgShared sh;
+  free_body<kPgCluster>(a, sh);
+}
+
 int launch_kv_free(const KvFreeLaunch& k) {
   FreeArgs a{k.block_table, k.seq_lens, k.extra_refs, k.rows, k.num_blocks, k.B, k.max_blocks,
              k.n, k.free_stack, k.free_top, k.status};
-  return launch_pdl(kv_free_kernel, dim3(kPgCluster), dim3(kPgThreads), 0,
-                    static_cast<cudaStream_t>(k.stream), a);
+  return launch_plan(kv_free_kernel, kv_free_cluster_kernel, int64_t(k.n) * k.max_blocks, a,
+                     k.stream);
 }
 
 }  // namespace sv

@@ -9,9 +9,10 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
+
 
 #include "../../include/specverify.h"
 #include "launch.h"
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(const AttnArgs a)
   const int r = tid >> 3, part = tid & 7;
   pdl_trigger();
   pdl_wait();
-  write_empty_rows<T>(a, c, nc);
+  write_empty_rows<T>(a, c, nc, tid, kAnyThreads);
   const AttnPlan plan = attn_plan(a, prefix, warp_sum, nc, c);
   if (plan.u0 >= plan.u1) {
     if (tid == 0) write_join(a, plan, nullptr, c);

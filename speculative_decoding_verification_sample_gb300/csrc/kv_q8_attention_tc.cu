@@ -319,12 +319,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   pdl_wait();
-  write_empty_rows<__nv_bfloat16>(a, c, nc);
   const AttnPlan plan = attn_plan(a, prefix, sh.warp_sum, nc, c);
   const bool work = plan.u0 < plan.u1;
   Segment g;
   if (work) g = find_segment(a, prefix, plan.u0, plan.u1);
-  if (tid == 0) write_join(a, plan, work ? &g : nullptr, c);
   __syncthreads();
   const int tiles = int(plan.u1 - plan.u0);
   if (work && (warp < kTmaWarp || warp >= kQWarp)) {
@@ -488,6 +486,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       }
       if (lane == 0 && warp == kQWarp) sh.seg[qb] = g;
       mbar_arrive(&sh.q_full[qb]);
+      if (first && lane == 0 && warp == kQWarp) write_join(a, plan, &g, c);
       qbuf.next();
       if (last_of_cta(g)) break;
       next_segment(a, g, plan.u1);
@@ -746,6 +745,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       if (last) break;
       bar_group(group);  // row_a, row_nm, part: every thread is done with the item
     }
+  }
+  if (warp >= kQWarp) {
+    // what needs no place in the row of the others' work
+    if (!work && tid == kQWarp * 32) write_join(a, plan, nullptr, c);
+    write_empty_rows<__nv_bfloat16>(a, c, nc, tid - kQWarp * 32, 64);
   }
   tc_fence_before();
   __syncthreads();

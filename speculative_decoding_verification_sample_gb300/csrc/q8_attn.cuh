@@ -149,8 +149,13 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix
   AttnPlan p;
   p.W = prefix[blockDim.x] * a.H * a.RB;
   p.nc = int(min(int64_t(nc), p.W));
-  p.u0 = c < p.nc ? p.W * c / p.nc : 0;
-  p.u1 = c < p.nc ? p.W * (c + 1) / p.nc : 0;
+  // W c / nc, in 32 bits where that does
+  auto share = [&](int i) -> int64_t {
+    const int64_t n = p.W * i;
+    return n >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(p.nc)) : n / p.nc;
+  };
+  p.u0 = c < p.nc ? share(c) : 0;
+  p.u1 = c < p.nc ? share(c + 1) : 0;
   return p;
 }
 
@@ -158,7 +163,11 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix
 __device__ __forceinline__ Segment find_segment(const AttnArgs& a, const int64_t* prefix, int64_t u,
                                                 int64_t u1) {
   const int64_t U = int64_t(a.H) * a.RB;
-  const int64_t x = u / U;
+  // 64-bit division is a long routine: only where 32 bits do not do
+  auto quotient = [](int64_t n, int64_t d) -> int64_t {
+    return (n | d) >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
+  };
+  const int64_t x = quotient(u, U);
   int lo = 0, hi = blockDim.x - 1;  // the last chunk with prefix <= x
   while (lo < hi) {
     const int m = (lo + hi + 1) >> 1;
@@ -175,7 +184,7 @@ __device__ __forceinline__ Segment find_segment(const AttnArgs& a, const int64_t
     s = row_span(a, ++b);
   }
   const int64_t rem = u - at * U;
-  const int hr = int(rem / s.tiles);
+  const int hr = int(quotient(rem, s.tiles));
   g.b = b;
   g.s = s;
   g.t0 = int(rem - int64_t(hr) * s.tiles);
@@ -201,17 +210,19 @@ __device__ __forceinline__ void next_segment(const AttnArgs& a, Segment& g, int6
   g.t1 = int(min(int64_t(g.s.tiles), u1 - g.u));
 }
 
-// Rows without keys: zeros, or NaN where the row's lengths are invalid.
+// Rows without keys: zeros, or NaN where the row's lengths are invalid. By thread
+// `me` of `threads` of a CTA.
 template <class T>
-__device__ __forceinline__ void write_empty_rows(const AttnArgs& a, int c, int nc) {
+__device__ __forceinline__ void write_empty_rows(const AttnArgs& a, int c, int nc, int me,
+                                                 int threads) {
   for (int b = c; b < a.B; b += nc) {
     const RowSpan s = row_span(a, b);
     if (s.tiles > 0) continue;
     const int64_t n = int64_t(a.T) * a.H * a.G * a.D;
     T* o = static_cast<T*>(a.out) + b * n;
     const T v = T(s.bad ? __uint_as_float(0x7fc00000u) : 0.0f);
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = v;
-    if (s.bad && a.err && threadIdx.x == 0) atomicOr(a.err, SPEC_DERR_BAD_LENGTH);
+    for (int64_t i = me; i < n; i += threads) o[i] = v;
+    if (s.bad && a.err && me == 0) atomicOr(a.err, SPEC_DERR_BAD_LENGTH);
   }
 }
 
