@@ -44,8 +44,8 @@ constexpr int kPgHeld = 8;        // entries that a thread holds
 constexpr int kPgMaxRows = 8192;  // rows (or pairs) of one call: the prefix sums lie in shared memory
 constexpr int kPgRowsPerThread = kPgMaxRows / kPgThreads;
 constexpr int kForkThreads = 256;
-constexpr int kForkPlanes = 8;    // planes of a tail block that one CTA copies
-constexpr int kForkWords = 4;     // 16-byte words that a thread of it has in flight
+constexpr int kForkWords = 8;     // 16-byte words that a thread of a copy has in flight
+constexpr int kForkMinPlanes = 8; // planes of a tail block that one CTA copies, at least
 
 struct PgShared {
   int prefix[kPgMaxRows + 1];  // flat index of each row's first entry
@@ -301,6 +301,7 @@ struct ForkArgs {
   uint8_t* pool;
   float* scales;  // null: the pool has none
   int NB, bs, B, MB, n, planes, tb;
+  int chunk;      // planes that a CTA of the copy takes
   int32_t* fs;
   int32_t* ftop;
   int32_t* status;
@@ -412,8 +413,9 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
   fork_plan_body<kPgCluster>(a, sh);
 }
 
-// The tail blocks' tokens and scales: CTA (chunk, pair) copies kForkPlanes
-// planes. Bound by memory: it reads and writes L % bs tokens of every plane. Its
+// The tail blocks' tokens and scales: CTA (chunk, pair) copies `chunk`
+// planes: 8 when there are few pairs, more when that would be many waves of CTAs with
+// the latency of their table reads each (128 pairs of 512 planes: 8 planes 38 us, 64 NN us). Bound by memory: it reads and writes L % bs tokens of every plane. Its
 // first loads do not wait for the plan, which changes neither the parents' rows nor
 // any block; they test what the plan has not yet vouched for.
 __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkArgs a) {
@@ -424,8 +426,8 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkAr
   const int j = off ? L / a.bs : 0;
   const int64_t x = off ? __ldcg(&a.bt[int64_t(s) * a.MB + j]) : -1;
   const bool some = x >= 0 && x < a.NB;
-  const int p0 = blockIdx.x * kForkPlanes;
-  const int np = min(kForkPlanes, a.planes - p0);
+  const int p0 = blockIdx.x * a.chunk;
+  const int np = min(a.chunk, a.planes - p0);
   const int64_t plane = int64_t(a.bs) * a.tb;
   const int vec = off * (a.tb / 16);  // 16-byte words of a plane's tokens
   const int total = some ? np * vec : 0;
@@ -464,18 +466,22 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkAr
       if (o[k] >= 0) *reinterpret_cast<uint4*>(to + o[k]) = v[k];
   }
   if (!plan_ok() || !some) return;
-  if (a.scales && threadIdx.x < np)
-    a.scales[y * a.planes + p0 + threadIdx.x] = a.scales[x * a.planes + p0 + threadIdx.x];
+  if (a.scales)
+    for (int p = threadIdx.x; p < np; p += kForkThreads)
+      a.scales[y * a.planes + p0 + p] = a.scales[x * a.planes + p0 + p];
 }
 
 int launch_kv_fork(const KvForkLaunch& k) {
   ForkArgs a{k.block_table, k.seq_lens, k.extra_refs, k.src_rows, k.dst_rows,
              static_cast<uint8_t*>(k.kv_pool), k.kv_scales, k.num_blocks, k.block_size, k.B,
-             k.max_blocks, k.n, k.planes, k.token_bytes, k.free_stack, k.free_top, k.status};
+             k.max_blocks, k.n, k.planes, k.token_bytes, 0, k.free_stack, k.free_top, k.status};
+  // about two waves of 8 CTAs an SM
+  const int64_t share = int64_t(k.n) * k.planes / 2432;
+  a.chunk = int(share < kForkMinPlanes ? kForkMinPlanes : share < k.planes ? share : k.planes);
   const int st = launch_plan(kv_fork_plan_kernel, kv_fork_plan_cluster_kernel,
                              int64_t(k.n) * k.max_blocks, a, k.stream);
   if (st != SPEC_OK) return st;
-  const int chunks = (k.planes + kForkPlanes - 1) / kForkPlanes;
+  const int chunks = (k.planes + a.chunk - 1) / a.chunk;
   return launch_pdl(kv_fork_copy_kernel, dim3(chunks, k.n), dim3(kForkThreads), 0,
                     static_cast<cudaStream_t>(k.stream), a);
 }

@@ -16,7 +16,9 @@
 // takes one (row, block, plane, head); neighbouring warps take neighbouring
 // heads, whose tokens are adjacent in k and v. The block's new tokens stay in
 // registers between the maximum and the rounding (up to 2048 bf16 numbers of
-// a warp; longer blocks read the rest again, from L2).
+// a warp; longer blocks read the rest again, from L2). Their loads are issued
+// before the block table answers, the maximum is taken on the packed bit patterns
+// (magnitudes order as integers), and x / s is a product with the exact 1 / s.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -45,40 +47,53 @@ struct AppendArgs {
   int32_t* err;
 };
 
-// Eight numbers of k or v in fp32; NaN becomes 0, infinities the largest
-// finite number (a NaN code would spread to rows that do not see its token).
+// Eight numbers of k or v: their bits, the largest magnitude's bits (bf16: two
+// halves at once), their values.
 template <bool kF32>
-__device__ __forceinline__ void load8(const uint8_t* p, uint4* raw) {
-  raw[0] = *reinterpret_cast<const uint4*>(p);
-  if (kF32) raw[1] = *reinterpret_cast<const uint4*>(p + 16);
-}
-template <bool kF32>
-__device__ __forceinline__ int unpack8(const uint4* raw, float* f) {
-  const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
-  if (kF32) {
-    const uint32_t u[4] = {raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+struct Eight {
+  uint4 w[kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    w[0] = *reinterpret_cast<const uint4*>(p);
+    if (kF32) w[kF32 ? 1 : 0] = *reinterpret_cast<const uint4*>(p + 16);
+  }
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+    const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = __uint_as_float(w[i]);
-      f[4 + i] = __uint_as_float(u[i]);
+    for (int i = 0; i < 4; ++i)
+      m = kF32 ? max(m, v[i] & 0x7fffffffu) : __vmaxu2(m, v[i] & 0x7fff7fffu);
+    if (kF32) {
+      const uint4 x = w[kF32 ? 1 : 0];
+      m = max(max(m, x.x & 0x7fffffffu), x.y & 0x7fffffffu);
+      m = max(max(m, x.z & 0x7fffffffu), x.w & 0x7fffffffu);
     }
-  } else {
+    return m;
+  }
+  // In fp32. `guard`: NaN becomes 0, infinities the largest finite number (a NaN code
+  // would spread to rows that do not see its token).
+  __device__ __forceinline__ void values(float* f, bool guard) const {
+    const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    if (kF32) {
+      const uint4 x = w[kF32 ? 1 : 0];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int i = 0; i < 4; ++i) {
+        f[i] = __uint_as_float(v[i]);
+        f[4 + i] = __uint_as_float(u[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+      }
+    }
+    if (guard) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        f[i] = f[i] != f[i] ? 0.0f : fminf(fmaxf(f[i], -FLT_MAX), FLT_MAX);
     }
   }
-  int bad = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (!(fabsf(f[i]) <= FLT_MAX)) {
-      bad = 1;
-      f[i] = f[i] != f[i] ? 0.0f : copysignf(FLT_MAX, f[i]);
-    }
-  }
-  return bad;
-}
+};
 
 template <bool kF32>
 __global__ void __launch_bounds__(kApThreads) kv_q8_append_kernel(const AppendArgs a) {
@@ -99,62 +114,62 @@ __global__ void __launch_bounds__(kApThreads) kv_q8_append_kernel(const AppendAr
   const int j = L / a.bs + jw;
   const int start = j * a.bs;  // position of the block's first token
   if (n == 0 || start >= L + n) return;
-  const int id = a.bt[int64_t(b) * a.MB + j];
-  if (id < 0 || id >= a.NB) {
-    if (a.err && lane == 0) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
-    return;
-  }
   constexpr int kEb = kF32 ? 4 : 2;
   const int first = max(L - start, 0);             // offset of the first new token
   const int cnt = min(a.bs, L + n - start) - first;
+  const int id = a.bt[int64_t(b) * a.MB + j];
   const int64_t unit = int64_t(plane) * a.H + h;
-  uint8_t* codes = a.pool + id * a.block_bytes + unit * a.bs * a.D;
-  float* sp = a.scales + id * a.block_scales + unit;
-  const float was = first > 0 ? *sp : 0.0f;
   const int64_t tok = int64_t(a.H) * a.D * kEb;    // bytes from token to token
   const uint8_t* x = (plane ? a.v : a.k) +
                      (int64_t(b) * a.T + (start + first - L)) * tok + int64_t(h) * a.D * kEb;
   const int gpt = a.D >> 3;                        // groups of 8 numbers a token
   const int groups = cnt * gpt;
-  constexpr int kHold = 8;                         // groups that a lane keeps
-  constexpr int kRaw = kF32 ? 2 : 1;
-  uint4 raw[kHold][kRaw];
-#pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int g = lane + 32 * i;
-    if (g < groups) {
-      const int t = g / gpt;
-      load8<kF32>(x + t * tok + (g - t * gpt) * 8 * kEb, raw[i]);
-    }
-  }
-  float amax = 0.0f;
-  int bad = 0;
-#pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    if (lane + 32 * i < groups) {
-      float f[8];
-      bad |= unpack8<kF32>(raw[i], f);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) amax = fmaxf(amax, fabsf(f[q]));
-    }
-  }
-  for (int g = lane + 32 * kHold; g < groups; g += 32) {
-    uint4 r[kRaw];
-    float f[8];
+  constexpr int kHold = kF32 ? 4 : 8;              // groups that a lane keeps
+  auto at = [&](int g) {
     const int t = g / gpt;
-    load8<kF32>(x + t * tok + (g - t * gpt) * 8 * kEb, r);
-    bad |= unpack8<kF32>(r, f);
+    return x + t * tok + (g - t * gpt) * 8 * kEb;
+  };
+  Eight<kF32> raw[kHold];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) amax = fmaxf(amax, fabsf(f[q]));
+  for (int i = 0; i < kHold; ++i)
+    if (lane + 32 * i < groups) raw[i].load(at(lane + 32 * i));
+  if (id < 0 || id >= a.NB) {
+    if (a.err && lane == 0) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
+    return;
   }
-  // non-negative floats order as their bit patterns
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  bad = __reduce_or_sync(0xffffffffu, bad);
-  const int e_new = q8_scale_exp(amax);
-  float scale = q8_pow2(e_new);
+  uint8_t* codes = a.pool + id * a.block_bytes + unit * a.bs * a.D;
+  float* sp = a.scales + id * a.block_scales + unit;
+  const float was = first > 0 ? *sp : 0.0f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (lane + 32 * i < groups) top = raw[i].top(top);
+  for (int g = lane + 32 * kHold; g < groups; g += 32) {
+    Eight<kF32> r;
+    r.load(at(g));
+    top = r.top(top);
+  }
+  if (!kF32) top = max(top << 16, top & 0xffff0000u);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const bool guard = top >= 0x7f800000u;  // an infinity or a NaN among the numbers
+  if (guard) {
+    float m = 0.0f;
+#pragma unroll 1
+    for (int g = lane; g < groups; g += 32) {
+      Eight<kF32> r;
+      float f[8];
+      r.load(at(g));
+      r.values(f, true);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));
+    }
+    top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+  }
+  float scale = q8_pow2(q8_scale_exp(__uint_as_float(top)));
   if (first > 0) scale = fmaxf(scale, was);
-  // x / scale: scale is q8_pow2(e_new), or an older and larger one, which the
-  // caller may have set to any number; the division is exact for a power of two
+  // an older and larger scale may be any number that the caller has put there
+  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
+  const float inv = 1.0f / scale;
   if (first > 0 && scale != was) {
     const float r = was / scale;
     const int words = first * a.D / 16;
@@ -170,28 +185,42 @@ __global__ void __launch_bounds__(kApThreads) kv_q8_append_kernel(const AppendAr
       *reinterpret_cast<uint4*>(codes + g * 16) = c;
     }
   }
-  auto put = [&](int g, const uint4* r) {
+  uint8_t* to = codes + int64_t(first) * a.D;
+  auto put = [&](int g, const Eight<kF32>& r) {
     float f[8];
-    unpack8<kF32>(r, f);
+    r.values(f, false);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[q] = f[q] / scale;
+    for (int q = 0; q < 8; ++q) f[q] *= inv;
     uint2 c;
     c.x = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
     c.y = f32x4_to_e4m3(f[4], f[5], f[6], f[7]);
-    *reinterpret_cast<uint2*>(codes + int64_t(first) * a.D + g * 8) = c;
+    *reinterpret_cast<uint2*>(to + g * 8) = c;
   };
+  if (exact && !guard) {
 #pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (lane + 32 * i < groups) put(lane + 32 * i, raw[i]);
-  for (int g = lane + 32 * kHold; g < groups; g += 32) {
-    uint4 r[kRaw];
-    const int t = g / gpt;
-    load8<kF32>(x + t * tok + (g - t * gpt) * 8 * kEb, r);
-    put(g, r);
+    for (int i = 0; i < kHold; ++i)
+      if (lane + 32 * i < groups) put(lane + 32 * i, raw[i]);
+    for (int g = lane + 32 * kHold; g < groups; g += 32) {
+      Eight<kF32> r;
+      r.load(at(g));
+      put(g, r);
+    }
+  } else {
+#pragma unroll 1
+    for (int g = lane; g < groups; g += 32) {
+      Eight<kF32> r;
+      float f[8];
+      r.load(at(g));
+      r.values(f, true);
+      uint2 c;
+      c.x = f32x4_to_e4m3(f[0] / scale, f[1] / scale, f[2] / scale, f[3] / scale);
+      c.y = f32x4_to_e4m3(f[4] / scale, f[5] / scale, f[6] / scale, f[7] / scale);
+      *reinterpret_cast<uint2*>(to + g * 8) = c;
+    }
   }
   if (lane == 0) {
     *sp = scale;
-    if (bad && a.err) atomicOr(a.err, SPEC_DERR_VALUE);
+    if (guard && a.err) atomicOr(a.err, SPEC_DERR_VALUE);
   }
 }
 
