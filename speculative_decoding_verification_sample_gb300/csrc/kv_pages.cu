@@ -430,7 +430,6 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkAr
   const int np = min(a.chunk, a.planes - p0);
   const int64_t plane = int64_t(a.bs) * a.tb;
   const int vec = off * (a.tb / 16);  // 16-byte words of a plane's tokens
-  const int total = some ? np * vec : 0;
   const uint8_t* from = a.pool + ((some ? x : 0) * a.planes + p0) * plane;
   uint8_t* to = a.pool;
   bool waited = false;
@@ -447,18 +446,23 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkAr
     }
     return true;
   };
-  for (int g0 = threadIdx.x; g0 < total; g0 += kForkThreads * kForkWords) {
+  // warps take 32 words at a time, through the planes
+  const int lane = threadIdx.x & 31, rows = (vec + 31) / 32;
+  int p = 0, c = threadIdx.x >> 5;
+  if (some)
+    for (; c >= rows; c -= rows) ++p;
+  while (some && p < np) {
     uint4 v[kForkWords];
     int64_t o[kForkWords];
 #pragma unroll
     for (int k = 0; k < kForkWords; ++k) {
-      const int g = g0 + k * kForkThreads;
+      const int g = 32 * c + lane;
       o[k] = -1;
-      if (g < total) {
-        const int p = g / vec;
-        o[k] = p * plane + int64_t(g - p * vec) * 16;
+      if (p < np && g < vec) {
+        o[k] = p * plane + int64_t(g) * 16;
         v[k] = __ldcg(reinterpret_cast<const uint4*>(from + o[k]));
       }
+      for (c += kForkThreads / 32; c >= rows; c -= rows) ++p;
     }
     if (!plan_ok()) return;
 #pragma unroll

@@ -51,18 +51,18 @@ constexpr float kTcSlack = 8.0f;            // binades by which keys may exceed 
 constexpr float kTcLift = 64.0f;            // 1 enters as 2^6: 2^6 2^8 < 2^16, e5m2's range
 constexpr int kTcSmem = 113 * 1024 - 512;   // of one CTA, two per SM
 
-template <int NR, int QB>
+template <int NR>
 struct TcShared {
-  alignas(16) float row_c[QB][NR];  // query row's scale * softmax_scale * log2(e)
+  alignas(16) float row_c[2][NR];  // query row's scale * softmax_scale * log2(e)
   alignas(16) float row_nm[NR];     // minus the reference of the exponentials
   alignas(16) float row_a[NR];      // rescale factor, then that of the output
   alignas(16) float part[4][NR];    // the warps' maxima, then sums
   alignas(16) float zero[NR];
-  uint64_t row_to[NR];              // where the row's outputs go, 0: nowhere
-  Segment seg[QB];                  // the items that the queries belong to
-  int64_t row_off[QB][NR];          // row of q and out, -1: none
-  int row_t[QB][NR];                // query (T for rows that do not exist)
-  uint32_t row_mask[QB][NR];
+  uint64_t row_to[NR];              // where the row's outputs go
+  Segment seg[2];                   // the items that the queries belong to
+  int64_t row_off[2][NR];          // row of q and out, -1: none
+  int row_t[2][NR];                // query (T for rows that do not exist)
+  uint32_t row_mask[2][NR];
   alignas(16) float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
   int2 tile[kTcScaleRing];  // first position; whether every query sees every key
   uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full,
@@ -84,12 +84,14 @@ struct TcShape {
   static constexpr int kSlot = kAttnTile * D;
   static constexpr int kQ = 2 * NR * D;
   static constexpr int kP = 3 * NO * kAttnTile;
-  static constexpr int kQBufs = NR <= 48 ? 2 : 1;          // two where four slots still fit
-  static constexpr int kSmall = kQBufs * kQ + kP + int(sizeof(TcShared<NR, kQBufs>));
+  static constexpr int kSmall = 2 * kQ + kP + int(sizeof(TcShared<NR>));
   static constexpr int kFit = (kTcSmem - kSmall) / kSlot;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
-  static constexpr int kSBufs = 4 * NR + NO <= 256 ? 2 : 1;
-  static constexpr int kCols = kSBufs * 2 * NR + NO;
+  // The three terms of P side by side as one operand of three times the columns: V is
+  // read once instead of three times, and O's three parts are summed at the end.
+  static constexpr int kTerms = NR <= 32 ? 3 : 1;
+  static constexpr int kSBufs = 4 * NR + kTerms * NO <= 256 ? 2 : 1;
+  static constexpr int kCols = kSBufs * 2 * NR + kTerms * NO;
   static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static constexpr size_t kBytes = size_t(kSlots) * kSlot + kSmall;
   static_assert(kCols <= 256 && kSlots >= 3, "two CTAs per SM");
@@ -183,7 +185,7 @@ __device__ __forceinline__ void reduce8(float (*v)[8], int lane) {
 
 // Which of the rows [col0, col0 + w) of an item see position p, as bits. Rows are
 // ordered by query, so those of a chain are a range of them.
-__device__ __forceinline__ uint32_t seen_rows(const AttnArgs& a, const Segment& g,
+__device__ __noinline__ uint32_t seen_rows(const AttnArgs& a, const Segment& g,
                                               const uint32_t* row_mask, const int* row_t, int p,
                                               int col0, int w) {
   const RowSpan& s = g.s;
@@ -201,6 +203,16 @@ __device__ __forceinline__ uint32_t seen_rows(const AttnArgs& a, const Segment& 
   const int lo = max(0, first * a.G - base), hi = min(w, end * a.G - base);
   if (hi <= lo) return 0u;
   return (hi == 32 ? ~0u : (1u << hi) - 1u) & (~0u << lo);
+}
+
+// Zeroes row `key` of a V tile: what lies there is not a number of the sequence
+// (and 0 * NaN is NaN).
+template <int D>
+__device__ __noinline__ void clear_row(uint8_t* tile, int key) {
+  uint4* v = reinterpret_cast<uint4*>(tile + key * D);
+#pragma unroll 1
+  for (int x = 0; x < D / 16; ++x)  // the lanes start in different banks
+    v[(x + key) % (D / 16)] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // An item's queries as two e4m3 terms a number, by warp w of n: kPerRow lanes a row,
@@ -282,13 +294,13 @@ template <int NR, int D>
 __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     attn_tc_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map) {
   using S = TcShape<NR, D>;
-  constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs, QB = S::kQBufs;
+  constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs;
   constexpr int kTmaWarp = S::kSoftmax / 32, kMmaWarp = kTmaWarp + 1, kQWarp = kTmaWarp + 2;
   constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // TMA and operands: 128- or 64-byte swizzle
   extern __shared__ __align__(1024) uint8_t sm[];  // ring, queries, P, the rest
   uint8_t* q_s = sm + NS * S::kSlot;
-  uint8_t* p_s = q_s + QB * S::kQ;
-  TcShared<NR, QB>& sh = *reinterpret_cast<TcShared<NR, QB>*>(p_s + S::kP);
+  uint8_t* p_s = q_s + 2 * S::kQ;
+  TcShared<NR>& sh = *reinterpret_cast<TcShared<NR>*>(p_s + S::kP);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, nc = gridDim.x;
   int64_t* prefix = reinterpret_cast<int64_t*>(p_s);  // before the first item only
@@ -371,8 +383,6 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       const float* sp = a.scales + (ok ? cur * a.block_scales : 0) + g.h;
       const int p0 = tile_start(g.s, k);
       const bool open = __all_sync(0xffffffffu, ok || lane >= pages) && tile_open(a, g.s, p0);
-      // with one query buffer an item's first scores wait for the outputs before them
-      const bool v_first = QB == 1 && k == g.t0;
       if (++k == g.t1 && j + 1 < tiles) {
         next_segment(a, g, plan.u1);
         k = g.t0;
@@ -380,7 +390,6 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       if (j + 1 < tiles) id = page_id(k);  // in flight while this tile's slots are awaited
       if (cur != -2 && !ok && a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
       const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-      if (j > 0 && v_first) load(v_ok, v_c1, v_plane);
       load(mask, c1, plane);
       bool copying = false;
       if (lane < pages) {
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       if (copying) cp_async_arrive(&sh.scales_full[sring.at]);
       else mbar_arrive(&sh.scales_full[sring.at]);
       sring.next();
-      if (j > 0 && !v_first) load(v_ok, v_c1, v_plane);
+      if (j > 0) load(v_ok, v_c1, v_plane);
       v_ok = mask;
       v_c1 = c1;
       v_plane = plane + a.H;
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
       constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, 2 * NR);
-      constexpr uint32_t idesc_o = tc_idesc(0, 1, 1, 1, 128, NO);
+      constexpr uint32_t idesc_o = tc_idesc(0, 1, 1, 1, 128, S::kTerms * NO);
       const uint64_t slot0 = tc_desc(smem_u32(sm), 16, 8 * D, kSwz);
       const uint64_t v_slot0 = tc_desc(smem_u32(sm), 0, 8 * D, kSwz);
       const uint64_t q0 = tc_desc(smem_u32(q_s), 16, 8 * D, kSwz);
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       int k = g.t0;  // tile of the next scores
       TcRing<NS> ring;
       TcRing<SB> sbuf;
-      TcRing<QB> qbuf;
+      TcRing<2> qbuf;
       uint32_t p_phase = 0;
       auto scores = [&]() {  // returns whether the tile is its item's first
         const bool first = k == g.t0;
@@ -457,7 +466,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
 #pragma unroll
         for (int x = 0; x < kAttnTile / 32; ++x)
 #pragma unroll
-          for (int m = 0; m < 3; ++m)
+          for (int m = 0; m < 3; m += S::kTerms)
             tc_mma_f8(tmem + SB * 2 * NR, v_desc + x * (32 * D / 16),
                       p0 + (m * NO * kAttnTile + x * 512) / 16, idesc_o,
                       !(first && x == 0 && m == 0));
@@ -467,12 +476,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       };
       bool first = scores();
       for (int j = 0; j < tiles; ++j) {
-        // the order of the copies
-        const bool v_first = QB == 1 && k == g.t0;
         bool next = false;
-        if (j + 1 < tiles && !v_first) next = scores();
+        if (j + 1 < tiles) next = scores();  // the order of the copies
         outputs(first);
-        if (j + 1 < tiles && v_first) next = scores();
         first = next;
       }
     }
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   } else if (work && warp >= kQWarp) {
     // ---------------------------------------------------------------- queries
     // of the next item while this one is worked on; the first item's were taken by all
-    TcRing<QB> qbuf;
+    TcRing<2> qbuf;
     for (bool first = true;; first = false) {
       const int qb = qbuf.at;
       if (!first) {
@@ -504,7 +510,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     const uint32_t lane_addr = tmem + (uint32_t(gw * 32) << 16) + col0;
     const uint32_t o_addr = lane_addr + SB * 2 * NR;
     const int page = key >> (a.bs >= kAttnTile ? 7 : 31 - __clz(a.bs));
-    TcRing<QB> qbuf;
+    TcRing<2> qbuf;
     int j = 0;  // tile of the CTA
     auto wait_outputs = [&]() {  // of the tile before
       tc_wait(&sh.pv_done, (j & 1) ^ 1, &sh.abort, a.err);
@@ -625,13 +631,15 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
             wait_outputs();
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < chunks; ++x) {
+            for (int x = 0; x < S::kTerms * chunks; ++x) {
+              const int r = 8 * (x % chunks);
+              const uint32_t at = o_addr + x / chunks * NO + r;
               float o[8];
-              tmem_ld8(o_addr + 8 * x, o);
+              tmem_ld8(at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] *= ra[8 * x + q];
-              tmem_st8(o_addr + 8 * x, o);
+              for (int q = 0; q < 8; ++q) o[q] *= ra[r + q];
+              tmem_st8(at, o);
             }
             tmem_wait_st();
           }
@@ -676,14 +684,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
             *reinterpret_cast<uint2*>(d + m * NO * kAttnTile) = make_uint2(t[m][0], t[m][1]);
         }
         if (!open && group == 0 && (!(ks == ks) || !needed(g.s, info.x + key, 1))) {
-          // what lies in this V row is not a number of the sequence (and 0 * NaN is NaN)
-          const bool k_after = j + 1 < tiles && !(QB == 1 && j + 1 == j_end);
-          const int vi = 2 * j + (k_after ? 2 : 1);  // loads before it: 0 .. j or j + 1 of K
+          const int vi = 2 * j + (j + 1 < tiles ? 2 : 1);  // loads before it: j or j + 1 of K
           tc_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, a.err);
-          uint4* v = reinterpret_cast<uint4*>(sm + vi % NS * S::kSlot + key * D);
-#pragma unroll 1
-          for (int x = 0; x < D / 16; ++x)  // the lanes start in different banks
-            v[(x + key) % (D / 16)] = make_uint4(0u, 0u, 0u, 0u);
+          clear_row<D>(sm + vi % NS * S::kSlot, key);
         }
         fence_async_smem();
         tc_fence_before();
@@ -713,13 +716,12 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         // scales, so a sum by itself may be as far from 1 as those.
         const int e = sum > 0.0f && sum <= FLT_MAX ? int(__float_as_uint(sum) >> 23) - 127 : 0;
         const float unlift = q8_pow2(vref) / kTcLift;
-        ra[key] = (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : q8_pow2(-e)) * unlift;
+        const float down = q8_pow2(-e);
+        ra[key] = (!whole ? down : sum == 0.0f ? 0.0f : __fdividef(down, sum * down)) * unlift;
         const int64_t off = sh.row_off[qb][col0 + key], part = slot * a.rows_per_block + col0 + key;
-        uint64_t to = 0;
-        if (off >= 0)
-          to = whole ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + off * D)
-                     : reinterpret_cast<uint64_t>(a.parts + part * D);
-        sh.row_to[col0 + key] = to;
+        sh.row_to[col0 + key] =
+            whole ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + off * D)
+                  : reinterpret_cast<uint64_t>(a.parts + part * D);
         if (!whole && off >= 0)
           a.stats[part] = make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e),
                                       sum * q8_pow2(-e));
@@ -728,21 +730,27 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       wait_outputs();
       tc_fence_after();
       const bool last = last_of_cta(g);
+      const int live = min(W, min(a.rows_per_block, a.R - g.rb * a.rows_per_block) - col0);
 #pragma unroll 1
       for (int x = 0; x < chunks; ++x) {
-        float o[8];
-        tmem_ld8(o_addr + 8 * x, o);
-        tmem_wait_ld();
-        if (D == 128 || key < D) {
+        float o[S::kTerms][8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint64_t to = sh.row_to[col0 + 8 * x + q];
-            const float v = o[q] * ra[8 * x + q];
-            if (to == 0) continue;
-            if (whole) reinterpret_cast<__nv_bfloat16*>(to)[key] = __float2bfloat16(v);
-            else reinterpret_cast<float*>(to)[key] = v;
-          }
+        for (int m = 0; m < S::kTerms; ++m) tmem_ld8(o_addr + m * NO + 8 * x, o[m]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+#pragma unroll
+          for (int m = 1; m < S::kTerms; ++m) o[0][q] += o[m][q];
+          o[0][q] *= ra[8 * x + q];
         }
+        if (D < 128 && key >= D) continue;
+        const uint64_t* to = &sh.row_to[col0 + 8 * x];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (8 * x + q < live) {
+            if (whole) reinterpret_cast<__nv_bfloat16*>(to[q])[key] = __float2bfloat16(o[0][q]);
+            else reinterpret_cast<float*>(to[q])[key] = o[0][q];
+          }
       }
       tc_fence_before();  // the next item's products overwrite O after its p_full
       mbar_arrive(&sh.q_empty[qb]);
