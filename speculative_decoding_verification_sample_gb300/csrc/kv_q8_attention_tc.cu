@@ -67,7 +67,7 @@ struct TcShared {
   int2 tile[kTcScaleRing];  // first position; whether every query sees every key
   uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full,
       pv_done, q_full[2], q_empty[2];
-  int64_t warp_sum[12];
+  int64_t warp_sum[16];
   uint32_t tmem;
   int abort;
 };
@@ -79,7 +79,8 @@ struct TcShape {
   static constexpr int NO = (NR + 15) / 16 * 16;
   static constexpr int kGroups = NR > 24 ? 2 : 1;
   static constexpr int kSoftmax = 128 * kGroups;
-  static constexpr int kThreads = kSoftmax + 128;
+  static constexpr int kQWarps = kGroups == 1 ? 2 : 1;     // 288 and 384 threads, two CTAs per SM
+  static constexpr int kThreads = kSoftmax + 96 + 32 * kQWarps;
   static constexpr int W = NR / kGroups;                   // rows of a group
   static constexpr int kSlot = kAttnTile * D;
   static constexpr int kQ = 2 * NR * D;
@@ -183,24 +184,23 @@ __device__ __forceinline__ void reduce8(float (*v)[8], int lane) {
     for (int x = 0; x < N; ++x) v[x][0] += __shfl_xor_sync(0xffffffffu, v[x][0], o);
 }
 
-// Which of the rows [col0, col0 + w) of an item see position p, as bits. Rows are
-// ordered by query, so those of a chain are a range of them.
-__device__ __noinline__ uint32_t seen_rows(const AttnArgs& a, const Segment& g,
-                                              const uint32_t* row_mask, const int* row_t, int p,
-                                              int col0, int w) {
-  const RowSpan& s = g.s;
-  if (p >= s.end) return 0u;
-  if (a.tree && p >= s.L) {
+// Which of w rows of an item, the first of them row `base` of the kv head, see
+// position p, as bits. Rows are ordered by query, so those of a chain are a range of
+// them; `mask` is null for a chain. Arguments by value: what a function takes by
+// reference goes through local memory, that is (with this much shared memory) L2.
+__device__ __noinline__ uint32_t seen_rows(int L, int n, int end, int G, int window, int sinks,
+                                           int base, int w, const uint32_t* mask, const int* row_t,
+                                           int p) {
+  if (p >= end) return 0u;
+  if (mask && p >= L) {
     uint32_t m = 0;
 #pragma unroll 1
-    for (int r = 0; r < w; ++r)
-      m |= uint32_t(row_t[col0 + r] < s.n && (row_mask[col0 + r] >> (p - s.L) & 1u)) << r;
+    for (int r = 0; r < w; ++r) m |= uint32_t(row_t[r] < n && (mask[r] >> (p - L) & 1u)) << r;
     return m;
   }
-  const int first = max(0, p - s.L);
-  const int end = a.window == 0 || p < a.sinks ? s.n : max(0, min(s.n, p - s.L + a.window));
-  const int base = g.rb * a.rows_per_block + col0;
-  const int lo = max(0, first * a.G - base), hi = min(w, end * a.G - base);
+  const int first = max(0, p - L);
+  const int last = window == 0 || p < sinks ? n : max(0, min(n, p - L + window));
+  const int lo = max(0, first * G - base), hi = min(w, last * G - base);
   if (hi <= lo) return 0u;
   return (hi == 32 ? ~0u : (1u << hi) - 1u) & (~0u << lo);
 }
@@ -216,40 +216,39 @@ __device__ __noinline__ void clear_row(uint8_t* tile, int key) {
 }
 
 // An item's queries as two e4m3 terms a number, by warp w of n: kPerRow lanes a row,
-// 8 numbers each; and what the softmax needs to know of the rows. One copy of the
-// code for its two callers, the next rows' loads in flight.
-template <int NR, int D, class Shared>
-__device__ __noinline__ void prepare_rows(const AttnArgs& a, Shared& sh, const Segment& g,
-                                          uint8_t* qs, int qb, int w, int n) {
+// 8 numbers each; and what the softmax needs to know of the rows.
+template <int NR, int D>
+__device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh, const Segment& g,
+                                             uint8_t* qs, int qb, int w, int n) {
   constexpr int kPerRow = D / 8, kRows = 32 / kPerRow;
   const int lane = threadIdx.x & 31, d8 = lane % kPerRow;
-  struct Row {
-    uint4 x;
-    int64_t off;
-    int t;
-  };
+  const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
+  const int64_t base = int64_t(g.b) * a.T * a.H * a.G + g.h * a.G;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) + d8;
+  uint4 next;
+  int64_t next_off;
+  int next_t;
   auto fetch = [&](int r) {
-    Row o;
-    const int row = g.rb * a.rows_per_block + r;
-    const bool live = r < a.rows_per_block && row < a.R;
-    o.t = live ? row / a.G : a.T;
-    o.off = live ? (int64_t(g.b) * a.T + o.t) * a.H * a.G + g.h * a.G + (row - o.t * a.G) : -1;
-    o.x = make_uint4(0u, 0u, 0u, 0u);
-    if (live)
-      o.x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + o.off * D +
-                                            d8 * 8);
-    return o;
+    next = make_uint4(0u, 0u, 0u, 0u);
+    next_off = -1;
+    next_t = a.T;
+    if (r < rows) {
+      const int row = g.rb * a.rows_per_block + r;
+      next_t = row / a.G;
+      next_off = base + int64_t(next_t) * a.H * a.G + (row - next_t * a.G);
+      next = q[next_off * (D / 8)];
+    }
   };
   int r = w * kRows + lane / kPerRow;
-  Row next = fetch(r);
+  fetch(r);
 #pragma unroll 1
   for (int i = w * kRows; i < NR; i += n * kRows) {
-    const Row o = next;
-    const int row = r;
+    const int row = r, t = next_t;
+    const int64_t off = next_off;
+    const uint32_t u[4] = {next.x, next.y, next.z, next.w};
     r += n * kRows;
-    if (i + n * kRows < NR) next = fetch(r);
+    fetch(r);  // in flight while this row is converted
     float f[8], lo[8];
-    const uint32_t u[4] = {o.x.x, o.x.y, o.x.z, o.x.w};
     uint32_t top = 0;
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
@@ -283,9 +282,9 @@ __device__ __noinline__ void prepare_rows(const AttnArgs& a, Shared& sh, const S
       // a row with an infinity or a NaN: its scores are NaN
       sh.row_c[qb][row] =
           top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
-      sh.row_t[qb][row] = o.t;
-      sh.row_off[qb][row] = o.off;
-      sh.row_mask[qb][row] = a.tree && o.off >= 0 ? a.tree[int64_t(g.b) * a.T + o.t] : 0u;
+      sh.row_t[qb][row] = t;
+      sh.row_off[qb][row] = off;
+      sh.row_mask[qb][row] = a.tree && off >= 0 ? a.tree[int64_t(g.b) * a.T + t] : 0u;
     }
   }
 }
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     attn_tc_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map) {
   using S = TcShape<NR, D>;
   constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs;
-  constexpr int kTmaWarp = S::kSoftmax / 32, kMmaWarp = kTmaWarp + 1, kQWarp = kTmaWarp + 2;
+  constexpr int kTmaWarp = S::kSoftmax / 32, kMmaWarp = kTmaWarp + 2, kQWarp = kTmaWarp + 3;
   constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // TMA and operands: 128- or 64-byte swizzle
   extern __shared__ __align__(1024) uint8_t sm[];  // ring, queries, P, the rest
   uint8_t* q_s = sm + NS * S::kSlot;
@@ -315,7 +314,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], S::kSoftmax);
-      mbar_init(&sh.q_full[i], 64);
+      mbar_init(&sh.q_full[i], 32 * S::kQWarps);
       mbar_init(&sh.q_empty[i], 1 + S::kSoftmax);
     }
     mbar_init(&sh.p_full, S::kSoftmax);
@@ -341,56 +340,85 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   if (work) g = find_segment(a, prefix, plan.u0, plan.u1);
   __syncthreads();
   const int tiles = int(plan.u1 - plan.u0);
-  if (work && (warp < kTmaWarp || warp >= kQWarp)) {
-    // the first item's queries
-    prepare_rows<NR, D>(a, sh, g, q_s, 0, warp < kTmaWarp ? warp : warp - 2, S::kSoftmax / 32 + 2);
-    fence_async_smem();
-    asm volatile("bar.sync 3, %0;" ::"n"(S::kSoftmax + 64) : "memory");
-  }
   auto last_of_cta = [&](const Segment& s) { return s.u + (s.t1 - s.t0) >= plan.u1; };
 
-  if (work && warp == kTmaWarp) {
+  if (work && (warp < kTmaWarp || warp >= kQWarp)) {
+    // ---------------------------------------------------------------- queries
+    // The first item's are taken by the softmax warps too; the next ones' by their own
+    // warps, while the item before is worked on. One place in the code for both.
+    TcRing<2> qbuf;
+    int w = warp < kTmaWarp ? warp : warp - 3, n = S::kSoftmax / 32 + S::kQWarps;
+    for (bool first = true;; first = false) {
+      const int qb = qbuf.at;
+      if (!first) {
+        // called into L2 while the buffer is still in use: DRAM's latency under this load
+        // is several times a row's conversion
+        const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
+        constexpr int kLines = D / 64;  // of 128 bytes
+        for (int x = tid - kQWarp * 32; x < rows * kLines; x += 32 * S::kQWarps) {
+          const int row = g.rb * a.rows_per_block + x / kLines, t = row / a.G;
+          const int64_t off =
+              (int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G);
+          prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + off * D + x % kLines * 64);
+        }
+        tc_wait(&sh.q_empty[qb], qbuf.phase ^ 1, &sh.abort, a.err);
+      }
+      prepare_rows<NR, D>(a, sh, g, q_s + qb * S::kQ, qb, w, n);
+      fence_async_smem();
+      if (first) asm volatile("bar.sync 3, %0;" ::"n"(S::kSoftmax + 32 * S::kQWarps) : "memory");
+      if (warp < kTmaWarp) break;
+      w = warp - kQWarp;
+      n = S::kQWarps;
+      if (lane == 0 && warp == kQWarp) sh.seg[qb] = g;
+      mbar_arrive(&sh.q_full[qb]);
+      if (first && lane == 0 && warp == kQWarp) write_join(a, plan, &g, c);
+      qbuf.next();
+      if (last_of_cta(g)) break;
+      next_segment(a, g, plan.u1);
+    }
+  }
+  if (work && (warp == kTmaWarp || warp == kTmaWarp + 1)) {
     // ---------------------------------------------------------------- TMA
+    // One warp for K (and the scales), one for V: a lane issues a block's copy, the
+    // lanes of a warp one after the other (some 100 cycles each), which for blocks of 16
+    // tokens is what one warp could not do fast enough. The ring's slots are taken in the
+    // order K_0, then K_(j+1) and V_j in turn, as the products take them: a V tile loaded
+    // with its K tile would hold its slot for longer.
+    const bool is_v = warp != kTmaWarp;
     const int bs = min(a.bs, kAttnTile);  // rows of one copy
     const int pages = kAttnTile / bs;
     auto page_id = [&](int k) {
       const int pos = tile_start(g.s, k) + lane * bs;
       return lane < pages && needed(g.s, pos, bs) ? a.bt[int64_t(g.b) * a.MB + pos / a.bs] : -2;
     };
-    // Order of the copies: K_0, then K_(j+1) and V_j in turn, the order in which the
-    // products take them; a V tile loaded with its K tile would hold its slot for longer.
-    int k = g.t0, loads = 0;
-    TcRing<NS> ring;
+    int k = g.t0;
     TcRing<kTcScaleRing> sring;
-    int id = page_id(k), v_c1 = 0, v_plane = 0;  // V of the tile before
-    uint32_t v_ok = 0;
-    auto load = [&](uint32_t mask, int c1, int plane) {
-      tc_wait(&sh.empty[ring.at], ring.phase ^ 1, &sh.abort, a.err);
-      if (lane == 0)
-        mbar_arrive_expect_tx(&sh.full[ring.at], __popc(mask) * uint32_t(bs) * D);
-      __syncwarp();
-      if (mask >> lane & 1)
-        tma_tile_3d(sm + ring.at * S::kSlot + lane * bs * D, &map, 0, c1, plane,
-                    &sh.full[ring.at]);
-      ring.next();
-      ++loads;
-    };
+    int id = page_id(k);
     for (int j = 0; j < tiles; ++j) {
       const int cur = id;
       const bool ok = cur >= 0 && cur < a.NB;
-      const int c1 = a.bs <= kAttnTile ? 0 : tile_start(g.s, k) % a.bs;
+      const int p0 = tile_start(g.s, k);
+      const int c1 = a.bs <= kAttnTile ? 0 : p0 % a.bs;
       const int plane = ok ? cur * a.planes_per_block + a.plane0 + g.h : 0;
       const float* sp = a.scales + (ok ? cur * a.block_scales : 0) + g.h;
-      const int p0 = tile_start(g.s, k);
-      const bool open = __all_sync(0xffffffffu, ok || lane >= pages) && tile_open(a, g.s, p0);
+      const bool open =
+          !is_v && __all_sync(0xffffffffu, ok || lane >= pages) && tile_open(a, g.s, p0);
       if (++k == g.t1 && j + 1 < tiles) {
         next_segment(a, g, plan.u1);
         k = g.t0;
       }
-      if (j + 1 < tiles) id = page_id(k);  // in flight while this tile's slots are awaited
+      if (j + 1 < tiles) id = page_id(k);  // in flight while this tile's slot is awaited
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * uint32_t(bs) * D;
+      const int i = is_v ? 2 * j + (j + 1 < tiles ? 2 : 1) : max(0, 2 * j - 1);
+      const int slot = i % NS;
+      tc_wait(&sh.empty[slot], ((i / NS) & 1) ^ 1, &sh.abort, a.err);
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+      __syncwarp();
+      if (ok)
+        tma_tile_3d(sm + slot * S::kSlot + lane * bs * D, &map, 0, c1, plane + (is_v ? a.H : 0),
+                    &sh.full[slot]);
+      if (is_v) continue;
       if (cur != -2 && !ok && a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-      load(mask, c1, plane);
       bool copying = false;
       if (lane < pages) {
         float* ks = &sh.ks[sring.at][lane];
@@ -409,15 +437,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       if (copying) cp_async_arrive(&sh.scales_full[sring.at]);
       else mbar_arrive(&sh.scales_full[sring.at]);
       sring.next();
-      if (j > 0) load(v_ok, v_c1, v_plane);
-      v_ok = mask;
-      v_c1 = c1;
-      v_plane = plane + a.H;
     }
-    load(v_ok, v_c1, v_plane);
-    // the copies land before the CTA may leave
-    for (int x = max(0, loads - NS); x < loads; ++x)
-      tc_wait(&sh.full[x % NS], (x / NS) & 1, &sh.abort, a.err);
+    // the last copies land before the CTA may leave
+    if (is_v)
+      for (int x = max(0, 2 * tiles - NS); x < 2 * tiles; ++x)
+        tc_wait(&sh.full[x % NS], (x / NS) & 1, &sh.abort, a.err);
   } else if (work && warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
@@ -483,24 +507,6 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       }
     }
     __syncwarp();
-  } else if (work && warp >= kQWarp) {
-    // ---------------------------------------------------------------- queries
-    // of the next item while this one is worked on; the first item's were taken by all
-    TcRing<2> qbuf;
-    for (bool first = true;; first = false) {
-      const int qb = qbuf.at;
-      if (!first) {
-        tc_wait(&sh.q_empty[qb], qbuf.phase ^ 1, &sh.abort, a.err);
-        prepare_rows<NR, D>(a, sh, g, q_s + qb * S::kQ, qb, warp - kQWarp, 2);
-        fence_async_smem();
-      }
-      if (lane == 0 && warp == kQWarp) sh.seg[qb] = g;
-      mbar_arrive(&sh.q_full[qb]);
-      if (first && lane == 0 && warp == kQWarp) write_join(a, plan, &g, c);
-      qbuf.next();
-      if (last_of_cta(g)) break;
-      next_segment(a, g, plan.u1);
-    }
   } else if (work && warp < kTmaWarp) {
     // ---------------------------------------------------------------- softmax
     constexpr int W = S::W, chunks = W / 8;  // rows of a group, in eights
@@ -551,8 +557,12 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         const float vr = vs * vdown;
         const float lv = float(scale_binade(vr));  // vr <= 2^lv
         const float2 ks2 = make_float2(ks, ks);
-        const uint32_t seen = open ? ~0u : seen_rows(a, g, sh.row_mask[qb], sh.row_t[qb],
-                                                     info.x + key, col0, W);
+        uint32_t seen = ~0u;
+        if (!open)
+          seen = seen_rows(g.s.L, g.s.n, g.s.end, a.G, a.window, a.sinks,
+                           g.rb * a.rows_per_block + col0, W,
+                           a.tree ? sh.row_mask[qb] + col0 : nullptr, sh.row_t[qb] + col0,
+                           info.x + key);
         float2 y[W / 2];  // exponents relative to the references
         tc_wait(&sh.s_full[sb], (SB == 2 ? j >> 1 : j) & 1, &sh.abort, a.err);
         tc_fence_after();
@@ -761,7 +771,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   if (warp >= kQWarp) {
     // what needs no place in the row of the others' work
     if (!work && tid == kQWarp * 32) write_join(a, plan, nullptr, c);
-    write_empty_rows<__nv_bfloat16>(a, c, nc, tid - kQWarp * 32, 64);
+    write_empty_rows<__nv_bfloat16>(a, c, nc, tid - kQWarp * 32, 32 * S::kQWarps);
   }
   tc_fence_before();
   __syncthreads();
