@@ -33,7 +33,7 @@
 
 #include <cfloat>
 #include <cstdint>
-#include <mutex>
+#include <type_traits>
 
 #include "../../include/specverify.h"
 #include "launch.h"
@@ -79,8 +79,7 @@ struct TcShape {
   static constexpr int NO = (NR + 15) / 16 * 16;
   static constexpr int kGroups = NR > 24 ? 2 : 1;
   static constexpr int kSoftmax = 128 * kGroups;
-  static constexpr int kQWarps = kGroups == 1 ? 2 : 1;     // 288 and 384 threads, two CTAs per SM
-  static constexpr int kThreads = kSoftmax + 96 + 32 * kQWarps;
+  static constexpr int kThreads = kSoftmax + 128;          // 256: 128 registers, 384: 80
   static constexpr int W = NR / kGroups;                   // rows of a group
   static constexpr int kSlot = kAttnTile * D;
   static constexpr int kQ = 2 * NR * D;
@@ -90,7 +89,7 @@ struct TcShape {
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   // The three terms of P side by side as one operand of three times the columns: V is
   // read once instead of three times, and O's three parts are summed at the end.
-  static constexpr int kTerms = NR <= 32 ? 3 : 1;
+  static constexpr int kTerms = NR <= 48 ? 3 : 1;
   static constexpr int kSBufs = 4 * NR + kTerms * NO <= 256 ? 2 : 1;
   static constexpr int kCols = kSBufs * 2 * NR + kTerms * NO;
   static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
@@ -216,27 +215,28 @@ __device__ __noinline__ void clear_row(uint8_t* tile, int key) {
 }
 
 // An item's queries as two e4m3 terms a number, by warp w of n: kPerRow lanes a row,
-// 8 numbers each; and what the softmax needs to know of the rows.
+// 16 numbers each; and what the softmax needs to know of the rows.
 template <int NR, int D>
 __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh, const Segment& g,
                                              uint8_t* qs, int qb, int w, int n) {
-  constexpr int kPerRow = D / 8, kRows = 32 / kPerRow;
-  const int lane = threadIdx.x & 31, d8 = lane % kPerRow;
+  constexpr int kPerRow = D / 16, kRows = 32 / kPerRow;
+  const int lane = threadIdx.x & 31, d16 = lane % kPerRow;
   const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
   const int64_t base = int64_t(g.b) * a.T * a.H * a.G + g.h * a.G;
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) + d8;
-  uint4 next;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) + 2 * d16;
+  uint4 next[2];
   int64_t next_off;
   int next_t;
   auto fetch = [&](int r) {
-    next = make_uint4(0u, 0u, 0u, 0u);
+    next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
     next_off = -1;
     next_t = a.T;
     if (r < rows) {
       const int row = g.rb * a.rows_per_block + r;
       next_t = row / a.G;
       next_off = base + int64_t(next_t) * a.H * a.G + (row - next_t * a.G);
-      next = q[next_off * (D / 8)];
+      next[0] = q[next_off * (D / 8)];
+      next[1] = q[next_off * (D / 8) + 1];
     }
   };
   int r = w * kRows + lane / kPerRow;
@@ -245,46 +245,47 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
   for (int i = w * kRows; i < NR; i += n * kRows) {
     const int row = r, t = next_t;
     const int64_t off = next_off;
-    const uint32_t u[4] = {next.x, next.y, next.z, next.w};
+    const uint32_t u[8] = {next[0].x, next[0].y, next[0].z, next[0].w,
+                           next[1].x, next[1].y, next[1].z, next[1].w};
     r += n * kRows;
     fetch(r);  // in flight while this row is converted
-    float f[8], lo[8];
-    uint32_t top = 0;
+    uint32_t two = 0;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      f[2 * y] = __uint_as_float(u[y] << 16);
-      f[2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
-      top = max(top, max((u[y] << 16) & 0x7fffffffu, u[y] & 0x7fff0000u));
-    }
+    for (int y = 0; y < 8; ++y) two = __vmaxu2(two, u[y] & 0x7fff7fffu);
+    uint32_t top = max(two << 16, two & 0xffff0000u);
 #pragma unroll
     for (int s = kPerRow / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
     // |f| 2^-e in [128, 256) at the largest; e stays in range for bf16 subnormals
     const int e = max(int(top >> 23) - 127 - 7, -110);
     const float down = q8_pow2(-e);
-    uint32_t hw[2], lw[2];
+    uint32_t hw[4], lw[4];
 #pragma unroll
-    for (int y = 0; y < 8; ++y) f[y] *= down;
-    hw[0] = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
-    hw[1] = f32x4_to_e4m3(f[4], f[5], f[6], f[7]);
-    e4m3x4_to_f32(hw[0], lo);
-    e4m3x4_to_f32(hw[1], lo + 4);
+    for (int y = 0; y < 4; ++y) {
+      float f[4], lo[4];
 #pragma unroll
-    for (int y = 0; y < 8; ++y) lo[y] = f[y] - lo[y];
-    lw[0] = f32x4_to_e4m3(lo[0], lo[1], lo[2], lo[3]);
-    lw[1] = f32x4_to_e4m3(lo[4], lo[5], lo[6], lo[7]);
+      for (int z = 0; z < 2; ++z) {
+        f[2 * z] = __uint_as_float(u[2 * y + z] << 16) * down;
+        f[2 * z + 1] = __uint_as_float(u[2 * y + z] & 0xffff0000u) * down;
+      }
+      hw[y] = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
+      e4m3x4_to_f32(hw[y], lo);
+      lw[y] = f32x4_to_e4m3(f[0] - lo[0], f[1] - lo[1], f[2] - lo[2], f[3] - lo[3]);
+    }
     auto put = [&](int rr, const uint32_t* v) {
-      const int chunk = (d8 >> 1) ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
-      *reinterpret_cast<uint2*>(qs + rr * D + chunk * 16 + (d8 & 1) * 8) = make_uint2(v[0], v[1]);
+      const int chunk = d16 ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
+      *reinterpret_cast<uint4*>(qs + rr * D + chunk * 16) = make_uint4(v[0], v[1], v[2], v[3]);
     };
-    put(row, hw);
-    put(NR + row, lw);
-    if (d8 == 0) {
-      // a row with an infinity or a NaN: its scores are NaN
-      sh.row_c[qb][row] =
-          top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
-      sh.row_t[qb][row] = t;
-      sh.row_off[qb][row] = off;
-      sh.row_mask[qb][row] = a.tree && off >= 0 ? a.tree[int64_t(g.b) * a.T + t] : 0u;
+    if (row < NR) {
+      put(row, hw);
+      put(NR + row, lw);
+      if (d16 == 0) {
+        // a row with an infinity or a NaN: its scores are NaN
+        sh.row_c[qb][row] =
+            top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
+        sh.row_t[qb][row] = t;
+        sh.row_off[qb][row] = off;
+        sh.row_mask[qb][row] = a.tree && off >= 0 ? a.tree[int64_t(g.b) * a.T + t] : 0u;
+      }
     }
   }
 }
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], S::kSoftmax);
-      mbar_init(&sh.q_full[i], 32 * S::kQWarps);
+      mbar_init(&sh.q_full[i], 32);
       mbar_init(&sh.q_empty[i], 1 + S::kSoftmax);
     }
     mbar_init(&sh.p_full, S::kSoftmax);
@@ -342,12 +343,12 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   const int tiles = int(plan.u1 - plan.u0);
   auto last_of_cta = [&](const Segment& s) { return s.u + (s.t1 - s.t0) >= plan.u1; };
 
-  if (work && (warp < kTmaWarp || warp >= kQWarp)) {
+  if (work && (warp < kTmaWarp || warp == kQWarp)) {
     // ---------------------------------------------------------------- queries
-    // The first item's are taken by the softmax warps too; the next ones' by their own
-    // warps, while the item before is worked on. One place in the code for both.
+    // The first item's are taken by the softmax warps too; the next ones' by a warp of
+    // their own, while the item before is worked on. One place in the code for both.
     TcRing<2> qbuf;
-    int w = warp < kTmaWarp ? warp : warp - 3, n = S::kSoftmax / 32 + S::kQWarps;
+    int w = warp < kTmaWarp ? warp : warp - 3, n = S::kSoftmax / 32 + 1;
     for (bool first = true;; first = false) {
       const int qb = qbuf.at;
       if (!first) {
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         // is several times a row's conversion
         const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
         constexpr int kLines = D / 64;  // of 128 bytes
-        for (int x = tid - kQWarp * 32; x < rows * kLines; x += 32 * S::kQWarps) {
+        for (int x = lane; x < rows * kLines; x += 32) {
           const int row = g.rb * a.rows_per_block + x / kLines, t = row / a.G;
           const int64_t off =
               (int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G);
@@ -365,13 +366,13 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       }
       prepare_rows<NR, D>(a, sh, g, q_s + qb * S::kQ, qb, w, n);
       fence_async_smem();
-      if (first) asm volatile("bar.sync 3, %0;" ::"n"(S::kSoftmax + 32 * S::kQWarps) : "memory");
+      if (first) asm volatile("bar.sync 3, %0;" ::"n"(S::kSoftmax + 32) : "memory");
       if (warp < kTmaWarp) break;
-      w = warp - kQWarp;
-      n = S::kQWarps;
-      if (lane == 0 && warp == kQWarp) sh.seg[qb] = g;
+      w = 0;
+      n = 1;
+      if (lane == 0) sh.seg[qb] = g;
       mbar_arrive(&sh.q_full[qb]);
-      if (first && lane == 0 && warp == kQWarp) write_join(a, plan, &g, c);
+      if (first && lane == 0) write_join(a, plan, &g, c);
       qbuf.next();
       if (last_of_cta(g)) break;
       next_segment(a, g, plan.u1);
@@ -563,64 +564,93 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
                            g.rb * a.rows_per_block + col0, W,
                            a.tree ? sh.row_mask[qb] + col0 : nullptr, sh.row_t[qb] + col0,
                            info.x + key);
-        float2 y[W / 2];  // exponents relative to the references
         tc_wait(&sh.s_full[sb], (SB == 2 ? j >> 1 : j) & 1, &sh.abort, a.err);
         tc_fence_after();
         const uint32_t s_addr = lane_addr + sb * 2 * NR;
-        // s k c (- m) of all rows; the scores come in two terms
-        auto exponents = [&](const float* minus) {
+        // s k c (- m) of N eights of rows from the x-th; the scores come in two terms
+        auto exponents = [&](int x, auto count, const float* minus, float2* y) {
+          constexpr int N = decltype(count)::value;
+          float hi[8 * N], lo[8 * N];
 #pragma unroll
-          for (int x = 0; x < chunks; x += 2) {  // two loads in flight
-            const int n = x + 1 < chunks ? 2 : 1;
-            float hi[16], lo[16];
-            tmem_ld8(s_addr + 8 * x, hi);
-            tmem_ld8(s_addr + NR + 8 * x, lo);
-            if (n == 2) {
-              tmem_ld8(s_addr + 8 * x + 8, hi + 8);
-              tmem_ld8(s_addr + NR + 8 * x + 8, lo + 8);
-            }
-            tmem_wait_ld();
+          for (int i = 0; i < N; ++i) {
+            tmem_ld8(s_addr + 8 * (x + i), hi + 8 * i);
+            tmem_ld8(s_addr + NR + 8 * (x + i), lo + 8 * i);
+          }
+          tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 2 * n; ++q) {
-              const float4 c4 = *reinterpret_cast<const float4*>(&sh.row_c[qb][col0 + 8 * x + 4 * q]);
-              const float4 m4 = *reinterpret_cast<const float4*>(minus + 8 * x + 4 * q);
-              const float2 s0 = __fadd2_rn(make_float2(hi[4 * q], hi[4 * q + 1]),
-                                           make_float2(lo[4 * q], lo[4 * q + 1]));
-              const float2 s1 = __fadd2_rn(make_float2(hi[4 * q + 2], hi[4 * q + 3]),
-                                           make_float2(lo[4 * q + 2], lo[4 * q + 3]));
-              y[4 * x + 2 * q] = __ffma2_rn(__fmul2_rn(s0, ks2), make_float2(c4.x, c4.y),
-                                            make_float2(m4.x, m4.y));
-              y[4 * x + 2 * q + 1] = __ffma2_rn(__fmul2_rn(s1, ks2), make_float2(c4.z, c4.w),
-                                                make_float2(m4.z, m4.w));
-            }
+          for (int q = 0; q < 2 * N; ++q) {
+            const float4 c4 = *reinterpret_cast<const float4*>(&sh.row_c[qb][col0 + 8 * x + 4 * q]);
+            const float4 m4 = *reinterpret_cast<const float4*>(minus + 8 * x + 4 * q);
+            const float2 s0 = __fadd2_rn(make_float2(hi[4 * q], hi[4 * q + 1]),
+                                         make_float2(lo[4 * q], lo[4 * q + 1]));
+            const float2 s1 = __fadd2_rn(make_float2(hi[4 * q + 2], hi[4 * q + 3]),
+                                         make_float2(lo[4 * q + 2], lo[4 * q + 3]));
+            y[2 * q] = __ffma2_rn(__fmul2_rn(s0, ks2), make_float2(c4.x, c4.y),
+                                  make_float2(m4.x, m4.y));
+            y[2 * q + 1] = __ffma2_rn(__fmul2_rn(s1, ks2), make_float2(c4.z, c4.w),
+                                      make_float2(m4.z, m4.w));
           }
           if (!open) {
+            const uint32_t bits = seen >> (8 * x);
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-              if (!(seen >> (2 * i) & 1u)) y[i].x = -INFINITY;
-              if (!(seen >> (2 * i + 1) & 1u)) y[i].y = -INFINITY;
+            for (int i = 0; i < 4 * N; ++i) {
+              if (!(bits >> (2 * i) & 1u)) y[i].x = -INFINITY;
+              if (!(bits >> (2 * i + 1) & 1u)) y[i].y = -INFINITY;
             }
           }
+        };
+        using One = std::integral_constant<int, 1>;
+        using Two = std::integral_constant<int, 2>;
+        // With few rows the exponents stay in registers between the test of the references
+        // and the exponentials. With 24 or 32 rows a thread they do not fit beside the sums
+        // (a spill goes to L2: shared memory takes L1's place), and are taken twice.
+        constexpr bool kKeep = S::kGroups == 1;
+        float2 y[kKeep ? W / 2 : 1];
+        auto all_exponents = [&](const float* minus) {
+#pragma unroll
+          for (int x = 0; x + 1 < chunks; x += 2) exponents(x, Two(), minus, y + 4 * x);
+          if (chunks % 2) exponents(chunks - 1, One(), minus, y + 4 * (chunks - 1));
         };
         // Usually one pass: relative to the references, none of which has to move. The
         // first tile and one that exceeds them take the plain scores (again).
         bool relative = j > j_first;
         for (;;) {
-          exponents(relative ? nm : sh.zero);
+          if (kKeep) all_exponents(relative ? nm : sh.zero);
           if (!relative) break;
           float top = -INFINITY;
+          if (kKeep) {
 #pragma unroll
-          for (int i = 0; i < W / 2; ++i) top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+            for (int i = 0; i < W / 2; ++i) top = fmaxf(top, fmaxf(y[i].x, y[i].y));
+          } else {
+#pragma unroll
+            for (int x = 0; x < chunks; ++x) {
+              float2 e[4];
+              exponents(x, One(), nm, e);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(e[i].x, e[i].y));
+            }
+          }
           if (!bar_group_or(group, top > kTcSlack - lv)) break;
           relative = false;
         }
         if (!relative) {
           // move the references to this tile's maxima (a NaN score is passed over: it makes
           // its row's sum NaN by itself)
+          auto maxima = [&](int at, float2 e) {
+            const float m0 = warp_max(e.x + lv), m1 = warp_max(e.y + lv);
+            if (lane == 0) *reinterpret_cast<float2*>(&sh.part[gw][col0 + at]) = make_float2(m0, m1);
+          };
+          if (kKeep) {
 #pragma unroll
-          for (int i = 0; i < W / 2; ++i) {
-            const float m0 = warp_max(y[i].x + lv), m1 = warp_max(y[i].y + lv);
-            if (lane == i) *reinterpret_cast<float2*>(&sh.part[gw][col0 + 2 * i]) = make_float2(m0, m1);
+            for (int i = 0; i < W / 2; ++i) maxima(2 * i, y[i]);
+          } else {
+#pragma unroll 1
+            for (int x = 0; x < chunks; ++x) {
+              float2 e[4];
+              exponents(x, One(), sh.zero, e);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) maxima(8 * x + 2 * i, e[i]);
+            }
           }
           bar_group(group);
           if (key < W) {
@@ -631,9 +661,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
             ra[key] = ex2_approx(old - m);
           }
           bar_group(group);
+          if (kKeep) {
 #pragma unroll
-          for (int i = 0; i < W / 2; ++i)
-            y[i] = __fadd2_rn(y[i], *reinterpret_cast<const float2*>(nm + 2 * i));
+            for (int i = 0; i < W / 2; ++i)
+              y[i] = __fadd2_rn(y[i], *reinterpret_cast<const float2*>(nm + 2 * i));
+          }
           if (j > j_first) {
 #pragma unroll
             for (int i = 0; i < W / 2; ++i)
@@ -654,13 +686,17 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
             tmem_wait_st();
           }
         }
-        tc_fence_before();
-        mbar_arrive(&sh.s_empty[sb]);
+        if (kKeep) {
+          tc_fence_before();
+          mbar_arrive(&sh.s_empty[sb]);
+        }
         wait_outputs();  // P may be replaced
         const float2 lift = make_float2(vr * kTcLift, vr * kTcLift);
         uint8_t* p_to = p_s + key * 16;
 #pragma unroll
         for (int x = 0; x < chunks; ++x) {
+          float2 e[4];
+          if (!kKeep) exponents(x, One(), nm, e);
           uint32_t t[3][2];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -668,7 +704,8 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const int i = 4 * x + 2 * q + w;
-              const float2 p = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+              const float2 z = kKeep ? y[kKeep ? i : 0] : e[2 * q + w];
+              const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
               l[i] = __fadd2_rn(l[i], p);
               const float2 v = __fmul2_rn(p, lift);
               asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[w]) : "f"(v.y), "f"(v.x));
@@ -692,6 +729,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
 #pragma unroll
           for (int m = 0; m < 3; ++m)
             *reinterpret_cast<uint2*>(d + m * NO * kAttnTile) = make_uint2(t[m][0], t[m][1]);
+        }
+        if (!kKeep) {
+          tc_fence_before();
+          mbar_arrive(&sh.s_empty[sb]);
         }
         if (!open && group == 0 && (!(ks == ks) || !needed(g.s, info.x + key, 1))) {
           const int vi = 2 * j + (j + 1 < tiles ? 2 : 1);  // loads before it: j or j + 1 of K
@@ -768,10 +809,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       bar_group(group);  // row_a, row_nm, part: every thread is done with the item
     }
   }
-  if (warp >= kQWarp) {
+  if (warp == kQWarp) {
     // what needs no place in the row of the others' work
-    if (!work && tid == kQWarp * 32) write_join(a, plan, nullptr, c);
-    write_empty_rows<__nv_bfloat16>(a, c, nc, tid - kQWarp * 32, 32 * S::kQWarps);
+    if (!work && lane == 0) write_join(a, plan, nullptr, c);
+    write_empty_rows<__nv_bfloat16>(a, c, nc, lane, 32);
   }
   tc_fence_before();
   __syncthreads();
