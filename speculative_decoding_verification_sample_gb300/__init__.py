@@ -374,7 +374,20 @@ def kv_commit_rollback(block_table, seq_lens, num_accepted, prov_blocks, kv_pool
 
 
 # The calls below take a few microseconds on the device, so their arguments are checked with
-# few Python steps: _arg covers the usual case and leaves the message to _check.
+# few Python steps: _arg covers the usual case and leaves the message to _check, and the torch
+# names are looked up once.
+_int32 = _float32 = _e4m3 = _uint8 = _raw_current = None
+
+
+def _ready() -> ctypes.CDLL:
+    """The library, with the torch names of this section set."""
+    global _int32, _float32, _e4m3, _uint8, _raw_current
+    import torch
+    _int32, _float32, _uint8 = torch.int32, torch.float32, torch.uint8
+    _e4m3, _raw_current = torch.float8_e4m3fn, torch._C._cuda_getCurrentRawStream
+    return lib()
+
+
 def _arg(t, name, ndim, dtype):
     """The device pointer of a contiguous CUDA tensor of `ndim` dims and `dtype` (None: any)."""
     try:
@@ -391,8 +404,7 @@ def _vec(t, name, n):
     """The pointer of an optional int32 [n] tensor."""
     if t is None:
         return None
-    import torch
-    p = _arg(t, name, 1, torch.int32)
+    p = _arg(t, name, 1, _int32)
     if t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
     return p
@@ -402,8 +414,7 @@ def _word(t, name):
     """The pointer of an optional int32 tensor of at least one entry."""
     if t is None:
         return None
-    import torch
-    p = _arg(t, name, 1, torch.int32)
+    p = _arg(t, name, 1, _int32)
     if t.shape[0] < 1:
         raise ValueError(f"{name} must have an entry")
     return p
@@ -413,16 +424,14 @@ def _raw_stream(stream, device):
     """cudaStream_t of `stream`, or of the current stream of the tensors' device."""
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_current(device.index)
 
 
 def _q8_pool(kv_pool, kv_scales):
     """Checks the 8-bit pool and its scales; returns their pointers and the pool's shape."""
-    import torch
     pool = _arg(kv_pool, "kv_pool", 6, None)
-    scales = _arg(kv_scales, "kv_scales", 4, torch.float32)
-    if kv_pool.dtype is not torch.float8_e4m3fn and kv_pool.dtype is not torch.uint8:
+    scales = _arg(kv_scales, "kv_scales", 4, _float32)
+    if kv_pool.dtype is not _e4m3 and kv_pool.dtype is not _uint8:
         raise TypeError(f"kv_pool must be float8_e4m3fn (or its uint8 bytes), got {kv_pool.dtype}")
     shape = kv_pool.shape
     if shape[2] != 2 or kv_scales.shape != shape[:4]:
@@ -436,16 +445,16 @@ def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int 
     """Writes k, v [B, T, kv_heads, head_dim] (bf16 or fp32) to positions seq_lens[b] ... of the
     8-bit cache's `layer`: kv_pool [num_blocks, layers, 2, kv_heads, block_size, head_dim]
     float8_e4m3fn, kv_scales [num_blocks, layers, 2, kv_heads]. num_new: optional int32 [B]."""
-    import torch
+    L = _lib if _int32 is not None else _ready()
     pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
     kp = _arg(k, "k", 4, None)
     vp = _arg(v, "v", 4, k.dtype)
-    bt = _arg(block_table, "block_table", 2, torch.int32)
+    bt = _arg(block_table, "block_table", 2, _int32)
     B, T, kh, kd = k.shape
     rows, MB = block_table.shape
     if v.shape != k.shape or kh != H or kd != D or rows != B:
         raise ValueError(f"k and v must be [B, T, {H}, {D}] and block_table [B, max_blocks]")
-    st = (_lib or lib()).kv_q8_append(
+    st = L.kv_q8_append(
         kp, vp, _dtype_code(k), pool, scales, bt, _vec(seq_lens, "seq_lens", B),
         _vec(num_new, "num_new", B), NB, NL, layer, H, D, bs, B, T, MB,
         _raw_stream(stream, k.device), _word(err_flag, "err_flag"))
@@ -496,11 +505,11 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
     tree_mask: optional int32 [B, T], bit s of entry t lets query t see position seq_lens[b] + s.
     workspace: a uint8 tensor of kv_q8_attention_workspace_bytes + 256; None: one that the
     binding keeps for the stream."""
-    import torch
+    L = _lib if _int32 is not None else _ready()
     pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
     qp = _arg(q, "q", 4, None)
     op = _arg(out, "out", 4, q.dtype)
-    bt = _arg(block_table, "block_table", 2, torch.int32)
+    bt = _arg(block_table, "block_table", 2, _int32)
     shape = q.shape
     B, T, Hq, qd = shape
     rows, MB = block_table.shape
@@ -508,7 +517,7 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
         raise ValueError(f"q and out must be [B, T, q_heads, {D}] and block_table [B, max_blocks]")
     tm = None
     if tree_mask is not None:
-        tm = _arg(tree_mask, "tree_mask", 2, torch.int32)
+        tm = _arg(tree_mask, "tree_mask", 2, _int32)
         if tuple(tree_mask.shape) != (B, T):
             raise ValueError(f"tree_mask must be [{B}, {T}], got {tuple(tree_mask.shape)}")
     device = q.device
@@ -518,7 +527,7 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
     else:
         off = (-workspace.data_ptr()) % 256
         wsp, wsn = workspace.data_ptr() + off, max(0, workspace.numel() - off)
-    st = (_lib or lib()).kv_q8_attention(
+    st = L.kv_q8_attention(
         qp, _dtype_code(q), pool, scales, bt, _vec(seq_lens, "seq_lens", B),
         _vec(num_new, "num_new", B), tm, op, D ** -0.5 if softmax_scale is None else softmax_scale,
         window, sinks, NB, NL, layer, Hq, H, D, bs, B, T, MB, wsp, wsn, raw,
@@ -530,10 +539,10 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
 def kv_reserve(block_table, seq_lens, free_stack, free_top, status, *, n: int, block_size: int,
                num_blocks: int, num_new=None, stream=None) -> None:
     """Blocks for n (or num_new[b]) tokens past seq_lens[b]; status receives 0 or error bits."""
-    import torch
-    bt = _arg(block_table, "block_table", 2, torch.int32)
+    L = _lib if _int32 is not None else _ready()
+    bt = _arg(block_table, "block_table", 2, _int32)
     B, MB = block_table.shape
-    st = (_lib or lib()).kv_reserve(
+    st = L.kv_reserve(
         bt, _vec(seq_lens, "seq_lens", B), _vec(num_new, "num_new", B), n, num_blocks, block_size,
         B, MB, _vec(free_stack, "free_stack", num_blocks), _word(free_top, "free_top"),
         _word(status, "status"), _raw_stream(stream, block_table.device))
@@ -546,8 +555,8 @@ def kv_fork(block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, free
     """Rows dst_rows[i] become copies of rows src_rows[i]: full blocks shared, tail blocks copied.
     kv_pool: the 8-bit pool with kv_scales, or kv_commit_rollback's [num_blocks, layers, 2,
     block_size, kv_heads, head_dim] pool without."""
-    import torch
-    bt = _arg(block_table, "block_table", 2, torch.int32)
+    L = _lib if _int32 is not None else _ready()
+    bt = _arg(block_table, "block_table", 2, _int32)
     B, MB = block_table.shape
     if kv_scales is not None:
         pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
@@ -560,9 +569,9 @@ def kv_fork(block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, free
         planes, token = NL * 2, H * D * kv_pool.element_size()
     if bs != block_size:
         raise ValueError(f"kv_pool holds blocks of {bs} tokens, not {block_size}")
-    src = _arg(src_rows, "src_rows", 1, torch.int32)
+    src = _arg(src_rows, "src_rows", 1, _int32)
     n = src_rows.shape[0]
-    st = (_lib or lib()).kv_fork(
+    st = L.kv_fork(
         bt, _vec(seq_lens, "seq_lens", B), _vec(extra_refs, "extra_refs", NB), src,
         _vec(dst_rows, "dst_rows", n), n, pool, planes, token, scales, NB, block_size, B, MB,
         _vec(free_stack, "free_stack", NB), _word(free_top, "free_top"), _word(status, "status"),
@@ -574,12 +583,12 @@ def kv_fork(block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, free
 def kv_free(block_table, seq_lens, extra_refs, rows, free_stack, free_top, status, *,
             num_blocks: int, stream=None) -> None:
     """Releases the listed rows; blocks that no other row holds go back on the free stack."""
-    import torch
-    bt = _arg(block_table, "block_table", 2, torch.int32)
+    L = _lib if _int32 is not None else _ready()
+    bt = _arg(block_table, "block_table", 2, _int32)
     B, MB = block_table.shape
-    st = (_lib or lib()).kv_free(
+    st = L.kv_free(
         bt, _vec(seq_lens, "seq_lens", B), _vec(extra_refs, "extra_refs", num_blocks),
-        _arg(rows, "rows", 1, torch.int32), rows.shape[0], num_blocks, B, MB,
+        _arg(rows, "rows", 1, _int32), rows.shape[0], num_blocks, B, MB,
         _vec(free_stack, "free_stack", num_blocks), _word(free_top, "free_top"),
         _word(status, "status"), _raw_stream(stream, block_table.device))
     if st != SPEC_OK:

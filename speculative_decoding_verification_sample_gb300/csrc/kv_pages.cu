@@ -446,28 +446,28 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const ForkAr
     }
     return true;
   };
-  // warps take 32 words at a time, through the planes
-  const int lane = threadIdx.x & 31, rows = (vec + 31) / 32;
-  int p = 0, c = threadIdx.x >> 5;
-  if (some)
-    for (; c >= rows; c -= rows) ++p;
-  while (some && p < np) {
-    uint4 v[kForkWords];
-    int64_t o[kForkWords];
+  // a warp takes two planes at a time, four times 32 words of each
+  const int lane = threadIdx.x & 31;
+  constexpr int kWarps = kForkThreads / 32, kEach = kForkWords / 2;
+  for (int p = threadIdx.x >> 5; some && p < np; p += 2 * kWarps) {
+    const bool two = p + kWarps < np;
+    for (int g0 = lane; g0 - lane < vec; g0 += 32 * kEach) {
+      uint4 v[2][kEach];
+      const int64_t o = p * plane + int64_t(g0) * 16;
 #pragma unroll
-    for (int k = 0; k < kForkWords; ++k) {
-      const int g = 32 * c + lane;
-      o[k] = -1;
-      if (p < np && g < vec) {
-        o[k] = p * plane + int64_t(g) * 16;
-        v[k] = __ldcg(reinterpret_cast<const uint4*>(from + o[k]));
-      }
-      for (c += kForkThreads / 32; c >= rows; c -= rows) ++p;
+      for (int k = 0; k < kEach; ++k)
+        if (g0 + 32 * k < vec) {
+          v[0][k] = __ldcg(reinterpret_cast<const uint4*>(from + o + 512 * k));
+          if (two) v[1][k] = __ldcg(reinterpret_cast<const uint4*>(from + o + kWarps * plane + 512 * k));
+        }
+      if (!plan_ok()) return;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (g0 + 32 * k < vec) {
+          *reinterpret_cast<uint4*>(to + o + 512 * k) = v[0][k];
+          if (two) *reinterpret_cast<uint4*>(to + o + kWarps * plane + 512 * k) = v[1][k];
+        }
     }
-    if (!plan_ok()) return;
-#pragma unroll
-    for (int k = 0; k < kForkWords; ++k)
-      if (o[k] >= 0) *reinterpret_cast<uint4*>(to + o[k]) = v[k];
   }
   if (!plan_ok() || !some) return;
   if (a.scales)

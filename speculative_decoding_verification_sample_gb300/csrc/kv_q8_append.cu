@@ -99,10 +99,9 @@ template <bool kF32>
 __global__ void __launch_bounds__(kApThreads) kv_q8_append_kernel(const AppendArgs a) {
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t task = int64_t(blockIdx.x) * (kApThreads / 32) + (threadIdx.x >> 5);
-  const int h = int(task % a.H);
-  const int plane = int(task / a.H % 2);
-  const int64_t w = task / (2 * a.H);
+  const uint32_t task = blockIdx.x * (kApThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t unit = task % (2 * a.H), w = task / (2 * a.H);  // unit: plane and head
+  const int plane = unit >= uint32_t(a.H), h = int(unit) - plane * a.H;
   const int b = int(w / a.J), jw = int(w % a.J);
   pdl_wait();
   if (b >= a.B) return;
@@ -118,7 +117,6 @@ __global__ void __launch_bounds__(kApThreads) kv_q8_append_kernel(const AppendAr
   const int first = max(L - start, 0);             // offset of the first new token
   const int cnt = min(a.bs, L + n - start) - first;
   const int id = a.bt[int64_t(b) * a.MB + j];
-  const int64_t unit = int64_t(plane) * a.H + h;
   const int64_t tok = int64_t(a.H) * a.D * kEb;    // bytes from token to token
   const uint8_t* x = (plane ? a.v : a.k) +
                      (int64_t(b) * a.T + (start + first - L)) * tok + int64_t(h) * a.D * kEb;
@@ -130,14 +128,22 @@ __global__ void __launch_bounds__(kApThreads) kv_q8_append_kernel(const AppendAr
     return x + t * tok + (g - t * gpt) * 8 * kEb;
   };
   Eight<kF32> raw[kHold];
+  if (32 % gpt == 0) {  // a lane's groups are 32 / gpt tokens apart
+    const uint8_t* p = at(lane);
+    const int64_t step = 32 / gpt * tok;
 #pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (lane + 32 * i < groups) raw[i].load(at(lane + 32 * i));
+    for (int i = 0; i < kHold; ++i)
+      if (lane + 32 * i < groups) raw[i].load(p + i * step);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (lane + 32 * i < groups) raw[i].load(at(lane + 32 * i));
+  }
   if (id < 0 || id >= a.NB) {
     if (a.err && lane == 0) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
     return;
   }
-  uint8_t* codes = a.pool + id * a.block_bytes + unit * a.bs * a.D;
+  uint8_t* codes = a.pool + id * a.block_bytes + int64_t(unit) * a.bs * a.D;
   float* sp = a.scales + id * a.block_scales + unit;
   const float was = first > 0 ? *sp : 0.0f;
   uint32_t top = 0;
@@ -247,7 +253,7 @@ int launch_kv_q8_append(const Q8AppendLaunch& k) {
   a.err = k.err;
   const int64_t tasks = int64_t(k.B) * a.J * 2 * k.H;
   const int64_t grid = (tasks + kApThreads / 32 - 1) / (kApThreads / 32);
-  if (grid > INT32_MAX) return SPEC_ENOTSUP;
+  if (tasks > INT32_MAX) return SPEC_ENOTSUP;
   cudaStream_t st = static_cast<cudaStream_t>(k.stream);
   return k.dtype == SPEC_F32
              ? launch_pdl(kv_q8_append_kernel<true>, dim3(unsigned(grid)), dim3(kApThreads), 0, st, a)
