@@ -126,21 +126,23 @@ __device__ PgAll pg_exchange(PgShared& sh, int cnt, int err) {
   return r;
 }
 
-// A CTA's part [e0, e1) of a flat list, in rounds of kPgThreads * kPgHeld entries;
-// thread t of a round has kPgHeld consecutive ones.
+// A CTA's part [e0, e1) of a flat list, in rounds; a thread has `held` consecutive
+// entries of a round, kPgHeld at most.
 template <int C>
 struct PgPart {
-  int e0, e1, rounds;
+  int e0, e1, held, rounds;
   __device__ PgPart(int total) {
     const int r = PgTeam<C>::rank();
     e0 = int(int64_t(total) * r / C);
     e1 = int(int64_t(total) * (r + 1) / C);
     // the same for every CTA of the team: all of them run all rounds
-    rounds = ((total + C - 1) / C + kPgThreads * kPgHeld - 1) / (kPgThreads * kPgHeld);
+    const int most = (total + C - 1) / C;
+    held = min(kPgHeld, max(1, (most + kPgThreads - 1) / kPgThreads));
+    rounds = (most + kPgThreads * held - 1) / (kPgThreads * held);
   }
   __device__ __forceinline__ int at(int round, int k) const {
-    const int e = e0 + (round * kPgThreads + int(threadIdx.x)) * kPgHeld + k;
-    return e < e1 ? e : -1;
+    const int e = e0 + (round * kPgThreads + int(threadIdx.x)) * held + k;
+    return k < held && e < e1 ? e : -1;
   }
 };
 
@@ -210,13 +212,14 @@ __device__ __forceinline__ void reserve_body(const ReserveArgs& a, PgShared& sh)
   int32_t* slot[kPgHeld];
   int x[kPgHeld];
   auto load = [&](int round) {  // entries of this thread, 0 where there is none
+    int b = part.at(round, 0) >= 0 ? pg_row(sh, a.B, part.at(round, 0)) : 0;
 #pragma unroll
     for (int k = 0; k < kPgHeld; ++k) {
       const int e = part.at(round, k);
       slot[k] = nullptr;
       x[k] = 0;
       if (e >= 0) {
-        const int b = pg_row(sh, a.B, e);
+        while (sh.prefix[b + 1] <= e) ++b;
         slot[k] = a.bt + int64_t(b) * a.MB + pg_cdiv(a.sl[b], a.bs) + (e - sh.prefix[b]);
         x[k] = *slot[k];
       }
@@ -315,7 +318,7 @@ __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) 
   // which this kernel does not change, and wait for it before they write.
   pdl_trigger();
   const int top = *a.ftop;
-  int err = 0;
+  int err = 0, mine = 0;  // mine: pairs of this thread with a partly filled tail block
   const int total = pg_prefix(sh, a.n, [&](int i) {
     const int s = a.src[i], d = a.dst[i];
     if (s < 0 || s >= a.B || d < 0 || d >= a.B) {
@@ -327,6 +330,7 @@ __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) 
       err |= SPEC_DERR_BAD_LENGTH;
       return 0;
     }
+    mine += L % a.bs != 0;
     return pg_cdiv(L, a.bs);
   });
   const PgPart<C> part(total);
@@ -334,12 +338,14 @@ __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) 
   int x[kPgHeld];
   int bad = 0;
   auto load = [&](int round) {
+    int i = part.at(round, 0) >= 0 ? pg_row(sh, a.n, part.at(round, 0)) : 0;
 #pragma unroll
     for (int k = 0; k < kPgHeld; ++k) {
       const int e = part.at(round, k);
       to[k] = nullptr;
       if (e >= 0) {
-        const int i = pg_row(sh, a.n, e), j = e - sh.prefix[i], s = a.src[i];
+        while (sh.prefix[i + 1] <= e) ++i;
+        const int j = e - sh.prefix[i], s = a.src[i];
         x[k] = a.bt[int64_t(s) * a.MB + j];
         to[k] = a.bt + int64_t(a.dst[i]) * a.MB + j;
         if (x[k] < 0 || x[k] >= a.NB || *to[k] != -1) bad = SPEC_DERR_BAD_BLOCK;
@@ -349,11 +355,8 @@ __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) 
   };
   for (int r = 0; r < part.rounds; ++r) load(r);
   err = pg_exchange<C>(sh, 0, err | bad).err;
-  // tails: pairs with a partly filled block, ranked in the order of the pairs
+  // tails are ranked in the order of the pairs (the prefix gave a thread the same ones)
   const int per = (a.n + kPgThreads - 1) / kPgThreads, i0 = tid * per;
-  int mine = 0;
-  if (err == 0)
-    for (int i = i0; i < i0 + per && i < a.n; ++i) mine += a.sl[a.src[i]] % a.bs != 0;
   int tails;
   const int at = pg_scan(mine, sh.warp, tails);
   if (err == 0 && (top < 0 || top > a.NB || tails > top)) err = SPEC_DERR_NO_SPACE;
@@ -531,14 +534,18 @@ __device__ __forceinline__ void free_body(const FreeArgs& a, PgShared& sh) {
   int32_t* slot[kPgHeld];
   int x[kPgHeld];  // block ids, -1: none
   auto load = [&](int round) {
+    const int e0 = max(0, part.at(round, 0));
+    int i = e0 / a.MB, j = e0 - i * a.MB - 1;
 #pragma unroll
     for (int k = 0; k < kPgHeld; ++k) {
-      const int e = part.at(round, k);
       slot[k] = nullptr;
       x[k] = -1;
-      if (e >= 0) {
-        const int i = e / a.MB;
-        slot[k] = a.bt + int64_t(a.rows[i]) * a.MB + (e - i * a.MB);
+      if (part.at(round, k) >= 0) {
+        if (++j == a.MB) {
+          j = 0;
+          ++i;
+        }
+        slot[k] = a.bt + int64_t(a.rows[i]) * a.MB + j;
         x[k] = *slot[k];
       }
     }
