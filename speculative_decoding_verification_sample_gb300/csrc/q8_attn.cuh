@@ -168,13 +168,13 @@ __device__ __forceinline__ Segment find_segment(const AttnArgs& a, const int64_t
     return (n | d) >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
   };
   const int64_t x = quotient(u, U);
-  int lo = 0, hi = blockDim.x - 1;  // the last chunk with prefix <= x
+  const int per = (a.B + blockDim.x - 1) / blockDim.x;
+  int lo = 0, hi = (a.B + per - 1) / per - 1;  // the last chunk with prefix <= x
   while (lo < hi) {
     const int m = (lo + hi + 1) >> 1;
     if (prefix[m] <= x) lo = m;
     else hi = m - 1;
   }
-  const int per = (a.B + blockDim.x - 1) / blockDim.x;
   Segment g;
   int64_t at = prefix[lo];
   int b = lo * per;
