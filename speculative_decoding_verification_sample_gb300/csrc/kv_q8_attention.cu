@@ -176,12 +176,19 @@ __global__ void __launch_bounds__(kAnyThreads) attn_any_kernel(const AttnArgs a)
 // ------------------------------------------------------------------ joining
 // CTA (c, y) joins rows 4 y .. 4 y + 3 of the item that ends in CTA c of the
 // attention kernel, two warps a row (even and odd parts), each warp's lanes
-// over the head's numbers.
+// over the head's numbers, four a lane. Bound by the latency of its dependent reads
+// (which parts, their statistics, their numbers), most of which lie in L2.
 constexpr int kJoinThreads = 256, kJoinRows = 4;
+
+__device__ __forceinline__ void store4(float* o, float4 v) { *reinterpret_cast<float4*>(o) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* o, float4 v) {
+  __nv_bfloat162 x[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+  *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(x);
+}
 
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
-  __shared__ float acc_s[kJoinRows][kAnyMaxD];
+  __shared__ float4 acc_s[kJoinRows][kAnyMaxD / 4];
   __shared__ float2 st_s[kJoinRows];
   pdl_trigger();
   pdl_wait();
@@ -193,42 +200,52 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   const bool live = r < a.rows_per_block && row < a.R;
   const int c0 = j.w & ~(1 << 30), slot0 = j.w >> 30 & 1;
   const int np = c - c0 + 1;
-  constexpr int kPer = kAnyMaxD / 32;
-  float m = -INFINITY, l = 0.0f, acc[kPer];
+  constexpr int kPer = kAnyMaxD / 128;
+  const int quads = a.D / 4;
+  float m = -INFINITY, l = 0.0f;
+  float4 acc[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-  auto add = [&](float pm, float pl, auto value) {
+  for (int i = 0; i < kPer; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](float pm, float pl, const float4* o) {
     const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.0f : mn;
     const float x = ex2_approx(m - base), y = ex2_approx(pm - base);
     l = l * x + pl * y;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < a.D) acc[i] = acc[i] * x + value(i) * y;
+      if (lane + 32 * i < quads) {
+        const float4 v = o[32 * i];
+        acc[i].x = acc[i].x * x + v.x * y;
+        acc[i].y = acc[i].y * x + v.y * y;
+        acc[i].z = acc[i].z * x + v.z * y;
+        acc[i].w = acc[i].w * x + v.w * y;
+      }
     m = mn;
   };
   if (live) {
+#pragma unroll 2
     for (int k = half; k < np; k += 2) {
-      const int64_t slot = 2 * int64_t(c0 + k) + (k == 0 ? slot0 : 0);
-      const float2 st = a.stats[slot * a.rows_per_block + r];
-      const float* o = a.parts + (slot * a.rows_per_block + r) * a.D + lane;
-      add(st.x, st.y, [&](int i) { return o[32 * i]; });
+      const int64_t part =
+          (2 * int64_t(c0 + k) + (k == 0 ? slot0 : 0)) * a.rows_per_block + r;
+      const float2 st = a.stats[part];
+      add(st.x, st.y, reinterpret_cast<const float4*>(a.parts + part * a.D) + lane);
     }
     if (half == 1) {
       st_s[rr] = make_float2(m, l);
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (lane + 32 * i < a.D) acc_s[rr][lane + 32 * i] = acc[i];
+        if (lane + 32 * i < quads) acc_s[rr][lane + 32 * i] = acc[i];
     }
   }
   __syncthreads();
   if (!live || half == 1) return;
-  add(st_s[rr].x, st_s[rr].y, [&](int i) { return acc_s[rr][lane + 32 * i]; });
+  add(st_s[rr].x, st_s[rr].y, &acc_s[rr][lane]);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   T* o = static_cast<T*>(a.out) +
-         ((int64_t(j.x) * a.T + row / a.G) * a.H * a.G + j.y * a.G + row % a.G) * a.D + lane;
+         ((int64_t(j.x) * a.T + row / a.G) * a.H * a.G + j.y * a.G + row % a.G) * a.D + 4 * lane;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < a.D) o[32 * i] = T(acc[i] * inv);
+    if (lane + 32 * i < quads)
+      store4(o + 128 * i, make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
 }
 
 int launch_attn_join(const AttnArgs& a, int nc, int dtype, void* stream) {
