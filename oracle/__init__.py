@@ -49,3 +49,5 @@ from .verify import (  # noqa: F401
 )
 from .kv import kv_commit, kv_truncate_inplace, pool_invariant_ok  # noqa: F401
 from .filters import filter_threshold, filter_thresholds, apply_threshold  # noqa: F401
+# oracle.q8 (8-bit cache: format, append, attention) and oracle.pages (reserve, fork, free)
+# are imported as modules by their tests.

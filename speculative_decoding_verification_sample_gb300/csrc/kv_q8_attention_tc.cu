@@ -23,10 +23,25 @@
 // 8: then O and l are rescaled once; otherwise a tile costs no reduction over its
 // keys. l stays per thread (one key of every tile) until the item ends.
 //
+//
 // Roles: one or two groups of 4 softmax warps (thread = key of the tile, each group
-// its own query rows), a TMA warp, an MMA warp and a warp that prepares the next
+// its own query rows), two copy warps, an MMA warp and a warp that prepares the next
 // item's queries. K and V tiles share one ring of slots, released separately. Two
 // CTAs per SM hide each other's latencies.
+//
+// Bound by memory up to 24 query rows of a kv head: 256 rows of 512-4096 tokens, 8 kv
+// heads x 128, 20 query rows, 1.23 GB: 205 us = 6.0 TB/s (0.89 of the copy peak); 8 rows
+// 195 us; 2 rows of 100-131 thousand tokens 85 us (5.6 TB/s). Beyond that by the
+// softmax warps' instructions (about 11 for each 32 scores): 32 rows 222 us, 48 rows
+// 307 us; a window of 4096 over 56 rows 139 us (3.0 TB/s). The steps that mattered:
+// the hot loop must stay small (waits out of line, one copy of each block of code:
+// 334 to 242 us for the 20-row case), the copies of 16-token blocks need two warps,
+// an item's queries must be in L2 and converted before it begins (230 to 205 us), and
+// nothing may go through local memory, which this much shared memory pushes out to L2.
+// Not kept, for the 20-row case: two groups taking the tiles in turn (374 us), three
+// CTAs per SM with short rings (351 us), tiles called into L2 ahead of the copies
+// (281 us), the copies' coordinates made uniform by shuffles (316 us); for many rows,
+// exponentials taken before the references are tested (177 instead of 139 us: spills).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
