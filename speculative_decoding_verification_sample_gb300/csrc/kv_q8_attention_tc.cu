@@ -4,7 +4,7 @@
 // The cached codes go from TMA straight into tcgen05.mma: nothing converts them.
 // Both products are taken with the cache as the M operand, so that the few
 // query rows of a verification step fill the small N side:
-//   S^T [128 keys x 2 NR]  = K  [128 x D]   * (Qhi | Qlo)^T       e4m3 x e4m3
+//   S^T [128 keys x NO]    = K  [128 x D]   * (Qhi + Qlo)^T       e4m3 x e4m3
 //   O^T [D x NO]          += V^T [D x 128]  * (P0 + P1 + P2)^T    e4m3 x e5m2
 // K is read along D, V along its other side (D is contiguous), both through the
 // swizzle that TMA wrote. A block scale belongs to a key, that is to a TMEM lane
@@ -105,8 +105,8 @@ struct TcShape {
   // The three terms of P side by side as one operand of three times the columns: V is
   // read once instead of three times, and O's three parts are summed at the end.
   static constexpr int kTerms = NR <= 48 ? 3 : 1;
-  static constexpr int kSBufs = 4 * NR + kTerms * NO <= 256 ? 2 : 1;
-  static constexpr int kCols = kSBufs * 2 * NR + kTerms * NO;
+  static constexpr int kSBufs = (2 + kTerms) * NO <= 256 ? 2 : 1;
+  static constexpr int kCols = (kSBufs + kTerms) * NO;
   static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static constexpr size_t kBytes = size_t(kSlots) * kSlot + kSmall;
   static_assert(kCols <= 256 && kSlots >= 3, "two CTAs per SM");
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   } else if (work && warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
-      constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, 2 * NR);
+      constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, 128, NO);
       constexpr uint32_t idesc_o = tc_idesc(0, 1, 1, 1, 128, S::kTerms * NO);
       const uint64_t slot0 = tc_desc(smem_u32(sm), 16, 8 * D, kSwz);
       const uint64_t v_slot0 = tc_desc(smem_u32(sm), 0, 8 * D, kSwz);
@@ -480,9 +480,13 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         tc_fence_after();
         const uint64_t k_desc = slot0 + ring.at * (S::kSlot / 16);
         const uint64_t q_desc = q0 + qbuf.at * (S::kQ / 16);
+        // both terms of the queries into one sum (columns past the rows are not read)
 #pragma unroll
         for (int x = 0; x < D / 32; ++x)
-          tc_mma_f8(tmem + sbuf.at * 2 * NR, k_desc + 2 * x, q_desc + 2 * x, idesc_s, x > 0);
+          tc_mma_f8(tmem + sbuf.at * NO, k_desc + 2 * x, q_desc + 2 * x, idesc_s, x > 0);
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x)
+          tc_mma_f8(tmem + sbuf.at * NO, k_desc + 2 * x, q_desc + NR * D / 16 + 2 * x, idesc_s, true);
         tc_commit(&sh.empty[ring.at]);
         tc_commit(&sh.s_full[sbuf.at]);
         ring.next();
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         for (int x = 0; x < kAttnTile / 32; ++x)
 #pragma unroll
           for (int m = 0; m < 3; m += S::kTerms)
-            tc_mma_f8(tmem + SB * 2 * NR, v_desc + x * (32 * D / 16),
+            tc_mma_f8(tmem + SB * NO, v_desc + x * (32 * D / 16),
                       p0 + (m * NO * kAttnTile + x * 512) / 16, idesc_o,
                       !(first && x == 0 && m == 0));
         tc_commit(&sh.empty[ring.at]);
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     float* const nm = sh.row_nm + col0;
     float* const ra = sh.row_a + col0;
     const uint32_t lane_addr = tmem + (uint32_t(gw * 32) << 16) + col0;
-    const uint32_t o_addr = lane_addr + SB * 2 * NR;
+    const uint32_t o_addr = lane_addr + SB * NO;
     const int page = key >> (a.bs >= kAttnTile ? 7 : 31 - __clz(a.bs));
     TcRing<2> qbuf;
     int j = 0;  // tile of the CTA
@@ -581,25 +585,20 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
                            info.x + key);
         tc_wait(&sh.s_full[sb], (SB == 2 ? j >> 1 : j) & 1, &sh.abort, a.err);
         tc_fence_after();
-        const uint32_t s_addr = lane_addr + sb * 2 * NR;
-        // s k c (- m) of N eights of rows from the x-th; the scores come in two terms
+        const uint32_t s_addr = lane_addr + sb * NO;
+        // s k c (- m) of N eights of rows from the x-th
         auto exponents = [&](int x, auto count, const float* minus, float2* y) {
           constexpr int N = decltype(count)::value;
-          float hi[8 * N], lo[8 * N];
+          float z[8 * N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            tmem_ld8(s_addr + 8 * (x + i), hi + 8 * i);
-            tmem_ld8(s_addr + NR + 8 * (x + i), lo + 8 * i);
-          }
+          for (int i = 0; i < N; ++i) tmem_ld8(s_addr + 8 * (x + i), z + 8 * i);
           tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < 2 * N; ++q) {
             const float4 c4 = *reinterpret_cast<const float4*>(&sh.row_c[qb][col0 + 8 * x + 4 * q]);
             const float4 m4 = *reinterpret_cast<const float4*>(minus + 8 * x + 4 * q);
-            const float2 s0 = __fadd2_rn(make_float2(hi[4 * q], hi[4 * q + 1]),
-                                         make_float2(lo[4 * q], lo[4 * q + 1]));
-            const float2 s1 = __fadd2_rn(make_float2(hi[4 * q + 2], hi[4 * q + 3]),
-                                         make_float2(lo[4 * q + 2], lo[4 * q + 3]));
+            const float2 s0 = make_float2(z[4 * q], z[4 * q + 1]);
+            const float2 s1 = make_float2(z[4 * q + 2], z[4 * q + 3]);
             y[2 * q] = __ffma2_rn(__fmul2_rn(s0, ks2), make_float2(c4.x, c4.y),
                                   make_float2(m4.x, m4.y));
             y[2 * q + 1] = __ffma2_rn(__fmul2_rn(s1, ks2), make_float2(c4.z, c4.w),
@@ -619,7 +618,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         // With few rows the exponents stay in registers between the test of the references
         // and the exponentials. With 24 or 32 rows a thread they do not fit beside the sums
         // (a spill goes to L2: shared memory takes L1's place), and are taken twice.
-        constexpr bool kKeep = S::kGroups == 1;
+        constexpr bool kKeep = W <= 24;
         float2 y[kKeep ? W / 2 : 1];
         auto all_exponents = [&](const float* minus) {
 #pragma unroll
