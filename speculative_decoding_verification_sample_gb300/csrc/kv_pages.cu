@@ -31,6 +31,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "../../include/specverify.h"
@@ -54,7 +55,7 @@ constexpr int kForkMinPlanes = 8; // planes of a tail block that one CTA copies,
 struct PgShared {
   int prefix[kPgMaxRows + 1];  // flat index of each row's first entry
   int warp[kPgThreads / 32];
-  int cnt, err;                // this CTA's share, read by the cluster
+  int cnt[4], err[4];          // this CTA's share of each exchange, read by the cluster
 };
 
 // The CTAs that plan together: C = 1 or kPgCluster.
@@ -66,6 +67,15 @@ struct PgTeam {
   __device__ __forceinline__ static void sync() {
     if (C == 1) __syncthreads();
     else cg::this_cluster().sync();
+  }
+  // First and last step of a kernel: the exchanges' sums start at 0, and a CTA's shared
+  // memory stays until nobody reads it any more.
+  __device__ __forceinline__ static void enter(PgShared& sh) {
+    if (threadIdx.x < 4) sh.cnt[threadIdx.x] = sh.err[threadIdx.x] = 0;
+    __syncthreads();
+  }
+  __device__ __forceinline__ static void leave() {
+    if (C != 1) cg::this_cluster().sync();
   }
 };
 
@@ -92,41 +102,36 @@ __device__ int pg_scan(int v, int* warp, int& total) {
   return (w > 0 ? before : 0) + inc - v;
 }
 
-// Block-wide sum of counts and union of bits into sh.cnt, sh.err.
-__device__ void pg_publish(PgShared& sh, int cnt, int err) {
-  __syncthreads();
-  if (threadIdx.x == 0) sh.cnt = sh.err = 0;
-  __syncthreads();
-  const int c = __reduce_add_sync(0xffffffffu, cnt);
-  const int e = __reduce_or_sync(0xffffffffu, err);
-  if ((threadIdx.x & 31) == 0) {
-    if (c) atomicAdd(&sh.cnt, c);
-    if (e) atomicOr(&sh.err, e);
-  }
-  __syncthreads();
-}
-
-// Over the team: sum of the counts, union of the errors, sum over lower ranks.
+// Over the team: sum of the counts, union of the errors, sum over lower ranks. Each
+// exchange of a kernel has a place of its own, so one barrier is enough.
 struct PgAll {
   int cnt, err, before;
 };
 template <int C>
-__device__ PgAll pg_exchange(PgShared& sh, int cnt, int err) {
-  pg_publish(sh, cnt, err);
-  if (C == 1) return PgAll{sh.cnt, sh.err, 0};
+__device__ PgAll pg_exchange(PgShared& sh, int place, int cnt, int err) {
+  const int c = __reduce_add_sync(0xffffffffu, cnt);
+  const int e = __reduce_or_sync(0xffffffffu, err);
+  if ((threadIdx.x & 31) == 0) {
+    if (c) atomicAdd(&sh.cnt[place], c);
+    if (e) atomicOr(&sh.err[place], e);
+  }
+  PgTeam<C>::sync();
+  if (C == 1) return PgAll{sh.cnt[place], sh.err[place], 0};
   cg::cluster_group cl = cg::this_cluster();
-  cl.sync();
   PgAll r{0, 0, 0};
   const int me = cl.block_rank();
+  int cs[C];
 #pragma unroll
   for (int k = 0; k < C; ++k) {
     const PgShared* o = cl.map_shared_rank(&sh, k);
-    const int c = o->cnt;
-    r.cnt += c;
-    r.err |= o->err;
-    if (k < me) r.before += c;
+    cs[k] = o->cnt[place];
+    r.err |= o->err[place];
   }
-  cl.sync();  // the values may be replaced, or the CTA may leave
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    r.cnt += cs[k];
+    if (k < me) r.before += cs[k];
+  }
   return r;
 }
 
@@ -200,6 +205,7 @@ struct ReserveArgs {
 template <int C>
 __device__ __forceinline__ void reserve_body(const ReserveArgs& a, PgShared& sh) {
   const int tid = threadIdx.x, rank = PgTeam<C>::rank();
+  PgTeam<C>::enter(sh);
   pdl_trigger();
   pdl_wait();
   const int top = *a.ftop;
@@ -238,7 +244,7 @@ __device__ __forceinline__ void reserve_body(const ReserveArgs& a, PgShared& sh)
       if (x[k] < -1 || x[k] >= a.NB) err |= SPEC_DERR_BAD_BLOCK;
     }
   }
-  PgAll all = pg_exchange<C>(sh, cnt, err);
+  PgAll all = pg_exchange<C>(sh, 0, cnt, err);
   const int need = all.cnt, base = all.before;
   err = all.err;
   if (err == 0 && (top < 0 || top > a.NB || need > top)) err = SPEC_DERR_NO_SPACE;
@@ -248,8 +254,9 @@ __device__ __forceinline__ void reserve_body(const ReserveArgs& a, PgShared& sh)
       const int y = a.fs[top - 1 - i];
       if (y < 0 || y >= a.NB) pe = SPEC_DERR_BAD_BLOCK;
     }
-    err = pg_exchange<C>(sh, 0, pe).err;
+    err = pg_exchange<C>(sh, 1, 0, pe).err;
   }
+  PgTeam<C>::leave();
   if (err != 0) {
     if (rank == 0 && tid == 0) *a.status = err;
     return;
@@ -317,6 +324,7 @@ struct ForkArgs {
 template <int C>
 __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) {
   const int tid = threadIdx.x, rank = PgTeam<C>::rank();
+  PgTeam<C>::enter(sh);
   pdl_wait();
   // From here on the copies may start: they read the parents' tables and blocks,
   // which this kernel does not change, and wait for it before they write.
@@ -358,7 +366,7 @@ __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) 
     }
   };
   for (int r = 0; r < part.rounds; ++r) load(r);
-  err = pg_exchange<C>(sh, 0, err | bad).err;
+  err = pg_exchange<C>(sh, 0, 0, err | bad).err;
   // tails are ranked in the order of the pairs (the prefix gave a thread the same ones)
   const int per = (a.n + kPgThreads - 1) / kPgThreads, i0 = tid * per;
   int tails;
@@ -380,10 +388,11 @@ __device__ __forceinline__ void fork_plan_body(const ForkArgs& a, PgShared& sh) 
       for (int i = i0; i < i0 + per && i < a.n; ++i)
         if (__ldcg(&a.sl[a.src[i]]) < 0) pe |= SPEC_DERR_BAD_SLOT;
     }
-    err = pg_exchange<C>(sh, 0, pe).err;
+    err = pg_exchange<C>(sh, 1, 0, pe).err;
     if (err != 0 && rank == 0)
       for (int i = i0; i < i0 + per && i < a.n; ++i) a.sl[a.dst[i]] = 0;
   }
+  PgTeam<C>::leave();
   if (err != 0) {
     if (rank == 0 && tid == 0) *a.status = err;
     return;
@@ -511,32 +520,36 @@ struct FreeArgs {
   int32_t* status;
 };
 
-// Phases over the flat list of the listed rows' entries (E = n * MB of them):
+// Phases over the flat list of the listed rows' entries (E = n * MB of them, at
+// most 2^30):
 //   1 one holder less for every entry: a block without any reads -1, one that
 //     is listed more often than it is held reads less (an error);
-//   2 a block at -1 takes the lowest flat index that lists it, as index - E - 1
-//     (below -1, so never mistaken for a count);
+//   2 a block at -1 takes the lowest flat index e that lists it, as INT_MIN + e,
+//     far below any count;
 //   3 the entry whose index its block holds pushes it, ranked by a scan;
 //   4 that entry sets the count to 0; all entries are cleared.
 template <int C>
 __device__ __forceinline__ void free_body(const FreeArgs& a, PgShared& sh) {
   const int tid = threadIdx.x, rank = PgTeam<C>::rank(), step = C * kPgThreads;
+  constexpr int kTaken = -(1 << 30);  // counts lie above, taken blocks below or at it
+  PgTeam<C>::enter(sh);
   pdl_trigger();
   pdl_wait();
   const int top = *a.ftop;
   const int E = a.n * a.MB;
   const PgPart<C> part(E);
   int err = 0;
-  for (int i = rank * kPgThreads + tid; i < a.n; i += step) {
-    const int r = a.rows[i];
-    if (r < 0 || r >= a.B) err |= SPEC_DERR_BAD_SLOT;
-    else if (a.sl[r] < 0) err |= SPEC_DERR_BAD_LENGTH;
-  }
-  err = pg_exchange<C>(sh, 0, err).err;
-  if (err != 0) {
-    if (rank == 0 && tid == 0) *a.status = err;
-    return;
-  }
+  // calls f(row, k) for this thread's rows that are in range, the k-th of them
+  auto each_row = [&](auto f) {
+    for (int i = rank * kPgThreads + tid, k = 0; i < a.n; i += step, ++k) {
+      const int r = a.rows[i];
+      if (r >= 0 && r < a.B) f(r, k);
+      else err |= SPEC_DERR_BAD_SLOT;
+    }
+  };
+  each_row([&](int r, int) {
+    if (a.sl[r] < 0) err |= SPEC_DERR_BAD_LENGTH;
+  });
   int32_t* slot[kPgHeld];
   int x[kPgHeld];  // block ids, -1: none
   auto load = [&](int round) {
@@ -551,8 +564,11 @@ __device__ __forceinline__ void free_body(const FreeArgs& a, PgShared& sh) {
           j = 0;
           ++i;
         }
-        slot[k] = a.bt + int64_t(a.rows[i]) * a.MB + j;
-        x[k] = *slot[k];
+        const int r = a.rows[i];
+        if (r >= 0 && r < a.B) {
+          slot[k] = a.bt + int64_t(r) * a.MB + j;
+          x[k] = *slot[k];
+        }
       }
     }
   };
@@ -565,80 +581,74 @@ __device__ __forceinline__ void free_body(const FreeArgs& a, PgShared& sh) {
         if (x[k] >= 0) f(part.at(r, k), k);
     }
   };
-  // rows must be distinct: each is claimed by complementing its length
-  for (int i = rank * kPgThreads + tid; i < a.n; i += step) {
-    int32_t* p = &a.sl[a.rows[i]];
-    const int L = *reinterpret_cast<volatile int32_t*>(p);
-    if (L < 0 || atomicCAS(p, L, ~L) != L) err |= SPEC_DERR_BAD_SLOT;
-  }
+  int bad = 0;
   for (int r = 0; r < part.rounds; ++r) {
     load(r);
 #pragma unroll
     for (int k = 0; k < kPgHeld; ++k)
-      if (x[k] < -1 || x[k] >= a.NB) err |= SPEC_DERR_BAD_BLOCK;
+      if (x[k] < -1 || x[k] >= a.NB) bad |= SPEC_DERR_BAD_BLOCK;
   }
-  if (top < 0 || top > a.NB) err |= SPEC_DERR_BAD_BLOCK;
+  if (top < 0 || top > a.NB) bad |= SPEC_DERR_BAD_BLOCK;
+  PgTeam<C>::sync();  // every length has been read
+  // rows must be distinct: each is claimed by complementing its length
+  uint32_t claimed = 0;
+  each_row([&](int r, int k) {
+    const int L = __ldcg(&a.sl[r]);
+    if (L < 0 || atomicCAS(&a.sl[r], L, ~L) != L) bad |= SPEC_DERR_BAD_SLOT;
+    else claimed |= 1u << k;
+  });
   auto unclaim = [&]() {  // only reached with every CTA past its claims
-    for (int i = rank * kPgThreads + tid; i < a.n; i += step) {
-      int32_t* p = &a.sl[a.rows[i]];
-      const int L = __ldcg(p);
-      if (L < 0) atomicCAS(p, L, ~L);  // a row listed twice is undone once
-    }
+    each_row([&](int r, int k) {
+      if (claimed >> k & 1u) a.sl[r] = ~__ldcg(&a.sl[r]);
+    });
   };
-  err = pg_exchange<C>(sh, 0, err).err;
+  // rows out of range and lengths come before the rest
+  err = pg_exchange<C>(sh, 0, 0, err << 16 | bad).err;
   if (err != 0) {
+    PgTeam<C>::leave();
     unclaim();
-    if (rank == 0 && tid == 0) *a.status = err;
+    if (rank == 0 && tid == 0) *a.status = err >> 16 ? err >> 16 : err;
     return;
   }
   each([&](int, int k) { atomicSub(&a.refs[x[k]], 1); });
   PgTeam<C>::sync();
-  each([&](int, int k) {
-    if (__ldcg(&a.refs[x[k]]) < -1) err |= SPEC_DERR_BAD_BLOCK;
-  });
-  auto give_back = [&]() {
-    each([&](int, int k) { atomicAdd(&a.refs[x[k]], 1); });
-    unclaim();
-    if (rank == 0 && tid == 0) *a.status = err;
-  };
-  err = pg_exchange<C>(sh, 0, err).err;
-  if (err != 0) {
-    give_back();
-    return;
-  }
   each([&](int e, int k) {
-    if (__ldcg(&a.refs[x[k]]) <= -1) atomicMin(&a.refs[x[k]], e - E - 1);
+    const int r = __ldcg(&a.refs[x[k]]);
+    if (r < -1 && r > kTaken) err |= SPEC_DERR_BAD_BLOCK;
+    else if (r <= -1) atomicMin(&a.refs[x[k]], INT_MIN + e);
   });
   PgTeam<C>::sync();
   int cnt = 0;
   uint32_t push = 0;  // this thread's entries that push, of the last round
-  int round = 0;
-  for (; round < part.rounds; ++round) {
-    if (part.rounds > 1) load(round);
+  auto find_pushes = [&](int r) {
     push = 0;
 #pragma unroll
     for (int k = 0; k < kPgHeld; ++k)
-      if (x[k] >= 0 && __ldcg(&a.refs[x[k]]) == part.at(round, k) - E - 1) push |= 1u << k;
+      if (x[k] >= 0 && __ldcg(&a.refs[x[k]]) == INT_MIN + part.at(r, k)) push |= 1u << k;
+  };
+  for (int r = 0; r < part.rounds; ++r) {
+    if (part.rounds > 1) load(r);
+    find_pushes(r);
     cnt += __popc(push);
   }
-  PgAll all = pg_exchange<C>(sh, cnt, 0);
-  if (all.cnt > a.NB - top) {  // some id would be held twice
+  PgAll all = pg_exchange<C>(sh, 1, cnt, err);
+  err = all.err;
+  if (all.cnt > a.NB - top) err |= SPEC_DERR_BAD_BLOCK;  // some id would be held twice
+  if (err != 0) {
     each([&](int, int k) {
-      if (__ldcg(&a.refs[x[k]]) < -1) a.refs[x[k]] = -1;
+      if (__ldcg(&a.refs[x[k]]) <= kTaken) a.refs[x[k]] = -1;
     });
     PgTeam<C>::sync();
-    err = SPEC_DERR_BAD_BLOCK;
-    give_back();
+    each([&](int, int k) { atomicAdd(&a.refs[x[k]], 1); });
+    unclaim();
+    if (rank == 0 && tid == 0) *a.status = err;
     return;
   }
   int carry = top + all.before;
   for (int r = 0; r < part.rounds; ++r) {
     if (part.rounds > 1) {
       load(r);
-      push = 0;
-#pragma unroll
-      for (int k = 0; k < kPgHeld; ++k)
-        if (x[k] >= 0 && __ldcg(&a.refs[x[k]]) == part.at(r, k) - E - 1) push |= 1u << k;
+      find_pushes(r);
     }
     int sum;
     int at = carry + pg_scan(__popc(push), sh.warp, sum);
@@ -649,18 +659,17 @@ __device__ __forceinline__ void free_body(const FreeArgs& a, PgShared& sh) {
   }
   PgTeam<C>::sync();  // every entry has been compared before a count changes
   for (int r = 0; r < part.rounds; ++r) {
-    if (part.rounds > 1) load(r);
+    if (part.rounds > 1) {
+      load(r);
+      find_pushes(r);  // a block is its pusher's until that entry comes
+    }
 #pragma unroll
     for (int k = 0; k < kPgHeld; ++k) {
-      // with one round the comparison above still holds
-      const bool mine = part.rounds == 1
-                            ? (push >> k & 1u)
-                            : x[k] >= 0 && __ldcg(&a.refs[x[k]]) == part.at(r, k) - E - 1;
-      if (mine) a.refs[x[k]] = 0;
+      if (push >> k & 1u) a.refs[x[k]] = 0;
       if (slot[k]) *slot[k] = -1;
     }
   }
-  for (int i = rank * kPgThreads + tid; i < a.n; i += step) a.sl[a.rows[i]] = 0;
+  each_row([&](int r, int) { a.sl[r] = 0; });
   if (rank == 0 && tid == 0) {
     *a.ftop = top + all.cnt;
     *a.status = 0;
