@@ -238,20 +238,24 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
   const int lane = threadIdx.x & 31, d16 = lane % kPerRow;
   const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
   const int64_t base = int64_t(g.b) * a.T * a.H * a.G + g.h * a.G;
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) + 2 * d16;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) +
+                   base * (D / 8) + 2 * d16;
+  // row / G: the quotient is at most 32, and half a row keeps it 1 / (2 G) off the integers
+  const float inv_g = 1.0f / float(a.G);
+  const int row0 = g.rb * a.rows_per_block, skip = a.H * a.G - a.G;
   uint4 next[2];
-  int64_t next_off;
-  int next_t;
+  int next_off, next_t;  // rows from `base`, -1: none
   auto fetch = [&](int r) {
     next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
     next_off = -1;
     next_t = a.T;
     if (r < rows) {
-      const int row = g.rb * a.rows_per_block + r;
-      next_t = row / a.G;
-      next_off = base + int64_t(next_t) * a.H * a.G + (row - next_t * a.G);
-      next[0] = q[next_off * (D / 8)];
-      next[1] = q[next_off * (D / 8) + 1];
+      const int row = row0 + r;
+      next_t = int((float(row) + 0.5f) * inv_g);
+      next_off = row + next_t * skip;  // t H G + (row - t G)
+      const uint4* x = q + int64_t(next_off) * (D / 8);
+      next[0] = x[0];
+      next[1] = x[1];
     }
   };
   int r = w * kRows + lane / kPerRow;
@@ -259,7 +263,7 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
 #pragma unroll 1
   for (int i = w * kRows; i < NR; i += n * kRows) {
     const int row = r, t = next_t;
-    const int64_t off = next_off;
+    const int off = next_off;
     const uint32_t u[8] = {next[0].x, next[0].y, next[0].z, next[0].w,
                            next[1].x, next[1].y, next[1].z, next[1].w};
     r += n * kRows;
@@ -273,18 +277,25 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
     // |f| 2^-e in [128, 256) at the largest; e stays in range for bf16 subnormals
     const int e = max(int(top >> 23) - 127 - 7, -110);
     const float down = q8_pow2(-e);
+    const float2 down2 = make_float2(down, down);
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
-      float f[4], lo[4];
+      uint32_t h[2], o[2];  // a bf16 number of this range is one of fp16 as well
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
-        f[2 * z] = __uint_as_float(u[2 * y + z] << 16) * down;
-        f[2 * z + 1] = __uint_as_float(u[2 * y + z] & 0xffff0000u) * down;
+        const float2 f = __fmul2_rn(make_float2(__uint_as_float(u[2 * y + z] << 16),
+                                                __uint_as_float(u[2 * y + z] & 0xffff0000u)),
+                                    down2);
+        uint32_t v, w;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(f.y), "f"(f.x));
+        h[z] = f16x2_to_e4m3(v);
+        w = e4m3x2_to_f16(h[z]);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(w) : "r"(v), "r"(w));
+        o[z] = f16x2_to_e4m3(w);
       }
-      hw[y] = f32x4_to_e4m3(f[0], f[1], f[2], f[3]);
-      e4m3x4_to_f32(hw[y], lo);
-      lw[y] = f32x4_to_e4m3(f[0] - lo[0], f[1] - lo[1], f[2] - lo[2], f[3] - lo[3]);
+      hw[y] = h[0] | h[1] << 16;
+      lw[y] = o[0] | o[1] << 16;
     }
     auto put = [&](int rr, const uint32_t* v) {
       const int chunk = d16 ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
@@ -298,7 +309,7 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
         sh.row_c[qb][row] =
             top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
         sh.row_t[qb][row] = t;
-        sh.row_off[qb][row] = off;
+        sh.row_off[qb][row] = off < 0 ? -1 : base + off;
         sh.row_mask[qb][row] = a.tree && off >= 0 ? a.tree[int64_t(g.b) * a.T + t] : 0u;
       }
     }
@@ -521,7 +532,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       bool first = scores();
       for (int j = 0; j < tiles; ++j) {
         bool next = false;
-        if (j + 1 < tiles) next = scores();  // the order of the copies
+        // The order of the copies, always: the ring's waits are by parity, and a slot
+        // freed out of turn would let a copy warp pass one that is two rounds behind.
+        if (j + 1 < tiles) next = scores();
         outputs(first);
         first = next;
       }

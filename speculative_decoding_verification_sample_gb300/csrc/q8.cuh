@@ -43,4 +43,21 @@ __device__ __forceinline__ uint32_t f32x4_to_e4m3(float a, float b, float c, flo
   return r;
 }
 
+// Two fp16 numbers to two codes and back (in the lower 16 bits), to nearest even,
+// saturating.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3(uint32_t v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n\tcvt.u32.u16 %0, c;\n\t}"
+      : "=r"(r)
+      : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t c) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}"
+      : "=r"(r)
+      : "r"(c));
+  return r;
+}
+
 }  // namespace sv
