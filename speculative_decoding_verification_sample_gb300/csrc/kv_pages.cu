@@ -25,9 +25,9 @@
 // All-or-nothing: nothing is written before every check has passed; what the
 // checks themselves write (claims in seq_lens, counts in extra_refs) is undone.
 //
-// Measured, device time of a call: reserve 6.5 us for one block a row of 256 rows (10.1 us
-// for 9 thousand blocks), fork 10.3 us for 4 rows and 31 us for 128 rows of 512-4096
-// tokens (32 layers x 8 heads x 128), free 9.1 us for 5 rows and 26 us for 200 rows.
+// Measured, device time of a call: reserve 6.8 us for one block a row of 256 rows (9.6 us
+// for 9 thousand blocks), fork 9.9 us for 4 rows and 30 us for 128 rows of 512-4096
+// tokens (32 layers x 8 heads x 128), free 7.7 us for 5 rows and 22 us for 200 rows.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -432,7 +432,8 @@ __global__ void __cluster_dims__(kPgCluster, 1, 1) __launch_bounds__(kPgThreads)
 // The tail blocks' tokens and scales: CTA (chunk, pair) copies `chunk`
 // planes: 8 when there are few pairs, more when that would be many waves of CTAs with
 // the latency of their table reads each. 128 pairs of 512 planes of 16 x 128 bytes, 126 MB
-// read and written: 8 planes a CTA with a division a word 24 us, as here about 18 us.
+// read and written: 8 planes a CTA with a division a word 24 us, as here 20.7 us alone
+// (6.1 TB/s).
 // Bound by memory: it reads and writes L % bs tokens of every plane. Its
 // first loads do not wait for the plan, which changes neither the parents' rows nor
 // any block; they test what the plan has not yet vouched for.

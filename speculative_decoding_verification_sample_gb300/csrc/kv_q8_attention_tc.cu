@@ -30,13 +30,15 @@
 // CTAs per SM hide each other's latencies.
 //
 // Bound by memory up to 24 query rows of a kv head: 256 rows of 512-4096 tokens, 8 kv
-// heads x 128, 20 query rows, 1.23 GB: 205 us = 6.0 TB/s (0.89 of the copy peak); 8 rows
-// 195 us; 2 rows of 100-131 thousand tokens 85 us (5.6 TB/s). Beyond that by the
-// softmax warps' instructions (about 11 for each 32 scores): 32 rows 222 us, 48 rows
-// 307 us; a window of 4096 over 56 rows 139 us (3.0 TB/s). The steps that mattered:
+// heads x 128, 20 query rows, 1.23 GB: 206 us = 6.0 TB/s (0.89 of the copy peak); 8 rows
+// 195 us; 2 rows of 100-131 thousand tokens 86 us (5.5 TB/s). Beyond that by the
+// softmax warps' instructions (about 11 for each 32 scores): 32 rows 218 us, 48 rows
+// 293 us; a window of 4096 over 56 rows 135 us (3.1 TB/s). Short rows (100-600 tokens)
+// by the changes of items: 89 us, of which the queries' conversion in fp32 and with
+// divisions cost 5. The steps that mattered:
 // the hot loop must stay small (waits out of line, one copy of each block of code:
 // 334 to 242 us for the 20-row case), the copies of 16-token blocks need two warps,
-// an item's queries must be in L2 and converted before it begins (230 to 205 us), and
+// an item's queries must be in L2 and converted before it begins (230 to 206 us), and
 // nothing may go through local memory, which this much shared memory pushes out to L2.
 // Not kept, for the 20-row case: two groups taking the tiles in turn (374 us), three
 // CTAs per SM with short rings (351 us), tiles called into L2 ahead of the copies
