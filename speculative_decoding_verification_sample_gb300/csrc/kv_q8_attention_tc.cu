@@ -62,6 +62,7 @@
 namespace sv {
 
 constexpr int kTcScaleRing = 8;             // tiles whose scales are held
+constexpr int kTcItems = 3;                 // items whose rows are described at a time
 constexpr int kTcMaxPages = 16;             // blocks of one tile
 constexpr float kTcUnset = 1e30f;           // minus the reference of a row that has seen no key
 constexpr float kTcSlack = 8.0f;            // binades by which keys may exceed the reference
@@ -70,20 +71,20 @@ constexpr int kTcSmem = 113 * 1024 - 512;   // of one CTA, two per SM
 
 template <int NR>
 struct TcShared {
-  alignas(16) float row_c[2][NR];  // query row's scale * softmax_scale * log2(e)
+  alignas(16) float row_c[kTcItems][NR];  // query row's scale * softmax_scale * log2(e)
   alignas(16) float row_nm[NR];     // minus the reference of the exponentials
   alignas(16) float row_a[NR];      // rescale factor, then that of the output
   alignas(16) float part[4][NR];    // the warps' maxima, then sums
   alignas(16) float zero[NR];
   uint64_t row_to[NR];              // where the row's outputs go
-  Segment seg[2];                   // the items that the queries belong to
-  int64_t row_off[2][NR];          // row of q and out, -1: none
-  int row_t[2][NR];                // query (T for rows that do not exist)
-  uint32_t row_mask[2][NR];
+  Segment seg[kTcItems];            // the items that the queries belong to
+  int row_off[kTcItems][NR];        // row of q and out from the item's first, -1: none
+  int row_t[kTcItems][NR];          // query (T for rows that do not exist)
+  uint32_t row_mask[kTcItems][NR];
   alignas(16) float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
   int2 tile[kTcScaleRing];  // first position; whether every query sees every key
   uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full,
-      pv_done, q_full[2], q_empty[2];
+      pv_done, q_full[kTcItems], q_empty[2], item_empty[kTcItems];
   int64_t warp_sum[16];
   uint32_t tmem;
   int abort;
@@ -231,6 +232,11 @@ __device__ __noinline__ void clear_row(uint8_t* tile, int key) {
     v[(x + key) % (D / 16)] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// The row of q and out where an item's kv head begins.
+__device__ __forceinline__ int64_t first_row(const AttnArgs& a, const Segment& g) {
+  return int64_t(g.b) * a.T * a.H * a.G + g.h * a.G;
+}
+
 // An item's queries as two e4m3 terms a number, by warp w of n: kPerRow lanes a row,
 // 16 numbers each; and what the softmax needs to know of the rows.
 template <int NR, int D>
@@ -239,7 +245,7 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
   constexpr int kPerRow = D / 16, kRows = 32 / kPerRow;
   const int lane = threadIdx.x & 31, d16 = lane % kPerRow;
   const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
-  const int64_t base = int64_t(g.b) * a.T * a.H * a.G + g.h * a.G;
+  const int64_t base = first_row(a, g);
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) +
                    base * (D / 8) + 2 * d16;
   // row / G: the quotient is at most 32, and half a row keeps it 1 / (2 G) off the integers
@@ -311,7 +317,7 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
         sh.row_c[qb][row] =
             top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
         sh.row_t[qb][row] = t;
-        sh.row_off[qb][row] = off < 0 ? -1 : base + off;
+        sh.row_off[qb][row] = off;
         sh.row_mask[qb][row] = a.tree && off >= 0 ? a.tree[int64_t(g.b) * a.T + t] : 0u;
       }
     }
@@ -343,8 +349,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], S::kSoftmax);
+      mbar_init(&sh.q_empty[i], 1);
+    }
+    for (int i = 0; i < kTcItems; ++i) {
       mbar_init(&sh.q_full[i], 32);
-      mbar_init(&sh.q_empty[i], 1 + S::kSoftmax);
+      mbar_init(&sh.item_empty[i], S::kSoftmax);
     }
     mbar_init(&sh.p_full, S::kSoftmax);
     mbar_init(&sh.pv_done, 1);
@@ -375,10 +384,12 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     // ---------------------------------------------------------------- queries
     // The first item's are taken by the softmax warps too; the next ones' by a warp of
     // their own, while the item before is worked on. One place in the code for both.
+    // The queries' buffer is free again with the item's last scores; what describes its
+    // rows is used to the item's end, and has one place more.
     TcRing<2> qbuf;
+    TcRing<kTcItems> item;
     int w = warp < kTmaWarp ? warp : warp - 3, n = S::kSoftmax / 32 + 1;
     for (bool first = true;; first = false) {
-      const int qb = qbuf.at;
       if (!first) {
         // called into L2 while the buffer is still in use: DRAM's latency under this load
         // is several times a row's conversion
@@ -390,18 +401,20 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
               (int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G);
           prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + off * D + x % kLines * 64);
         }
-        tc_wait(&sh.q_empty[qb], qbuf.phase ^ 1, &sh.abort, a.err);
+        tc_wait(&sh.q_empty[qbuf.at], qbuf.phase ^ 1, &sh.abort, a.err);
+        tc_wait(&sh.item_empty[item.at], item.phase ^ 1, &sh.abort, a.err);
       }
-      prepare_rows<NR, D>(a, sh, g, q_s + qb * S::kQ, qb, w, n);
+      prepare_rows<NR, D>(a, sh, g, q_s + qbuf.at * S::kQ, item.at, w, n);
       fence_async_smem();
       if (first) asm volatile("bar.sync 3, %0;" ::"n"(S::kSoftmax + 32) : "memory");
       if (warp < kTmaWarp) break;
       w = 0;
       n = 1;
-      if (lane == 0) sh.seg[qb] = g;
-      mbar_arrive(&sh.q_full[qb]);
+      if (lane == 0) sh.seg[item.at] = g;
+      mbar_arrive(&sh.q_full[item.at]);
       if (first && lane == 0) write_join(a, plan, &g, c);
       qbuf.next();
+      item.next();
       if (last_of_cta(g)) break;
       next_segment(a, g, plan.u1);
     }
@@ -484,10 +497,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       TcRing<NS> ring;
       TcRing<SB> sbuf;
       TcRing<2> qbuf;
+      TcRing<kTcItems> item;
       uint32_t p_phase = 0;
       auto scores = [&]() {  // returns whether the tile is its item's first
         const bool first = k == g.t0;
-        if (first) tc_wait(&sh.q_full[qbuf.at], qbuf.phase, &sh.abort, a.err);
+        if (first) tc_wait(&sh.q_full[item.at], item.phase, &sh.abort, a.err);
         tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
         tc_wait(&sh.s_empty[sbuf.at], sbuf.phase ^ 1, &sh.abort, a.err);
         tc_fence_after();
@@ -509,6 +523,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           if (!last_of_cta(g)) next_segment(a, g, plan.u1);
           k = g.t0;
           qbuf.next();
+          item.next();
         }
         return first;
       };
@@ -551,14 +566,14 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     const uint32_t lane_addr = tmem + (uint32_t(gw * 32) << 16) + col0;
     const uint32_t o_addr = lane_addr + SB * NO;
     const int page = key >> (a.bs >= kAttnTile ? 7 : 31 - __clz(a.bs));
-    TcRing<2> qbuf;
+    TcRing<kTcItems> item;
     int j = 0;  // tile of the CTA
     auto wait_outputs = [&]() {  // of the tile before
       tc_wait(&sh.pv_done, (j & 1) ^ 1, &sh.abort, a.err);
     };
-    for (;; qbuf.next()) {
-      const int qb = qbuf.at;
-      tc_wait(&sh.q_full[qb], qbuf.phase, &sh.abort, a.err);
+    for (;; item.next()) {
+      const int qb = item.at;
+      tc_wait(&sh.q_full[qb], item.phase, &sh.abort, a.err);
       const Segment& g = sh.seg[qb];  // read where it is needed: registers are scarce here
       const int j_first = j, j_end = j + (g.t1 - g.t0);
       if (key < W) nm[key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
@@ -798,9 +813,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         const float unlift = q8_pow2(vref) / kTcLift;
         const float down = q8_pow2(-e);
         ra[key] = (!whole ? down : sum == 0.0f ? 0.0f : __fdividef(down, sum * down)) * unlift;
-        const int64_t off = sh.row_off[qb][col0 + key], part = slot * a.rows_per_block + col0 + key;
+        const int off = sh.row_off[qb][col0 + key];
+        const int64_t part = slot * a.rows_per_block + col0 + key;
         sh.row_to[col0 + key] =
-            whole ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + off * D)
+            whole ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + (first_row(a, g) + off) * D)
                   : reinterpret_cast<uint64_t>(a.parts + part * D);
         if (!whole && off >= 0)
           a.stats[part] = make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e),
@@ -833,7 +849,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           }
       }
       tc_fence_before();  // the next item's products overwrite O after its p_full
-      mbar_arrive(&sh.q_empty[qb]);
+      mbar_arrive(&sh.item_empty[qb]);
       if (last) break;
       bar_group(group);  // row_a, row_nm, part: every thread is done with the item
     }
