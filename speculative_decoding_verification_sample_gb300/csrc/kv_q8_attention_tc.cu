@@ -32,10 +32,10 @@
 // Bound by memory up to 24 query rows of a kv head: 256 rows of 512-4096 tokens, 8 kv
 // heads x 128, 20 query rows, 1.23 GB: 206 us = 6.0 TB/s (0.89 of the copy peak); 8 rows
 // 195 us; 2 rows of 100-131 thousand tokens 86 us (5.5 TB/s). Beyond that by the
-// softmax warps' instructions (about 11 for each 32 scores): 32 rows 218 us, 48 rows
-// 293 us; a window of 4096 over 56 rows 135 us (3.1 TB/s). Short rows (100-600 tokens)
-// by the changes of items: 89 us, of which the queries' conversion in fp32 and with
-// divisions cost 5. The steps that mattered:
+// softmax warps' instructions (about 11 for each 32 scores): 32 rows 217 us, 48 rows
+// 293 us; a window of 4096 over 56 rows 134 us (3.1 TB/s). Short rows (100-600 tokens)
+// by the changes of items: 80 us, 48 query rows 126 us (94 and 166 before the queries were
+// prepared two items ahead and in fewer steps). The steps that mattered:
 // the hot loop must stay small (waits out of line, one copy of each block of code:
 // 334 to 242 us for the 20-row case), the copies of 16-token blocks need two warps,
 // an item's queries must be in L2 and converted before it begins (230 to 206 us), and
@@ -238,47 +238,63 @@ __device__ __forceinline__ int64_t first_row(const AttnArgs& a, const Segment& g
 }
 
 // An item's queries as two e4m3 terms a number, by warp w of n: kPerRow lanes a row,
-// 16 numbers each; and what the softmax needs to know of the rows.
+// N numbers each; and what the softmax needs to know of the rows. The two terms take as
+// many bytes as the bf16 numbers, which are copied to where their terms will be, all of
+// them in flight at once, and converted in place. This warp is what items of a few tiles
+// wait for: with loads one step ahead, 16 numbers a lane and the rows' description in the
+// same loop (1100 cycles a step) 256 rows of 100-600 tokens took 143 us with 48 query
+// rows, so 126 us. 16 numbers a lane there: 130 us; 32 with 20 query rows: 82 instead of
+// 80 us.
 template <int NR, int D>
 __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh, const Segment& g,
                                              uint8_t* qs, int qb, int w, int n) {
-  constexpr int kPerRow = D / 16, kRows = 32 / kPerRow;
-  const int lane = threadIdx.x & 31, d16 = lane % kPerRow;
+  constexpr int N = NR > 24 ? 32 : 16, kPerRow = D / N, kRows = 32 / kPerRow;
+  const int lane = threadIdx.x & 31, part = lane % kPerRow;
   const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
-  const int64_t base = first_row(a, g);
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q)) +
-                   base * (D / 8) + 2 * d16;
+                   first_row(a, g) * (D / 8) + N / 8 * part;
   // row / G: the quotient is at most 32, and half a row keeps it 1 / (2 G) off the integers
   const float inv_g = 1.0f / float(a.G);
   const int row0 = g.rb * a.rows_per_block, skip = a.H * a.G - a.G;
-  uint4 next[2];
-  int next_off, next_t;  // rows from `base`, -1: none
-  auto fetch = [&](int r) {
-    next[0] = next[1] = make_uint4(0u, 0u, 0u, 0u);
-    next_off = -1;
-    next_t = a.T;
-    if (r < rows) {
-      const int row = row0 + r;
-      next_t = int((float(row) + 0.5f) * inv_g);
-      next_off = row + next_t * skip;  // t H G + (row - t G)
-      const uint4* x = q + int64_t(next_off) * (D / 8);
-      next[0] = x[0];
-      next[1] = x[1];
-    }
+  auto query = [&](int r) { return int((float(row0 + r) + 0.5f) * inv_g); };
+  // this lane's 16 bytes of a row: of its upper terms, and NR * D bytes on of its lower
+  // ones (the swizzle is the same, as the rows differ by a multiple of 8)
+  auto place = [&](int r, int y) {
+    return qs + r * D + ((N / 16 * part + y) ^ (D == 128 ? r & 7 : (r >> 1) & 3)) * 16;
   };
-  int r = w * kRows + lane / kPerRow;
-  fetch(r);
+  const int r0 = w * kRows + lane / kPerRow;
 #pragma unroll 1
-  for (int i = w * kRows; i < NR; i += n * kRows) {
-    const int row = r, t = next_t;
-    const int off = next_off;
-    const uint32_t u[8] = {next[0].x, next[0].y, next[0].z, next[0].w,
-                           next[1].x, next[1].y, next[1].z, next[1].w};
-    r += n * kRows;
-    fetch(r);  // in flight while this row is converted
+  for (int r = r0; r < NR; r += n * kRows) {
+    const bool ok = r < rows;  // else zeros
+    const uint4* x = q + (ok ? int64_t(row0 + r + query(r) * skip) * (D / 8) : 0);
+#pragma unroll
+    for (int y = 0; y < N / 8; ++y)
+      cp_async16(place(r, y >> 1) + (y & 1) * NR * D, x + y, ok);
+  }
+#pragma unroll 1
+  for (int x = w * 32 + lane; x < NR; x += n * 32) {  // a lane a row
+    const bool live = x < rows;
+    const int t = query(x);
+    sh.row_t[qb][x] = live ? t : a.T;
+    sh.row_off[qb][x] = live ? row0 + x + t * skip : -1;  // t H G + (row - t G)
+    sh.row_mask[qb][x] = a.tree && live ? a.tree[int64_t(g.b) * a.T + t] : 0u;
+  }
+  cp_async_wait_all();
+#pragma unroll 1
+  for (int row = r0; row - lane / kPerRow < NR; row += n * kRows) {
+    uint32_t u[N / 2];
+#pragma unroll
+    for (int y = 0; y < N / 8; ++y) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row < NR) v = *reinterpret_cast<const uint4*>(place(row, y >> 1) + (y & 1) * NR * D);
+      u[4 * y] = v.x;
+      u[4 * y + 1] = v.y;
+      u[4 * y + 2] = v.z;
+      u[4 * y + 3] = v.w;
+    }
     uint32_t two = 0;
 #pragma unroll
-    for (int y = 0; y < 8; ++y) two = __vmaxu2(two, u[y] & 0x7fff7fffu);
+    for (int y = 0; y < N / 2; ++y) two = __vmaxu2(two, u[y] & 0x7fff7fffu);
     uint32_t top = max(two << 16, two & 0xffff0000u);
 #pragma unroll
     for (int s = kPerRow / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
@@ -286,9 +302,9 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
     const int e = max(int(top >> 23) - 127 - 7, -110);
     const float down = q8_pow2(-e);
     const float2 down2 = make_float2(down, down);
-    uint32_t hw[4], lw[4];
+    uint32_t hw[N / 4], lw[N / 4];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
+    for (int y = 0; y < N / 4; ++y) {
       uint32_t h[2], o[2];  // a bf16 number of this range is one of fp16 as well
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
@@ -305,21 +321,18 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
       hw[y] = h[0] | h[1] << 16;
       lw[y] = o[0] | o[1] << 16;
     }
-    auto put = [&](int rr, const uint32_t* v) {
-      const int chunk = d16 ^ (D == 128 ? rr & 7 : (rr >> 1) & 3);
-      *reinterpret_cast<uint4*>(qs + rr * D + chunk * 16) = make_uint4(v[0], v[1], v[2], v[3]);
-    };
     if (row < NR) {
-      put(row, hw);
-      put(NR + row, lw);
-      if (d16 == 0) {
-        // a row with an infinity or a NaN: its scores are NaN
+#pragma unroll
+      for (int y = 0; y < N / 16; ++y) {
+        uint8_t* to = place(row, y);
+        const uint32_t *h = hw + 4 * y, *l = lw + 4 * y;
+        *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(to + NR * D) = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+      // a row with an infinity or a NaN: its scores are NaN
+      if (part == 0)
         sh.row_c[qb][row] =
             top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
-        sh.row_t[qb][row] = t;
-        sh.row_off[qb][row] = off;
-        sh.row_mask[qb][row] = a.tree && off >= 0 ? a.tree[int64_t(g.b) * a.T + t] : 0u;
-      }
     }
   }
 }
