@@ -30,16 +30,16 @@
 // CTAs per SM hide each other's latencies.
 //
 // Bound by memory up to 24 query rows of a kv head: 256 rows of 512-4096 tokens, 8 kv
-// heads x 128, 20 query rows, 1.23 GB: 206 us = 6.0 TB/s (0.89 of the copy peak); 8 rows
+// heads x 128, 20 query rows, 1.23 GB: 203 us = 6.1 TB/s (0.90 of the copy peak); 8 rows
 // 195 us; 2 rows of 100-131 thousand tokens 86 us (5.5 TB/s). Beyond that by the
-// softmax warps' instructions (about 11 for each 32 scores): 32 rows 217 us, 48 rows
-// 293 us; a window of 4096 over 56 rows 134 us (3.1 TB/s). Short rows (100-600 tokens)
-// by the changes of items: 80 us, 48 query rows 126 us (94 and 166 before the queries were
+// softmax warps' instructions (about 11 for each 32 scores): 32 rows 215 us, 48 rows
+// 279 us; a window of 4096 over 56 rows 132 us (3.1 TB/s). Short rows (100-600 tokens)
+// by the changes of items: 77 us, 48 query rows 127 us (94 and 166 before the queries were
 // prepared two items ahead and in fewer steps). The steps that mattered:
 // the hot loop must stay small (waits out of line, one copy of each block of code:
 // 334 to 242 us for the 20-row case), the copies of 16-token blocks need two warps,
-// an item's queries must be in L2 and converted before it begins (230 to 206 us), and
-// nothing may go through local memory, which this much shared memory pushes out to L2.
+// an item's queries must be converted before it begins (230 to 206 us), an item's end
+// reads its shared memory before its first store (206 to 203 us), and nothing may go through local memory, which this much shared memory pushes out to L2.
 // Not kept, for the 20-row case: two groups taking the tiles in turn (374 us), three
 // CTAs per SM with short rings (351 us), tiles called into L2 ahead of the copies
 // (281 us), the copies' coordinates made uniform by shuffles (316 us); for many rows,
@@ -76,7 +76,7 @@ struct TcShared {
   alignas(16) float row_a[NR];      // rescale factor, then that of the output
   alignas(16) float part[4][NR];    // the warps' maxima, then sums
   alignas(16) float zero[NR];
-  uint64_t row_to[NR];              // where the row's outputs go
+  alignas(16) uint64_t row_to[NR];  // where the row's outputs go
   Segment seg[kTcItems];            // the items that the queries belong to
   int row_off[kTcItems][NR];        // row of q and out from the item's first, -1: none
   int row_t[kTcItems][NR];          // query (T for rows that do not exist)
@@ -404,16 +404,6 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     int w = warp < kTmaWarp ? warp : warp - 3, n = S::kSoftmax / 32 + 1;
     for (bool first = true;; first = false) {
       if (!first) {
-        // called into L2 while the buffer is still in use: DRAM's latency under this load
-        // is several times a row's conversion
-        const int rows = min(a.rows_per_block, a.R - g.rb * a.rows_per_block);
-        constexpr int kLines = D / 64;  // of 128 bytes
-        for (int x = lane; x < rows * kLines; x += 32) {
-          const int row = g.rb * a.rows_per_block + x / kLines, t = row / a.G;
-          const int64_t off =
-              (int64_t(g.b) * a.T + t) * a.H * a.G + g.h * a.G + (row - t * a.G);
-          prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + off * D + x % kLines * 64);
-        }
         tc_wait(&sh.q_empty[qbuf.at], qbuf.phase ^ 1, &sh.abort, a.err);
         tc_wait(&sh.item_empty[item.at], item.phase ^ 1, &sh.abort, a.err);
       }
@@ -847,13 +837,24 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         for (int m = 0; m < S::kTerms; ++m) tmem_ld8(o_addr + m * NO + 8 * x, o[m]);
         tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 8; q += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(ra + 8 * x + q);
+          const float by[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int m = 1; m < S::kTerms; ++m) o[0][q] += o[m][q];
-          o[0][q] *= ra[8 * x + q];
+          for (int z = 0; z < 4; ++z) {
+#pragma unroll
+            for (int m = 1; m < S::kTerms; ++m) o[0][q + z] += o[m][q + z];
+            o[0][q + z] *= by[z];
+          }
         }
         if (D < 128 && key >= D) continue;
-        const uint64_t* to = &sh.row_to[col0 + 8 * x];
+        uint64_t to[8];  // all read before the first store: it could be to any of them
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&sh.row_to[col0 + 8 * x + q]);
+          to[q] = v.x;
+          to[q + 1] = v.y;
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (8 * x + q < live) {

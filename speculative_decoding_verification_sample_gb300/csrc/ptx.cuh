@@ -167,11 +167,6 @@ __device__ __forceinline__ float f2_hi(uint64_t r) {
   return hi;
 }
 
-// The line of p into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
 // Streaming 16-byte global load that does not allocate in L1.
 __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
   uint4 v;
