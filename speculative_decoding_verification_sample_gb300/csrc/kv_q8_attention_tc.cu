@@ -39,7 +39,8 @@
 // the hot loop must stay small (waits out of line, one copy of each block of code:
 // 334 to 242 us for the 20-row case), the copies of 16-token blocks need two warps,
 // an item's queries must be converted before it begins (230 to 206 us), an item's end
-// reads its shared memory before its first store (206 to 203 us), and nothing may go through local memory, which this much shared memory pushes out to L2.
+// reads its shared memory before its first store (206 to 203 us), and nothing may go
+// through local memory, which this much shared memory pushes out to L2.
 // Not kept, for the 20-row case: two groups taking the tiles in turn (374 us), three
 // CTAs per SM with short rings (351 us), tiles called into L2 ahead of the copies
 // (281 us), the copies' coordinates made uniform by shuffles (316 us); for many rows,
