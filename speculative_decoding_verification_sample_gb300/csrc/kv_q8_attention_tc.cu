@@ -33,7 +33,7 @@
 // heads x 128, 20 query rows, 1.23 GB: 203 us = 6.1 TB/s (0.90 of the copy peak); 8 rows
 // 195 us; 2 rows of 100-131 thousand tokens 86 us (5.5 TB/s). Beyond that by the
 // softmax warps' instructions (about 11 for each 32 scores): 32 rows 215 us, 48 rows
-// 279 us; a window of 4096 over 56 rows 132 us (3.1 TB/s). Short rows (100-600 tokens)
+// 270 us; a window of 4096 over 56 rows 132 us (3.1 TB/s). Short rows (100-600 tokens)
 // by the changes of items: 77 us, 48 query rows 127 us (94 and 166 before the queries were
 // prepared two items ahead and in fewer steps). The steps that mattered:
 // the hot loop must stay small (waits out of line, one copy of each block of code:
@@ -626,11 +626,16 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           float z[8 * N];
 #pragma unroll
           for (int i = 0; i < N; ++i) tmem_ld8(s_addr + 8 * (x + i), z + 8 * i);
+          float4 cs[2 * N], ms[2 * N];
+#pragma unroll
+          for (int q = 0; q < 2 * N; ++q) {
+            cs[q] = *reinterpret_cast<const float4*>(&sh.row_c[qb][col0 + 8 * x + 4 * q]);
+            ms[q] = *reinterpret_cast<const float4*>(minus + 8 * x + 4 * q);
+          }
           tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < 2 * N; ++q) {
-            const float4 c4 = *reinterpret_cast<const float4*>(&sh.row_c[qb][col0 + 8 * x + 4 * q]);
-            const float4 m4 = *reinterpret_cast<const float4*>(minus + 8 * x + 4 * q);
+            const float4 c4 = cs[q], m4 = ms[q];
             const float2 s0 = make_float2(z[4 * q], z[4 * q + 1]);
             const float2 s1 = make_float2(z[4 * q + 2], z[4 * q + 3]);
             y[2 * q] = __ffma2_rn(__fmul2_rn(s0, ks2), make_float2(c4.x, c4.y),
