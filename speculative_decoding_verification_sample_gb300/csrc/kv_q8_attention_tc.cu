@@ -31,7 +31,7 @@
 //
 // Bound by memory up to 24 query rows of a kv head: 256 rows of 512-4096 tokens, 8 kv
 // heads x 128, 20 query rows, 1.23 GB: 203 us = 6.1 TB/s (0.90 of the copy peak); 8 rows
-// 195 us; 2 rows of 100-131 thousand tokens 86 us (5.5 TB/s). Beyond that by the
+// 195 us; 2 rows of 100-131 thousand tokens 85 us (5.6 TB/s). Beyond that by the
 // softmax warps' instructions (about 11 for each 32 scores): 32 rows 215 us, 48 rows
 // 270 us; a window of 4096 over 56 rows 132 us (3.1 TB/s). Short rows (100-600 tokens)
 // by the changes of items: 77 us, 48 query rows 127 us (94 and 166 before the queries were
