@@ -177,6 +177,18 @@ def test_attention_matches_oracle(T, Hq, H, D, bs):
     assert _attn_same(gpu_lib(), c) == 0
 
 
+@pytest.mark.parametrize("T,G,D,bs", [(1, 2, 128, 16), (5, 4, 128, 16), (5, 4, 64, 32),
+                                      (7, 4, 128, 64), (12, 4, 128, 16), (16, 4, 128, 16),
+                                      (16, 4, 64, 16)])
+def test_attention_many_items_a_cta(T, G, D, bs):
+    """1200 (row, kv head) pairs of one to three tiles: every CTA goes through several, so that
+    what it keeps of an item is used again, for each number of query rows."""
+    rng = np.random.default_rng(T * G + D)
+    c = _attn_case(T * G + D, lengths=[int(x) for x in rng.integers(0, 300, 150)], T=T, Hq=8 * G,
+                   H=8, D=D, bs=bs)
+    assert _attn_same(gpu_lib(), c) == 0
+
+
 @pytest.mark.parametrize("T,Hq,H,D,bs", [(1, 4, 1, 128, 16), (5, 4, 2, 64, 16), (9, 3, 1, 48, 5)])
 def test_attention_fp32(T, Hq, H, D, bs):
     c = _attn_case(T * D + bs, lengths=LENGTHS, T=T, Hq=Hq, H=H, D=D, bs=bs, dtype="fp32")
