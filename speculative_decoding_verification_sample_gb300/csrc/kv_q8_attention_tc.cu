@@ -217,7 +217,8 @@ __device__ __noinline__ uint32_t seen_rows(int L, int n, int end, int G, int win
     return m;
   }
   const int first = max(0, p - L);
-  const int last = window == 0 || p < sinks ? n : max(0, min(n, p - L + window));
+  // compared before it is added: a window may be as large as an int
+  const int last = window == 0 || p < sinks || window >= n - (p - L) ? n : max(0, p - L + window);
   const int lo = max(0, first * G - base), hi = min(w, last * G - base);
   if (hi <= lo) return 0u;
   return (hi == 32 ? ~0u : (1u << hi) - 1u) & (~0u << lo);

@@ -203,6 +203,19 @@ def test_attention_window_and_sinks(D, bs, window, sinks):
     assert _attn_same(gpu_lib(), c, dict(window=window, sinks=sinks)) == 0
 
 
+NO_LIMIT = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("T,G,D,bs,dtype", [(6, 4, 128, 16, "bf16"), (32, 2, 64, 32, "bf16"),
+                                            (6, 4, 96, 16, "bf16"), (3, 2, 128, 16, "fp32")])
+@pytest.mark.parametrize("window,sinks", [(NO_LIMIT, 0), (NO_LIMIT, NO_LIMIT), (NO_LIMIT - 20, 4),
+                                          (1, NO_LIMIT), (2 ** 30, 1)])
+def test_attention_largest_windows(T, G, D, bs, dtype, window, sinks):
+    """Windows and sinks that stand for "no limit": arithmetic on them must not leave 32 bits."""
+    c = _attn_case(D + T, lengths=[0, 1, 60, 127, 300], T=T, Hq=2 * G, H=2, D=D, bs=bs, dtype=dtype)
+    assert _attn_same(gpu_lib(), c, dict(window=window, sinks=sinks)) == 0
+
+
 @pytest.mark.parametrize("T,G,D,bs", [(15, 4, 128, 16), (32, 2, 128, 64), (9, 1, 64, 16),
                                       (5, 2, 32, 16)])
 def test_attention_tree(T, G, D, bs):
