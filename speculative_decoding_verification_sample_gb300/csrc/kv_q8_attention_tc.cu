@@ -12,15 +12,21 @@
 // probabilities for V's.
 //   Queries: each row is scaled by a power of two to [128, 256) and split into two
 // e4m3 terms (4 + 4 bits: a bf16 number exactly, down to 2^-10 of the row's
-// largest). Probabilities: p is rounded once to 9 bits (2^-9 relative) and split
+// largest). Probabilities: p is rounded to 9 bits (2^-9 relative) and split
 // into three e5m2 terms of at most 3 bits, exactly; e5m2 is the upper byte of
 // fp16, so a term is a byte of the fp16 number and the rest one subtraction.
-// 9 bits leave the bf16 output's own rounding the larger error; e5m2's 32
-// binades hold what a key contributes (probability times V scale) down to 2^-22 of
-// the row's reference.
+// 9 bits leave the bf16 output's own rounding the larger error. e5m2's smallest step
+// is 2^-24 of the row's reference (in what a key contributes, probability times V scale),
+// and the terms cut below it. So that many small keys do not lose in one direction,
+// each has a number between 0 and a step added first, by turns of its position: a key is
+// off by less than a step, and N of them by about half a step times sqrt(N), while the
+// denominator takes p in fp32. Rounding to nearest instead would drop every key under
+// half a step: 2^-8 of the row's weight for 131072 of them; a finer step takes a smaller
+// distance by which keys may exceed the reference, and moving it more often: steps of 2^-27
+// cost 1 to 9 % (48 query rows 290 to 317 us, 20 rows 206 to 210).
 //   Softmax: a row's reference m is the largest z_j + log2(V scale of j) (rounded up
 // to a binade) of the first tile, and is only moved when a later one exceeds it by
-// 8: then O and l are rescaled once; otherwise a tile costs no reduction over its
+// 7.75: then O and l are rescaled once; otherwise a tile costs no reduction over its
 // keys. l stays per thread (one key of every tile) until the item ends.
 //
 //
@@ -66,8 +72,8 @@ constexpr int kTcScaleRing = 8;             // tiles whose scales are held
 constexpr int kTcItems = 3;                 // items whose rows are described at a time
 constexpr int kTcMaxPages = 16;             // blocks of one tile
 constexpr float kTcUnset = 1e30f;           // minus the reference of a row that has seen no key
-constexpr float kTcSlack = 8.0f;            // binades by which keys may exceed the reference
-constexpr float kTcLift = 64.0f;            // 1 enters as 2^6: 2^6 2^8 < 2^16, e5m2's range
+constexpr float kTcSlack = 7.75f;           // binades by which keys may exceed the reference
+constexpr float kTcLift = 256.0f;           // 1 enters as 2^8: 2^8 2^7.75 < 1.75 2^15, e5m2's largest
 constexpr int kTcSmem = 113 * 1024 - 512;   // of one CTA, two per SM
 
 template <int NR>
@@ -746,6 +752,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         }
         wait_outputs();  // P may be replaced
         const float2 lift = make_float2(vr * kTcLift, vr * kTcLift);
+        // What the key adds before the terms cut to multiples of 2^-16: (2 x + 1) 2^-24 (an
+        // fp16 subnormal, so its bits are 2 x + 1), x from 0 to 127 by turns of the position.
+        uint32_t turn = ((uint32_t(key) * 79u + uint32_t(info.x >> 7) * 37u) & 127u) * 2u + 1u;
+        turn = (turn | (vr < 0.0f ? 0x8000u : 0u)) * 0x00010001u;
         uint8_t* p_to = p_s + key * 16;
 #pragma unroll
         for (int x = 0; x < chunks; ++x) {
@@ -764,6 +774,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
               const float2 v = __fmul2_rn(p, lift);
               asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[w]) : "f"(v.y), "f"(v.x));
               h[w] = (h[w] + 0x00020002u) & 0xfffcfffcu;  // 9 bits, half up
+              asm("add.rn.f16x2 %0, %0, %1;" : "+r"(h[w]) : "r"(turn));
             }
             auto rest = [](uint32_t v) {
               uint32_t o;

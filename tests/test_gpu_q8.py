@@ -260,6 +260,61 @@ def test_attention_peaked_scores(D):
     assert _attn_same(gpu_lib(), c) == 0
 
 
+def _tail_bound(want, spread, codes2, top):
+    """bf16 output, half a step: 2^-8. A weight is held in 9 bits (half a step 2^-9), and q . k is
+    exact here; a score in log2 units is below 64, rounded to 2^-19 twice, in the weight and in the
+    sum, whose exponentials and additions are fp32: 2^-16. A small weight is cut to one of the two
+    multiples of a step next to it, by turns: off by half a step in the mean square, so the sum
+    over the keys by less than 8 times step / 2 * sqrt(sum of squared codes). The step is 2^-24 of
+    the row's reference, which is at most twice the largest product of weight and V scale."""
+    return (2.0 ** -8 * np.abs(want) + (2.0 ** -9 + 2.0 ** -16) * spread
+            + 8 * 2.0 ** -24 * top * np.sqrt(codes2))
+
+
+@pytest.mark.parametrize("G", [4, 20, 40, 64])
+@pytest.mark.parametrize("low,high,sign", [(2.75, 5.5, 1), (2.75, 5.5, -1), (-0.5, 3.0, 1),
+                                           (0.0, 0.0, 1)])
+def test_attention_many_small_probabilities(G, low, high, sign):
+    """One key with most of the weight and V = 0, then 100 thousand with 2^-18 to 2^-27 of its
+    probability each and V of one sign: what the small ones lose adds up. About as many rows as
+    there are CTAs share the blocks, so that a row lies in one CTA or two."""
+    import torch
+    sv = gpu_lib()
+    rng = np.random.default_rng(G)
+    N, bs, D = 100 * 1024, 64, 64
+    rows = 300
+    nb = N // bs
+    pool = np.zeros((nb, 1, 2, 1, bs, D), np.uint8)
+    grid = q8.VALUES[:127]
+    grid = np.concatenate([-grid[1:], grid])
+    k = rng.choice(grid[(grid >= low) & (grid <= high)], N)
+    k[0] = 18.0
+    v = rng.integers(64, 448, (N, D)).astype(np.float64)
+    v[0] = 0.0
+    pool[:, 0, 0, 0, :, 0] = q8.encode(k).reshape(nb, bs)
+    pool[:, 0, 1, 0] = q8.encode(sign * v).reshape(nb, bs, D)
+    v = q8.VALUES[pool[:, 0, 1, 0]].reshape(N, D)
+    scales = np.ones((nb, 1, 2, 1))
+    scales[:, 0, 1] = 2.0 ** -8
+    q = np.zeros((rows, 1, G, D))
+    q[..., 0] = rng.choice([1.0, 0.984375, 1.015625], (rows, 1, G))   # bf16 numbers
+    bt = np.tile(np.append(0, 1 + rng.permutation(nb - 1)), (rows, 1))
+    k, v = (x.reshape(nb, bs, -1)[bt[0]].reshape(N, -1) for x in (k, v))
+    x = torch.from_numpy(q).bfloat16().cuda()
+    out = torch.empty_like(x)
+    sv.kv_q8_attention(x, dev_pool(pool), dev_scales(scales), i32(bt), i32([N - 1] * rows), out,
+                       softmax_scale=1.0)
+    got = out.double().cpu().numpy()
+    for f in (1.0, 0.984375, 1.015625):
+        z = f * k[:, 0]
+        w = np.exp(z - z.max())
+        w /= w.sum()
+        want = w @ v * 2.0 ** -8
+        lim = _tail_bound(want, w @ np.abs(v) * 2.0 ** -8, (v * v).sum(0), w.max() * 2.0 ** -8)
+        off = np.abs(got[q[..., 0] == f] - want)
+        assert off.size and np.max(off / lim) <= 1.0, float(np.max(off / lim))
+
+
 def test_attention_softmax_scale_and_small_queries():
     sv = gpu_lib()
     c = _attn_case(16, lengths=[200, 50], T=2, Hq=4, H=1, D=128, bs=16)
