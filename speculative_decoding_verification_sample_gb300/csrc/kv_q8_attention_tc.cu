@@ -74,13 +74,17 @@ constexpr int kTcMaxPages = 16;             // blocks of one tile
 constexpr float kTcUnset = 1e30f;           // minus the reference of a row that has seen no key
 constexpr float kTcSlack = 7.75f;           // binades by which keys may exceed the reference
 constexpr float kTcLift = 256.0f;           // 1 enters as 2^8: 2^8 2^7.75 < 1.75 2^15, e5m2's largest
+// V scales are 2^-100 to 2^120 and enter as half of it: with the lift they stay below 2^128,
+// and a row's sum, whose probabilities go up to 2^7.75 over the V scale, too.
+constexpr float kTcVDown = 0.5f;
+constexpr float kTcMaxSum = 0x1.fffffep126f;
 constexpr int kTcSmem = 113 * 1024 - 512;   // of one CTA, two per SM
 
 template <int NR>
 struct TcShared {
   alignas(16) float row_c[kTcItems][NR];  // query row's scale * softmax_scale * log2(e)
   alignas(16) float row_nm[NR];     // minus the reference of the exponentials
-  alignas(16) float row_a[NR];      // rescale factor, then that of the output
+  alignas(16) float row_a[NR];      // root of the rescale factor, then the output's factor
   alignas(16) float part[4][NR];    // the warps' maxima, then sums
   alignas(16) float zero[NR];
   alignas(16) uint64_t row_to[NR];  // where the row's outputs go
@@ -170,11 +174,11 @@ __device__ __forceinline__ bool bar_group_or(int group, bool x) {
   return r != 0;
 }
 
-// The smallest e in [-100, 100] with |x| <= 2^e (100 for larger ones).
+// The smallest e in [-101, 119] with |x| <= 2^e (119 for larger ones).
 __device__ __forceinline__ int scale_binade(float x) {
   const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
   const int e = int(u >> 23) - 127 + ((u & 0x7fffffu) != 0);
-  return max(-100, min(100, e));
+  return max(-101, min(119, e));
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -387,7 +391,6 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     if (lane == 0) tma_prefetch_map(&map);
   }
   if (tid < NR) sh.zero[tid] = 0.0f;
-  if (tid < kTcScaleRing * kTcMaxPages) (&sh.vs[0][0])[tid] = 0.0f;  // pages that a tile does not have
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -589,19 +592,6 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       const int j_first = j, j_end = j + (g.t1 - g.t0);
       if (key < W) nm[key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
       bar_group(group);
-      // V scales are taken relative to the first tile's largest, a power of two
-      int vref = 0;
-      tc_wait(&sh.scales_full[j % kTcScaleRing], j / kTcScaleRing & 1, &sh.abort, a.err);
-      {
-        float x = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kTcMaxPages; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(&sh.vs[j % kTcScaleRing][i]);
-          x = fmaxf(fmaxf(x, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-        }
-        vref = scale_binade(x);
-      }
-      const float vdown = q8_pow2(-vref);
       float2 l[W / 2];
 #pragma unroll
       for (int r = 0; r < W / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
@@ -615,7 +605,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         const int2 info = sh.tile[se];
         const bool open = info.y;
         if (!(fabsf(vs) <= FLT_MAX)) ks = __uint_as_float(0x7fc00000u);
-        const float vr = vs * vdown;
+        const float vr = vs * kTcVDown;
         const float lv = float(scale_binade(vr));  // vr <= 2^lv
         const float2 ks2 = make_float2(ks, ks);
         uint32_t seen = ~0u;
@@ -718,7 +708,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
             const float old = -nm[key];
             const float m = fmaxf(fmaxf(fmaxf(mp[0], mp[NR]), fmaxf(mp[2 * NR], mp[3 * NR])), old);
             nm[key] = -m;
-            ra[key] = ex2_approx(old - m);
+            // the root: references may move by 230 binades with the V scales, and a sum that
+            // holds as many still counts
+            ra[key] = ex2_approx(0.5f * (old - m));
           }
           bar_group(group);
           if (kKeep) {
@@ -728,8 +720,10 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           }
           if (j > j_first) {
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i)
-              l[i] = __fmul2_rn(l[i], *reinterpret_cast<const float2*>(ra + 2 * i));
+            for (int i = 0; i < W / 2; ++i) {
+              const float2 root = *reinterpret_cast<const float2*>(ra + 2 * i);
+              l[i] = __fmul2_rn(__fmul2_rn(l[i], root), root);
+            }
             wait_outputs();
             tc_fence_after();
 #pragma unroll 1
@@ -740,7 +734,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
               tmem_ld8(at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] *= ra[r + q];
+              for (int q = 0; q < 8; ++q) o[q] *= ra[r + q] * ra[r + q];
               tmem_st8(at, o);
             }
             tmem_wait_st();
@@ -827,11 +821,13 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       const int64_t slot = 2 * c + (g.u == plan.u0 ? 0 : 1);
       if (key < W) {
         const float* mp = sh.part[0] + col0 + key;
-        const float sum = mp[0] + mp[NR] + mp[2 * NR] + mp[3 * NR];
+        float sum = mp[0] + mp[NR] + mp[2 * NR] + mp[3 * NR];
+        // half a million keys above the reference whose values are all zero; a NaN stays
+        if (sum > kTcMaxSum) sum = kTcMaxSum;
         // A part is left with its sum in [1, 2): references of parts differ by their V
         // scales, so a sum by itself may be as far from 1 as those.
-        const int e = sum > 0.0f && sum <= FLT_MAX ? int(__float_as_uint(sum) >> 23) - 127 : 0;
-        const float unlift = q8_pow2(vref) / kTcLift;
+        const int e = sum > 0.0f ? int(__float_as_uint(sum) >> 23) - 127 : 0;
+        constexpr float unlift = 1.0f / (kTcLift * kTcVDown);
         const float down = q8_pow2(-e);
         ra[key] = (!whole ? down : sum == 0.0f ? 0.0f : __fdividef(down, sum * down)) * unlift;
         const int off = sh.row_off[qb][col0 + key];

@@ -260,6 +260,29 @@ def test_attention_peaked_scores(D):
     assert _attn_same(gpu_lib(), c) == 0
 
 
+@pytest.mark.parametrize("T,G,D", [(1, 4, 128), (5, 4, 64), (16, 4, 128)])
+@pytest.mark.parametrize("first,rest", [(-100, 4), (-100, 60), (-100, 110), (-100, 0), (60, -60),
+                                        (-60, 60), (0, -100), (110, -100), (-100, -100), (110, 110), (-90, -90)])
+def test_attention_value_scales_far_apart(T, G, D, first, rest):
+    """V scales of the first tile 2^first (2^-100: its values were zero), of the others 2^rest, of
+    every fifth block in between; 1200 rows over the same two rows' blocks, so that a CTA takes
+    whole rows."""
+    c = _attn_case(24 + T, lengths=[150, 1000], T=T, Hq=G, H=1, D=D, bs=16)
+    for row in c["bt"]:
+        for j, x in enumerate(row[row >= 0]):
+            e = first if j < 8 else (first + rest) // 2 if j % 5 == 0 else rest
+            c["scales"][x, :, 1] = 2.0 ** e
+            if e == -100:
+                c["pool"][x, :, 1] &= 0x80
+    many = dict(c, **{k: np.tile(c[k], (600,) + (1,) * (c[k].ndim - 1)) for k in ("q", "bt", "sl")})
+    got, err = _attn_gpu(gpu_lib(), many)
+    want, spread, reach = q8.attention(c["q"], c["pool"], c["scales"], c["bt"], c["sl"], layer=1)
+    lim = _bound(c, want, spread, reach, D)
+    got = got.reshape(600, *want.shape)
+    assert err == 0 and np.isfinite(got).all()
+    assert np.max(np.abs(got - want) / lim) <= 1.0
+
+
 def _tail_bound(want, spread, codes2, top):
     """bf16 output, half a step: 2^-8. A weight is held in 9 bits (half a step 2^-9), and q . k is
     exact here; a score in log2 units is below 64, rounded to 2^-19 twice, in the weight and in the
