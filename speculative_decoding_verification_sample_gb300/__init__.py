@@ -376,15 +376,16 @@ def kv_commit_rollback(block_table, seq_lens, num_accepted, prov_blocks, kv_pool
 # The calls below take a few microseconds on the device, so their arguments are checked with
 # few Python steps: _arg covers the usual case and leaves the message to _check, and the torch
 # names are looked up once.
-_int32 = _float32 = _e4m3 = _uint8 = _raw_current = None
+_int32 = _float32 = _e4m3 = _uint8 = _raw_current = _capturing = None
 
 
 def _ready() -> ctypes.CDLL:
     """The library, with the torch names of this section set."""
-    global _int32, _float32, _e4m3, _uint8, _raw_current
+    global _int32, _float32, _e4m3, _uint8, _raw_current, _capturing
     import torch
     _int32, _float32, _uint8 = torch.int32, torch.float32, torch.uint8
     _e4m3, _raw_current = torch.float8_e4m3fn, torch._C._cuda_getCurrentRawStream
+    _capturing = torch._C._cuda_isCurrentStreamCapturing
     return lib()
 
 
@@ -472,26 +473,39 @@ _attn_workspaces = {}
 
 
 def _attn_workspace(shape, device, raw, stream):
-    """(pointer, bytes) of a cached workspace, one per device and stream: calls on one stream
-    are ordered, calls on two may overlap."""
-    key = (shape, device.index, raw)
-    ws = _attn_workspaces.get(key)
-    if ws is None:
-        import torch
-        need = kv_q8_attention_workspace_bytes(*shape)
-        if need == 0:
-            return None, 0  # an unsupported shape: the library call itself reports why
-        held = _attn_workspaces.get((device.index, raw))
-        if held is None or held.numel() < need + 256:
-            if held is not None:
-                # its last call may still be running
-                held.record_stream(stream or torch.cuda.current_stream(device))
-                for k in [k for k in _attn_workspaces if k[1:] == (device.index, raw)]:
-                    del _attn_workspaces[k]
-            held = torch.empty(need + 256, dtype=torch.uint8, device=device)
+    """(pointer, bytes, the tensor that holds them) of a workspace for a call on a stream.
+
+    One is kept for each device and stream: calls on one stream are ordered, calls on two may
+    overlap. It is allocated in its stream's order, so a larger one may replace it at any time.
+    A capture gets a workspace of its own for each call instead, from the graph's memory: a
+    replay may come long after, and on another stream than the calls that share the kept one."""
+    import torch
+    if stream is None or raw == _raw_current(device.index):
+        if not _capturing():
+            ws = _attn_workspaces.get((shape, device.index, raw))
+            return _new_attn_workspace(shape, device, raw, True) if ws is None else ws
+        return _new_attn_workspace(shape, device, raw, False)
+    with torch.cuda.stream(stream):
+        return _attn_workspace(shape, device, raw, None)
+
+
+def _new_attn_workspace(shape, device, raw, keep):
+    """A workspace in the order of the current stream, `raw`; `keep`: for the calls to come."""
+    import torch
+    need = kv_q8_attention_workspace_bytes(*shape)
+    if need == 0:
+        return None, 0, None  # an unsupported shape: the library call itself reports why
+    held = _attn_workspaces.get((device.index, raw)) if keep else None
+    if held is None or held.numel() < need + 256:
+        held = torch.empty(need + 256, dtype=torch.uint8, device=device)
+    off = (-held.data_ptr()) % 256
+    ws = held.data_ptr() + off, held.numel() - off, held
+    if keep:
+        if _attn_workspaces.get((device.index, raw)) is not held:
+            for k in [k for k in list(_attn_workspaces) if k[1:] == (device.index, raw)]:
+                _attn_workspaces.pop(k, None)
             _attn_workspaces[(device.index, raw)] = held
-        off = (-held.data_ptr()) % 256
-        ws = _attn_workspaces[key] = held.data_ptr() + off, held.numel() - off
+        _attn_workspaces[(shape, device.index, raw)] = ws
     return ws
 
 
@@ -504,7 +518,7 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
     to head_dim ** -0.5; window / sinks: sliding window and always-visible first positions;
     tree_mask: optional int32 [B, T], bit s of entry t lets query t see position seq_lens[b] + s.
     workspace: a uint8 tensor of kv_q8_attention_workspace_bytes + 256; None: one that the
-    binding keeps for the stream."""
+    binding keeps for the stream, or under a capture one in the graph's memory."""
     L = _lib if _int32 is not None else _ready()
     pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
     qp = _arg(q, "q", 4, None)
@@ -523,7 +537,8 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
     device = q.device
     raw = _raw_stream(stream, device)
     if workspace is None:
-        wsp, wsn = _attn_workspace((T, Hq, H, D), device, raw, stream)
+        # `held` lives until the launch is made
+        wsp, wsn, held = _attn_workspace((T, Hq, H, D), device, raw, stream)
     else:
         off = (-workspace.data_ptr()) % 256
         wsp, wsn = workspace.data_ptr() + off, max(0, workspace.numel() - off)

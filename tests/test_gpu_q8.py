@@ -446,6 +446,96 @@ def test_append_then_attend_in_a_graph():
         assert np.all(off <= _bound(c, want, spread, reach, 128))
 
 
+def _attend(sv, c, out, stream=None):
+    """A call on the case's device tensors, kept in the case."""
+    import torch
+    if "dev" not in c:
+        c["dev"] = (torch.from_numpy(c["q"]).bfloat16().cuda(), dev_pool(c["pool"]),
+                    dev_scales(c["scales"]), i32(c["bt"]), i32(c["sl"]))
+    sv.kv_q8_attention(*c["dev"], out, layer=c["layer"], stream=stream)
+
+
+def test_attention_graph_outlives_a_larger_workspace():
+    """A graph of a small shape, then a larger shape on its stream and new tensors wherever there
+    is memory: the replay neither uses nor changes what is not its own."""
+    import torch
+    sv = gpu_lib()
+    small = _attn_case(25, lengths=[5000, 700], T=1, Hq=4, H=2, D=64, bs=16)
+    large = _attn_case(26, lengths=[3000, 90], T=32, Hq=4, H=2, D=128, bs=16)
+    assert (sv.kv_q8_attention_workspace_bytes(32, 4, 2, 128)
+            > sv.kv_q8_attention_workspace_bytes(1, 4, 2, 64))
+    s = torch.cuda.Stream()
+    want, out = (torch.empty((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    big = torch.empty((2, 32, 4, 128), dtype=torch.bfloat16, device="cuda")
+    _attend(sv, small, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        _attend(sv, small, out)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        _attend(sv, small, out)
+    with torch.cuda.stream(s):
+        _attend(sv, large, big)
+    torch.cuda.synchronize()
+    sizes = [sv.kv_q8_attention_workspace_bytes(*x) + 256 for x in ((1, 4, 2, 64), (32, 4, 2, 128))]
+    with torch.cuda.stream(s):
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in 3 * sizes]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all(bool((x == 7).all()) for x in others)
+
+
+def test_attention_graphs_of_one_stream_replayed_on_two():
+    import torch
+    sv = gpu_lib()
+    s = torch.cuda.Stream()
+    got = []
+    for seed, lengths in ((27, [9000, 300]), (28, [100, 8000])):
+        c = _attn_case(seed, lengths=lengths, T=4, Hq=8, H=2, D=128, bs=16)
+        want, out = (torch.empty((2, 4, 8, 128), dtype=torch.bfloat16, device="cuda")
+                     for _ in range(2))
+        _attend(sv, c, want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            _attend(sv, c, out)
+        got.append((graph, out, want, torch.cuda.Stream(), c))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, out, _, stream, _ in got:
+            with torch.cuda.stream(stream):
+                out.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in got:
+        assert torch.equal(out, want)
+
+
+def test_attention_workspace_is_allocated_in_its_streams_order():
+    """Memory that was just freed on the current stream may still be in use there: a call on
+    another stream must not take it."""
+    import torch
+    sv = gpu_lib()
+    c = _attn_case(29, lengths=[3000, 700], T=5, Hq=8, H=2, D=128, bs=16)
+    out = torch.empty((2, 5, 8, 128), dtype=torch.bfloat16, device="cuda")
+    n = sv.kv_q8_attention_workspace_bytes(5, 8, 2, 128) + 256
+    _attend(sv, c, out)
+    torch.cuda.synchronize()
+    x = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    was = {t.data_ptr() for t in x}
+    del x
+    s = torch.cuda.Stream(priority=-1)
+    _attend(sv, c, out, stream=s)
+    held = sv._attn_workspaces[(out.device.index, s.cuda_stream)]
+    assert held.data_ptr() not in was
+    torch.cuda.synchronize()
+
+
 def test_binding_refuses():
     import torch
     sv = gpu_lib()
