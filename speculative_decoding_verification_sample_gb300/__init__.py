@@ -376,62 +376,82 @@ def kv_commit_rollback(block_table, seq_lens, num_accepted, prov_blocks, kv_pool
 # The calls below take a few microseconds on the device, so their arguments are checked with
 # few Python steps: _arg covers the usual case and leaves the message to _check, and the torch
 # names are looked up once.
-_int32 = _float32 = _e4m3 = _uint8 = _raw_current = _capturing = None
+_int32 = _float32 = _bfloat16 = _e4m3 = _uint8 = _raw_current = None
+_capturing = _current_device = None
 
 
 def _ready() -> ctypes.CDLL:
     """The library, with the torch names of this section set."""
-    global _int32, _float32, _e4m3, _uint8, _raw_current, _capturing
+    global _int32, _float32, _bfloat16, _e4m3, _uint8, _raw_current, _capturing, _current_device
     import torch
     _int32, _float32, _uint8 = torch.int32, torch.float32, torch.uint8
+    _bfloat16 = torch.bfloat16
     _e4m3, _raw_current = torch.float8_e4m3fn, torch._C._cuda_getCurrentRawStream
     _capturing = torch._C._cuda_isCurrentStreamCapturing
+    _current_device = torch._C._cuda_getDevice
     return lib()
 
 
-def _arg(t, name, ndim, dtype):
-    """The device pointer of a contiguous CUDA tensor of `ndim` dims and `dtype` (None: any)."""
+def _place(t, name):
+    """The index of the device of a call's tensors, which has to be the current one: the launch
+    goes there."""
     try:
-        if t.is_cuda and (t.dtype is dtype or dtype is None) and t.ndim == ndim \
+        dev = t.get_device()
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        _check(t, name)
+        raise ValueError(f"{name} is not a usable tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _arg(t, name, ndim, dtype, dev):
+    """The pointer of a contiguous tensor of `ndim` dims and `dtype` (None: any) on device `dev`."""
+    try:
+        if t.get_device() == dev and (t.dtype is dtype or dtype is None) and t.ndim == ndim \
                 and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
     _check(t, name, ndim, dtype)
-    raise ValueError(f"{name} is not a usable tensor")
+    raise ValueError(f"{name} must be on cuda:{dev} with the other tensors, not on {t.device}")
 
 
-def _vec(t, name, n):
+def _vec(t, name, n, dev):
     """The pointer of an optional int32 [n] tensor."""
     if t is None:
         return None
-    p = _arg(t, name, 1, _int32)
+    p = _arg(t, name, 1, _int32, dev)
     if t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
     return p
 
 
-def _word(t, name):
+def _word(t, name, dev):
     """The pointer of an optional int32 tensor of at least one entry."""
     if t is None:
         return None
-    p = _arg(t, name, 1, _int32)
+    p = _arg(t, name, 1, _int32, dev)
     if t.shape[0] < 1:
         raise ValueError(f"{name} must have an entry")
     return p
 
 
-def _raw_stream(stream, device):
+def _raw_stream(stream, dev):
     """cudaStream_t of `stream`, or of the current stream of the tensors' device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_current(device.index)
+    if stream is None:
+        return _raw_current(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
-def _q8_pool(kv_pool, kv_scales):
+def _q8_pool(kv_pool, kv_scales, dev):
     """Checks the 8-bit pool and its scales; returns their pointers and the pool's shape."""
-    pool = _arg(kv_pool, "kv_pool", 6, None)
-    scales = _arg(kv_scales, "kv_scales", 4, _float32)
+    pool = _arg(kv_pool, "kv_pool", 6, None, dev)
+    scales = _arg(kv_scales, "kv_scales", 4, _float32, dev)
     if kv_pool.dtype is not _e4m3 and kv_pool.dtype is not _uint8:
         raise TypeError(f"kv_pool must be float8_e4m3fn (or its uint8 bytes), got {kv_pool.dtype}")
     shape = kv_pool.shape
@@ -447,18 +467,19 @@ def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int 
     8-bit cache's `layer`: kv_pool [num_blocks, layers, 2, kv_heads, block_size, head_dim]
     float8_e4m3fn, kv_scales [num_blocks, layers, 2, kv_heads]. num_new: optional int32 [B]."""
     L = _lib if _int32 is not None else _ready()
-    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
-    kp = _arg(k, "k", 4, None)
-    vp = _arg(v, "v", 4, k.dtype)
-    bt = _arg(block_table, "block_table", 2, _int32)
+    dev = _place(k, "k")
+    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales, dev)
+    kp = _arg(k, "k", 4, None, dev)
+    vp = _arg(v, "v", 4, k.dtype, dev)
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
     B, T, kh, kd = k.shape
     rows, MB = block_table.shape
     if v.shape != k.shape or kh != H or kd != D or rows != B:
         raise ValueError(f"k and v must be [B, T, {H}, {D}] and block_table [B, max_blocks]")
     st = L.kv_q8_append(
-        kp, vp, _dtype_code(k), pool, scales, bt, _vec(seq_lens, "seq_lens", B),
-        _vec(num_new, "num_new", B), NB, NL, layer, H, D, bs, B, T, MB,
-        _raw_stream(stream, k.device), _word(err_flag, "err_flag"))
+        kp, vp, SPEC_BF16 if k.dtype is _bfloat16 else _dtype_code(k), pool, scales, bt,
+        _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), NB, NL, layer, H, D, bs, B, T, MB,
+        _raw_stream(stream, dev), _word(err_flag, "err_flag", dev))
     if st != SPEC_OK:
         raise SpecError("kv_q8_append", st)
 
@@ -520,10 +541,11 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
     workspace: a uint8 tensor of kv_q8_attention_workspace_bytes + 256; None: one that the
     binding keeps for the stream, or under a capture one in the graph's memory."""
     L = _lib if _int32 is not None else _ready()
-    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
-    qp = _arg(q, "q", 4, None)
-    op = _arg(out, "out", 4, q.dtype)
-    bt = _arg(block_table, "block_table", 2, _int32)
+    dev = _place(q, "q")
+    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales, dev)
+    qp = _arg(q, "q", 4, None, dev)
+    op = _arg(out, "out", 4, q.dtype, dev)
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
     shape = q.shape
     B, T, Hq, qd = shape
     rows, MB = block_table.shape
@@ -531,22 +553,25 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
         raise ValueError(f"q and out must be [B, T, q_heads, {D}] and block_table [B, max_blocks]")
     tm = None
     if tree_mask is not None:
-        tm = _arg(tree_mask, "tree_mask", 2, _int32)
+        tm = _arg(tree_mask, "tree_mask", 2, _int32, dev)
         if tuple(tree_mask.shape) != (B, T):
             raise ValueError(f"tree_mask must be [{B}, {T}], got {tuple(tree_mask.shape)}")
-    device = q.device
-    raw = _raw_stream(stream, device)
+    raw = _raw_stream(stream, dev)
     if workspace is None:
-        # `held` lives until the launch is made
-        wsp, wsn, held = _attn_workspace((T, Hq, H, D), device, raw, stream)
+        ws = _attn_workspaces.get(((T, Hq, H, D), dev, raw))
+        if ws is None or stream is not None or _capturing():
+            ws = _attn_workspace((T, Hq, H, D), q.device, raw, stream)
+        wsp, wsn, held = ws  # `held` lives until the launch is made
     else:
-        off = (-workspace.data_ptr()) % 256
-        wsp, wsn = workspace.data_ptr() + off, max(0, workspace.numel() - off)
+        wsp = _arg(workspace, "workspace", 1, _uint8, dev)
+        off = -wsp % 256
+        wsp, wsn = wsp + off, max(0, workspace.numel() - off)
     st = L.kv_q8_attention(
-        qp, _dtype_code(q), pool, scales, bt, _vec(seq_lens, "seq_lens", B),
-        _vec(num_new, "num_new", B), tm, op, D ** -0.5 if softmax_scale is None else softmax_scale,
+        qp, SPEC_BF16 if q.dtype is _bfloat16 else _dtype_code(q), pool, scales, bt,
+        _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), tm, op,
+        D ** -0.5 if softmax_scale is None else softmax_scale,
         window, sinks, NB, NL, layer, Hq, H, D, bs, B, T, MB, wsp, wsn, raw,
-        _word(err_flag, "err_flag"))
+        _word(err_flag, "err_flag", dev))
     if st != SPEC_OK:
         raise SpecError("kv_q8_attention", st)
 
@@ -555,12 +580,13 @@ def kv_reserve(block_table, seq_lens, free_stack, free_top, status, *, n: int, b
                num_blocks: int, num_new=None, stream=None) -> None:
     """Blocks for n (or num_new[b]) tokens past seq_lens[b]; status receives 0 or error bits."""
     L = _lib if _int32 is not None else _ready()
-    bt = _arg(block_table, "block_table", 2, _int32)
+    dev = _place(block_table, "block_table")
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
     B, MB = block_table.shape
     st = L.kv_reserve(
-        bt, _vec(seq_lens, "seq_lens", B), _vec(num_new, "num_new", B), n, num_blocks, block_size,
-        B, MB, _vec(free_stack, "free_stack", num_blocks), _word(free_top, "free_top"),
-        _word(status, "status"), _raw_stream(stream, block_table.device))
+        bt, _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), n, num_blocks,
+        block_size, B, MB, _vec(free_stack, "free_stack", num_blocks, dev),
+        _word(free_top, "free_top", dev), _word(status, "status", dev), _raw_stream(stream, dev))
     if st != SPEC_OK:
         raise SpecError("kv_reserve", st)
 
@@ -571,26 +597,27 @@ def kv_fork(block_table, seq_lens, extra_refs, src_rows, dst_rows, kv_pool, free
     kv_pool: the 8-bit pool with kv_scales, or kv_commit_rollback's [num_blocks, layers, 2,
     block_size, kv_heads, head_dim] pool without."""
     L = _lib if _int32 is not None else _ready()
-    bt = _arg(block_table, "block_table", 2, _int32)
+    dev = _place(block_table, "block_table")
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
     B, MB = block_table.shape
     if kv_scales is not None:
-        pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales)
+        pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales, dev)
         planes, token = NL * 2 * H, D
     else:
-        pool, scales = _arg(kv_pool, "kv_pool", 6, None), None
+        pool, scales = _arg(kv_pool, "kv_pool", 6, None, dev), None
         NB, NL, two, bs, H, D = kv_pool.shape
         if two != 2:
             raise ValueError("kv_pool must be [num_blocks, layers, 2, block_size, heads, head_dim]")
         planes, token = NL * 2, H * D * kv_pool.element_size()
     if bs != block_size:
         raise ValueError(f"kv_pool holds blocks of {bs} tokens, not {block_size}")
-    src = _arg(src_rows, "src_rows", 1, _int32)
+    src = _arg(src_rows, "src_rows", 1, _int32, dev)
     n = src_rows.shape[0]
     st = L.kv_fork(
-        bt, _vec(seq_lens, "seq_lens", B), _vec(extra_refs, "extra_refs", NB), src,
-        _vec(dst_rows, "dst_rows", n), n, pool, planes, token, scales, NB, block_size, B, MB,
-        _vec(free_stack, "free_stack", NB), _word(free_top, "free_top"), _word(status, "status"),
-        _raw_stream(stream, block_table.device))
+        bt, _vec(seq_lens, "seq_lens", B, dev), _vec(extra_refs, "extra_refs", NB, dev), src,
+        _vec(dst_rows, "dst_rows", n, dev), n, pool, planes, token, scales, NB, block_size, B, MB,
+        _vec(free_stack, "free_stack", NB, dev), _word(free_top, "free_top", dev),
+        _word(status, "status", dev), _raw_stream(stream, dev))
     if st != SPEC_OK:
         raise SpecError("kv_fork", st)
 
@@ -599,13 +626,14 @@ def kv_free(block_table, seq_lens, extra_refs, rows, free_stack, free_top, statu
             num_blocks: int, stream=None) -> None:
     """Releases the listed rows; blocks that no other row holds go back on the free stack."""
     L = _lib if _int32 is not None else _ready()
-    bt = _arg(block_table, "block_table", 2, _int32)
+    dev = _place(block_table, "block_table")
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
     B, MB = block_table.shape
     st = L.kv_free(
-        bt, _vec(seq_lens, "seq_lens", B), _vec(extra_refs, "extra_refs", num_blocks),
-        _arg(rows, "rows", 1, _int32), rows.shape[0], num_blocks, B, MB,
-        _vec(free_stack, "free_stack", num_blocks), _word(free_top, "free_top"),
-        _word(status, "status"), _raw_stream(stream, block_table.device))
+        bt, _vec(seq_lens, "seq_lens", B, dev), _vec(extra_refs, "extra_refs", num_blocks, dev),
+        _arg(rows, "rows", 1, _int32, dev), rows.shape[0], num_blocks, B, MB,
+        _vec(free_stack, "free_stack", num_blocks, dev), _word(free_top, "free_top", dev),
+        _word(status, "status", dev), _raw_stream(stream, dev))
     if st != SPEC_OK:
         raise SpecError("kv_free", st)
 

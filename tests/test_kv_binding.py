@@ -51,3 +51,110 @@ def test_workspace_of_a_capture_is_its_own(workspaces):
     assert kept.keys() == before.keys() and all(kept[k] is before[k] for k in kept)
     state["capturing"] = False
     assert sv._attn_workspace(SMALL, dev, 5, None)[0] == eager[0]
+
+
+# ------------------------------------------------------------------ checks of tensors
+class OnDevice:
+    """A CPU tensor that says it is on a CUDA device: what the binding looks at."""
+
+    def __init__(self, t, index=0):
+        self.t, self.index, self.is_cuda = t, index, True
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class Library:
+    """Notes the calls that would launch."""
+
+    def __init__(self, calls):
+        self.calls = calls
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    calls = []
+    monkeypatch.setattr(sv, "_lib", Library(calls))
+    monkeypatch.setattr(sv, "_raw_current", lambda index: 0)
+    monkeypatch.setattr(sv, "_capturing", lambda: False, raising=False)
+    monkeypatch.setattr(sv, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(sv, "_check", lambda t, name, ndim=None, dtype=None: _check(t, name, ndim,
+                                                                                    dtype))
+    return calls
+
+
+def _check(t, name, ndim, dtype):
+    if not getattr(t, "is_cuda", False) or not t.is_contiguous() or ndim not in (None, t.dim()):
+        raise ValueError(name)
+    if dtype not in (None, t.dtype):
+        raise TypeError(name)
+
+
+def _arguments():
+    import torch
+    i32, f32, bf16, u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+    z = lambda *s, dtype=i32: OnDevice(torch.zeros(s, dtype=dtype))  # noqa: E731
+    pool, scales = z(4, 1, 2, 2, 16, 64, dtype=u8), z(4, 1, 2, 2, dtype=f32)
+    table, lens = z(1, 2), z(1)
+    blocks = dict(free_stack=z(4), free_top=z(1), status=z(1))
+    return {
+        "kv_q8_append": dict(k=z(1, 2, 2, 64, dtype=bf16), v=z(1, 2, 2, 64, dtype=bf16),
+                             kv_pool=pool, kv_scales=scales, block_table=table, seq_lens=lens,
+                             num_new=z(1), err_flag=z(1)),
+        "kv_q8_attention": dict(q=z(1, 2, 4, 64, dtype=bf16), kv_pool=pool, kv_scales=scales,
+                                block_table=table, seq_lens=lens, out=z(1, 2, 4, 64, dtype=bf16),
+                                num_new=z(1), tree_mask=z(1, 2), workspace=z(1 << 10, dtype=u8),
+                                err_flag=z(1)),
+        "kv_reserve": dict(block_table=table, seq_lens=lens, num_new=z(1), **blocks),
+        "kv_fork": dict(block_table=table, seq_lens=lens, extra_refs=z(4), src_rows=z(1),
+                        dst_rows=z(1), kv_pool=pool, kv_scales=scales, **blocks),
+        "kv_free": dict(block_table=table, seq_lens=lens, extra_refs=z(4), rows=z(1), **blocks),
+    }
+
+
+REST = {"kv_q8_append": {}, "kv_q8_attention": {}, "kv_reserve": dict(n=1, block_size=16, num_blocks=4),
+        "kv_fork": dict(block_size=16), "kv_free": dict(num_blocks=4)}
+
+
+@pytest.mark.parametrize("name", list(REST))
+def test_every_tensor_must_be_on_the_current_device(calls, monkeypatch, name):
+    f, ok = getattr(sv, name), _arguments()[name]
+    f(**ok, **REST[name])
+    assert calls == [name]
+    for key, t in ok.items():
+        for other in (OnDevice(t.t, 1), t.t):    # another device, the host
+            with pytest.raises(ValueError):
+                f(**{**ok, key: other}, **REST[name])
+    monkeypatch.setattr(sv, "_current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        f(**ok, **REST[name])
+    assert calls == [name]
+
+
+def test_stream_must_be_of_the_tensors_device(calls):
+    class Stream:
+        cuda_stream, device_index = 0, 1
+    for name, ok in _arguments().items():
+        with pytest.raises(ValueError):
+            getattr(sv, name)(**ok, **REST[name], stream=Stream())
+    assert calls == []
+
+
+def test_workspace_is_checked_before_the_launch(calls):
+    import torch
+    ok = _arguments()["kv_q8_attention"]
+    w = torch.zeros(1 << 10, dtype=torch.uint8)
+    for err, bad in [(ValueError, w), (ValueError, OnDevice(w[::2])), (TypeError, OnDevice(w.int())),
+                     (ValueError, OnDevice(w.view(32, 32))), (ValueError, OnDevice(w, 1))]:
+        with pytest.raises(err):
+            sv.kv_q8_attention(**{**ok, "workspace": bad})
+    assert calls == []
