@@ -381,15 +381,17 @@ _capturing = _current_device = None
 
 
 def _ready() -> ctypes.CDLL:
-    """The library, with the torch names of this section set."""
+    """The library, with the torch names of this section set. The calls test _int32: it is set
+    last, so that another thread's call meanwhile comes here too and finds nothing half set."""
     global _int32, _float32, _bfloat16, _e4m3, _uint8, _raw_current, _capturing, _current_device
     import torch
-    _int32, _float32, _uint8 = torch.int32, torch.float32, torch.uint8
-    _bfloat16 = torch.bfloat16
+    _float32, _bfloat16, _uint8 = torch.float32, torch.bfloat16, torch.uint8
     _e4m3, _raw_current = torch.float8_e4m3fn, torch._C._cuda_getCurrentRawStream
     _capturing = torch._C._cuda_isCurrentStreamCapturing
     _current_device = torch._C._cuda_getDevice
-    return lib()
+    L = lib()
+    _int32 = torch.int32
+    return L
 
 
 def _place(t, name):
@@ -478,7 +480,8 @@ def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int 
         raise ValueError(f"k and v must be [B, T, {H}, {D}] and block_table [B, max_blocks]")
     st = L.kv_q8_append(
         kp, vp, SPEC_BF16 if k.dtype is _bfloat16 else _dtype_code(k), pool, scales, bt,
-        _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), NB, NL, layer, H, D, bs, B, T, MB,
+        _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), NB, NL, layer, H, D,
+        bs, B, T, MB,
         _raw_stream(stream, dev), _word(err_flag, "err_flag", dev))
     if st != SPEC_OK:
         raise SpecError("kv_q8_append", st)

@@ -22,6 +22,26 @@ def workspaces(monkeypatch):
     return kept, state, torch.device("cpu")
 
 
+def test_first_call_sets_the_tested_name_last(monkeypatch):
+    """Calls of other threads while one loads the library: what they test is set once everything
+    that they use is."""
+    names = ("_int32", "_float32", "_bfloat16", "_e4m3", "_uint8", "_raw_current", "_capturing",
+             "_current_device", "_lib")
+    for n in names:
+        monkeypatch.setattr(sv, n, None, raising=False)
+    load = sv.lib
+
+    def slow():
+        assert sv._int32 is None
+        library = load()
+        assert sv._int32 is None
+        return library
+
+    monkeypatch.setattr(sv, "lib", slow)
+    assert sv._ready() is sv._lib
+    assert all(getattr(sv, n) is not None for n in names)
+
+
 SMALL, LARGE = (1, 4, 2, 64), (32, 4, 2, 128)
 
 
