@@ -237,6 +237,81 @@ def test_free_errors_change_nothing():
     assert run(list(range(8)), ft=base["nb"] - 1) == pages.BAD_BLOCK
 
 
+# ------------------------------------------------------------------ long lists
+# Lists above 8192 entries are planned by a cluster of CTAs, above 65536 in several rounds.
+LONG = [(20, 900), (70, 2048)]
+
+
+def _changed(s, **kw):
+    s = {k: np.copy(v) if isinstance(v, np.ndarray) else v for k, v in s.items()}
+    for k, (at, v) in kw.items():
+        s[k][at] = v
+    return s
+
+
+@pytest.mark.parametrize("rows,blocks", LONG)
+def test_reserve_long_lists(rows, blocks):
+    sv = gpu_lib()
+    rng = np.random.default_rng(rows)
+    bs = 2
+    lengths = rng.integers(0, 9, rows)
+    s = _state(rng, lengths, bs, blocks, rows * blocks)
+    for b in range(0, rows, 3):   # entries that hold a block already, here and there
+        for j in rng.integers(6, blocks - 8, 20):
+            if s["bt"][b, j] == -1:
+                s["ft"] -= 1
+                s["bt"][b, j] = s["fs"][s["ft"]]
+    n = bs * (blocks - 6)
+    assert _reserve(sv, s, n, bs)["err"] == 0
+    assert _reserve(sv, s, 0, bs, rng.integers(0, n + 1, rows))["err"] == 0
+    last = (rows - 1, blocks - 8)
+    assert _reserve(sv, _changed(s, bt=(last, s["nb"])), n, bs)["err"] == pages.BAD_BLOCK
+    assert _reserve(sv, _changed(s, sl=(rows - 1, -1)), n, bs)["err"] == pages.BAD_LENGTH
+    assert _reserve(sv, dict(s, ft=rows * (blocks - 40)), n, bs)["err"] == pages.NO_SPACE
+    assert _reserve(sv, _changed(s, fs=(s["ft"] - 9000, -1)), n, bs)["err"] == pages.BAD_BLOCK
+
+
+@pytest.mark.parametrize("children,blocks", LONG)
+def test_fork_long_lists(children, blocks):
+    sv = gpu_lib()
+    rng = np.random.default_rng(children)
+    bs, parents = 2, 3
+    lengths = [2 * blocks - 1, 2 * blocks, 2 * blocks - 301] + [0] * children
+    s = _state(rng, lengths, bs, blocks, children + 3)
+    src, dst = rng.integers(0, parents, children), parents + rng.permutation(children)
+    small = dict(layers=1, H=1)
+    assert _fork(sv, s, src, dst, bs, **small)["err"] == 0
+    assert pages.BAD_SLOT == _fork(sv, s, src, np.append(dst[:-1], dst[0]), bs, **small)["err"]
+    assert pages.BAD_SLOT == _fork(sv, s, np.append(src[:-1], dst[0]), dst, bs, **small)["err"]
+    row, late = int(src[-1]), blocks - 200
+    for kw in (dict(bt=((row, late), s["nb"])), dict(bt=((int(dst[-1]), late), 0))):
+        assert _fork(sv, _changed(s, **kw), src, dst, bs, **small)["err"] == pages.BAD_BLOCK
+    assert _fork(sv, dict(s, ft=3), src, dst, bs, **small)["err"] == pages.NO_SPACE
+    assert _fork(sv, _changed(s, fs=(s["ft"] - 2, -1)), src, dst, bs, **small)["err"] == \
+        pages.BAD_BLOCK
+
+
+@pytest.mark.parametrize("children,blocks", LONG)
+def test_free_long_lists(children, blocks):
+    sv = gpu_lib()
+    rng = np.random.default_rng(children)
+    s = _shared(rng, 4, children, 2, blocks, 3)
+    n = 4 + children
+    rows = rng.permutation(n)
+    assert _free(sv, s, rows)["err"] == 0
+    assert _free(sv, s, rows[:n - 3])["err"] == 0
+    # the undo of claims and counts
+    assert _free(sv, s, np.append(rows[:-1], rows[0]))["err"] == pages.BAD_SLOT
+    assert _free(sv, s, np.append(rows[:-1], n))["err"] == pages.BAD_SLOT
+    held = int(s["bt"][rows[-1]][0])
+    assert held >= 0
+    assert _free(sv, _changed(s, refs=(held, 0)), rows)["err"] == pages.BAD_BLOCK
+    assert _free(sv, _changed(s, bt=((rows[-1], blocks - 1), s["nb"])), rows)["err"] == \
+        pages.BAD_BLOCK
+    assert _free(sv, _changed(s, sl=(rows[-1], -2)), rows)["err"] == pages.BAD_LENGTH
+    assert _free(sv, dict(s, ft=s["nb"] - 5), rows)["err"] == pages.BAD_BLOCK
+
+
 def test_a_shared_prefix_lives_until_its_last_holder():
     """reserve, append, fork, attend and free together: children read their parent's tokens."""
     import torch
