@@ -426,11 +426,12 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
  * invalid, gets NaN, and the bit is set in *err_flag. Scores, maxima and sums are
  * fp32. With bf16 queries, head_dim 64 or 128 and blocks of 8, 16, 32, 64 tokens or a
  * multiple of 128, the products run on the tensor cores: queries enter as two e4m3
- * terms (exact for numbers down to 2^-10 of their row's largest), probabilities as
- * three e5m2 terms: 9 bits, in steps of 2^-24 of the row's reference at least (what a key
- * contributes, probability times V scale, against about the largest of the row's keys).
- * Keys below 2^-16 of the reference go up or down to a step by turns of their position, so
- * that many of them lose nothing together. Everything else runs in fp32.
+ * terms (exact for numbers down to 2^-9 of their row's largest, smaller ones off by up to
+ * 2^-17 of it), probabilities as three e5m2 terms: 9 bits, in steps of 2^-24 of the row's
+ * reference at least (what a key contributes, probability times V scale, against about
+ * the largest of the row's keys). Keys below 2^-16 of the reference go up or down to a
+ * step by turns of their position, so that many of them lose nothing together.
+ * Everything else runs in fp32.
  */
 int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
                     const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,

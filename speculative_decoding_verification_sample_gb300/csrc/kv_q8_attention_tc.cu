@@ -11,7 +11,7 @@
 // of S^T, so scaling costs one product for K's and is folded into the
 // probabilities for V's.
 //   Queries: each row is scaled by a power of two to [128, 256) and split into two
-// e4m3 terms (4 + 4 bits: a bf16 number exactly, down to 2^-10 of the row's
+// e4m3 terms (4 + 4 bits: a bf16 number exactly, down to 2^-9 of the row's
 // largest). Probabilities: p is rounded to 9 bits (2^-9 relative) and split
 // into three e5m2 terms of at most 3 bits, exactly; e5m2 is the upper byte of
 // fp16, so a term is a byte of the fp16 number and the rest one subtraction.
@@ -119,7 +119,7 @@ struct TcShape {
   // The three terms of P side by side as one operand of three times the columns: V is
   // read once instead of three times, and O's three parts are summed at the end.
   static constexpr int kTerms = NR <= 48 ? 3 : 1;
-  static constexpr int kSBufs = (2 + kTerms) * NO <= 256 ? 2 : 1;
+  static constexpr int kSBufs = 2;  // buffers of scores
   static constexpr int kCols = (kSBufs + kTerms) * NO;
   static constexpr int kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static constexpr size_t kBytes = size_t(kSlots) * kSlot + kSmall;
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
 
 #pragma unroll 1
       for (; j < j_end; ++j) {
-        const int se = j % kTcScaleRing, sb = SB == 2 ? j & 1 : 0;
+        const int se = j % kTcScaleRing, sb = j & 1;
         tc_wait(&sh.scales_full[se], j / kTcScaleRing & 1, &sh.abort, a.err);
         const float vs = sh.vs[se][page];
         float ks = sh.ks[se][page];
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
                            g.rb * a.rows_per_block + col0, W,
                            a.tree ? sh.row_mask[qb] + col0 : nullptr, sh.row_t[qb] + col0,
                            info.x + key);
-        tc_wait(&sh.s_full[sb], (SB == 2 ? j >> 1 : j) & 1, &sh.abort, a.err);
+        tc_wait(&sh.s_full[sb], (j >> 1) & 1, &sh.abort, a.err);
         tc_fence_after();
         const uint32_t s_addr = lane_addr + sb * NO;
         // s k c (- m) of N eights of rows from the x-th
@@ -651,9 +651,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         };
         using One = std::integral_constant<int, 1>;
         using Two = std::integral_constant<int, 2>;
-        // With few rows the exponents stay in registers between the test of the references
-        // and the exponentials. With 24 or 32 rows a thread they do not fit beside the sums
-        // (a spill goes to L2: shared memory takes L1's place), and are taken twice.
+        // Up to 24 rows a thread the exponents stay in registers between the test of the
+        // references and the exponentials. 32 do not fit beside the sums (a spill goes to L2:
+        // shared memory takes L1's place), and are taken twice.
         constexpr bool kKeep = W <= 24;
         float2 y[kKeep ? W / 2 : 1];
         auto all_exponents = [&](const float* minus) {

@@ -348,6 +348,34 @@ def test_attention_softmax_scale_and_small_queries():
     assert _attn_same(sv, c) == 0
 
 
+@pytest.mark.parametrize("D,T", [(128, 1), (64, 5), (128, 16)])
+@pytest.mark.parametrize("largest", [1.0, 1.9921875])
+@pytest.mark.parametrize("e", [-3, -8, -9, -10, -11, -14])
+def test_attention_small_query_numbers(D, T, largest, e):
+    """Numbers down to 2^-9 of their row's largest are exact, smaller ones are off by up to 2^-17
+    of it. The score, 2, is the difference of two products of 256."""
+    import torch
+    sv = gpu_lib()
+    y = 2.0 ** e
+    x = y * (1 + 2.0 ** -7)
+    q = np.zeros((1, T, 4, D))
+    q[..., 0], q[..., 1], q[..., 2] = largest, x, y
+    pool = np.zeros((1, 1, 2, 1, 64, D), np.uint8)
+    pool[0, 0, 0, 0, 1, 1:3] = q8.encode(np.array([256.0, -256.0]))
+    pool[0, 0, 1, 0, 1] = q8.encode(256.0)
+    scales = np.ones((1, 1, 2, 1))
+    scales[0, 0, 0] = 2.0 ** -e
+    out = torch.empty((1, T, 4, D), dtype=torch.bfloat16, device="cuda")
+    sv.kv_q8_attention(torch.from_numpy(q).bfloat16().cuda(), dev_pool(pool), dev_scales(scales),
+                       i32([[0]]), i32([1]), out, softmax_scale=1.0, num_new=i32([1]))
+    got = out.double().cpu().numpy()[0, 0]
+    # keys of scores 0 and 2, values 0 and 256
+    off = 0.0 if y >= 2.0 ** -9 * largest else 2 * 256 * 2.0 ** -e * largest * 2.0 ** -17
+    lo, hi = (256 / (1 + np.exp(-(2 + d))) for d in (-off, off))
+    tol = 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -16
+    assert np.all(got >= lo * (1 - tol)) and np.all(got <= hi * (1 + tol))
+
+
 def test_attention_zero_scales():
     c = _attn_case(17, lengths=[200, 50], T=2, Hq=4, H=1, D=128, bs=16)
     c["scales"][:, :, 1] = 0.0
