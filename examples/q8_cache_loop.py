@@ -11,8 +11,10 @@ projection) decodes greedily with drafts of K tokens. Every step:
 
 After the prompts each row is forked (kv_fork), so that two candidates share its full blocks,
 and at the end all rows are released (kv_free). The drafts are the target's own next tokens
-with some replaced, so that acceptance varies; the output must not depend on them, which is
-what the script checks: it decodes once with drafts and once without (K = 0).
+with some replaced, so that acceptance varies; the output should not depend on them, which is
+what the script looks at: it decodes once with drafts and once without (K = 0). Rows may differ
+where two logits nearly tie: the scale of a block that keeps committed tokens may have grown with
+a rejected draft, which rounds the block's codes once more.
 
     python examples/q8_cache_loop.py
 """

@@ -393,6 +393,11 @@ int kv_evict_provisional(int32_t* block_table, int32_t* seq_lens, int num_blocks
  * codes are e4m3(x / scale), to nearest even; kept codes are rewritten for a scale
  * that grew. What lay at or after L_b in a block is dropped, scale included when
  * nothing lies before L_b, so rejected tokens leave no trace in a block of their own.
+ * In a block that keeps earlier tokens they do: codes that were rewritten for a larger
+ * scale, which rounds those that become subnormal, stay so after the rejection, and later
+ * tokens of that block keep the scale. A draft whose largest number is 64 times the kept
+ * ones' changes them by about 1e-5 of their norm, 512 times by 2e-4, 8192 times by 1 %
+ * (e4m3 itself rounds by 2.7 %), 65536 times by 15 %.
  * Appending the same tokens again gives the same bytes. Blocks are written by one
  * holder only: kv_fork copies the block that a row will write to.
  * Device errors (in *err_flag, when given): SPEC_DERR_BAD_LENGTH (a negative length,
@@ -415,7 +420,10 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
  *                written the new tokens; seq_lens L_b counts the tokens before them
  *   tree_mask    optional [B, T] uint32, the ancestor-only mask of a draft tree ([G]): bit s
  *                of tree_mask[b][t] lets query t see position L_b + s (its own slot included);
- *                positions before L_b are seen by all. Null: query t sees j <= L_b + t
+ *                positions before L_b are seen by all. Null: query t sees j <= L_b + t.
+ *                No commit call moves a tree's accepted path within this cache
+ *                (kv_commit_inplace truncates, kv_commit_rollback knows no scales): keep the
+ *                path's k and v and append them again at L_b, every layer, then set the length
  *   window       0, or w >= 1: query t sees only j > L_b + t - w, and the first `sinks`
  *                positions. Not together with tree_mask (SPEC_ENOTSUP)
  *   softmax_scale  > 0: out = sum_j softmax_j(softmax_scale * q . k_j) v_j over the keys seen

@@ -83,6 +83,26 @@ def test_pages_by_hand():
     assert pages.free(two, [1, 1], refs, [0, 1], fs, 2, num_blocks=6)["err"] == pages.BAD_BLOCK
 
 
+@pytest.mark.parametrize("size,least,most", [(1, 0.0, 0.0), (64, 0.0, 3e-5), (512, 5e-5, 5e-4),
+                                             (8192, 0.005, 0.03), (65536, 0.05, 0.3)])
+def test_rejected_token_leaves_its_scale(size, least, most):
+    """15 kept tokens of N(0, 1), a provisional one with a number of `size`, then the row's next
+    token in its place: the scale stays, and the kept codes stay as that scale rounds them."""
+    rng = np.random.default_rng(9)
+    kept, draft, new = (rng.normal(0, 1, (1, n, 1, 128)) for n in (15, 1, 1))
+    draft[0, 0, 0, 5] = size
+    bt, at = np.array([[0]]), np.array([15])
+    pool, scales = np.zeros((1, 1, 2, 1, 16, 128), np.uint8), np.zeros((1, 1, 2, 1))
+    pool, scales, _ = q8.append(kept, kept, pool, scales, bt, np.array([0]))
+    drafted = q8.append(draft, draft, pool, scales, bt, at)
+    after = q8.append(new, new, drafted[0], drafted[1], bt, at)
+    plain = q8.append(new, new, pool, scales, bt, at)
+    values = [q8.VALUES[x[0][0, 0, 0, 0, :15]] * x[1][0, 0, 0, 0] for x in (after, plain)]
+    assert np.array_equal(after[1], drafted[1])
+    change = np.linalg.norm(values[0] - values[1]) / np.linalg.norm(values[1])
+    assert least <= change <= most
+
+
 @pytest.mark.parametrize("bs", [1, 4, 16])
 def test_fork_and_free_leak_nothing(bs):
     """Random forks and frees: every block always has extra_refs + 1 holders or lies on the stack."""
