@@ -439,7 +439,8 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
  * reference at least (what a key contributes, probability times V scale, against about
  * the largest of the row's keys). Keys below 2^-16 of the reference go up or down to a
  * step by turns of their position, so that many of them lose nothing together.
- * Everything else runs in fp32.
+ * Everything else runs in fp32. SPEC_DERR_TIMEOUT in *err_flag: a wait in the kernel
+ * ran out after 2 s (should never happen); out is not to be used.
  */
 int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
                     const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,

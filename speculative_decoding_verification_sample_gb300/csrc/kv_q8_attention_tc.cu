@@ -95,8 +95,9 @@ struct TcShared {
   alignas(16) float ks[kTcScaleRing][kTcMaxPages], vs[kTcScaleRing][kTcMaxPages];
   int2 tile[kTcScaleRing];  // first position; whether every query sees every key
   uint64_t full[8], empty[8], scales_full[kTcScaleRing], s_full[2], s_empty[2], p_full,
-      pv_done, q_full[kTcItems], q_empty[2], item_empty[kTcItems];
+      pv_done, q_full[kTcItems], q_empty[2], item_empty[kTcItems], drained;
   int64_t warp_sum[16];
+  int issued[8];  // the last index of the ring that was copied to each slot, -1: none
   uint32_t tmem;
   int abort;
 };
@@ -140,15 +141,21 @@ struct TcRing {
   }
 };
 
-// Bounded wait. Once one has given up, every wait returns at once: the roles
-// run out their loops (the barriers among the softmax threads stay matched),
-// the error bit is set and the outputs are not to be used. The loop is a function of
-// its own: inlined at every wait it made the hot code outgrow the instruction caches
-// (256 rows of 512-4096 tokens, 20 query rows: 284 us inlined, 242 us so).
+// Bounded wait. Once one has given up, every one that would wait returns at once, and what
+// it was for may not be there. The copies and the preparation of queries end then, before
+// a false completion lets them write to memory in use; the products run out their loop,
+// the softmax groups the item that they have (the barriers among them have to stay
+// matched). What is in flight ends before the CTA does, the error bit is set and the
+// outputs are not to be used. The loop is a function of its own: inlined at every wait it
+// made the hot code outgrow the instruction caches (256 rows of 512-4096 tokens, 20 query
+// rows: 223 us inlined, 207 us so).
+__device__ __forceinline__ bool tc_aborted(const int* abort) {
+  return *reinterpret_cast<const volatile int*>(abort) != 0;
+}
 __device__ __noinline__ void tc_wait_long(uint64_t* bar, uint32_t parity, int* abort, int32_t* err) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (*reinterpret_cast<volatile int*>(abort)) return;
+    if (tc_aborted(abort)) return;
     if (mbar_try_wait(bar, parity, kSuspendNs)) return;
     if (global_ns() - t0 > kWaitNs) break;
   }
@@ -382,6 +389,8 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     }
     mbar_init(&sh.p_full, S::kSoftmax);
     mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < 8; ++i) sh.issued[i] = -1;
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -417,6 +426,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       if (!first) {
         tc_wait(&sh.q_empty[qbuf.at], qbuf.phase ^ 1, &sh.abort, a.err);
         tc_wait(&sh.item_empty[item.at], item.phase ^ 1, &sh.abort, a.err);
+        if (__any_sync(0xffffffffu, tc_aborted(&sh.abort))) break;
       }
       prepare_rows<NR, D>(a, sh, g, q_s + qbuf.at * S::kQ, item.at, w, n);
       fence_async_smem();
@@ -468,7 +478,11 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       const int i = is_v ? 2 * j + (j + 1 < tiles ? 2 : 1) : max(0, 2 * j - 1);
       const int slot = i % NS;
       tc_wait(&sh.empty[slot], ((i / NS) & 1) ^ 1, &sh.abort, a.err);
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+      if (__any_sync(0xffffffffu, tc_aborted(&sh.abort))) break;
+      if (lane == 0) {
+        sh.issued[slot] = i;
+        mbar_arrive_expect_tx(&sh.full[slot], bytes);
+      }
       __syncwarp();
       if (ok)
         tma_tile_3d(sm + slot * S::kSlot + lane * bs * D, &map, 0, c1, plane + (is_v ? a.H : 0),
@@ -494,10 +508,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       else mbar_arrive(&sh.scales_full[sring.at]);
       sring.next();
     }
-    // the last copies land before the CTA may leave
-    if (is_v)
-      for (int x = max(0, 2 * tiles - NS); x < 2 * tiles; ++x)
-        tc_wait(&sh.full[x % NS], (x / NS) & 1, &sh.abort, a.err);
+    cp_async_wait_all();  // (done with already, unless the loop was left)
   } else if (work && warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       const Segment& g = sh.seg[qb];  // read where it is needed: registers are scarce here
       const int j_first = j, j_end = j + (g.t1 - g.t0);
       if (key < W) nm[key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
-      bar_group(group);
+      if (bar_group_or(group, tc_aborted(&sh.abort))) break;  // the item may never be described
       float2 l[W / 2];
 #pragma unroll
       for (int r = 0; r < W / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
@@ -889,6 +900,19 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
+  if (sh.abort) {
+    // nothing more is issued: what is in flight ends before the CTA's memory is another's
+    if (warp == kTmaWarp)
+      for (int x = 0; x < NS; ++x)
+        if (sh.issued[x] >= 0) mbar_wait(&sh.full[x], (sh.issued[x] / NS) & 1);
+    if (warp == kMmaWarp) {
+      if (lane == 0) tc_commit(&sh.drained);
+      __syncwarp();
+      mbar_wait(&sh.drained, 0);
+      __syncwarp();  // the warp frees the TMEM as one
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, S::kAlloc);
 }
