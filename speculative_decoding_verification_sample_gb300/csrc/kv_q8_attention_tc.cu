@@ -29,23 +29,23 @@
 // 7.75: then O and l are rescaled once; otherwise a tile costs no reduction over its
 // keys. l stays per thread (one key of every tile) until the item ends.
 //
-//
 // Roles: one or two groups of 4 softmax warps (thread = key of the tile, each group
 // its own query rows), two copy warps, an MMA warp and a warp that prepares the next
 // item's queries. K and V tiles share one ring of slots, released separately. Two
 // CTAs per SM hide each other's latencies.
 //
 // Bound by memory up to 24 query rows of a kv head: 256 rows of 512-4096 tokens, 8 kv
-// heads x 128, 20 query rows, 1.23 GB: 203 us = 6.1 TB/s (0.90 of the copy peak); 8 rows
-// 195 us; 2 rows of 100-131 thousand tokens 85 us (5.6 TB/s). Beyond that by the
-// softmax warps' instructions (about 11 for each 32 scores): 32 rows 215 us, 48 rows
-// 270 us; a window of 4096 over 56 rows 132 us (3.1 TB/s). Short rows (100-600 tokens)
-// by the changes of items: 77 us, 48 query rows 127 us (94 and 166 before the queries were
-// prepared two items ahead and in fewer steps). The steps that mattered:
+// heads x 128, 20 query rows, 1.23 GB: 207 us = 6.0 TB/s (0.88 of the copy peak); 8 rows
+// 200 us; 2 rows of 100-131 thousand tokens 84 us (5.6 TB/s). With D = 64 and beyond that
+// by the softmax warps' instructions (about 12 for each 32 scores): D = 64 174 us
+// (3.6 TB/s), 32 rows 222 us, 48 rows 293 us, 64 rows 376 us; a window of 4096 over 56 rows
+// 134 us (3.1 TB/s). Short rows (100-600 tokens) by the changes of items: 82 us, 48 query
+// rows 125 us (94 and 166 before the queries were prepared two items ahead and in fewer
+// steps). The steps that mattered:
 // the hot loop must stay small (waits out of line, one copy of each block of code:
 // 334 to 242 us for the 20-row case), the copies of 16-token blocks need two warps,
 // an item's queries must be converted before it begins (230 to 206 us), an item's end
-// reads its shared memory before its first store (206 to 203 us), and nothing may go
+// reads its shared memory before its first store (3 us), and nothing may go
 // through local memory, which this much shared memory pushes out to L2.
 // Not kept, for the 20-row case: two groups taking the tiles in turn (374 us), three
 // CTAs per SM with short rings (351 us), tiles called into L2 ahead of the copies
