@@ -97,9 +97,10 @@ extern "C" {
                                     the launch drains and unfinished rows' outputs are not
                                     written. Failure-detection tests provoke it with the
                                     environment knobs SPECVERIFY_STALL_ROW=b (every stage
-                                    arrival of batch row b is withheld) and
-                                    SPECVERIFY_IDLE_NS (the producers' idle limit, default
-                                    2 s), read at every verify launch */
+                                    arrival of batch row b is withheld; in kv_q8_attention
+                                    its V tiles) and SPECVERIFY_IDLE_NS (the limit of the
+                                    producers' idle wait and of the attention's waits,
+                                    default 2 s), read at every verify and attention launch */
 #define SPEC_DERR_BAD_SLOT 128   /* kv: a slot_map entry of a kept position outside [0, K], or a
                                     row of kv_fork / kv_free out of range or listed twice */
 #define SPEC_DERR_VALUE 256      /* kv_q8_append: a NaN (stored as 0) or an infinity (stored as the

@@ -13,7 +13,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
-
+#include <cstdlib>
 
 #include "../../include/specverify.h"
 #include "launch.h"
@@ -287,6 +287,22 @@ int launch_any(const AttnArgs& a, int nc, void* stream) {
                     static_cast<cudaStream_t>(stream), a);
 }
 
+// Failure-detection test knobs, as the verification kernels have them, read at every launch:
+// SPECVERIFY_STALL_ROW=b withholds the V tiles of batch row b, so that the tensor-core
+// kernel's waits run out; SPECVERIFY_IDLE_NS shortens their limit.
+void set_test_knobs(AttnArgs& a) {
+  a.wait_ns = kWaitNs;
+  a.stall_row = -1;
+  const char* row = std::getenv("SPECVERIFY_STALL_ROW");
+  if (!row) return;
+  const long b = std::strtol(row, nullptr, 10);
+  if (b >= 0 && b < a.B) a.stall_row = int(b);
+  if (const char* ns = std::getenv("SPECVERIFY_IDLE_NS")) {
+    const long long v = std::strtoll(ns, nullptr, 10);
+    if (v > 0 && uint64_t(v) < kWaitNs) a.wait_ns = uint64_t(v);
+  }
+}
+
 }  // namespace
 
 // Enough for either kernel on any part of this family: at most kAttnMaxCtas
@@ -324,6 +340,7 @@ int launch_kv_q8_attention(const Q8AttnLaunch& k) {
   a.block_scales = int64_t(k.num_layers) * 2 * k.H;
   a.R = k.T * k.G;
   a.err = k.err;
+  set_test_knobs(a);
   a.plane0 = k.layer * 2 * k.H;
   a.planes_per_block = k.num_layers * 2 * k.H;
   const int sms = sm_count();

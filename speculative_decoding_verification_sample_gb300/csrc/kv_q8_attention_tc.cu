@@ -80,6 +80,14 @@ constexpr float kTcVDown = 0.5f;
 constexpr float kTcMaxSum = 0x1.fffffep126f;
 constexpr int kTcSmem = 113 * 1024 - 512;   // of one CTA, two per SM
 
+struct TcGuard {
+  uint64_t limit_ns;  // of a wait
+  int abort;          // one has run out
+  __device__ __forceinline__ bool aborted() const {
+    return *reinterpret_cast<const volatile int*>(&abort) != 0;
+  }
+};
+
 template <int NR>
 struct TcShared {
   alignas(16) float row_c[kTcItems][NR];  // query row's scale * softmax_scale * log2(e)
@@ -99,7 +107,7 @@ struct TcShared {
   int64_t warp_sum[16];
   int issued[8];  // the last index of the ring that was copied to each slot, -1: none
   uint32_t tmem;
-  int abort;
+  TcGuard guard;
 };
 
 // Softmax threads: one group of 128 (a thread a key) up to 24 rows, beyond that two
@@ -149,21 +157,20 @@ struct TcRing {
 // outputs are not to be used. The loop is a function of its own: inlined at every wait it
 // made the hot code outgrow the instruction caches (256 rows of 512-4096 tokens, 20 query
 // rows: 223 us inlined, 207 us so).
-__device__ __forceinline__ bool tc_aborted(const int* abort) {
-  return *reinterpret_cast<const volatile int*>(abort) != 0;
-}
-__device__ __noinline__ void tc_wait_long(uint64_t* bar, uint32_t parity, int* abort, int32_t* err) {
+__device__ __noinline__ void tc_wait_long(uint64_t* bar, uint32_t parity, TcGuard* guard,
+                                          int32_t* err) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (tc_aborted(abort)) return;
+    if (guard->aborted()) return;
     if (mbar_try_wait(bar, parity, kSuspendNs)) return;
-    if (global_ns() - t0 > kWaitNs) break;
+    if (global_ns() - t0 > guard->limit_ns) break;
   }
-  *reinterpret_cast<volatile int*>(abort) = 1;
+  *reinterpret_cast<volatile int*>(&guard->abort) = 1;
   if (err) atomicOr(err, SPEC_DERR_TIMEOUT);
 }
-__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, int* abort, int32_t* err) {
-  if (!mbar_try_wait(bar, parity, kSuspendNs)) tc_wait_long(bar, parity, abort, err);
+__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, TcGuard* guard,
+                                        int32_t* err) {
+  if (!mbar_try_wait(bar, parity, kSuspendNs)) tc_wait_long(bar, parity, guard, err);
 }
 
 // Barriers of one softmax group (ids 1 and 2).
@@ -391,7 +398,8 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.drained, 1);
     for (int i = 0; i < 8; ++i) sh.issued[i] = -1;
-    sh.abort = 0;
+    sh.guard.abort = 0;
+    sh.guard.limit_ns = a.wait_ns;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -424,9 +432,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     int w = warp < kTmaWarp ? warp : warp - 3, n = S::kSoftmax / 32 + 1;
     for (bool first = true;; first = false) {
       if (!first) {
-        tc_wait(&sh.q_empty[qbuf.at], qbuf.phase ^ 1, &sh.abort, a.err);
-        tc_wait(&sh.item_empty[item.at], item.phase ^ 1, &sh.abort, a.err);
-        if (__any_sync(0xffffffffu, tc_aborted(&sh.abort))) break;
+        tc_wait(&sh.q_empty[qbuf.at], qbuf.phase ^ 1, &sh.guard, a.err);
+        tc_wait(&sh.item_empty[item.at], item.phase ^ 1, &sh.guard, a.err);
+        if (__any_sync(0xffffffffu, sh.guard.aborted())) break;
       }
       prepare_rows<NR, D>(a, sh, g, q_s + qbuf.at * S::kQ, item.at, w, n);
       fence_async_smem();
@@ -461,6 +469,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     TcRing<kTcScaleRing> sring;
     int id = page_id(k);
     for (int j = 0; j < tiles; ++j) {
+      if (is_v && g.b == a.stall_row) break;
       const int cur = id;
       const bool ok = cur >= 0 && cur < a.NB;
       const int p0 = tile_start(g.s, k);
@@ -477,8 +486,8 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, ok)) * uint32_t(bs) * D;
       const int i = is_v ? 2 * j + (j + 1 < tiles ? 2 : 1) : max(0, 2 * j - 1);
       const int slot = i % NS;
-      tc_wait(&sh.empty[slot], ((i / NS) & 1) ^ 1, &sh.abort, a.err);
-      if (__any_sync(0xffffffffu, tc_aborted(&sh.abort))) break;
+      tc_wait(&sh.empty[slot], ((i / NS) & 1) ^ 1, &sh.guard, a.err);
+      if (__any_sync(0xffffffffu, sh.guard.aborted())) break;
       if (lane == 0) {
         sh.issued[slot] = i;
         mbar_arrive_expect_tx(&sh.full[slot], bytes);
@@ -526,9 +535,9 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
       uint32_t p_phase = 0;
       auto scores = [&]() {  // returns whether the tile is its item's first
         const bool first = k == g.t0;
-        if (first) tc_wait(&sh.q_full[item.at], item.phase, &sh.abort, a.err);
-        tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
-        tc_wait(&sh.s_empty[sbuf.at], sbuf.phase ^ 1, &sh.abort, a.err);
+        if (first) tc_wait(&sh.q_full[item.at], item.phase, &sh.guard, a.err);
+        tc_wait(&sh.full[ring.at], ring.phase, &sh.guard, a.err);
+        tc_wait(&sh.s_empty[sbuf.at], sbuf.phase ^ 1, &sh.guard, a.err);
         tc_fence_after();
         const uint64_t k_desc = slot0 + ring.at * (S::kSlot / 16);
         const uint64_t q_desc = q0 + qbuf.at * (S::kQ / 16);
@@ -553,8 +562,8 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         return first;
       };
       auto outputs = [&](bool first) {
-        tc_wait(&sh.full[ring.at], ring.phase, &sh.abort, a.err);
-        tc_wait(&sh.p_full, p_phase, &sh.abort, a.err);
+        tc_wait(&sh.full[ring.at], ring.phase, &sh.guard, a.err);
+        tc_wait(&sh.p_full, p_phase, &sh.guard, a.err);
         p_phase ^= 1;
         tc_fence_after();
         // V as stored: D contiguous, groups of 8 keys 8 D bytes apart. With D = 64 the
@@ -594,15 +603,15 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
     TcRing<kTcItems> item;
     int j = 0;  // tile of the CTA
     auto wait_outputs = [&]() {  // of the tile before
-      tc_wait(&sh.pv_done, (j & 1) ^ 1, &sh.abort, a.err);
+      tc_wait(&sh.pv_done, (j & 1) ^ 1, &sh.guard, a.err);
     };
     for (;; item.next()) {
       const int qb = item.at;
-      tc_wait(&sh.q_full[qb], item.phase, &sh.abort, a.err);
+      tc_wait(&sh.q_full[qb], item.phase, &sh.guard, a.err);
       const Segment& g = sh.seg[qb];  // read where it is needed: registers are scarce here
       const int j_first = j, j_end = j + (g.t1 - g.t0);
       if (key < W) nm[key] = sh.row_off[qb][col0 + key] >= 0 ? kTcUnset : 0.0f;
-      if (bar_group_or(group, tc_aborted(&sh.abort))) break;  // the item may never be described
+      if (bar_group_or(group, sh.guard.aborted())) break;  // the item may never be described
       float2 l[W / 2];
 #pragma unroll
       for (int r = 0; r < W / 2; ++r) l[r] = make_float2(0.0f, 0.0f);
@@ -610,7 +619,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
 #pragma unroll 1
       for (; j < j_end; ++j) {
         const int se = j % kTcScaleRing, sb = j & 1;
-        tc_wait(&sh.scales_full[se], j / kTcScaleRing & 1, &sh.abort, a.err);
+        tc_wait(&sh.scales_full[se], j / kTcScaleRing & 1, &sh.guard, a.err);
         const float vs = sh.vs[se][page];
         float ks = sh.ks[se][page];
         const int2 info = sh.tile[se];
@@ -625,7 +634,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
                            g.rb * a.rows_per_block + col0, W,
                            a.tree ? sh.row_mask[qb] + col0 : nullptr, sh.row_t[qb] + col0,
                            info.x + key);
-        tc_wait(&sh.s_full[sb], (j >> 1) & 1, &sh.abort, a.err);
+        tc_wait(&sh.s_full[sb], (j >> 1) & 1, &sh.guard, a.err);
         tc_fence_after();
         const uint32_t s_addr = lane_addr + sb * NO;
         // s k c (- m) of N eights of rows from the x-th
@@ -806,7 +815,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         }
         if (!open && group == 0 && (!(ks == ks) || !needed(g.s, info.x + key, 1))) {
           const int vi = 2 * j + (j + 1 < tiles ? 2 : 1);  // loads before it: j or j + 1 of K
-          tc_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, a.err);
+          tc_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.guard, a.err);
           clear_row<D>(sm + vi % NS * S::kSlot, key);
         }
         fence_async_smem();
@@ -900,7 +909,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (sh.abort) {
+  if (sh.guard.abort) {
     // nothing more is issued: what is in flight ends before the CTA's memory is another's
     if (warp == kTmaWarp)
       for (int x = 0; x < NS; ++x)

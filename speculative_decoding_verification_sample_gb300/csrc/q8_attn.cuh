@@ -46,6 +46,8 @@ struct AttnArgs {
   float2* stats;              // [2 NC][rows_per_block] (maximum in log2 units, sum)
   int4* joins;                // [NC] (item row, kv head, row block, first CTA); x < 0: none
   int32_t* err;
+  uint64_t wait_ns;           // limit of a wait of the tensor-core kernel
+  int stall_row;              // -1, or the row whose V tiles are withheld (a test)
   int plane0;                 // tensor-map plane index of (block 0, this layer, keys, head 0)
   int planes_per_block;       // planes from block to block
 };

@@ -141,6 +141,8 @@ void test(int seed, int T, int G, bool stall) {
   a.stats = static_cast<float2*>(guarded(2 * ctas * a.R * 8));
   a.joins = static_cast<int4*>(guarded(ctas * 16));
   a.err = &err;
+  a.wait_ns = kWaitNs;
+  a.stall_row = -1;
   a.planes_per_block = 2 * H;
   box_bytes = bs * D;
   shared_bytes = S::kBytes;

@@ -564,6 +564,40 @@ def test_attention_workspace_is_allocated_in_its_streams_order():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("T,G,D,rows,stall", [
+    (5, 4, 128, 8, 3), (5, 4, 64, 8, 0), (12, 4, 128, 8, 7), (16, 4, 128, 8, 3), (8, 4, 128, 8, 0),
+    (16, 4, 64, 8, 2), (1, 1, 128, 8, 2), (16, 4, 128, 160, 80), (12, 4, 128, 160, 5)])
+def test_attention_wait_runs_out(monkeypatch, T, G, D, rows, stall):
+    """SPECVERIFY_STALL_ROW withholds a row's V tiles: the waits of the CTAs that have it run out
+    (after 5 ms instead of 2 s), the call ends and reports it, and the CTAs that work on other
+    rows are not concerned. The next call is as ever."""
+    import torch
+    sv = gpu_lib()
+    rng = np.random.default_rng(30)
+    top = 3000 if rows < 100 else 700
+    c = _attn_case(30, lengths=[int(x) for x in rng.integers(top // 2, top, rows)], T=T, Hq=8 * G,
+                   H=8, D=D, bs=16, layers=1, layer=0)
+    want, hurt, again = (torch.empty((rows, T, 8 * G, D), dtype=torch.bfloat16, device="cuda")
+                         for _ in range(3))
+    _attend(sv, c, want)
+    err = i32([0])
+    torch.cuda.synchronize()
+    monkeypatch.setenv("SPECVERIFY_STALL_ROW", str(stall))
+    monkeypatch.setenv("SPECVERIFY_IDLE_NS", "5000000")
+    sv.kv_q8_attention(*c["dev"], hurt, layer=c["layer"], err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == sv.SPEC_DERR_TIMEOUT
+    # a CTA has less than a row
+    far = [b for b in range(rows) if abs(b - stall) > 1]
+    assert torch.equal(hurt[far], want[far])
+    monkeypatch.delenv("SPECVERIFY_STALL_ROW")
+    monkeypatch.delenv("SPECVERIFY_IDLE_NS")
+    err.zero_()
+    sv.kv_q8_attention(*c["dev"], again, layer=c["layer"], err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(again, want)
+
+
 def test_binding_refuses():
     import torch
     sv = gpu_lib()
