@@ -13,7 +13,9 @@
  *   - kv_q8_append, kv_q8_attention: the cache in e4m3 with a scale for each
  *     block of tokens and head, and the attention of the provisional tokens;
  *   - kv_reserve, kv_fork, kv_free: blocks for new tokens, rows that share
- *     their prefix with another row, and their release.
+ *     their prefix with another row, and their release;
+ *   - qk_norm_rope, kv_q8_norm_rope_append: norms of queries and keys for each head with
+ *     rotary positions, by themselves or with keys and values written to that cache.
  *
  * Sources (page title, section):
  *   [L] aiengineeringfromscratch.com, "Speculative decoding and EAGLE-3":
@@ -409,6 +411,66 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
                  const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
                  int num_blocks, int num_layers, int layer, int num_kv_heads, int head_dim,
                  int block_size, int B, int T, int max_blocks, void* stream, int32_t* err_flag);
+
+/*
+ * qk_norm_rope - norms of queries and keys for each head, and rotary positions.
+ *
+ *   q, k         [B, T, num_q_heads (num_kv_heads), head_dim] dtype (SPEC_BF16 or SPEC_F32); a
+ *                token's heads lie side by side, q_stride (k_stride) numbers from token to
+ *                token, so q and k may be parts of one projection's output. k may be null
+ *                (with num_kv_heads 0)
+ *   q_out, k_out the same shapes and dtype, with strides of their own; they may be q and k
+ *                themselves (same address and stride), but not overlap them otherwise
+ *   q_weight, k_weight  optional [head_dim] dtype: y = x * weight / sqrt(mean(x^2) + eps) over a
+ *                head's numbers, eps >= 0; null: no norm
+ *   inv_freq     [num_pairs] float, radians a position; null with num_pairs 0 (no rotation).
+ *                2 * num_pairs <= head_dim: the numbers after the first 2 * num_pairs stay
+ *   interleaved  0: pair i is (i, i + num_pairs); else (2 i, 2 i + 1)
+ *   rope_factor  position p turns pair i by p * inv_freq[i]: (a, b) -> rope_factor *
+ *                (a cos - b sin, b cos + a sin). Scalings for long contexts are a choice of
+ *                inv_freq and rope_factor. Angles are exact to 2^-54 turns a position and
+ *                2^-25 of an eighth turn, however far the position; an |inv_freq| that is
+ *                not finite counts as 0
+ *   seq_lens     [B] int32: token t of row b is at position seq_lens[b] + t
+ *   positions    optional [B, T] int32 instead (a draft tree's: seq_lens[b] + depth);
+ *                seq_lens may then be null
+ *   num_new      optional [B] int32: tokens t >= num_new[b] are neither read nor written
+ *   head_dim     even, up to 256
+ * Everything is computed in fp32 and rounded once. Any strides and addresses that are
+ * multiples of the element size do; 16-byte (else 8-byte) ones with num_pairs a multiple of a
+ * vector's numbers take vector loads. Device errors: SPEC_DERR_BAD_LENGTH (a negative length,
+ * num_new outside [0, T]: that row is not written).
+ */
+int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int dtype,
+                 void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                 const void* q_weight, const void* k_weight, float eps, const float* inv_freq,
+                 int num_pairs, int interleaved, float rope_factor, const int32_t* seq_lens,
+                 const int32_t* positions, const int32_t* num_new, int num_q_heads,
+                 int num_kv_heads, int head_dim, int B, int T, void* stream, int32_t* err_flag);
+
+/*
+ * kv_q8_norm_rope_append - qk_norm_rope whose keys go to the 8-bit paged cache, and the
+ * values with them: q_out as from qk_norm_rope, the cache as from kv_q8_append of the keys
+ * and v, but the keys are taken in fp32 as they come from the rotation, so that they are
+ * rounded once.
+ *
+ *   v            [B, T, num_kv_heads, head_dim] dtype, v_stride numbers from token to token
+ *   kv_pool, kv_scales, block_table, layer: as kv_q8_append. head_dim a multiple of 16
+ *   seq_lens     [B] int32, not changed: the tokens' places in the cache, and their positions
+ *                for the rotation unless `positions` is given
+ * Device errors: those of kv_q8_append; a row with invalid lengths is not written, q_out
+ * included; a bad block concerns its keys and values only.
+ */
+int kv_q8_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, int dtype, void* q_out,
+                           int64_t q_out_stride, const void* q_weight, const void* k_weight,
+                           float eps, const float* inv_freq, int num_pairs, int interleaved,
+                           float rope_factor, void* kv_pool, float* kv_scales,
+                           const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* positions, const int32_t* num_new, int num_blocks,
+                           int num_layers, int layer, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int B, int T, int max_blocks,
+                           void* stream, int32_t* err_flag);
 
 /*
  * kv_q8_attention - attention of every row's newest tokens over its 8-bit paged

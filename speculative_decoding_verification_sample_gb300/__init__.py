@@ -13,6 +13,8 @@ The entry points carry the C names:
   kv_q8_append(...)         tokens into the 8-bit paged cache (e4m3, a scale per block and head)
   kv_q8_attention(...)      attention of the provisional tokens over that cache
   kv_reserve, kv_fork, kv_free   blocks for new tokens, shared prefixes, release
+  qk_norm_rope(...)         norms of queries and keys for each head, rotary positions
+  kv_q8_norm_rope_append(...)  the same with keys and values into the 8-bit cache
 See include/specverify.h for layouts, ownership and error behaviour.
 """
 from __future__ import annotations
@@ -38,7 +40,8 @@ EXPORTED = ("spec_verify_sample", "spec_verify_greedy", "spec_verify_workspace_b
             "spec_verify_greedy_noalloc", "spec_verify_greedy_noalloc_max_bytes",
             "kv_commit_inplace", "kv_evict_provisional", "spec_verify_tree_greedy",
             "spec_filter_thresholds", "kv_q8_append", "kv_q8_attention",
-            "kv_q8_attention_workspace_bytes", "kv_reserve", "kv_fork", "kv_free")
+            "kv_q8_attention_workspace_bytes", "kv_reserve", "kv_fork", "kv_free",
+            "qk_norm_rope", "kv_q8_norm_rope_append")
 
 _lib = None
 
@@ -97,6 +100,13 @@ def lib() -> ctypes.CDLL:
         L.kv_fork.restype = I
         L.kv_free.argtypes = [P, P, P, P, I, I, I, I, P, P, P, P]
         L.kv_free.restype = I
+        S = ctypes.c_int64
+        L.qk_norm_rope.argtypes = [P, S, P, S, I, P, S, P, S, P, P, F, P, I, I, F, P, P, P, I, I,
+                                   I, I, I, P, P]
+        L.qk_norm_rope.restype = I
+        L.kv_q8_norm_rope_append.argtypes = [P, S, P, S, P, S, I, P, S, P, P, F, P, I, I, F, P, P,
+                                             P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
+        L.kv_q8_norm_rope_append.restype = I
         L.spec_selftest_ex2.argtypes = [F, F, P, P]
         L.spec_selftest_ex2.restype = I
         L.spec_status_string.argtypes = [I]
@@ -487,6 +497,115 @@ def kv_q8_append(k, v, kv_pool, kv_scales, block_table, seq_lens, *, layer: int 
         raise SpecError("kv_q8_append", st)
 
 
+def _heads(t, name, dtype, dev):
+    """(pointer, numbers from token to token) of a [B, T, heads, head_dim] tensor whose tokens are
+    a constant number of elements apart and whose heads lie side by side."""
+    try:
+        if t.get_device() != dev or t.ndim != 4 or (dtype is not None and t.dtype is not dtype):
+            raise AttributeError
+    except AttributeError:
+        _arg(t, name, 4, dtype, dev)
+        raise
+    B, T, H, D = t.shape
+    s0, s1, s2, s3 = t.stride()
+    step = s1 if T > 1 else s0 if B > 1 else H * D
+    if (D > 1 and s3 != 1) or (H > 1 and s2 != D) or (T > 1 and B > 1 and s0 != T * s1) \
+            or step < H * D:
+        raise ValueError(f"{name} must be [B, T, heads, head_dim] with a token's heads side by "
+                         f"side and tokens a constant stride apart, got strides {t.stride()}")
+    return t.data_ptr(), step
+
+
+def _turning(q, q_weight, k_weight, inv_freq, positions, dev):
+    """Pointers of the weights, the frequencies (with their number) and the positions."""
+    B, T, _, D = q.shape
+
+    def weight(w, name):
+        if w is None:
+            return None
+        p = _arg(w, name, 1, q.dtype, dev)
+        if w.shape[0] != D:
+            raise ValueError(f"{name} must have {D} entries, got {w.shape[0]}")
+        return p
+
+    freq, pairs = None, 0
+    if inv_freq is not None:
+        freq, pairs = _arg(inv_freq, "inv_freq", 1, _float32, dev), inv_freq.shape[0]
+        if pairs == 0:
+            freq = None
+    pos = None
+    if positions is not None:
+        pos = _arg(positions, "positions", 2, _int32, dev)
+        if positions.shape != (B, T):
+            raise ValueError(f"positions must be [{B}, {T}], got {tuple(positions.shape)}")
+    return weight(q_weight, "q_weight"), weight(k_weight, "k_weight"), freq, pairs, pos
+
+
+def qk_norm_rope(q, k, seq_lens, q_out, k_out, *, inv_freq=None, rope_factor: float = 1.0,
+                 interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 positions=None, num_new=None, stream=None, err_flag=None) -> None:
+    """Norms (with weights [head_dim] given) and rotary positions of q [B, T, q_heads, head_dim]
+    and k [B, T, kv_heads, head_dim] (or None) into q_out and k_out, which may be q and k. The
+    tensors may be views of one projection's output. inv_freq: float32 [pairs], radians a
+    position (rope_frequencies); token t is at seq_lens[b] + t, or at positions [B, T]."""
+    L = _lib if _int32 is not None else _ready()
+    dev = _place(q, "q")
+    dt = q.dtype
+    qp, qs = _heads(q, "q", None, dev)
+    qo, qos = _heads(q_out, "q_out", dt, dev)
+    B, T, Hq, D = q.shape
+    if q_out.shape != q.shape:
+        raise ValueError(f"q_out must be {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    kp = ko = None
+    ks = kos = H = 0
+    if k is not None:
+        kp, ks = _heads(k, "k", dt, dev)
+        ko, kos = _heads(k_out, "k_out", dt, dev)
+        H = k.shape[2]
+        if k_out.shape != k.shape or tuple(k.shape) != (B, T, H, D):
+            raise ValueError(f"k and k_out must be [{B}, {T}, kv_heads, {D}]")
+    qw, kw, freq, pairs, pos = _turning(q, q_weight, k_weight, inv_freq, positions, dev)
+    st = L.qk_norm_rope(
+        qp, qs, kp, ks, SPEC_BF16 if dt is _bfloat16 else _dtype_code(q), qo, qos, ko, kos, qw, kw,
+        eps, freq, pairs, interleaved, rope_factor, _vec(seq_lens, "seq_lens", B, dev), pos,
+        _vec(num_new, "num_new", B, dev), Hq, H, D, B, T, _raw_stream(stream, dev),
+        _word(err_flag, "err_flag", dev))
+    if st != SPEC_OK:
+        raise SpecError("qk_norm_rope", st)
+
+
+def kv_q8_norm_rope_append(q, k, v, q_out, kv_pool, kv_scales, block_table, seq_lens, *,
+                           layer: int = 0, inv_freq=None, rope_factor: float = 1.0,
+                           interleaved: bool = False, q_weight=None, k_weight=None,
+                           eps: float = 1e-6, positions=None, num_new=None, stream=None,
+                           err_flag=None) -> None:
+    """qk_norm_rope of q into q_out, and of k into the 8-bit cache together with v (kv_q8_append's
+    layout and places), in one pass: the keys are rounded once."""
+    L = _lib if _int32 is not None else _ready()
+    dev = _place(q, "q")
+    dt = q.dtype
+    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales, dev)
+    qp, qs = _heads(q, "q", None, dev)
+    kp, ks = _heads(k, "k", dt, dev)
+    vp, vs = _heads(v, "v", dt, dev)
+    qo, qos = _heads(q_out, "q_out", dt, dev)
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
+    B, T, Hq, qd = q.shape
+    rows, MB = block_table.shape
+    if q_out.shape != q.shape or qd != D or rows != B or tuple(k.shape) != (B, T, H, D) \
+            or v.shape != k.shape:
+        raise ValueError(f"q and q_out must be [B, T, q_heads, {D}], k and v [B, T, {H}, {D}] and "
+                         "block_table [B, max_blocks]")
+    qw, kw, freq, pairs, pos = _turning(q, q_weight, k_weight, inv_freq, positions, dev)
+    st = L.kv_q8_norm_rope_append(
+        qp, qs, kp, ks, vp, vs, SPEC_BF16 if dt is _bfloat16 else _dtype_code(q), qo, qos, qw, kw,
+        eps, freq, pairs, interleaved, rope_factor, pool, scales, bt,
+        _vec(seq_lens, "seq_lens", B, dev), pos, _vec(num_new, "num_new", B, dev), NB, NL, layer,
+        Hq, H, D, bs, B, T, MB, _raw_stream(stream, dev), _word(err_flag, "err_flag", dev))
+    if st != SPEC_OK:
+        raise SpecError("kv_q8_norm_rope_append", st)
+
+
 def kv_q8_attention_workspace_bytes(T: int, num_q_heads: int, num_kv_heads: int,
                                     head_dim: int) -> int:
     """Device workspace bytes of kv_q8_attention (0: the call would be rejected)."""
@@ -653,6 +772,42 @@ def spec_selftest_ex2(lo: float, hi: float, *, stream=None) -> float:
 
 
 # ------------------------------------------------------------------ conveniences
+def rope_frequencies(pairs: int, base: float = 10000.0, *, scaling: str = "none",
+                     factor: float = 1.0, trained_length: int = 4096, fast_turns: float = 32.0,
+                     slow_turns: float = 1.0, device="cuda"):
+    """(inv_freq float32 [pairs], rope_factor) for qk_norm_rope: base ** (-i / pairs), scaled for
+    contexts `factor` times as long as the trained one:
+
+      "none"    as it is
+      "linear"  all frequencies / factor (positions closer together)
+      "base"    a base of base * factor ** (pairs / (pairs - 1)): the slowest pair is slowed by
+                `factor`, the fastest not at all
+      "parts"   pairs that turn at least fast_turns times in trained_length as they are, those
+                that turn at most slow_turns times / factor, those between them mixed linearly;
+                rope_factor = 0.1 ln(factor) + 1
+    """
+    import math
+    import torch
+    if pairs < 1 or not base > 0 or not factor > 0:
+        raise ValueError("pairs, base and factor must be positive")
+    by = 1.0
+    if scaling == "base":
+        base = base * factor ** (pairs / max(1, pairs - 1))
+    f = base ** (-torch.arange(pairs, dtype=torch.float64) / pairs)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if not fast_turns > slow_turns or trained_length < 1:
+            raise ValueError("fast_turns must exceed slow_turns, trained_length be positive")
+        turns = trained_length * f / (2 * math.pi)
+        keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        by = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.float().to(device), by
+
+
 def verify(target_logits, draft_logits, draft_tokens, uniforms, temperature: float, *,
            stream=None, with_info: bool = False):
     """Allocates the outputs on the logits' device and runs spec_verify_sample.

@@ -262,6 +262,122 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
   return sv::launch_kv_q8_append(a);
 }
 
+// What the two calls that norm and turn heads have in common. `tokens`: of one CTA at most.
+static int check_norm_rope(const sv::NormRopeLaunch& r, int tokens) {
+  const int eb = elem_bytes(r.dtype);
+  if (!r.q || !r.q_out || eb == 0 || r.B < 1 || r.T < 1 || r.Hq < 1 || r.H < 0) return SPEC_EINVAL;
+  if (r.D < 2 || r.D % 2 != 0 || r.half < 0 || 2 * r.half > r.D || (r.half > 0) != (r.inv_freq != nullptr))
+    return SPEC_EINVAL;
+  if (!(r.eps >= 0.0f) || std::isinf(r.eps) || !std::isfinite(r.factor)) return SPEC_EINVAL;
+  if (!r.seq_lens && (!r.positions || r.pool)) return SPEC_EINVAL;
+  if (r.D > 256 || int64_t(r.B) * r.T > INT32_MAX || r.T > (1 << 30) ||
+      int64_t(tokens) * (int64_t(r.Hq) + r.H) > INT32_MAX)
+    return SPEC_ENOTSUP;
+  const int64_t q_min = int64_t(r.Hq) * r.D, k_min = int64_t(r.H) * r.D;
+  if (r.q_stride < q_min || r.q_out_stride < q_min || r.k_stride < k_min ||
+      (r.v && r.v_stride < k_min) || (r.k_out && r.k_out_stride < k_min))
+    return SPEC_EINVAL;
+  for (const int64_t s : {r.q_stride, r.k_stride, r.v_stride, r.q_out_stride, r.k_out_stride})
+    if (s > (int64_t(1) << 31)) return SPEC_ENOTSUP;
+  for (const void* p : {r.q, r.k, r.v, (const void*)r.q_out, (const void*)r.k_out, r.q_weight,
+                        r.k_weight})
+    if (reinterpret_cast<uintptr_t>(p) % eb != 0) return SPEC_ENOTSUP;
+  return SPEC_OK;
+}
+
+int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int dtype,
+                 void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                 const void* q_weight, const void* k_weight, float eps, const float* inv_freq,
+                 int num_pairs, int interleaved, float rope_factor, const int32_t* seq_lens,
+                 const int32_t* positions, const int32_t* num_new, int num_q_heads,
+                 int num_kv_heads, int head_dim, int B, int T, void* stream, int32_t* err_flag) {
+  if ((k != nullptr) != (k_out != nullptr) || (k != nullptr) != (num_kv_heads > 0))
+    return SPEC_EINVAL;
+  sv::NormRopeLaunch r = {};
+  r.q = q;
+  r.q_stride = q_stride;
+  r.k = k;
+  r.k_stride = k ? k_stride : 0;
+  r.dtype = dtype;
+  r.q_out = q_out;
+  r.q_out_stride = q_out_stride;
+  r.k_out = k_out;
+  r.k_out_stride = k ? k_out_stride : 0;
+  r.q_weight = q_weight;
+  r.k_weight = k ? k_weight : nullptr;
+  r.eps = eps;
+  r.inv_freq = inv_freq;
+  r.half = num_pairs;
+  r.interleaved = interleaved != 0;
+  r.factor = rope_factor;
+  r.seq_lens = seq_lens;
+  r.positions = positions;
+  r.num_new = num_new;
+  r.Hq = num_q_heads;
+  r.H = num_kv_heads;
+  r.D = head_dim;
+  r.B = B;
+  r.T = T;
+  r.stream = stream;
+  r.err = err_flag;
+  const int st = check_norm_rope(r, 16);
+  return st != SPEC_OK ? st : sv::launch_norm_rope(r);
+}
+
+int kv_q8_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, int dtype, void* q_out,
+                           int64_t q_out_stride, const void* q_weight, const void* k_weight,
+                           float eps, const float* inv_freq, int num_pairs, int interleaved,
+                           float rope_factor, void* kv_pool, float* kv_scales,
+                           const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* positions, const int32_t* num_new, int num_blocks,
+                           int num_layers, int layer, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int B, int T, int max_blocks,
+                           void* stream, int32_t* err_flag) {
+  if (!k || !v || !block_table || !seq_lens) return SPEC_EINVAL;
+  const int pool = check_q8_pool(kv_pool, kv_scales, num_blocks, num_layers, layer, num_kv_heads,
+                                 head_dim, block_size, B, max_blocks);
+  if (pool != SPEC_OK) return pool;
+  if (T > (1 << 30) - 2 * block_size) return SPEC_EINVAL;
+  sv::NormRopeLaunch r = {};
+  r.q = q;
+  r.q_stride = q_stride;
+  r.k = k;
+  r.k_stride = k_stride;
+  r.v = v;
+  r.v_stride = v_stride;
+  r.dtype = dtype;
+  r.q_out = q_out;
+  r.q_out_stride = q_out_stride;
+  r.q_weight = q_weight;
+  r.k_weight = k_weight;
+  r.eps = eps;
+  r.inv_freq = inv_freq;
+  r.half = num_pairs;
+  r.interleaved = interleaved != 0;
+  r.factor = rope_factor;
+  r.seq_lens = seq_lens;
+  r.positions = positions;
+  r.num_new = num_new;
+  r.Hq = num_q_heads;
+  r.H = num_kv_heads;
+  r.D = head_dim;
+  r.B = B;
+  r.T = T;
+  r.pool = kv_pool;
+  r.scales = kv_scales;
+  r.block_table = block_table;
+  r.num_blocks = num_blocks;
+  r.num_layers = num_layers;
+  r.layer = layer;
+  r.bs = block_size;
+  r.max_blocks = max_blocks;
+  r.stream = stream;
+  r.err = err_flag;
+  const int st = check_norm_rope(r, T < block_size ? T : block_size);
+  return st != SPEC_OK ? st : sv::launch_norm_rope(r);
+}
+
 size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads, int head_dim) {
   if (T < 1 || T > 32 || num_kv_heads < 1 || num_q_heads < num_kv_heads ||
       num_q_heads % num_kv_heads != 0 || head_dim < 16 || head_dim > 256 || head_dim % 16 != 0)

@@ -153,6 +153,27 @@ struct Q8AttnLaunch {
   int32_t* err;
 };
 
+struct NormRopeLaunch {
+  const void *q, *k, *v;
+  int dtype;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // numbers from token to token
+  const void *q_weight, *k_weight;
+  float eps;
+  const float* inv_freq;
+  int half, interleaved;
+  float factor;
+  const int32_t *seq_lens, *positions, *num_new;
+  int Hq, H, D, B, T;
+  void* pool;  // null: no cache (k_out); else the keys and values go there
+  float* scales;
+  const int32_t* block_table;
+  int num_blocks, num_layers, layer, bs, max_blocks;
+  void* stream;
+  int32_t* err;
+};
+
+int launch_norm_rope(const NormRopeLaunch& r);
 int launch_kv_reserve(const KvReserveLaunch& k);
 int launch_kv_fork(const KvForkLaunch& k);
 int launch_kv_free(const KvFreeLaunch& k);
