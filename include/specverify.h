@@ -15,7 +15,9 @@
  *   - kv_reserve, kv_fork, kv_free: blocks for new tokens, rows that share
  *     their prefix with another row, and their release;
  *   - qk_norm_rope, kv_q8_norm_rope_append: norms of queries and keys for each head with
- *     rotary positions, by themselves or with keys and values written to that cache.
+ *     rotary positions, by themselves or with keys and values written to that cache;
+ *   - kv_prefix_plan, kv_q8_prefix_attention: the attention of rows that share the blocks
+ *     of a prefix, which is read once for all of them.
  *
  * Sources (page title, section):
  *   [L] aiengineeringfromscratch.com, "Speculative decoding and EAGLE-3":
@@ -515,6 +517,64 @@ int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* 
 /* kv_q8_attention_workspace_bytes - size of the workspace of kv_q8_attention (it does
  * not depend on B or on the lengths); 0 for arguments that the call rejects. */
 size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads, int head_dim);
+
+/*
+ * kv_prefix_plan - what kv_q8_prefix_attention shares and how it splits its work, for one
+ * step (all layers, as long as tables and lengths stay as they are).
+ *
+ *   block_table  [B, max_blocks] int32; seq_lens [B], num_new optional [B], T: as
+ *                kv_q8_attention's calls will have them
+ *   group_rows   [num_members] int32: rows, group after group; group_starts [num_groups + 1]
+ *                int32, ascending: group g has members group_starts[g] ..
+ *                group_starts[g + 1] - 1. Rows may be in no group
+ *   plan         kv_prefix_plan_bytes(B, num_groups, num_members) bytes, 256-byte aligned,
+ *                no initialisation
+ * A group shares the blocks that the tables of its rows (those with new tokens) have in
+ * common from the start, as kv_fork leaves them, as far as all of them have committed tokens
+ * there, in whole tiles of 128 positions; a group that has nothing in common shares nothing.
+ * So groups may be a guess: they change the time only, never the result.
+ * Device errors: SPEC_DERR_BAD_SLOT: a row out of range, or listed again (that entry is passed
+ * over), or group_starts that are not ascending within [0, num_members] (nothing is shared).
+ * B, num_groups, num_members <= 8192, T <= 32 (SPEC_ENOTSUP).
+ */
+int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
+                   const int32_t* group_starts, const int32_t* group_rows, int num_groups,
+                   int num_members, int T, int num_q_heads, int num_kv_heads, int num_blocks,
+                   int block_size, int B, int max_blocks, void* plan, size_t plan_bytes,
+                   void* stream, int32_t* err_flag);
+
+/* kv_prefix_plan_bytes - size of a plan; 0 for sizes that kv_prefix_plan rejects. */
+size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
+
+/*
+ * kv_q8_prefix_attention - kv_q8_attention (without a window) for rows some of which share
+ * a prefix: the blocks that a group shares are read once for all of its queries.
+ *
+ *   plan         of kv_prefix_plan with the same tables, lengths, T and heads; plan_bytes its
+ *                size. A row whose lengths are not the plan's gets NaN and
+ *                SPEC_DERR_BAD_LENGTH; with a plan of other sizes all do, and SPEC_DERR_BAD_SLOT
+ *   workspace    kv_q8_prefix_attention_workspace_bytes bytes, 256-byte aligned, no
+ *                initialisation; calls that share one must be ordered on the device
+ * Everything else is as in kv_q8_attention. With bf16 queries and head_dim 64 or 128 (any
+ * block size) the products run on the tensor cores in bf16: queries and cached codes are
+ * exact there, with scales that are powers of two between 2^-100 and 2^7 (others round
+ * code * scale to bf16), probabilities are rounded to bf16; scores, maxima, sums and outputs
+ * up to the last rounding are fp32. The NaN code counts as 480 there (kv_q8_append leaves
+ * none). Other types and head sizes are kv_q8_attention's, each row by itself.
+ */
+int kv_q8_prefix_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
+                           const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* num_new, const uint32_t* tree_mask, const void* plan,
+                           size_t plan_bytes, void* out, float softmax_scale, int num_blocks,
+                           int num_layers, int layer, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int B, int T, int max_blocks,
+                           void* workspace, size_t workspace_bytes, void* stream,
+                           int32_t* err_flag);
+
+/* kv_q8_prefix_attention_workspace_bytes - size of the workspace of kv_q8_prefix_attention; 0
+ * for arguments that the call rejects. */
+size_t kv_q8_prefix_attention_workspace_bytes(int B, int T, int num_q_heads, int num_kv_heads,
+                                              int head_dim);
 
 /*
  * kv_reserve - blocks for new tokens: entries ceil(L_b / bs) .. ceil((L_b + n_b) / bs) - 1

@@ -15,6 +15,7 @@ The entry points carry the C names:
   kv_reserve, kv_fork, kv_free   blocks for new tokens, shared prefixes, release
   qk_norm_rope(...)         norms of queries and keys for each head, rotary positions
   kv_q8_norm_rope_append(...)  the same with keys and values into the 8-bit cache
+  kv_prefix_plan, kv_q8_prefix_attention   attention of rows that share a prefix's blocks
 See include/specverify.h for layouts, ownership and error behaviour.
 """
 from __future__ import annotations
@@ -41,7 +42,8 @@ EXPORTED = ("spec_verify_sample", "spec_verify_greedy", "spec_verify_workspace_b
             "kv_commit_inplace", "kv_evict_provisional", "spec_verify_tree_greedy",
             "spec_filter_thresholds", "kv_q8_append", "kv_q8_attention",
             "kv_q8_attention_workspace_bytes", "kv_reserve", "kv_fork", "kv_free",
-            "qk_norm_rope", "kv_q8_norm_rope_append")
+            "qk_norm_rope", "kv_q8_norm_rope_append", "kv_prefix_plan", "kv_prefix_plan_bytes",
+            "kv_q8_prefix_attention", "kv_q8_prefix_attention_workspace_bytes")
 
 _lib = None
 
@@ -107,6 +109,15 @@ def lib() -> ctypes.CDLL:
         L.kv_q8_norm_rope_append.argtypes = [P, S, P, S, P, S, I, P, S, P, P, F, P, I, I, F, P, P,
                                              P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
         L.kv_q8_norm_rope_append.restype = I
+        L.kv_prefix_plan.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, Z, P, P]
+        L.kv_prefix_plan.restype = I
+        L.kv_prefix_plan_bytes.argtypes = [I, I, I]
+        L.kv_prefix_plan_bytes.restype = Z
+        L.kv_q8_prefix_attention.argtypes = [P, I, P, P, P, P, P, P, P, Z, P, F, I, I, I, I, I, I,
+                                             I, I, I, I, P, Z, P, P]
+        L.kv_q8_prefix_attention.restype = I
+        L.kv_q8_prefix_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.kv_q8_prefix_attention_workspace_bytes.restype = Z
         L.spec_selftest_ex2.argtypes = [F, F, P, P]
         L.spec_selftest_ex2.restype = I
         L.spec_status_string.argtypes = [I]
@@ -635,7 +646,8 @@ def _attn_workspace(shape, device, raw, stream):
 def _new_attn_workspace(shape, device, raw, keep):
     """A workspace in the order of the current stream, `raw`; `keep`: for the calls to come."""
     import torch
-    need = kv_q8_attention_workspace_bytes(*shape)
+    need = (kv_q8_attention_workspace_bytes if len(shape) == 4
+            else kv_q8_prefix_attention_workspace_bytes)(*shape)
     if need == 0:
         return None, 0, None  # an unsupported shape: the library call itself reports why
     held = _attn_workspaces.get((device.index, raw)) if keep else None
@@ -696,6 +708,98 @@ def kv_q8_attention(q, kv_pool, kv_scales, block_table, seq_lens, out, *, layer:
         _word(err_flag, "err_flag", dev))
     if st != SPEC_OK:
         raise SpecError("kv_q8_attention", st)
+
+
+def kv_prefix_plan_bytes(B: int, num_groups: int, num_members: int) -> int:
+    """Bytes of a plan of kv_prefix_plan (0: the call would be rejected)."""
+    return int(lib().kv_prefix_plan_bytes(B, num_groups, num_members))
+
+
+def kv_prefix_plan(block_table, seq_lens, group_starts, group_rows, *, tokens: int, q_heads: int,
+                   kv_heads: int, block_size: int, num_blocks: int, num_new=None, plan=None,
+                   stream=None, err_flag=None):
+    """The plan of a step's kv_q8_prefix_attention calls (every layer's): which rows share the
+    first blocks of their tables. group_rows int32 [members]: rows, group after group;
+    group_starts int32 [groups + 1]. `tokens` is the T of the queries. Returns `plan`, a uint8
+    tensor of kv_prefix_plan_bytes + 256 (None: a new one)."""
+    L = _lib if _int32 is not None else _ready()
+    dev = _place(block_table, "block_table")
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
+    B, MB = block_table.shape
+    starts = _arg(group_starts, "group_starts", 1, _int32, dev)
+    rows = _arg(group_rows, "group_rows", 1, _int32, dev)
+    NG, NE = group_starts.shape[0] - 1, group_rows.shape[0]
+    raw = _raw_stream(stream, dev)
+    if plan is None:
+        import torch
+        need = L.kv_prefix_plan_bytes(B, NG, NE)
+        if raw == _raw_current(dev):
+            plan = torch.empty(need + 256, dtype=_uint8, device=block_table.device)
+        else:  # in the order of the stream that uses it
+            with torch.cuda.stream(stream):
+                plan = torch.empty(need + 256, dtype=_uint8, device=block_table.device)
+    p, n = _aligned(plan, "plan", dev)
+    st = L.kv_prefix_plan(
+        bt, _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), starts, rows, NG,
+        NE, tokens, q_heads, kv_heads, num_blocks, block_size, B, MB, p, n, raw,
+        _word(err_flag, "err_flag", dev))
+    if st != SPEC_OK:
+        raise SpecError("kv_prefix_plan", st)
+    return plan
+
+
+def _aligned(t, name, dev):
+    """(pointer, bytes) of a uint8 tensor from its first 256-byte boundary."""
+    p = _arg(t, name, 1, _uint8, dev)
+    off = -p % 256
+    return p + off, max(0, t.shape[0] - off)
+
+
+def kv_q8_prefix_attention_workspace_bytes(B: int, T: int, num_q_heads: int, num_kv_heads: int,
+                                           head_dim: int) -> int:
+    """Device workspace bytes of kv_q8_prefix_attention (0: the call would be rejected)."""
+    return int(lib().kv_q8_prefix_attention_workspace_bytes(B, T, num_q_heads, num_kv_heads,
+                                                            head_dim))
+
+
+def kv_q8_prefix_attention(q, kv_pool, kv_scales, block_table, seq_lens, plan, out, *,
+                           layer: int = 0, softmax_scale: float | None = None, num_new=None,
+                           tree_mask=None, workspace=None, stream=None, err_flag=None) -> None:
+    """kv_q8_attention (without a window) for rows some of which share the first blocks of their
+    tables: `plan` is kv_prefix_plan's for the same tables, lengths and heads. workspace as there,
+    of kv_q8_prefix_attention_workspace_bytes + 256."""
+    L = _lib if _int32 is not None else _ready()
+    dev = _place(q, "q")
+    pool, scales, (NB, NL, _, H, bs, D) = _q8_pool(kv_pool, kv_scales, dev)
+    qp = _arg(q, "q", 4, None, dev)
+    op = _arg(out, "out", 4, q.dtype, dev)
+    bt = _arg(block_table, "block_table", 2, _int32, dev)
+    shape = q.shape
+    B, T, Hq, qd = shape
+    rows, MB = block_table.shape
+    if out.shape != shape or qd != D or rows != B:
+        raise ValueError(f"q and out must be [B, T, q_heads, {D}] and block_table [B, max_blocks]")
+    tm = None
+    if tree_mask is not None:
+        tm = _arg(tree_mask, "tree_mask", 2, _int32, dev)
+        if tuple(tree_mask.shape) != (B, T):
+            raise ValueError(f"tree_mask must be [{B}, {T}], got {tuple(tree_mask.shape)}")
+    pp, pn = _aligned(plan, "plan", dev)
+    raw = _raw_stream(stream, dev)
+    if workspace is None:
+        ws = _attn_workspaces.get(((B, T, Hq, H, D), dev, raw))
+        if ws is None or stream is not None or _capturing():
+            ws = _attn_workspace((B, T, Hq, H, D), q.device, raw, stream)
+        wsp, wsn, held = ws  # `held` lives until the launch is made
+    else:
+        wsp, wsn = _aligned(workspace, "workspace", dev)
+    st = L.kv_q8_prefix_attention(
+        qp, SPEC_BF16 if q.dtype is _bfloat16 else _dtype_code(q), pool, scales, bt,
+        _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), tm, pp, pn, op,
+        D ** -0.5 if softmax_scale is None else softmax_scale, NB, NL, layer, Hq, H, D, bs, B, T,
+        MB, wsp, wsn, raw, _word(err_flag, "err_flag", dev))
+    if st != SPEC_OK:
+        raise SpecError("kv_q8_prefix_attention", st)
 
 
 def kv_reserve(block_table, seq_lens, free_stack, free_top, status, *, n: int, block_size: int,

@@ -412,4 +412,73 @@ int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* 
   return sv::launch_kv_q8_attention(a);
 }
 
+size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members) {
+  if (B < 1 || B > kMaxPageRows || num_groups < 1 || num_groups > kMaxPageRows ||
+      num_members < 1 || num_members > kMaxPageRows)
+    return 0;
+  return sv::kv_prefix_plan_size(B, num_groups, num_members);
+}
+
+int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
+                   const int32_t* group_starts, const int32_t* group_rows, int num_groups,
+                   int num_members, int T, int num_q_heads, int num_kv_heads, int num_blocks,
+                   int block_size, int B, int max_blocks, void* plan, size_t plan_bytes,
+                   void* stream, int32_t* err_flag) {
+  if (!block_table || !seq_lens || !group_starts || !group_rows || !plan) return SPEC_EINVAL;
+  if (bad_table(num_blocks, block_size, B, max_blocks) || num_groups < 1 || num_members < 1 ||
+      T < 1 || num_kv_heads < 1 || num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0)
+    return SPEC_EINVAL;
+  const size_t need = kv_prefix_plan_bytes(B, num_groups, num_members);
+  if (need == 0 || T > 32 || int64_t(T) * num_q_heads > (1 << 20)) return SPEC_ENOTSUP;
+  if ((reinterpret_cast<uintptr_t>(plan) & 255u) != 0 || plan_bytes < need) return SPEC_EINVAL;
+  sv::KvPrefixPlanLaunch k{block_table, seq_lens, num_new, group_starts, group_rows, num_groups,
+                           num_members, T, num_q_heads / num_kv_heads, num_kv_heads, num_blocks,
+                           block_size, B, max_blocks, plan, stream, err_flag};
+  return sv::launch_kv_prefix_plan(k);
+}
+
+size_t kv_q8_prefix_attention_workspace_bytes(int B, int T, int num_q_heads, int num_kv_heads,
+                                              int head_dim) {
+  const size_t each = kv_q8_attention_workspace_bytes(T, num_q_heads, num_kv_heads, head_dim);
+  if (B < 1 || B > kMaxPageRows || each == 0) return 0;
+  const size_t shared = sv::kv_prefix_workspace(B, T, num_q_heads, head_dim);
+  return each > shared ? each : shared;
+}
+
+int kv_q8_prefix_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
+                           const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* num_new, const uint32_t* tree_mask, const void* plan,
+                           size_t plan_bytes, void* out, float softmax_scale, int num_blocks,
+                           int num_layers, int layer, int num_q_heads, int num_kv_heads,
+                           int head_dim, int block_size, int B, int T, int max_blocks,
+                           void* workspace, size_t workspace_bytes, void* stream,
+                           int32_t* err_flag) {
+  if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) != 0) return SPEC_EINVAL;
+  const size_t need =
+      kv_q8_prefix_attention_workspace_bytes(B, T, num_q_heads, num_kv_heads, head_dim);
+  if (!sv::kv_prefix_takes(dtype, head_dim) || need == 0)
+    // each row by itself (and the refusals that the calls have in common)
+    return B > kMaxPageRows
+               ? SPEC_ENOTSUP
+               : kv_q8_attention(q, dtype, kv_pool, kv_scales, block_table, seq_lens, num_new,
+                                 tree_mask, out, softmax_scale, 0, 0, num_blocks, num_layers,
+                                 layer, num_q_heads, num_kv_heads, head_dim, block_size, B, T,
+                                 max_blocks, workspace, workspace_bytes, stream, err_flag);
+  if (!q || !out || !block_table || !seq_lens) return SPEC_EINVAL;
+  if (!(softmax_scale > 0.0f) || std::isinf(softmax_scale)) return SPEC_EINVAL;
+  const int st = check_q8_pool(kv_pool, kv_scales, num_blocks, num_layers, layer, num_kv_heads,
+                               head_dim, block_size, B, max_blocks);
+  if (st != SPEC_OK) return st;
+  if (int64_t(T) * num_q_heads > (1 << 20) || int64_t(B) * num_kv_heads > INT32_MAX)
+    return SPEC_ENOTSUP;
+  if (!aligned16(q) || !aligned16(out)) return SPEC_ENOTSUP;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)
+    return SPEC_EINVAL;
+  sv::Q8AttnLaunch a{q, dtype, kv_pool, kv_scales, block_table, seq_lens, num_new, tree_mask, out,
+                     softmax_scale, 0, 0, num_blocks, num_layers, layer, num_kv_heads,
+                     num_q_heads / num_kv_heads, head_dim, block_size, B, T, max_blocks, workspace,
+                     stream, err_flag};
+  return sv::launch_kv_prefix_attention(a, plan, plan_bytes);
+}
+
 }  // extern "C"

@@ -1,0 +1,414 @@
+// The plan of the prefix attention (kv_prefix.cuh), and the kernel that joins its parts.
+//
+// The plan. One cluster of 8 CTAs, so that its five steps can follow each other with
+// cluster barriers: each row's place in the list of members (the first, if it is listed
+// twice); each group's first row and shortest length; the first block in which a row's
+// table differs from the group's; units and their sums. Bound by latency, and for many
+// long tables by reading them (B x max_blocks entries once).
+//
+// Joining. A CTA takes the queries of one row and kv head, a warp a query, its lanes over
+// the head's numbers: one part of the prefix and one of the row's own keys, each with the
+// pieces of further CTAs, added in that order. Bound by reading the parts, mostly from L2.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstdlib>
+
+#include "kv_prefix.cuh"
+#include "launch_util.cuh"
+
+namespace sv {
+
+namespace cg = cooperative_groups;
+
+constexpr int kPlanCtas = 8, kPlanThreads = 1024;
+constexpr int kPlanChunk = 256;  // table entries that a warp compares at a time
+
+struct PlanArgs {
+  const int32_t *bt, *sl, *nn, *starts, *members;
+  int NG, NE, T, G, H, NB, bs, B, MB;
+  uint8_t* plan;
+  int32_t* err;
+};
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    kv_prefix_plan_kernel(const PlanArgs a) {
+  __shared__ int64_t sums[kPlanThreads / 32];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const PfLayout lay = pf_layout(a.B, a.NG, a.NE);
+  PfHeader* head = reinterpret_cast<PfHeader*>(a.plan);
+  PfGroup* groups = reinterpret_cast<PfGroup*>(a.plan + lay.groups);
+  PfRow* rows = reinterpret_cast<PfRow*>(a.plan + lay.rows);
+  int64_t* prefix = reinterpret_cast<int64_t*>(a.plan + lay.prefix);
+  int32_t* members = reinterpret_cast<int32_t*>(a.plan + lay.members);
+  int32_t* row_entry = reinterpret_cast<int32_t*>(a.plan + lay.scratch);
+  int32_t *first = row_entry + a.B, *shortest = first + a.NG, *live = shortest + a.NG,
+          *common = live + a.NG;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int me = int(cluster.block_rank()) * kPlanThreads + tid, all = kPlanCtas * kPlanThreads;
+  pdl_trigger();
+  pdl_wait();
+
+  // the list's bounds: every CTA looks at all of them
+  bool bad = false;
+  for (int g = tid; g <= a.NG; g += kPlanThreads) {
+    const int s = a.starts[g];
+    bad = bad || s < 0 || s > a.NE || (g > 0 && s < a.starts[g - 1]);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && me == 0 && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
+  const int e0 = bad ? 0 : a.starts[0], e1 = bad ? 0 : a.starts[a.NG];
+  for (int b = me; b < a.B; b += all) row_entry[b] = INT32_MAX;
+  for (int g = me; g < a.NG; g += all) {
+    first[g] = shortest[g] = common[g] = INT32_MAX;
+    live[g] = 0;
+  }
+  if (me == 0) head->magic = 0;
+  cluster.sync();
+
+  for (int i = e0 + me; i < e1; i += all) {
+    const int r = a.members[i];
+    if (r >= 0 && r < a.B) atomicMin(&row_entry[r], i);
+    else if (a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
+  }
+  cluster.sync();
+
+  auto group_of = [&](int i) {  // the last group that starts at or before entry i
+    int lo = 0, hi = a.NG - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (a.starts[m] <= i) lo = m;
+      else hi = m - 1;
+    }
+    return lo;
+  };
+  auto lengths = [&](int r, int& L, int& n) {  // whether they are valid
+    L = a.sl[r];
+    n = a.nn ? a.nn[r] : a.T;
+    return L >= 0 && n >= 0 && n <= a.T && int64_t(L) + n <= int64_t(a.MB) * a.bs;
+  };
+  for (int i = e0 + me; i < e1; i += all) {
+    const int r = a.members[i];
+    members[i] = -1;  // a member without queries
+    if (r < 0 || r >= a.B) continue;
+    if (row_entry[r] != i) {
+      if (a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
+      continue;
+    }
+    int L, n;
+    if (!lengths(r, L, n) || n == 0) continue;
+    members[i] = r;
+    const int g = group_of(i);
+    atomicMin(&first[g], i);
+    atomicMin(&shortest[g], L);
+    atomicAdd(&live[g], 1);
+  }
+  cluster.sync();
+
+  // tables against the first row's, a warp 256 entries at a time
+  const int chunks = (a.MB + kPlanChunk - 1) / kPlanChunk;
+  const int64_t tasks = int64_t(e1 - e0) * chunks;
+  for (int64_t t = me >> 5; t < tasks; t += all / 32) {
+    const int i = e0 + int(t / chunks), j0 = int(t % chunks) * kPlanChunk;
+    const int r = a.members[i];
+    if (r < 0 || r >= a.B || row_entry[r] != i) continue;
+    int L, n;
+    if (!lengths(r, L, n) || n == 0) continue;
+    const int g = group_of(i);
+    if (live[g] < 2) continue;
+    const int j1 = min(shortest[g] / a.bs, j0 + kPlanChunk);
+    if (j0 >= j1 || *reinterpret_cast<volatile int32_t*>(&common[g]) <= j0) continue;
+    const int32_t* mine = a.bt + int64_t(r) * a.MB;
+    const int32_t* other = a.bt + int64_t(a.members[first[g]]) * a.MB;
+    int x[kPlanChunk / 32], y[kPlanChunk / 32];
+#pragma unroll
+    for (int k = 0; k < kPlanChunk / 32; ++k) {
+      const int j = j0 + 32 * k + lane;
+      x[k] = j < j1 ? mine[j] : 0;
+      y[k] = j < j1 ? other[j] : 0;
+    }
+    int at = INT32_MAX;
+#pragma unroll
+    for (int k = kPlanChunk / 32 - 1; k >= 0; --k) {
+      const int j = j0 + 32 * k + lane;
+      if (j < j1 && (x[k] != y[k] || x[k] < 0 || x[k] >= a.NB)) at = j;
+    }
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (at != INT32_MAX && lane == 0) atomicMin(&common[g], at);
+  }
+  cluster.sync();
+  if (cluster.block_rank() != 0) return;
+
+  // units, and their sums from entry to entry: each thread some consecutive entries
+  auto shared_tiles = [&](int g) {
+    return bad || live[g] < 2 ? 0
+                              : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs / kPfTile);
+  };
+  const int entries = a.NG + a.B, per = (entries + kPlanThreads - 1) / kPlanThreads;
+  auto entry = [&](int e, bool write) -> int64_t {
+    if (e < a.NG) {
+      const int tiles = shared_tiles(e);
+      const int s0 = bad ? 0 : a.starts[e], many = bad ? 0 : a.starts[e + 1] - s0;
+      if (write) groups[e] = PfGroup{tiles, tiles > 0 ? a.members[first[e]] : 0, s0, many};
+      return a.H * pf_units(int64_t(many) * a.T * a.G, tiles);
+    }
+    const int b = e - a.NG;
+    PfRow r = {};
+    const bool ok = lengths(b, r.L, r.n);
+    r.group = r.at = -1;
+    const int i = row_entry[b];
+    if (ok && r.n > 0 && i != INT32_MAX) {
+      const int g = group_of(i);
+      r.skip = shared_tiles(g);
+      if (r.skip > 0) {
+        r.group = g;
+        r.at = i - a.starts[g];
+      }
+    }
+    r.tiles = !ok ? -1 : r.n == 0 ? 0 : (r.L + r.n + kPfTile - 1) / kPfTile - r.skip;
+    if (write) rows[b] = r;
+    return r.tiles > 0 ? a.H * pf_units(int64_t(r.n) * a.G, r.tiles) : 0;
+  };
+  int64_t sum = 0;
+  for (int x = 0; x < per; ++x) {
+    const int e = tid * per + x;
+    if (e < entries) sum += entry(e, true);
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sums[tid >> 5] = inc;
+  __syncthreads();
+  for (int w = 0; w < (tid >> 5); ++w) inc += sums[w];
+  int64_t at = inc - sum;
+  for (int x = 0; x < per; ++x) {
+    const int e = tid * per + x;
+    if (e >= entries) break;
+    prefix[e] = at;
+    at += entry(e, false);
+    if (e == entries - 1) {
+      prefix[entries] = at;
+      head->units = at;
+      head->B = a.B;
+      head->T = a.T;
+      head->G = a.G;
+      head->H = a.H;
+      head->bs = a.bs;
+      head->MB = a.MB;
+      head->NG = a.NG;
+      head->NE = a.NE;
+      head->magic = kPfMagic;
+    }
+  }
+}
+
+int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
+  PlanArgs a;
+  a.bt = k.block_table;
+  a.sl = k.seq_lens;
+  a.nn = k.num_new;
+  a.starts = k.group_starts;
+  a.members = k.group_rows;
+  a.NG = k.num_groups;
+  a.NE = k.num_members;
+  a.T = k.T;
+  a.G = k.G;
+  a.H = k.H;
+  a.NB = k.num_blocks;
+  a.bs = k.block_size;
+  a.B = k.B;
+  a.MB = k.max_blocks;
+  a.plan = static_cast<uint8_t*>(k.plan);
+  a.err = k.err;
+  return launch_pdl(kv_prefix_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0,
+                    static_cast<cudaStream_t>(k.stream), a);
+}
+
+size_t kv_prefix_plan_size(int B, int num_groups, int num_members) {
+  return pf_layout(B, num_groups, num_members).bytes;
+}
+
+// ------------------------------------------------------------------ joining
+constexpr int kPfJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const PfArgs a, int ctas) {
+  constexpr int N = D / 32;  // numbers of a lane
+  pdl_trigger();
+  pdl_wait();
+  const PfPlan p = pf_plan(a, ctas);
+  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, lane = threadIdx.x & 31;
+  const int R = a.T * a.G;
+  PfRow row = {};
+  row.tiles = -1;
+  if (p.ok) row = p.rows[b];
+  // lengths that changed since the plan was made: the row's keys are not the plan's
+  const bool same = p.ok && row.L == a.sl[b] && row.n == (a.nn ? a.nn[b] : a.T);
+  const bool bad = row.tiles < 0 || !same;
+  if (bad && a.err && h == 0 && threadIdx.x == 0)
+    atomicOr(a.err, p.ok ? SPEC_DERR_BAD_LENGTH : SPEC_DERR_BAD_SLOT);
+  for (int r = threadIdx.x >> 5; r < R; r += kPfJoinThreads / 32) {
+    const int t = r / a.G;
+    const int64_t query = (int64_t(b) * a.T + t) * a.H * a.G + h * a.G + r % a.G;
+    float m = -INFINITY, l = 0.0f, o[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = 0.0f;
+    auto add = [&](const float* part, float2 st) {
+      float v[N];
+      if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(part + 4 * lane);
+        v[0] = x.x;
+        v[1] = x.y;
+        v[N - 2] = x.z;
+        v[N - 1] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(part + 2 * lane);
+        v[0] = x.x;
+        v[1] = x.y;
+      }
+      const float mn = fmaxf(m, st.x), base = mn == -INFINITY ? 0.0f : mn;
+      const float x = ex2_approx(m - base), y = ex2_approx(st.x - base);
+      l = l * x + st.y * y;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = o[i] * x + v[i] * y;
+      m = mn;
+    };
+    // the parts of one entry's item that holds query qi of its nq
+    auto gather = [&](int e, int which, int64_t qi, int64_t nq, int tiles) {
+      const int64_t per_h = pf_units(nq, tiles), qb = qi / 256;
+      const int w = nq - qb * 256 > 128 ? 2 : 1;
+      const int64_t u = p.prefix[e] + h * per_h + qb * 2 * tiles, end = u + int64_t(w) * tiles;
+      add(a.parts[which] + query * D, a.stats[which][query]);
+      const int c0 = pf_owner(p, u), c1 = pf_owner(p, end - 1);
+      for (int c = c0 + 1; c <= c1; ++c) {
+        const int64_t u0 = pf_share(p, c) - u, u1 = min(pf_share(p, c + 1), end) - u;
+        if ((u0 + w - 1) / w >= (u1 + w - 1) / w) continue;  // no whole tile
+        const int64_t at = int64_t(c) * 256 + qi % 256;
+        add(a.mid + at * D, a.mid_stats[at]);
+      }
+    };
+    if (!bad && t < row.n) {
+      if (row.group >= 0) {
+        const PfGroup g = p.groups[row.group];
+        gather(row.group, 0, int64_t(row.at) * R + r, int64_t(g.count) * R, g.tiles);
+      }
+      if (row.tiles > 0) gather(p.NG + b, 1, r, int64_t(row.n) * a.G, row.tiles);
+    }
+    const float inv = bad ? __uint_as_float(0x7fc00000u) : l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t x[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+      x[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + query * D) +
+                   N / 2 * lane;
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[N / 2 - 1]);
+    else *to = x[0];
+  }
+}
+
+namespace {
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Places {  // byte offsets in the workspace
+  size_t parts[2], stats[2], mid, mid_stats, bytes;
+};
+Places places(int64_t queries, int D) {
+  Places p;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t x = at;
+    at += up256(n);
+    return x;
+  };
+  for (int i = 0; i < 2; ++i) {
+    p.parts[i] = take(size_t(queries) * D * sizeof(float));
+    p.stats[i] = take(size_t(queries) * sizeof(float2));
+  }
+  p.mid = take(size_t(kPfMaxCtas) * 256 * D * sizeof(float));
+  p.mid_stats = take(size_t(kPfMaxCtas) * 256 * sizeof(float2));
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace
+
+bool kv_prefix_takes(int dtype, int D) { return dtype == SPEC_BF16 && (D == 64 || D == 128); }
+
+size_t kv_prefix_workspace(int B, int T, int Hq, int D) {
+  return places(int64_t(B) * T * Hq, D).bytes;
+}
+
+int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t plan_bytes) {
+  PfArgs a = {};
+  const int64_t layer_bytes = int64_t(2) * k.H * k.bs * k.D;
+  a.q = k.q;
+  a.pool = static_cast<const uint8_t*>(k.pool) + k.layer * layer_bytes;
+  a.scales = k.scales + int64_t(k.layer) * 2 * k.H;
+  a.bt = k.block_table;
+  a.sl = k.seq_lens;
+  a.nn = k.num_new;
+  a.tree = k.tree_mask;
+  a.out = k.out;
+  a.plan = static_cast<const uint8_t*>(plan);
+  a.plan_bytes = plan_bytes;
+  a.scale_log2 = float(double(k.softmax_scale) * 1.4426950408889634);
+  a.NB = k.num_blocks;
+  a.H = k.H;
+  a.G = k.G;
+  a.D = k.D;
+  a.bs = k.bs;
+  a.B = k.B;
+  a.T = k.T;
+  a.MB = k.max_blocks;
+  a.block_bytes = k.num_layers * layer_bytes;
+  a.block_scales = int64_t(k.num_layers) * 2 * k.H;
+  const Places p = places(int64_t(k.B) * k.T * k.H * k.G, k.D);
+  uint8_t* ws = static_cast<uint8_t*>(k.workspace);
+  for (int i = 0; i < 2; ++i) {
+    a.parts[i] = reinterpret_cast<float*>(ws + p.parts[i]);
+    a.stats[i] = reinterpret_cast<float2*>(ws + p.stats[i]);
+  }
+  a.mid = reinterpret_cast<float*>(ws + p.mid);
+  a.mid_stats = reinterpret_cast<float2*>(ws + p.mid_stats);
+  a.err = k.err;
+  // the failure-detection knobs of kv_q8_attention
+  a.wait_ns = kWaitNs;
+  a.stall_row = -1;
+  if (const char* row = std::getenv("SPECVERIFY_STALL_ROW")) {
+    const long b = std::strtol(row, nullptr, 10);
+    if (b >= 0 && b < a.B) a.stall_row = int(b);
+    if (const char* ns = std::getenv("SPECVERIFY_IDLE_NS")) {
+      const long long v = std::strtoll(ns, nullptr, 10);
+      if (v > 0 && uint64_t(v) < kWaitNs) a.wait_ns = uint64_t(v);
+    }
+  }
+  static std::atomic<int> known[64];
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ECUDA;
+  if (dev < 64) sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return SPEC_ECUDA;
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  }
+  const int ctas = sms < kPfMaxCtas ? sms : kPfMaxCtas;
+  const int st = launch_pf_attention(a, ctas, k.stream);
+  if (st != SPEC_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
+  const dim3 grid(unsigned(a.B * a.H));
+  return a.D == 128
+             ? launch_pdl(kv_prefix_join_kernel<128>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas)
+             : launch_pdl(kv_prefix_join_kernel<64>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas);
+}
+
+}  // namespace sv

@@ -174,6 +174,23 @@ struct NormRopeLaunch {
 };
 
 int launch_norm_rope(const NormRopeLaunch& r);
+struct KvPrefixPlanLaunch {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* num_new;  // null: T
+  const int32_t* group_starts;
+  const int32_t* group_rows;
+  int num_groups, num_members, T, G, H, num_blocks, block_size, B, max_blocks;
+  void* plan;
+  void* stream;
+  int32_t* err;
+};
+
+int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k);
+size_t kv_prefix_plan_size(int B, int num_groups, int num_members);
+bool kv_prefix_takes(int dtype, int D);
+size_t kv_prefix_workspace(int B, int T, int Hq, int D);
+int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t plan_bytes);
 int launch_kv_reserve(const KvReserveLaunch& k);
 int launch_kv_fork(const KvForkLaunch& k);
 int launch_kv_free(const KvFreeLaunch& k);
