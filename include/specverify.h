@@ -555,12 +555,12 @@ size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
  *                SPEC_DERR_BAD_LENGTH; with a plan of other sizes all do, and SPEC_DERR_BAD_SLOT
  *   workspace    kv_q8_prefix_attention_workspace_bytes bytes, 256-byte aligned, no
  *                initialisation; calls that share one must be ordered on the device
- * Everything else is as in kv_q8_attention. With bf16 queries and head_dim 64 or 128 (any
- * block size) the products run on the tensor cores in bf16: queries and cached codes are
+ * Everything else is as in kv_q8_attention. With bf16 queries, head_dim 64 or 128 and
+ * blocks of a multiple of 16 tokens the products run on the tensor cores in bf16: queries and cached codes are
  * exact there, with scales that are powers of two between 2^-100 and 2^7 (others round
  * code * scale to bf16), probabilities are rounded to bf16; scores, maxima, sums and outputs
  * up to the last rounding are fp32. The NaN code counts as 480 there (kv_q8_append leaves
- * none). Other types and head sizes are kv_q8_attention's, each row by itself.
+ * none). Other types, head and block sizes are kv_q8_attention's, each row by itself.
  */
 int kv_q8_prefix_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
                            const int32_t* block_table, const int32_t* seq_lens,

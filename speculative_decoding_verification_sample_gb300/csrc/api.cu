@@ -429,7 +429,9 @@ int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const in
       T < 1 || num_kv_heads < 1 || num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0)
     return SPEC_EINVAL;
   const size_t need = kv_prefix_plan_bytes(B, num_groups, num_members);
-  if (need == 0 || T > 32 || int64_t(T) * num_q_heads > (1 << 20)) return SPEC_ENOTSUP;
+  if (need == 0 || T > 32 || int64_t(T) * num_q_heads > (1 << 20) ||
+      int64_t(B > num_members ? B : num_members) * T * num_q_heads > INT32_MAX)
+    return SPEC_ENOTSUP;
   if ((reinterpret_cast<uintptr_t>(plan) & 255u) != 0 || plan_bytes < need) return SPEC_EINVAL;
   sv::KvPrefixPlanLaunch k{block_table, seq_lens, num_new, group_starts, group_rows, num_groups,
                            num_members, T, num_q_heads / num_kv_heads, num_kv_heads, num_blocks,
@@ -456,7 +458,9 @@ int kv_q8_prefix_attention(const void* q, int dtype, const void* kv_pool, const 
   if (!plan || (reinterpret_cast<uintptr_t>(plan) & 255u) != 0) return SPEC_EINVAL;
   const size_t need =
       kv_q8_prefix_attention_workspace_bytes(B, T, num_q_heads, num_kv_heads, head_dim);
-  if (!sv::kv_prefix_takes(dtype, head_dim) || need == 0)
+  if (!sv::kv_prefix_takes(dtype, head_dim, block_size,
+                           int64_t(num_blocks) * num_layers * 2 * num_kv_heads) ||
+      need == 0)
     // each row by itself (and the refusals that the calls have in common)
     return B > kMaxPageRows
                ? SPEC_ENOTSUP
@@ -469,7 +473,7 @@ int kv_q8_prefix_attention(const void* q, int dtype, const void* kv_pool, const 
   const int st = check_q8_pool(kv_pool, kv_scales, num_blocks, num_layers, layer, num_kv_heads,
                                head_dim, block_size, B, max_blocks);
   if (st != SPEC_OK) return st;
-  if (int64_t(T) * num_q_heads > (1 << 20) || int64_t(B) * num_kv_heads > INT32_MAX)
+  if (int64_t(T) * num_q_heads > (1 << 20) || int64_t(B) * T * num_q_heads > INT32_MAX)
     return SPEC_ENOTSUP;
   if (!aligned16(q) || !aligned16(out)) return SPEC_ENOTSUP;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)

@@ -8,15 +8,18 @@
 // m >= about the largest z_j, l = sum 2^(z_j - m), o = sum 2^(z_j - m) v_j in log2
 // units, and parts add up as 2^(m_i - M) (l_i, o_i).
 //
-// Entries: first the groups, then the rows. An entry's queries (group: all rows of it,
-// row by row; row: its own) are taken in blocks of 256, two M tiles of the tensor core,
-// the last one maybe one tile. An item is (entry, kv head, block); it costs `w` units a
-// key tile, w its M tiles. The units of all items form one list, entries outermost, then
-// kv heads, blocks, tiles; CTA c of NC takes units [W c / NC, W (c + 1) / NC), cut up
-// to whole tiles. A piece that begins its item leaves its part in the place of its
-// queries (one place for the prefix, one for the row's own keys), another one in the
-// place of its CTA, which has at most one such. Everything follows from the plan, so the
-// result does not depend on timing.
+// Entries: first the groups, then the rows' own keys. A group's queries (all rows of it,
+// row by row) are taken in blocks of 256, two M tiles of the tensor core, the last one
+// maybe one tile; a row's queries R = T G likewise, but with R <= 64 as many consecutive
+// rows as fit share one M tile, a pack: their key tiles follow each other, and a tile's
+// probabilities are zero for the other rows of the pack. (An item for each row, with 20 of
+// 128 places in use, spent 15 us each on its beginning and end.) An item is (entry, kv
+// head, block); it costs `w` units a key tile, w its M tiles. The units of all items form
+// one list, entries outermost, then kv heads, blocks, tiles; CTA c of NC takes units
+// [W c / NC, W (c + 1) / NC), cut up to whole tiles. A piece that begins its item leaves its
+// part in the place of its queries (one place for the prefix, one for the row's own keys),
+// another one in the place of its CTA, which has at most one such. Everything follows from
+// the plan, so the result does not depend on timing.
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -66,6 +69,9 @@ __host__ __device__ inline PfLayout pf_layout(int B, int NG, int NE) {
   return l;
 }
 
+// Rows of a pack with R queries each.
+__host__ __device__ inline int pf_pack(int R) { return R <= 64 ? 128 / R : 1; }
+
 // Units of one kv head of an entry with nq queries and `tiles` key tiles.
 __host__ __device__ inline int64_t pf_units(int64_t nq, int tiles) {
   const int64_t full = nq / 256;
@@ -93,6 +99,8 @@ struct PfArgs {
   int32_t* err;
   uint64_t wait_ns;
   int stall_row;           // -1, or the row whose own keys are withheld (a test)
+  int plane0;              // tensor-map plane of (block 0, this layer, keys, head 0)
+  int planes_per_block;
 };
 
 // The plan as a kernel sees it; `ok` false: not a plan for this call.
@@ -133,6 +141,7 @@ __device__ __forceinline__ int pf_owner(const PfPlan& p, int64_t u) {
   return int((n | p.W) >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(p.W)) : n / p.W);
 }
 
-int launch_pf_attention(const PfArgs& a, int ctas, void* stream);
+int launch_pf_attention(const PfArgs& a, const void* pool_base, int64_t planes, int ctas,
+                        void* stream);
 
 }  // namespace sv

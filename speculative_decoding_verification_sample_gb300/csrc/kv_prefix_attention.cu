@@ -2,30 +2,33 @@
 // how the work is split).
 //
 // With the queries of many rows there are enough of them to be the M operand:
-//   S [128 queries x 128 keys]  = Q [128 x D] * K^T          bf16 x bf16, fp32 sums in TMEM
-//   O [128 queries x D]        += P [128 x 128] * V          P bf16 in TMEM, V bf16
+//   S [128 queries x 128 keys]  = (Qhi + Qlo) [128 x D] * K^T   e4m3 x e4m3, fp32 sums in TMEM
+//   O [128 queries x D]        += P [128 x 128] * V             bf16 x bf16, P in TMEM
 // A thread owns a query: no maximum or sum crosses lanes. Two M tiles per CTA take turns, so
 // that the tensor core works for one while the other's softmax runs: with more than 128
 // queries they are two halves of the block and share each key tile, else both hold the same
 // queries and take the key tiles by turns, each with a part of its own, added at the end.
 //
-// The cached codes are read by ordinary loads, widened to bf16 on the way to shared memory:
-// a code is exact in bf16 (its exponent and fraction moved to their place, then one product
-// with scale * 2^120, exact for the powers of two that appending leaves; other scales take a
-// path that multiplies in fp32 and rounds once to bf16). A copy by TMA would pass the codes
-// through shared memory once more, whose bandwidth the products need: of its 128 bytes a
-// cycle S takes 128 and O 64 while each runs.
-// P is rounded to bf16 (2^-9 relative, as the output); the sums l take it in fp32 before.
+// K goes from TMA into the products as it is cached (queries as in the other attention kernel:
+// a row scaled by a power of two, two e4m3 terms a number, 4 + 4 bits). V is widened to bf16 on
+// its way to shared memory, exactly: a code's exponent and fraction are moved to their place,
+// then one product with scale * 2^120, exact for the powers of two that appending leaves (other
+// scales take a path that multiplies in fp32 and rounds once to bf16). Widening K too kept the
+// loading warps from keeping up. P is rounded to bf16 (2^-9 relative, as the output); the sums l
+// take it in fp32 before. K's scales belong to 16 keys and enter the softmax as one factor each.
 //   Softmax: a row's reference is the largest z_j so far, moved only when a later one
-// exceeds it by 2^8; then O and l are rescaled.
+// exceeds it by 2^8; then O and l are rescaled. A tile's scores of a query are loaded once and
+// stay in registers from the maximum to the probabilities.
 //
-// Roles: two groups of 4 softmax warps, 4 loading warps, a warp that issues the products,
-// and one that walks the work list and copies the queries: 14 warps, so that no quarter of
-// the SM has more than 4 and a thread may have 128 registers. One CTA per SM.
+// Roles, of 4 warps each with registers moved to the softmax: two softmax groups; loading of V;
+// a warp for each group's products, one that walks the work list and prepares queries, one that
+// finds the tiles and starts the copies of K. One CTA per SM.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 
 #include "kv_prefix.cuh"
@@ -35,15 +38,26 @@
 
 namespace sv {
 
-constexpr int kPfSoftmax = 256, kPfLoad = 128;
-constexpr int kPfThreads = kPfSoftmax + kPfLoad + 64;
-constexpr int kPfItems = 4;     // items described at a time
-constexpr int kPfQueries = 3;   // M tiles of queries held at a time
+constexpr int kPfSoftmax = 256, kPfLoad = 128, kPfThreads = kPfSoftmax + kPfLoad + 128;
+constexpr int kPfSoftmaxRegs = 184, kPfLoadRegs = 64, kPfOtherRegs = 80;
+static_assert(256 * kPfSoftmaxRegs + 128 * (kPfLoadRegs + kPfOtherRegs) == 65536,
+              "what the groups give up is what the softmax takes");
+constexpr int kPfItems = 6;     // items described at a time
+constexpr int kPfQueries = 2;   // M tiles of queries held at a time
+constexpr int kPfFactors = 16;  // M tiles whose rows' factors are held: more than kPfItems items have
+constexpr int kPfPart = 16;     // keys of a part of a tile: of one block (block_size % 16 == 0)
+constexpr int kPfParts = kPfTile / kPfPart;
+constexpr float kMaxBf16 = 0x1.fep127f;
 constexpr float kPfSlack = 8.0f;  // binades by which keys may exceed the reference
 
+// Bounded waits. A wait ends when its barrier's phase does or when `abort` is set; the walking
+// warp sets it (and the error bit) when no tile has been done for a while, and every role then
+// leaves its loop. So a wait is a few instructions: with a clock of its own in each, the code
+// of the loops outgrew the instruction cache.
 struct PfGuard {
-  uint64_t limit_ns;
   int abort;
+  int beat[2];   // tiles that each softmax group has done
+  int done[2];   // whether it has ended
   __device__ __forceinline__ bool aborted() const {
     return *reinterpret_cast<const volatile int*>(&abort) != 0;
   }
@@ -53,51 +67,56 @@ struct PfGuard {
 struct PfItem {
   int stop;       // no more items
   int two;        // two M tiles (else one, and its key tiles by turns)
-  int row;        // whose table the keys come from
+  int own;        // 0 a group's prefix, 1 rows' own keys
+  int row, rows;  // prefix: a row of the group; own keys: the first row, rows of the pack
+  int entry;      // prefix: the group's first member
   int h;
   int t0, t1;     // tiles of the item
-  int tile0;      // the item's first tile in the row
-  int L, n, end;  // own keys: committed, new, end. A prefix: all keys are seen, end past them
-  int own;        // 0 prefix, 1 own keys
   int q0, nq;     // first query of the block in its entry, queries of the block
-  int entry;      // prefix: the group's first member
 };
 
-struct PfShared {
-  PfItem item[kPfItems];
-  float2 part[2][kPfTile];  // what one group tells the other at the end of an item
-  uint64_t item_full[kPfItems], item_empty[kPfItems];
-  uint64_t q_full[kPfQueries], q_empty[kPfQueries];
-  uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[2], p_full[2], o_full[2], told[2], read[2], drained;
-  uint32_t tmem;
-  PfGuard guard;
+// A key tile: what the warps need of it.
+struct PfTile {
+  int plane[kPfParts], in_block[kPfParts];  // where the parts' V is (plane -1: nowhere)
+  float ks[kPfParts], vs[kPfParts];         // scales of K, of V
+  int pos, L, n, first;      // position, its row's tokens (a prefix: L past all), the row's first
+                             // query of the M tile
+  int keys, valid;           // keys of the tile that there are; bits: parts that can be read
+  int plain_k, plain_v;      // K's scales are positive and finite; V's 2^-100 .. 2^7
 };
 
+// kTiles: more than the key tiles between their finding and the end of their V: one being
+// written, those in K's slots, one at each softmax group, those whose V is in slots.
 template <int D>
 struct PfShape {
-  static constexpr int kTileBytes = kPfTile * D * 2;  // K, V or an M tile of queries
-  static constexpr int kSlots = D == 128 ? 4 : 8;
-  static constexpr size_t kBytes = size_t(kSlots + kPfQueries) * kTileBytes + sizeof(PfShared);
+  static constexpr int kCodeBytes = kPfTile * D;        // K or V as cached, a term of the queries
+  static constexpr int kWideBytes = kPfTile * D * 2;    // V in bf16, an M tile of queries
+  static constexpr int kKSlots = D == 128 ? 3 : 4, kRawSlots = kKSlots - 1;
+  static constexpr int kVSlots = D == 128 ? 2 : 3;
+  static constexpr int kTiles = 1 + kKSlots + 2 + kRawSlots + kVSlots + 4;
+  struct Shared {
+    PfTile tile[kTiles];
+    PfItem item[kPfItems];
+    float factor[kPfFactors][kPfTile];  // of the rows' scores
+    float2 part[2][kPfTile];  // what one group tells the other at the end of an item
+    int raw_tile[kRawSlots];  // whose V is there
+    uint64_t item_full[kPfItems], item_empty[kPfItems];
+    uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+    uint64_t q_full[kPfQueries], q_empty[kPfQueries];
+    uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+    uint64_t s_full[2], p_full[2], o_full[2], told[2], read[2], drained;
+    uint32_t tmem;
+    PfGuard guard;
+  };
+  static constexpr size_t kBytes = size_t(kKSlots + kRawSlots) * kCodeBytes +
+                                   size_t(kVSlots + kPfQueries) * kWideBytes + sizeof(Shared);
   static_assert(kBytes <= 227 * 1024, "one CTA per SM");
 };
 
-// Bounded waits, as in the other attention kernel: once one has run out, all return at once
-// and every role leaves its loop; the error bit is set.
-__device__ __noinline__ void pf_wait_long(uint64_t* bar, uint32_t parity, PfGuard* guard,
-                                          int32_t* err) {
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (guard->aborted()) return;
-    if (mbar_try_wait(bar, parity, kSuspendNs)) return;
-    if (global_ns() - t0 > guard->limit_ns) break;
-  }
-  *reinterpret_cast<volatile int*>(&guard->abort) = 1;
-  if (err) atomicOr(err, SPEC_DERR_TIMEOUT);
-}
-__device__ __forceinline__ void pf_wait(uint64_t* bar, uint32_t parity, PfGuard* guard,
-                                        int32_t* err) {
-  if (!mbar_try_wait(bar, parity, kSuspendNs)) pf_wait_long(bar, parity, guard, err);
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, const PfGuard* guard) {
+  while (!mbar_try_wait(bar, parity, kSuspendNs))
+    if (guard->aborted()) return false;
+  return true;
 }
 
 template <int N>
@@ -112,36 +131,33 @@ struct PfRing {
   }
 };
 
-// Where an M tile, K or V holds 16-byte chunk c (of D / 8) of row r: halves of 64 numbers,
-// rows of 128 bytes, 128-byte swizzle.
+// Where a V tile holds 16-byte chunk c (of D / 8) of key r: halves of 64 numbers, rows of 128
+// bytes, 128-byte swizzle. Where K, or a term of the queries, holds chunk c (of D / 16) of row
+// r: rows of D bytes, swizzled over D bytes.
 __device__ __forceinline__ uint32_t pf_place(int r, int c) {
   return uint32_t((c >> 3) * (kPfTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
-
-// The query of index qi of an entry: its row of q and out ([B, T, H * G]), or -1; t: its query.
-__device__ __forceinline__ int64_t pf_query(const PfArgs& a, const PfPlan& p, const PfItem& it,
-                                            int x, int& t) {
-  t = 0;
-  if (x >= it.nq) return -1;
-  const int R = a.T * a.G, qi = it.q0 + x;
-  int b = it.row, r = qi;
-  if (!it.own) {
-    const int e = qi / R;
-    r = qi - e * R;
-    b = it.entry + e < p.NE ? p.members[it.entry + e] : -1;
-    if (b < 0 || b >= a.B) return -1;
-  }
-  t = r / a.G;
-  return (int64_t(b) * a.T + t) * a.H * a.G + it.h * a.G + (r - t * a.G);
+template <int D>
+__device__ __forceinline__ uint32_t pf_place8(int r, int c) {
+  return uint32_t(r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
 }
 
-// Sixteen codes, where the call stands (ahead of their use), not kept in L1.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// The row of q and out ([B, T, H * G]) of query x of an item's block, or -1; b, t: its row and
+// place among the new tokens; n: how many of those there are.
+__device__ __forceinline__ int64_t pf_query(const PfArgs& a, const PfPlan& p, const PfItem& it,
+                                            int x, int& b, int& t, int& n) {
+  b = -1;
+  t = n = 0;
+  if (x >= it.nq) return -1;
+  const int R = a.T * a.G, qi = it.q0 + x;
+  const int e = it.own && it.rows == 1 ? 0 : qi / R, r = qi - e * R;
+  if (it.own) b = it.row + e;
+  else b = it.entry + e < p.NE ? p.members[it.entry + e] : -1;
+  if (b < 0 || b >= a.B) return -1;
+  n = p.rows[b].n;
+  t = r / a.G;
+  if (t >= n) return -1;
+  return (int64_t(b) * a.T + t) * a.H * a.G + it.h * a.G + (r - t * a.G);
 }
 
 // Two e4m3 codes to two bf16 numbers divided by 2^120: the sign to bit 15, the exponent's and
@@ -158,6 +174,23 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(n)
+      : "memory");
+}
+
+// 32 columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* f) {
   uint32_t* r = reinterpret_cast<uint32_t*>(f);
   asm volatile(
@@ -170,6 +203,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* f) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
+// Waits for the loads; what uses f (or, with `tie` alone, comes after the wait) stays behind it.
+__device__ __forceinline__ void tmem_tie32(float* f) {
+  asm volatile(""
+               : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]),
+                 "+f"(f[7]), "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]),
+                 "+f"(f[13]), "+f"(f[14]), "+f"(f[15]), "+f"(f[16]), "+f"(f[17]), "+f"(f[18]),
+                 "+f"(f[19]), "+f"(f[20]), "+f"(f[21]), "+f"(f[22]), "+f"(f[23]), "+f"(f[24]),
+                 "+f"(f[25]), "+f"(f[26]), "+f"(f[27]), "+f"(f[28]), "+f"(f[29]), "+f"(f[30]),
+                 "+f"(f[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -179,56 +224,166 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-// D[tmem] (+)= A B in bf16, K = 16; one thread issues. A in shared memory or in TMEM.
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// D[tmem] (+)= A B; one thread issues. Scores: e4m3, K = 32, both in shared memory. Outputs: bf16,
+// K = 16, A in TMEM. `hi`: the upper half of the descriptors.
+__device__ __forceinline__ void pf_mma_s(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                         uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(accumulate))
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                               bool accumulate) {
+__device__ __forceinline__ void pf_mma_o(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                         uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(accumulate))
       : "memory");
 }
 
-// ------------------------------------------------------------------ the order of the tiles
-// The products go through steps; in each, first group 0, then group 1, takes the output of its
-// tile before (V), then the scores of the next (K). The loading warps follow the same order:
-// phases 0 to 3 of a step are V and K of group 0, V and K of group 1.
-struct PfTile {
-  int row, h, p0, end, own;  // keys [p0, p0 + 128) of the row's table, those past `end` zero
-  bool v;
-};
+// An M tile of an item's queries (from query x0 of its block) as two e4m3 terms a number, and
+// the factors of its rows' scores, by warp w of n. A row's bf16 numbers are copied to where
+// their terms will be (as many bytes), all in flight at once, then converted in place, 32 a
+// lane: scaled by a power of two to [128, 256) at the row's largest, and split.
+template <int D>
+__device__ __forceinline__ void pf_prepare(const PfArgs& a, const PfPlan& p, const PfItem& it, int x0,
+                                        uint8_t* to, float* factor, int w, int n) {
+  constexpr int kChunks = D / 8, kLanes = D / 32, kRows = 32 / kLanes, kTerm = kPfTile * D;
+  const int lane = threadIdx.x & 31;
+  const int rows = min(kPfTile, max(0, it.nq - x0));
+  // raw chunk c of a row: even ones to the upper term's chunk c / 2, odd ones to the lower's
+  for (int r0 = w * 32; r0 < kPfTile; r0 += n * 32) {
+    int b, t, m;
+    const int64_t mine = pf_query(a, p, it, x0 + r0 + lane, b, t, m);
+    if (mine < 0) factor[r0 + lane] = 0.0f;
+#pragma unroll 4
+    for (int x = 0; x < kChunks; ++x) {
+      const int c = x * 32 + lane, r = c / kChunks, y = c % kChunks;
+      const int64_t row = __shfl_sync(0xffffffffu, mine, r);
+      cp_async16(to + (y & 1) * kTerm + pf_place8<D>(r0 + r, y >> 1),
+                 static_cast<const __nv_bfloat16*>(a.q) + (row < 0 ? 0 : row) * D + y * 8, row >= 0);
+    }
+  }
+  cp_async_wait_all();
+  __syncwarp();
+  for (int r0 = w * 32; r0 < rows; r0 += n * 32)
+#pragma unroll 1
+    for (int s = 0; s < 32; s += kRows) {
+      const int r = r0 + s + lane / kLanes, part = lane % kLanes;
+      uint32_t u[16];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            to + (y & 1) * kTerm + pf_place8<D>(r, 2 * part + (y >> 1)));
+        u[4 * y] = v.x;
+        u[4 * y + 1] = v.y;
+        u[4 * y + 2] = v.z;
+        u[4 * y + 3] = v.w;
+      }
+      uint32_t two = 0;
+#pragma unroll
+      for (int y = 0; y < 16; ++y) two = __vmaxu2(two, u[y] & 0x7fff7fffu);
+      uint32_t top = max(two << 16, two & 0xffff0000u);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // e stays in range for bf16 subnormals
+      const int e = max(int(top >> 23) - 127 - 7, -110);
+      const float down = q8_pow2(-e);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t hw[4], lw[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          uint32_t h[2], o[2];  // a bf16 number of this range is one of fp16 as well
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t x = u[8 * y + 2 * z + q];
+            uint32_t v, g;
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                : "=r"(v)
+                : "f"(__uint_as_float(x & 0xffff0000u) * down), "f"(__uint_as_float(x << 16) * down));
+            h[q] = f16x2_to_e4m3(v);
+            g = e4m3x2_to_f16(h[q]);
+            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(g) : "r"(v), "r"(g));
+            o[q] = f16x2_to_e4m3(g);
+          }
+          hw[z] = h[0] | h[1] << 16;
+          lw[z] = o[0] | o[1] << 16;
+        }
+        uint8_t* at = to + pf_place8<D>(r, 2 * part + y);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(at + kTerm) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      }
+      // a row with an infinity or a NaN: its scores are NaN
+      if (part == 0)
+        factor[r] = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : q8_pow2(e) * a.scale_log2;
+    }
+}
+
+// O of a row times `by`.
+template <int D>
+__device__ __forceinline__ void pf_rescale(uint32_t o_addr, float by) {
+#pragma unroll 1
+  for (int y = 0; y < D; y += 32) {
+    float o[32];
+    tmem_ld32(o_addr + y, o);
+    tmem_wait_ld();
+    tmem_tie32(o);
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[x] *= by;
+    tmem_st16(o_addr + y, reinterpret_cast<uint32_t*>(o));
+    tmem_st16(o_addr + y + 16, reinterpret_cast<uint32_t*>(o) + 16);
+  }
+}
 
 template <int D>
-__global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(const PfArgs a) {
+__global__ void __launch_bounds__(kPfThreads, 1)
+    kv_prefix_attention_kernel(const __grid_constant__ PfArgs a,
+                               const __grid_constant__ CUtensorMap map) {
   using S = PfShape<D>;
-  constexpr int NS = S::kSlots, kTile = S::kTileBytes;
-  constexpr int kMmaWarp = (kPfSoftmax + kPfLoad) / 32, kWalkWarp = kMmaWarp + 1;
-  extern __shared__ __align__(1024) uint8_t sm[];  // ring of K and V, queries, the rest
-  uint8_t* q_s = sm + NS * kTile;
-  PfShared& sh = *reinterpret_cast<PfShared*>(q_s + kPfQueries * kTile);
+  constexpr int KS = S::kKSlots, RS = S::kRawSlots, VS = S::kVSlots, NT = S::kTiles;
+  constexpr int kCode = S::kCodeBytes, kWide = S::kWideBytes;
+  constexpr int kMmaWarp = (kPfSoftmax + kPfLoad) / 32, kWalkWarp = kMmaWarp + 2,
+                kFindWarp = kMmaWarp + 3;
+  extern __shared__ __align__(1024) uint8_t sm[];  // V, queries, K, V as cached, the rest
+  uint8_t* q_s = sm + VS * kWide;
+  uint8_t* k_s = q_s + kPfQueries * kWide;
+  uint8_t* raw_s = k_s + KS * kCode;
+  typename S::Shared& sh = *reinterpret_cast<typename S::Shared*>(raw_s + RS * kCode);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < kPfItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], (kPfSoftmax + kPfLoad) / 32 + 1);
+      mbar_init(&sh.item_empty[i], kPfSoftmax / 32 + 3);
+    }
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], kPfLoad / 32);
     }
     for (int i = 0; i < kPfQueries; ++i) {
-      mbar_init(&sh.q_full[i], 32);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_full[i], kPfSoftmax / 32);
+      mbar_init(&sh.q_empty[i], 2);
     }
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.kv_full[i], kPfLoad / 32);
-      mbar_init(&sh.kv_empty[i], 1);
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 2);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&sh.v_full[i], kPfLoad / 32);
+      mbar_init(&sh.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -237,15 +392,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(cons
       mbar_init(&sh.told[i], 128);
       mbar_init(&sh.read[i], 128);
     }
-    mbar_init(&sh.drained, 1);
-    sh.guard.abort = 0;
-    sh.guard.limit_ns = a.wait_ns;
+    mbar_init(&sh.drained, 2);
+    sh.guard.abort = sh.guard.beat[0] = sh.guard.beat[1] = sh.guard.done[0] = sh.guard.done[1] = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  if (warp == kFindWarp && lane == 0) tma_prefetch_map(&map);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -255,19 +410,293 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(cons
   const bool work = int(blockIdx.x) < plan.nc;
   PfGuard* guard = &sh.guard;
 
-  // The next item, as the other roles take it; false: no more.
-  auto next_item = [&](PfRing<kPfItems>& ring, PfItem& it) {
-    pf_wait(&sh.item_full[ring.at], ring.phase, guard, a.err);
-    if (__any_sync(0xffffffffu, guard->aborted())) return false;
-    it = sh.item[ring.at];
-    return it.stop == 0;
+  // Whether there is a next item (by a whole warp).
+  auto next_item = [&](const PfRing<kPfItems>& ring) {
+    const bool came = pf_wait(&sh.item_full[ring.at], ring.phase, guard);
+    if (!__all_sync(0xffffffffu, came)) return false;
+    return sh.item[ring.at].stop == 0;
   };
 
-  if (work && warp == kWalkWarp) {
+  // What the registers are moved for has to stand in a branch of its own.
+  if (work && warp < kPfSoftmax / 32) {
+    setmaxnreg_inc<kPfSoftmaxRegs>();
+    // ---------------------------------------------------------------- softmax
+    const int g = warp >> 2, row = tid & 127;
+    const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lane_addr + g * 128, o_addr = lane_addr + 256 + g * 128;
+    PfRing<kPfItems> ring;
+    uint32_t s_phase = 0, o_phase = 0, told_phase = 0;
+    int seq = 0, count = 0;  // key tiles, M tiles of the items before
+    bool begun = false;
+    while (next_item(ring)) {
+      PfItem& it = sh.item[ring.at];
+      if (!begun) {
+        for (int m = 0; m <= it.two; ++m) {
+          pf_prepare<D>(a, plan, it, m * kPfTile, q_s + m * kWide, sh.factor[m], (warp + 4 * m) & 7,
+                        kPfSoftmax / 32);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full[m]);
+        }
+        begun = true;
+      }
+      const int two = it.two, own = it.own, tiles = it.t1 - it.t0;
+      const bool begins = it.t0 == 0;
+      const int turns = two ? tiles : (tiles + 1 - g) / 2;
+      const int x0 = (two ? g * kPfTile : 0) + row;
+      int b, t, n;
+      const int64_t query = pf_query(a, plan, it, x0, b, t, n);
+      const float* factor = sh.factor[(count + (two ? g : 0)) % kPfFactors];
+      const int seq0 = seq;
+      seq += tiles;
+      count += 1 + two;
+      // the new tokens that the query sees, as bits
+      uint32_t bits = 0;
+      if (own && query >= 0) {
+        bits = a.tree ? a.tree[int64_t(b) * a.T + t] : (2u << t) - 1u;
+        if (n < 32) bits &= (1u << n) - 1u;
+      }
+      const bool any = __any_sync(0xffffffffu, query >= 0);
+      float c = 0.0f;
+      float ref = -INFINITY, l = 0.0f;  // ref: of the scores before the row's factor
+      bool stop = false;
+#pragma unroll 1
+      for (int i = 0; i < turns; ++i) {
+        const bool came = pf_wait(&sh.s_full[g], s_phase, guard);
+        s_phase ^= 1;
+        stop = !__all_sync(0xffffffffu, came);
+        if (stop) break;
+        tc_fence_after();
+        if (i == 0) c = factor[row];  // (the products waited for the queries)
+        const PfTile& tile = sh.tile[(seq0 + (two ? i : 2 * i + g)) % NT];
+        const int x1 = x0 - tile.first;
+        const bool live = query >= 0 && (!own || (x1 >= 0 && x1 < tile.n * a.G));
+        if (__any_sync(0xffffffffu, live)) {
+          float z[128];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) tmem_ld32(s_addr + 32 * y, z + 32 * y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) tmem_tie32(z + 32 * y);
+          const bool plain = tile.plain_k;  // the maximum of a part is taken before its scale
+          if (!plain) {
+#pragma unroll
+            for (int x = 0; x < 128; ++x) z[x] *= tile.ks[x / kPfPart];
+          }
+          // all queries of the warp see all keys
+          const int d0 = tile.pos - tile.L;
+          if (!__all_sync(0xffffffffu, live || query < 0) || d0 + kPfTile > 0) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // keys from position d on, relative to the row's L
+              const int d = d0 + 32 * y;
+              const uint32_t m = !live ? 0u : d <= -32 ? ~0u : d < 0 ? (bits << -d) | ((1u << -d) - 1u)
+                                 : d < 32 ? bits >> d : 0u;
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!(m >> x & 1u)) z[32 * y + x] = -INFINITY;
+            }
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < kPfParts; ++y) {
+            const float* v = z + 16 * y;
+            float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
+            m0 = max3(m0, v[6], v[7]);
+            m1 = max3(m1, v[8], v[9]);
+            m0 = max3(m0, v[10], v[11]);
+            m1 = max3(m1, v[12], v[13]);
+            top = fmaxf(top, max3(m0, m1, fmaxf(v[14], v[15])) * (plain ? tile.ks[y] : 1.0f));
+          }
+          const bool moves = __any_sync(0xffffffffu, (top - ref) * c > kPfSlack);
+          float down = 1.0f;
+          if (moves) {
+            // -inf - -inf is NaN: not greater, and the reference stays unset
+            const float to = fmaxf(ref, top);
+            down = to == -INFINITY ? 1.0f : ex2_approx((ref - to) * c);
+            l *= down;
+            ref = to;
+          }
+          const float minus = ref == -INFINITY ? 0.0f : -ref * c;
+          float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+          const float2 minus2 = make_float2(minus, minus);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float by = (plain ? tile.ks[y] : 1.0f) * c;
+            const float2 by2 = make_float2(by, by);
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+              const float2 e = __ffma2_rn(make_float2(z[16 * y + x], z[16 * y + x + 1]), by2, minus2);
+              const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              if (x & 2) sum1 = __fadd2_rn(sum1, p);
+              else sum0 = __fadd2_rn(sum0, p);
+              const __nv_bfloat162 v = __floats2bfloat162_rn(p.x, p.y);
+              w[x / 2] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            tmem_st8(s_addr + 8 * y, reinterpret_cast<const float*>(w));
+          }
+          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          // The output before this tile is done: its products were issued before the scores. (O
+          // of a row that had no tile yet is zero.)
+          if (moves && i > 0) pf_rescale<D>(o_addr, down);
+          tmem_wait_st();
+        } else if (any) {
+          // another row's tile
+          const uint32_t none[16] = {};
+#pragma unroll 1
+          for (int y = 0; y < 64; y += 16) tmem_st16(s_addr + y, none);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[g]);
+        if (row == 0) *reinterpret_cast<volatile int*>(&sh.guard.beat[g]) = seq0 + i + 1;
+      }
+      // released only now: the factors' places are counted by items
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
+      ring.next();
+      if (stop) break;
+      if (turns == 0) continue;
+      // ------------------------------------------------------------ the piece's end
+      pf_wait(&sh.o_full[g], o_phase, guard);
+      o_phase ^= 1;
+      const bool both = !two && tiles > 1;
+      float m = ref == -INFINITY ? -INFINITY : ref * c;
+      float mine = 1.0f, other = 0.0f;
+      if (both) {
+        sh.part[g][row] = make_float2(m, l);
+        mbar_arrive(&sh.told[g]);
+        pf_wait(&sh.told[g ^ 1], told_phase, guard);
+        const float2 st = sh.part[g ^ 1][row];
+        const float mn = fmaxf(m, st.x), base = mn == -INFINITY ? 0.0f : mn;
+        mine = ex2_approx(m - base);
+        other = ex2_approx(st.x - base);
+        l = l * mine + st.y * other;
+        m = mn;
+      }
+      if (__any_sync(0xffffffffu, guard->aborted())) break;
+      tc_fence_after();
+      if (any) {
+        const int64_t at = begins ? query : int64_t(blockIdx.x) * 256 + x0;
+        float* to = (begins ? a.parts[own] : a.mid) + (query < 0 ? 0 : at) * D;
+        if (query >= 0 && (!both || g == 0))
+          (begins ? a.stats[own] : a.mid_stats)[at] = make_float2(m, l);
+        // with both groups' parts each takes half of the numbers
+        const int y0 = both ? g * (D / 2) : 0, y1 = both ? y0 + D / 2 : D;
+#pragma unroll 1
+        for (int y = y0; y < y1; y += 32) {
+          float o[32];
+          tmem_ld32(o_addr + y, o);
+          if (both) {
+            float o2[32];
+            tmem_ld32(lane_addr + 256 + (g ^ 1) * 128 + y, o2);
+            tmem_wait_ld();
+            tmem_tie32(o);
+            tmem_tie32(o2);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = o[x] * mine + o2[x] * other;
+          } else {
+            tmem_wait_ld();
+            tmem_tie32(o);
+          }
+          if (query >= 0) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 4)
+              *reinterpret_cast<float4*>(to + y + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (both) {
+        mbar_arrive(&sh.read[g ^ 1]);
+        pf_wait(&sh.read[g], told_phase, guard);
+        told_phase ^= 1;
+        if (__any_sync(0xffffffffu, guard->aborted())) break;
+      }
+    }
+    if (row == 0) *reinterpret_cast<volatile int*>(&sh.guard.done[g]) = 1;
+  } else if (work && warp < kMmaWarp) {
+    setmaxnreg_dec<kPfLoadRegs>();
+    // ---------------------------------------------------------------- values
+    // From the codes in shared memory to bf16. (Read into registers from global memory, the
+    // code of two tiles in flight was four times as long, and the instruction cache too small.)
+    constexpr int kPerKey = D / 16;              // 16-byte chunks of a key's codes
+    constexpr int kAtOnce = 32 / kPerKey;        // keys of a warp's step
+    constexpr int kSteps = kPfTile * kPerKey / kPfLoad;
+    constexpr int kKeyStep = kPfTile / kSteps;   // from step to step: a part, or two
+    static_assert(kKeyStep % kPfPart == 0, "a lane's keys are in the same place of their parts");
+    const int lw = warp - kPfSoftmax / 32;
+    // a quarter of the warp writes two keys that are not 8 apart: no bank twice
+    const int chunk = D == 128 ? (lane & 3) + 4 * (lane >> 3 & 1) : lane & 3;
+    const int key0 = lw * kAtOnce + (D == 128 ? (lane >> 2 & 1) + 2 * (lane >> 4) : lane >> 2);
+    // (a lane's keys are multiples of 8 apart: the swizzles are the same)
+    const uint32_t from = pf_place8<D>(key0, chunk);
+    const uint32_t place0 = pf_place(key0, 2 * chunk), place1 = pf_place(key0, 2 * chunk + 1);
+    PfRing<RS> rr;
+    PfRing<VS> vr;
+    for (;; rr.next(), vr.next()) {
+      bool came = pf_wait(&sh.raw_full[rr.at], rr.phase, guard);
+      const int what = sh.raw_tile[rr.at];
+      came = came && what >= 0 && pf_wait(&sh.v_empty[vr.at], vr.phase ^ 1, guard);
+      if (!__all_sync(0xffffffffu, came)) break;
+      const PfTile& t = sh.tile[what];
+      const uint8_t* raw = raw_s + rr.at * kCode + from;
+      uint8_t* to = sm + vr.at * kWide;
+      const bool plain = t.plain_v;
+      const int keys = t.keys, valid = t.valid;
+#pragma unroll 2
+      for (int i = 0; i < kSteps; ++i) {
+        const int key = key0 + i * kKeyStep, part = key / kPfPart;
+        uint4 v = *reinterpret_cast<const uint4*>(raw + i * kKeyStep * D);
+        // what was not copied, or lies past the end
+        if (key >= keys || !(valid >> part & 1)) v = make_uint4(0u, 0u, 0u, 0u);
+        const float scale = t.vs[part];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t r[8];
+        if (plain) {
+          // the product with scale * 2^120 is exact
+          const uint32_t up = ((__float_as_uint(scale) >> 23) + 120 << 7) * 0x00010001u;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            r[2 * y] = mul_bf16x2(e4m3_in_bf16<0x9180u>(w[y]), up);
+            r[2 * y + 1] = mul_bf16x2(e4m3_in_bf16<0xb3a2u>(w[y]), up);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float f[4];
+            e4m3x4_to_f32(w[y], f);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {  // nor may a product overflow; a NaN stays
+              f[z] *= scale;
+              f[z] = f[z] > kMaxBf16 ? kMaxBf16 : f[z] < -kMaxBf16 ? -kMaxBf16 : f[z];
+            }
+            const __nv_bfloat162 v0 = __floats2bfloat162_rn(f[0], f[1]);
+            const __nv_bfloat162 v1 = __floats2bfloat162_rn(f[2], f[3]);
+            r[2 * y] = *reinterpret_cast<const uint32_t*>(&v0);
+            r[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&v1);
+          }
+        }
+        *reinterpret_cast<uint4*>(to + place0 + i * kKeyStep * 128) =
+            make_uint4(r[0], r[1], r[2], r[3]);
+        *reinterpret_cast<uint4*>(to + place1 + i * kKeyStep * 128) =
+            make_uint4(r[4], r[5], r[6], r[7]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.raw_empty[rr.at]);
+        mbar_arrive(&sh.v_full[vr.at]);
+      }
+    }
+  } else if (work) {
+    setmaxnreg_dec<kPfOtherRegs>();
+    if (warp == kWalkWarp) {
     // ---------------------------------------------------------------- work list, queries
     const int64_t u_end = pf_share(plan, blockIdx.x + 1);
     int64_t u = pf_share(plan, blockIdx.x);
-    const int entries = plan.NG + a.B;
+    const int pack = pf_pack(a.T * a.G);
+    const int entries = plan.NG + (a.B + pack - 1) / pack;
     int lo = 0, hi = entries - 1;  // the last entry that begins at or before u
     while (lo < hi) {
       const int m = (lo + hi + 1) >> 1;
@@ -275,9 +704,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(cons
       else hi = m - 1;
     }
     int e = lo;
-    PfRing<kPfItems> ring;
-    PfRing<kPfQueries> qring;
-    for (;;) {
+    // the piece that begins at u, and u past it; stop at the end
+    auto describe = [&]() {
       PfItem it = {};
       it.stop = 1;
       while (u < u_end && e < entries) {
@@ -286,36 +714,35 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(cons
           ++e;
           continue;
         }
-        int64_t nq;
-        int tiles;
+        const int64_t per_h = len / a.H;
+        int64_t nq, tiles;
         if (e < plan.NG) {
           const PfGroup g = plan.groups[e];
+          it.own = 0;
           it.row = g.row;
+          it.rows = 1;
           it.entry = g.entry;
           nq = int64_t(g.count) * a.T * a.G;
           tiles = g.tiles;
-          it.own = 0;
-          it.tile0 = 0;
-          it.L = it.end = tiles * kPfTile;
-          it.n = 0;
         } else {
-          const PfRow r = plan.rows[e - plan.NG];
-          it.row = e - plan.NG;
-          nq = int64_t(r.n) * a.G;
-          tiles = r.tiles;
           it.own = 1;
-          it.tile0 = r.skip;
-          it.L = r.L;
-          it.n = r.n;
-          it.end = r.L + r.n;
+          it.row = (e - plan.NG) * pack;
+          it.rows = min(pack, a.B - it.row);
+          if (pack > 1) {
+            nq = it.rows * a.T * a.G;
+            tiles = per_h;
+          } else {
+            const PfRow r = plan.rows[it.row];
+            nq = int64_t(r.n) * a.G;
+            tiles = r.tiles;
+          }
         }
-        const int64_t per_h = pf_units(nq, tiles);
         const int64_t in = u - base, h = per_h > 0 ? in / per_h : a.H, in_h = in - h * per_h;
         if (tiles <= 0 || nq <= 0 || h >= a.H || it.row < 0 || it.row >= a.B)
           break;  // not a plan that was made here
-        const int64_t qb = in_h / (2 * int64_t(tiles));
+        const int64_t qb = in_h / (2 * tiles);
         const int w = nq - qb * 256 > 128 ? 2 : 1;
-        const int64_t at = in_h - qb * 2 * tiles, stop = min(int64_t(w) * tiles, at + (u_end - u));
+        const int64_t at = in_h - qb * 2 * tiles, stop = min(w * tiles, at + (u_end - u));
         it.h = int(h);
         it.two = w == 2;
         it.q0 = int(qb * 256);
@@ -328,475 +755,363 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(cons
           break;
         }
       }
-      pf_wait(&sh.item_empty[ring.at], ring.phase ^ 1, guard, a.err);
+      return it;
+    };
+    // Items are described as far ahead as there are places, whatever their queries wait for.
+    // The first item's queries are the softmax warps' to prepare.
+    PfRing<kPfItems> ring, qitem;
+    PfRing<kPfQueries> qring;
+    int ahead = 0, m = 0;  // items whose queries are not there; M tile of the first of them
+    int count = 0;         // M tiles before it
+    bool ended = false, begun = false;
+    // Between its work the warp watches: tiles have to be done.
+    const volatile PfGuard* watch = &sh.guard;
+    uint64_t since = global_ns();
+    int seen = 0;
+    while (!ended || ahead > 0 || !watch->done[0] || !watch->done[1]) {
       if (__any_sync(0xffffffffu, guard->aborted())) break;
+      const int beats = watch->beat[0] + watch->beat[1];
+      if (beats != seen) since = global_ns();
+      seen = beats;
+      if (!ended && ahead < kPfItems &&
+          __all_sync(0xffffffffu, mbar_test_wait(&sh.item_empty[ring.at], ring.phase ^ 1))) {
+        const PfItem it = describe();
+        if (lane == 0) {
+          sh.item[ring.at] = it;
+          mbar_arrive(&sh.item_full[ring.at]);
+        }
+        __syncwarp();
+        ring.next();
+        ended = it.stop;
+        if (!begun) {
+          qitem.next();
+          for (; !ended && count <= it.two; ++count) qring.next();
+        } else if (!ended) {
+          ++ahead;
+        }
+        begun = true;
+        continue;
+      }
+      if (ahead > 0 &&
+          __all_sync(0xffffffffu, mbar_test_wait(&sh.q_empty[qring.at], qring.phase ^ 1))) {
+        const PfItem& it = sh.item[qitem.at];
+        const int two = it.two;
+        pf_prepare<D>(a, plan, it, m * kPfTile, q_s + qring.at * kWide,
+                      sh.factor[count % kPfFactors], 0, 1);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(&sh.q_full[qring.at], kPfSoftmax / 32);
+        qring.next();
+        ++count;
+        if (++m > two) {
+          m = 0;
+          --ahead;
+          qitem.next();
+        }
+        continue;
+      }
+      // nothing has a place yet
+      __nanosleep(500);
+      if (global_ns() - since > a.wait_ns) {
+        *reinterpret_cast<volatile int*>(&guard->abort) = 1;
+        if (a.err) atomicOr(a.err, SPEC_DERR_TIMEOUT);
+      }
+    }
+    } else if (warp == kFindWarp) {
+    // ---------------------------------------------------------------- where the tiles are
+    // Four tiles at a time, a lane a part: ids, then scales. Copies of K and V are started here, in
+    // the order in which the products take them: those
+    // go through steps, in each of which first group 0, then group 1 takes the output of its
+    // tile before (V), then the scores of the next (K).
+    PfRing<kPfItems> ring;
+    PfRing<RS> rr;
+    PfRing<KS> kr;
+    // slots that have been copied to, and the phase of the last copy (V's from bit 16)
+    uint32_t started = 0, started_phase = 0;
+    bool ok = true, half = false;  // half: group 1 has not had its turn in the step
+    int seq = 0, pend0 = -1, pend1 = -1;
+    // V of a tile; -1: no more
+    auto values = [&](int what) {
+      const bool came = ok && pf_wait(&sh.raw_empty[rr.at], rr.phase ^ 1, guard);
+      ok = __all_sync(0xffffffffu, came);
+      if (!ok) return;
+      if (what < 0) {
+        if (lane == 0) {
+          sh.raw_tile[rr.at] = what;
+          mbar_arrive(&sh.raw_full[rr.at]);
+        }
+        return;
+      }
+      const PfTile& tile = sh.tile[what];
       if (lane == 0) {
-        sh.item[ring.at] = it;
-        mbar_arrive(&sh.item_full[ring.at]);
+        sh.raw_tile[rr.at] = what;
+        mbar_arrive_expect_tx(&sh.raw_full[rr.at], __popc(tile.valid) * kPfPart * D);
       }
       __syncwarp();
-      ring.next();
-      if (it.stop) break;
-      for (int m = 0; m <= it.two; ++m) {
-        pf_wait(&sh.q_empty[qring.at], qring.phase ^ 1, guard, a.err);
-        if (__any_sync(0xffffffffu, guard->aborted())) break;
-        uint8_t* to = q_s + qring.at * kTile;
-        int64_t mine[kPfTile / 32];  // rows lane, lane + 32, ...
-#pragma unroll
-        for (int i = 0; i < kPfTile / 32; ++i) {
-          int t;
-          mine[i] = pf_query(a, plan, it, m * kPfTile + 32 * i + lane, t);
-        }
-        constexpr int kChunks = D / 8;  // of a row
-#pragma unroll
-        for (int i = 0; i < kPfTile / 32; ++i)
-#pragma unroll 4
-          for (int x = 0; x < kChunks; ++x) {
-            const int c = x * 32 + lane, r = c / kChunks;  // r: of these 32 rows
-            const int64_t row = __shfl_sync(0xffffffffu, mine[i], r);
-            cp_async16(to + pf_place(32 * i + r, c % kChunks),
-                       static_cast<const __nv_bfloat16*>(a.q) + (row < 0 ? 0 : row) * D +
-                           c % kChunks * 8,
-                       row >= 0);
-          }
-        cp_async_wait_all();
-        fence_async_smem();
-        mbar_arrive(&sh.q_full[qring.at]);
-        qring.next();
-      }
-    }
-  } else if (work && warp == kMmaWarp) {
-    // ---------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = tc_idesc(1, 1, 0, 0, kPfTile, kPfTile);
-      constexpr uint32_t idesc_o = tc_idesc(1, 1, 0, 1, kPfTile, D);
-      const uint64_t kv0 = tc_desc(smem_u32(sm), kPfTile * 128, 1024, 2);
-      const uint64_t q0 = tc_desc(smem_u32(q_s), kPfTile * 128, 1024, 2);
-      PfRing<kPfItems> ring;
-      PfRing<kPfQueries> qring;
-      PfRing<NS> kv;
-      uint32_t p_phase[2] = {0, 0};
-      bool pending[2] = {false, false}, first[2] = {}, last[2] = {}, shared[2] = {};
-      int v_slot = 0;  // of a V tile that both groups take
-      auto output = [&](int g) {
-        if (!pending[g]) return;
-        pending[g] = false;
-        int slot = v_slot;
-        if (!(shared[g] && g == 1)) {
-          slot = v_slot = kv.at;
-          pf_wait(&sh.kv_full[kv.at], kv.phase, guard, a.err);
-          kv.next();
-        }
-        pf_wait(&sh.p_full[g], p_phase[g], guard, a.err);
-        p_phase[g] ^= 1;
-        if (guard->aborted()) return;
-        tc_fence_after();
-        const uint64_t v = kv0 + slot * (kTile / 16);
-#pragma unroll
-        for (int x = 0; x < kPfTile / 16; ++x)
-          tc_mma_bf16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * x, v + x * 128, idesc_o,
-                         !(first[g] && x == 0));
-        if (!(shared[g] && g == 0)) tc_commit(&sh.kv_empty[slot]);
-        if (last[g]) tc_commit(&sh.o_full[g]);
-      };
-      for (;;) {
-        pf_wait(&sh.item_full[ring.at], ring.phase, guard, a.err);
-        if (guard->aborted()) break;
-        const PfItem& it = sh.item[ring.at];
-        if (it.stop) break;
-        const int two = it.two, tiles = it.t1 - it.t0;
-        mbar_arrive(&sh.item_empty[ring.at]);
-        ring.next();
-        const int steps = two ? tiles : (tiles + 1) / 2;
-        int qs[2];
-        uint32_t qp[2];
-        qs[0] = qs[1] = qring.at;
-        qp[0] = qp[1] = qring.phase;
-        qring.next();
-        if (two) {
-          qs[1] = qring.at;
-          qp[1] = qring.phase;
-          qring.next();
-        }
-        int k_slot = 0;
-        for (int s = 0; s < steps; ++s) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            output(g);
-            const bool on = two || 2 * s + g < tiles;
-            if (!on || guard->aborted()) continue;
-            if (s == 0 && (two || g == 0)) pf_wait(&sh.q_full[qs[g]], qp[g], guard, a.err);
-            if (!(two && g == 1)) {
-              k_slot = kv.at;
-              pf_wait(&sh.kv_full[kv.at], kv.phase, guard, a.err);
-              kv.next();
-            }
-            if (guard->aborted()) continue;
-            tc_fence_after();
-            const uint64_t k = kv0 + k_slot * (kTile / 16), q = q0 + qs[g] * (kTile / 16);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              const int at = (x & 3) * 2 + (x >> 2) * (kPfTile * 128 / 16);
-              tc_mma_bf16(tmem + g * 128, q + at, k + at, idesc_s, x > 0);
-            }
-            if (!(two && g == 0)) tc_commit(&sh.kv_empty[k_slot]);
-            tc_commit(&sh.s_full[g]);
-            pending[g] = true;
-            first[g] = s == 0;
-            shared[g] = two;
-            last[g] = two ? s + 1 == steps : 2 * (s + 1) + g >= tiles;
-            // the item's last scores of these queries
-            if (two ? s + 1 == steps : 2 * s + g + 1 == tiles) tc_commit(&sh.q_empty[qs[g]]);
-          }
-          if (guard->aborted()) break;
-        }
-      }
-      output(0);
-      output(1);
-    }
-    __syncwarp();
-  } else if (work && warp < kPfSoftmax / 32) {
-    // ---------------------------------------------------------------- softmax
-    const int g = warp >> 2, row = tid & 127;
-    const uint32_t lane_addr = tmem + (uint32_t((warp & 3) * 32) << 16);
-    const uint32_t s_addr = lane_addr + g * 128;
-    PfRing<kPfItems> ring;
-    uint32_t s_phase = 0, o_phase = 0, told_phase = 0;
-    PfItem it;
-    while (next_item(ring, it)) {
+      if (lane < kPfParts && tile.plane[lane] >= 0)
+        tma_tile_3d(raw_s + rr.at * kCode + lane * kPfPart * D, &map, 0, tile.in_block[lane],
+                    tile.plane[lane], &sh.raw_full[rr.at]);
+      started |= 0x10000u << rr.at;
+      started_phase = (started_phase & ~(0x10000u << rr.at)) | rr.phase << (16 + rr.at);
+      rr.next();
+    };
+    auto values0 = [&]() {
+      if (pend0 >= 0) values(pend0);
+      pend0 = -1;
+    };
+    auto values1 = [&]() {
+      if (pend1 >= 0) values(pend1);
+      pend1 = -1;
+      half = false;
+    };
+    auto row_of = [&](int b) {  // L, n, first tile, tiles
+      return b < a.B ? *reinterpret_cast<const int4*>(plan.rows + b) : make_int4(0, 0, 0, 0);
+    };
+    while (ok && next_item(ring)) {
+      const PfItem it = sh.item[ring.at];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
       ring.next();
-      const int tiles = it.t1 - it.t0;
-      const int turns = it.two ? tiles : (tiles + 1 - g) / 2;
-      if (turns == 0) continue;
-      int t;
-      const int64_t query = pf_query(a, plan, it, (it.two ? g * kPfTile : 0) + row, t);
-      // the new tokens that the query sees, as bits
-      uint32_t bits = 0;
-      if (it.own && query >= 0) {
-        bits = a.tree ? a.tree[int64_t(it.row) * a.T + t] : (2u << t) - 1u;
-        if (it.n < 32) bits &= (1u << it.n) - 1u;
-      }
-      const bool live = __any_sync(0xffffffffu, query >= 0);
-      const float c = a.scale_log2;
-      float ref = -INFINITY, l = 0.0f;  // ref: of the scores before they are scaled
-      bool stop = false;
-#pragma unroll 1
-      for (int i = 0; i < turns; ++i) {
-        const int p0 = (it.tile0 + it.t0 + (it.two ? i : 2 * i + g)) * kPfTile;
-        pf_wait(&sh.s_full[g], s_phase, guard, a.err);
-        s_phase ^= 1;
-        stop = __any_sync(0xffffffffu, guard->aborted());
-        if (stop) break;
-        tc_fence_after();
-        if (live) {
-          const bool masked = p0 + kPfTile > it.L;
-          auto hide = [&](float* z, int at) {  // of the 32 keys from position `at`
-            const int d = at - it.L;
-            const uint32_t m = d <= -32 ? ~0u : d < 0 ? (bits << -d) | ((1u << -d) - 1u)
-                               : d < 32 ? bits >> d : 0u;
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!(m >> x & 1u)) z[x] = -INFINITY;
-          };
-          float top = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < 4; y += 2) {
-            float z[64];
-            tmem_ld32(s_addr + 32 * y, z);
-            tmem_ld32(s_addr + 32 * y + 32, z + 32);
-            tmem_wait_ld();
-            if (masked) {
-              hide(z, p0 + 32 * y);
-              hide(z + 32, p0 + 32 * y + 32);
-            }
-            float m[4] = {top, z[0], z[1], z[2]};
-#pragma unroll
-            for (int x = 3; x < 64; x += 1) m[x & 3] = fmaxf(m[x & 3], z[x]);
-            top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-          }
-          if (__any_sync(0xffffffffu, (top - ref) * c > kPfSlack)) {
-            // -inf - -inf is NaN: not greater, and the reference stays unset
-            const float to = fmaxf(ref, top);
-            const float by = to == -INFINITY ? 1.0f : ex2_approx((ref - to) * c);
-            l *= by;
-            ref = to;
-            if (i > 0) {
-              // the output before this tile is done: its products were issued before the scores
-#pragma unroll 1
-              for (int y = 0; y < D; y += 32) {
-                float o[32];
-                tmem_ld32(lane_addr + 256 + g * 128 + y, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= by;
-                tmem_st16(lane_addr + 256 + g * 128 + y, reinterpret_cast<uint32_t*>(o));
-                tmem_st16(lane_addr + 256 + g * 128 + y + 16, reinterpret_cast<uint32_t*>(o) + 16);
-              }
-            }
-          }
-          const float minus = ref == -INFINITY ? 0.0f : -ref * c;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float z[32];
-            uint32_t w[16];
-            tmem_ld32(s_addr + 32 * y, z);
-            tmem_wait_ld();
-            if (masked) hide(z, p0 + 32 * y);
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              const float e0 = ex2_approx(fmaf(z[x], c, minus));
-              const float e1 = ex2_approx(fmaf(z[x + 1], c, minus));
-              sum[x & 3] += e0;
-              sum[(x & 3) + 1] += e1;
-              const __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
-              w[x / 2] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            tmem_st16(s_addr + 16 * y, w);  // over scores that have been read
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          tmem_wait_st();
+      int row = it.row, in_row = it.t0;  // the tile's row, and its place among the row's own
+      int4 now = make_int4(INT32_MAX, 0, 0, INT32_MAX), then = now;
+      if (it.own) {
+        now = row_of(row);
+        while (in_row >= now.w && row + 1 < it.row + it.rows) {
+          in_row -= max(now.w, 0);
+          now = row_of(++row);
         }
-        tc_fence_before();
-        mbar_arrive(&sh.p_full[g]);
+        then = row_of(row + 1);
       }
-      if (stop) break;
-      // ------------------------------------------------------------ the piece's end
-      pf_wait(&sh.o_full[g], o_phase, guard, a.err);
-      o_phase ^= 1;
-      const bool both = !it.two && tiles > 1;
-      float m = ref == -INFINITY ? -INFINITY : ref * c;
-      float mine = 1.0f, other = 0.0f;
-      if (both) {
-        sh.part[g][row] = make_float2(m, l);
-        mbar_arrive(&sh.told[g]);
-        pf_wait(&sh.told[g ^ 1], told_phase, guard, a.err);
-        const float2 st = sh.part[g ^ 1][row];
-        const float mn = fmaxf(m, st.x), base = mn == -INFINITY ? 0.0f : mn;
-        mine = ex2_approx(m - base);
-        other = ex2_approx(st.x - base);
-        l = l * mine + st.y * other;
-        m = mn;
-      }
-      if (__any_sync(0xffffffffu, guard->aborted())) break;
-      tc_fence_after();
-      if (live) {
-        const bool begins = it.t0 == 0;
-        const int64_t at = begins ? query
-                                  : int64_t(blockIdx.x) * 256 + (it.two ? g * kPfTile : 0) + row;
-        float* to = (begins ? a.parts[it.own] : a.mid) + (query < 0 ? 0 : at) * D;
-        if (query >= 0 && (!both || g == 0))
-          (begins ? a.stats[it.own] : a.mid_stats)[at] = make_float2(m, l);
-        // with both groups' parts each takes half of the numbers
-        const int y0 = both ? g * (D / 2) : 0, y1 = both ? y0 + D / 2 : D;
-#pragma unroll 1
-        for (int y = y0; y < y1; y += 32) {
-          float o[32];
-          tmem_ld32(lane_addr + 256 + g * 128 + y, o);
-          if (both) {
-            float o2[32];
-            tmem_ld32(lane_addr + 256 + (g ^ 1) * 128 + y, o2);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = o[x] * mine + o2[x] * other;
-          } else {
-            tmem_wait_ld();
-          }
-          if (query >= 0) {
-#pragma unroll
-            for (int x = 0; x < 32; x += 4)
-              *reinterpret_cast<float4*>(to + y + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-          }
+      for (int t = it.t0; t < it.t1 && ok;) {
+        if (in_row >= now.w) {
+          in_row = 0;
+          do {
+            now = then;
+            then = row_of(++row + 1);
+          } while (now.w <= 0 && row + 1 < it.row + it.rows);
         }
-      }
-      tc_fence_before();
-      if (both) {
-        mbar_arrive(&sh.read[g ^ 1]);
-        pf_wait(&sh.read[g], told_phase, guard, a.err);
-        told_phase ^= 1;
-        if (__any_sync(0xffffffffu, guard->aborted())) break;
-      }
-    }
-  } else if (work && warp < (kPfSoftmax + kPfLoad) / 32) {
-    // ---------------------------------------------------------------- keys and values
-    constexpr int kPerKey = D / 16;              // 16-byte chunks of a key's codes
-    constexpr int kAtOnce = 32 / kPerKey;        // keys of a warp's load
-    constexpr int kLoads = kPfTile * kPerKey / kPfLoad;
-    constexpr int kPfAhead = D == 128 ? 2 : 4;   // tiles in flight
-    const int lw = warp - kPfSoftmax / 32;
-    // a quarter of the warp writes two keys that are not 8 apart: no bank twice
-    const int chunk = D == 128 ? (lane & 3) + 4 * (lane >> 3 & 1) : lane & 3;
-    const int sub = D == 128 ? (lane >> 2 & 1) + 2 * (lane >> 4) : lane >> 2;
-    // the key of load i and place s of it; each lane finds one key's address
-    static_assert(kLoads * kAtOnce == 32, "a warp's keys of a tile");
-    auto key_of = [&](int i, int s) { return i * (kPfTile / kLoads) + lw * kAtOnce + s; };
-    const int found = key_of(lane / kAtOnce, lane % kAtOnce);
-
-    PfRing<kPfItems> ring;
-    PfItem it;
-    bool have = next_item(ring, it), stalled = false;
-    int step = 0, phase = 0;
-    PfTile pend0 = {}, pend1 = {};
-    bool pending0 = false, pending1 = false;  // group 1 shares a tile with group 0: not pending
-    // the tiles in their order; false: no more
-    auto advance = [&](PfTile& out) {
-      for (;;) {
-        const int at = phase;
-        if (at == 0) {
-          ++phase;
-          if (pending0) {
-            pending0 = false;
-            out = pend0;
-            out.v = true;
-            return true;
-          }
-          continue;
+        const int many = min(min(4, it.t1 - t), now.w - in_row);
+        if (many <= 0 || row >= a.B) {
+          ok = false;  // not a plan that was made here: the waits run out
+          break;
         }
-        if (at == 2) {
-          ++phase;
-          if (pending1) {
-            pending1 = false;
-            out = pend1;
-            out.v = true;
-            return true;
-          }
-          continue;
-        }
-        if (!have) {
-          if (at == 3) return false;
-          ++phase;
-          continue;
-        }
-        const int tiles = it.t1 - it.t0;
-        const int x = it.two ? step : 2 * step + (at >> 1);
-        const bool on = it.two ? at == 1 : x < tiles;
+        const int end = it.own ? now.x + now.y : INT32_MAX;
+        const int pos = (now.z + in_row + (lane >> 3)) * kPfTile + (lane & 7) * kPfPart;
+        const bool on = lane >> 3 < many && pos < end;
+        const int j = pos / a.bs, in_block = pos - j * a.bs;
+        int id = -1;
+        if (on && j < a.MB) id = a.bt[int64_t(row) * a.MB + j];
+        int plane = -1;
+        float ks = 1.0f, vs = 1.0f;
         if (on) {
-          out.row = it.row;
-          out.h = it.h;
-          out.p0 = (it.tile0 + it.t0 + x) * kPfTile;
-          out.end = it.end;
-          out.own = it.own;
-          out.v = false;
-          if (at == 1) {
-            pend0 = out;
-            pending0 = true;
+          if (id >= 0 && id < a.NB) {
+            const float* at = a.scales + id * a.block_scales + it.h;
+            ks = at[0];
+            vs = at[a.H];
+            plane = id * a.planes_per_block + a.plane0 + it.h;
+            // values that are no numbers would reach the pack's other rows (0 * NaN): they are
+            // zero here, and their keys NaN
+            if (!(fabsf(vs) <= FLT_MAX)) {
+              vs = 0.0f;
+              ks = __uint_as_float(0x7fc00000u);
+            }
           } else {
-            pend1 = out;
-            pending1 = true;
+            // keys that cannot be read: their queries' outputs become NaN
+            ks = __uint_as_float(0x7fc00000u);
+            if (a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
           }
         }
-        if (++phase == 4) {
-          phase = 0;
-          if (++step == (it.two ? tiles : (tiles + 1) / 2)) {
-            step = 0;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
-            ring.next();
-            have = next_item(ring, it);
+        const uint32_t vu = __float_as_uint(vs);
+        const uint32_t k_plain = __ballot_sync(0xffffffffu, ks > 0.0f && ks <= FLT_MAX),
+                       v_plain = __ballot_sync(0xffffffffu, (vu & 0x807fffffu) == 0 &&
+                                                                vu >> 23 >= 27 && vu >> 23 <= 134);
+#pragma unroll 1
+        for (int x = 0; x < many && ok; ++x, ++t, ++in_row, ++seq) {
+          const int g = it.two ? 0 : (t - it.t0) & 1, at = seq % NT;
+          if (g == 0) {
+            if (half) values1();
+            values0();
+          } else {
+            values1();
+          }
+          // the test of a wait that runs out: this row's keys never come
+          if (it.own && row == a.stall_row) ok = false;
+          const bool came = ok && pf_wait(&sh.k_empty[kr.at], kr.phase ^ 1, guard);
+          ok = __all_sync(0xffffffffu, came);
+          if (!ok) break;
+          const bool mine = lane >> 3 == x;
+          const uint32_t valid = __ballot_sync(0xffffffffu, mine && plane >= 0);
+          if (mine) {
+            PfTile& tile = sh.tile[at];
+            tile.plane[lane & 7] = plane < 0 ? -1 : plane + a.H;
+            tile.in_block[lane & 7] = in_block;
+            tile.ks[lane & 7] = ks;
+            tile.vs[lane & 7] = vs;
+            if ((lane & 7) == 0) {
+              tile.pos = pos;
+              tile.L = now.x;
+              tile.n = now.y;
+              tile.first = it.rows > 1 ? (row - it.row) * a.T * a.G : 0;
+              tile.keys = min(kPfTile, end - pos);
+              tile.valid = valid >> 8 * x & 255u;
+              tile.plain_k = (k_plain >> 8 * x & 255u) == 255u;
+              tile.plain_v = (v_plain >> 8 * x & 255u) == 255u;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[kr.at], __popc(valid) * kPfPart * D);
+          started |= 1u << kr.at;
+          started_phase = (started_phase & ~(1u << kr.at)) | kr.phase << kr.at;
+          __syncwarp();
+          if (mine && plane >= 0)
+            tma_tile_3d(k_s + kr.at * kCode + (lane & 7) * kPfPart * D, &map, 0, in_block, plane,
+                        &sh.k_full[kr.at]);
+          kr.next();
+          if (g == 1) {
+            pend1 = at;
+          } else {
+            pend0 = at;
+            if (it.two) values1();
+            else half = true;
           }
         }
-        if (on) return true;
       }
-    };
-
-    PfTile tile[kPfAhead];
-    bool full[kPfAhead];
-    uint4 code[kPfAhead][kLoads];
-    float scale[kPfAhead];  // of the key that this lane finds
-    // where the codes are: found by one lane a key, passed to those that load it
-    auto issue = [&](int x) {
-      const PfTile& t = tile[x];
-      const int pos = t.p0 + found;
-      int64_t from = -1;
-      scale[x] = 1.0f;
-      if (pos < t.end) {
-        const int j = pos / a.bs;
-        const int id = j < a.MB ? a.bt[int64_t(t.row) * a.MB + j] : -1;
-        const int unit = (t.v ? a.H : 0) + t.h;
-        if (id >= 0 && id < a.NB) {
-          scale[x] = a.scales[id * a.block_scales + unit];
-          from = id * a.block_bytes + (int64_t(unit) * a.bs + (pos - j * a.bs)) * D;
-        } else {
-          // a key that cannot be read: its queries' outputs become NaN
-          if (!t.v) scale[x] = __uint_as_float(0x7fc00000u);
-          if (a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int64_t at = __shfl_sync(0xffffffffu, from, i * kAtOnce + sub);
-        code[x][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0) code[x][i] = load_codes(a.pool + at + chunk * 16);
-      }
-    };
-    PfRing<NS> kv;
-    auto widen = [&](int x) {
-      pf_wait(&sh.kv_empty[kv.at], kv.phase ^ 1, guard, a.err);
-      uint8_t* to = sm + kv.at * kTile;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int key = key_of(i, sub);
-        const float s = __shfl_sync(0xffffffffu, scale[x], i * kAtOnce + sub);
-        const uint32_t bits = __float_as_uint(s), exponent = bits >> 23;
-        const uint32_t w[4] = {code[x][i].x, code[x][i].y, code[x][i].z, code[x][i].w};
-        uint32_t r[8];
-        if ((bits & 0x807fffffu) == 0 && exponent >= 27 && exponent <= 134) {
-          // 2^-100 .. 2^7: the product with scale * 2^120 is exact
-          const uint32_t up = ((exponent + 120) << 7) * 0x00010001u;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            r[2 * y] = mul_bf16x2(e4m3_in_bf16<0x9180u>(w[y]), up);
-            r[2 * y + 1] = mul_bf16x2(e4m3_in_bf16<0xb3a2u>(w[y]), up);
-          }
-        } else {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float f[4];
-            e4m3x4_to_f32(w[y], f);
-            const __nv_bfloat162 v0 = __floats2bfloat162_rn(f[0] * s, f[1] * s);
-            const __nv_bfloat162 v1 = __floats2bfloat162_rn(f[2] * s, f[3] * s);
-            r[2 * y] = *reinterpret_cast<const uint32_t*>(&v0);
-            r[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&v1);
-          }
-        }
-        *reinterpret_cast<uint4*>(to + pf_place(key, 2 * chunk)) = make_uint4(r[0], r[1], r[2], r[3]);
-        *reinterpret_cast<uint4*>(to + pf_place(key, 2 * chunk + 1)) =
-            make_uint4(r[4], r[5], r[6], r[7]);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.kv_full[kv.at]);
-      kv.next();
-    };
-#pragma unroll
-    for (int x = 0; x < kPfAhead; ++x) {
-      full[x] = (x == 0 || full[x > 0 ? x - 1 : 0]) && advance(tile[x]);
-      if (full[x]) issue(x);
     }
-    for (bool more = true; more;) {
+    if (half) values1();
+    values0();
+    values1();
+    values(-1);
+    // a wait has run out: copies in flight end before the CTA does
+    if (__any_sync(0xffffffffu, guard->aborted())) {
+      for (int i = 0; i < KS; ++i)
+        if (started >> i & 1u) mbar_wait(&sh.k_full[i], started_phase >> i & 1u);
+      for (int i = 0; i < RS; ++i)
+        if (started >> (16 + i) & 1u) mbar_wait(&sh.raw_full[i], started_phase >> (16 + i) & 1u);
+    }
+    } else {
+    // ---------------------------------------------------------------- products
+    // A warp a group, each with its own order: the output of a tile, then the next scores,
+    // which take the place of that tile's probabilities. Tiles that only the other group
+    // takes are waited for and released too, so that no warp falls two rounds behind in a
+    // ring, where the parity of its waits would mislead it.
+    if (lane == 0) {
+      constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // K and queries: 128- or 64-byte swizzle
+      constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, kPfTile, kPfTile);
+      constexpr uint32_t idesc_o = tc_idesc(1, 1, 0, 1, kPfTile, D);
+      const int g = warp - kMmaWarp;
+      const uint64_t k0 = tc_desc(smem_u32(k_s), 16, 8 * D, kSwz);
+      const uint64_t v0 = tc_desc(smem_u32(sm), kPfTile * 128, 1024, 2);
+      const uint32_t k_hi = uint32_t(k0 >> 32), v_hi = uint32_t(v0 >> 32), k_lo = uint32_t(k0),
+                     v_lo = uint32_t(v0), q_lo = uint32_t(tc_desc(smem_u32(q_s), 16, 8 * D, kSwz));
+      const uint32_t s_at = tmem + g * 128, o_at = tmem + 256 + g * 128;
+      PfRing<kPfItems> ring;
+      PfRing<kPfQueries> qring;
+      PfRing<KS> kr;
+      PfRing<VS> vr;
+      uint32_t p_phase = 0;
+      // outputs that wait: group 0's, group 1's, whether both of one V tile; of this group's,
+      // whether it is its item's first and last
+      bool pend0 = false, pend1 = false, shared = false, first = false, last = false;
+      bool ok = true;  // no wait has run out
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        ok = ok && pf_wait(bar, phase, guard);
+      };
+      auto pass_q = [&]() {
+        wait(&sh.q_full[qring.at], qring.phase);
+        mbar_arrive(&sh.q_empty[qring.at]);
+        qring.next();
+      };
+      auto pass_k = [&]() {
+        wait(&sh.k_full[kr.at], kr.phase);
+        mbar_arrive(&sh.k_empty[kr.at]);
+        kr.next();
+      };
+      auto pass_v = [&]() {
+        wait(&sh.v_full[vr.at], vr.phase);
+        mbar_arrive(&sh.v_empty[vr.at]);
+        vr.next();
+      };
+      // steps of items, and one after the last for the outputs that wait
+      for (bool more = true; more && ok;) {
+        wait(&sh.item_full[ring.at], ring.phase);
+        if (!ok) break;
+        const PfItem& it = sh.item[ring.at];
+        more = !it.stop;
+        const int two = more && it.two, tiles = more ? it.t1 - it.t0 : 0;
+        if (more) mbar_arrive(&sh.item_empty[ring.at]);
+        ring.next();
+        PfRing<kPfQueries> q = qring;
+        uint32_t q_desc = 0;
+        int x = two ? 0 : g;  // this group's next tile of the item
+        const int by = two ? 1 : 2, steps = !more ? 1 : (tiles + by - 1) / by;
+#pragma unroll 1
+        for (int s = 0; s < steps && ok; ++s, x += by) {
+          const bool on1 = two || 2 * s + 1 < tiles;
+          if (g == 1 && !shared && pend0) pass_v();
+          if (g ? pend1 : pend0) {
+            wait(&sh.v_full[vr.at], vr.phase);
+            wait(&sh.p_full[g], p_phase);
+            if (!ok) break;
+            p_phase ^= 1;
+            tc_fence_after();
+            const uint32_t v_desc = v_lo + vr.at * (kWide / 16);
 #pragma unroll
-      for (int x = 0; x < kPfAhead; ++x) {
-        if (!more) continue;
-        more = full[x];
-        if (!more) continue;
-        stalled = stalled || (tile[x].own && tile[x].v && tile[x].row == a.stall_row);
-        if (stalled || __any_sync(0xffffffffu, guard->aborted())) {
-          more = false;
-          continue;
+            for (int y = 0; y < kPfTile / 16; ++y)
+              pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
+            tc_commit(&sh.v_empty[vr.at]);
+            if (last) tc_commit(&sh.o_full[g]);
+            vr.next();
+          }
+          if (s == 0 && more) {
+            // the queries; the first half's are not group 1's
+            if (g == 1 && two) pass_q();
+            q = qring;
+            qring.next();
+            wait(&sh.q_full[q.at], q.phase);
+            if (g == 1 && tiles == 1 && !two) mbar_arrive(&sh.q_empty[q.at]);
+            q_desc = q_lo + q.at * (kWide / 16);
+          }
+          if (g == 1 && !two && more) pass_k();
+          if (x < tiles) {
+            wait(&sh.k_full[kr.at], kr.phase);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t k_desc = k_lo + kr.at * (kCode / 16);
+            // both terms of the queries into one sum
+#pragma unroll
+            for (int y = 0; y < 2 * (D / 32); ++y) {
+              const int z = y % (D / 32), term = y / (D / 32);
+              pf_mma_s(s_at, q_desc + term * (kCode / 16) + 2 * z, k_desc + 2 * z, k_hi, idesc_s,
+                       y > 0);
+            }
+            tc_commit(&sh.s_full[g]);
+            tc_commit(&sh.k_empty[kr.at]);
+            kr.next();
+            first = s == 0;
+            last = x + by >= tiles;
+            // the item's last scores of these queries
+            if (last) tc_commit(&sh.q_empty[q.at]);
+            if (last && two && g == 0) pass_q();
+          }
+          if (g == 0) {
+            if (pend1 && !shared) pass_v();
+            if (on1 && !two) pass_k();
+          }
+          pend0 = more;
+          pend1 = on1;
+          shared = two;
         }
-        widen(x);
-        full[x] = full[(x + kPfAhead - 1) % kPfAhead] && advance(tile[x]);
-        if (full[x]) issue(x);
       }
+    }
+    __syncwarp();
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (sh.guard.abort) {
     // what has been issued ends before the CTA's memory is another's
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       if (lane == 0) tc_commit(&sh.drained);
       __syncwarp();
       mbar_wait(&sh.drained, 0);
@@ -810,20 +1125,51 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv_prefix_attention_kernel(cons
 
 namespace {
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
 template <int D>
-int launch_shape(const PfArgs& a, int ctas, cudaStream_t st) {
+int launch_shape(const PfArgs& a, const CUtensorMap& map, int ctas, cudaStream_t st) {
   auto kern = kv_prefix_attention_kernel<D>;
   constexpr size_t smem = PfShape<D>::kBytes;
   static std::atomic<uint64_t> done{0};
   if (allow_smem(kern, smem, done) != SPEC_OK) return SPEC_ECUDA;
-  return launch_pdl(kern, dim3(unsigned(ctas)), dim3(kPfThreads), smem, st, a);
+  return launch_pdl(kern, dim3(unsigned(ctas)), dim3(kPfThreads), smem, st, a, map);
 }
 
 }  // namespace
 
-int launch_pf_attention(const PfArgs& a, int ctas, void* stream) {
+int launch_pf_attention(const PfArgs& a, const void* pool_base, int64_t planes, int ctas,
+                        void* stream) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) return SPEC_ECUDA;
+  CUtensorMap map;
+  const cuuint64_t dims[3] = {cuuint64_t(a.D), cuuint64_t(a.bs), cuuint64_t(planes)};
+  const cuuint64_t strides[2] = {cuuint64_t(a.D), cuuint64_t(a.bs) * a.D};
+  const cuuint32_t box[3] = {cuuint32_t(a.D), kPfPart, 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool_base), dims, strides, box,
+          step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          a.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return SPEC_ECUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a.D == 128 ? launch_shape<128>(a, ctas, st) : launch_shape<64>(a, ctas, st);
+  return a.D == 128 ? launch_shape<128>(a, map, ctas, st) : launch_shape<64>(a, map, ctas, st);
 }
 
 }  // namespace sv

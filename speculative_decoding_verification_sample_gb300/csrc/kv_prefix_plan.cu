@@ -148,7 +148,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     return bad || live[g] < 2 ? 0
                               : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs / kPfTile);
   };
-  const int entries = a.NG + a.B, per = (entries + kPlanThreads - 1) / kPlanThreads;
+  const int pack = pf_pack(a.T * a.G);
+  const int entries = a.NG + (a.B + pack - 1) / pack, per = (entries + kPlanThreads - 1) / kPlanThreads;
   auto entry = [&](int e, bool write) -> int64_t {
     if (e < a.NG) {
       const int tiles = shared_tiles(e);
@@ -156,22 +157,26 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       if (write) groups[e] = PfGroup{tiles, tiles > 0 ? a.members[first[e]] : 0, s0, many};
       return a.H * pf_units(int64_t(many) * a.T * a.G, tiles);
     }
-    const int b = e - a.NG;
-    PfRow r = {};
-    const bool ok = lengths(b, r.L, r.n);
-    r.group = r.at = -1;
-    const int i = row_entry[b];
-    if (ok && r.n > 0 && i != INT32_MAX) {
-      const int g = group_of(i);
-      r.skip = shared_tiles(g);
-      if (r.skip > 0) {
-        r.group = g;
-        r.at = i - a.starts[g];
+    int64_t units = 0;
+    const int b0 = (e - a.NG) * pack, b1 = min(a.B, b0 + pack);
+    for (int b = b0; b < b1; ++b) {
+      PfRow r = {};
+      const bool ok = lengths(b, r.L, r.n);
+      r.group = r.at = -1;
+      const int i = row_entry[b];
+      if (ok && r.n > 0 && i != INT32_MAX) {
+        const int g = group_of(i);
+        r.skip = shared_tiles(g);
+        if (r.skip > 0) {
+          r.group = g;
+          r.at = i - a.starts[g];
+        }
       }
+      r.tiles = !ok ? -1 : r.n == 0 ? 0 : (r.L + r.n + kPfTile - 1) / kPfTile - r.skip;
+      if (write) rows[b] = r;
+      if (r.tiles > 0) units += pack > 1 ? r.tiles : pf_units(int64_t(r.n) * a.G, r.tiles);
     }
-    r.tiles = !ok ? -1 : r.n == 0 ? 0 : (r.L + r.n + kPfTile - 1) / kPfTile - r.skip;
-    if (write) rows[b] = r;
-    return r.tiles > 0 ? a.H * pf_units(int64_t(r.n) * a.G, r.tiles) : 0;
+    return a.H * units;
   };
   int64_t sum = 0;
   for (int x = 0; x < per; ++x) {
@@ -280,11 +285,12 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
       for (int i = 0; i < N; ++i) o[i] = o[i] * x + v[i] * y;
       m = mn;
     };
-    // the parts of one entry's item that holds query qi of its nq
-    auto gather = [&](int e, int which, int64_t qi, int64_t nq, int tiles) {
-      const int64_t per_h = pf_units(nq, tiles), qb = qi / 256;
-      const int w = nq - qb * 256 > 128 ? 2 : 1;
-      const int64_t u = p.prefix[e] + h * per_h + qb * 2 * tiles, end = u + int64_t(w) * tiles;
+    // the parts of the item that holds query qi of an entry's nq
+    auto gather = [&](int e, int which, int qi, int64_t nq, int64_t tiles) {
+      const int64_t base = p.prefix[e], per_h = (p.prefix[e + 1] - base) / a.H;
+      const int qb = qi / 256, w = nq - qb * 256 > 128 ? 2 : 1;
+      if (tiles == 0) tiles = per_h;  // a pack: all of its rows'
+      const int64_t u = base + h * per_h + qb * 2 * tiles, end = u + w * tiles;
       add(a.parts[which] + query * D, a.stats[which][query]);
       const int c0 = pf_owner(p, u), c1 = pf_owner(p, end - 1);
       for (int c = c0 + 1; c <= c1; ++c) {
@@ -297,9 +303,11 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
     if (!bad && t < row.n) {
       if (row.group >= 0) {
         const PfGroup g = p.groups[row.group];
-        gather(row.group, 0, int64_t(row.at) * R + r, int64_t(g.count) * R, g.tiles);
+        gather(row.group, 0, row.at * R + r, int64_t(g.count) * R, g.tiles);
       }
-      if (row.tiles > 0) gather(p.NG + b, 1, r, int64_t(row.n) * a.G, row.tiles);
+      const int pack = pf_pack(R);
+      if (pack > 1) gather(p.NG + b / pack, 1, b % pack * R + r, 128, 0);
+      else if (row.tiles > 0) gather(p.NG + b, 1, r, int64_t(row.n) * a.G, row.tiles);
     }
     const float inv = bad ? __uint_as_float(0x7fc00000u) : l == 0.0f ? 0.0f : 1.0f / l;
     uint32_t x[N / 2];
@@ -342,7 +350,9 @@ Places places(int64_t queries, int D) {
 
 }  // namespace
 
-bool kv_prefix_takes(int dtype, int D) { return dtype == SPEC_BF16 && (D == 64 || D == 128); }
+bool kv_prefix_takes(int dtype, int D, int bs, int64_t planes) {
+  return dtype == SPEC_BF16 && (D == 64 || D == 128) && bs % 16 == 0 && planes <= INT32_MAX;
+}
 
 size_t kv_prefix_workspace(int B, int T, int Hq, int D) {
   return places(int64_t(B) * T * Hq, D).bytes;
@@ -402,7 +412,10 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
     if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   }
   const int ctas = sms < kPfMaxCtas ? sms : kPfMaxCtas;
-  const int st = launch_pf_attention(a, ctas, k.stream);
+  a.plane0 = k.layer * 2 * k.H;
+  a.planes_per_block = k.num_layers * 2 * k.H;
+  const int st = launch_pf_attention(a, k.pool, int64_t(k.num_blocks) * a.planes_per_block, ctas,
+                                     k.stream);
   if (st != SPEC_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
   const dim3 grid(unsigned(a.B * a.H));

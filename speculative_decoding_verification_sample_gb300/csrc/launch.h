@@ -188,7 +188,7 @@ struct KvPrefixPlanLaunch {
 
 int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k);
 size_t kv_prefix_plan_size(int B, int num_groups, int num_members);
-bool kv_prefix_takes(int dtype, int D);
+bool kv_prefix_takes(int dtype, int D, int bs, int64_t planes);
 size_t kv_prefix_workspace(int B, int T, int Hq, int D);
 int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t plan_bytes);
 int launch_kv_reserve(const KvReserveLaunch& k);
