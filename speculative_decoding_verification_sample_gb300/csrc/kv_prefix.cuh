@@ -10,9 +10,9 @@
 //
 // Entries: first the groups, then the rows' own keys. A group's queries (all rows of it,
 // row by row) are taken in blocks of 256, two M tiles of the tensor core, the last one
-// maybe one tile; a row's queries R = T G likewise, but with R <= 64 as many consecutive
-// rows as fit share one M tile, a pack: their key tiles follow each other, and a tile's
-// probabilities are zero for the other rows of the pack. (An item for each row, with 20 of
+// maybe one tile; a row's queries R = T G likewise, but with R <= 32 four consecutive rows,
+// with R <= 64 two, share one M tile, a pack: their key tiles follow each other, and a tile's
+// probabilities are zero for the other rows of the pack, which are other warps'. (An item for each row, with 20 of
 // 128 places in use, spent 15 us each on its beginning and end.) An item is (entry, kv
 // head, block); it costs `w` units a key tile, w its M tiles. The units of all items form
 // one list, entries outermost, then kv heads, blocks, tiles; CTA c of NC takes units
@@ -70,7 +70,7 @@ __host__ __device__ inline PfLayout pf_layout(int B, int NG, int NE) {
 }
 
 // Rows of a pack with R queries each.
-__host__ __device__ inline int pf_pack(int R) { return R <= 64 ? 128 / R : 1; }
+__host__ __device__ inline int pf_pack(int R) { return R <= 32 ? 4 : R <= 64 ? 2 : 1; }
 
 // Units of one kv head of an entry with nq queries and `tiles` key tiles.
 __host__ __device__ inline int64_t pf_units(int64_t nq, int tiles) {

@@ -45,6 +45,7 @@ static_assert(256 * kPfSoftmaxRegs + 128 * (kPfLoadRegs + kPfOtherRegs) == 65536
 constexpr int kPfItems = 6;     // items described at a time
 constexpr int kPfQueries = 2;   // M tiles of queries held at a time
 constexpr int kPfFactors = 16;  // M tiles whose rows' factors are held: more than kPfItems items have
+constexpr int kPfTurns = 8;     // steps that group 0 may be ahead of group 1 (K's slots: fewer)
 constexpr int kPfPart = 16;     // keys of a part of a tile: of one block (block_size % 16 == 0)
 constexpr int kPfParts = kPfTile / kPfPart;
 constexpr float kMaxBf16 = 0x1.fep127f;
@@ -70,6 +71,7 @@ struct PfItem {
   int own;        // 0 a group's prefix, 1 rows' own keys
   int row, rows;  // prefix: a row of the group; own keys: the first row, rows of the pack
   int entry;      // prefix: the group's first member
+  int stride;     // a pack's queries from row to row; 0: no pack
   int h;
   int t0, t1;     // tiles of the item
   int q0, nq;     // first query of the block in its entry, queries of the block
@@ -78,11 +80,12 @@ struct PfItem {
 // A key tile: what the warps need of it.
 struct PfTile {
   int plane[kPfParts], in_block[kPfParts];  // where the parts' V is (plane -1: nowhere)
-  float ks[kPfParts], vs[kPfParts];         // scales of K, of V
-  int pos, L, n, first;      // position, its row's tokens (a prefix: L past all), the row's first
-                             // query of the M tile
-  int keys, valid;           // keys of the tile that there are; bits: parts that can be read
-  int plain_k, plain_v;      // K's scales are positive and finite; V's 2^-100 .. 2^7
+  float2 ks[kPfParts];       // of K: scale, and -inf for a part that is hidden (else 0)
+  float raw_ks[kPfParts], vs[kPfParts];     // the scales of K where one is below 0, of V
+  int pos, L;                // position; committed tokens of its row
+  int slot, last;            // the row's place in the pack; whether it is the row's last tile
+  int keys, valid;           // keys up to the row's end; bits: parts that are copied
+  int below, plain_v;        // a scale of K is below 0; V's are 2^-100 .. 2^7
 };
 
 // kTiles: more than the key tiles between their finding and the end of their V: one being
@@ -104,6 +107,7 @@ struct PfShape {
     uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
     uint64_t q_full[kPfQueries], q_empty[kPfQueries];
     uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+    uint64_t turn[kPfTurns];
     uint64_t s_full[2], p_full[2], o_full[2], told[2], read[2], drained;
     uint32_t tmem;
     PfGuard guard;
@@ -150,7 +154,9 @@ __device__ __forceinline__ int64_t pf_query(const PfArgs& a, const PfPlan& p, co
   t = n = 0;
   if (x >= it.nq) return -1;
   const int R = a.T * a.G, qi = it.q0 + x;
-  const int e = it.own && it.rows == 1 ? 0 : qi / R, r = qi - e * R;
+  const int each = !it.own ? R : it.stride;  // queries from row to row
+  const int e = each == 0 ? 0 : qi / each, r = qi - e * each;
+  if (r >= R) return -1;
   if (it.own) b = it.row + e;
   else b = it.entry + e < p.NE ? p.members[it.entry + e] : -1;
   if (b < 0 || b >= a.B) return -1;
@@ -174,6 +180,19 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void store8(float* p, const float* f) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(f[0]), "f"(f[1]),
+               "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -392,10 +411,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&sh.told[i], 128);
       mbar_init(&sh.read[i], 128);
     }
+    for (int i = 0; i < kPfTurns; ++i) mbar_init(&sh.turn[i], 1);
     mbar_init(&sh.drained, 2);
     sh.guard.abort = sh.guard.beat[0] = sh.guard.beat[1] = sh.guard.done[0] = sh.guard.done[1] = 0;
     fence_mbar_init();
   }
+  // parts of K that are not copied hold numbers of an earlier tile, or these
+  for (int i = tid; i < KS * kCode / 16; i += kPfThreads)
+    reinterpret_cast<uint4*>(k_s)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_async_smem();
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         begun = true;
       }
-      const int two = it.two, own = it.own, tiles = it.t1 - it.t0;
+      const int two = it.two, own = it.own, stride = it.stride, tiles = it.t1 - it.t0;
       const bool begins = it.t0 == 0;
       const int turns = two ? tiles : (tiles + 1 - g) / 2;
       const int x0 = (two ? g * kPfTile : 0) + row;
@@ -469,43 +493,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tc_fence_after();
         if (i == 0) c = factor[row];  // (the products waited for the queries)
         const PfTile& tile = sh.tile[(seq0 + (two ? i : 2 * i + g)) % NT];
-        const int x1 = x0 - tile.first;
-        const bool live = query >= 0 && (!own || (x1 >= 0 && x1 < tile.n * a.G));
-        if (__any_sync(0xffffffffu, live)) {
+        // (a warp's queries are all of one row)
+        if (any && (!own || stride == 0 || row / stride == tile.slot)) {
+          // All of a query's scores at once: a load takes some 800 cycles while products run.
           float z[128];
 #pragma unroll
           for (int y = 0; y < 4; ++y) tmem_ld32(s_addr + 32 * y, z + 32 * y);
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 4; ++y) tmem_tie32(z + 32 * y);
-          const bool plain = tile.plain_k;  // the maximum of a part is taken before its scale
-          if (!plain) {
+          if (tile.below) {  // a scale below zero: the maximum of a part is taken before it else
 #pragma unroll
-            for (int x = 0; x < 128; ++x) z[x] *= tile.ks[x / kPfPart];
+            for (int x = 0; x < 128; ++x) z[x] *= tile.raw_ks[x / kPfPart];
           }
-          // all queries of the warp see all keys
-          const int d0 = tile.pos - tile.L;
-          if (!__all_sync(0xffffffffu, live || query < 0) || d0 + kPfTile > 0) {
+          if (tile.last) {
+            // New tokens, seen by some queries only, and what lies past them: in the last 48 keys
+            // of a row's last tile, whose end is that of the part with the last token.
+            const int d = tile.pos + 80 - tile.L;  // at most 0, as there are at most 32 of them
+            const uint64_t seen = uint64_t(bits) << -d | ((uint64_t(1) << -d) - 1);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {  // keys from position d on, relative to the row's L
-              const int d = d0 + 32 * y;
-              const uint32_t m = !live ? 0u : d <= -32 ? ~0u : d < 0 ? (bits << -d) | ((1u << -d) - 1u)
-                                 : d < 32 ? bits >> d : 0u;
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!(m >> x & 1u)) z[32 * y + x] = -INFINITY;
-            }
+            for (int x = 0; x < 48; ++x)
+              if (!(seen >> x & 1)) z[80 + x] = -INFINITY;
           }
           float top = -INFINITY;
 #pragma unroll
           for (int y = 0; y < kPfParts; ++y) {
-            const float* v = z + 16 * y;
+            const float* v = z + kPfPart * y;
             float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
             m0 = max3(m0, v[6], v[7]);
             m1 = max3(m1, v[8], v[9]);
             m0 = max3(m0, v[10], v[11]);
             m1 = max3(m1, v[12], v[13]);
-            top = fmaxf(top, max3(m0, m1, fmaxf(v[14], v[15])) * (plain ? tile.ks[y] : 1.0f));
+            const float2 k = tile.ks[y];
+            top = fmaxf(top, fmaf(max3(m0, m1, fmaxf(v[14], v[15])), k.x, k.y));
           }
           const bool moves = __any_sync(0xffffffffu, (top - ref) * c > kPfSlack);
           float down = 1.0f;
@@ -518,15 +538,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
           const float minus = ref == -INFINITY ? 0.0f : -ref * c;
           float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
-          const float2 minus2 = make_float2(minus, minus);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float by = (plain ? tile.ks[y] : 1.0f) * c;
-            const float2 by2 = make_float2(by, by);
+          for (int y = 0; y < kPfParts; ++y) {
+            const float2 k = tile.ks[y];
+            const float by = k.x * c, less = minus + k.y;
+            const float2 by2 = make_float2(by, by), less2 = make_float2(less, less);
             uint32_t w[8];
 #pragma unroll
-            for (int x = 0; x < 16; x += 2) {
-              const float2 e = __ffma2_rn(make_float2(z[16 * y + x], z[16 * y + x + 1]), by2, minus2);
+            for (int x = 0; x < kPfPart; x += 2) {
+              const float2 e =
+                  __ffma2_rn(make_float2(z[16 * y + x], z[16 * y + x + 1]), by2, less2);
               const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
               if (x & 2) sum1 = __fadd2_rn(sum1, p);
               else sum0 = __fadd2_rn(sum0, p);
@@ -585,24 +606,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int y0 = both ? g * (D / 2) : 0, y1 = both ? y0 + D / 2 : D;
 #pragma unroll 1
         for (int y = y0; y < y1; y += 32) {
-          float o[32];
+          float o[32], o2[32];
           tmem_ld32(o_addr + y, o);
-          if (both) {
-            float o2[32];
-            tmem_ld32(lane_addr + 256 + (g ^ 1) * 128 + y, o2);
-            tmem_wait_ld();
-            tmem_tie32(o);
-            tmem_tie32(o2);
+          // (without a part of the other group: twice its own, other 0)
+          tmem_ld32(lane_addr + 256 + (both ? g ^ 1 : g) * 128 + y, o2);
+          tmem_wait_ld();
+          tmem_tie32(o);
+          tmem_tie32(o2);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = o[x] * mine + o2[x] * other;
-          } else {
-            tmem_wait_ld();
-            tmem_tie32(o);
-          }
+          for (int x = 0; x < 32; ++x) o[x] = o[x] * mine + o2[x] * other;
           if (query >= 0) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 4)
-              *reinterpret_cast<float4*>(to + y + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+            for (int x = 0; x < 32; x += 8) store8(to + y + x, o + x);
           }
         }
       }
@@ -729,7 +744,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           it.row = (e - plan.NG) * pack;
           it.rows = min(pack, a.B - it.row);
           if (pack > 1) {
-            nq = it.rows * a.T * a.G;
+            it.stride = kPfTile / pack;
+            nq = it.rows * it.stride;
             tiles = per_h;
           } else {
             const PfRow r = plan.rows[it.row];
@@ -892,37 +908,41 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         const int many = min(min(4, it.t1 - t), now.w - in_row);
         if (many <= 0 || row >= a.B) {
-          ok = false;  // not a plan that was made here: the waits run out
+          ok = false;  // not a plan that was made here: the watch ends it
           break;
         }
-        const int end = it.own ? now.x + now.y : INT32_MAX;
-        const int pos = (now.z + in_row + (lane >> 3)) * kPfTile + (lane & 7) * kPfPart;
-        const bool on = lane >> 3 < many && pos < end;
+        // A row's own tiles end with the part of its last token; the first may begin before them.
+        const int end = it.own ? now.x + now.y : INT32_MAX, begin = now.z * kPfTile;
+        const int tile0 = it.own ? (end + kPfPart - 1) / kPfPart * kPfPart - (now.w - in_row) * kPfTile
+                                 : in_row * kPfTile;
+        const int pos = tile0 + (lane >> 3) * kPfTile + (lane & 7) * kPfPart;
+        const bool on = lane >> 3 < many && pos >= begin && pos < end;
         const int j = pos / a.bs, in_block = pos - j * a.bs;
         int id = -1;
         if (on && j < a.MB) id = a.bt[int64_t(row) * a.MB + j];
         int plane = -1;
-        float ks = 1.0f, vs = 1.0f;
+        float2 ks = make_float2(1.0f, on ? 0.0f : -INFINITY);  // scale; -inf: hidden
+        float vs = 1.0f;
         if (on) {
           if (id >= 0 && id < a.NB) {
             const float* at = a.scales + id * a.block_scales + it.h;
-            ks = at[0];
+            ks.x = at[0];
             vs = at[a.H];
             plane = id * a.planes_per_block + a.plane0 + it.h;
             // values that are no numbers would reach the pack's other rows (0 * NaN): they are
             // zero here, and their keys NaN
             if (!(fabsf(vs) <= FLT_MAX)) {
               vs = 0.0f;
-              ks = __uint_as_float(0x7fc00000u);
+              ks.x = __uint_as_float(0x7fc00000u);
             }
           } else {
             // keys that cannot be read: their queries' outputs become NaN
-            ks = __uint_as_float(0x7fc00000u);
+            ks.x = __uint_as_float(0x7fc00000u);
             if (a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
           }
         }
         const uint32_t vu = __float_as_uint(vs);
-        const uint32_t k_plain = __ballot_sync(0xffffffffu, ks > 0.0f && ks <= FLT_MAX),
+        const uint32_t k_below = __ballot_sync(0xffffffffu, ks.x < 0.0f),
                        v_plain = __ballot_sync(0xffffffffu, (vu & 0x807fffffu) == 0 &&
                                                                 vu >> 23 >= 27 && vu >> 23 <= 134);
 #pragma unroll 1
@@ -945,16 +965,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             PfTile& tile = sh.tile[at];
             tile.plane[lane & 7] = plane < 0 ? -1 : plane + a.H;
             tile.in_block[lane & 7] = in_block;
-            tile.ks[lane & 7] = ks;
+            const bool below = k_below >> 8 * x & 255u;
+            tile.ks[lane & 7] = below ? make_float2(1.0f, ks.y) : ks;
+            tile.raw_ks[lane & 7] = ks.x;
             tile.vs[lane & 7] = vs;
             if ((lane & 7) == 0) {
               tile.pos = pos;
               tile.L = now.x;
-              tile.n = now.y;
-              tile.first = it.rows > 1 ? (row - it.row) * a.T * a.G : 0;
+              tile.slot = row - it.row;
+              tile.last = it.own && in_row + 1 == now.w;
               tile.keys = min(kPfTile, end - pos);
               tile.valid = valid >> 8 * x & 255u;
-              tile.plain_k = (k_plain >> 8 * x & 255u) == 255u;
+              tile.below = below;
               tile.plain_v = (v_plain >> 8 * x & 255u) == 255u;
             }
           }
@@ -994,16 +1016,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // which take the place of that tile's probabilities. Tiles that only the other group
     // takes are waited for and released too, so that no warp falls two rounds behind in a
     // ring, where the parity of its waits would mislead it.
-    if (lane == 0) {
+    // The whole warp goes through the loops, so that what the products need is known to be
+    // uniform; one lane issues them.
+    {
       constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // K and queries: 128- or 64-byte swizzle
       constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, kPfTile, kPfTile);
       constexpr uint32_t idesc_o = tc_idesc(1, 1, 0, 1, kPfTile, D);
-      const int g = warp - kMmaWarp;
+      auto uniform = [](uint32_t x) { return __reduce_max_sync(0xffffffffu, x); };
+      const int g = int(uniform(warp)) - kMmaWarp;
+      const uint32_t tmem_u = uniform(tmem);
       const uint64_t k0 = tc_desc(smem_u32(k_s), 16, 8 * D, kSwz);
       const uint64_t v0 = tc_desc(smem_u32(sm), kPfTile * 128, 1024, 2);
       const uint32_t k_hi = uint32_t(k0 >> 32), v_hi = uint32_t(v0 >> 32), k_lo = uint32_t(k0),
                      v_lo = uint32_t(v0), q_lo = uint32_t(tc_desc(smem_u32(q_s), 16, 8 * D, kSwz));
-      const uint32_t s_at = tmem + g * 128, o_at = tmem + 256 + g * 128;
+      const uint32_t s_at = tmem_u + g * 128, o_at = tmem_u + 256 + g * 128;
       PfRing<kPfItems> ring;
       PfRing<kPfQueries> qring;
       PfRing<KS> kr;
@@ -1013,22 +1039,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // whether it is its item's first and last
       bool pend0 = false, pend1 = false, shared = false, first = false, last = false;
       bool ok = true;  // no wait has run out
+      int step = 0;
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        ok = ok && pf_wait(bar, phase, guard);
+        if (ok) ok = __all_sync(0xffffffffu, pf_wait(bar, phase, guard));
       };
       auto pass_q = [&]() {
         wait(&sh.q_full[qring.at], qring.phase);
-        mbar_arrive(&sh.q_empty[qring.at]);
+        if (lane == 0) mbar_arrive(&sh.q_empty[qring.at]);
         qring.next();
       };
       auto pass_k = [&]() {
         wait(&sh.k_full[kr.at], kr.phase);
-        mbar_arrive(&sh.k_empty[kr.at]);
+        if (lane == 0) mbar_arrive(&sh.k_empty[kr.at]);
         kr.next();
       };
       auto pass_v = [&]() {
         wait(&sh.v_full[vr.at], vr.phase);
-        mbar_arrive(&sh.v_empty[vr.at]);
+        if (lane == 0) mbar_arrive(&sh.v_empty[vr.at]);
         vr.next();
       };
       // steps of items, and one after the last for the outputs that wait
@@ -1036,9 +1063,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         wait(&sh.item_full[ring.at], ring.phase);
         if (!ok) break;
         const PfItem& it = sh.item[ring.at];
-        more = !it.stop;
-        const int two = more && it.two, tiles = more ? it.t1 - it.t0 : 0;
-        if (more) mbar_arrive(&sh.item_empty[ring.at]);
+        more = !uniform(it.stop);
+        const int two = more ? uniform(it.two) : 0, tiles = more ? uniform(it.t1 - it.t0) : 0;
+        __syncwarp();
+        if (more && lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
         ring.next();
         PfRing<kPfQueries> q = qring;
         uint32_t q_desc = 0;
@@ -1048,51 +1076,72 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int s = 0; s < steps && ok; ++s, x += by) {
           const bool on1 = two || 2 * s + 1 < tiles;
           if (g == 1 && !shared && pend0) pass_v();
-          if (g ? pend1 : pend0) {
-            wait(&sh.v_full[vr.at], vr.phase);
-            wait(&sh.p_full[g], p_phase);
-            if (!ok) break;
-            p_phase ^= 1;
-            tc_fence_after();
-            const uint32_t v_desc = v_lo + vr.at * (kWide / 16);
-#pragma unroll
-            for (int y = 0; y < kPfTile / 16; ++y)
-              pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
-            tc_commit(&sh.v_empty[vr.at]);
-            if (last) tc_commit(&sh.o_full[g]);
-            vr.next();
-          }
-          if (s == 0 && more) {
-            // the queries; the first half's are not group 1's
-            if (g == 1 && two) pass_q();
-            q = qring;
-            qring.next();
-            wait(&sh.q_full[q.at], q.phase);
-            if (g == 1 && tiles == 1 && !two) mbar_arrive(&sh.q_empty[q.at]);
-            q_desc = q_lo + q.at * (kWide / 16);
-          }
-          if (g == 1 && !two && more) pass_k();
-          if (x < tiles) {
-            wait(&sh.k_full[kr.at], kr.phase);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t k_desc = k_lo + kr.at * (kCode / 16);
-            // both terms of the queries into one sum
-#pragma unroll
-            for (int y = 0; y < 2 * (D / 32); ++y) {
-              const int z = y % (D / 32), term = y / (D / 32);
-              pf_mma_s(s_at, q_desc + term * (kCode / 16) + 2 * z, k_desc + 2 * z, k_hi, idesc_s,
-                       y > 0);
+          // The output and the scores are issued together. An item's first scores wait for its
+          // queries, and the output before them does not wait for that.
+          bool out = g ? pend1 : pend0;
+#pragma unroll 1
+          for (int r = out && s == 0 ? 0 : 1; r < 2 && ok; ++r) {
+            const bool score = r == 1 && x < tiles;
+            if (r == 1) {
+              if (s == 0 && more) {
+                // the first half's queries are not group 1's
+                if (g == 1 && two) pass_q();
+                q = qring;
+                qring.next();
+                wait(&sh.q_full[q.at], q.phase);
+                if (g == 1 && tiles == 1 && !two && lane == 0) mbar_arrive(&sh.q_empty[q.at]);
+                q_desc = q_lo + q.at * (kWide / 16);
+              }
+              if (g == 1 && !two && more) pass_k();
+              if (score) wait(&sh.k_full[kr.at], kr.phase);
             }
-            tc_commit(&sh.s_full[g]);
-            tc_commit(&sh.k_empty[kr.at]);
-            kr.next();
-            first = s == 0;
-            last = x + by >= tiles;
-            // the item's last scores of these queries
-            if (last) tc_commit(&sh.q_empty[q.at]);
-            if (last && two && g == 0) pass_q();
+            if (out) {
+              wait(&sh.v_full[vr.at], vr.phase);
+              // group 0 first: in turns one's products run while the other's softmax does
+              if (g == 1) wait(&sh.turn[step % kPfTurns], step / kPfTurns & 1);
+              wait(&sh.p_full[g], p_phase);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v_desc = v_lo + vr.at * (kWide / 16), k_desc = k_lo + kr.at * (kCode / 16);
+            const bool ends = x + by >= tiles;
+            if (elect_one()) {
+              if (out) {
+#pragma unroll
+                for (int y = 0; y < kPfTile / 16; ++y)
+                  pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
+                tc_commit(&sh.v_empty[vr.at]);
+                if (last) tc_commit(&sh.o_full[g]);
+              }
+              if (score) {
+                // both terms of the queries into one sum
+#pragma unroll
+                for (int y = 0; y < 2 * (D / 32); ++y) {
+                  const int z = y % (D / 32), term = y / (D / 32);
+                  pf_mma_s(s_at, q_desc + term * (kCode / 16) + 2 * z, k_desc + 2 * z, k_hi, idesc_s,
+                           y > 0);
+                }
+                tc_commit(&sh.s_full[g]);
+                tc_commit(&sh.k_empty[kr.at]);
+                // the item's last scores of these queries
+                if (ends) tc_commit(&sh.q_empty[q.at]);
+              }
+            }
+            __syncwarp();
+            if (out) {
+              p_phase ^= 1;
+              vr.next();
+              out = false;
+            }
+            if (score) {
+              kr.next();
+              first = s == 0;
+              last = ends;
+              if (ends && two && g == 0) pass_q();
+            }
           }
+          if (g == 0 && lane == 0) mbar_arrive(&sh.turn[step % kPfTurns]);
+          ++step;
           if (g == 0) {
             if (pend1 && !shared) pass_v();
             if (on1 && !two) pass_k();

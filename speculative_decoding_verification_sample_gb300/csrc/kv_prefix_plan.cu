@@ -172,7 +172,10 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
           r.at = i - a.starts[g];
         }
       }
-      r.tiles = !ok ? -1 : r.n == 0 ? 0 : (r.L + r.n + kPfTile - 1) / kPfTile - r.skip;
+      // they end with the 16 keys of the last token (the first tile may begin in the prefix)
+      r.tiles = !ok ? -1
+                : r.n == 0 ? 0
+                           : ((r.L + r.n + 15) / 16 * 16 - r.skip * kPfTile + kPfTile - 1) / kPfTile;
       if (write) rows[b] = r;
       if (r.tiles > 0) units += pack > 1 ? r.tiles : pf_units(int64_t(r.n) * a.G, r.tiles);
     }
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
         gather(row.group, 0, row.at * R + r, int64_t(g.count) * R, g.tiles);
       }
       const int pack = pf_pack(R);
-      if (pack > 1) gather(p.NG + b / pack, 1, b % pack * R + r, 128, 0);
+      if (pack > 1) gather(p.NG + b / pack, 1, b % pack * (kPfTile / pack) + r, kPfTile, 0);
       else if (row.tiles > 0) gather(p.NG + b, 1, r, int64_t(row.n) * a.G, row.tiles);
     }
     const float inv = bad ? __uint_as_float(0x7fc00000u) : l == 0.0f ? 0.0f : 1.0f / l;
