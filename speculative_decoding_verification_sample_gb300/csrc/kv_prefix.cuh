@@ -14,9 +14,9 @@
 // with R <= 64 two, share one M tile, a pack: their key tiles follow each other, and a tile's
 // probabilities are zero for the other rows of the pack, which are other warps'. (An item for each row, with 20 of
 // 128 places in use, spent 15 us each on its beginning and end.) An item is (entry, kv
-// head, block); it costs `w` units a key tile, w its M tiles. The units of all items form
+// head, block). The units of all items form
 // one list, entries outermost, then kv heads, blocks, tiles; CTA c of NC takes units
-// [W c / NC, W (c + 1) / NC), cut up to whole tiles. A piece that begins its item leaves its
+// [W c / NC, W (c + 1) / NC), of each item the tiles that begin there. A piece that begins its item leaves its
 // part in the place of its queries (one place for the prefix, one for the row's own keys),
 // another one in the place of its CTA, which has at most one such. Everything follows from
 // the plan, so the result does not depend on timing.
@@ -72,11 +72,25 @@ __host__ __device__ inline PfLayout pf_layout(int B, int NG, int NE) {
 // Rows of a pack with R queries each.
 __host__ __device__ inline int pf_pack(int R) { return R <= 32 ? 4 : R <= 64 ? 2 : 1; }
 
-// Units of one kv head of an entry with nq queries and `tiles` key tiles.
-__host__ __device__ inline int64_t pf_units(int64_t nq, int tiles) {
+// What an item costs, about 0.3 us each: its beginning and end (queries, parts), a key tile
+// with two M tiles, one with one. The split only needs their proportions.
+constexpr int kPfItemUnits = 16, kPfTwoUnits = 5, kPfOneUnits = 4;
+__host__ __device__ inline int64_t pf_item_units(int w, int64_t tiles) {
+  return kPfItemUnits + w * tiles;
+}
+// Units of one kv head of an entry with nq queries and `tiles` key tiles (none: no items).
+__host__ __device__ inline int64_t pf_units(int64_t nq, int64_t tiles) {
   const int64_t full = nq / 256;
   const int rest = int(nq % 256);
-  return (2 * full + (rest > 128 ? 2 : rest > 0 ? 1 : 0)) * tiles;
+  if (tiles == 0) return 0;
+  return full * pf_item_units(kPfTwoUnits, tiles) +
+         (rest > 128 ? pf_item_units(kPfTwoUnits, tiles)
+          : rest > 0 ? pf_item_units(kPfOneUnits, tiles)
+                     : 0);
+}
+// Tiles of an item that begin before its unit x.
+__host__ __device__ inline int pf_cut(int64_t x, int w) {
+  return x <= kPfItemUnits ? 0 : int((x - kPfItemUnits + w - 1) / w);
 }
 
 struct PfArgs {

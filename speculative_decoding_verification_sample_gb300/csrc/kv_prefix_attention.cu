@@ -107,7 +107,7 @@ struct PfShape {
     uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
     uint64_t q_full[kPfQueries], q_empty[kPfQueries];
     uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
-    uint64_t turn[kPfTurns];
+    uint64_t turn[2][kPfTurns];
     uint64_t s_full[2], p_full[2], o_full[2], told[2], read[2], drained;
     uint32_t tmem;
     PfGuard guard;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&sh.told[i], 128);
       mbar_init(&sh.read[i], 128);
     }
-    for (int i = 0; i < kPfTurns; ++i) mbar_init(&sh.turn[i], 1);
+    for (int i = 0; i < 2 * kPfTurns; ++i) mbar_init(&sh.turn[0][0] + i, 1);
     mbar_init(&sh.drained, 2);
     sh.guard.abort = sh.guard.beat[0] = sh.guard.beat[1] = sh.guard.done[0] = sh.guard.done[1] = 0;
     fence_mbar_init();
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       uint8_t* to = sm + vr.at * kWide;
       const bool plain = t.plain_v;
       const int keys = t.keys, valid = t.valid;
-#pragma unroll 2
+#pragma unroll 4
       for (int i = 0; i < kSteps; ++i) {
         const int key = key0 + i * kKeyStep, part = key / kPfPart;
         uint4 v = *reinterpret_cast<const uint4*>(raw + i * kKeyStep * D);
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (pack > 1) {
             it.stride = kPfTile / pack;
             nq = it.rows * it.stride;
-            tiles = per_h;
+            tiles = (per_h - kPfItemUnits) / kPfOneUnits;
           } else {
             const PfRow r = plan.rows[it.row];
             nq = int64_t(r.n) * a.G;
@@ -756,15 +756,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int64_t in = u - base, h = per_h > 0 ? in / per_h : a.H, in_h = in - h * per_h;
         if (tiles <= 0 || nq <= 0 || h >= a.H || it.row < 0 || it.row >= a.B)
           break;  // not a plan that was made here
-        const int64_t qb = in_h / (2 * tiles);
-        const int w = nq - qb * 256 > 128 ? 2 : 1;
-        const int64_t at = in_h - qb * 2 * tiles, stop = min(w * tiles, at + (u_end - u));
+        const int64_t qb = in_h / pf_item_units(kPfTwoUnits, tiles);
+        const int w = nq - qb * 256 > 128 ? kPfTwoUnits : kPfOneUnits;
+        const int64_t at = in_h - qb * pf_item_units(kPfTwoUnits, tiles),
+                      stop = min(pf_item_units(w, tiles), at + (u_end - u));
         it.h = int(h);
-        it.two = w == 2;
+        it.two = w == kPfTwoUnits;
         it.q0 = int(qb * 256);
         it.nq = int(min(nq - qb * 256, int64_t(256)));
-        it.t0 = int((at + w - 1) / w);
-        it.t1 = int((stop + w - 1) / w);
+        it.t0 = pf_cut(at, w);
+        it.t1 = pf_cut(stop, w);
         u += stop - at;
         if (it.t0 < it.t1) {
           it.stop = 0;
@@ -1097,8 +1098,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             if (out) {
               wait(&sh.v_full[vr.at], vr.phase);
-              // group 0 first: in turns one's products run while the other's softmax does
-              if (g == 1) wait(&sh.turn[step % kPfTurns], step / kPfTurns & 1);
+              // In turns, so that one group's products run while the other's softmax does: each
+              // waits for the other's products of before to be issued.
+              const int turn = g == 1 ? step : step - 1;
+              if (turn >= 0) wait(&sh.turn[g ^ 1][turn % kPfTurns], turn / kPfTurns & 1);
               wait(&sh.p_full[g], p_phase);
             }
             if (!ok) break;
@@ -1140,7 +1143,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               if (ends && two && g == 0) pass_q();
             }
           }
-          if (g == 0 && lane == 0) mbar_arrive(&sh.turn[step % kPfTurns]);
+          if (lane == 0) mbar_arrive(&sh.turn[g][step % kPfTurns]);
           ++step;
           if (g == 0) {
             if (pend1 && !shared) pass_v();

@@ -179,6 +179,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       if (write) rows[b] = r;
       if (r.tiles > 0) units += pack > 1 ? r.tiles : pf_units(int64_t(r.n) * a.G, r.tiles);
     }
+    if (pack > 1 && units > 0) units = pf_item_units(kPfOneUnits, units);
     return a.H * units;
   };
   int64_t sum = 0;
@@ -291,14 +292,15 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
     // the parts of the item that holds query qi of an entry's nq
     auto gather = [&](int e, int which, int qi, int64_t nq, int64_t tiles) {
       const int64_t base = p.prefix[e], per_h = (p.prefix[e + 1] - base) / a.H;
-      const int qb = qi / 256, w = nq - qb * 256 > 128 ? 2 : 1;
-      if (tiles == 0) tiles = per_h;  // a pack: all of its rows'
-      const int64_t u = base + h * per_h + qb * 2 * tiles, end = u + w * tiles;
+      const int qb = qi / 256, w = nq - qb * 256 > 128 ? kPfTwoUnits : kPfOneUnits;
+      if (tiles == 0) tiles = (per_h - kPfItemUnits) / w;  // a pack: all of its rows'
+      const int64_t u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, tiles),
+                    end = u + pf_item_units(w, tiles);
       add(a.parts[which] + query * D, a.stats[which][query]);
-      const int c0 = pf_owner(p, u), c1 = pf_owner(p, end - 1);
+      const int c0 = pf_owner(p, u + kPfItemUnits), c1 = pf_owner(p, end - 1);
       for (int c = c0 + 1; c <= c1; ++c) {
         const int64_t u0 = pf_share(p, c) - u, u1 = min(pf_share(p, c + 1), end) - u;
-        if ((u0 + w - 1) / w >= (u1 + w - 1) / w) continue;  // no whole tile
+        if (pf_cut(u0, w) >= pf_cut(u1, w)) continue;  // no tile begins there
         const int64_t at = int64_t(c) * 256 + qi % 256;
         add(a.mid + at * D, a.mid_stats[at]);
       }
