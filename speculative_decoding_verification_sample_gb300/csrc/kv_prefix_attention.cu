@@ -16,13 +16,13 @@
 // scales take a path that multiplies in fp32 and rounds once to bf16). Widening K too kept the
 // loading warps from keeping up. P is rounded to bf16 (2^-9 relative, as the output); the sums l
 // take it in fp32 before. K's scales belong to 16 keys and enter the softmax as one factor each.
-//   Softmax: a row's reference is the largest z_j so far, moved only when a later one
-// exceeds it by 2^8; then O and l are rescaled. A tile's scores of a query are loaded once and
-// stay in registers from the maximum to the probabilities.
+//   Softmax: a row's reference is a bound of its scores, in whole binades, 24 above the largest
+// of those that set it; when a later one exceeds it, it is set anew, and O and l are scaled,
+// exactly. A query's scores of a tile stay in registers from the maximum to the probabilities.
 //
-// Roles, of 4 warps each with registers moved to the softmax: two softmax groups; loading of V;
-// a warp for each group's products, one that walks the work list and prepares queries, one that
-// finds the tiles and starts the copies of K. One CTA per SM.
+// Roles, of 4 warps each with registers moved to the softmax: two softmax groups; widening of V;
+// a warp that issues the products, one that walks the work list and prepares queries, one that
+// finds the tiles and starts their copies. One CTA per SM.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,11 +45,12 @@ static_assert(256 * kPfSoftmaxRegs + 128 * (kPfLoadRegs + kPfOtherRegs) == 65536
 constexpr int kPfItems = 6;     // items described at a time
 constexpr int kPfQueries = 2;   // M tiles of queries held at a time
 constexpr int kPfFactors = 16;  // M tiles whose rows' factors are held: more than kPfItems items have
-constexpr int kPfTurns = 8;     // steps that group 0 may be ahead of group 1 (K's slots: fewer)
 constexpr int kPfPart = 16;     // keys of a part of a tile: of one block (block_size % 16 == 0)
 constexpr int kPfParts = kPfTile / kPfPart;
 constexpr float kMaxBf16 = 0x1.fep127f;
-constexpr float kPfSlack = 8.0f;  // binades by which keys may exceed the reference
+// Binades between the largest score of a row and its reference when that is set: probabilities
+// are 2^-24 to 1 then, in which bf16 and fp32 lose nothing (keys 2^-100 of the largest are lost).
+constexpr float kPfHeadroom = 24.0f;
 
 // Bounded waits. A wait ends when its barrier's phase does or when `abort` is set; the walking
 // warp sets it (and the error bit) when no tile has been done for a while, and every role then
@@ -80,7 +81,7 @@ struct PfItem {
 // A key tile: what the warps need of it.
 struct PfTile {
   int plane[kPfParts], in_block[kPfParts];  // where the parts' V is (plane -1: nowhere)
-  float2 ks[kPfParts];       // of K: scale, and -inf for a part that is hidden (else 0)
+  alignas(16) float2 ks[kPfParts];  // of K: scale, and -inf for a part that is hidden (else 0)
   float raw_ks[kPfParts], vs[kPfParts];     // the scales of K where one is below 0, of V
   int pos, L;                // position; committed tokens of its row
   int slot, last;            // the row's place in the pack; whether it is the row's last tile
@@ -107,7 +108,6 @@ struct PfShape {
     uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
     uint64_t q_full[kPfQueries], q_empty[kPfQueries];
     uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
-    uint64_t turn[2][kPfTurns];
     uint64_t s_full[2], p_full[2], o_full[2], told[2], read[2], drained;
     uint32_t tmem;
     PfGuard guard;
@@ -353,16 +353,19 @@ __device__ __forceinline__ void pf_prepare(const PfArgs& a, const PfPlan& p, con
 // O of a row times `by`.
 template <int D>
 __device__ __forceinline__ void pf_rescale(uint32_t o_addr, float by) {
+  float o[16];
 #pragma unroll 1
-  for (int y = 0; y < D; y += 32) {
-    float o[32];
-    tmem_ld32(o_addr + y, o);
+  for (int y = 0; y < D; y += 16) {
+    tmem_ld8(o_addr + y, o);
+    tmem_ld8(o_addr + y + 8, o + 8);
     tmem_wait_ld();
-    tmem_tie32(o);
 #pragma unroll
-    for (int x = 0; x < 32; ++x) o[x] *= by;
-    tmem_st16(o_addr + y, reinterpret_cast<uint32_t*>(o));
-    tmem_st16(o_addr + y + 16, reinterpret_cast<uint32_t*>(o) + 16);
+    for (int x = 0; x < 16; ++x) {
+      asm volatile("" : "+f"(o[x]));
+      o[x] *= by;
+    }
+    tmem_st8(o_addr + y, o);
+    tmem_st8(o_addr + y + 8, o + 8);
   }
 }
 
@@ -373,8 +376,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   using S = PfShape<D>;
   constexpr int KS = S::kKSlots, RS = S::kRawSlots, VS = S::kVSlots, NT = S::kTiles;
   constexpr int kCode = S::kCodeBytes, kWide = S::kWideBytes;
-  constexpr int kMmaWarp = (kPfSoftmax + kPfLoad) / 32, kWalkWarp = kMmaWarp + 2,
-                kFindWarp = kMmaWarp + 3;
+  constexpr int kMmaWarp = (kPfSoftmax + kPfLoad) / 32, kWalkWarp = kMmaWarp + 1,
+                kFindWarp = kMmaWarp + 2;  // (and one to fill the four)
   extern __shared__ __align__(1024) uint8_t sm[];  // V, queries, K, V as cached, the rest
   uint8_t* q_s = sm + VS * kWide;
   uint8_t* k_s = q_s + kPfQueries * kWide;
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kPfItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], kPfSoftmax / 32 + 3);
+      mbar_init(&sh.item_empty[i], kPfSoftmax / 32 + 2);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -394,15 +397,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     for (int i = 0; i < kPfQueries; ++i) {
       mbar_init(&sh.q_full[i], kPfSoftmax / 32);
-      mbar_init(&sh.q_empty[i], 2);
+      mbar_init(&sh.q_empty[i], 1);
     }
     for (int i = 0; i < KS; ++i) {
       mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 2);
+      mbar_init(&sh.k_empty[i], 1);
     }
     for (int i = 0; i < VS; ++i) {
       mbar_init(&sh.v_full[i], kPfLoad / 32);
-      mbar_init(&sh.v_empty[i], 2);
+      mbar_init(&sh.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -411,8 +414,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&sh.told[i], 128);
       mbar_init(&sh.read[i], 128);
     }
-    for (int i = 0; i < 2 * kPfTurns; ++i) mbar_init(&sh.turn[0][0] + i, 1);
-    mbar_init(&sh.drained, 2);
+    mbar_init(&sh.drained, 1);
     sh.guard.abort = sh.guard.beat[0] = sh.guard.beat[1] = sh.guard.done[0] = sh.guard.done[1] = 0;
     fence_mbar_init();
   }
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       const bool any = __any_sync(0xffffffffu, query >= 0);
       float c = 0.0f;
-      float ref = -INFINITY, l = 0.0f;  // ref: of the scores before the row's factor
+      float ref = -INFINITY, l = 0.0f;  // ref: a whole number, in log2 units
       bool stop = false;
 #pragma unroll 1
       for (int i = 0; i < turns; ++i) {
@@ -495,22 +497,24 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const PfTile& tile = sh.tile[(seq0 + (two ? i : 2 * i + g)) % NT];
         // (a warp's queries are all of one row)
         if (any && (!own || stride == 0 || row / stride == tile.slot)) {
-          // All of a query's scores at once: a load takes some 800 cycles while products run.
+          // All of a query's scores at once: a load takes 500 to 800 cycles while products run.
+          // (32 at a time, in a loop of a fifth of the code, the softmax took 3400 instead of
+          // 1900 cycles.)
           float z[128];
 #pragma unroll
           for (int y = 0; y < 4; ++y) tmem_ld32(s_addr + 32 * y, z + 32 * y);
           tmem_wait_ld();
 #pragma unroll
           for (int y = 0; y < 4; ++y) tmem_tie32(z + 32 * y);
-          if (tile.below) {  // a scale below zero: the maximum of a part is taken before it else
+          if (tile.below) {  // a scale below zero: the maximum of a part is not taken before it
 #pragma unroll
             for (int x = 0; x < 128; ++x) z[x] *= tile.raw_ks[x / kPfPart];
           }
           if (tile.last) {
             // New tokens, seen by some queries only, and what lies past them: in the last 48 keys
             // of a row's last tile, whose end is that of the part with the last token.
-            const int d = tile.pos + 80 - tile.L;  // at most 0, as there are at most 32 of them
-            const uint64_t seen = uint64_t(bits) << -d | ((uint64_t(1) << -d) - 1);
+            const int before = tile.L - tile.pos - 80;  // at least 1: there are at most 32 of them
+            const uint64_t seen = uint64_t(bits) << before | ((uint64_t(1) << before) - 1);
 #pragma unroll
             for (int x = 0; x < 48; ++x)
               if (!(seen >> x & 1)) z[80 + x] = -INFINITY;
@@ -527,16 +531,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const float2 k = tile.ks[y];
             top = fmaxf(top, fmaf(max3(m0, m1, fmaxf(v[14], v[15])), k.x, k.y));
           }
-          const bool moves = __any_sync(0xffffffffu, (top - ref) * c > kPfSlack);
+          top *= c;
+          const bool moves = __any_sync(0xffffffffu, top > ref);
           float down = 1.0f;
           if (moves) {
-            // -inf - -inf is NaN: not greater, and the reference stays unset
-            const float to = fmaxf(ref, top);
-            down = to == -INFINITY ? 1.0f : ex2_approx((ref - to) * c);
-            l *= down;
+            // The references move, by whole binades and some more, as in rows of a warp the
+            // largest score would else grow at some row in every other tile.
+            const float to = top > ref ? ceilf(top) + kPfHeadroom : ref;
+            down = to == -INFINITY ? 1.0f : ex2_approx(ref - to);
             ref = to;
+            l *= down;
           }
-          const float minus = ref == -INFINITY ? 0.0f : -ref * c;
+          const float minus = ref == -INFINITY ? 0.0f : -ref;
           float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
           for (int y = 0; y < kPfParts; ++y) {
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       pf_wait(&sh.o_full[g], o_phase, guard);
       o_phase ^= 1;
       const bool both = !two && tiles > 1;
-      float m = ref == -INFINITY ? -INFINITY : ref * c;
+      float m = ref;
       float mine = 1.0f, other = 0.0f;
       if (both) {
         sh.part[g][row] = make_float2(m, l);
@@ -659,7 +665,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       uint8_t* to = sm + vr.at * kWide;
       const bool plain = t.plain_v;
       const int keys = t.keys, valid = t.valid;
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < kSteps; ++i) {
         const int key = key0 + i * kKeyStep, part = key / kPfPart;
         uint4 v = *reinterpret_cast<const uint4*>(raw + i * kKeyStep * D);
@@ -828,7 +834,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         continue;
       }
       // nothing has a place yet
-      __nanosleep(500);
+      __nanosleep(1000);
       if (global_ns() - since > a.wait_ns) {
         *reinterpret_cast<volatile int*>(&guard->abort) = 1;
         if (a.err) atomicOr(a.err, SPEC_DERR_TIMEOUT);
@@ -1011,151 +1017,115 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       for (int i = 0; i < RS; ++i)
         if (started >> (16 + i) & 1u) mbar_wait(&sh.raw_full[i], started_phase >> (16 + i) & 1u);
     }
-    } else {
+    } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
-    // A warp a group, each with its own order: the output of a tile, then the next scores,
-    // which take the place of that tile's probabilities. Tiles that only the other group
-    // takes are waited for and released too, so that no warp falls two rounds behind in a
-    // ring, where the parity of its waits would mislead it.
-    // The whole warp goes through the loops, so that what the products need is known to be
-    // uniform; one lane issues them.
-    {
-      constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // K and queries: 128- or 64-byte swizzle
-      constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, kPfTile, kPfTile);
-      constexpr uint32_t idesc_o = tc_idesc(1, 1, 0, 1, kPfTile, D);
-      auto uniform = [](uint32_t x) { return __reduce_max_sync(0xffffffffu, x); };
-      const int g = int(uniform(warp)) - kMmaWarp;
-      const uint32_t tmem_u = uniform(tmem);
-      const uint64_t k0 = tc_desc(smem_u32(k_s), 16, 8 * D, kSwz);
-      const uint64_t v0 = tc_desc(smem_u32(sm), kPfTile * 128, 1024, 2);
-      const uint32_t k_hi = uint32_t(k0 >> 32), v_hi = uint32_t(v0 >> 32), k_lo = uint32_t(k0),
-                     v_lo = uint32_t(v0), q_lo = uint32_t(tc_desc(smem_u32(q_s), 16, 8 * D, kSwz));
-      const uint32_t s_at = tmem_u + g * 128, o_at = tmem_u + 256 + g * 128;
-      PfRing<kPfItems> ring;
-      PfRing<kPfQueries> qring;
-      PfRing<KS> kr;
-      PfRing<VS> vr;
-      uint32_t p_phase = 0;
-      // outputs that wait: group 0's, group 1's, whether both of one V tile; of this group's,
-      // whether it is its item's first and last
-      bool pend0 = false, pend1 = false, shared = false, first = false, last = false;
-      bool ok = true;  // no wait has run out
-      int step = 0;
-      auto wait = [&](uint64_t* bar, uint32_t phase) {
-        if (ok) ok = __all_sync(0xffffffffu, pf_wait(bar, phase, guard));
-      };
-      auto pass_q = [&]() {
-        wait(&sh.q_full[qring.at], qring.phase);
-        if (lane == 0) mbar_arrive(&sh.q_empty[qring.at]);
-        qring.next();
-      };
-      auto pass_k = [&]() {
-        wait(&sh.k_full[kr.at], kr.phase);
-        if (lane == 0) mbar_arrive(&sh.k_empty[kr.at]);
-        kr.next();
-      };
-      auto pass_v = [&]() {
-        wait(&sh.v_full[vr.at], vr.phase);
-        if (lane == 0) mbar_arrive(&sh.v_empty[vr.at]);
-        vr.next();
-      };
-      // steps of items, and one after the last for the outputs that wait
-      for (bool more = true; more && ok;) {
-        wait(&sh.item_full[ring.at], ring.phase);
-        if (!ok) break;
-        const PfItem& it = sh.item[ring.at];
-        more = !uniform(it.stop);
-        const int two = more ? uniform(it.two) : 0, tiles = more ? uniform(it.t1 - it.t0) : 0;
-        __syncwarp();
-        if (more && lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
-        ring.next();
-        PfRing<kPfQueries> q = qring;
-        uint32_t q_desc = 0;
-        int x = two ? 0 : g;  // this group's next tile of the item
-        const int by = two ? 1 : 2, steps = !more ? 1 : (tiles + by - 1) / by;
+    // In each step first group 0, then group 1: the output of its tile before, then the scores
+    // of the next, which take the place of that tile's probabilities. So one group's products
+    // run while the other's softmax does. The whole warp goes through the loops, so that what
+    // the products need is known to be uniform; one lane issues them. (A warp for each group
+    // left the tensor cores idle while they handed over to each other.)
+    constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // K and queries: 128- or 64-byte swizzle
+    constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, kPfTile, kPfTile);
+    constexpr uint32_t idesc_o = tc_idesc(1, 1, 0, 1, kPfTile, D);
+    auto uniform = [](uint32_t x) { return __reduce_max_sync(0xffffffffu, x); };
+    const uint32_t tmem_u = uniform(tmem);
+    const uint64_t k0 = tc_desc(smem_u32(k_s), 16, 8 * D, kSwz);
+    const uint64_t v0 = tc_desc(smem_u32(sm), kPfTile * 128, 1024, 2);
+    const uint32_t k_hi = uint32_t(k0 >> 32), v_hi = uint32_t(v0 >> 32), k_lo = uint32_t(k0),
+                   v_lo = uint32_t(v0), q_lo = uint32_t(tc_desc(smem_u32(q_s), 16, 8 * D, kSwz));
+    PfRing<kPfItems> ring;
+    PfRing<kPfQueries> qring;
+    PfRing<KS> kr;
+    PfRing<VS> vr;
+    // bits of the groups: the phase of their probabilities; an output that waits, whether it is
+    // of its item's first and last tile, and of a V tile that both take
+    uint32_t p_phase = 0, pending = 0, firsts = 0, lasts = 0, both = 0;
+    int v_at = 0, k_at = 0;  // slots of the last V and K
+    bool ok = true;          // no wait has run out
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (ok) ok = __all_sync(0xffffffffu, pf_wait(bar, phase, guard));
+    };
+    // steps of items, and one after the last for the outputs that wait
+    for (bool more = true; more && ok;) {
+      wait(&sh.item_full[ring.at], ring.phase);
+      if (!ok) break;
+      const PfItem& it = sh.item[ring.at];
+      more = !uniform(it.stop);
+      const int two = more ? uniform(it.two) : 0, tiles = more ? uniform(it.t1 - it.t0) : 0;
+      __syncwarp();
+      if (more && lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
+      ring.next();
+      const PfRing<kPfQueries> q0 = qring;
+      if (more) qring.next();
+      const PfRing<kPfQueries> q1 = two ? qring : q0;
+      if (two) qring.next();
+      const int turns = !more ? 2 : two ? 2 * tiles : (tiles + 1) / 2 * 2;
 #pragma unroll 1
-        for (int s = 0; s < steps && ok; ++s, x += by) {
-          const bool on1 = two || 2 * s + 1 < tiles;
-          if (g == 1 && !shared && pend0) pass_v();
-          // The output and the scores are issued together. An item's first scores wait for its
-          // queries, and the output before them does not wait for that.
-          bool out = g ? pend1 : pend0;
+      for (int e = 0; e < turns && ok; ++e) {
+        const int g = e & 1;
+        const bool starts = e < 2, shared = both >> g & 1u;
+        const bool on = two || e < tiles, ends = two ? e + 2 >= turns : e + 2 >= tiles;
+        const PfRing<kPfQueries> q = g ? q1 : q0;
+        // The output and the scores are issued together, but an item's first scores wait for its
+        // queries, and the output before them does not wait for that.
+        bool out = pending >> g & 1u;
 #pragma unroll 1
-          for (int r = out && s == 0 ? 0 : 1; r < 2 && ok; ++r) {
-            const bool score = r == 1 && x < tiles;
-            if (r == 1) {
-              if (s == 0 && more) {
-                // the first half's queries are not group 1's
-                if (g == 1 && two) pass_q();
-                q = qring;
-                qring.next();
-                wait(&sh.q_full[q.at], q.phase);
-                if (g == 1 && tiles == 1 && !two && lane == 0) mbar_arrive(&sh.q_empty[q.at]);
-                q_desc = q_lo + q.at * (kWide / 16);
-              }
-              if (g == 1 && !two && more) pass_k();
-              if (score) wait(&sh.k_full[kr.at], kr.phase);
+        for (int r = out && starts ? 0 : 1; r < 2 && ok; ++r) {
+          const bool score = r == 1 && on;
+          if (score) {
+            if (starts) wait(&sh.q_full[q.at], q.phase);
+            if (!two || g == 0) {
+              wait(&sh.k_full[kr.at], kr.phase);
+              k_at = kr.at;
+              kr.next();
             }
-            if (out) {
+          }
+          if (out) {
+            if (!shared || g == 0) {
               wait(&sh.v_full[vr.at], vr.phase);
-              // In turns, so that one group's products run while the other's softmax does: each
-              // waits for the other's products of before to be issued.
-              const int turn = g == 1 ? step : step - 1;
-              if (turn >= 0) wait(&sh.turn[g ^ 1][turn % kPfTurns], turn / kPfTurns & 1);
-              wait(&sh.p_full[g], p_phase);
-            }
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v_desc = v_lo + vr.at * (kWide / 16), k_desc = k_lo + kr.at * (kCode / 16);
-            const bool ends = x + by >= tiles;
-            if (elect_one()) {
-              if (out) {
-#pragma unroll
-                for (int y = 0; y < kPfTile / 16; ++y)
-                  pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
-                tc_commit(&sh.v_empty[vr.at]);
-                if (last) tc_commit(&sh.o_full[g]);
-              }
-              if (score) {
-                // both terms of the queries into one sum
-#pragma unroll
-                for (int y = 0; y < 2 * (D / 32); ++y) {
-                  const int z = y % (D / 32), term = y / (D / 32);
-                  pf_mma_s(s_at, q_desc + term * (kCode / 16) + 2 * z, k_desc + 2 * z, k_hi, idesc_s,
-                           y > 0);
-                }
-                tc_commit(&sh.s_full[g]);
-                tc_commit(&sh.k_empty[kr.at]);
-                // the item's last scores of these queries
-                if (ends) tc_commit(&sh.q_empty[q.at]);
-              }
-            }
-            __syncwarp();
-            if (out) {
-              p_phase ^= 1;
+              v_at = vr.at;
               vr.next();
-              out = false;
+            }
+            wait(&sh.p_full[g], p_phase >> g & 1u);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s_at = tmem_u + g * 128, o_at = s_at + 256;
+          const uint32_t v_desc = v_lo + v_at * (kWide / 16), k_desc = k_lo + k_at * (kCode / 16),
+                         q_desc = q_lo + q.at * (kWide / 16);
+          const bool first = firsts >> g & 1u, last = lasts >> g & 1u;
+          if (elect_one()) {
+            if (out) {
+#pragma unroll 2
+              for (int y = 0; y < kPfTile / 16; ++y)
+                pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
+              if (!shared || g == 1) tc_commit(&sh.v_empty[v_at]);
+              if (last) tc_commit(&sh.o_full[g]);
             }
             if (score) {
-              kr.next();
-              first = s == 0;
-              last = ends;
-              if (ends && two && g == 0) pass_q();
+              // both terms of the queries into one sum
+#pragma unroll 1
+              for (int z = 0; z < D / 32; ++z) {
+                pf_mma_s(s_at, q_desc + 2 * z, k_desc + 2 * z, k_hi, idesc_s, z > 0);
+                pf_mma_s(s_at, q_desc + kCode / 16 + 2 * z, k_desc + 2 * z, k_hi, idesc_s, true);
+              }
+              tc_commit(&sh.s_full[g]);
+              if (!two || g == 1) tc_commit(&sh.k_empty[k_at]);
+              // the item's last scores of these queries
+              if (two ? ends : e + 1 == tiles) tc_commit(&sh.q_empty[q.at]);
             }
           }
-          if (lane == 0) mbar_arrive(&sh.turn[g][step % kPfTurns]);
-          ++step;
-          if (g == 0) {
-            if (pend1 && !shared) pass_v();
-            if (on1 && !two) pass_k();
-          }
-          pend0 = more;
-          pend1 = on1;
-          shared = two;
+          __syncwarp();
+          if (out) p_phase ^= 1u << g;
+          out = false;
         }
+        const uint32_t bit = 1u << g;
+        pending = on && more ? pending | bit : pending & ~bit;
+        firsts = starts ? firsts | bit : firsts & ~bit;
+        lasts = ends ? lasts | bit : lasts & ~bit;
+        both = two ? both | bit : both & ~bit;
       }
     }
-    __syncwarp();
     }
   }
   __syncwarp();
@@ -1163,7 +1133,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   if (sh.guard.abort) {
     // what has been issued ends before the CTA's memory is another's
-    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    if (warp == kMmaWarp) {
       if (lane == 0) tc_commit(&sh.drained);
       __syncwarp();
       mbar_wait(&sh.drained, 0);
