@@ -1072,21 +1072,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll 1
         for (int r = out && starts ? 0 : 1; r < 2 && ok; ++r) {
           const bool score = r == 1 && on;
-          if (score) {
-            if (starts) wait(&sh.q_full[q.at], q.phase);
-            if (!two || g == 0) {
-              wait(&sh.k_full[kr.at], kr.phase);
-              k_at = kr.at;
-              kr.next();
-            }
+          const bool new_k = score && (!two || g == 0), new_v = out && (!shared || g == 0);
+          // all waits at once, a lane each
+          {
+            uint64_t* bar = lane == 0   ? &sh.p_full[g]
+                            : lane == 1 ? &sh.v_full[vr.at]
+                            : lane == 2 ? &sh.k_full[kr.at]
+                                        : &sh.q_full[q.at];
+            const uint32_t phase = lane == 0   ? p_phase >> g & 1u
+                                   : lane == 1 ? vr.phase
+                                   : lane == 2 ? kr.phase
+                                               : q.phase;
+            const bool need = lane == 0   ? out
+                              : lane == 1 ? new_v
+                              : lane == 2 ? new_k
+                                          : lane == 3 && score && starts;
+            ok = __all_sync(0xffffffffu, !need || pf_wait(bar, phase, guard));
           }
-          if (out) {
-            if (!shared || g == 0) {
-              wait(&sh.v_full[vr.at], vr.phase);
-              v_at = vr.at;
-              vr.next();
-            }
-            wait(&sh.p_full[g], p_phase >> g & 1u);
+          if (new_k) {
+            k_at = kr.at;
+            kr.next();
+          }
+          if (new_v) {
+            v_at = vr.at;
+            vr.next();
           }
           if (!ok) break;
           tc_fence_after();
@@ -1096,7 +1105,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const bool first = firsts >> g & 1u, last = lasts >> g & 1u;
           if (elect_one()) {
             if (out) {
-#pragma unroll 2
+#pragma unroll
               for (int y = 0; y < kPfTile / 16; ++y)
                 pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
               if (!shared || g == 1) tc_commit(&sh.v_empty[v_at]);
@@ -1104,7 +1113,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             if (score) {
               // both terms of the queries into one sum
-#pragma unroll 1
+#pragma unroll
               for (int z = 0; z < D / 32; ++z) {
                 pf_mma_s(s_at, q_desc + 2 * z, k_desc + 2 * z, k_hi, idesc_s, z > 0);
                 pf_mma_s(s_at, q_desc + kCode / 16 + 2 * z, k_desc + 2 * z, k_hi, idesc_s, true);
