@@ -526,7 +526,8 @@ size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads,
  *                kv_q8_attention's calls will have them
  *   group_rows   [num_members] int32: rows, group after group; group_starts [num_groups + 1]
  *                int32, ascending: group g has members group_starts[g] ..
- *                group_starts[g + 1] - 1. Rows may be in no group
+ *                group_starts[g + 1] - 1. Rows may be in no group; no groups, and a null
+ *                group_rows with no members, are allowed
  *   plan         kv_prefix_plan_bytes(B, num_groups, num_members) bytes, 256-byte aligned,
  *                no initialisation
  * A group shares the blocks that the tables of its rows (those with new tokens) have in

@@ -413,8 +413,8 @@ int kv_q8_attention(const void* q, int dtype, const void* kv_pool, const float* 
 }
 
 size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members) {
-  if (B < 1 || B > kMaxPageRows || num_groups < 1 || num_groups > kMaxPageRows ||
-      num_members < 1 || num_members > kMaxPageRows)
+  if (B < 1 || B > kMaxPageRows || num_groups < 0 || num_groups > kMaxPageRows ||
+      num_members < 0 || num_members > kMaxPageRows)
     return 0;
   return sv::kv_prefix_plan_size(B, num_groups, num_members);
 }
@@ -424,8 +424,9 @@ int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const in
                    int num_members, int T, int num_q_heads, int num_kv_heads, int num_blocks,
                    int block_size, int B, int max_blocks, void* plan, size_t plan_bytes,
                    void* stream, int32_t* err_flag) {
-  if (!block_table || !seq_lens || !group_starts || !group_rows || !plan) return SPEC_EINVAL;
-  if (bad_table(num_blocks, block_size, B, max_blocks) || num_groups < 1 || num_members < 1 ||
+  if (!block_table || !seq_lens || !group_starts || (!group_rows && num_members > 0) || !plan)
+    return SPEC_EINVAL;
+  if (bad_table(num_blocks, block_size, B, max_blocks) || num_groups < 0 || num_members < 0 ||
       T < 1 || num_kv_heads < 1 || num_q_heads < num_kv_heads || num_q_heads % num_kv_heads != 0)
     return SPEC_EINVAL;
   const size_t need = kv_prefix_plan_bytes(B, num_groups, num_members);

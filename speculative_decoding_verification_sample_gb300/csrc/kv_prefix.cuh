@@ -11,15 +11,15 @@
 // Entries: first the groups, then the rows' own keys. A group's queries (all rows of it,
 // row by row) are taken in blocks of 256, two M tiles of the tensor core, the last one
 // maybe one tile; a row's queries R = T G likewise, but with R <= 32 four consecutive rows,
-// with R <= 64 two, share one M tile, a pack: their key tiles follow each other, and a tile's
-// probabilities are zero for the other rows of the pack, which are other warps'. (An item for each row, with 20 of
-// 128 places in use, spent 15 us each on its beginning and end.) An item is (entry, kv
-// head, block). The units of all items form
-// one list, entries outermost, then kv heads, blocks, tiles; CTA c of NC takes units
-// [W c / NC, W (c + 1) / NC), of each item the tiles that begin there. A piece that begins its item leaves its
-// part in the place of its queries (one place for the prefix, one for the row's own keys),
-// another one in the place of its CTA, which has at most one such. Everything follows from
-// the plan, so the result does not depend on timing.
+// with R <= 64 two, share one M tile, a pack: their key tiles follow each other, and a
+// tile's probabilities are zero for the other rows of the pack, which are other warps'. (An
+// item for each row, with 20 of 128 places in use, spent 15 us each on its beginning and
+// end.) An item is (entry, kv head, block). The units of all items form one list, entries
+// outermost, then kv heads, blocks, tiles; CTA c of NC takes units [W c / NC,
+// W (c + 1) / NC), of each item the tiles that begin there. A piece that begins its item
+// leaves its part in the place of its queries (one place for the prefix, one for the row's
+// own keys), another one in the place of its CTA, which has at most one such. Everything
+// follows from the plan, so the result does not depend on timing.
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -54,7 +54,7 @@ struct PfRow {
 
 // The plan's arrays, by their byte offsets.
 struct PfLayout {
-  size_t groups, rows, prefix, members, scratch, bytes;
+  size_t groups, rows, prefix, members, bytes;
 };
 __host__ __device__ inline PfLayout pf_layout(int B, int NG, int NE) {
   PfLayout l;
@@ -63,17 +63,15 @@ __host__ __device__ inline PfLayout pf_layout(int B, int NG, int NE) {
   l.rows = (l.rows + 31) / 32 * 32;
   l.prefix = l.rows + size_t(B) * sizeof(PfRow);
   l.members = l.prefix + (size_t(NG) + B + 1) * 8;
-  l.scratch = l.members + size_t(NE) * 4;
-  l.bytes = l.scratch + (size_t(B) + 4 * size_t(NG)) * 4;
-  l.bytes = (l.bytes + 255) / 256 * 256;
+  l.bytes = (l.members + size_t(NE) * 4 + 255) / 256 * 256;
   return l;
 }
 
 // Rows of a pack with R queries each.
 __host__ __device__ inline int pf_pack(int R) { return R <= 32 ? 4 : R <= 64 ? 2 : 1; }
 
-// What an item costs, about 0.3 us each: its beginning and end (queries, parts), a key tile
-// with two M tiles, one with one. The split only needs their proportions.
+// What an item costs: its beginning and end (queries, parts), a key tile with two M tiles,
+// one with one. The split only needs their proportions (2.4 us a tile with two: 0.5 us each).
 constexpr int kPfItemUnits = 16, kPfTwoUnits = 5, kPfOneUnits = 4;
 __host__ __device__ inline int64_t pf_item_units(int w, int64_t tiles) {
   return kPfItemUnits + w * tiles;

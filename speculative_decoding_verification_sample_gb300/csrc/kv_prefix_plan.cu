@@ -1,14 +1,10 @@
 // The plan of the prefix attention (kv_prefix.cuh), and the kernel that joins its parts.
 //
-// The plan. One cluster of 8 CTAs, so that its five steps can follow each other with
-// cluster barriers: each row's place in the list of members (the first, if it is listed
-// twice); each group's first row and shortest length; the first block in which a row's
-// table differs from the group's; units and their sums. Bound by latency, and for many
-// long tables by reading them (B x max_blocks entries once).
-//
-// Joining. A CTA takes the queries of one row and kv head, a warp a query, its lanes over
-// the head's numbers: one part of the prefix and one of the row's own keys, each with the
-// pieces of further CTAs, added in that order. Bound by reading the parts, mostly from L2.
+// The plan. A cluster of 8 CTAs: each makes out in its own shared memory the rows' places in
+// the list of members (the first, if one is listed twice), the groups' first rows and
+// shortest lengths, and compares its share of the tables with those of the first rows;
+// the first CTA takes the first differences from all and sums up the units. Bound by
+// latency, and for many long tables by reading them (B x max_blocks entries once).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,51 +33,50 @@ struct PlanArgs {
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     kv_prefix_plan_kernel(const PlanArgs a) {
+  extern __shared__ int32_t sm[];
   __shared__ int64_t sums[kPlanThreads / 32];
+  int32_t *common = sm, *first = common + a.NG, *shortest = first + a.NG, *live = shortest + a.NG,
+          *starts = live + a.NG, *row_entry = starts + a.NG + 1;
   const cg::cluster_group cluster = cg::this_cluster();
+  const bool lead = cluster.block_rank() == 0;
   const PfLayout lay = pf_layout(a.B, a.NG, a.NE);
   PfHeader* head = reinterpret_cast<PfHeader*>(a.plan);
   PfGroup* groups = reinterpret_cast<PfGroup*>(a.plan + lay.groups);
   PfRow* rows = reinterpret_cast<PfRow*>(a.plan + lay.rows);
   int64_t* prefix = reinterpret_cast<int64_t*>(a.plan + lay.prefix);
   int32_t* members = reinterpret_cast<int32_t*>(a.plan + lay.members);
-  int32_t* row_entry = reinterpret_cast<int32_t*>(a.plan + lay.scratch);
-  int32_t *first = row_entry + a.B, *shortest = first + a.NG, *live = shortest + a.NG,
-          *common = live + a.NG;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int me = int(cluster.block_rank()) * kPlanThreads + tid, all = kPlanCtas * kPlanThreads;
   pdl_trigger();
-  pdl_wait();
-
-  // the list's bounds: every CTA looks at all of them
-  bool bad = false;
-  for (int g = tid; g <= a.NG; g += kPlanThreads) {
-    const int s = a.starts[g];
-    bad = bad || s < 0 || s > a.NE || (g > 0 && s < a.starts[g - 1]);
-  }
-  bad = __syncthreads_or(bad);
-  if (bad && me == 0 && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
-  const int e0 = bad ? 0 : a.starts[0], e1 = bad ? 0 : a.starts[a.NG];
-  for (int b = me; b < a.B; b += all) row_entry[b] = INT32_MAX;
-  for (int g = me; g < a.NG; g += all) {
+  for (int b = tid; b < a.B; b += kPlanThreads) row_entry[b] = INT32_MAX;
+  for (int g = tid; g < a.NG; g += kPlanThreads) {
     first[g] = shortest[g] = common[g] = INT32_MAX;
     live[g] = 0;
   }
-  if (me == 0) head->magic = 0;
-  cluster.sync();
+  pdl_wait();
+  if (lead && tid == 0) head->magic = 0;
 
-  for (int i = e0 + me; i < e1; i += all) {
+  // the list's bounds
+  bool bad = false;
+  for (int g = tid; g <= a.NG; g += kPlanThreads) {
+    const int s = a.starts[g];
+    starts[g] = s;
+    bad = bad || s < 0 || s > a.NE || (g > 0 && s < a.starts[g - 1]);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && lead && tid == 0 && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
+  const int e0 = bad ? 0 : starts[0], e1 = bad ? 0 : starts[a.NG];
+
+  for (int i = e0 + tid; i < e1; i += kPlanThreads) {
     const int r = a.members[i];
     if (r >= 0 && r < a.B) atomicMin(&row_entry[r], i);
-    else if (a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
+    else if (lead && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
   }
-  cluster.sync();
-
+  __syncthreads();
   auto group_of = [&](int i) {  // the last group that starts at or before entry i
     int lo = 0, hi = a.NG - 1;
     while (lo < hi) {
       const int m = (lo + hi + 1) >> 1;
-      if (a.starts[m] <= i) lo = m;
+      if (starts[m] <= i) lo = m;
       else hi = m - 1;
     }
     return lo;
@@ -91,37 +86,38 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     n = a.nn ? a.nn[r] : a.T;
     return L >= 0 && n >= 0 && n <= a.T && int64_t(L) + n <= int64_t(a.MB) * a.bs;
   };
-  for (int i = e0 + me; i < e1; i += all) {
+  for (int i = e0 + tid; i < e1; i += kPlanThreads) {
     const int r = a.members[i];
-    members[i] = -1;  // a member without queries
-    if (r < 0 || r >= a.B) continue;
-    if (row_entry[r] != i) {
-      if (a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
-      continue;
+    int member = -1;  // none: without queries
+    if (r >= 0 && r < a.B) {
+      int L, n;
+      if (row_entry[r] != i) {
+        if (lead && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
+      } else if (lengths(r, L, n) && n > 0) {
+        member = r;
+        const int g = group_of(i);
+        atomicMin(&first[g], i);
+        atomicMin(&shortest[g], L);
+        atomicAdd(&live[g], 1);
+      }
     }
-    int L, n;
-    if (!lengths(r, L, n) || n == 0) continue;
-    members[i] = r;
-    const int g = group_of(i);
-    atomicMin(&first[g], i);
-    atomicMin(&shortest[g], L);
-    atomicAdd(&live[g], 1);
+    if (lead) members[i] = member;
   }
-  cluster.sync();
+  cluster.sync();  // (the first CTA's shared memory is written by the others below)
 
   // tables against the first row's, a warp 256 entries at a time
   const int chunks = (a.MB + kPlanChunk - 1) / kPlanChunk;
   const int64_t tasks = int64_t(e1 - e0) * chunks;
-  for (int64_t t = me >> 5; t < tasks; t += all / 32) {
+  for (int64_t t = int64_t(cluster.block_rank()) * (kPlanThreads / 32) + (tid >> 5); t < tasks;
+       t += kPlanCtas * kPlanThreads / 32) {
     const int i = e0 + int(t / chunks), j0 = int(t % chunks) * kPlanChunk;
-    const int r = a.members[i];
-    if (r < 0 || r >= a.B || row_entry[r] != i) continue;
-    int L, n;
-    if (!lengths(r, L, n) || n == 0) continue;
     const int g = group_of(i);
     if (live[g] < 2) continue;
     const int j1 = min(shortest[g] / a.bs, j0 + kPlanChunk);
     if (j0 >= j1 || *reinterpret_cast<volatile int32_t*>(&common[g]) <= j0) continue;
+    const int r = a.members[i];
+    int L, n;
+    if (r < 0 || r >= a.B || row_entry[r] != i || !lengths(r, L, n) || n == 0) continue;
     const int32_t* mine = a.bt + int64_t(r) * a.MB;
     const int32_t* other = a.bt + int64_t(a.members[first[g]]) * a.MB;
     int x[kPlanChunk / 32], y[kPlanChunk / 32];
@@ -140,8 +136,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     at = __reduce_min_sync(0xffffffffu, at);
     if (at != INT32_MAX && lane == 0) atomicMin(&common[g], at);
   }
+  if (!lead) {
+    __syncthreads();
+    int32_t* to = cluster.map_shared_rank(common, 0);
+    for (int g = tid; g < a.NG; g += kPlanThreads)
+      if (common[g] != INT32_MAX) atomicMin(&to[g], common[g]);
+  }
   cluster.sync();
-  if (cluster.block_rank() != 0) return;
+  if (!lead) return;
 
   // units, and their sums from entry to entry: each thread some consecutive entries
   auto shared_tiles = [&](int g) {
@@ -149,12 +151,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                               : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs / kPfTile);
   };
   const int pack = pf_pack(a.T * a.G);
-  const int entries = a.NG + (a.B + pack - 1) / pack, per = (entries + kPlanThreads - 1) / kPlanThreads;
-  auto entry = [&](int e, bool write) -> int64_t {
+  const int entries = a.NG + (a.B + pack - 1) / pack,
+            per = (entries + kPlanThreads - 1) / kPlanThreads;
+  auto entry = [&](int e) -> int64_t {
     if (e < a.NG) {
       const int tiles = shared_tiles(e);
-      const int s0 = bad ? 0 : a.starts[e], many = bad ? 0 : a.starts[e + 1] - s0;
-      if (write) groups[e] = PfGroup{tiles, tiles > 0 ? a.members[first[e]] : 0, s0, many};
+      const int s0 = bad ? 0 : starts[e], many = bad ? 0 : starts[e + 1] - s0;
+      groups[e] = PfGroup{tiles, tiles > 0 ? a.members[first[e]] : 0, s0, many};
       return a.H * pf_units(int64_t(many) * a.T * a.G, tiles);
     }
     int64_t units = 0;
@@ -169,14 +172,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         r.skip = shared_tiles(g);
         if (r.skip > 0) {
           r.group = g;
-          r.at = i - a.starts[g];
+          r.at = i - starts[g];
         }
       }
       // they end with the 16 keys of the last token (the first tile may begin in the prefix)
       r.tiles = !ok ? -1
                 : r.n == 0 ? 0
                            : ((r.L + r.n + 15) / 16 * 16 - r.skip * kPfTile + kPfTile - 1) / kPfTile;
-      if (write) rows[b] = r;
+      rows[b] = r;
       if (r.tiles > 0) units += pack > 1 ? r.tiles : pf_units(int64_t(r.n) * a.G, r.tiles);
     }
     if (pack > 1 && units > 0) units = pf_item_units(kPfOneUnits, units);
@@ -185,7 +188,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   int64_t sum = 0;
   for (int x = 0; x < per; ++x) {
     const int e = tid * per + x;
-    if (e < entries) sum += entry(e, true);
+    if (e >= entries) break;
+    prefix[e] = sum;  // of this thread's so far
+    sum += entry(e);
   }
   int64_t inc = sum;
 #pragma unroll
@@ -196,15 +201,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   if (lane == 31) sums[tid >> 5] = inc;
   __syncthreads();
   for (int w = 0; w < (tid >> 5); ++w) inc += sums[w];
-  int64_t at = inc - sum;
   for (int x = 0; x < per; ++x) {
     const int e = tid * per + x;
     if (e >= entries) break;
-    prefix[e] = at;
-    at += entry(e, false);
+    prefix[e] += inc - sum;
     if (e == entries - 1) {
-      prefix[entries] = at;
-      head->units = at;
+      prefix[entries] = inc;
+      head->units = inc;
       head->B = a.B;
       head->T = a.T;
       head->G = a.G;
@@ -236,7 +239,10 @@ int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
   a.MB = k.max_blocks;
   a.plan = static_cast<uint8_t*>(k.plan);
   a.err = k.err;
-  return launch_pdl(kv_prefix_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0,
+  const size_t smem = (5 * size_t(a.NG) + 1 + a.B) * 4;
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(kv_prefix_plan_kernel, 200 * 1024, done) != SPEC_OK) return SPEC_ECUDA;
+  return launch_pdl(kv_prefix_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), smem,
                     static_cast<cudaStream_t>(k.stream), a);
 }
 
@@ -245,7 +251,10 @@ size_t kv_prefix_plan_size(int B, int num_groups, int num_members) {
 }
 
 // ------------------------------------------------------------------ joining
-constexpr int kPfJoinThreads = 256;
+// A warp a query, its lanes over the head's numbers. The pieces of the query's two items
+// (prefix, own keys) are found a lane each, so that their statistics come at once and their
+// numbers follow without a wait between them; they are added in the order of their CTAs.
+constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const PfArgs a, int ctas) {
@@ -253,79 +262,142 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
   pdl_trigger();
   pdl_wait();
   const PfPlan p = pf_plan(a, ctas);
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, lane = threadIdx.x & 31;
-  const int R = a.T * a.G;
+  const int R = a.T * a.G, groups = (R + kPfJoinWarps - 1) / kPfJoinWarps;
+  const int bh = blockIdx.x / groups, b = bh / a.H, h = bh - b * a.H, lane = threadIdx.x & 31;
+  const int r = (blockIdx.x - bh * groups) * kPfJoinWarps + (threadIdx.x >> 5);
+  if (r >= R) return;
   PfRow row = {};
   row.tiles = -1;
   if (p.ok) row = p.rows[b];
   // lengths that changed since the plan was made: the row's keys are not the plan's
   const bool same = p.ok && row.L == a.sl[b] && row.n == (a.nn ? a.nn[b] : a.T);
   const bool bad = row.tiles < 0 || !same;
-  if (bad && a.err && h == 0 && threadIdx.x == 0)
+  if (bad && a.err && h == 0 && r == 0 && lane == 0)
     atomicOr(a.err, p.ok ? SPEC_DERR_BAD_LENGTH : SPEC_DERR_BAD_SLOT);
-  for (int r = threadIdx.x >> 5; r < R; r += kPfJoinThreads / 32) {
-    const int t = r / a.G;
-    const int64_t query = (int64_t(b) * a.T + t) * a.H * a.G + h * a.G + r % a.G;
-    float m = -INFINITY, l = 0.0f, o[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = 0.0f;
-    auto add = [&](const float* part, float2 st) {
-      float v[N];
-      if constexpr (N == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(part + 4 * lane);
-        v[0] = x.x;
-        v[1] = x.y;
-        v[N - 2] = x.z;
-        v[N - 1] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(part + 2 * lane);
-        v[0] = x.x;
-        v[1] = x.y;
-      }
-      const float mn = fmaxf(m, st.x), base = mn == -INFINITY ? 0.0f : mn;
-      const float x = ex2_approx(m - base), y = ex2_approx(st.x - base);
-      l = l * x + st.y * y;
-#pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = o[i] * x + v[i] * y;
-      m = mn;
-    };
-    // the parts of the item that holds query qi of an entry's nq
-    auto gather = [&](int e, int which, int qi, int64_t nq, int64_t tiles) {
-      const int64_t base = p.prefix[e], per_h = (p.prefix[e + 1] - base) / a.H;
-      const int qb = qi / 256, w = nq - qb * 256 > 128 ? kPfTwoUnits : kPfOneUnits;
-      if (tiles == 0) tiles = (per_h - kPfItemUnits) / w;  // a pack: all of its rows'
-      const int64_t u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, tiles),
-                    end = u + pf_item_units(w, tiles);
-      add(a.parts[which] + query * D, a.stats[which][query]);
-      const int c0 = pf_owner(p, u + kPfItemUnits), c1 = pf_owner(p, end - 1);
-      for (int c = c0 + 1; c <= c1; ++c) {
-        const int64_t u0 = pf_share(p, c) - u, u1 = min(pf_share(p, c + 1), end) - u;
-        if (pf_cut(u0, w) >= pf_cut(u1, w)) continue;  // no tile begins there
-        const int64_t at = int64_t(c) * 256 + qi % 256;
-        add(a.mid + at * D, a.mid_stats[at]);
-      }
-    };
-    if (!bad && t < row.n) {
-      if (row.group >= 0) {
-        const PfGroup g = p.groups[row.group];
-        gather(row.group, 0, row.at * R + r, int64_t(g.count) * R, g.tiles);
-      }
-      const int pack = pf_pack(R);
-      if (pack > 1) gather(p.NG + b / pack, 1, b % pack * (kPfTile / pack) + r, kPfTile, 0);
-      else if (row.tiles > 0) gather(p.NG + b, 1, r, int64_t(row.n) * a.G, row.tiles);
+  float m, l, o[N];
+  auto load = [&](const float* part, float* v) {
+    if constexpr (N == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(part + 4 * lane);
+      v[0] = x.x;
+      v[1] = x.y;
+      v[N - 2] = x.z;
+      v[N - 1] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(part + 2 * lane);
+      v[0] = x.x;
+      v[1] = x.y;
     }
-    const float inv = bad ? __uint_as_float(0x7fc00000u) : l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t x[N / 2];
+  };
+  // up to 32 pieces, a lane each (st: -inf, 0 where there is none), `part` their numbers
+  auto gather = [&](float2 st, const float* part) {
+    float top = st.x;
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
-      x[i] = *reinterpret_cast<const uint32_t*>(&v);
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
+    const float was = ex2_approx(m - base), mine = ex2_approx(st.x - base);
+    m = mn;
+    l *= was;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] *= was;
+    unsigned left = __ballot_sync(0xffffffffu, part != nullptr);
+    const uint64_t at = reinterpret_cast<uint64_t>(part);
+    while (left) {
+      constexpr int kAtOnce = 4;
+      float v[kAtOnce][N], w[kAtOnce], s[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int x = left ? __ffs(left) - 1 : 0;
+        w[k] = __shfl_sync(0xffffffffu, mine, x);
+        s[k] = __shfl_sync(0xffffffffu, st.y, x);
+        const uint64_t from = __shfl_sync(0xffffffffu, at, x);
+        if (left) {
+          load(reinterpret_cast<const float*>(from), v[k]);
+        } else {
+          w[k] = s[k] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[k][i] = 0.0f;
+        }
+        left &= left - 1;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        l += s[k] * w[k];
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] += v[k][i] * w[k];
+      }
     }
-    uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + query * D) +
-                   N / 2 * lane;
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[N / 2 - 1]);
-    else *to = x[0];
+  };
+  struct Item {
+    int64_t u, end;
+    int w, c0, c1;
+  };
+  auto quotient = [](int64_t n, int d) -> int64_t {
+    return n >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
+  };
+  auto item = [&](int e, int qb, int64_t nq, int64_t tiles) {
+    Item x;
+    const int64_t base = p.prefix[e], per_h = quotient(p.prefix[e + 1] - base, a.H);
+    x.w = nq - qb * 256 > 128 ? kPfTwoUnits : kPfOneUnits;
+    if (tiles == 0) tiles = (per_h - kPfItemUnits) / x.w;  // a pack: all of its rows'
+    x.u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, tiles);
+    x.end = x.u + pf_item_units(x.w, tiles);
+    x.c0 = pf_owner(p, x.u + kPfItemUnits);
+    x.c1 = pf_owner(p, x.end - 1);
+    return x;
+  };
+  const int pack = pf_pack(R), t = r / a.G;
+  const int64_t query = (int64_t(b) * a.T + t) * a.H * a.G + h * a.G + r - t * a.G;
+  const int q0 = row.at * R + r, q1 = pack > 1 ? b % pack * (kPfTile / pack) + r : r;
+  m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = 0.0f;
+  if (!bad && t < row.n) {
+    // lane 0: the first piece of the prefix, lane 1: of the row's own keys, then the others
+    const bool has0 = row.group >= 0, has1 = row.tiles > 0;
+    Item both[2] = {};
+    if (has0) {
+      const PfGroup g = p.groups[row.group];
+      both[0] = item(row.group, q0 / 256, int64_t(g.count) * R, g.tiles);
+    }
+    if (has1)
+      both[1] = pack > 1 ? item(p.NG + b / pack, 0, kPfTile, 0)
+                         : item(p.NG + b, q1 / 256, int64_t(row.n) * a.G, row.tiles);
+    const int more0 = both[0].c1 - both[0].c0, more = more0 + both[1].c1 - both[1].c0;
+    for (int first = 0; first < 2 + more; first += 32) {
+      const int x = first + lane;
+      float2 st = make_float2(-INFINITY, 0.0f);
+      const float* part = nullptr;
+      if (x < 2) {
+        if (x == 0 ? has0 : has1) {
+          st = (x == 0 ? a.stats[0] : a.stats[1])[query];
+          part = (x == 0 ? a.parts[0] : a.parts[1]) + query * D;
+        }
+      } else if (x < 2 + more) {
+        const bool own = x - 2 >= more0;
+        const Item i = own ? both[1] : both[0];
+        const int c = i.c0 + 1 + x - 2 - (own ? more0 : 0);
+        const int64_t u0 = pf_share(p, c) - i.u, u1 = min(pf_share(p, c + 1), i.end) - i.u;
+        if (pf_cut(u0, i.w) < pf_cut(u1, i.w)) {  // else no tile begins there
+          const int64_t at = int64_t(c) * 256 + (own ? q1 : q0) % 256;
+          st = a.mid_stats[at];
+          part = a.mid + at * D;
+        }
+      }
+      gather(st, part);
+    }
   }
+  const float inv = bad ? __uint_as_float(0x7fc00000u) : l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t x[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+    x[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  uint32_t* to =
+      reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + query * D) + N / 2 * lane;
+  if constexpr (N == 4) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[N / 2 - 1]);
+  else *to = x[0];
 }
 
 namespace {
@@ -423,7 +495,8 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
                                      k.stream);
   if (st != SPEC_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
-  const dim3 grid(unsigned(a.B * a.H));
+  const int R = a.T * a.G;
+  const dim3 grid(unsigned(a.B * a.H * ((R + kPfJoinWarps - 1) / kPfJoinWarps)));
   return a.D == 128
              ? launch_pdl(kv_prefix_join_kernel<128>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas)
              : launch_pdl(kv_prefix_join_kernel<64>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas);

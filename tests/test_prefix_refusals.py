@@ -13,7 +13,7 @@ ATTN = dict(q=P, dtype=0, pool=P, scales=P, bt=P, sl=P, nn=None, tree=None, plan
 
 @pytest.mark.parametrize("want,changed", [
     *[(EINVAL, {k: None}) for k in ("bt", "sl", "starts", "rows", "plan")],
-    *[(EINVAL, c) for c in (dict(NG=0), dict(NE=0), dict(T=0), dict(H=0), dict(Hq=3), dict(Hq=1),
+    *[(EINVAL, c) for c in (dict(NG=-1), dict(NE=-1), dict(T=0), dict(H=0), dict(Hq=3), dict(Hq=1),
                             dict(NB=0), dict(bs=0), dict(B=0), dict(MB=0), dict(MB=1 << 27),
                             dict(plan=P + 16), dict(pn=100))],
     *[(ENOTSUP, c) for c in (dict(B=8193), dict(NG=8193), dict(NE=8193), dict(T=33))],
@@ -38,7 +38,8 @@ def test_attention_refuses(L, want, changed):  # noqa: F811
 def test_sizes(L):  # noqa: F811
     f = L.kv_prefix_plan_bytes
     assert f(4, 1, 4) > 0 and f(4, 1, 4) % 256 == 0 and f(400, 100, 300) > f(4, 1, 4)
-    assert f(0, 1, 1) == f(1, 0, 1) == f(1, 1, 0) == f(8193, 1, 1) == 0
+    assert f(0, 1, 1) == f(1, -1, 1) == f(1, 1, -1) == f(8193, 1, 1) == 0
+    assert f(1, 0, 0) > 0
     w = L.kv_q8_prefix_attention_workspace_bytes
     assert w(2, 5, 32, 8, 128) % 256 == 0
     assert w(1, 5, 32, 8, 96) >= L.kv_q8_attention_workspace_bytes(5, 32, 8, 96) > 0
