@@ -35,13 +35,13 @@
 #include "launch_util.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
+#include "tc.cuh"
 
 namespace sv {
 
 constexpr int kNrThreads = 256, kNrWarps = kNrThreads / 32;
 constexpr int kNrTile = 16;              // tokens of a CTA without a cache
 constexpr int kNrTable = 64 * 1024;      // bytes of cos and sin at most
-constexpr int kNrHold = 64;              // numbers that a lane keeps
 
 struct NormRopeArgs {
   const uint8_t *q, *k, *v;              // first token; v: with a cache
@@ -57,6 +57,7 @@ struct NormRopeArgs {
   const int32_t* bt;
   int NB, bs, MB, J;                     // J: blocks (tiles) that T tokens can touch
   int64_t block_bytes, block_scales;
+  int per;                               // units of a task
   int32_t* err;
 };
 
@@ -100,38 +101,95 @@ __device__ __forceinline__ float2 turned(uint64_t fraction, int p, float f) {
   return make_float2(c * f, s * f);
 }
 
-// N numbers at an address that is a multiple of their size.
+// N numbers at an address that is a multiple of their size, as they are, in W registers.
 template <bool kF32, int N>
-__device__ __forceinline__ void load_numbers(const void* p, float* f) {
-  if constexpr (kF32 && N == 4) {
-    const float4 v = *static_cast<const float4*>(p);
-    f[0] = v.x;
-    f[1] = v.y;
-    f[2] = v.z;
-    f[3] = v.w;
+constexpr int kNrWords = N == 1 ? 1 : N * (kF32 ? 4 : 2) / 4;
+
+template <bool kF32, int N>
+__device__ __forceinline__ void load_raw(const void* p, uint32_t* w) {
+  if constexpr (kNrWords<kF32, N> == 4) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if constexpr (kNrWords<kF32, N> == 2) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
   } else if constexpr (kF32) {
-    f[0] = *static_cast<const float*>(p);
-  } else if constexpr (N == 1) {
-    f[0] = __uint_as_float(uint32_t(*static_cast<const uint16_t*>(p)) << 16);
+    w[0] = *static_cast<const uint32_t*>(p);
   } else {
-    uint32_t w[N / 2];
-    if constexpr (N == 8) {
-      const uint4 v = *static_cast<const uint4*>(p);
-      w[0] = v.x;
-      w[1] = v.y;
-      w[2] = v.z;
-      w[3] = v.w;
-    } else {
-      const uint2 v = *static_cast<const uint2*>(p);
-      w[0] = v.x;
-      w[1] = v.y;
-    }
+    w[0] = *static_cast<const uint16_t*>(p);
+  }
+}
+
+template <bool kF32, int N>
+__device__ __forceinline__ void widen(const uint32_t* w, float* f) {
+  if constexpr (kF32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+  } else if constexpr (N == 1) {
+    f[0] = __uint_as_float(w[0] << 16);
+  } else {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (W == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// N numbers from global to shared memory, zeros if not `on`; cp_async_wait before they are read.
+template <bool kF32, int N>
+__device__ __forceinline__ void copy_raw(uint8_t* to, const uint8_t* from, bool on) {
+  constexpr int kBytes = 4 * kNrWords<kF32, N>;
+  if constexpr (!kF32 && N == 1) {  // (there is no such copy of 2 bytes)
+    *reinterpret_cast<uint32_t*>(to) = on ? *reinterpret_cast<const uint16_t*>(from) : 0u;
+  } else {
+    if constexpr (kBytes == 16) cp_async16(to, from, on);
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(to)), "l"(from),
+                   "n"(kBytes), "r"(on ? kBytes : 0)
+                   : "memory");
+  }
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>  // all groups but the newest N
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two products, or sums of products, of adjacent numbers in one instruction.
+__device__ __forceinline__ void mul2(float* r, const float* a, const float* b) {
+  const float2 v = __fmul2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+  r[0] = v.x;
+  r[1] = v.y;
+}
+__device__ __forceinline__ void fma2(float* r, const float* a, const float* b, const float* c) {
+  const float2 v =
+      __ffma2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]), make_float2(c[0], c[1]));
+  r[0] = v.x;
+  r[1] = v.y;
 }
 
 template <bool kF32, int N>
@@ -165,16 +223,20 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float* f) {
     *p = uint8_t(f32x4_to_e4m3(f[0], 0.0f, 0.0f, 0.0f));
 }
 
+// A warp's ring: two tasks' numbers as they are, units of `heads` heads, two vectors a lane.
+constexpr int kNrHalf = 4096;
+template <bool kF32, int N>
+constexpr int kNrUnits = kNrHalf / ((N == 1 ? 4 : 1) * 2 * 32 * 4 * kNrWords<kF32, N>);
+constexpr int kNrCtas = 3;  // of an SM
+
 // N: numbers of a vector; N = 1 is for sizes, strides and addresses that longer ones do not
 // fit, and for blocks whose table would be too large: a lane takes up to 4 pairs of a head
 // and makes its angles itself.
 template <bool kF32, int N, bool kCache>
-__global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int E = kF32 ? 4 : 2, U = N == 1 ? 4 : 1;
-  constexpr int kPasses = kNrHold / (2 * N * U);
-  extern __shared__ __align__(16) uint8_t sm[];  // fractions [half], then the table
-  uint64_t* fractions = reinterpret_cast<uint64_t*>(sm);
-  float2* table = reinterpret_cast<float2*>(sm + (a.half * 8 + 15) / 16 * 16);
+__global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int E = kF32 ? 4 : 2, U = N == 1 ? 4 : 1, W = kNrWords<kF32, N>;
+  constexpr int kUnits = kNrUnits<kF32, N>;
+  extern __shared__ __align__(16) uint8_t sm[];  // rings, fractions [half], weights [2][D], the table
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
@@ -201,159 +263,278 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
   const int lanes = pairs <= 1 ? 1 : N == 1 ? 32 : 1 << (32 - __clz(pairs - 1));  // of a head
   const int heads = 32 / lanes;                           // of a warp
   const int sub = lane / lanes, u = lane % lanes;
-  const int32_t* pos = a.pos ? a.pos + int64_t(b) * a.T + t0 : nullptr;
-  auto position = [&](int t) { return pos ? pos[t] : L + t0 + t; };
-  for (int i = tid; i < a.half; i += kNrThreads) fractions[i] = turn_fraction(a.freq[i]);
-  __syncthreads();
-  if constexpr (N > 1) {
-    for (int i = tid; i < cnt * a.half; i += kNrThreads) {
-      const int t = i / a.half, p = i - t * a.half, x = p / N, y = p % N;
-      // by halves of y, then x: the lanes of a head read 16 bytes side by side
-      table[((t * (N / 2) + y / 2) * turning + x) * 2 + (y & 1)] =
-          turned(fractions[p], position(t), a.factor);
-    }
-    __syncthreads();
-  }
-
   // numbers of unit x of a head: vectors at ea and eb
   auto place = [&](int x, int& ea, int& eb) {
     const bool apart = !a.interleaved && x < turning;
     ea = apart ? x * N : 2 * x * N;
     eb = apart ? ea + a.half : ea + N;
   };
-  auto fetch = [&](const uint8_t* head, bool on, float (*x)[2][N]) {
+  // A lane reads only what it has copied itself.
+  constexpr int kVector = 32 * 4 * W, kUnit = U * 2 * kVector;
+  uint8_t* const mine = sm + (tid >> 5) * 2 * kNrHalf + lane * 4 * W;
+  int half_at = 0;  // of the task at work
+  auto fetch = [&](const uint8_t* head, bool on, uint8_t* to) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int w = u + 32 * i;
       int ea, eb;
       place(w, ea, eb);
-      if (on && w < pairs) {
-        load_numbers<kF32, N>(head + ea * E, x[i][0]);
-        load_numbers<kF32, N>(head + eb * E, x[i][1]);
-      } else {
-#pragma unroll
-        for (int y = 0; y < N; ++y) x[i][0][y] = x[i][1][y] = 0.0f;
-      }
-    }
-  };
-  // norm and turn of a head that `lanes` lanes hold
-  auto finish = [&](float (*x)[2][N], const void* weight, int t) {
-    if (weight) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int y = 0; y < N; ++y) s = fmaf(x[i][0][y], x[i][0][y], fmaf(x[i][1][y], x[i][1][y], s));
-      for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float r = 1.0f / sqrtf(s / float(a.D) + a.eps);
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int w = u + 32 * i;
-        if (w >= pairs) continue;
-        int ea, eb;
-        place(w, ea, eb);
-        float g[2][N];
-        load_numbers<kF32, N>(static_cast<const uint8_t*>(weight) + ea * E, g[0]);
-        load_numbers<kF32, N>(static_cast<const uint8_t*>(weight) + eb * E, g[1]);
-#pragma unroll
-        for (int y = 0; y < N; ++y) {
-          x[i][0][y] *= r * g[0][y];
-          x[i][1][y] *= r * g[1][y];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int w = u + 32 * i;
-      if (w >= turning) continue;
-      float2 cs[N];
-      if constexpr (N == 1) {
-        cs[0] = turned(fractions[w], position(t), a.factor);
-      } else {
-#pragma unroll
-        for (int y = 0; y < N / 2; ++y) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(&table[((t * (N / 2) + y) * turning + w) * 2]);
-          cs[2 * y] = make_float2(v.x, v.y);
-          cs[2 * y + 1] = make_float2(v.z, v.w);
-        }
-      }
-      auto turn = [](float& p, float& q, float2 c) {
-        const float x0 = p, y0 = q;
-        p = x0 * c.x - y0 * c.y;
-        q = y0 * c.x + x0 * c.y;
-      };
-      if (N == 1 || !a.interleaved) {
-#pragma unroll
-        for (int y = 0; y < N; ++y) turn(x[i][0][y], x[i][1][y], cs[y]);
-      } else if constexpr (N > 1) {
-#pragma unroll
-        for (int y = 0; y < N / 2; ++y) {
-          turn(x[i][0][2 * y], x[i][0][2 * y + 1], cs[y]);
-          turn(x[i][1][2 * y], x[i][1][2 * y + 1], cs[N / 2 + y]);
-        }
-      }
-    }
-  };
-  auto put = [&](uint8_t* head, bool on, float (*x)[2][N]) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int w = u + 32 * i;
-      int ea, eb;
-      place(w, ea, eb);
-      if (on && w < pairs) {
-        store_numbers<kF32, N>(head + ea * E, x[i][0]);
-        store_numbers<kF32, N>(head + eb * E, x[i][1]);
-      }
+      const bool some = on && w < pairs;
+      copy_raw<kF32, N>(to + 2 * i * kVector, some ? head + ea * E : a.q, some);
+      copy_raw<kF32, N>(to + (2 * i + 1) * kVector, some ? head + eb * E : a.q, some);
     }
   };
 
+  // A task: a plane and head of the block, or `per` units of queries (without a cache: and
+  // keys), token by token. A plane's tokens beyond what a warp holds follow in further loads.
   const int64_t token0 = int64_t(b) * a.T + t0;
   const int planes = kCache ? 2 * a.H : 0;
-  const int q_groups = (a.Hq + 2 * heads - 1) / (2 * heads);
-  const int k_groups = kCache ? 0 : (a.H + 2 * heads - 1) / (2 * heads);
-  const int groups = q_groups + k_groups;
-  const int64_t tasks = planes + int64_t(cnt) * groups;
-  for (int64_t task = blockIdx.y * kNrWarps + (tid >> 5); task < tasks;
-       task += int64_t(gridDim.y) * kNrWarps) {
+  const int q_groups = (a.Hq + heads - 1) / heads;
+  const int groups = q_groups + (kCache ? 0 : (a.H + heads - 1) / heads);
+  const int units = cnt * groups;
+  const int tasks = planes + (units + a.per - 1) / a.per;
+  auto fetch_plane = [&](int task, int t_first, uint8_t* to) {
+    const int plane = task >= a.H, h = task - plane * a.H;
+    const uint8_t* from = (plane ? a.v : a.k) + int64_t(h) * a.D * E;
+    const int64_t step = plane ? a.v_step : a.k_step;
+#pragma unroll 1
+    for (int i = 0; i < kUnits && t_first + i * heads < cnt; ++i) {
+      const int t = t_first + i * heads + sub;
+      fetch(from + (token0 + t) * step, t < cnt, to + i * kUnit);
+    }
+  };
+  // unit (t, g): its head's place in the input, or the output; whether there is one
+  auto place_of = [&](int t, int g, bool out, const uint8_t*& at) {
+    const bool is_k = !kCache && g >= q_groups;
+    const int h = (is_k ? g - q_groups : g) * heads + sub;
+    const uint8_t* base = out ? (is_k ? a.ko : a.qo) : is_k ? a.k : a.q;
+    const int64_t step = out ? (is_k ? a.ko_step : a.qo_step) : is_k ? a.k_step : a.q_step;
+    at = base + (token0 + t) * step + int64_t(h) * a.D * E;
+    return h < (is_k ? a.H : a.Hq);
+  };
+  auto fetch_units = [&](int first_unit, uint8_t* to) {
+    int t = first_unit / groups, g = first_unit - t * groups;
+#pragma unroll 1
+    for (int i = 0; i < a.per && t < cnt; ++i) {
+      const uint8_t* at;
+      const bool on = place_of(t, g, false, at);
+      fetch(at, on, to + i * kUnit);
+      if (++g == groups) g = 0, ++t;
+    }
+  };
+  auto fetch_task = [&](int task, uint8_t* to) {
+    if (task < planes) fetch_plane(task, 0, to);
+    else if (task < tasks) fetch_units((task - planes) * a.per, to);
+    cp_async_commit();
+  };
+  int task = blockIdx.y * kNrWarps + (tid >> 5);
+  fetch_task(task, mine);
+
+  // ------------------------------------------------------------------ the tile's table
+  uint64_t* fractions = reinterpret_cast<uint64_t*>(sm + kNrWarps * 2 * kNrHalf);
+  float4* weights = reinterpret_cast<float4*>(fractions + (a.half + 1) / 2 * 2);
+  float4* table = weights + a.D / 2;
+  const int32_t* pos = a.pos ? a.pos + int64_t(b) * a.T + t0 : nullptr;
+  auto position = [&](int t) { return pos ? pos[t] : L + t0 + t; };
+  for (int i = tid; i < a.half; i += kNrThreads) fractions[i] = turn_fraction(a.freq[i]);
+  if constexpr (N > 1) {
+    // by quarters of what a lane needs of them: the lanes of a head read side by side
+    for (int i = tid; i < 2 * pairs; i += kNrThreads) {
+      const int w = i % pairs;
+      const uint8_t* from = static_cast<const uint8_t*>(i < pairs ? a.qw : a.kw);
+      if (!from) continue;
+      int ea, eb;
+      place(w, ea, eb);
+      uint32_t r[2][W];
+      float f[2][N];
+      load_raw<kF32, N>(from + ea * E, r[0]);
+      load_raw<kF32, N>(from + eb * E, r[1]);
+      widen<kF32, N>(r[0], f[0]);
+      widen<kF32, N>(r[1], f[1]);
+      float4* to = weights + (i < pairs ? 0 : a.D / 4) + w;
+#pragma unroll
+      for (int y = 0; y < 2 * N; y += 4)
+        to[y / 4 * pairs] =
+            make_float4(f[y / N][y % N], f[y / N][y % N + 1], f[y / N][y % N + 2], f[y / N][y % N + 3]);
+    }
+  }
+  __syncthreads();
+  if constexpr (N > 1) {
+    float* to = reinterpret_cast<float*>(table);
+    for (int i = tid; i < cnt * a.half; i += kNrThreads) {
+      const int t = i / a.half, p = i - t * a.half, x = p / N, y = p % N;
+      const float2 v = turned(fractions[p], position(t), a.factor);
+      // N cosines, then N sines, by four
+      const int at = (t * (N / 2) + y / 4) * turning + x;
+      to[4 * at + y % 4] = v.x;
+      to[4 * (at + N / 4 * turning) + y % 4] = v.y;
+    }
+    __syncthreads();
+  }
+
+  // norm and turn of a head that `lanes` lanes hold
+  const float share = 1.0f / float(a.D);
+  auto finish = [&](float (*x)[2][N], int is_k, int t) {
+    const void* weight = is_k ? a.kw : a.qw;
+    if (weight) {
+      float s;
+      if constexpr (N > 1) {
+        float s2[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int y = 0; y < 2 * N; y += 2) fma2(s2, &x[0][y / N][y % N], &x[0][y / N][y % N], s2);
+        s = s2[0] + s2[1];
+      } else {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) s = fmaf(x[i][0][0], x[i][0][0], fmaf(x[i][1][0], x[i][1][0], s));
+      }
+      for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float r = rsqrtf(fmaf(s, share, a.eps)), r2[2] = {r, r};
+      if constexpr (N > 1) {
+        if (u < pairs) {
+          const float4* from = weights + (is_k ? a.D / 4 : 0) + u;
+#pragma unroll
+          for (int y = 0; y < 2 * N; y += 4) {
+            const float4 v = from[y / 4 * pairs];
+            const float g[4] = {v.x, v.y, v.z, v.w};
+            float* f = &x[0][y / N][y % N];
+            mul2(f, f, r2);
+            mul2(f + 2, f + 2, r2);
+            mul2(f, f, g);
+            mul2(f + 2, f + 2, g + 2);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int w = u + 32 * i;
+          if (w >= pairs) continue;
+          int ea, eb;
+          place(w, ea, eb);
+          uint32_t g[2][W];
+          float f[2];
+          load_raw<kF32, N>(static_cast<const uint8_t*>(weight) + ea * E, g[0]);
+          load_raw<kF32, N>(static_cast<const uint8_t*>(weight) + eb * E, g[1]);
+          widen<kF32, N>(g[0], f);
+          widen<kF32, N>(g[1], f + 1);
+          x[i][0][0] *= r * f[0];
+          x[i][1][0] *= r * f[1];
+        }
+      }
+    }
+    auto turn = [](float& p, float& q, float c, float s) {
+      const float x0 = p, y0 = q;
+      p = x0 * c - y0 * s;
+      q = y0 * c + x0 * s;
+    };
+    if constexpr (N == 1) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int w = u + 32 * i;
+        if (w >= turning) continue;
+        const float2 v = turned(fractions[w], position(t), a.factor);
+        turn(x[i][0][0], x[i][1][0], v.x, v.y);
+      }
+    } else if (u < turning) {
+      const float4* from = table + t * (N / 2) * turning + u;
+#pragma unroll
+      for (int y = 0; y < N; y += 4) {
+        const float4 vc = from[y / 4 * turning], vs = from[(N + y) / 4 * turning];
+        const float c[4] = {vc.x, vc.y, vc.z, vc.w}, s[4] = {vs.x, vs.y, vs.z, vs.w};
+        if (!a.interleaved) {
+#pragma unroll
+          for (int z = 0; z < 4; z += 2) {
+            float *p = &x[0][0][y + z], *q = &x[0][1][y + z];
+            float ps[2], qs[2];
+            mul2(ps, p, s + z);
+            mul2(qs, q, s + z);
+            p[0] = fmaf(p[0], c[z], -qs[0]);
+            p[1] = fmaf(p[1], c[z + 1], -qs[1]);
+            fma2(q, q, c + z, ps);
+          }
+        } else {
+          // pairs 4 (y / 4) ... of the unit: of its first vector, then of the second
+          float* p = &x[0][2 * y / N][2 * y % N];
+          turn(p[0], p[1], c[0], s[0]);
+          turn(p[2], p[3], c[1], s[1]);
+          p = &x[0][(2 * y + 4) / N][(2 * y + 4) % N];
+          turn(p[0], p[1], c[2], s[2]);
+          turn(p[2], p[3], c[3], s[3]);
+        }
+      }
+    }
+  };
+  auto number = [&](const uint8_t* from, float (*x)[2][N]) {
+#pragma unroll
+    for (int i = 0; i < 2 * U; ++i) {
+      uint32_t w[W];
+      load_words<W>(from + i * kVector, w);
+      widen<kF32, N>(w, x[i / 2][i % 2]);
+    }
+  };
+
+  const int stride = gridDim.y * kNrWarps;
+#pragma unroll 1
+  for (; task < tasks; task += stride, half_at ^= kNrHalf) {
+    uint8_t* const held = mine + half_at;
+    fetch_task(task + stride, mine + (half_at ^ kNrHalf));
+    cp_async_wait<1>();
     if (task >= planes) {
-      // ---------------------------------------------------- two loads of a token's heads
-      const int x = int(task - planes), t = x / groups;
-      int g = x - t * groups;
-      const bool is_k = g >= q_groups;
-      if (is_k) g -= q_groups;
-      const int h0 = 2 * g * heads + sub, many = is_k ? a.H : a.Hq;
-      const uint8_t* from = is_k ? a.k + (token0 + t) * a.k_step : a.q + (token0 + t) * a.q_step;
-      uint8_t* to = is_k ? a.ko + (token0 + t) * a.ko_step : a.qo + (token0 + t) * a.qo_step;
-      const void* weight = is_k ? a.kw : a.qw;
-      float x0[U][2][N], x1[U][2][N];
-      const int64_t o0 = int64_t(h0) * a.D * E, o1 = o0 + int64_t(heads) * a.D * E;
-      fetch(from + o0, h0 < many, x0);
-      fetch(from + o1, h0 + heads < many, x1);
-      finish(x0, weight, t);
-      put(to + o0, h0 < many, x0);
-      if (2 * g * heads + heads >= many) continue;
-      finish(x1, weight, t);
-      put(to + o1, h0 + heads < many, x1);
+      // ---------------------------------------------------- units of queries and keys
+      const int unit = (task - planes) * a.per;
+      int t = unit / groups, g = unit - t * groups;
+#pragma unroll 1
+      for (int i = 0; i < a.per && t < cnt; ++i) {
+        float x[U][2][N];
+        number(held + i * kUnit, x);
+        finish(x, !kCache && g >= q_groups, t);
+        const uint8_t* at;
+        const bool on = place_of(t, g, true, at);
+        uint8_t* head = const_cast<uint8_t*>(at);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int w = u + 32 * k;
+          int ea, eb;
+          place(w, ea, eb);
+          if (on && w < pairs) {
+            store_numbers<kF32, N>(head + ea * E, x[k][0]);
+            store_numbers<kF32, N>(head + eb * E, x[k][1]);
+          }
+        }
+        if (++g == groups) g = 0, ++t;
+      }
     } else if constexpr (kCache) {
       // ---------------------------------------------------- a plane and head of the block
-      const int plane = task >= a.H, h = int(task) - plane * a.H;
-      const uint8_t* from = (plane ? a.v : a.k) + int64_t(h) * a.D * E;
-      const int64_t step = plane ? a.v_step : a.k_step;
-      const void* weight = plane ? nullptr : a.kw;
+      const int plane = task >= a.H;
       const int id = a.bt[int64_t(b) * a.MB + j];
-      auto head_of = [&](int t) { return from + (token0 + t) * step; };
-      auto make = [&](float (*x)[2][N], int t) {
-        if (plane == 0) finish(x, weight, min(t, cnt - 1));
-      };
-      uint32_t top = 0;
-      auto larger = [&](const float (*x)[2][N]) {
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-          for (int y = 0; y < N; ++y)
-            top = max(top, max(__float_as_uint(x[i][0][y]) & 0x7fffffffu,
-                               __float_as_uint(x[i][1][y]) & 0x7fffffffu));
+      if (id < 0 || id >= a.NB) {
+        if (a.err && lane == 0) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
+        continue;
+      }
+      uint8_t* codes = a.pool + id * a.block_bytes + int64_t(task) * a.bs * a.D;
+      float* sp = a.scales + id * a.block_scales + task;
+      const float was = first > 0 ? *sp : 0.0f;
+      // f(numbers, token) for all tokens of the block, made from what is held or loaded again
+      const int span = kUnits * heads;
+      bool again = false;
+      auto sweep = [&](auto&& f) {
+#pragma unroll 1
+        for (int c = 0; c < cnt; c += span) {
+          if (again || c > 0) {
+            fetch_plane(task, c, held);
+            cp_async_commit();
+            cp_async_wait<0>();
+          }
+#pragma unroll 1
+          for (int i = 0; i < kUnits && c + i * heads < cnt; ++i) {
+            const int t = c + i * heads + sub;
+            float x[U][2][N];
+            number(held + i * kUnit, x);
+            if (plane == 0) finish(x, 1, min(t, cnt - 1));
+            f(x, t);
+          }
+        }
+        again = cnt > span;
       };
       // NaN becomes 0, infinities the largest finite number (a NaN code would spread to
       // rows that do not see its token)
@@ -366,50 +547,23 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
             f = f != f ? 0.0f : fminf(fmaxf(f, -FLT_MAX), FLT_MAX);
           }
       };
-      float x[kPasses][U][2][N];
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int t = p * heads + sub;
-        fetch(head_of(t), t < cnt, x[p]);
-      }
-      if (id < 0 || id >= a.NB) {
-        if (a.err && lane == 0) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
-        continue;
-      }
-      uint8_t* codes = a.pool + id * a.block_bytes + int64_t(task) * a.bs * a.D;
-      float* sp = a.scales + id * a.block_scales + task;
-      const float was = first > 0 ? *sp : 0.0f;
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        if (p * heads >= cnt) continue;
-        make(x[p], p * heads + sub);
-        larger(x[p]);
-      }
+      uint32_t top = 0;
+      bool bad = false;
 #pragma unroll 1
-      for (int t = kPasses * heads; t < cnt; t += heads) {
-        float y[U][2][N];
-        fetch(head_of(t + sub), t + sub < cnt, y);
-        make(y, t + sub);
-        larger(y);
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      const bool bad = top >= 0x7f800000u;
-      if (bad) {
-        top = 0;
+      for (;;) {
+        sweep([&](float (*x)[2][N], int) {
+          if (bad) guard(x);
 #pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-          guard(x[p]);
-          larger(x[p]);
-        }
-#pragma unroll 1
-        for (int t = kPasses * heads; t < cnt; t += heads) {
-          float y[U][2][N];
-          fetch(head_of(t + sub), t + sub < cnt, y);
-          make(y, t + sub);
-          guard(y);
-          larger(y);
-        }
+          for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int y = 0; y < N; ++y)
+              top = max(top, max(__float_as_uint(x[i][0][y]) & 0x7fffffffu,
+                                 __float_as_uint(x[i][1][y]) & 0x7fffffffu));
+        });
         top = __reduce_max_sync(0xffffffffu, top);
+        if (bad || top < 0x7f800000u) break;
+        bad = true;
+        top = 0;
         if (a.err && lane == 0) atomicOr(a.err, SPEC_DERR_VALUE);
       }
       float scale = q8_pow2(q8_scale_exp(__uint_as_float(top)));
@@ -431,33 +585,28 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_kernel(const NormRope
           *reinterpret_cast<uint4*>(codes + i * 16) = c;
         }
       }
-      auto encode = [&](float (*v)[2][N], int t) {
+      sweep([&](float (*x)[2][N], int t) {
+        if (bad) guard(x);
+        if (t >= cnt) return;
+        uint8_t* to = codes + int64_t(first + t) * a.D;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           const int w = u + 32 * i;
           int ea, eb;
           place(w, ea, eb);
-          if (t >= cnt || w >= pairs) continue;
+          if (w >= pairs) continue;
+          float* f = x[i][0];
+          if (exact) {
 #pragma unroll
-          for (int y = 0; y < 2 * N; ++y) {
-            float& f = v[i][y / N][y % N];
-            f = exact ? f * inv : f / scale;
+            for (int y = 0; y < 2 * N; ++y) f[y] *= inv;
+          } else {
+#pragma unroll
+            for (int y = 0; y < 2 * N; ++y) f[y] /= scale;
           }
-          uint8_t* to = codes + int64_t(first + t) * a.D;
-          store_codes<N>(to + ea, v[i][0]);
-          store_codes<N>(to + eb, v[i][1]);
+          store_codes<N>(to + ea, x[i][0]);
+          store_codes<N>(to + eb, x[i][1]);
         }
-      };
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) encode(x[p], p * heads + sub);
-#pragma unroll 1
-      for (int t = kPasses * heads; t < cnt; t += heads) {
-        float y[U][2][N];
-        fetch(head_of(t + sub), t + sub < cnt, y);
-        make(y, t + sub);
-        if (bad) guard(y);
-        encode(y, t + sub);
-      }
+      });
       if (lane == 0) *sp = scale;
     }
   }
@@ -469,22 +618,28 @@ template <bool kF32, int N, bool kCache>
 int launch_shape(const NormRopeArgs& a, int tokens, int sms, cudaStream_t st) {
   auto kern = norm_rope_kernel<kF32, N, kCache>;
   const size_t fractions = (size_t(a.half) * 8 + 15) / 16 * 16;
-  const size_t smem = fractions + (N > 1 ? size_t(tokens) * a.half * 8 : 0);
+  const size_t smem = kNrWarps * 2 * kNrHalf + fractions + (N > 1 ? size_t(a.D) * 8 + size_t(tokens) * a.half * 8 : 0);
   static std::atomic<uint64_t> done{0};
-  if (allow_smem(kern, kNrTable + 2048, done) != SPEC_OK) return SPEC_ECUDA;
-  // few tokens: the tasks of a tile over several CTAs, up to a task for each warp
+  if (allow_smem(kern, kNrWarps * 2 * kNrHalf + kNrTable + 4096, done) != SPEC_OK) return SPEC_ECUDA;
+  // few tokens: the tasks of a tile over several CTAs, up to a task for each warp, and less in
+  // a task than a warp can hold
   const int64_t tiles = int64_t(a.B) * a.J;
+  if (tiles > INT32_MAX) return SPEC_ENOTSUP;
   const int pairs = a.D / (2 * N);
   int lanes = N == 1 ? 32 : 1;
   while (lanes < pairs && lanes < 32) lanes *= 2;
-  const int heads = 2 * (32 / lanes);
+  const int heads = 32 / lanes;
   const int64_t groups = (a.Hq + heads - 1) / heads + (kCache ? 0 : (a.H + heads - 1) / heads);
-  const int64_t tasks = (kCache ? 2 * a.H : 0) + groups * (tokens < a.T ? tokens : a.T);
-  int64_t parts = 2 * int64_t(sms) / tiles, most = (tasks + kNrWarps - 1) / kNrWarps;
+  const int64_t units = groups * (tokens < a.T ? tokens : a.T);
+  const int64_t warps = int64_t(sms) * kNrCtas * kNrWarps;
+  int64_t per = units * tiles / warps;
+  NormRopeArgs with = a;
+  with.per = int(per < 1 ? 1 : per > kNrUnits<kF32, N> ? kNrUnits<kF32, N> : per);
+  const int64_t tasks = (kCache ? 2 * a.H : 0) + (units + with.per - 1) / with.per;
+  int64_t parts = kNrCtas * int64_t(sms) / tiles, most = (tasks + kNrWarps - 1) / kNrWarps;
   parts = parts < 1 ? 1 : parts > most ? most : parts;
-  if (tiles > INT32_MAX) return SPEC_ENOTSUP;
   if (parts > 65535) parts = 65535;
-  return launch_pdl(kern, dim3(unsigned(tiles), unsigned(parts)), dim3(kNrThreads), smem, st, a);
+  return launch_pdl(kern, dim3(unsigned(tiles), unsigned(parts)), dim3(kNrThreads), smem, st, with);
 }
 
 template <bool kF32, bool kCache>
