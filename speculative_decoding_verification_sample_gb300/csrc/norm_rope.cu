@@ -13,22 +13,28 @@
 // do not share. sin and cos of the eighth turn that is left are Taylor polynomials (the
 // first terms left out are below 2e-9 and 2e-10).
 //
-// Split. A CTA takes the new tokens of one cache block (without a cache: 16 tokens) of a
-// row: it makes their table of cos and sin in shared memory once for all heads, then its
-// warps take tasks. A lane holds two vectors of a head, those that belong to each other
-// in the turn, so that only the norm's sum crosses lanes: 8 lanes a head of 128 bf16
-// numbers, 4 heads a warp. A task is two such loads of one token's heads, or with a cache
-// a plane and head of the block: its numbers stay in registers from the maximum to the
-// rounding (as many as 64 a lane hold; those of longer blocks are made twice). Few tokens:
-// the tasks of a block are split over several CTAs, each with the table.
+// Split. A CTA takes the new tokens of one cache block (without a cache: 16 or 8 tokens) of
+// a row: it makes their table of cos and sin in shared memory once for all heads, then its
+// warps take tasks. A lane holds two vectors of a head, those that belong to each other in
+// the turn, so that only the norm's sum crosses lanes: 8 lanes a head of 128 bf16 numbers,
+// 4 heads a warp, a unit. A task is up to 4 units (8 with 8-byte vectors) of queries, or with
+// a cache a plane and head of the block, whose numbers are taken twice from shared memory:
+// for the maximum, then for the rounding. Each warp copies its next task while it works on
+// one, a lane its own numbers. Few tokens: the tasks of a block are split over several CTAs,
+// each with the table.
 //
-// Bound by memory: every number is read and written once.
+// Bound by memory for long prompts (every number is read and written once) and, next to
+// that, by the instructions: about 20 a number (loads into registers with two CTAs an SM,
+// all tasks unrolled, took 306 us where this takes 150: 12 prompts, 0.85 GB, 5.5 TB/s; pairs
+// of numbers in one instruction took as many with the moves that they need, 157). Verification
+// steps and single tokens are bound by their launch and its latencies, 11 to 17 us a call.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/specverify.h"
 #include "launch.h"
@@ -40,7 +46,7 @@
 namespace sv {
 
 constexpr int kNrThreads = 256, kNrWarps = kNrThreads / 32;
-constexpr int kNrTile = 16;              // tokens of a CTA without a cache
+constexpr int kNrTile = 16;              // tokens of a CTA without a cache, at most
 constexpr int kNrTable = 64 * 1024;      // bytes of cos and sin at most
 
 struct NormRopeArgs {
@@ -50,13 +56,14 @@ struct NormRopeArgs {
   const void *qw, *kw;                   // [D] of the tensors' type; null: no norm
   const float* freq;                     // [half]
   const int32_t *sl, *nn, *pos;          // pos [B, T]; null: sl + t. nn null: T
-  int Hq, H, D, half, B, T, interleaved;
+  int Hq, H, D, half, B, T;
   float eps, factor;
   uint8_t* pool;                         // at the layer; the rest is for a cache
   float* scales;
   const int32_t* bt;
   int NB, bs, MB, J;                     // J: blocks (tiles) that T tokens can touch
   int64_t block_bytes, block_scales;
+  int tile;                              // tokens of a CTA without a cache
   int per;                               // units of a task
   int32_t* err;
 };
@@ -157,19 +164,18 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   }
 }
 
-// N numbers from global to shared memory, zeros if not `on`; cp_async_wait before they are read.
+// N numbers from global to shared memory; cp_async_wait before they are read.
 template <bool kF32, int N>
-__device__ __forceinline__ void copy_raw(uint8_t* to, const uint8_t* from, bool on) {
+__device__ __forceinline__ void copy_raw(uint8_t* to, const uint8_t* from) {
   constexpr int kBytes = 4 * kNrWords<kF32, N>;
-  if constexpr (!kF32 && N == 1) {  // (there is no such copy of 2 bytes)
-    *reinterpret_cast<uint32_t*>(to) = on ? *reinterpret_cast<const uint16_t*>(from) : 0u;
-  } else {
-    if constexpr (kBytes == 16) cp_async16(to, from, on);
-    else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(to)), "l"(from),
-                   "n"(kBytes), "r"(on ? kBytes : 0)
-                   : "memory");
-  }
+  if constexpr (!kF32 && N == 1)  // (there is no such copy of 2 bytes)
+    *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint16_t*>(from);
+  else if constexpr (kBytes == 16)
+    cp_async16(to, from, true);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from),
+                 "n"(kBytes)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -177,19 +183,6 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>  // all groups but the newest N
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Two products, or sums of products, of adjacent numbers in one instruction.
-__device__ __forceinline__ void mul2(float* r, const float* a, const float* b) {
-  const float2 v = __fmul2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
-  r[0] = v.x;
-  r[1] = v.y;
-}
-__device__ __forceinline__ void fma2(float* r, const float* a, const float* b, const float* c) {
-  const float2 v =
-      __ffma2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]), make_float2(c[0], c[1]));
-  r[0] = v.x;
-  r[1] = v.y;
 }
 
 template <bool kF32, int N>
@@ -232,7 +225,7 @@ constexpr int kNrCtas = 3;  // of an SM
 // N: numbers of a vector; N = 1 is for sizes, strides and addresses that longer ones do not
 // fit, and for blocks whose table would be too large: a lane takes up to 4 pairs of a head
 // and makes its angles itself.
-template <bool kF32, int N, bool kCache>
+template <bool kF32, int N, bool kCache, bool kInterleaved>
 __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int E = kF32 ? 4 : 2, U = N == 1 ? 4 : 1, W = kNrWords<kF32, N>;
   constexpr int kUnits = kNrUnits<kF32, N>;
@@ -254,8 +247,8 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
     t0 = start + first - L;
     cnt = min(a.bs - first, n - t0);
   } else {
-    t0 = jw * kNrTile;
-    cnt = min(kNrTile, n - t0);
+    t0 = jw * a.tile;
+    cnt = min(a.tile, n - t0);
   }
   if (cnt <= 0) return;
 
@@ -265,24 +258,30 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
   const int sub = lane / lanes, u = lane % lanes;
   // numbers of unit x of a head: vectors at ea and eb
   auto place = [&](int x, int& ea, int& eb) {
-    const bool apart = !a.interleaved && x < turning;
+    const bool apart = !kInterleaved && x < turning;
     ea = apart ? x * N : 2 * x * N;
     eb = apart ? ea + a.half : ea + N;
   };
-  // A lane reads only what it has copied itself.
+  int off[U][2];  // a lane's vectors in a head, bytes
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    int ea, eb;
+    place(u + 32 * i, ea, eb);
+    off[i][0] = ea * E;
+    off[i][1] = eb * E;
+  }
+  // A lane reads only what it has copied itself; where there is nothing (lanes beyond a head,
+  // heads and tokens beyond the last) it copies nothing, and what it makes of that is not used.
   constexpr int kVector = 32 * 4 * W, kUnit = U * 2 * kVector;
   uint8_t* const mine = sm + (tid >> 5) * 2 * kNrHalf + lane * 4 * W;
   int half_at = 0;  // of the task at work
   auto fetch = [&](const uint8_t* head, bool on, uint8_t* to) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int w = u + 32 * i;
-      int ea, eb;
-      place(w, ea, eb);
-      const bool some = on && w < pairs;
-      copy_raw<kF32, N>(to + 2 * i * kVector, some ? head + ea * E : a.q, some);
-      copy_raw<kF32, N>(to + (2 * i + 1) * kVector, some ? head + eb * E : a.q, some);
-    }
+    for (int i = 0; i < U; ++i)
+      if (on && u + 32 * i < pairs) {
+        copy_raw<kF32, N>(to + 2 * i * kVector, head + off[i][0]);
+        copy_raw<kF32, N>(to + (2 * i + 1) * kVector, head + off[i][1]);
+      }
   };
 
   // A task: a plane and head of the block, or `per` units of queries (without a cache: and
@@ -293,34 +292,45 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
   const int groups = q_groups + (kCache ? 0 : (a.H + heads - 1) / heads);
   const int units = cnt * groups;
   const int tasks = planes + (units + a.per - 1) / a.per;
-  auto fetch_plane = [&](int task, int t_first, uint8_t* to) {
+  const int head_step = heads * a.D * E;
+  auto fetch_plane = [&](int task, int t, uint8_t* to) {
     const int plane = task >= a.H, h = task - plane * a.H;
-    const uint8_t* from = (plane ? a.v : a.k) + int64_t(h) * a.D * E;
-    const int64_t step = plane ? a.v_step : a.k_step;
+    const int64_t step = plane ? a.v_step : a.k_step, unit_step = heads * step;
+    const uint8_t* from = (plane ? a.v : a.k) + (token0 + t + sub) * step + int64_t(h) * a.D * E;
 #pragma unroll 1
-    for (int i = 0; i < kUnits && t_first + i * heads < cnt; ++i) {
-      const int t = t_first + i * heads + sub;
-      fetch(from + (token0 + t) * step, t < cnt, to + i * kUnit);
+    for (const uint8_t* end = to + kNrHalf; to < end && t < cnt; to += kUnit) {
+      fetch(from, t + sub < cnt, to);
+      from += unit_step;
+      t += heads;
     }
   };
-  // unit (t, g): its head's place in the input, or the output; whether there is one
-  auto place_of = [&](int t, int g, bool out, const uint8_t*& at) {
-    const bool is_k = !kCache && g >= q_groups;
-    const int h = (is_k ? g - q_groups : g) * heads + sub;
-    const uint8_t* base = out ? (is_k ? a.ko : a.qo) : is_k ? a.k : a.q;
-    const int64_t step = out ? (is_k ? a.ko_step : a.qo_step) : is_k ? a.k_step : a.q_step;
-    at = base + (token0 + t) * step + int64_t(h) * a.D * E;
-    return h < (is_k ? a.H : a.Hq);
+  // the units from `first_unit`: f(head, whether there is one, token, keys, place in the ring)
+  auto walk = [&](int first_unit, const uint8_t* q, int64_t q_step, const uint8_t* k,
+                  int64_t k_step, uint8_t* at, auto&& f) {
+    int t = first_unit / groups, g = first_unit - t * groups;
+    const uint8_t* const end = at + a.per * kUnit;
+#pragma unroll 1
+    while (at < end && t < cnt) {
+      // units of one tensor and token
+      const bool is_k = !kCache && g >= q_groups;
+      const int64_t first_head = int64_t(is_k ? g - q_groups : g) * heads + sub;
+      const uint8_t* head = (is_k ? k : q) + (token0 + t) * (is_k ? k_step : q_step) +
+                            first_head * (a.D * E);
+      int left = (is_k ? a.H : a.Hq) - int(first_head);  // heads from there
+      const int g_end = is_k ? groups : q_groups;
+#pragma unroll 1
+      do {
+        f(head, left > 0, t, is_k, at);
+        head += head_step;
+        left -= heads;
+        at += kUnit;
+      } while (++g < g_end && at < end);
+      if (g == groups) g = 0, ++t;
+    }
   };
   auto fetch_units = [&](int first_unit, uint8_t* to) {
-    int t = first_unit / groups, g = first_unit - t * groups;
-#pragma unroll 1
-    for (int i = 0; i < a.per && t < cnt; ++i) {
-      const uint8_t* at;
-      const bool on = place_of(t, g, false, at);
-      fetch(at, on, to + i * kUnit);
-      if (++g == groups) g = 0, ++t;
-    }
+    walk(first_unit, a.q, a.q_step, a.k, a.k_step, to,
+         [&](const uint8_t* head, bool on, int, bool, uint8_t* at) { fetch(head, on, at); });
   };
   auto fetch_task = [&](int task, uint8_t* to) {
     if (task < planes) fetch_plane(task, 0, to);
@@ -377,19 +387,21 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
   auto finish = [&](float (*x)[2][N], int is_k, int t) {
     const void* weight = is_k ? a.kw : a.qw;
     if (weight) {
-      float s;
-      if constexpr (N > 1) {
-        float s2[2] = {0.0f, 0.0f};
+      float s = 0.0f;
 #pragma unroll
-        for (int y = 0; y < 2 * N; y += 2) fma2(s2, &x[0][y / N][y % N], &x[0][y / N][y % N], s2);
-        s = s2[0] + s2[1];
-      } else {
-        s = 0.0f;
+      for (int i = 0; i < U; ++i) {
+        float one = 0.0f, two = 0.0f;
 #pragma unroll
-        for (int i = 0; i < U; ++i) s = fmaf(x[i][0][0], x[i][0][0], fmaf(x[i][1][0], x[i][1][0], s));
+        for (int y = 0; y < N; ++y) {
+          one = fmaf(x[i][0][y], x[i][0][y], one);
+          two = fmaf(x[i][1][y], x[i][1][y], two);
+        }
+        if (u + 32 * i < pairs) s += one + two;
       }
-      for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float r = rsqrtf(fmaf(s, share, a.eps)), r2[2] = {r, r};
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float r = rsqrtf(fmaf(s, share, a.eps));
       if constexpr (N > 1) {
         if (u < pairs) {
           const float4* from = weights + (is_k ? a.D / 4 : 0) + u;
@@ -397,11 +409,8 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
           for (int y = 0; y < 2 * N; y += 4) {
             const float4 v = from[y / 4 * pairs];
             const float g[4] = {v.x, v.y, v.z, v.w};
-            float* f = &x[0][y / N][y % N];
-            mul2(f, f, r2);
-            mul2(f + 2, f + 2, r2);
-            mul2(f, f, g);
-            mul2(f + 2, f + 2, g + 2);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) x[0][(y + z) / N][(y + z) % N] *= r * g[z];
           }
         }
       } else {
@@ -409,12 +418,10 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
         for (int i = 0; i < U; ++i) {
           const int w = u + 32 * i;
           if (w >= pairs) continue;
-          int ea, eb;
-          place(w, ea, eb);
           uint32_t g[2][W];
           float f[2];
-          load_raw<kF32, N>(static_cast<const uint8_t*>(weight) + ea * E, g[0]);
-          load_raw<kF32, N>(static_cast<const uint8_t*>(weight) + eb * E, g[1]);
+          load_raw<kF32, N>(static_cast<const uint8_t*>(weight) + off[i][0], g[0]);
+          load_raw<kF32, N>(static_cast<const uint8_t*>(weight) + off[i][1], g[1]);
           widen<kF32, N>(g[0], f);
           widen<kF32, N>(g[1], f + 1);
           x[i][0][0] *= r * f[0];
@@ -441,17 +448,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
       for (int y = 0; y < N; y += 4) {
         const float4 vc = from[y / 4 * turning], vs = from[(N + y) / 4 * turning];
         const float c[4] = {vc.x, vc.y, vc.z, vc.w}, s[4] = {vs.x, vs.y, vs.z, vs.w};
-        if (!a.interleaved) {
+        if constexpr (!kInterleaved) {
 #pragma unroll
-          for (int z = 0; z < 4; z += 2) {
-            float *p = &x[0][0][y + z], *q = &x[0][1][y + z];
-            float ps[2], qs[2];
-            mul2(ps, p, s + z);
-            mul2(qs, q, s + z);
-            p[0] = fmaf(p[0], c[z], -qs[0]);
-            p[1] = fmaf(p[1], c[z + 1], -qs[1]);
-            fma2(q, q, c + z, ps);
-          }
+          for (int z = 0; z < 4; ++z) turn(x[0][0][y + z], x[0][1][y + z], c[z], s[z]);
         } else {
           // pairs 4 (y / 4) ... of the unit: of its first vector, then of the second
           float* p = &x[0][2 * y / N][2 * y % N];
@@ -481,28 +480,19 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
     cp_async_wait<1>();
     if (task >= planes) {
       // ---------------------------------------------------- units of queries and keys
-      const int unit = (task - planes) * a.per;
-      int t = unit / groups, g = unit - t * groups;
-#pragma unroll 1
-      for (int i = 0; i < a.per && t < cnt; ++i) {
-        float x[U][2][N];
-        number(held + i * kUnit, x);
-        finish(x, !kCache && g >= q_groups, t);
-        const uint8_t* at;
-        const bool on = place_of(t, g, true, at);
-        uint8_t* head = const_cast<uint8_t*>(at);
+      walk((task - planes) * a.per, a.qo, a.qo_step, a.ko, a.ko_step, held,
+           [&](const uint8_t* at, bool on, int t, bool is_k, uint8_t* from) {
+             float x[U][2][N];
+             number(from, x);
+             finish(x, is_k, t);
+             uint8_t* head = const_cast<uint8_t*>(at);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const int w = u + 32 * k;
-          int ea, eb;
-          place(w, ea, eb);
-          if (on && w < pairs) {
-            store_numbers<kF32, N>(head + ea * E, x[k][0]);
-            store_numbers<kF32, N>(head + eb * E, x[k][1]);
-          }
-        }
-        if (++g == groups) g = 0, ++t;
-      }
+             for (int i = 0; i < U; ++i)
+               if (on && u + 32 * i < pairs) {
+                 store_numbers<kF32, N>(head + off[i][0], x[i][0]);
+                 store_numbers<kF32, N>(head + off[i][1], x[i][1]);
+               }
+           });
     } else if constexpr (kCache) {
       // ---------------------------------------------------- a plane and head of the block
       const int plane = task >= a.H;
@@ -551,12 +541,13 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
       bool bad = false;
 #pragma unroll 1
       for (;;) {
-        sweep([&](float (*x)[2][N], int) {
+        sweep([&](float (*x)[2][N], int t) {
           if (bad) guard(x);
+          if (t >= cnt) return;
 #pragma unroll
           for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int y = 0; y < N; ++y)
+            for (int y = 0; y < N && u + 32 * i < pairs; ++y)
               top = max(top, max(__float_as_uint(x[i][0][y]) & 0x7fffffffu,
                                  __float_as_uint(x[i][1][y]) & 0x7fffffffu));
         });
@@ -591,10 +582,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
         uint8_t* to = codes + int64_t(first + t) * a.D;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const int w = u + 32 * i;
-          int ea, eb;
-          place(w, ea, eb);
-          if (w >= pairs) continue;
+          if (u + 32 * i >= pairs) continue;
           float* f = x[i][0];
           if (exact) {
 #pragma unroll
@@ -603,8 +591,8 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
 #pragma unroll
             for (int y = 0; y < 2 * N; ++y) f[y] /= scale;
           }
-          store_codes<N>(to + ea, x[i][0]);
-          store_codes<N>(to + eb, x[i][1]);
+          store_codes<N>(to + off[i][0] / E, x[i][0]);
+          store_codes<N>(to + off[i][1] / E, x[i][1]);
         }
       });
       if (lane == 0) *sp = scale;
@@ -614,9 +602,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
 
 namespace {
 
-template <bool kF32, int N, bool kCache>
+template <bool kF32, int N, bool kCache, bool kInterleaved>
 int launch_shape(const NormRopeArgs& a, int tokens, int sms, cudaStream_t st) {
-  auto kern = norm_rope_kernel<kF32, N, kCache>;
+  auto kern = norm_rope_kernel<kF32, N, kCache, kInterleaved>;
   const size_t fractions = (size_t(a.half) * 8 + 15) / 16 * 16;
   const size_t smem = kNrWarps * 2 * kNrHalf + fractions + (N > 1 ? size_t(a.D) * 8 + size_t(tokens) * a.half * 8 : 0);
   static std::atomic<uint64_t> done{0};
@@ -631,10 +619,16 @@ int launch_shape(const NormRopeArgs& a, int tokens, int sms, cudaStream_t st) {
   const int heads = 32 / lanes;
   const int64_t groups = (a.Hq + heads - 1) / heads + (kCache ? 0 : (a.H + heads - 1) / heads);
   const int64_t units = groups * (tokens < a.T ? tokens : a.T);
-  const int64_t warps = int64_t(sms) * kNrCtas * kNrWarps;
-  int64_t per = units * tiles / warps;
+  // The longer the tasks, the fewer of them wait: the longest that leave no warp much less
+  // to do than another.
+  const int64_t each = units * tiles / (int64_t(sms) * kNrCtas * kNrWarps);  // of a warp
+  const int most_units = each < 1 ? 1 : each < kNrUnits<kF32, N> ? int(each) : kNrUnits<kF32, N>;
   NormRopeArgs with = a;
-  with.per = int(per < 1 ? 1 : per > kNrUnits<kF32, N> ? kNrUnits<kF32, N> : per);
+  int64_t least = INT64_MAX;
+  for (int per = most_units; per > 0; --per) {
+    const int64_t rounds = ((units + per - 1) / per + kNrWarps - 1) / kNrWarps * per;
+    if (rounds < least) least = rounds, with.per = per;
+  }
   const int64_t tasks = (kCache ? 2 * a.H : 0) + (units + with.per - 1) / with.per;
   int64_t parts = kNrCtas * int64_t(sms) / tiles, most = (tasks + kNrWarps - 1) / kNrWarps;
   parts = parts < 1 ? 1 : parts > most ? most : parts;
@@ -642,7 +636,7 @@ int launch_shape(const NormRopeArgs& a, int tokens, int sms, cudaStream_t st) {
   return launch_pdl(kern, dim3(unsigned(tiles), unsigned(parts)), dim3(kNrThreads), smem, st, with);
 }
 
-template <bool kF32, bool kCache>
+template <bool kF32, bool kCache, bool kInterleaved>
 int launch_type(const NormRopeArgs& a, int tokens, int sms, uintptr_t bits, cudaStream_t st) {
   // `bits`: every address and stride or-ed together
   const bool table = int64_t(tokens) * a.half * 8 <= kNrTable;
@@ -650,9 +644,9 @@ int launch_type(const NormRopeArgs& a, int tokens, int sms, uintptr_t bits, cuda
     return table && a.half % n == 0 && a.D % (2 * n) == 0 && bits % (n * (kF32 ? 4 : 2)) == 0;
   };
   if constexpr (!kF32)
-    if (fits(8)) return launch_shape<kF32, 8, kCache>(a, tokens, sms, st);
-  if (fits(4)) return launch_shape<kF32, 4, kCache>(a, tokens, sms, st);
-  return launch_shape<kF32, 1, kCache>(a, tokens, sms, st);
+    if (fits(8)) return launch_shape<kF32, 8, kCache, kInterleaved>(a, tokens, sms, st);
+  if (fits(4)) return launch_shape<kF32, 4, kCache, kInterleaved>(a, tokens, sms, st);
+  return launch_shape<kF32, 1, kCache, kInterleaved>(a, tokens, sms, st);
 }
 
 }  // namespace
@@ -682,7 +676,6 @@ int launch_norm_rope(const NormRopeLaunch& r) {
   a.half = r.half;
   a.B = r.B;
   a.T = r.T;
-  a.interleaved = r.interleaved;
   a.eps = r.eps;
   a.factor = r.factor;
   a.err = r.err;
@@ -701,11 +694,22 @@ int launch_norm_rope(const NormRopeLaunch& r) {
     if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
   }
   cudaStream_t st = static_cast<cudaStream_t>(r.stream);
+  auto launch = [&](auto cache, int tokens) {
+    constexpr bool kCache = decltype(cache)::value;
+    const bool f32 = r.dtype == SPEC_F32;
+    if (r.interleaved)
+      return f32 ? launch_type<true, kCache, true>(a, tokens, sms, bits, st)
+                 : launch_type<false, kCache, true>(a, tokens, sms, bits, st);
+    return f32 ? launch_type<true, kCache, false>(a, tokens, sms, bits, st)
+               : launch_type<false, kCache, false>(a, tokens, sms, bits, st);
+  };
   if (!r.pool) {
-    a.J = (r.T + kNrTile - 1) / kNrTile;
-    const int tokens = r.T < kNrTile ? r.T : kNrTile;
-    return r.dtype == SPEC_F32 ? launch_type<true, false>(a, tokens, sms, bits, st)
-                               : launch_type<false, false>(a, tokens, sms, bits, st);
+    // half of it where the last round of CTAs would be a large part of them all
+    a.tile = int64_t(r.B) * ((r.T + kNrTile - 1) / kNrTile) > int64_t(4) * sms * kNrCtas
+                 ? kNrTile
+                 : kNrTile / 2;
+    a.J = (r.T + a.tile - 1) / a.tile;
+    return launch(std::false_type{}, r.T < a.tile ? r.T : a.tile);
   }
   const int64_t layer_bytes = int64_t(2) * r.H * r.bs * r.D;
   a.pool = static_cast<uint8_t*>(r.pool) + r.layer * layer_bytes;
@@ -717,9 +721,7 @@ int launch_norm_rope(const NormRopeLaunch& r) {
   a.J = (r.T + 2 * r.bs - 2) / r.bs;
   a.block_bytes = r.num_layers * layer_bytes;
   a.block_scales = int64_t(r.num_layers) * 2 * r.H;
-  const int tokens = r.T < r.bs ? r.T : r.bs;
-  return r.dtype == SPEC_F32 ? launch_type<true, true>(a, tokens, sms, bits, st)
-                             : launch_type<false, true>(a, tokens, sms, bits, st);
+  return launch(std::true_type{}, r.T < r.bs ? r.T : r.bs);
 }
 
 }  // namespace sv
