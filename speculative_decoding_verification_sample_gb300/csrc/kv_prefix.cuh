@@ -86,9 +86,13 @@ __host__ __device__ inline int64_t pf_units(int64_t nq, int64_t tiles) {
           : rest > 0 ? pf_item_units(kPfOneUnits, tiles)
                      : 0);
 }
-// Tiles of an item that begin before its unit x.
+// Tiles of an item that begin before its unit x (divided by one of two constants: a division
+// of 64 bits by w is a hundred instructions).
 __host__ __device__ inline int pf_cut(int64_t x, int w) {
-  return x <= kPfItemUnits ? 0 : int((x - kPfItemUnits + w - 1) / w);
+  if (x <= kPfItemUnits) return 0;
+  const uint64_t n = uint64_t(x - kPfItemUnits);
+  return int(w == kPfOneUnits ? (n + kPfOneUnits - 1) / kPfOneUnits
+                              : (n + kPfTwoUnits - 1) / kPfTwoUnits);
 }
 
 struct PfArgs {
