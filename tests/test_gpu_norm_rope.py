@@ -1,9 +1,9 @@
 """Norms and rotary positions, with and without the 8-bit cache, against the fp64 oracle.
 
 Error bound. With u = 2^-24: the sum of squares of a head is off by at most 21 u of itself (16
-sequential terms of a lane and 5 steps across lanes), so 1 / sqrt by 13 u with its own roundings,
-a normed number by 15 u; cos and sin by 4 u (2 of the angle, 2 of the polynomial and the factor),
-a turned number's products and sum by 2 u: 22 u of |a| + |b| in all, taken as 32 u. The angle is
+terms of a lane and 5 steps across lanes), its mean by 3 u more, so 1 / sqrt by 12 u and 4 u of its
+own, a normed number by 18 u; cos and sin by 4 u (2 of the angle, 2 of the polynomial and the
+factor), a turned number's products and sum by 2 u: 24 u of |a| + |b| in all, taken as 32 u. The angle is
 off by 2^-52 of its fraction of a turn a position, the oracle's by 2^-53. Then one rounding to the
 output's type, half of finfo.eps.
 """
@@ -191,7 +191,7 @@ def test_binding_refuses_layouts():
 
 # ------------------------------------------------------------------ into the cache
 def _append_case(seed, B, T, Hq, H, D, pairs, bs, dtype, *, interleaved=False, norm=True, lo=0,
-                 hi=100, ragged=False, layers=2, tree=False, grow=1.0):
+                 hi=100, ragged=False, layers=2, tree=False, grow=1.0, scale_by=1.0):
     rng = np.random.default_rng(seed)
     (q, k, v), (qn, kn, vn) = _inputs(rng, B, T, Hq, H, D, dtype)
     w, wn = _weights(rng, D, dtype, norm)
@@ -203,6 +203,7 @@ def _append_case(seed, B, T, Hq, H, D, pairs, bs, dtype, *, interleaved=False, n
     n = rng.integers(0, T + 1, B) if ragged else np.full(B, T)
     bt, _, nb = h.table(rng, L + n, bs)
     pool, scales = h.cache(rng, nb, layers, H, bs, D)
+    scales = scales * scale_by
     pos = L[:, None] + (rng.integers(0, T, (B, T)) if tree else np.arange(T))
     qo = torch.full((B, T, Hq, D), 5.0, dtype=TYPES[dtype], device="cuda")
     dp, ds, err = h.dev_pool(pool), h.dev_scales(scales), h.i32([0])
@@ -273,6 +274,10 @@ def _append_case(seed, B, T, Hq, H, D, pairs, bs, dtype, *, interleaved=False, n
     (3, 7, 3, 5, 48, 24, 5, "fp32", dict(ragged=True)),           # odd blocks
     (4, 5, 2, 2, 64, 32, 16, "bf16", dict(norm=False, grow=3000.0)),  # kept codes move
     (64, 5, 8, 2, 64, 32, 16, "bf16", dict(ragged=True)),
+    # older scales between powers of two (a quotient of bf16 numbers by 1.5 2^e is a tie or at
+    # least a third of a step from one: the values' codes are the oracle's)
+    (5, 5, 4, 2, 128, 64, 64, "bf16", dict(lo=20, scale_by=1.5)),
+    (3, 40, 4, 2, 64, 32, 128, "bf16", dict(lo=20, scale_by=96.0)),
 ])
 def test_append(B, T, Hq, H, D, pairs, bs, dtype, more):
     _append_case(B * 31 + T, B, T, Hq, H, D, pairs, bs, dtype, **more)
@@ -314,6 +319,31 @@ def test_append_errors_and_values():
     vals = q8.VALUES[gp[5, 0]]
     assert np.isfinite(vals).all() and np.isfinite(gs).all()
     assert vals[1, 1, 11, 3] == 0 and vals[1, 0, 12, 3] * gs[5, 0, 1, 0] < -3e38 / 1.1
+
+
+def test_values_that_are_not_finite_in_long_blocks():
+    """Beyond what a warp holds at a time: zeros and the largest number, the others as ever."""
+    rng = np.random.default_rng(13)
+    T, D = 60, 128
+    (q, k, v), (_, _, vn) = _inputs(rng, 1, T, 2, 1, D, "bf16", packed=False)
+    v[0, 45, 0, 7], v[0, 3, 0, 9] = float("nan"), float("inf")
+    k[0, 50, 0, 1] = float("nan")
+    vn = v.double().cpu().numpy()
+    pool, scales = h.cache(rng, 2, 1, 1, 64, D)
+    dp, ds, err = h.dev_pool(pool), h.dev_scales(scales), h.i32([0])
+    sv.kv_q8_norm_rope_append(q, k, v, torch.empty_like(q), dp, ds, h.i32([[1, 0]]), h.i32([0]),
+                              k_weight=torch.ones(D, device="cuda").bfloat16(), err_flag=err)
+    assert int(err) == sv.SPEC_DERR_VALUE
+    wp, wsc, _ = q8.append(np.zeros((1, T, 1, D)), vn, pool, scales, np.array([[1, 0]]), [0])
+    gp = dp.view(torch.uint8).cpu().numpy()
+    assert np.array_equal(gp[1, 0, 1], wp[1, 0, 1]) and float(ds[1, 0, 1, 0]) == wsc[1, 0, 1, 0]
+    keys = q8.VALUES[gp[1, 0, 0, 0]] * float(ds[1, 0, 0, 0])
+    assert (keys[50] == 0).all() and np.isfinite(keys).all()
+    y, _ = rope.heads(k.double().cpu().numpy(), np.ones(D), np.arange(T)[None], None)
+    s = float(ds[1, 0, 0, 0])
+    rows = [t for t in range(T) if t != 50]
+    assert (np.abs(keys[rows] - y[0, rows, 0])
+            <= np.maximum(np.abs(y[0, rows, 0]) * 2.0 ** -4, s * 2.0 ** -10) * 1.001).all()
 
 
 def test_captured_and_on_another_stream():

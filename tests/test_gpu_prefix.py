@@ -1,12 +1,15 @@
 """Attention of rows that share a prefix's blocks against the fp64 oracle, which takes each row by
 itself.
 
-Error bound. Queries and cached numbers are exact in bf16 (power-of-two scales); a score is a sum
-of D products in fp32, off by at most (D + 8) 2^-23 of sum |q_d k_d| * softmax_scale (`reach`; the
-tensor cores may cut the sum's terms, hence 2^-23), and a weight by as much of itself; the
-probability's rounding to bf16 is 2^-8 of each term; exponentials, their argument (2^-24 of an
-argument that itself is at most twice reach, in log2 units) and the joins add 2^-19 of the sum of
-magnitudes (`spread`) at most where reach stays below 8. Then one rounding to bf16, 2^-8.
+Error bound. Cached numbers are exact in the products (e4m3 codes of keys, values widened to bf16,
+power-of-two scales), queries down to 2^-9 of their head's largest; smaller ones, fewer than one in
+a hundred of these normal numbers, are off by 2^-17 of the largest, so a score by less than 2^-20 of
+its sum of magnitudes for them. A score is a sum of 2 D products in fp32; with that it is off by at
+most (D + 8) 2^-23 of sum |q_d k_d| * softmax_scale (`reach`; the tensor cores may cut the sum's
+terms, hence 2^-23), and a weight by as much of itself; the probability's rounding to bf16 is 2^-8
+of each term; exponentials, their argument (2^-24 of an argument that itself is at most twice reach,
+in log2 units) and the joins add 2^-19 of the sum of magnitudes (`spread`) at most where reach stays
+below 8. Then one rounding to bf16, 2^-8.
 """
 import numpy as np
 import pytest
@@ -222,7 +225,7 @@ def test_rising_and_large_scores():
     """Keys that grow along the sequence move the references again and again; scores of a few
     hundred leave one key with all the weight."""
     rng, L, bt, starts, members, nb, pool, scales, q, dq = _small(4, groups=((1500, 4), (700, 3)))
-    order = np.empty(nb)
+    order = np.zeros(nb)
     for g in range(2):
         for r in members[starts[g]:starts[g + 1]]:
             for j, x in enumerate(bt[r]):
