@@ -251,146 +251,153 @@ size_t kv_prefix_plan_size(int B, int num_groups, int num_members) {
 }
 
 // ------------------------------------------------------------------ joining
-// A warp a query, its lanes over the head's numbers. The pieces of the query's two items
-// (prefix, own keys) are found a lane each, so that their statistics come at once and their
-// numbers follow without a wait between them; they are added in a fixed order. Bound by
-// instructions, those that find the pieces: 41 us for 40960 queries of 128 numbers, 58 MB.
-constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32;
+// A warp takes up to 8 queries of a row and kv head. What their pieces are is found four lanes a
+// query side by side: its items of the prefix and of the row's own keys, and of each the first
+// piece (in the place of the query) and the second (in that of a CTA); further pieces, of items
+// that cross several CTAs, come by two. Then the queries follow one by one, the lanes over the
+// head's numbers. (Found for one query at a time, this was most of 750 instructions a query.)
+constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32, kPfJoinQueries = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const PfArgs a, int ctas) {
+__global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const PfArgs a, int ctas, int per) {
   constexpr int N = D / 32;  // numbers of a lane
+  constexpr uint32_t kAll = 0xffffffffu;
   pdl_trigger();
   pdl_wait();
   const PfPlan p = pf_plan(a, ctas);
-  const int R = a.T * a.G, groups = (R + kPfJoinWarps - 1) / kPfJoinWarps;
-  const int bh = blockIdx.x / groups, b = bh / a.H, h = bh - b * a.H, lane = threadIdx.x & 31;
-  const int r = (blockIdx.x - bh * groups) * kPfJoinWarps + (threadIdx.x >> 5);
-  if (r >= R) return;
+  const int R = a.T * a.G, chunks = (R + per - 1) / per;
+  const int warp = blockIdx.x * kPfJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int bh = warp / chunks, b = bh / a.H, h = bh - b * a.H, r0 = (warp - bh * chunks) * per;
+  if (b >= a.B) return;
   PfRow row = {};
   row.tiles = -1;
   if (p.ok) row = p.rows[b];
   // lengths that changed since the plan was made: the row's keys are not the plan's
   const bool same = p.ok && row.L == a.sl[b] && row.n == (a.nn ? a.nn[b] : a.T);
   const bool bad = row.tiles < 0 || !same;
-  if (bad && a.err && h == 0 && r == 0 && lane == 0)
+  if (bad && a.err && h == 0 && r0 == 0 && lane == 0)
     atomicOr(a.err, p.ok ? SPEC_DERR_BAD_LENGTH : SPEC_DERR_BAD_SLOT);
-  float m = -INFINITY, l = 0.0f, o[N] = {};
-  auto load = [&](const float* part, float* v) {
-    if constexpr (N == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(part + 4 * lane);
-      v[0] = x.x;
-      v[1] = x.y;
-      v[N - 2] = x.z;
-      v[N - 1] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(part + 2 * lane);
-      v[0] = x.x;
-      v[1] = x.y;
-    }
-  };
-  // up to 32 pieces, a lane each (st: -inf, 0 where there is none), `part` their numbers
-  auto gather = [&](float2 st, const float* part) {
-    float top = st.x;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.0f : mn;
-    const float was = ex2_approx(m - base), mine = ex2_approx(st.x - base);
-    m = mn;
-    l *= was;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] *= was;
-    unsigned left = __ballot_sync(0xffffffffu, part != nullptr);
-    const uint64_t at = reinterpret_cast<uint64_t>(part);
-    while (left) {
-      constexpr int kAtOnce = 4;
-      float v[kAtOnce][N], w[kAtOnce], s[kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int x = left ? __ffs(left) - 1 : 0;
-        w[k] = __shfl_sync(0xffffffffu, mine, x);
-        s[k] = __shfl_sync(0xffffffffu, st.y, x);
-        const uint64_t from = __shfl_sync(0xffffffffu, at, x);
-        if (left) {
-          load(reinterpret_cast<const float*>(from), v[k]);
-        } else {
-          w[k] = s[k] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < N; ++i) v[k][i] = 0.0f;
-        }
-        left &= left - 1;
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        l += s[k] * w[k];
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] += v[k][i] * w[k];
-      }
-    }
-  };
   auto quotient = [](int64_t n, int d) -> int64_t {
     return n >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
   };
-  const int pack = pf_pack(R), t = r / a.G;
+  const int r = r0 + (lane >> 2), t = r / a.G;
   const int64_t query = (int64_t(b) * a.T + t) * a.H * a.G + h * a.G + r - t * a.G;
-  if (!bad && t < row.n) {
-    // even lanes: the query's item of the prefix, odd lanes: the one of the row's own keys
-    const bool own = lane & 1, has = own ? row.tiles > 0 : row.group >= 0;
-    const int x0 = own ? (pack > 1 ? b % pack * (kPfTile / pack) + r : r) : row.at * R + r;
-    int64_t u = 0, end = 0;
-    int w = kPfOneUnits, c0 = 0, c1 = 0;
-    if (has) {
-      const int e = own ? p.NG + b / pack : row.group, qb = x0 / 256;
-      int64_t nq = int64_t(row.n) * a.G, tiles = row.tiles;
-      if (!own) {
-        const PfGroup g = p.groups[e];
-        nq = int64_t(g.count) * R;
-        tiles = g.tiles;
-      }
-      const int64_t base = p.prefix[e], per_h = quotient(p.prefix[e + 1] - base, a.H);
-      if (own && pack > 1) tiles = uint64_t(per_h - kPfItemUnits) / kPfOneUnits;  // all its rows'
-      else if (nq - qb * 256 > 128) w = kPfTwoUnits;
-      u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, tiles);
-      end = u + pf_item_units(w, tiles);
-      c0 = pf_owner(p, u + kPfItemUnits);
-      c1 = pf_owner(p, end - 1);
+  // even lanes: the item of the prefix, odd lanes: the one of the row's own keys
+  const int pack = pf_pack(R), pack_at = pack == 4 ? b >> 2 : pack == 2 ? b >> 1 : b;
+  const bool own = lane & 1, has = !bad && (lane >> 2) < per && r < R && t < row.n &&
+                                   (own ? row.tiles > 0 : row.group >= 0);
+  const int x0 = own ? (pack > 1 ? (b & (pack - 1)) * (kPfTile / pack) + r : r) : row.at * R + r;
+  int64_t u = 0, end = 0;
+  int w = kPfOneUnits, c0 = 0, c1 = 0;
+  if (has) {
+    const int e = own ? p.NG + pack_at : row.group, qb = x0 / 256;
+    int64_t nq = int64_t(row.n) * a.G, tiles = row.tiles;
+    if (!own) {
+      const PfGroup g = p.groups[e];
+      nq = int64_t(g.count) * R;
+      tiles = g.tiles;
     }
-    // Pieces: first those in the places of the queries, a lane each, then those of the prefix in
-    // the places of CTAs, and those of the row's own keys, two lanes by turns.
-    const int more0 = __shfl_sync(0xffffffffu, c1 - c0, 0),
-              more1 = __shfl_sync(0xffffffffu, c1 - c0, 1), more = more0 > more1 ? more0 : more1;
-    float2 st = make_float2(-INFINITY, 0.0f);
-    const float* part = nullptr;
-    if (lane < 2 && has) {
+    const int64_t base = p.prefix[e], per_h = quotient(p.prefix[e + 1] - base, a.H);
+    if (own && pack > 1) tiles = uint64_t(per_h - kPfItemUnits) / kPfOneUnits;  // all its rows'
+    else if (nq - qb * 256 > 128) w = kPfTwoUnits;
+    u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, tiles);
+    end = u + pf_item_units(w, tiles);
+    c0 = pf_owner(p, u + kPfItemUnits);
+    c1 = pf_owner(p, end - 1);
+  }
+  // piece x of the lane's item: its statistics and numbers, if any
+  auto piece = [&](int x, float2& st, const float*& part) {
+    st = make_float2(-INFINITY, 0.0f);
+    part = nullptr;
+    const int c = c0 + x;
+    if (!has || c > c1) return;
+    if (x == 0) {
       st = (own ? a.stats[1] : a.stats[0])[query];
       part = (own ? a.parts[1] : a.parts[0]) + query * D;
+      return;
     }
-    for (int first = 0; first <= more; first += 16) {
-      const int x = first + (lane >> 1), c = c0 + x;  // piece x > 0: of CTA c
-      if (x > 0 && has && c <= c1) {
-        const int64_t u0 = pf_share(p, c) - u, u1 = min(pf_share(p, c + 1), end) - u;
-        if (pf_cut(u0, w) < pf_cut(u1, w)) {  // else no tile begins there
-          const int64_t at = int64_t(c) * 256 + x0 % 256;
-          st = a.mid_stats[at];
-          part = a.mid + at * D;
+    const int64_t u0 = pf_share(p, c) - u, u1 = min(pf_share(p, c + 1), end) - u;
+    if (pf_cut(u0, w) < pf_cut(u1, w)) {  // else no tile begins there
+      const int64_t at = int64_t(c) * 256 + x0 % 256;
+      st = a.mid_stats[at];
+      part = a.mid + at * D;
+    }
+  };
+  auto most = [](float x) {  // of four lanes
+    x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
+    return fmaxf(x, __shfl_xor_sync(kAll, x, 2));
+  };
+  auto sum = [](float x) {
+    x += __shfl_xor_sync(kAll, x, 1);
+    return x + __shfl_xor_sync(kAll, x, 2);
+  };
+  float2 st;
+  const float* part;
+  piece(lane >> 1 & 1, st, part);
+  const float m = most(st.x), base = m == -INFINITY ? 0.0f : m;
+  const float weight = ex2_approx(st.x - base), l = sum(st.y * weight);
+  int more = max(c1 - c0, __shfl_xor_sync(kAll, c1 - c0, 1));
+
+  for (int k = 0; k < per && r0 + k < R; ++k) {
+    float o[N] = {};
+    // the four pieces that the lanes of query k have
+    auto add = [&](const float* part, float weight) {
+      float v[4][N], f[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint64_t from = __shfl_sync(kAll, reinterpret_cast<uint64_t>(part), 4 * k + y);
+        f[y] = __shfl_sync(kAll, weight, 4 * k + y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[y][i] = 0.0f;
+        if (from == 0) continue;
+        const float* at = reinterpret_cast<const float*>(from) + N * lane;
+        if constexpr (N == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(at);
+          v[y][0] = x.x;
+          v[y][1] = x.y;
+          v[y][N - 2] = x.z;
+          v[y][N - 1] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(at);
+          v[y][0] = x.x;
+          v[y][1] = x.y;
         }
       }
-      gather(st, part);
-      st = make_float2(-INFINITY, 0.0f);
-      part = nullptr;
-    }
-  }
-  const float inv = bad ? __uint_as_float(0x7fc00000u) : l == 0.0f ? 0.0f : 1.0f / l;
-  uint32_t x[N / 2];
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
-    x[i] = *reinterpret_cast<const uint32_t*>(&v);
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] += v[y][i] * f[y];
+    };
+    add(part, weight);
+    float lk = __shfl_sync(kAll, l, 4 * k), mk = __shfl_sync(kAll, m, 4 * k);
+    const int last = __shfl_sync(kAll, more, 4 * k);
+#pragma unroll 1
+    for (int x = 2; x <= last; x += 2) {
+      float2 st2;
+      const float* part2;
+      piece(x + (lane >> 1 & 1), st2, part2);
+      const float mn = fmaxf(mk, __shfl_sync(kAll, most(st2.x), 4 * k));
+      const float base2 = mn == -INFINITY ? 0.0f : mn, was = ex2_approx(mk - base2);
+      const float weight2 = ex2_approx(st2.x - base2);
+      lk = lk * was + __shfl_sync(kAll, sum(st2.y * weight2), 4 * k);
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] *= was;
+      mk = mn;
+      add(part2, weight2);
+    }
+    const float inv = bad ? __uint_as_float(0x7fc00000u) : lk == 0.0f ? 0.0f : 1.0f / lk;
+    uint32_t x[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+      x[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const int64_t at = __shfl_sync(kAll, query, 4 * k);
+    uint32_t* to =
+        reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at * D) + N / 2 * lane;
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[N / 2 - 1]);
+    else *to = x[0];
   }
-  uint32_t* to =
-      reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + query * D) + N / 2 * lane;
-  if constexpr (N == 4) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[N / 2 - 1]);
-  else *to = x[0];
 }
 
 namespace {
@@ -488,11 +495,17 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
                                      k.stream);
   if (st != SPEC_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
+  // as many queries a warp as leave 32 warps for each SM, in equal chunks
   const int R = a.T * a.G;
-  const dim3 grid(unsigned(a.B * a.H * ((R + kPfJoinWarps - 1) / kPfJoinWarps)));
+  const int64_t each = int64_t(a.B) * a.H * R / (int64_t(sms) * 32);
+  int per = each < 1 ? 1 : each > kPfJoinQueries ? kPfJoinQueries : int(each);
+  const int chunks = (R + per - 1) / per;
+  per = (R + chunks - 1) / chunks;
+  const int64_t warps = int64_t(a.B) * a.H * chunks;
+  const dim3 grid(unsigned((warps + kPfJoinWarps - 1) / kPfJoinWarps));
   return a.D == 128
-             ? launch_pdl(kv_prefix_join_kernel<128>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas)
-             : launch_pdl(kv_prefix_join_kernel<64>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas);
+             ? launch_pdl(kv_prefix_join_kernel<128>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas, per)
+             : launch_pdl(kv_prefix_join_kernel<64>, grid, dim3(kPfJoinThreads), 0, stream, a, ctas, per);
 }
 
 }  // namespace sv
