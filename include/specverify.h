@@ -528,6 +528,8 @@ size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads,
  *                int32, ascending: group g has members group_starts[g] ..
  *                group_starts[g + 1] - 1. Rows may be in no group; no groups, and a null
  *                group_rows with no members, are allowed
+ *   always       0: share where it saves time (long prefixes of many rows); else wherever
+ *                rows have whole tiles in common
  *   plan         kv_prefix_plan_bytes(B, num_groups, num_members) bytes, 256-byte aligned,
  *                no initialisation
  * A group shares the blocks that the tables of its rows (those with new tokens) have in
@@ -541,8 +543,8 @@ size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads,
 int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
                    const int32_t* group_starts, const int32_t* group_rows, int num_groups,
                    int num_members, int T, int num_q_heads, int num_kv_heads, int num_blocks,
-                   int block_size, int B, int max_blocks, void* plan, size_t plan_bytes,
-                   void* stream, int32_t* err_flag);
+                   int block_size, int B, int max_blocks, int always, void* plan,
+                   size_t plan_bytes, void* stream, int32_t* err_flag);
 
 /* kv_prefix_plan_bytes - size of a plan; 0 for sizes that kv_prefix_plan rejects. */
 size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
@@ -556,12 +558,13 @@ size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
  *                SPEC_DERR_BAD_LENGTH; with a plan of other sizes all do, and SPEC_DERR_BAD_SLOT
  *   workspace    kv_q8_prefix_attention_workspace_bytes bytes, 256-byte aligned, no
  *                initialisation; calls that share one must be ordered on the device
- * Everything else is as in kv_q8_attention. With bf16 queries, head_dim 64 or 128 and
- * blocks of a multiple of 16 tokens the products run on the tensor cores in bf16: queries and cached codes are
- * exact there, with scales that are powers of two between 2^-100 and 2^7 (others round
- * code * scale to bf16), probabilities are rounded to bf16; scores, maxima, sums and outputs
- * up to the last rounding are fp32. The NaN code counts as 480 there (kv_q8_append leaves
- * none). Other types, head and block sizes are kv_q8_attention's, each row by itself.
+ * Everything else is as in kv_q8_attention, which takes the rows' own keys. Shared keys: queries
+ * as there in two e4m3 terms, against the keys' codes; probabilities are rounded to bf16
+ * against values in bf16 (exact with scales that are powers of two between 2^-100 and 2^7;
+ * others round code * scale to bf16); scores, maxima, sums and outputs up to the last rounding
+ * are fp32. A value's NaN code counts as 480 there (kv_q8_append leaves none). Nothing is shared
+ * with fp32 queries, head sizes but 64 and 128, and blocks that are not 16, 32, 64 or a multiple
+ * of 128 tokens. The result does not depend on timing, but on the groups in its roundings.
  */
 int kv_q8_prefix_attention(const void* q, int dtype, const void* kv_pool, const float* kv_scales,
                            const int32_t* block_table, const int32_t* seq_lens,

@@ -14,7 +14,7 @@
 // its way to shared memory, exactly: a code's exponent and fraction are moved to their place,
 // then one product with scale * 2^120, exact for the powers of two that appending leaves (other
 // scales take a path that multiplies in fp32 and rounds once to bf16). Widening K too kept the
-// loading warps from keeping up. P is rounded to bf16 (2^-9 relative, as the output); the sums l
+// loading warps from keeping up. P is rounded to bf16 (2^-8 relative, as the output); the sums l
 // take it in fp32 before. K's scales belong to 16 keys and enter the softmax as one factor each.
 //   Softmax: a row's reference is a bound of its scores, in whole binades, 24 above the largest
 // of those that set it; when a later one exceeds it, it is set anew, and O and l are scaled,
@@ -23,6 +23,13 @@
 // Roles, of 4 warps each with registers moved to the softmax: two softmax groups; widening of V;
 // a warp that issues the products, one that walks the work list and prepares queries, one that
 // finds the tiles and starts their copies. One CTA per SM.
+//
+// Bound by the chain of a tile: scores 240 cycles after the last product is issued, softmax 1700
+// to 2100, a turn's products 1170 and what the issuing warp does before them, 1100 with code from
+// the second-level instruction cache; a step of two M tiles takes 4860 cycles, its products 2050.
+// 440 us for 5120 queries a kv head before 16000 shared keys, 346 GFLOP: 0.42 of the bf16 peak,
+// the tensor cores 37 % of the time at work. (A warp for each group's products made a step 4450
+// cycles, and the call no faster: the turns' order costs as much at items' ends.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -69,24 +76,20 @@ struct PfGuard {
 struct PfItem {
   int stop;       // no more items
   int two;        // two M tiles (else one, and its key tiles by turns)
-  int own;        // 0 a group's prefix, 1 rows' own keys
-  int row, rows;  // prefix: a row of the group; own keys: the first row, rows of the pack
-  int entry;      // prefix: the group's first member
-  int stride;     // a pack's queries from row to row; 0: no pack
+  int row;        // one of the group
+  int entry;      // the group's first member
   int h;
   int t0, t1;     // tiles of the item
-  int q0, nq;     // first query of the block in its entry, queries of the block
+  int q0, nq;     // first query of the block in its group, queries of the block
 };
 
 // A key tile: what the warps need of it.
 struct PfTile {
   int plane[kPfParts], in_block[kPfParts];  // where the parts' V is (plane -1: nowhere)
-  alignas(16) float2 ks[kPfParts];  // of K: scale, and -inf for a part that is hidden (else 0)
-  float raw_ks[kPfParts], vs[kPfParts];     // the scales of K where one is below 0, of V
-  int pos, L;                // position; committed tokens of its row
-  int slot, last;            // the row's place in the pack; whether it is the row's last tile
-  int keys, valid;           // keys up to the row's end; bits: parts that are copied
-  int below, plain_v;        // a scale of K is below 0; V's are 2^-100 .. 2^7
+  alignas(16) float ks[kPfParts];           // scales of K (1 where one of them is below 0),
+  float raw_ks[kPfParts], vs[kPfParts];     // those of K then, of V
+  int valid;                                // bits: parts that are copied
+  int below, plain_v;                       // a scale of K is below 0; V's are 2^-100 .. 2^7
 };
 
 // kTiles: more than the key tiles between their finding and the end of their V: one being
@@ -153,12 +156,8 @@ __device__ __forceinline__ int64_t pf_query(const PfArgs& a, const PfPlan& p, co
   b = -1;
   t = n = 0;
   if (x >= it.nq) return -1;
-  const int R = a.T * a.G, qi = it.q0 + x;
-  const int each = !it.own ? R : it.stride;  // queries from row to row
-  const int e = each == 0 ? 0 : qi / each, r = qi - e * each;
-  if (r >= R) return -1;
-  if (it.own) b = it.row + e;
-  else b = it.entry + e < p.NE ? p.members[it.entry + e] : -1;
+  const int R = a.T * a.G, qi = it.q0 + x, e = qi / R, r = qi - e * R;
+  b = it.entry + e < p.NE ? p.members[it.entry + e] : -1;
   if (b < 0 || b >= a.B) return -1;
   n = p.rows[b].n;
   t = r / a.G;
@@ -234,15 +233,6 @@ __device__ __forceinline__ void tmem_tie32(float* f) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -466,7 +456,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         begun = true;
       }
-      const int two = it.two, own = it.own, stride = it.stride, tiles = it.t1 - it.t0;
+      const int two = it.two, tiles = it.t1 - it.t0;
       const bool begins = it.t0 == 0;
       const int turns = two ? tiles : (tiles + 1 - g) / 2;
       const int x0 = (two ? g * kPfTile : 0) + row;
@@ -476,12 +466,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int seq0 = seq;
       seq += tiles;
       count += 1 + two;
-      // the new tokens that the query sees, as bits
-      uint32_t bits = 0;
-      if (own && query >= 0) {
-        bits = a.tree ? a.tree[int64_t(b) * a.T + t] : (2u << t) - 1u;
-        if (n < 32) bits &= (1u << n) - 1u;
-      }
       const bool any = __any_sync(0xffffffffu, query >= 0);
       float c = 0.0f;
       float ref = -INFINITY, l = 0.0f;  // ref: a whole number, in log2 units
@@ -495,8 +479,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tc_fence_after();
         if (i == 0) c = factor[row];  // (the products waited for the queries)
         const PfTile& tile = sh.tile[(seq0 + (two ? i : 2 * i + g)) % NT];
-        // (a warp's queries are all of one row)
-        if (any && (!own || stride == 0 || row / stride == tile.slot)) {
+        if (any) {
           // All of a query's scores at once: a load takes 500 to 800 cycles while products run.
           // (32 at a time, in a loop of a fifth of the code, the softmax took 3400 instead of
           // 1900 cycles.)
@@ -510,15 +493,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
             for (int x = 0; x < 128; ++x) z[x] *= tile.raw_ks[x / kPfPart];
           }
-          if (tile.last) {
-            // New tokens, seen by some queries only, and what lies past them: in the last 48 keys
-            // of a row's last tile, whose end is that of the part with the last token.
-            const int before = tile.L - tile.pos - 80;  // at least 1: there are at most 32 of them
-            const uint64_t seen = uint64_t(bits) << before | ((uint64_t(1) << before) - 1);
-#pragma unroll
-            for (int x = 0; x < 48; ++x)
-              if (!(seen >> x & 1)) z[80 + x] = -INFINITY;
-          }
           float top = -INFINITY;
 #pragma unroll
           for (int y = 0; y < kPfParts; ++y) {
@@ -528,8 +502,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             m1 = max3(m1, v[8], v[9]);
             m0 = max3(m0, v[10], v[11]);
             m1 = max3(m1, v[12], v[13]);
-            const float2 k = tile.ks[y];
-            top = fmaxf(top, fmaf(max3(m0, m1, fmaxf(v[14], v[15])), k.x, k.y));
+            top = fmaxf(top, max3(m0, m1, fmaxf(v[14], v[15])) * tile.ks[y]);
           }
           top *= c;
           const bool moves = __any_sync(0xffffffffu, top > ref);
@@ -546,9 +519,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
           for (int y = 0; y < kPfParts; ++y) {
-            const float2 k = tile.ks[y];
-            const float by = k.x * c, less = minus + k.y;
-            const float2 by2 = make_float2(by, by), less2 = make_float2(less, less);
+            const float by = tile.ks[y] * c;
+            const float2 by2 = make_float2(by, by), less2 = make_float2(minus, minus);
             uint32_t w[8];
 #pragma unroll
             for (int x = 0; x < kPfPart; x += 2) {
@@ -563,15 +535,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tmem_st8(s_addr + 8 * y, reinterpret_cast<const float*>(w));
           }
           l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-          // The output before this tile is done: its products were issued before the scores. (O
-          // of a row that had no tile yet is zero.)
+          // The output before this tile is done: its products were issued before the scores.
           if (moves && i > 0) pf_rescale<D>(o_addr, down);
-          tmem_wait_st();
-        } else if (any) {
-          // another row's tile
-          const uint32_t none[16] = {};
-#pragma unroll 1
-          for (int y = 0; y < 64; y += 16) tmem_st16(s_addr + y, none);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -605,9 +570,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc_fence_after();
       if (any) {
         const int64_t at = begins ? query : int64_t(blockIdx.x) * 256 + x0;
-        float* to = (begins ? a.parts[own] : a.mid) + (query < 0 ? 0 : at) * D;
+        float* to = (begins ? a.parts[0] : a.mid) + (query < 0 ? 0 : at) * D;
         if (query >= 0 && (!both || g == 0))
-          (begins ? a.stats[own] : a.mid_stats)[at] = make_float2(m, l);
+          (begins ? a.stats[0] : a.mid_stats)[at] = make_float2(m, l);
         // with both groups' parts each takes half of the numbers
         const int y0 = both ? g * (D / 2) : 0, y1 = both ? y0 + D / 2 : D;
 #pragma unroll 1
@@ -664,13 +629,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint8_t* raw = raw_s + rr.at * kCode + from;
       uint8_t* to = sm + vr.at * kWide;
       const bool plain = t.plain_v;
-      const int keys = t.keys, valid = t.valid;
+      const int valid = t.valid;
 #pragma unroll 2
       for (int i = 0; i < kSteps; ++i) {
         const int key = key0 + i * kKeyStep, part = key / kPfPart;
         uint4 v = *reinterpret_cast<const uint4*>(raw + i * kKeyStep * D);
-        // what was not copied, or lies past the end
-        if (key >= keys || !(valid >> part & 1)) v = make_uint4(0u, 0u, 0u, 0u);
+        if (!(valid >> part & 1)) v = make_uint4(0u, 0u, 0u, 0u);  // not copied
         const float scale = t.vs[part];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t r[8];
@@ -716,9 +680,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // ---------------------------------------------------------------- work list, queries
     const int64_t u_end = pf_share(plan, blockIdx.x + 1);
     int64_t u = pf_share(plan, blockIdx.x);
-    const int pack = pf_pack(a.T * a.G);
-    const int entries = plan.NG + (a.B + pack - 1) / pack;
-    int lo = 0, hi = entries - 1;  // the last entry that begins at or before u
+    int lo = 0, hi = plan.NG - 1;  // the last group that begins at or before u
     while (lo < hi) {
       const int m = (lo + hi + 1) >> 1;
       if (plan.prefix[m] <= u) lo = m;
@@ -729,36 +691,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     auto describe = [&]() {
       PfItem it = {};
       it.stop = 1;
-      while (u < u_end && e < entries) {
+      while (u < u_end && e < plan.NG) {
         const int64_t base = plan.prefix[e], len = plan.prefix[e + 1] - base;
         if (u >= base + len) {
           ++e;
           continue;
         }
         const int64_t per_h = len / a.H;
-        int64_t nq, tiles;
-        if (e < plan.NG) {
-          const PfGroup g = plan.groups[e];
-          it.own = 0;
-          it.row = g.row;
-          it.rows = 1;
-          it.entry = g.entry;
-          nq = int64_t(g.count) * a.T * a.G;
-          tiles = g.tiles;
-        } else {
-          it.own = 1;
-          it.row = (e - plan.NG) * pack;
-          it.rows = min(pack, a.B - it.row);
-          if (pack > 1) {
-            it.stride = kPfTile / pack;
-            nq = it.rows * it.stride;
-            tiles = (per_h - kPfItemUnits) / kPfOneUnits;
-          } else {
-            const PfRow r = plan.rows[it.row];
-            nq = int64_t(r.n) * a.G;
-            tiles = r.tiles;
-          }
-        }
+        const PrefixGroup g = plan.groups[e];
+        it.row = g.row;
+        it.entry = g.entry;
+        const int64_t nq = int64_t(g.count) * a.T * a.G, tiles = g.tiles;
         const int64_t in = u - base, h = per_h > 0 ? in / per_h : a.H, in_h = in - h * per_h;
         if (tiles <= 0 || nq <= 0 || h >= a.H || it.row < 0 || it.row >= a.B)
           break;  // not a plan that was made here
@@ -887,73 +830,44 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       pend1 = -1;
       half = false;
     };
-    auto row_of = [&](int b) {  // L, n, first tile, tiles
-      return b < a.B ? *reinterpret_cast<const int4*>(plan.rows + b) : make_int4(0, 0, 0, 0);
-    };
     while (ok && next_item(ring)) {
       const PfItem it = sh.item[ring.at];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[ring.at]);
       ring.next();
-      int row = it.row, in_row = it.t0;  // the tile's row, and its place among the row's own
-      int4 now = make_int4(INT32_MAX, 0, 0, INT32_MAX), then = now;
-      if (it.own) {
-        now = row_of(row);
-        while (in_row >= now.w && row + 1 < it.row + it.rows) {
-          in_row -= max(now.w, 0);
-          now = row_of(++row);
-        }
-        then = row_of(row + 1);
-      }
+      const int row = it.row;
       for (int t = it.t0; t < it.t1 && ok;) {
-        if (in_row >= now.w) {
-          in_row = 0;
-          do {
-            now = then;
-            then = row_of(++row + 1);
-          } while (now.w <= 0 && row + 1 < it.row + it.rows);
-        }
-        const int many = min(min(4, it.t1 - t), now.w - in_row);
-        if (many <= 0 || row >= a.B) {
-          ok = false;  // not a plan that was made here: the watch ends it
-          break;
-        }
-        // A row's own tiles end with the part of its last token; the first may begin before them.
-        const int end = it.own ? now.x + now.y : INT32_MAX, begin = now.z * kPfTile;
-        const int tile0 = it.own ? (end + kPfPart - 1) / kPfPart * kPfPart - (now.w - in_row) * kPfTile
-                                 : in_row * kPfTile;
-        const int pos = tile0 + (lane >> 3) * kPfTile + (lane & 7) * kPfPart;
-        const bool on = lane >> 3 < many && pos >= begin && pos < end;
+        const int many = min(4, it.t1 - t);
+        const int pos = t * kPfTile + (lane >> 3) * kPfTile + (lane & 7) * kPfPart;
+        const bool on = lane >> 3 < many;
         const int j = pos / a.bs, in_block = pos - j * a.bs;
         int id = -1;
         if (on && j < a.MB) id = a.bt[int64_t(row) * a.MB + j];
         int plane = -1;
-        float2 ks = make_float2(1.0f, on ? 0.0f : -INFINITY);  // scale; -inf: hidden
-        float vs = 1.0f;
+        float ks = 1.0f, vs = 1.0f;
         if (on) {
           if (id >= 0 && id < a.NB) {
             const float* at = a.scales + id * a.block_scales + it.h;
-            ks.x = at[0];
+            ks = at[0];
             vs = at[a.H];
             plane = id * a.planes_per_block + a.plane0 + it.h;
-            // values that are no numbers would reach the pack's other rows (0 * NaN): they are
-            // zero here, and their keys NaN
+            // values that are no numbers: zeros, and their keys are NaN
             if (!(fabsf(vs) <= FLT_MAX)) {
               vs = 0.0f;
-              ks.x = __uint_as_float(0x7fc00000u);
+              ks = __uint_as_float(0x7fc00000u);
             }
           } else {
             // keys that cannot be read: their queries' outputs become NaN
-            ks.x = __uint_as_float(0x7fc00000u);
+            ks = __uint_as_float(0x7fc00000u);
             if (a.err) atomicOr(a.err, SPEC_DERR_BAD_BLOCK);
           }
         }
         const uint32_t vu = __float_as_uint(vs);
-        const uint32_t k_below = __ballot_sync(0xffffffffu, ks.x < 0.0f),
+        const uint32_t k_below = __ballot_sync(0xffffffffu, ks < 0.0f),
                        v_plain = __ballot_sync(0xffffffffu, (vu & 0x807fffffu) == 0 &&
                                                                 vu >> 23 >= 27 && vu >> 23 <= 134);
 #pragma unroll 1
-        for (int x = 0; x < many && ok; ++x, ++t, ++in_row, ++seq) {
+        for (int x = 0; x < many && ok; ++x, ++t, ++seq) {
           const int g = it.two ? 0 : (t - it.t0) & 1, at = seq % NT;
           if (g == 0) {
             if (half) values1();
@@ -961,8 +875,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           } else {
             values1();
           }
-          // the test of a wait that runs out: this row's keys never come
-          if (it.own && row == a.stall_row) ok = false;
+          // the test of a wait that runs out: these keys never come
+          if (row == a.stall_row) ok = false;
           const bool came = ok && pf_wait(&sh.k_empty[kr.at], kr.phase ^ 1, guard);
           ok = __all_sync(0xffffffffu, came);
           if (!ok) break;
@@ -973,15 +887,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tile.plane[lane & 7] = plane < 0 ? -1 : plane + a.H;
             tile.in_block[lane & 7] = in_block;
             const bool below = k_below >> 8 * x & 255u;
-            tile.ks[lane & 7] = below ? make_float2(1.0f, ks.y) : ks;
-            tile.raw_ks[lane & 7] = ks.x;
+            tile.ks[lane & 7] = below ? 1.0f : ks;
+            tile.raw_ks[lane & 7] = ks;
             tile.vs[lane & 7] = vs;
             if ((lane & 7) == 0) {
-              tile.pos = pos;
-              tile.L = now.x;
-              tile.slot = row - it.row;
-              tile.last = it.own && in_row + 1 == now.w;
-              tile.keys = min(kPfTile, end - pos);
               tile.valid = valid >> 8 * x & 255u;
               tile.below = below;
               tile.plain_v = (v_plain >> 8 * x & 255u) == 255u;

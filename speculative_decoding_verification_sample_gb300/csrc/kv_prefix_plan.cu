@@ -4,7 +4,8 @@
 // the list of members (the first, if one is listed twice), the groups' first rows and
 // shortest lengths, and compares its share of the tables with those of the first rows;
 // the first CTA takes the first differences from all and sums up the units. Bound by
-// latency, and for many long tables by reading them (B x max_blocks entries once).
+// latency, and for many long tables by reading them (B x max_blocks entries once): 9 us for 4
+// rows, 18 us for 256 rows that share 1000 blocks.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -26,10 +27,23 @@ constexpr int kPlanChunk = 256;  // table entries that a warp compares at a time
 
 struct PlanArgs {
   const int32_t *bt, *sl, *nn, *starts, *members;
-  int NG, NE, T, G, H, NB, bs, B, MB;
+  int NG, NE, T, G, H, NB, bs, B, MB, always;
   uint8_t* plan;
   int32_t* err;
 };
+
+// What sharing `tiles` tiles of a group saves, in 10 ns of an SM for each kv head; `rows` of
+// its `many` members have R queries each. Row by row a tile takes 0.6 us with up to 24 queries
+// and 17 ns more for each further one, in blocks of up to 64 (measured: 264 thousand tiles with
+// 20 queries 1035 us on 152 SMs, 48 thousand with 64 queries 404 us). Shared, a unit takes 0.5
+// us, and the join of a query 90 ns.
+__device__ __forceinline__ int64_t pf_gain(int rows, int many, int R, int tiles) {
+  const int blocks = (R + 63) / 64, each = (R + blocks - 1) / blocks;
+  const int64_t alone = int64_t(rows) * tiles * blocks * (60 + 17 * max(0, each - 24) / 10);
+  return alone - 50 * pf_units(int64_t(many) * R, tiles) - int64_t(rows) * R * 9;
+}
+// Two more kernels that find work: about 8 us of all SMs.
+constexpr int64_t kPfLeast = 120000;
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     kv_prefix_plan_kernel(const PlanArgs a) {
@@ -39,10 +53,10 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
           *starts = live + a.NG, *row_entry = starts + a.NG + 1;
   const cg::cluster_group cluster = cg::this_cluster();
   const bool lead = cluster.block_rank() == 0;
-  const PfLayout lay = pf_layout(a.B, a.NG, a.NE);
-  PfHeader* head = reinterpret_cast<PfHeader*>(a.plan);
-  PfGroup* groups = reinterpret_cast<PfGroup*>(a.plan + lay.groups);
-  PfRow* rows = reinterpret_cast<PfRow*>(a.plan + lay.rows);
+  const PrefixLayout lay = prefix_layout(a.B, a.NG, a.NE);
+  PrefixHeader* head = reinterpret_cast<PrefixHeader*>(a.plan);
+  PrefixGroup* groups = reinterpret_cast<PrefixGroup*>(a.plan + lay.groups);
+  PrefixRow* rows = reinterpret_cast<PrefixRow*>(a.plan + sizeof(PrefixHeader));
   int64_t* prefix = reinterpret_cast<int64_t*>(a.plan + lay.prefix);
   int32_t* members = reinterpret_cast<int32_t*>(a.plan + lay.members);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -72,6 +86,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     else if (lead && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
   }
   __syncthreads();
+  auto total = [&](int64_t x) {  // of all threads
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) sums[tid >> 5] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) x += sums[w];
+    return x;
+  };
   auto group_of = [&](int i) {  // the last group that starts at or before entry i
     int lo = 0, hi = a.NG - 1;
     while (lo < hi) {
@@ -145,50 +168,49 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   cluster.sync();
   if (!lead) return;
 
-  // units, and their sums from entry to entry: each thread some consecutive entries
-  auto shared_tiles = [&](int g) {
-    return bad || live[g] < 2 ? 0
-                              : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs / kPfTile);
-  };
-  const int pack = pf_pack(a.T * a.G);
-  const int entries = a.NG + (a.B + pack - 1) / pack,
-            per = (entries + kPlanThreads - 1) / kPlanThreads;
-  auto entry = [&](int e) -> int64_t {
-    if (e < a.NG) {
-      const int tiles = shared_tiles(e);
-      const int s0 = bad ? 0 : starts[e], many = bad ? 0 : starts[e + 1] - s0;
-      groups[e] = PfGroup{tiles, tiles > 0 ? a.members[first[e]] : 0, s0, many};
-      return a.H * pf_units(int64_t(many) * a.T * a.G, tiles);
-    }
-    int64_t units = 0;
-    const int b0 = (e - a.NG) * pack, b1 = min(a.B, b0 + pack);
-    for (int b = b0; b < b1; ++b) {
-      PfRow r = {};
-      const bool ok = lengths(b, r.L, r.n);
-      r.group = r.at = -1;
-      const int i = row_entry[b];
-      if (ok && r.n > 0 && i != INT32_MAX) {
-        const int g = group_of(i);
-        r.skip = shared_tiles(g);
-        if (r.skip > 0) {
-          r.group = g;
-          r.at = i - starts[g];
-        }
+  // What the groups share, in tiles, and what that saves. common[] holds it from here on.
+  const int R = a.T * a.G;
+  int64_t saved = 0;
+  for (int g = tid; g < a.NG; g += kPlanThreads) {
+    const int tiles = bad || live[g] < 2 ? 0
+                                         : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs /
+                                               kPfTile);
+    const int64_t gain = pf_gain(live[g], starts[g + 1] - starts[g], R, tiles);
+    common[g] = a.always || gain > 0 ? tiles : 0;
+    if (gain > 0) saved += gain;
+  }
+  saved = total(saved);
+  const bool share = a.always || saved * a.H > kPfLeast;
+  auto shared_tiles = [&](int g) { return share ? common[g] : 0; };
+
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    PrefixRow r = {};
+    const bool ok = lengths(b, r.L, r.n);
+    r.group = r.at = -1;
+    const int i = row_entry[b];
+    if (ok && r.n > 0 && i != INT32_MAX) {
+      const int g = group_of(i);
+      r.skip = shared_tiles(g);
+      if (r.skip > 0) {
+        r.group = g;
+        r.at = i - starts[g];
       }
-      // they end with the 16 keys of the last token (the first tile may begin in the prefix)
-      r.tiles = !ok ? -1
-                : r.n == 0 ? 0
-                           : ((r.L + r.n + 15) / 16 * 16 - r.skip * kPfTile + kPfTile - 1) / kPfTile;
-      rows[b] = r;
-      if (r.tiles > 0) units += pack > 1 ? r.tiles : pf_units(int64_t(r.n) * a.G, r.tiles);
     }
-    if (pack > 1 && units > 0) units = pf_item_units(kPfOneUnits, units);
-    return a.H * units;
+    rows[b] = r;
+  }
+
+  // units, and their sums from group to group: each thread some consecutive ones
+  const int per = (a.NG + kPlanThreads - 1) / kPlanThreads;
+  auto entry = [&](int e) -> int64_t {
+    const int tiles = shared_tiles(e);
+    const int s0 = bad ? 0 : starts[e], many = bad ? 0 : starts[e + 1] - s0;
+    groups[e] = PrefixGroup{tiles, tiles > 0 ? a.members[first[e]] : 0, s0, many};
+    return a.H * pf_units(int64_t(many) * R, tiles);
   };
   int64_t sum = 0;
   for (int x = 0; x < per; ++x) {
     const int e = tid * per + x;
-    if (e >= entries) break;
+    if (e >= a.NG) break;
     prefix[e] = sum;  // of this thread's so far
     sum += entry(e);
   }
@@ -198,26 +220,27 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
+  __syncthreads();  // (total's readers of sums)
   if (lane == 31) sums[tid >> 5] = inc;
   __syncthreads();
   for (int w = 0; w < (tid >> 5); ++w) inc += sums[w];
   for (int x = 0; x < per; ++x) {
     const int e = tid * per + x;
-    if (e >= entries) break;
+    if (e >= a.NG) break;
     prefix[e] += inc - sum;
-    if (e == entries - 1) {
-      prefix[entries] = inc;
-      head->units = inc;
-      head->B = a.B;
-      head->T = a.T;
-      head->G = a.G;
-      head->H = a.H;
-      head->bs = a.bs;
-      head->MB = a.MB;
-      head->NG = a.NG;
-      head->NE = a.NE;
-      head->magic = kPfMagic;
-    }
+  }
+  if (tid == kPlanThreads - 1) {
+    prefix[a.NG] = inc;
+    head->units = inc;
+    head->B = a.B;
+    head->T = a.T;
+    head->G = a.G;
+    head->H = a.H;
+    head->bs = a.bs;
+    head->MB = a.MB;
+    head->NG = a.NG;
+    head->NE = a.NE;
+    head->magic = kPrefixMagic;
   }
 }
 
@@ -237,6 +260,7 @@ int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
   a.bs = k.block_size;
   a.B = k.B;
   a.MB = k.max_blocks;
+  a.always = k.always;
   a.plan = static_cast<uint8_t*>(k.plan);
   a.err = k.err;
   const size_t smem = (5 * size_t(a.NG) + 1 + a.B) * 4;
@@ -247,15 +271,16 @@ int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
 }
 
 size_t kv_prefix_plan_size(int B, int num_groups, int num_members) {
-  return pf_layout(B, num_groups, num_members).bytes;
+  return prefix_layout(B, num_groups, num_members).bytes;
 }
 
 // ------------------------------------------------------------------ joining
 // A warp takes up to 8 queries of a row and kv head. What their pieces are is found four lanes a
-// query side by side: its items of the prefix and of the row's own keys, and of each the first
-// piece (in the place of the query) and the second (in that of a CTA); further pieces, of items
-// that cross several CTAs, come by two. Then the queries follow one by one, the lanes over the
-// head's numbers. (Found for one query at a time, this was most of 750 instructions a query.)
+// query side by side: the row's own part, the first piece of the prefix (in the place of the
+// query) and the second (in that of a CTA); further pieces, of items that cross several CTAs,
+// come by two. Then the queries follow one by one, the lanes over the head's numbers. (Found for
+// one query at a time, this was most of 750 instructions a query.) Bound by those that are left
+// and by memory: 23 us for 40960 queries of 128 numbers.
 constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32, kPfJoinQueries = 8;
 
 template <int D>
@@ -269,39 +294,28 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
   const int warp = blockIdx.x * kPfJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int bh = warp / chunks, b = bh / a.H, h = bh - b * a.H, r0 = (warp - bh * chunks) * per;
   if (b >= a.B) return;
-  PfRow row = {};
-  row.tiles = -1;
-  if (p.ok) row = p.rows[b];
-  // lengths that changed since the plan was made: the row's keys are not the plan's
-  const bool same = p.ok && row.L == a.sl[b] && row.n == (a.nn ? a.nn[b] : a.T);
-  const bool bad = row.tiles < 0 || !same;
-  if (bad && a.err && h == 0 && r0 == 0 && lane == 0)
-    atomicOr(a.err, p.ok ? SPEC_DERR_BAD_LENGTH : SPEC_DERR_BAD_SLOT);
+  // rows that share nothing, and those whose lengths are not the plan's, are done
+  if (!p.ok) return;
+  const PrefixRow row = p.rows[b];
+  if (row.group < 0 || row.L != a.sl[b] || row.n != (a.nn ? a.nn[b] : a.T)) return;
   auto quotient = [](int64_t n, int d) -> int64_t {
     return n >> 32 == 0 ? int64_t(uint32_t(n) / uint32_t(d)) : n / d;
   };
   const int r = r0 + (lane >> 2), t = r / a.G;
   const int64_t query = (int64_t(b) * a.T + t) * a.H * a.G + h * a.G + r - t * a.G;
-  // even lanes: the item of the prefix, odd lanes: the one of the row's own keys
-  const int pack = pf_pack(R), pack_at = pack == 4 ? b >> 2 : pack == 2 ? b >> 1 : b;
-  const bool own = lane & 1, has = !bad && (lane >> 2) < per && r < R && t < row.n &&
-                                   (own ? row.tiles > 0 : row.group >= 0);
-  const int x0 = own ? (pack > 1 ? (b & (pack - 1)) * (kPfTile / pack) + r : r) : row.at * R + r;
+  // even lanes: the item of the prefix, odd lanes: the row's own keys, one piece
+  const bool own = lane & 1, has = (lane >> 2) < per && r < R && t < row.n;
+  const int x0 = row.at * R + r;
   int64_t u = 0, end = 0;
   int w = kPfOneUnits, c0 = 0, c1 = 0;
-  if (has) {
-    const int e = own ? p.NG + pack_at : row.group, qb = x0 / 256;
-    int64_t nq = int64_t(row.n) * a.G, tiles = row.tiles;
-    if (!own) {
-      const PfGroup g = p.groups[e];
-      nq = int64_t(g.count) * R;
-      tiles = g.tiles;
-    }
-    const int64_t base = p.prefix[e], per_h = quotient(p.prefix[e + 1] - base, a.H);
-    if (own && pack > 1) tiles = uint64_t(per_h - kPfItemUnits) / kPfOneUnits;  // all its rows'
-    else if (nq - qb * 256 > 128) w = kPfTwoUnits;
-    u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, tiles);
-    end = u + pf_item_units(w, tiles);
+  if (has && !own) {
+    const PrefixGroup g = p.groups[row.group];
+    const int qb = x0 / 256;
+    const int64_t base = p.prefix[row.group],
+                  per_h = quotient(p.prefix[row.group + 1] - base, a.H);
+    if (int64_t(g.count) * R - qb * 256 > 128) w = kPfTwoUnits;
+    u = base + h * per_h + qb * pf_item_units(kPfTwoUnits, g.tiles);
+    end = u + pf_item_units(w, g.tiles);
     c0 = pf_owner(p, u + kPfItemUnits);
     c1 = pf_owner(p, end - 1);
   }
@@ -385,7 +399,7 @@ __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const Pf
       mk = mn;
       add(part2, weight2);
     }
-    const float inv = bad ? __uint_as_float(0x7fc00000u) : lk == 0.0f ? 0.0f : 1.0f / lk;
+    const float inv = lk == 0.0f ? 0.0f : 1.0f / lk;
     uint32_t x[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
@@ -405,9 +419,10 @@ namespace {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Places {  // byte offsets in the workspace
-  size_t parts[2], stats[2], mid, mid_stats, bytes;
+  size_t parts[2], stats[2], mid, mid_stats, each, bytes;
 };
-Places places(int64_t queries, int D) {
+Places places(int B, int T, int H, int G, int D) {
+  const int64_t queries = int64_t(B) * T * H * G;
   Places p;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -421,6 +436,7 @@ Places places(int64_t queries, int D) {
   }
   p.mid = take(size_t(kPfMaxCtas) * 256 * D * sizeof(float));
   p.mid_stats = take(size_t(kPfMaxCtas) * 256 * sizeof(float2));
+  p.each = take(kv_q8_attention_workspace(T, G, D));
   p.bytes = at;
   return p;
 }
@@ -428,11 +444,11 @@ Places places(int64_t queries, int D) {
 }  // namespace
 
 bool kv_prefix_takes(int dtype, int D, int bs, int64_t planes) {
-  return dtype == SPEC_BF16 && (D == 64 || D == 128) && bs % 16 == 0 && planes <= INT32_MAX;
+  return kv_q8_attention_on_tc(dtype, D, bs, planes) && bs % 16 == 0;
 }
 
-size_t kv_prefix_workspace(int B, int T, int Hq, int D) {
-  return places(int64_t(B) * T * Hq, D).bytes;
+size_t kv_prefix_workspace(int B, int T, int H, int G, int D) {
+  return places(B, T, H, G, D).bytes;
 }
 
 int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t plan_bytes) {
@@ -444,7 +460,6 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
   a.bt = k.block_table;
   a.sl = k.seq_lens;
   a.nn = k.num_new;
-  a.tree = k.tree_mask;
   a.out = k.out;
   a.plan = static_cast<const uint8_t*>(plan);
   a.plan_bytes = plan_bytes;
@@ -459,7 +474,7 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
   a.MB = k.max_blocks;
   a.block_bytes = k.num_layers * layer_bytes;
   a.block_scales = int64_t(k.num_layers) * 2 * k.H;
-  const Places p = places(int64_t(k.B) * k.T * k.H * k.G, k.D);
+  const Places p = places(k.B, k.T, k.H, k.G, k.D);
   uint8_t* ws = static_cast<uint8_t*>(k.workspace);
   for (int i = 0; i < 2; ++i) {
     a.parts[i] = reinterpret_cast<float*>(ws + p.parts[i]);
@@ -494,6 +509,14 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
   const int st = launch_pf_attention(a, k.pool, int64_t(k.num_blocks) * a.planes_per_block, ctas,
                                      k.stream);
   if (st != SPEC_OK) return st;
+  Q8AttnLaunch rows = k;
+  rows.workspace = ws + p.each;
+  rows.plan = plan;
+  rows.plan_bytes = plan_bytes;
+  rows.own = a.parts[1];
+  rows.own_stats = a.stats[1];
+  const int sr = launch_kv_q8_attention(rows);
+  if (sr != SPEC_OK) return sr;
   cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
   // as many queries a warp as leave 32 warps for each SM, in equal chunks
   const int R = a.T * a.G;

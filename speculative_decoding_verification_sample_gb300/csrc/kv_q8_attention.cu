@@ -240,9 +240,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   __syncthreads();
   if (!live || half == 1) return;
   add(st_s[rr].x, st_s[rr].y, &acc_s[rr][lane]);
+  const int64_t query = (int64_t(j.x) * a.T + row / a.G) * a.H * a.G + j.y * a.G + row % a.G;
+  if (a.plan && leaves_part(a, row_span(a, j.x))) {
+    float4* o = reinterpret_cast<float4*>(a.own + query * a.D) + lane;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i < quads) o[32 * i] = acc[i];
+    if (lane == 0) a.own_stats[query] = make_float2(m, l);
+    return;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  T* o = static_cast<T*>(a.out) +
-         ((int64_t(j.x) * a.T + row / a.G) * a.H * a.G + j.y * a.G + row % a.G) * a.D + 4 * lane;
+  T* o = static_cast<T*>(a.out) + query * a.D + 4 * lane;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     if (lane + 32 * i < quads)
@@ -314,6 +322,10 @@ size_t kv_q8_attention_workspace(int T, int G, int D) {
          up256(2 * kAttnMaxCtas * pad * sizeof(float2)) + up256(kAttnMaxCtas * sizeof(int4));
 }
 
+bool kv_q8_attention_on_tc(int dtype, int D, int bs, int64_t planes) {
+  return attn_tc_takes(dtype, D, bs, planes);
+}
+
 int launch_kv_q8_attention(const Q8AttnLaunch& k) {
   AttnArgs a;
   const int64_t layer_bytes = int64_t(2) * k.H * k.bs * k.D;
@@ -343,6 +355,10 @@ int launch_kv_q8_attention(const Q8AttnLaunch& k) {
   set_test_knobs(a);
   a.plane0 = k.layer * 2 * k.H;
   a.planes_per_block = k.num_layers * 2 * k.H;
+  a.plan = static_cast<const uint8_t*>(k.plan);
+  a.plan_bytes = k.plan_bytes;
+  a.own = k.own;
+  a.own_stats = k.own_stats;
   const int sms = sm_count();
   if (sms == 0) return SPEC_ECUDA;
   const int64_t planes = int64_t(k.num_blocks) * a.planes_per_block;

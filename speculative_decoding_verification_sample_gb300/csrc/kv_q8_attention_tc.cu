@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           for (int x = 0; x < chunks; ++x) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = v[x][0];
       }
       bar_group(group);
-      const bool whole = g.t0 == 0 && g.t1 == g.s.tiles;
+      const bool whole = g.t0 == 0 && g.t1 == g.s.tiles, done = whole && !leaves_part(a, g.s);
       const int64_t slot = 2 * c + (g.u == plan.u0 ? 0 : 1);
       if (key < W) {
         const float* mp = sh.part[0] + col0 + key;
@@ -849,15 +849,16 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         const int e = sum > 0.0f ? int(__float_as_uint(sum) >> 23) - 127 : 0;
         constexpr float unlift = 1.0f / (kTcLift * kTcVDown);
         const float down = q8_pow2(-e);
-        ra[key] = (!whole ? down : sum == 0.0f ? 0.0f : __fdividef(down, sum * down)) * unlift;
+        ra[key] = (!done ? down : sum == 0.0f ? 0.0f : __fdividef(down, sum * down)) * unlift;
         const int off = sh.row_off[qb][col0 + key];
         const int64_t part = slot * a.rows_per_block + col0 + key;
+        const int64_t query = first_row(a, g) + off;
         sh.row_to[col0 + key] =
-            whole ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + (first_row(a, g) + off) * D)
-                  : reinterpret_cast<uint64_t>(a.parts + part * D);
-        if (!whole && off >= 0)
-          a.stats[part] = make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e),
-                                      sum * q8_pow2(-e));
+            done ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + query * D)
+                 : reinterpret_cast<uint64_t>(whole ? a.own + query * D : a.parts + part * D);
+        if (!done && off >= 0)
+          *(whole ? a.own_stats + query : a.stats + part) =
+              make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e), sum * q8_pow2(-e));
       }
       bar_group(group);
       wait_outputs();
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (8 * x + q < live) {
-            if (whole) reinterpret_cast<__nv_bfloat16*>(to[q])[key] = __float2bfloat16(o[0][q]);
+            if (done) reinterpret_cast<__nv_bfloat16*>(to[q])[key] = __float2bfloat16(o[0][q]);
             else reinterpret_cast<float*>(to[q])[key] = o[0][q];
           }
       }

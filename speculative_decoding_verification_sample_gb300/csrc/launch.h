@@ -151,6 +151,12 @@ struct Q8AttnLaunch {
   void* workspace;
   void* stream;
   int32_t* err;
+  // on the tensor cores only: a plan of kv_prefix_plan and where rows with shared tiles leave
+  // their parts
+  const void* plan = nullptr;
+  size_t plan_bytes = 0;
+  float* own = nullptr;
+  float2* own_stats = nullptr;
 };
 
 struct NormRopeLaunch {
@@ -181,6 +187,7 @@ struct KvPrefixPlanLaunch {
   const int32_t* group_starts;
   const int32_t* group_rows;
   int num_groups, num_members, T, G, H, num_blocks, block_size, B, max_blocks;
+  int always;  // share whatever is common, not only where it saves time
   void* plan;
   void* stream;
   int32_t* err;
@@ -189,7 +196,7 @@ struct KvPrefixPlanLaunch {
 int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k);
 size_t kv_prefix_plan_size(int B, int num_groups, int num_members);
 bool kv_prefix_takes(int dtype, int D, int bs, int64_t planes);
-size_t kv_prefix_workspace(int B, int T, int Hq, int D);
+size_t kv_prefix_workspace(int B, int T, int H, int G, int D);
 int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t plan_bytes);
 int launch_kv_reserve(const KvReserveLaunch& k);
 int launch_kv_fork(const KvForkLaunch& k);
@@ -197,6 +204,7 @@ int launch_kv_free(const KvFreeLaunch& k);
 int launch_kv_q8_append(const Q8AppendLaunch& k);
 int launch_kv_q8_attention(const Q8AttnLaunch& k);
 size_t kv_q8_attention_workspace(int T, int G, int D);
+bool kv_q8_attention_on_tc(int dtype, int D, int bs, int64_t planes);
 
 int launch_verify_sample(const SampleLaunch& s);
 int launch_filter(const FilterLaunch& f);

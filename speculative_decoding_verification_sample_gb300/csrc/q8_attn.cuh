@@ -17,6 +17,10 @@
 // once; one that crosses CTAs leaves in each a part (maximum, sum, unnormalised
 // output), joined by a second kernel in CTA order, so the result does not
 // depend on timing.
+//
+// With a plan (kv_prefix.cuh) rows may leave their first tiles, which they share
+// with others, to another kernel: such a row begins at its tile `skip`, and what
+// would be its output is left as a part.
 #pragma once
 #include <cstdint>
 
@@ -27,6 +31,47 @@
 namespace sv {
 
 constexpr int kAttnTile = 128;
+
+// A plan of shared prefixes (kv_prefix.cuh): what it was made for, from byte 256 its rows, then
+// the groups, their units from group to group, and the list of members.
+struct PrefixHeader {
+  int32_t magic, B, T, G, H, bs, MB, NG, NE;
+  int64_t units;
+  int32_t pad[52];
+};
+static_assert(sizeof(PrefixHeader) == 256, "the rows follow it");
+constexpr int32_t kPrefixMagic = 0x70667832;
+struct PrefixRow {
+  int32_t L, n;       // as the plan found them
+  int32_t skip;       // tiles that the row shares: those of its group, else 0
+  int32_t group, at;  // group (skip 0: -1) and the row's place among its members
+  int32_t pad[3];
+};
+struct PrefixGroup {  // tiles 0: nothing is shared
+  int32_t tiles, row, entry, count;  // shared tiles, a row of the group, its members
+};
+struct PrefixLayout {  // byte offsets
+  size_t groups, prefix, members, bytes;
+};
+__host__ __device__ inline PrefixLayout prefix_layout(int B, int NG, int NE) {
+  PrefixLayout l;
+  l.groups = sizeof(PrefixHeader) + size_t(B) * sizeof(PrefixRow);
+  l.prefix = l.groups + size_t(NG) * sizeof(PrefixGroup);
+  l.members = l.prefix + (size_t(NG) + 1) * 8;
+  l.bytes = (l.members + size_t(NE) * 4 + 255) / 256 * 256;
+  return l;
+}
+// Whether a plan of `bytes` was made for such calls (at least a header).
+__device__ __forceinline__ bool prefix_fits(const uint8_t* plan, size_t bytes, int B, int T, int G,
+                                            int H, int bs, int MB) {
+  const PrefixHeader* h = reinterpret_cast<const PrefixHeader*>(plan);
+  return h->magic == kPrefixMagic && h->B == B && h->T == T && h->G == G && h->H == H &&
+         h->bs == bs && h->MB == MB && h->NG >= 0 && h->NE >= 0 && h->NG <= (1 << 20) &&
+         h->NE <= (1 << 20) && prefix_layout(B, h->NG, h->NE).bytes <= bytes;
+}
+__device__ __forceinline__ const PrefixRow* prefix_row(const uint8_t* plan, int b) {
+  return reinterpret_cast<const PrefixRow*>(plan + sizeof(PrefixHeader)) + b;
+}
 
 struct AttnArgs {
   const void* q;         // [B, T, H * G, D]
@@ -50,6 +95,10 @@ struct AttnArgs {
   int stall_row;              // -1, or the row whose V tiles are withheld (a test)
   int plane0;                 // tensor-map plane index of (block 0, this layer, keys, head 0)
   int planes_per_block;       // planes from block to block
+  const uint8_t* plan;        // null: none; at least a header and B rows
+  size_t plan_bytes;
+  float* own;                 // [B T H G][D], with a plan: of rows with shared tiles
+  float2* own_stats;          // [B T H G]
 };
 
 struct RowSpan {
@@ -60,12 +109,23 @@ struct RowSpan {
   bool bad;
 };
 
+__device__ __forceinline__ bool plan_fits(const AttnArgs& a) {
+  return prefix_fits(a.plan, a.plan_bytes, a.B, a.T, a.G, a.H, a.bs, a.MB);
+}
+
 __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
   RowSpan s;
   s.L = a.sl[b];
   s.n = a.nn ? a.nn[b] : a.T;
   s.bad = s.L < 0 || s.n < 0 || s.n > a.T || int64_t(s.L) + s.n > int64_t(a.MB) * a.bs;
   s.lo = s.sink_end = 0;
+  int skip = 0;
+  if (a.plan) {
+    // lengths that changed since the plan was made: the row's keys are not the plan's
+    const PrefixRow* r = prefix_row(a.plan, b);
+    s.bad = s.bad || r->L != s.L || r->n != s.n || !plan_fits(a);
+    skip = r->skip;
+  }
   if (s.bad || s.n == 0) {
     s.end = s.tiles = s.sink_tiles = s.win_tile = 0;
     return s;
@@ -73,7 +133,7 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
   s.end = s.L + s.n;
   const int all = (s.end + kAttnTile - 1) / kAttnTile;
   s.sink_tiles = 0;
-  s.win_tile = 0;
+  s.win_tile = max(0, min(skip, s.L / kAttnTile));
   if (a.window > 0 && s.L >= a.window) {
     s.lo = s.L - a.window + 1;
     s.sink_end = min(a.sinks, s.end);
@@ -87,6 +147,11 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
 
 __device__ __forceinline__ int tile_start(const RowSpan& s, int k) {
   return (k < s.sink_tiles ? k : k - s.sink_tiles + s.win_tile) * kAttnTile;
+}
+
+// Whether a row's outputs are left as parts (calls with a plan have no window).
+__device__ __forceinline__ bool leaves_part(const AttnArgs& a, const RowSpan& s) {
+  return a.plan && s.win_tile > 0;
 }
 
 // May a query of the row see a position of [p, p + n)? Blocks for which this is
@@ -224,7 +289,8 @@ __device__ __forceinline__ void write_empty_rows(const AttnArgs& a, int c, int n
     T* o = static_cast<T*>(a.out) + b * n;
     const T v = T(s.bad ? __uint_as_float(0x7fc00000u) : 0.0f);
     for (int64_t i = me; i < n; i += threads) o[i] = v;
-    if (s.bad && a.err && me == 0) atomicOr(a.err, SPEC_DERR_BAD_LENGTH);
+    if (s.bad && a.err && me == 0)
+      atomicOr(a.err, a.plan && !plan_fits(a) ? SPEC_DERR_BAD_SLOT : SPEC_DERR_BAD_LENGTH);
   }
 }
 

@@ -53,10 +53,11 @@ def grouped(rng, groups, own, alone, bs, T, n=None):
     return L, bt, starts, members, nb
 
 
-def plan_of(bt, L, starts, members, T, Hq, H, bs, nb, n=None, err=None):
+def plan_of(bt, L, starts, members, T, Hq, H, bs, nb, n=None, err=None, always=True):
+    """A plan that shares whatever is common: most of these cases are too small for it to pay."""
     return sv.kv_prefix_plan(h.i32(bt), h.i32(L), h.i32(starts), h.i32(members), tokens=T,
                              q_heads=Hq, kv_heads=H, block_size=bs, num_blocks=nb,
-                             num_new=None if n is None else h.i32(n), err_flag=err)
+                             num_new=None if n is None else h.i32(n), always=always, err_flag=err)
 
 
 def bound(out, spread, reach, D):
@@ -279,7 +280,7 @@ def test_after_fork_and_on_streams_and_captured():
     def step(out, stream=None):
         sv.kv_q8_append(k, k, dp, ds, table, lens, stream=stream, err_flag=err)
         plan = sv.kv_prefix_plan(table, lens, starts, members, tokens=T, q_heads=Hq, kv_heads=H,
-                                 block_size=bs, num_blocks=nb, stream=stream, err_flag=err)
+                                 block_size=bs, num_blocks=nb, always=True, stream=stream, err_flag=err)
         sv.kv_q8_prefix_attention(dq, dp, ds, table, lens, plan, out, stream=stream, err_flag=err)
 
     def expect(out):
@@ -318,6 +319,11 @@ def test_a_wait_runs_out(monkeypatch):
     err = h.i32([0])
     monkeypatch.setenv("SPECVERIFY_STALL_ROW", "3")
     monkeypatch.setenv("SPECVERIFY_IDLE_NS", "5000000")
+    _run(dq, pool, scales, bt, L, plan, err_flag=err)
+    assert int(err) == sv.SPEC_DERR_TIMEOUT
+    # the row with which a group begins: its shared keys as well
+    err = h.i32([0])
+    monkeypatch.setenv("SPECVERIFY_STALL_ROW", str(int(members[0])))
     _run(dq, pool, scales, bt, L, plan, err_flag=err)
     assert int(err) == sv.SPEC_DERR_TIMEOUT
     monkeypatch.delenv("SPECVERIFY_STALL_ROW")
