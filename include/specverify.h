@@ -528,14 +528,13 @@ size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads,
  *                int32, ascending: group g has members group_starts[g] ..
  *                group_starts[g + 1] - 1. Rows may be in no group; no groups, and a null
  *                group_rows with no members, are allowed
- *   always       0: share where it saves time (long prefixes of many rows); else wherever
- *                rows have whole tiles in common
  *   plan         kv_prefix_plan_bytes(B, num_groups, num_members) bytes, 256-byte aligned,
  *                no initialisation
  * A group shares the blocks that the tables of its rows (those with new tokens) have in
  * common from the start, as kv_fork leaves them, as far as all of them have committed tokens
  * there, in whole tiles of 128 positions; a group that has nothing in common shares nothing.
- * So groups may be a guess: they change the time only, never the result.
+ * So groups may be a guess: they change the time only, never the result. And it shares only
+ * where that saves time by an estimate: long prefixes of many rows.
  * Device errors: SPEC_DERR_BAD_SLOT: a row out of range, or listed again (that entry is passed
  * over), or group_starts that are not ascending within [0, num_members] (nothing is shared).
  * B, num_groups, num_members <= 8192, T <= 32 (SPEC_ENOTSUP).
@@ -543,8 +542,8 @@ size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads,
 int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
                    const int32_t* group_starts, const int32_t* group_rows, int num_groups,
                    int num_members, int T, int num_q_heads, int num_kv_heads, int num_blocks,
-                   int block_size, int B, int max_blocks, int always, void* plan,
-                   size_t plan_bytes, void* stream, int32_t* err_flag);
+                   int block_size, int B, int max_blocks, void* plan, size_t plan_bytes,
+                   void* stream, int32_t* err_flag);
 
 /* kv_prefix_plan_bytes - size of a plan; 0 for sizes that kv_prefix_plan rejects. */
 size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
@@ -556,6 +555,7 @@ size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
  *   plan         of kv_prefix_plan with the same tables, lengths, T and heads; plan_bytes its
  *                size. A row whose lengths are not the plan's gets NaN and
  *                SPEC_DERR_BAD_LENGTH; with a plan of other sizes all do, and SPEC_DERR_BAD_SLOT
+ *                (calls whose tables are too short to share anything do not look at it)
  *   workspace    kv_q8_prefix_attention_workspace_bytes bytes, 256-byte aligned, no
  *                initialisation; calls that share one must be ordered on the device
  * Everything else is as in kv_q8_attention, which takes the rows' own keys. Shared keys: queries

@@ -109,7 +109,7 @@ def lib() -> ctypes.CDLL:
         L.kv_q8_norm_rope_append.argtypes = [P, S, P, S, P, S, I, P, S, P, P, F, P, I, I, F, P, P,
                                              P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
         L.kv_q8_norm_rope_append.restype = I
-        L.kv_prefix_plan.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, Z, P, P]
+        L.kv_prefix_plan.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, P, Z, P, P]
         L.kv_prefix_plan.restype = I
         L.kv_prefix_plan_bytes.argtypes = [I, I, I]
         L.kv_prefix_plan_bytes.restype = Z
@@ -716,12 +716,11 @@ def kv_prefix_plan_bytes(B: int, num_groups: int, num_members: int) -> int:
 
 
 def kv_prefix_plan(block_table, seq_lens, group_starts, group_rows, *, tokens: int, q_heads: int,
-                   kv_heads: int, block_size: int, num_blocks: int, num_new=None, always=False,
-                   plan=None, stream=None, err_flag=None):
+                   kv_heads: int, block_size: int, num_blocks: int, num_new=None, plan=None,
+                   stream=None, err_flag=None):
     """The plan of a step's kv_q8_prefix_attention calls (every layer's): which rows share the
     first blocks of their tables. group_rows int32 [members]: rows, group after group;
-    group_starts int32 [groups + 1]. `tokens` is the T of the queries. `always`: share whatever is
-    common, not only where it saves time. Returns `plan`, a uint8
+    group_starts int32 [groups + 1]. `tokens` is the T of the queries. Returns `plan`, a uint8
     tensor of kv_prefix_plan_bytes + 256 (None: a new one)."""
     L = _lib if _int32 is not None else _ready()
     dev = _place(block_table, "block_table")
@@ -742,7 +741,7 @@ def kv_prefix_plan(block_table, seq_lens, group_starts, group_rows, *, tokens: i
     p, n = _aligned(plan, "plan", dev)
     st = L.kv_prefix_plan(
         bt, _vec(seq_lens, "seq_lens", B, dev), _vec(num_new, "num_new", B, dev), starts, rows, NG,
-        NE, tokens, q_heads, kv_heads, num_blocks, block_size, B, MB, int(always), p, n, raw,
+        NE, tokens, q_heads, kv_heads, num_blocks, block_size, B, MB, p, n, raw,
         _word(err_flag, "err_flag", dev))
     if st != SPEC_OK:
         raise SpecError("kv_prefix_plan", st)

@@ -422,8 +422,8 @@ size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members) {
 int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const int32_t* num_new,
                    const int32_t* group_starts, const int32_t* group_rows, int num_groups,
                    int num_members, int T, int num_q_heads, int num_kv_heads, int num_blocks,
-                   int block_size, int B, int max_blocks, int always, void* plan,
-                   size_t plan_bytes, void* stream, int32_t* err_flag) {
+                   int block_size, int B, int max_blocks, void* plan, size_t plan_bytes,
+                   void* stream, int32_t* err_flag) {
   if (!block_table || !seq_lens || !group_starts || (!group_rows && num_members > 0) || !plan)
     return SPEC_EINVAL;
   if (bad_table(num_blocks, block_size, B, max_blocks) || num_groups < 0 || num_members < 0 ||
@@ -436,7 +436,7 @@ int kv_prefix_plan(const int32_t* block_table, const int32_t* seq_lens, const in
   if ((reinterpret_cast<uintptr_t>(plan) & 255u) != 0 || plan_bytes < need) return SPEC_EINVAL;
   sv::KvPrefixPlanLaunch k{block_table, seq_lens, num_new, group_starts, group_rows, num_groups,
                            num_members, T, num_q_heads / num_kv_heads, num_kv_heads, num_blocks,
-                           block_size, B, max_blocks, always, plan, stream, err_flag};
+                           block_size, B, max_blocks, plan, stream, err_flag};
   return sv::launch_kv_prefix_plan(k);
 }
 

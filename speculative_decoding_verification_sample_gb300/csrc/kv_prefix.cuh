@@ -37,9 +37,9 @@ namespace sv {
 constexpr int kPfTile = 128;      // keys of a tile, queries of an M tile
 constexpr int kPfMaxCtas = 256;   // bound of the work split, for the workspace
 
-// What an item costs: its beginning and end (queries, parts), a key tile with two M tiles,
-// one with one. The split only needs their proportions (2.4 us a tile with two: 0.5 us each).
-constexpr int kPfItemUnits = 16, kPfTwoUnits = 5, kPfOneUnits = 4;
+// What an item costs, in units of 0.36 us: its beginning and end (queries, parts), a key tile
+// with two M tiles, one with one (measured: 64 items of 94 tiles more take 86 and 57 us longer).
+constexpr int kPfItemUnits = 24, kPfTwoUnits = 6, kPfOneUnits = 4;
 __host__ __device__ inline int64_t pf_item_units(int w, int64_t tiles) {
   return kPfItemUnits + w * tiles;
 }
@@ -53,6 +53,25 @@ __host__ __device__ inline int64_t pf_units(int64_t nq, int64_t tiles) {
           : rest > 0 ? pf_item_units(kPfOneUnits, tiles)
                      : 0);
 }
+// What `tiles` tiles of `rows` rows of a group with R queries each cost row by row, in 10 ns of
+// an SM for each kv head: a tile 0.53 us with up to 24 queries and 17 ns more for each further
+// one, in blocks of up to 64 (measured: 264 thousand tiles with 20 queries 1035 us on 152 SMs,
+// 48 thousand with 64 queries 404 us, of which the changes between items are a tenth).
+__host__ __device__ inline int64_t pf_alone(int64_t rows, int64_t tiles, int R) {
+  const int blocks = (R + 63) / 64, each = (R + blocks - 1) / blocks;
+  return rows * tiles * blocks * (53 + 17 * (each > 24 ? each - 24 : 0) / 10);
+}
+// The same shared: the units, and the join, 0.12 us a query.
+__host__ __device__ inline int64_t pf_shared(int64_t rows, int64_t many, int64_t tiles, int R) {
+  return 36 * pf_units(many * R, tiles) + rows * R * 12;
+}
+// What two more kernels cost that find work: about 18 us of all SMs.
+constexpr int64_t kPfLeast = 270000;
+// Whether rows of such sizes could share enough of their tables.
+__host__ inline bool pf_could(int B, int MB, int bs, int R, int H) {
+  return pf_alone(B, int64_t(MB) * bs / kPfTile, R) * H > kPfLeast;
+}
+
 // Tiles of an item that begin before its unit x (divided by one of two constants: a division
 // of 64 bits by w is a hundred instructions).
 __host__ __device__ inline int pf_cut(int64_t x, int w) {

@@ -408,10 +408,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     sh.guard.abort = sh.guard.beat[0] = sh.guard.beat[1] = sh.guard.done[0] = sh.guard.done[1] = 0;
     fence_mbar_init();
   }
-  // parts of K that are not copied hold numbers of an earlier tile, or these
-  for (int i = tid; i < KS * kCode / 16; i += kPfThreads)
-    reinterpret_cast<uint4*>(k_s)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_async_smem();
+  pdl_wait();
+  const PfPlan plan = pf_plan(a, gridDim.x);
+  if (int(blockIdx.x) >= plan.nc) return;  // (nothing to share: before the TMEM is taken)
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
@@ -421,9 +420,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  pdl_wait();
-  const PfPlan plan = pf_plan(a, gridDim.x);
-  const bool work = int(blockIdx.x) < plan.nc;
   PfGuard* guard = &sh.guard;
 
   // Whether there is a next item (by a whole warp).
@@ -434,7 +430,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   };
 
   // What the registers are moved for has to stand in a branch of its own.
-  if (work && warp < kPfSoftmax / 32) {
+  if (warp < kPfSoftmax / 32) {
     setmaxnreg_inc<kPfSoftmaxRegs>();
     // ---------------------------------------------------------------- softmax
     const int g = warp >> 2, row = tid & 127;
@@ -601,7 +597,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
     }
     if (row == 0) *reinterpret_cast<volatile int*>(&sh.guard.done[g]) = 1;
-  } else if (work && warp < kMmaWarp) {
+  } else if (warp < kMmaWarp) {
     setmaxnreg_dec<kPfLoadRegs>();
     // ---------------------------------------------------------------- values
     // From the codes in shared memory to bf16. (Read into registers from global memory, the
@@ -674,7 +670,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         mbar_arrive(&sh.v_full[vr.at]);
       }
     }
-  } else if (work) {
+  } else {
     setmaxnreg_dec<kPfOtherRegs>();
     if (warp == kWalkWarp) {
     // ---------------------------------------------------------------- work list, queries

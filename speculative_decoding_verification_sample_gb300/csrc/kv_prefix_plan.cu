@@ -32,18 +32,11 @@ struct PlanArgs {
   int32_t* err;
 };
 
-// What sharing `tiles` tiles of a group saves, in 10 ns of an SM for each kv head; `rows` of
-// its `many` members have R queries each. Row by row a tile takes 0.6 us with up to 24 queries
-// and 17 ns more for each further one, in blocks of up to 64 (measured: 264 thousand tiles with
-// 20 queries 1035 us on 152 SMs, 48 thousand with 64 queries 404 us). Shared, a unit takes 0.5
-// us, and the join of a query 90 ns.
-__device__ __forceinline__ int64_t pf_gain(int rows, int many, int R, int tiles) {
-  const int blocks = (R + 63) / 64, each = (R + blocks - 1) / blocks;
-  const int64_t alone = int64_t(rows) * tiles * blocks * (60 + 17 * max(0, each - 24) / 10);
-  return alone - 50 * pf_units(int64_t(many) * R, tiles) - int64_t(rows) * R * 9;
+// A test knob, read at every launch: share whatever rows have in common.
+static bool share_always() {
+  const char* s = std::getenv("SPECVERIFY_SHARE");
+  return s && s[0] == '1';
 }
-// Two more kernels that find work: about 8 us of all SMs.
-constexpr int64_t kPfLeast = 120000;
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     kv_prefix_plan_kernel(const PlanArgs a) {
@@ -175,7 +168,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int tiles = bad || live[g] < 2 ? 0
                                          : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs /
                                                kPfTile);
-    const int64_t gain = pf_gain(live[g], starts[g + 1] - starts[g], R, tiles);
+    const int64_t gain =
+        tiles == 0 ? 0 : pf_alone(live[g], tiles, R) - pf_shared(live[g], starts[g + 1] - starts[g], tiles, R);
     common[g] = a.always || gain > 0 ? tiles : 0;
     if (gain > 0) saved += gain;
   }
@@ -260,7 +254,7 @@ int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
   a.bs = k.block_size;
   a.B = k.B;
   a.MB = k.max_blocks;
-  a.always = k.always;
+  a.always = share_always();
   a.plan = static_cast<uint8_t*>(k.plan);
   a.err = k.err;
   const size_t smem = (5 * size_t(a.NG) + 1 + a.B) * 4;
@@ -452,6 +446,8 @@ size_t kv_prefix_workspace(int B, int T, int H, int G, int D) {
 }
 
 int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t plan_bytes) {
+  if (!share_always() && !pf_could(k.B, k.max_blocks, k.bs, k.T * k.G, k.H))
+    return launch_kv_q8_attention(k);
   PfArgs a = {};
   const int64_t layer_bytes = int64_t(2) * k.H * k.bs * k.D;
   a.q = k.q;

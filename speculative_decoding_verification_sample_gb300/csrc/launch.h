@@ -187,7 +187,6 @@ struct KvPrefixPlanLaunch {
   const int32_t* group_starts;
   const int32_t* group_rows;
   int num_groups, num_members, T, G, H, num_blocks, block_size, B, max_blocks;
-  int always;  // share whatever is common, not only where it saves time
   void* plan;
   void* stream;
   int32_t* err;

@@ -22,6 +22,12 @@ from tests import q8_helpers as h
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def share(monkeypatch):
+    """Most of these cases are too small for sharing to pay: share whatever is common."""
+    monkeypatch.setenv("SPECVERIFY_SHARE", "1")
+
+
 def grouped(rng, groups, own, alone, bs, T, n=None):
     """(L, block_table, starts, members, num_blocks): groups [(prefix, rows)], each row's own
     lengths from own = (lo, hi), `alone` rows in no group, all in a shuffled order."""
@@ -53,11 +59,10 @@ def grouped(rng, groups, own, alone, bs, T, n=None):
     return L, bt, starts, members, nb
 
 
-def plan_of(bt, L, starts, members, T, Hq, H, bs, nb, n=None, err=None, always=True):
-    """A plan that shares whatever is common: most of these cases are too small for it to pay."""
+def plan_of(bt, L, starts, members, T, Hq, H, bs, nb, n=None, err=None):
     return sv.kv_prefix_plan(h.i32(bt), h.i32(L), h.i32(starts), h.i32(members), tokens=T,
                              q_heads=Hq, kv_heads=H, block_size=bs, num_blocks=nb,
-                             num_new=None if n is None else h.i32(n), always=always, err_flag=err)
+                             num_new=None if n is None else h.i32(n), err_flag=err)
 
 
 def bound(out, spread, reach, D):
@@ -280,7 +285,7 @@ def test_after_fork_and_on_streams_and_captured():
     def step(out, stream=None):
         sv.kv_q8_append(k, k, dp, ds, table, lens, stream=stream, err_flag=err)
         plan = sv.kv_prefix_plan(table, lens, starts, members, tokens=T, q_heads=Hq, kv_heads=H,
-                                 block_size=bs, num_blocks=nb, always=True, stream=stream, err_flag=err)
+                                 block_size=bs, num_blocks=nb, stream=stream, err_flag=err)
         sv.kv_q8_prefix_attention(dq, dp, ds, table, lens, plan, out, stream=stream, err_flag=err)
 
     def expect(out):

@@ -10,7 +10,7 @@ import speculative_decoding_verification_sample_gb300 as sv
 from oracle import rope
 from tests import q8_helpers as h
 from tests.test_gpu_norm_rope import _bound
-from tests.test_gpu_prefix import _run, _small, check, grouped, plan_of, queries
+from tests.test_gpu_prefix import _run, _small, check, grouped, plan_of, queries, share  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -54,7 +54,7 @@ def test_steps_of_forked_rows(T, Hq, H, D, tree, L0):
                                   k_weight=w[1], positions=h.i32(pos) if tree else None,
                                   err_flag=err)
         plan = sv.kv_prefix_plan(table, lens, starts, members, tokens=T, q_heads=Hq, kv_heads=H,
-                                 block_size=bs, num_blocks=nb, always=True, err_flag=err)
+                                 block_size=bs, num_blocks=nb, err_flag=err)
         sv.kv_q8_prefix_attention(qo, dp, ds, table, lens, plan, out, tree_mask=tm, err_flag=err)
         assert int(err) == 0 and int(status) == 0
         y, reach = rope.heads(q.double().cpu().numpy(), wn[0], pos, f.cpu().numpy())
@@ -134,27 +134,32 @@ def test_no_groups():
         check(out, q, pool, scales, bt, L)
 
 
-def test_what_is_shared():
+def test_what_is_shared(monkeypatch):
     """By itself a plan shares where that saves time: rows that it leaves alone have the bytes that
     kv_q8_attention gives them, and a plan that shares nothing all of them."""
     _, L, bt, starts, members, nb, pool, scales, q, dq = _small(16, groups=((500, 3), (300, 2)))
     want = torch.empty_like(dq)
     sv.kv_q8_attention(dq, h.dev_pool(pool), h.dev_scales(scales), h.i32(bt), h.i32(L), want)
-    out = _run(dq, pool, scales, bt, L,
-               plan_of(bt, L, starts, members, 4, 8, 2, 16, nb, always=False))
-    assert torch.equal(out, want)
     out = _run(dq, pool, scales, bt, L, plan_of(bt, L, starts, members, 4, 8, 2, 16, nb))
     alone = [r for r in range(len(L)) if r not in members]
     assert torch.equal(out[alone], want[alone]) and not torch.equal(out, want)
+    monkeypatch.delenv("SPECVERIFY_SHARE")
+    out = _run(dq, pool, scales, bt, L, plan_of(bt, L, starts, members, 4, 8, 2, 16, nb))
+    assert torch.equal(out, want)
+    # tables long enough to share much, rows that do not
+    wide = np.concatenate([bt, np.full((len(L), 20000), -1)], 1)
+    out = _run(dq, pool, scales, wide, L, plan_of(wide, L, starts, members, 4, 8, 2, 16, nb))
+    assert torch.equal(out, want)
     # 64 rows behind 12000 common tokens
     rng = np.random.default_rng(16)
     L, bt, starts, members, nb = grouped(rng, [(12000, 64)], (0, 100), 2, 16, 2)
     pool, scales = h.cache(rng, nb, 1, 2, 16, 64, spread=1)
     q, dq = queries(rng, 66, 2, 32, 64)
-    outs = [_run(dq, pool, scales, bt, L,
-                 plan_of(bt, L, starts, members, 2, 32, 2, 16, nb, always=x)) for x in (False, True)]
-    assert torch.equal(*outs)
-    check(outs[0], q, pool, scales, bt, L)
+    args = bt, L, starts, members, 2, 32, 2, 16, nb
+    out = _run(dq, pool, scales, bt, L, plan_of(*args))
+    check(out, q, pool, scales, bt, L)
+    monkeypatch.setenv("SPECVERIFY_SHARE", "1")
+    assert torch.equal(out, _run(dq, pool, scales, bt, L, plan_of(*args)))
 
 
 def test_first_tokens():

@@ -5,7 +5,7 @@ import speculative_decoding_verification_sample_gb300 as sv
 from tests.test_kv_operators_refusals import EINVAL, ENOTSUP, P, L, _call  # noqa: F401
 
 PLAN = dict(bt=P, sl=P, nn=None, starts=P, rows=P, NG=1, NE=2, T=3, Hq=4, H=2, NB=4, bs=16, B=2,
-            MB=2, always=0, plan=P, pn=1 << 20, stream=None, err=None)
+            MB=2, plan=P, pn=1 << 20, stream=None, err=None)
 ATTN = dict(q=P, dtype=0, pool=P, scales=P, bt=P, sl=P, nn=None, tree=None, plan=P, pn=1 << 20,
             out=P, scale=0.125, NB=4, NL=2, layer=0, Hq=4, H=2, D=64, bs=16, B=1, T=3, MB=2, ws=P,
             wsn=1 << 30, stream=None, err=None)
