@@ -54,12 +54,12 @@ __host__ __device__ inline int64_t pf_units(int64_t nq, int64_t tiles) {
                      : 0);
 }
 // What `tiles` tiles of `rows` rows of a group with R queries each cost row by row, in 10 ns of
-// an SM for each kv head: a tile 0.53 us with up to 24 queries and 17 ns more for each further
+// an SM for each kv head: a tile 0.6 us with up to 24 queries and 17 ns more for each further
 // one, in blocks of up to 64 (measured: 264 thousand tiles with 20 queries 1035 us on 152 SMs,
-// 48 thousand with 64 queries 404 us, of which the changes between items are a tenth).
+// 48 thousand with 64 queries 404 us).
 __host__ __device__ inline int64_t pf_alone(int64_t rows, int64_t tiles, int R) {
   const int blocks = (R + 63) / 64, each = (R + blocks - 1) / blocks;
-  return rows * tiles * blocks * (53 + 17 * (each > 24 ? each - 24 : 0) / 10);
+  return rows * tiles * blocks * (60 + 17 * (each > 24 ? each - 24 : 0) / 10);
 }
 // The same shared: the units, and the join, 0.12 us a query.
 __host__ __device__ inline int64_t pf_shared(int64_t rows, int64_t many, int64_t tiles, int R) {

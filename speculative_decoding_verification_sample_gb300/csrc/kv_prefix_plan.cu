@@ -514,9 +514,9 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
   const int sr = launch_kv_q8_attention(rows);
   if (sr != SPEC_OK) return sr;
   cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
-  // as many queries a warp as leave 32 warps for each SM, in equal chunks
+  // as few queries a warp as all warps can take at once (32 on each SM), in equal chunks
   const int R = a.T * a.G;
-  const int64_t each = int64_t(a.B) * a.H * R / (int64_t(sms) * 32);
+  const int64_t at_once = int64_t(sms) * 32, each = (int64_t(a.B) * a.H * R + at_once - 1) / at_once;
   int per = each < 1 ? 1 : each > kPfJoinQueries ? kPfJoinQueries : int(each);
   const int chunks = (R + per - 1) / per;
   per = (R + chunks - 1) / chunks;
