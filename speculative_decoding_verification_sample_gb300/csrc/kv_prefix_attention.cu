@@ -27,9 +27,8 @@
 // Bound by the chain of a tile: scores 240 cycles after the last product is issued, softmax 1700
 // to 2100, a turn's products 1170 and what the issuing warp does before them, 1100 with code from
 // the second-level instruction cache; a step of two M tiles takes 4860 cycles, its products 2050.
-// 440 us for 5120 queries a kv head before 16000 shared keys, 346 GFLOP: 0.42 of the bf16 peak,
-// the tensor cores 37 % of the time at work. (A warp for each group's products made a step 4450
-// cycles, and the call no faster: the turns' order costs as much at items' ends.)
+// 319 us for 5120 queries of each of 8 kv heads before 16000 shared keys, 336 GFLOP: 0.56 of the
+// bf16 peak.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
