@@ -21,14 +21,13 @@
 // exactly. A query's scores of a tile stay in registers from the maximum to the probabilities.
 //
 // Roles, of 4 warps each with registers moved to the softmax: two softmax groups; widening of V;
-// a warp that issues the products, one that walks the work list and prepares queries, one that
+// a warp for each group's products, one that walks the work list and prepares queries, one that
 // finds the tiles and starts their copies. One CTA per SM.
 //
-// Bound by the chain of a tile: scores 240 cycles after the last product is issued, softmax 1700
-// to 2100, a turn's products 1170 and what the issuing warp does before them, 1100 with code from
-// the second-level instruction cache; a step of two M tiles takes 4860 cycles, its products 2050.
-// 319 us for 5120 queries of each of 8 kv heads before 16000 shared keys, 336 GFLOP: 0.56 of the
-// bf16 peak.
+// Bound by the chain of a tile: scores 240 cycles after the last product is issued, softmax 1900
+// to 2400, a turn's products 1500; a step of two M tiles takes 4450 cycles, its products 2050 (one
+// warp for both groups' products, with 1100 cycles of its own code before each turn: 4860). 297 us
+// for 5120 queries of each of 8 kv heads before 16000 shared keys, 336 GFLOP: 0.60 of the bf16 peak.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -51,6 +50,7 @@ static_assert(256 * kPfSoftmaxRegs + 128 * (kPfLoadRegs + kPfOtherRegs) == 65536
 constexpr int kPfItems = 6;     // items described at a time
 constexpr int kPfQueries = 2;   // M tiles of queries held at a time
 constexpr int kPfFactors = 16;  // M tiles whose rows' factors are held: more than kPfItems items have
+constexpr int kPfTurns = 8;     // more than the steps between the groups
 constexpr int kPfPart = 16;     // keys of a part of a tile: of one block (block_size % 16 == 0)
 constexpr int kPfParts = kPfTile / kPfPart;
 constexpr float kMaxBf16 = 0x1.fep127f;
@@ -110,6 +110,7 @@ struct PfShape {
     uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
     uint64_t q_full[kPfQueries], q_empty[kPfQueries];
     uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+    uint64_t turn[2][kPfTurns];
     uint64_t s_full[2], p_full[2], o_full[2], told[2], read[2], drained;
     uint32_t tmem;
     PfGuard guard;
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   using S = PfShape<D>;
   constexpr int KS = S::kKSlots, RS = S::kRawSlots, VS = S::kVSlots, NT = S::kTiles;
   constexpr int kCode = S::kCodeBytes, kWide = S::kWideBytes;
-  constexpr int kMmaWarp = (kPfSoftmax + kPfLoad) / 32, kWalkWarp = kMmaWarp + 1,
-                kFindWarp = kMmaWarp + 2;  // (and one to fill the four)
+  constexpr int kMmaWarp = (kPfSoftmax + kPfLoad) / 32, kWalkWarp = kMmaWarp + 2,
+                kFindWarp = kMmaWarp + 3;
   extern __shared__ __align__(1024) uint8_t sm[];  // V, queries, K, V as cached, the rest
   uint8_t* q_s = sm + VS * kWide;
   uint8_t* k_s = q_s + kPfQueries * kWide;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kPfItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_empty[i], kPfSoftmax / 32 + 2);
+      mbar_init(&sh.item_empty[i], kPfSoftmax / 32 + 3);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -386,15 +387,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     for (int i = 0; i < kPfQueries; ++i) {
       mbar_init(&sh.q_full[i], kPfSoftmax / 32);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_empty[i], 2);
     }
     for (int i = 0; i < KS; ++i) {
       mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.k_empty[i], 2);
     }
     for (int i = 0; i < VS; ++i) {
       mbar_init(&sh.v_full[i], kPfLoad / 32);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&sh.told[i], 128);
       mbar_init(&sh.read[i], 128);
     }
-    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < 2 * kPfTurns; ++i) mbar_init(&sh.turn[0][0] + i, 1);
+    mbar_init(&sh.drained, 2);
     sh.guard.abort = sh.guard.beat[0] = sh.guard.beat[1] = sh.guard.done[0] = sh.guard.done[1] = 0;
     fence_mbar_init();
   }
@@ -921,18 +923,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       for (int i = 0; i < RS; ++i)
         if (started >> (16 + i) & 1u) mbar_wait(&sh.raw_full[i], started_phase >> (16 + i) & 1u);
     }
-    } else if (warp == kMmaWarp) {
+    } else {
     // ---------------------------------------------------------------- products
-    // In each step first group 0, then group 1: the output of its tile before, then the scores
-    // of the next, which take the place of that tile's probabilities. So one group's products
-    // run while the other's softmax does. The whole warp goes through the loops, so that what
-    // the products need is known to be uniform; one lane issues them. (A warp for each group
-    // left the tensor cores idle while they handed over to each other.)
+    // A warp a group: the output of a tile, then the next scores, which take the place of that
+    // tile's probabilities. They take turns, so that one group's products run while the other's
+    // softmax does; as issuing lasts as long as the products, one warp for both would leave the
+    // tensor cores idle while it waits and prepares. All waits of a turn are made at once, a
+    // lane each. Tiles that only the other group takes are waited for and released too, so that
+    // no warp falls two rounds behind in a ring, where the parity of its waits would mislead it.
+    // The whole warp goes through the loops, so that what the products need is known to be
+    // uniform; one lane issues them.
     constexpr uint32_t kSwz = D == 128 ? 2 : 4;  // K and queries: 128- or 64-byte swizzle
     constexpr uint32_t idesc_s = tc_idesc(0, 0, 0, 0, kPfTile, kPfTile);
     constexpr uint32_t idesc_o = tc_idesc(1, 1, 0, 1, kPfTile, D);
     auto uniform = [](uint32_t x) { return __reduce_max_sync(0xffffffffu, x); };
-    const uint32_t tmem_u = uniform(tmem);
+    const int g = uniform(warp) - kMmaWarp;
+    const uint32_t s_at = uniform(tmem) + g * 128, o_at = s_at + 256;
     const uint64_t k0 = tc_desc(smem_u32(k_s), 16, 8 * D, kSwz);
     const uint64_t v0 = tc_desc(smem_u32(sm), kPfTile * 128, 1024, 2);
     const uint32_t k_hi = uint32_t(k0 >> 32), v_hi = uint32_t(v0 >> 32), k_lo = uint32_t(k0),
@@ -941,17 +947,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     PfRing<kPfQueries> qring;
     PfRing<KS> kr;
     PfRing<VS> vr;
-    // bits of the groups: the phase of their probabilities; an output that waits, whether it is
-    // of its item's first and last tile, and of a V tile that both take
-    uint32_t p_phase = 0, pending = 0, firsts = 0, lasts = 0, both = 0;
-    int v_at = 0, k_at = 0;  // slots of the last V and K
-    bool ok = true;          // no wait has run out
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      if (ok) ok = __all_sync(0xffffffffu, pf_wait(bar, phase, guard));
-    };
+    PfRing<kPfTurns> turn;  // group 1: the one of this step; group 0: of the step before
+    uint32_t p_phase = 0;
+    // An output that waits, whether it is of its item's first and last tile, and of a V tile
+    // that both take. The other group's V and K that are to be released.
+    bool pending = false, first = false, last = false, shared = false, begun = false;
+    bool pend0 = false, pend1 = false, other_v = false, other_k = false;
+    int s_turn = 0;  // step, round and round
+    bool ok = true;  // no wait has run out
     // steps of items, and one after the last for the outputs that wait
     for (bool more = true; more && ok;) {
-      wait(&sh.item_full[ring.at], ring.phase);
+      ok = __all_sync(0xffffffffu, pf_wait(&sh.item_full[ring.at], ring.phase, guard));
       if (!ok) break;
       const PfItem& it = sh.item[ring.at];
       more = !uniform(it.stop);
@@ -963,57 +969,50 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (more) qring.next();
       const PfRing<kPfQueries> q1 = two ? qring : q0;
       if (two) qring.next();
-      const int turns = !more ? 2 : two ? 2 * tiles : (tiles + 1) / 2 * 2;
+      const PfRing<kPfQueries> q = g ? q1 : q0, q_other = g ? q0 : q1;
+      const int by = two ? 1 : 2, steps = !more ? 1 : (tiles + by - 1) / by;
+      int x = two ? 0 : g;  // this group's next tile of the item
 #pragma unroll 1
-      for (int e = 0; e < turns && ok; ++e) {
-        const int g = e & 1;
-        const bool starts = e < 2, shared = both >> g & 1u;
-        const bool on = two || e < tiles, ends = two ? e + 2 >= turns : e + 2 >= tiles;
-        const PfRing<kPfQueries> q = g ? q1 : q0;
+      for (int s = 0; s < steps && ok; ++s, x += by) {
+        if (g == 1) {  // group 0's of this step come before its own
+          other_v = pend0 && !shared;
+          other_k = more && !two;
+        }
+        const PfRing<VS> v_other = vr;
+        if (other_v) vr.next();
+        const PfRing<KS> k_other = kr;
+        if (other_k) kr.next();
+        const bool on = x < tiles, ends = x + by >= tiles;
         // The output and the scores are issued together, but an item's first scores wait for its
         // queries, and the output before them does not wait for that.
-        bool out = pending >> g & 1u;
+        bool out = pending, waits = begun || g == 1;  // for its turn
 #pragma unroll 1
-        for (int r = out && starts ? 0 : 1; r < 2 && ok; ++r) {
-          const bool score = r == 1 && on;
-          const bool new_k = score && (!two || g == 0), new_v = out && (!shared || g == 0);
-          // all waits at once, a lane each
+        for (int r = out && s == 0 ? 0 : 1; r < 2 && ok; ++r) {
+          const bool now = r == 1, score = now && on;
           {
-            uint64_t* bar = lane == 0   ? &sh.p_full[g]
-                            : lane == 1 ? &sh.v_full[vr.at]
-                            : lane == 2 ? &sh.k_full[kr.at]
-                                        : &sh.q_full[q.at];
-            const uint32_t phase = lane == 0   ? p_phase >> g & 1u
-                                   : lane == 1 ? vr.phase
-                                   : lane == 2 ? kr.phase
-                                               : q.phase;
-            const bool need = lane == 0   ? out
-                              : lane == 1 ? new_v
-                              : lane == 2 ? new_k
-                                          : lane == 3 && score && starts;
+            uint64_t* bar = &sh.p_full[g];
+            uint32_t phase = p_phase;
+            bool need = out;
+            if (lane == 1) bar = &sh.v_full[vr.at], phase = vr.phase;
+            if (lane == 2) bar = &sh.k_full[kr.at], phase = kr.phase, need = score;
+            if (lane == 3) bar = &sh.q_full[q.at], phase = q.phase, need = now && more && s == 0;
+            if (lane == 4)
+              bar = &sh.q_full[q_other.at], phase = q_other.phase, need = now && two && s + 1 == steps;
+            if (lane == 5) bar = &sh.v_full[v_other.at], phase = v_other.phase, need = now && other_v;
+            if (lane == 6) bar = &sh.k_full[k_other.at], phase = k_other.phase, need = now && other_k;
+            if (lane == 7) bar = &sh.turn[g ^ 1][turn.at], phase = turn.phase, need = waits;
+            need = need && lane < 8;
             ok = __all_sync(0xffffffffu, !need || pf_wait(bar, phase, guard));
-          }
-          if (new_k) {
-            k_at = kr.at;
-            kr.next();
-          }
-          if (new_v) {
-            v_at = vr.at;
-            vr.next();
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t s_at = tmem_u + g * 128, o_at = s_at + 256;
-          const uint32_t v_desc = v_lo + v_at * (kWide / 16), k_desc = k_lo + k_at * (kCode / 16),
+          const uint32_t v_desc = v_lo + vr.at * (kWide / 16), k_desc = k_lo + kr.at * (kCode / 16),
                          q_desc = q_lo + q.at * (kWide / 16);
-          const bool first = firsts >> g & 1u, last = lasts >> g & 1u;
           if (elect_one()) {
             if (out) {
 #pragma unroll
               for (int y = 0; y < kPfTile / 16; ++y)
                 pf_mma_o(o_at, s_at + 8 * y, v_desc + 128 * y, v_hi, idesc_o, y > 0 || !first);
-              if (!shared || g == 1) tc_commit(&sh.v_empty[v_at]);
-              if (last) tc_commit(&sh.o_full[g]);
             }
             if (score) {
               // both terms of the queries into one sum
@@ -1023,20 +1022,44 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 pf_mma_s(s_at, q_desc + kCode / 16 + 2 * z, k_desc + 2 * z, k_hi, idesc_s, true);
               }
               tc_commit(&sh.s_full[g]);
-              if (!two || g == 1) tc_commit(&sh.k_empty[k_at]);
-              // the item's last scores of these queries
-              if (two ? ends : e + 1 == tiles) tc_commit(&sh.q_empty[q.at]);
+            }
+            if (now) mbar_arrive(&sh.turn[g][s_turn]);
+            if (out) {
+              tc_commit(&sh.v_empty[vr.at]);
+              if (last) tc_commit(&sh.o_full[g]);
+            }
+            if (score) {
+              tc_commit(&sh.k_empty[kr.at]);
+              if (ends) tc_commit(&sh.q_empty[q.at]);  // the item's last scores of these queries
+            }
+            if (now) {
+              if (other_v) mbar_arrive(&sh.v_empty[v_other.at]);
+              if (other_k) mbar_arrive(&sh.k_empty[k_other.at]);
+              if (two && s + 1 == steps) mbar_arrive(&sh.q_empty[q_other.at]);
+              if (!two && more && s == 0 && g >= tiles) mbar_arrive(&sh.q_empty[q.at]);
             }
           }
           __syncwarp();
-          if (out) p_phase ^= 1u << g;
-          out = false;
+          if (out) {
+            p_phase ^= 1;
+            vr.next();
+          }
+          if (score) kr.next();
+          out = waits = false;
         }
-        const uint32_t bit = 1u << g;
-        pending = on && more ? pending | bit : pending & ~bit;
-        firsts = starts ? firsts | bit : firsts & ~bit;
-        lasts = ends ? lasts | bit : lasts & ~bit;
-        both = two ? both | bit : both & ~bit;
+        if (g == 1 || begun) turn.next();
+        if (++s_turn == kPfTurns) s_turn = 0;
+        if (g == 0) {  // group 1's of this step come after its own
+          other_v = pend1 && !shared;
+          other_k = !two && 2 * s + 1 < tiles;
+        }
+        pend0 = more;
+        pend1 = two || 2 * s + 1 < tiles;
+        pending = on;
+        first = s == 0;
+        last = ends;
+        shared = two;
+        begun = true;
       }
     }
     }
@@ -1046,7 +1069,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   if (sh.guard.abort) {
     // what has been issued ends before the CTA's memory is another's
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
       if (lane == 0) tc_commit(&sh.drained);
       __syncwarp();
       mbar_wait(&sh.drained, 0);
