@@ -149,19 +149,13 @@ __device__ __forceinline__ uint32_t pf_place8(int r, int c) {
   return uint32_t(r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4));
 }
 
-// The row of q and out ([B, T, H * G]) of query x of an item's block, or -1; b, t: its row and
-// place among the new tokens; n: how many of those there are.
+// The row of q and out ([B, T, H * G]) of query x of an item's block, or -1.
 __device__ __forceinline__ int64_t pf_query(const PfArgs& a, const PfPlan& p, const PfItem& it,
-                                            int x, int& b, int& t, int& n) {
-  b = -1;
-  t = n = 0;
+                                            int x) {
   if (x >= it.nq) return -1;
   const int R = a.T * a.G, qi = it.q0 + x, e = qi / R, r = qi - e * R;
-  b = it.entry + e < p.NE ? p.members[it.entry + e] : -1;
-  if (b < 0 || b >= a.B) return -1;
-  n = p.rows[b].n;
-  t = r / a.G;
-  if (t >= n) return -1;
+  const int b = it.entry + e < p.NE ? p.members[it.entry + e] : -1, t = r / a.G;
+  if (b < 0 || b >= a.B || t >= p.rows[b].n) return -1;
   return (int64_t(b) * a.T + t) * a.H * a.G + it.h * a.G + (r - t * a.G);
 }
 
@@ -272,8 +266,7 @@ __device__ __forceinline__ void pf_prepare(const PfArgs& a, const PfPlan& p, con
   const int rows = min(kPfTile, max(0, it.nq - x0));
   // raw chunk c of a row: even ones to the upper term's chunk c / 2, odd ones to the lower's
   for (int r0 = w * 32; r0 < kPfTile; r0 += n * 32) {
-    int b, t, m;
-    const int64_t mine = pf_query(a, p, it, x0 + r0 + lane, b, t, m);
+    const int64_t mine = pf_query(a, p, it, x0 + r0 + lane);
     if (mine < 0) factor[r0 + lane] = 0.0f;
 #pragma unroll 4
     for (int x = 0; x < kChunks; ++x) {
@@ -457,8 +450,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const bool begins = it.t0 == 0;
       const int turns = two ? tiles : (tiles + 1 - g) / 2;
       const int x0 = (two ? g * kPfTile : 0) + row;
-      int b, t, n;
-      const int64_t query = pf_query(a, plan, it, x0, b, t, n);
+      const int64_t query = pf_query(a, plan, it, x0);
       const float* factor = sh.factor[(count + (two ? g : 0)) % kPfFactors];
       const int seq0 = seq;
       seq += tiles;
@@ -783,9 +775,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     } else if (warp == kFindWarp) {
     // ---------------------------------------------------------------- where the tiles are
     // Four tiles at a time, a lane a part: ids, then scales. Copies of K and V are started here, in
-    // the order in which the products take them: those
-    // go through steps, in each of which first group 0, then group 1 takes the output of its
-    // tile before (V), then the scores of the next (K).
+    // the order in which the products take them: those go through steps, in each of which first
+    // group 0, then group 1 takes the output of its tile before (V), then the scores of the next
+    // (K).
     PfRing<kPfItems> ring;
     PfRing<RS> rr;
     PfRing<KS> kr;

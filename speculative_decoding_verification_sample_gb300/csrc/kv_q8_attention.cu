@@ -187,8 +187,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* o, float4 v) {
   *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(x);
 }
 
-template <class T>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+template <class T, class Args>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const Args a) {
   __shared__ float4 acc_s[kJoinRows][kAnyMaxD / 4];
   __shared__ float2 st_s[kJoinRows];
   pdl_trigger();
@@ -241,14 +241,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   if (!live || half == 1) return;
   add(st_s[rr].x, st_s[rr].y, &acc_s[rr][lane]);
   const int64_t query = (int64_t(j.x) * a.T + row / a.G) * a.H * a.G + j.y * a.G + row % a.G;
-  if (a.plan && leaves_part(a, row_span(a, j.x))) {
-    float4* o = reinterpret_cast<float4*>(a.own + query * a.D) + lane;
+  if constexpr (Args::kPlan)
+    if (leaves_part<Args>(row_span(a, j.x))) {
+      float4* o = reinterpret_cast<float4*>(a.own + query * a.D) + lane;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < quads) o[32 * i] = acc[i];
-    if (lane == 0) a.own_stats[query] = make_float2(m, l);
-    return;
-  }
+      for (int i = 0; i < kPer; ++i)
+        if (lane + 32 * i < quads) o[32 * i] = acc[i];
+      if (lane == 0) a.own_stats[query] = make_float2(m, l);
+      return;
+    }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   T* o = static_cast<T*>(a.out) + query * a.D + 4 * lane;
 #pragma unroll
@@ -257,12 +258,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
       store4(o + 128 * i, make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
 }
 
-int launch_attn_join(const AttnArgs& a, int nc, int dtype, void* stream) {
+template <class T, class Args>
+int launch_attn_join(const Args& a, int nc, void* stream) {
   const dim3 grid(nc, (min(a.rows_per_block, a.R) + kJoinRows - 1) / kJoinRows);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return dtype == SPEC_F32
-             ? launch_pdl(attn_join_kernel<float>, grid, dim3(kJoinThreads), 0, st, a)
-             : launch_pdl(attn_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, st, a);
+  return launch_pdl(attn_join_kernel<T, Args>, grid, dim3(kJoinThreads), 0,
+                    static_cast<cudaStream_t>(stream), a);
 }
 
 // ------------------------------------------------------------------ host
@@ -327,7 +327,7 @@ bool kv_q8_attention_on_tc(int dtype, int D, int bs, int64_t planes) {
 }
 
 int launch_kv_q8_attention(const Q8AttnLaunch& k) {
-  AttnArgs a;
+  PlanAttnArgs a;
   const int64_t layer_bytes = int64_t(2) * k.H * k.bs * k.D;
   a.q = k.q;
   a.pool = static_cast<const uint8_t*>(k.pool) + k.layer * layer_bytes;
@@ -372,15 +372,17 @@ int launch_kv_q8_attention(const Q8AttnLaunch& k) {
   ws += up256(size_t(2) * kAttnMaxCtas * a.rows_per_block * sizeof(float2));
   a.joins = reinterpret_cast<int4*>(ws);
   int nc = 2 * sms < kAttnMaxCtas ? 2 * sms : kAttnMaxCtas;
-  if (tc) {
+  const AttnArgs& plain = a;
+  if (tc && k.plan) {
     const int st = launch_attn_tc(a, k.pool, planes, sms, kAttnMaxCtas, &nc, k.stream);
-    if (st != SPEC_OK) return st;
-  } else {
-    const int st = k.dtype == SPEC_F32 ? launch_any<float>(a, nc, k.stream)
-                                       : launch_any<__nv_bfloat16>(a, nc, k.stream);
-    if (st != SPEC_OK) return st;
+    return st != SPEC_OK ? st : launch_attn_join<__nv_bfloat16>(a, nc, k.stream);
   }
-  return launch_attn_join(a, nc, k.dtype, k.stream);
+  const int st = tc ? launch_attn_tc(plain, k.pool, planes, sms, kAttnMaxCtas, &nc, k.stream)
+                 : k.dtype == SPEC_F32 ? launch_any<float>(plain, nc, k.stream)
+                                       : launch_any<__nv_bfloat16>(plain, nc, k.stream);
+  if (st != SPEC_OK) return st;
+  return k.dtype == SPEC_F32 ? launch_attn_join<float>(plain, nc, k.stream)
+                             : launch_attn_join<__nv_bfloat16>(plain, nc, k.stream);
 }
 
 }  // namespace sv

@@ -363,9 +363,9 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& a, TcShared<NR>& sh
   }
 }
 
-template <int NR, int D>
+template <int NR, int D, class Args>
 __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
-    attn_tc_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map) {
+    attn_tc_kernel(const Args a, const __grid_constant__ CUtensorMap map) {
   using S = TcShape<NR, D>;
   constexpr int NS = S::kSlots, NO = S::NO, SB = S::kSBufs;
   constexpr int kTmaWarp = S::kSoftmax / 32, kMmaWarp = kTmaWarp + 2, kQWarp = kTmaWarp + 3;
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
           for (int x = 0; x < chunks; ++x) sh.part[gw][col0 + 8 * x + reduce8_row(lane)] = v[x][0];
       }
       bar_group(group);
-      const bool whole = g.t0 == 0 && g.t1 == g.s.tiles, done = whole && !leaves_part(a, g.s);
+      const bool whole = g.t0 == 0 && g.t1 == g.s.tiles, done = whole && !leaves_part<Args>(g.s);
       const int64_t slot = 2 * c + (g.u == plan.u0 ? 0 : 1);
       if (key < W) {
         const float* mp = sh.part[0] + col0 + key;
@@ -852,13 +852,19 @@ __global__ void __launch_bounds__(TcShape<NR, D>::kThreads, 2)
         ra[key] = (!done ? down : sum == 0.0f ? 0.0f : __fdividef(down, sum * down)) * unlift;
         const int off = sh.row_off[qb][col0 + key];
         const int64_t part = slot * a.rows_per_block + col0 + key;
-        const int64_t query = first_row(a, g) + off;
+        float* to = a.parts + part * D;
+        float2* stats = a.stats + part;
+        if constexpr (Args::kPlan)
+          if (whole) {
+            to = a.own + (first_row(a, g) + off) * D;
+            stats = a.own_stats + first_row(a, g) + off;
+          }
         sh.row_to[col0 + key] =
-            done ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + query * D)
-                 : reinterpret_cast<uint64_t>(whole ? a.own + query * D : a.parts + part * D);
+            done ? reinterpret_cast<uint64_t>(static_cast<__nv_bfloat16*>(a.out) + (first_row(a, g) + off) * D)
+                 : reinterpret_cast<uint64_t>(to);
         if (!done && off >= 0)
-          *(whole ? a.own_stats + query : a.stats + part) =
-              make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e), sum * q8_pow2(-e));
+          *stats = make_float2(sum == 0.0f ? -INFINITY : -nm[key] + float(e),
+                               sum * q8_pow2(-e));
       }
       bar_group(group);
       wait_outputs();
@@ -959,17 +965,17 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-template <int NR, int D>
-int launch_shape(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t st) {
-  auto kern = attn_tc_kernel<NR, D>;
+template <int NR, int D, class Args>
+int launch_shape(const Args& a, const CUtensorMap& map, int nc, cudaStream_t st) {
+  auto kern = attn_tc_kernel<NR, D, Args>;
   constexpr size_t smem = TcShape<NR, D>::kBytes;
   static std::atomic<uint64_t> done{0};
   if (allow_smem(kern, smem, done) != SPEC_OK) return SPEC_ECUDA;
   return launch_pdl(kern, dim3(nc), dim3(TcShape<NR, D>::kThreads), smem, st, a, map);
 }
 
-template <int D>
-int launch_rows(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t st) {
+template <int D, class Args>
+int launch_rows(const Args& a, const CUtensorMap& map, int nc, cudaStream_t st) {
   const int r = a.rows_per_block;
   if (r <= 8) return launch_shape<8, D>(a, map, nc, st);
   if (r <= 16) return launch_shape<16, D>(a, map, nc, st);
@@ -979,10 +985,9 @@ int launch_rows(const AttnArgs& a, const CUtensorMap& map, int nc, cudaStream_t 
   return launch_shape<64, D>(a, map, nc, st);
 }
 
-}  // namespace
-
-int launch_attn_tc(const AttnArgs& a, const void* pool_base, int64_t planes, int sms, int max_ctas,
-                   int* nc, void* stream) {
+template <class Args>
+int launch_with(const Args& a, const void* pool_base, int64_t planes, int sms, int max_ctas,
+                int* nc, void* stream) {
   EncodeTiled enc = encode_tiled();
   if (!enc) return SPEC_ECUDA;
   CUtensorMap map;
@@ -998,6 +1003,17 @@ int launch_attn_tc(const AttnArgs& a, const void* pool_base, int64_t planes, int
   *nc = 2 * sms < max_ctas ? 2 * sms : max_ctas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a.D == 128 ? launch_rows<128>(a, map, *nc, st) : launch_rows<64>(a, map, *nc, st);
+}
+
+}  // namespace
+
+int launch_attn_tc(const AttnArgs& a, const void* pool_base, int64_t planes, int sms, int max_ctas,
+                   int* nc, void* stream) {
+  return launch_with(a, pool_base, planes, sms, max_ctas, nc, stream);
+}
+int launch_attn_tc(const PlanAttnArgs& a, const void* pool_base, int64_t planes, int sms,
+                   int max_ctas, int* nc, void* stream) {
+  return launch_with(a, pool_base, planes, sms, max_ctas, nc, stream);
 }
 
 }  // namespace sv

@@ -619,6 +619,7 @@ int launch_shape(const NormRopeArgs& a, int tokens, int sms, cudaStream_t st) {
   const int heads = 32 / lanes;
   const int64_t groups = (a.Hq + heads - 1) / heads + (kCache ? 0 : (a.H + heads - 1) / heads);
   const int64_t units = groups * (tokens < a.T ? tokens : a.T);
+  if (units > INT32_MAX / 2) return SPEC_ENOTSUP;
   // The longer the tasks, the fewer of them wait: the longest that leave no warp much less
   // to do than another.
   const int64_t each = units * tiles / (int64_t(sms) * kNrCtas * kNrWarps);  // of a warp

@@ -74,6 +74,7 @@ __device__ __forceinline__ const PrefixRow* prefix_row(const uint8_t* plan, int 
 }
 
 struct AttnArgs {
+  static constexpr bool kPlan = false;
   const void* q;         // [B, T, H * G, D]
   const uint8_t* pool;   // at the layer
   const float* scales;   // at the layer
@@ -95,9 +96,14 @@ struct AttnArgs {
   int stall_row;              // -1, or the row whose V tiles are withheld (a test)
   int plane0;                 // tensor-map plane index of (block 0, this layer, keys, head 0)
   int planes_per_block;       // planes from block to block
-  const uint8_t* plan;        // null: none; at least a header and B rows
+};
+// With a plan. Kernels are made for either: tests of a pointer in the kernels for calls without
+// one took them from 207 to 220 us (256 rows of 512 to 4096 tokens).
+struct PlanAttnArgs : AttnArgs {
+  static constexpr bool kPlan = true;
+  const uint8_t* plan;        // at least a header and B rows
   size_t plan_bytes;
-  float* own;                 // [B T H G][D], with a plan: of rows with shared tiles
+  float* own;                 // [B T H G][D]: the parts of rows with shared tiles
   float2* own_stats;          // [B T H G]
 };
 
@@ -109,18 +115,19 @@ struct RowSpan {
   bool bad;
 };
 
-__device__ __forceinline__ bool plan_fits(const AttnArgs& a) {
+__device__ __forceinline__ bool plan_fits(const PlanAttnArgs& a) {
   return prefix_fits(a.plan, a.plan_bytes, a.B, a.T, a.G, a.H, a.bs, a.MB);
 }
 
-__device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
+template <class Args>
+__device__ __forceinline__ RowSpan row_span(const Args& a, int b) {
   RowSpan s;
   s.L = a.sl[b];
   s.n = a.nn ? a.nn[b] : a.T;
   s.bad = s.L < 0 || s.n < 0 || s.n > a.T || int64_t(s.L) + s.n > int64_t(a.MB) * a.bs;
   s.lo = s.sink_end = 0;
   int skip = 0;
-  if (a.plan) {
+  if constexpr (Args::kPlan) {
     // lengths that changed since the plan was made: the row's keys are not the plan's
     const PrefixRow* r = prefix_row(a.plan, b);
     s.bad = s.bad || r->L != s.L || r->n != s.n || !plan_fits(a);
@@ -133,7 +140,7 @@ __device__ __forceinline__ RowSpan row_span(const AttnArgs& a, int b) {
   s.end = s.L + s.n;
   const int all = (s.end + kAttnTile - 1) / kAttnTile;
   s.sink_tiles = 0;
-  s.win_tile = max(0, min(skip, s.L / kAttnTile));
+  s.win_tile = Args::kPlan ? max(0, min(skip, s.L / kAttnTile)) : 0;
   if (a.window > 0 && s.L >= a.window) {
     s.lo = s.L - a.window + 1;
     s.sink_end = min(a.sinks, s.end);
@@ -150,8 +157,9 @@ __device__ __forceinline__ int tile_start(const RowSpan& s, int k) {
 }
 
 // Whether a row's outputs are left as parts (calls with a plan have no window).
-__device__ __forceinline__ bool leaves_part(const AttnArgs& a, const RowSpan& s) {
-  return a.plan && s.win_tile > 0;
+template <class Args>
+__device__ __forceinline__ bool leaves_part(const RowSpan& s) {
+  return Args::kPlan && s.win_tile > 0;
 }
 
 // May a query of the row see a position of [p, p + n)? Blocks for which this is
@@ -191,7 +199,8 @@ struct Segment {
 
 // Every thread of the CTA; in shared memory `prefix` takes blockDim.x + 1 tile counts,
 // `warp_sum` one of each warp.
-__device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix, int64_t* warp_sum,
+template <class Args>
+__device__ __forceinline__ AttnPlan attn_plan(const Args& a, int64_t* prefix, int64_t* warp_sum,
                                               int nc, int c) {
   const int per = (a.B + blockDim.x - 1) / blockDim.x;
   int64_t sum = 0;
@@ -227,7 +236,8 @@ __device__ __forceinline__ AttnPlan attn_plan(const AttnArgs& a, int64_t* prefix
 }
 
 // The segment that starts at unit u of [u, u1).
-__device__ __forceinline__ Segment find_segment(const AttnArgs& a, const int64_t* prefix, int64_t u,
+template <class Args>
+__device__ __forceinline__ Segment find_segment(const Args& a, const int64_t* prefix, int64_t u,
                                                 int64_t u1) {
   const int64_t U = int64_t(a.H) * a.RB;
   // 64-bit division is a long routine: only where 32 bits do not do
@@ -263,7 +273,8 @@ __device__ __forceinline__ Segment find_segment(const AttnArgs& a, const int64_t
 }
 
 // The segment after g, which ended its item (the caller checks that units are left).
-__device__ __forceinline__ void next_segment(const AttnArgs& a, Segment& g, int64_t u1) {
+template <class Args>
+__device__ __forceinline__ void next_segment(const Args& a, Segment& g, int64_t u1) {
   g.u += g.t1 - g.t0;
   g.t0 = 0;
   if (++g.rb == a.RB) {
@@ -279,8 +290,8 @@ __device__ __forceinline__ void next_segment(const AttnArgs& a, Segment& g, int6
 
 // Rows without keys: zeros, or NaN where the row's lengths are invalid. By thread
 // `me` of `threads` of a CTA.
-template <class T>
-__device__ __forceinline__ void write_empty_rows(const AttnArgs& a, int c, int nc, int me,
+template <class T, class Args>
+__device__ __forceinline__ void write_empty_rows(const Args& a, int c, int nc, int me,
                                                  int threads) {
   for (int b = c; b < a.B; b += nc) {
     const RowSpan s = row_span(a, b);
@@ -289,8 +300,11 @@ __device__ __forceinline__ void write_empty_rows(const AttnArgs& a, int c, int n
     T* o = static_cast<T*>(a.out) + b * n;
     const T v = T(s.bad ? __uint_as_float(0x7fc00000u) : 0.0f);
     for (int64_t i = me; i < n; i += threads) o[i] = v;
-    if (s.bad && a.err && me == 0)
-      atomicOr(a.err, a.plan && !plan_fits(a) ? SPEC_DERR_BAD_SLOT : SPEC_DERR_BAD_LENGTH);
+    if (s.bad && a.err && me == 0) {
+      int bit = SPEC_DERR_BAD_LENGTH;
+      if constexpr (Args::kPlan) bit = plan_fits(a) ? bit : SPEC_DERR_BAD_SLOT;
+      atomicOr(a.err, bit);
+    }
   }
 }
 
@@ -317,7 +331,7 @@ bool attn_tc_takes(int dtype, int D, int bs, int64_t planes);
 int attn_tc_rows(int R);
 int launch_attn_tc(const AttnArgs& a, const void* pool_base, int64_t planes, int sms, int max_ctas,
                    int* nc, void* stream);
-
-int launch_attn_join(const AttnArgs& a, int nc, int dtype, void* stream);
+int launch_attn_tc(const PlanAttnArgs& a, const void* pool_base, int64_t planes, int sms,
+                   int max_ctas, int* nc, void* stream);
 
 }  // namespace sv
