@@ -3,7 +3,8 @@
 // The plan. A cluster of 8 CTAs: each makes out in its own shared memory the rows' places in
 // the list of members (the first, if one is listed twice), the groups' first rows and
 // shortest lengths, and compares its share of the tables with those of the first rows;
-// the first CTA takes the first differences from all and sums up the units. Bound by
+// the first CTA takes the first differences from all and sums up the units. Where tables are too
+// short to share anything by the estimate it only looks at the lists. Bound by
 // latency, and for many long tables by reading them (B x max_blocks entries once): 9 us for 4
 // rows, 18 us for 256 rows that share 1000 blocks.
 #include <cooperative_groups.h>
@@ -27,7 +28,7 @@ constexpr int kPlanChunk = 256;  // table entries that a warp compares at a time
 
 struct PlanArgs {
   const int32_t *bt, *sl, *nn, *starts, *members;
-  int NG, NE, T, G, H, NB, bs, B, MB, always;
+  int NG, NE, T, G, H, NB, bs, B, MB, always, could;
   uint8_t* plan;
   int32_t* err;
 };
@@ -119,11 +120,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
     if (lead) members[i] = member;
   }
-  cluster.sync();  // (the first CTA's shared memory is written by the others below)
+  // (the first CTA's shared memory is written by the others below)
+  if (a.could) cluster.sync();
+  else if (!lead) return;
 
   // tables against the first row's, a warp 256 entries at a time
   const int chunks = (a.MB + kPlanChunk - 1) / kPlanChunk;
-  const int64_t tasks = int64_t(e1 - e0) * chunks;
+  const int64_t tasks = a.could ? int64_t(e1 - e0) * chunks : 0;
   for (int64_t t = int64_t(cluster.block_rank()) * (kPlanThreads / 32) + (tid >> 5); t < tasks;
        t += kPlanCtas * kPlanThreads / 32) {
     const int i = e0 + int(t / chunks), j0 = int(t % chunks) * kPlanChunk;
@@ -158,14 +161,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     for (int g = tid; g < a.NG; g += kPlanThreads)
       if (common[g] != INT32_MAX) atomicMin(&to[g], common[g]);
   }
-  cluster.sync();
+  if (a.could) cluster.sync();
   if (!lead) return;
 
   // What the groups share, in tiles, and what that saves. common[] holds it from here on.
   const int R = a.T * a.G;
   int64_t saved = 0;
   for (int g = tid; g < a.NG; g += kPlanThreads) {
-    const int tiles = bad || live[g] < 2 ? 0
+    const int tiles = bad || !a.could || live[g] < 2 ? 0
                                          : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs /
                                                kPfTile);
     const int64_t gain =
@@ -255,6 +258,7 @@ int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
   a.B = k.B;
   a.MB = k.max_blocks;
   a.always = share_always();
+  a.could = a.always || pf_could(a.B, a.MB, a.bs, a.T * a.G, a.H);
   a.plan = static_cast<uint8_t*>(k.plan);
   a.err = k.err;
   const size_t smem = (5 * size_t(a.NG) + 1 + a.B) * 4;

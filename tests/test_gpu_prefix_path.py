@@ -146,6 +146,12 @@ def test_what_is_shared(monkeypatch):
     monkeypatch.delenv("SPECVERIFY_SHARE")
     out = _run(dq, pool, scales, bt, L, plan_of(bt, L, starts, members, 4, 8, 2, 16, nb))
     assert torch.equal(out, want)
+    # its lists are looked at all the same
+    for st, mem in (([0, 4, 2], members), (starts, [99, *members[1:]]), ([0, 5], [members[0]] * 5)):
+        err = h.i32([0])
+        plan = plan_of(bt, L, st, mem, 4, 8, 2, 16, nb, err=err)
+        assert int(err) == sv.SPEC_DERR_BAD_SLOT
+        assert torch.equal(_run(dq, pool, scales, bt, L, plan), want)
     # tables long enough to share much, rows that do not
     wide = np.concatenate([bt, np.full((len(L), 20000), -1)], 1)
     out = _run(dq, pool, scales, wide, L, plan_of(wide, L, starts, members, 4, 8, 2, 16, nb))
