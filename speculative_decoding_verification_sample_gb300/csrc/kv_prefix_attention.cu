@@ -173,7 +173,7 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   return r;
 }
 
-// One lane of the warp.
+// One lane of the warp, the same one at every call.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -1060,9 +1060,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (sh.guard.abort) {
-    // what has been issued ends before the CTA's memory is another's
+    // What has been issued ends before the CTA's memory is another's. A commit stands for the
+    // products of its own thread: it has to come from the lane that issued them.
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-      if (lane == 0) tc_commit(&sh.drained);
+      if (elect_one()) tc_commit(&sh.drained);
       __syncwarp();
       mbar_wait(&sh.drained, 0);
       __syncwarp();  // the warp frees the TMEM as one
