@@ -14,7 +14,7 @@
 //
 // Sharing pays where the prefix is long and the rows are many: the plan compares, for each
 // group, what its tiles cost row by row with what they cost shared, and shares nothing at all
-// where that saves less than the launches of the two kernels more.
+// where that saves less than the two kernels more cost once they have work.
 //
 // Split of the shared part. A group's queries (all rows of it, row by row) are taken in
 // blocks of 256, two M tiles of the tensor core, the last one maybe one tile. An item is
@@ -53,20 +53,61 @@ __host__ __device__ inline int64_t pf_units(int64_t nq, int64_t tiles) {
           : rest > 0 ? pf_item_units(kPfOneUnits, tiles)
                      : 0);
 }
-// What `tiles` tiles of `rows` rows of a group with R queries each cost row by row, in 10 ns of
-// an SM for each kv head: a tile 0.6 us with up to 24 queries and 17 ns more for each further
-// one, in blocks of up to 64 (measured: 264 thousand tiles with 20 queries 1035 us on 152 SMs,
-// 48 thousand with 64 queries 404 us).
+// The estimate by which the plan shares, in 10 ns of an SM for each kv head. What a row costs
+// either way (its item of kv_q8_attention's kernel, 1 to 6 us with its change) is not in it.
+//
+// Fitted to 7500 measured pairs of times, the same call with a plan that shares nothing and with
+// all shared: 2 to 256 rows in 1 to 8 groups, 2 to 256 tiles in common, 1 to 16 kv heads of 64 and
+// 128 numbers, 1 to 128 queries a row and kv head. The estimate's way is more than 5 % slower than
+// the other in 2.2 % of them and 1.19 times as slow at most. (A price of 0.60 us a tile, changes
+// of items included, and none for the join's further pieces: 3.6 %, and 2.7 times.) Of them, with
+// 8 kv heads of 128, row by row and shared, us:
+//
+//   queries  rows     4 tiles        8       16       32       64      128      256
+//      4     1 x 16    23, 37   25, 38   28, 41   36, 45   49, 47   81, 56  134, 68
+//     20     1 x 16    28, 44   30, 49   33, 50   42, 55   59, 61   93, 75  156, 106
+//     20     8 x 16    69, 93   86, 96  116, 105 176, 140 309, 195
+//     64     8 x 8     68, 113  85, 113 117, 135 179, 157 302, 217 550, 330
+//    128     8 x 16   177, 298 239, 324 356, 392 600, 496
+//
+// kPfTile keys of one row, with the columns that its queries take in kv_q8_attention's kernel.
+__host__ __device__ inline int pf_tile_price(int columns) {
+  return columns <= 8    ? 52
+         : columns <= 16 ? 54
+         : columns <= 24 ? 60
+         : columns <= 32 ? 68
+         : columns <= 48 ? 83
+                         : 115;
+}
+// What `tiles` tiles of `rows` rows with R queries each cost row by row: blocks of up to 64.
 __host__ __device__ inline int64_t pf_alone(int64_t rows, int64_t tiles, int R) {
-  const int blocks = (R + 63) / 64, each = (R + blocks - 1) / blocks;
-  return rows * tiles * blocks * (60 + 17 * (each > 24 ? each - 24 : 0) / 10);
+  const int blocks = (R + 63) / 64;
+  return rows * tiles * blocks * pf_tile_price((R + blocks - 1) / blocks);
 }
-// The same shared: the units, and the join, 0.12 us a query.
+// The same shared: the units, 0.31 us each, and the parts and their join, 0.1 us a query.
 __host__ __device__ inline int64_t pf_shared(int64_t rows, int64_t many, int64_t tiles, int R) {
-  return 36 * pf_units(many * R, tiles) + rows * R * 12;
+  return 31 * pf_units(many * R, tiles) + rows * R * 10;
 }
-// What two more kernels cost that find work: about 18 us of all SMs.
-constexpr int64_t kPfLeast = 270000;
+// What the kernels cost once they find work, whatever it is: 19.4 us of all SMs (kPfSms of them).
+constexpr int kPfSms = 152;
+constexpr int64_t kPfLeast = int64_t(1940) * kPfSms;
+// And what the join waits for where few items are cut over many CTAs: 0.41 us for each piece
+// beyond two and query of a warp. `item`: units of the longest item, `units`: of all.
+__host__ __device__ inline int64_t pf_pieces(int64_t item, int64_t units, int per) {
+  const int64_t all = item * (units < kPfSms ? units : kPfSms);
+  if (all < 2 * units || units == 0) return 0;
+  const int64_t each = all >> 32 == 0 ? int64_t(uint32_t(all) / uint32_t(units)) : all / units;
+  return 41 * kPfSms * (each - 1) * per;
+}
+// Queries of a warp of the join: as few as all warps can take at once (32 on each SM), in equal
+// chunks of a row and kv head's.
+constexpr int kPfJoinQueries = 8;
+__host__ __device__ inline int pf_join_queries(int64_t rows_heads, int R, int sms) {
+  const int64_t at_once = int64_t(sms) * 32, each = (rows_heads * R + at_once - 1) / at_once;
+  const int per = each < 1 ? 1 : each > kPfJoinQueries ? kPfJoinQueries : int(each);
+  const int chunks = (R + per - 1) / per;
+  return (R + chunks - 1) / chunks;
+}
 // Whether rows of such sizes could share enough of their tables.
 __host__ inline bool pf_could(int B, int MB, int bs, int R, int H) {
   return pf_alone(B, int64_t(MB) * bs / kPfTile, R) * H > kPfLeast;

@@ -29,6 +29,7 @@ constexpr int kPlanChunk = 256;  // table entries that a warp compares at a time
 struct PlanArgs {
   const int32_t *bt, *sl, *nn, *starts, *members;
   int NG, NE, T, G, H, NB, bs, B, MB, always, could;
+  int per;  // queries of a warp of the join
   uint8_t* plan;
   int32_t* err;
 };
@@ -42,7 +43,8 @@ static bool share_always() {
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
     kv_prefix_plan_kernel(const PlanArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t sums[kPlanThreads / 32];
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ int64_t sums[3][kWarps];
   int32_t *common = sm, *first = common + a.NG, *shortest = first + a.NG, *live = shortest + a.NG,
           *starts = live + a.NG, *row_entry = starts + a.NG + 1;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -80,15 +82,6 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     else if (lead && a.err) atomicOr(a.err, SPEC_DERR_BAD_SLOT);
   }
   __syncthreads();
-  auto total = [&](int64_t x) {  // of all threads
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) sums[tid >> 5] = x;
-    __syncthreads();
-    x = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) x += sums[w];
-    return x;
-  };
   auto group_of = [&](int i) {  // the last group that starts at or before entry i
     int lo = 0, hi = a.NG - 1;
     while (lo < hi) {
@@ -166,7 +159,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 
   // What the groups share, in tiles, and what that saves. common[] holds it from here on.
   const int R = a.T * a.G;
-  int64_t saved = 0;
+  int64_t saved = 0, units_of = 0;
+  int item = 0;
   for (int g = tid; g < a.NG; g += kPlanThreads) {
     const int tiles = bad || !a.could || live[g] < 2 ? 0
                                          : int(int64_t(min(common[g], shortest[g] / a.bs)) * a.bs /
@@ -174,10 +168,36 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int64_t gain =
         tiles == 0 ? 0 : pf_alone(live[g], tiles, R) - pf_shared(live[g], starts[g + 1] - starts[g], tiles, R);
     common[g] = a.always || gain > 0 ? tiles : 0;
-    if (gain > 0) saved += gain;
+    if (gain > 0) {
+      const int64_t nq = int64_t(starts[g + 1] - starts[g]) * R;
+      saved += gain;
+      units_of += pf_units(nq, tiles);
+      item = max(item, int(pf_item_units(nq > 128 ? kPfTwoUnits : kPfOneUnits, tiles)));
+    }
   }
-  saved = total(saved);
-  const bool share = a.always || saved * a.H > kPfLeast;
+  bool share = a.always;
+  if (a.could && !a.always) {
+    auto sum_of = [](int64_t x) {  // of a warp
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      return x;
+    };
+    saved = sum_of(saved);
+    units_of = sum_of(units_of);
+    item = __reduce_max_sync(0xffffffffu, item);
+    if (lane == 0) {
+      sums[0][tid >> 5] = saved;
+      sums[1][tid >> 5] = units_of;
+      sums[2][tid >> 5] = item;
+    }
+    __syncthreads();
+    static_assert(kWarps == 32, "a lane for each");
+    saved = sum_of(sums[0][lane]) * a.H;
+    units_of = sum_of(sums[1][lane]) * a.H;
+    item = __reduce_max_sync(0xffffffffu, int(sums[2][lane]));
+    share = saved > kPfLeast + pf_pieces(item, units_of, a.per);
+  }
+  __syncthreads();  // common[], and sums have been read
   auto shared_tiles = [&](int g) { return share ? common[g] : 0; };
 
   for (int b = tid; b < a.B; b += kPlanThreads) {
@@ -197,7 +217,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   }
 
   // units, and their sums from group to group: each thread some consecutive ones
-  const int per = (a.NG + kPlanThreads - 1) / kPlanThreads;
+  const int mine = (a.NG + kPlanThreads - 1) / kPlanThreads;
   auto entry = [&](int e) -> int64_t {
     const int tiles = shared_tiles(e);
     const int s0 = bad ? 0 : starts[e], many = bad ? 0 : starts[e + 1] - s0;
@@ -205,8 +225,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     return a.H * pf_units(int64_t(many) * R, tiles);
   };
   int64_t sum = 0;
-  for (int x = 0; x < per; ++x) {
-    const int e = tid * per + x;
+  for (int x = 0; x < mine; ++x) {
+    const int e = tid * mine + x;
     if (e >= a.NG) break;
     prefix[e] = sum;  // of this thread's so far
     sum += entry(e);
@@ -217,12 +237,11 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
-  __syncthreads();  // (total's readers of sums)
-  if (lane == 31) sums[tid >> 5] = inc;
+  if (lane == 31) sums[0][tid >> 5] = inc;
   __syncthreads();
-  for (int w = 0; w < (tid >> 5); ++w) inc += sums[w];
-  for (int x = 0; x < per; ++x) {
-    const int e = tid * per + x;
+  for (int w = 0; w < (tid >> 5); ++w) inc += sums[0][w];
+  for (int x = 0; x < mine; ++x) {
+    const int e = tid * mine + x;
     if (e >= a.NG) break;
     prefix[e] += inc - sum;
   }
@@ -259,6 +278,7 @@ int launch_kv_prefix_plan(const KvPrefixPlanLaunch& k) {
   a.MB = k.max_blocks;
   a.always = share_always();
   a.could = a.always || pf_could(a.B, a.MB, a.bs, a.T * a.G, a.H);
+  a.per = pf_join_queries(int64_t(a.B) * a.H, a.T * a.G, kPfSms);
   a.plan = static_cast<uint8_t*>(k.plan);
   a.err = k.err;
   const size_t smem = (5 * size_t(a.NG) + 1 + a.B) * 4;
@@ -279,7 +299,7 @@ size_t kv_prefix_plan_size(int B, int num_groups, int num_members) {
 // come by two. Then the queries follow one by one, the lanes over the head's numbers. (Found for
 // one query at a time, this was most of 750 instructions a query.) Bound by those that are left
 // and by memory: 23 us for 40960 queries of 128 numbers.
-constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32, kPfJoinQueries = 8;
+constexpr int kPfJoinThreads = 256, kPfJoinWarps = kPfJoinThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kPfJoinThreads) kv_prefix_join_kernel(const PfArgs a, int ctas, int per) {
@@ -518,12 +538,8 @@ int launch_kv_prefix_attention(const Q8AttnLaunch& k, const void* plan, size_t p
   const int sr = launch_kv_q8_attention(rows);
   if (sr != SPEC_OK) return sr;
   cudaStream_t stream = static_cast<cudaStream_t>(k.stream);
-  // as few queries a warp as all warps can take at once (32 on each SM), in equal chunks
-  const int R = a.T * a.G;
-  const int64_t at_once = int64_t(sms) * 32, each = (int64_t(a.B) * a.H * R + at_once - 1) / at_once;
-  int per = each < 1 ? 1 : each > kPfJoinQueries ? kPfJoinQueries : int(each);
+  const int R = a.T * a.G, per = pf_join_queries(int64_t(a.B) * a.H, R, sms);
   const int chunks = (R + per - 1) / per;
-  per = (R + chunks - 1) / chunks;
   const int64_t warps = int64_t(a.B) * a.H * chunks;
   const dim3 grid(unsigned((warps + kPfJoinWarps - 1) / kPfJoinWarps));
   return a.D == 128

@@ -7,7 +7,7 @@ import torch
 
 import speculative_decoding_verification_sample_gb300 as sv
 from tests import q8_helpers as h
-from tests.test_gpu_prefix import _run, _small, check, plan_of, share  # noqa: F401
+from tests.test_gpu_prefix import _run, _small, check, grouped, plan_of, share  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,38 @@ def test_waits_run_out_with_products_in_flight(monkeypatch, D, T, groups):
         out = _run(dq, pool, scales, bt, L, plan, err_flag=err)
         assert int(err) == 0
         check(out, q, pool, scales, bt, L)
+
+
+@pytest.mark.parametrize("T,G,H,D,groups,forks,tiles,shared", [
+    # measured row by row and shared, us
+    (1, 8, 1, 128, 1, 32, 256, False),    # 50, 136: one item cut over all CTAs
+    (1, 8, 1, 128, 2, 16, 256, False),    # 49, 84
+    (1, 8, 1, 128, 1, 256, 24, False),    # 42, 58
+    (1, 4, 8, 128, 1, 64, 12, False),     # 44, 56
+    (5, 4, 1, 128, 1, 32, 256, False),    # 58, 76
+    (5, 4, 8, 128, 8, 16, 8, False),      # 86, 96
+    (5, 4, 8, 128, 8, 16, 32, True),      # 176, 140
+    (5, 4, 8, 128, 1, 16, 32, False),     # 42, 55
+    (5, 4, 8, 128, 1, 16, 256, True),     # 156, 106
+    (5, 4, 8, 128, 1, 256, 2, False),     # 94, 135
+    (5, 4, 8, 128, 1, 256, 24, True),     # 262, 183
+    (16, 8, 8, 128, 8, 2, 8, False),      # 58, 74
+    (16, 8, 8, 128, 8, 2, 64, True),      # 167, 139
+    (8, 8, 8, 64, 2, 128, 32, True),      # 581, 370
+])
+def test_what_pays(monkeypatch, T, G, H, D, groups, forks, tiles, shared):
+    """On both sides of where sharing pays: outputs with the bytes of kv_q8_attention's where it
+    does not."""
+    monkeypatch.delenv("SPECVERIFY_SHARE")
+    rng = np.random.default_rng(30)
+    L, bt, starts, members, nb = grouped(rng, [(128 * tiles, forks)] * groups, (10, 300), 0, 16, T)
+    g = torch.Generator(device="cuda").manual_seed(30)
+    shape = (nb, 1, 2, H)
+    pool = (torch.randn((*shape, 16, D), device="cuda", generator=g) * 64).to(torch.float8_e4m3fn)
+    scales = torch.exp2(torch.randint(-7, -4, shape, device="cuda", generator=g).float())
+    q = torch.randn((len(L), T, H * G, D), device="cuda", generator=g).bfloat16()
+    args = q, pool, scales, h.i32(bt), h.i32(L)
+    out, rows = torch.empty_like(q), torch.empty_like(q)
+    sv.kv_q8_prefix_attention(*args, plan_of(bt, L, starts, members, T, G * H, H, 16, nb), out)
+    sv.kv_q8_attention(*args, rows)
+    assert torch.equal(out, rows) != shared
