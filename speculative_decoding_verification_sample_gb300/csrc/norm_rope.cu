@@ -77,8 +77,8 @@ __device__ __forceinline__ uint64_t turn_fraction(float w) {
 }
 
 // cos and sin of p * (fraction of a turn), times f.
-__device__ __forceinline__ float2 turned(uint64_t fraction, int p, float f) {
-  const uint64_t a = fraction * static_cast<uint64_t>(int64_t(p));
+__device__ __forceinline__ float2 turned(uint64_t fraction, int64_t p, float f) {
+  const uint64_t a = fraction * static_cast<uint64_t>(p);
   // to the nearest quarter turn, and what is left of it, at most an eighth of a turn
   const uint64_t b = a + (uint64_t(1) << 61);
   const uint32_t quarter = uint32_t(b >> 62);
@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kNrThreads, kNrCtas) norm_rope_kernel(const No
   float4* weights = reinterpret_cast<float4*>(fractions + (a.half + 1) / 2 * 2);
   float4* table = weights + a.D / 2;
   const int32_t* pos = a.pos ? a.pos + int64_t(b) * a.T + t0 : nullptr;
-  auto position = [&](int t) { return pos ? pos[t] : L + t0 + t; };
+  // (in 64 bits: the tokens after a length near the largest int are past it)
+  auto position = [&](int t) -> int64_t { return pos ? pos[t] : int64_t(L) + t0 + t; };
   for (int i = tid; i < a.half; i += kNrThreads) fractions[i] = turn_fraction(a.freq[i]);
   if constexpr (N > 1) {
     // by quarters of what a lane needs of them: the lanes of a head read side by side
