@@ -266,7 +266,8 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
 static int check_norm_rope(const sv::NormRopeLaunch& r, int tokens) {
   const int eb = elem_bytes(r.dtype);
   if (!r.q || !r.q_out || eb == 0 || r.B < 1 || r.T < 1 || r.Hq < 1 || r.H < 0) return SPEC_EINVAL;
-  if (r.D < 2 || r.D % 2 != 0 || r.half < 0 || 2 * r.half > r.D || (r.half > 0) != (r.inv_freq != nullptr))
+  if (r.D < 2 || r.D % 2 != 0 || r.half < 0 || r.half > r.D / 2 ||
+      (r.half > 0) != (r.inv_freq != nullptr))
     return SPEC_EINVAL;
   if (!(r.eps >= 0.0f) || std::isinf(r.eps) || !std::isfinite(r.factor)) return SPEC_EINVAL;
   if (!r.seq_lens && (!r.positions || r.pool)) return SPEC_EINVAL;
