@@ -627,7 +627,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const float scale = t.vs[part];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t r[8];
-        if (plain) {
+        // a code that is no number (all ones but the sign) would become 480 below
+        uint32_t none = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) none |= (w[y] & 0x7f7f7f7fu) + 0x01010101u;
+        if (plain && !(none & 0x80808080u)) {
           // the product with scale * 2^120 is exact
           const uint32_t up = ((__float_as_uint(scale) >> 23) + 120 << 7) * 0x00010001u;
 #pragma unroll

@@ -6,8 +6,9 @@ import pytest
 import torch
 
 import speculative_decoding_verification_sample_gb300 as sv
+from oracle import q8
 from tests import q8_helpers as h
-from tests.test_gpu_prefix import _run, _small, check, grouped, plan_of, share  # noqa: F401
+from tests.test_gpu_prefix import _run, _small, bound, check, grouped, plan_of, share  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,27 @@ def test_what_pays(monkeypatch, T, G, H, D, groups, forks, tiles, shared):
     sv.kv_q8_prefix_attention(*args, plan_of(bt, L, starts, members, T, G * H, H, 16, nb), out)
     sv.kv_q8_attention(*args, rows)
     assert torch.equal(out, rows) != shared
+
+
+@pytest.mark.parametrize("plain", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_that_are_no_numbers(D, plain):
+    """A NaN code among the shared values: that number of the outputs is NaN, as from
+    kv_q8_attention, whatever the tile's scales are; the other codes of its tile are as ever."""
+    _, L, bt, starts, members, nb, pool, scales, q, dq = _small(23, D=D)
+    if not plain:
+        scales[:, 0, 1] *= 1.5
+    a, b = members[0], members[3]
+    pool[bt[a, 2], 0, 1, 0, 5, 17] = 0x7f
+    pool[bt[a, 3], 0, 1, 1, 0, D - 1] = 0xff
+    pool[bt[b, 1], 0, 1, 1, 15, 0] = 0xff
+    out = _run(dq, pool, scales, bt, L, plan_of(bt, L, starts, members, 4, 8, 2, 16, nb))
+    want, spread, reach = q8.attention(q, pool, scales, bt, L)
+    got, nan = out.double().cpu().numpy(), np.isnan(want)
+    assert nan.any() and np.array_equal(np.isnan(got), nan)
+    # code * scale is rounded to bf16 where the scale is no power of two: once more 2^-8
+    lim = bound(want, spread, reach, D) + (0 if plain else 2.0 ** -8 * spread)
+    assert (np.abs(got - want) <= lim)[~nan].all()
+    rows = torch.empty_like(dq)
+    sv.kv_q8_attention(dq, h.dev_pool(pool), h.dev_scales(scales), h.i32(bt), h.i32(L), rows)
+    assert np.array_equal(torch.isnan(rows).cpu().numpy(), nan)
