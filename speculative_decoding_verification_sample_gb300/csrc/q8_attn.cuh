@@ -34,14 +34,14 @@ constexpr int kAttnTile = 128;
 
 // A plan of shared prefixes (kv_prefix.cuh): what it was made for, from byte 256 its rows, then
 // the groups, their units from group to group, and the list of members.
-struct PrefixHeader {
+struct alignas(16) PrefixHeader {
   int32_t magic, B, T, G, H, bs, MB, NG, NE;
   int64_t units;
   int32_t pad[52];
 };
 static_assert(sizeof(PrefixHeader) == 256, "the rows follow it");
 constexpr int32_t kPrefixMagic = 0x70667832;
-struct PrefixRow {
+struct alignas(16) PrefixRow {
   int32_t L, n;       // as the plan found them
   int32_t skip;       // tiles that the row shares: those of its group, else 0
   int32_t group, at;  // group (skip 0: -1) and the row's place among its members
@@ -61,13 +61,18 @@ __host__ __device__ inline PrefixLayout prefix_layout(int B, int NG, int NE) {
   l.bytes = (l.members + size_t(NE) * 4 + 255) / 256 * 256;
   return l;
 }
-// Whether a plan of `bytes` was made for such calls (at least a header).
+// Whether a plan of `bytes` was made for such calls (at least a header). The header is read in
+// three loads that wait for nothing, and nothing waits for a part of the answer: one comparison
+// after the other took a plan that shares nothing from 90 to 107 us (130 rows, 8 kv heads).
 __device__ __forceinline__ bool prefix_fits(const uint8_t* plan, size_t bytes, int B, int T, int G,
                                             int H, int bs, int MB) {
-  const PrefixHeader* h = reinterpret_cast<const PrefixHeader*>(plan);
-  return h->magic == kPrefixMagic && h->B == B && h->T == T && h->G == G && h->H == H &&
-         h->bs == bs && h->MB == MB && h->NG >= 0 && h->NE >= 0 && h->NG <= (1 << 20) &&
-         h->NE <= (1 << 20) && prefix_layout(B, h->NG, h->NE).bytes <= bytes;
+  const int4* h = reinterpret_cast<const int4*>(plan);
+  const int4 x = h[0], y = h[1];      // magic, B, T, G; H, bs, MB, NG
+  const int NE = h[2].x;
+  const int other = (x.x ^ kPrefixMagic) | (x.y ^ B) | (x.z ^ T) | (x.w ^ G) | (y.x ^ H) | (y.y ^ bs) |
+                    (y.z ^ MB);
+  const bool sizes = (uint32_t(y.w) <= 1u << 20) & (uint32_t(NE) <= 1u << 20);
+  return (other == 0) & sizes & (prefix_layout(B, y.w, NE).bytes <= bytes);
 }
 __device__ __forceinline__ const PrefixRow* prefix_row(const uint8_t* plan, int b) {
   return reinterpret_cast<const PrefixRow*>(plan + sizeof(PrefixHeader)) + b;
@@ -129,9 +134,9 @@ __device__ __forceinline__ RowSpan row_span(const Args& a, int b) {
   int skip = 0;
   if constexpr (Args::kPlan) {
     // lengths that changed since the plan was made: the row's keys are not the plan's
-    const PrefixRow* r = prefix_row(a.plan, b);
-    s.bad = s.bad || r->L != s.L || r->n != s.n || !plan_fits(a);
-    skip = r->skip;
+    const int4 r = *reinterpret_cast<const int4*>(prefix_row(a.plan, b));
+    s.bad = s.bad | (r.x != s.L) | (r.y != s.n) | !plan_fits(a);
+    skip = r.z;
   }
   if (s.bad || s.n == 0) {
     s.end = s.tiles = s.sink_tiles = s.win_tile = 0;
