@@ -56,27 +56,28 @@ __host__ __device__ inline int64_t pf_units(int64_t nq, int64_t tiles) {
 // The estimate by which the plan shares, in 10 ns of an SM for each kv head. What a row costs
 // either way (its item of kv_q8_attention's kernel, 1 to 6 us with its change) is not in it.
 //
-// Fitted to 7500 measured pairs of times, the same call with a plan that shares nothing and with
+// Fitted to 7502 measured pairs of times, the same call with a plan that shares nothing and with
 // all shared: 2 to 256 rows in 1 to 8 groups, 2 to 256 tiles in common, 1 to 16 kv heads of 64 and
-// 128 numbers, 1 to 128 queries a row and kv head. The estimate's way is more than 5 % slower than
-// the other in 2.2 % of them and 1.19 times as slow at most. (A price of 0.60 us a tile, changes
-// of items included, and none for the join's further pieces: 3.6 %, and 2.7 times.) Of them, with
-// 8 kv heads of 128, row by row and shared, us:
+// 128 numbers, 1 to 128 queries a row and kv head. The way taken is more than 5 % slower than the
+// other in 2.5 % of them; with heads of 128 at most 1.14 times, with heads of 64, for which the
+// plan shares late (it is not told of them), 1.30. (A price of 0.60 us a tile, changes of items
+// included, and none for the join's further pieces: 4.8 %, 2.9 times.) Some of them, with 8 kv
+// heads of 128, row by row and shared, us:
 //
-//   queries  rows     4 tiles        8       16       32       64      128      256
-//      4     1 x 16    23, 37   25, 38   28, 41   36, 45   49, 47   81, 56  134, 68
-//     20     1 x 16    28, 44   30, 49   33, 50   42, 55   59, 61   93, 75  156, 106
-//     20     8 x 16    69, 93   86, 96  116, 105 176, 140 309, 195
-//     64     8 x 8     68, 113  85, 113 117, 135 179, 157 302, 217 550, 330
-//    128     8 x 16   177, 298 239, 324 356, 392 600, 496
+//   queries  rows     4 tiles        8       16       24       32       64      128      256
+//      4     1 x 16    21, 34   22, 35   25, 38   28, 39   32, 40   45, 45   79, 57  130, 68
+//     20     1 x 16    25, 41   26, 45   32, 46   33, 52   40, 52   56, 57   84, 76  146, 110
+//     20     8 x 16    64, 90   76, 93  101, 107 133, 132 163, 148 289, 210
+//     64     8 x 8     63, 108  81, 109 113, 128 144, 142 175, 152 298, 212 544, 324
+//    128     8 x 16   175, 283 236, 311 357, 377 479, 432 598, 485
 //
 // kPfTile keys of one row, with the columns that its queries take in kv_q8_attention's kernel.
 __host__ __device__ inline int pf_tile_price(int columns) {
   return columns <= 8    ? 52
-         : columns <= 16 ? 54
-         : columns <= 24 ? 60
-         : columns <= 32 ? 68
-         : columns <= 48 ? 83
+         : columns <= 16 ? 55
+         : columns <= 24 ? 57
+         : columns <= 32 ? 67
+         : columns <= 48 ? 79
                          : 115;
 }
 // What `tiles` tiles of `rows` rows with R queries each cost row by row: blocks of up to 64.
@@ -84,20 +85,20 @@ __host__ __device__ inline int64_t pf_alone(int64_t rows, int64_t tiles, int R) 
   const int blocks = (R + 63) / 64;
   return rows * tiles * blocks * pf_tile_price((R + blocks - 1) / blocks);
 }
-// The same shared: the units, 0.31 us each, and the parts and their join, 0.1 us a query.
+// The same shared: the units, 0.32 us each, and the parts and their join, 0.13 us a query.
 __host__ __device__ inline int64_t pf_shared(int64_t rows, int64_t many, int64_t tiles, int R) {
-  return 31 * pf_units(many * R, tiles) + rows * R * 10;
+  return 32 * pf_units(many * R, tiles) + rows * R * 13;
 }
-// What the kernels cost once they find work, whatever it is: 19.4 us of all SMs (kPfSms of them).
+// What the kernels cost once they find work, whatever it is: 27 us of all SMs (kPfSms of them).
 constexpr int kPfSms = 152;
-constexpr int64_t kPfLeast = int64_t(1940) * kPfSms;
-// And what the join waits for where few items are cut over many CTAs: 0.41 us for each piece
+constexpr int64_t kPfLeast = int64_t(2700) * kPfSms;
+// And what the join waits for where few items are cut over many CTAs: 0.25 us for each piece
 // beyond two and query of a warp. `item`: units of the longest item, `units`: of all.
 __host__ __device__ inline int64_t pf_pieces(int64_t item, int64_t units, int per) {
   const int64_t all = item * (units < kPfSms ? units : kPfSms);
   if (all < 2 * units || units == 0) return 0;
   const int64_t each = all >> 32 == 0 ? int64_t(uint32_t(all) / uint32_t(units)) : all / units;
-  return 41 * kPfSms * (each - 1) * per;
+  return 25 * kPfSms * (each - 1) * per;
 }
 // Queries of a warp of the join: as few as all warps can take at once (32 on each SM), in equal
 // chunks of a row and kv head's.
