@@ -8,7 +8,9 @@ candidates begin with the prompt's likeliest tokens. Every step:
     kv_reserve              blocks for the K + 1 provisional tokens of each row
     kv_q8_norm_rope_append  norms and positions of queries and keys, keys and values to the cache
     kv_prefix_plan          which rows begin with the same blocks (once for all layers)
-    kv_q8_prefix_attention  each prompt's blocks read once for all of its candidates
+    kv_q8_prefix_attention  each prompt's blocks read once for all of its candidates, where that
+                            saves time: not for the few short rows here (SPECVERIFY_SHARE=1, a
+                            test knob, shares them all the same)
     spec_verify_greedy      the drafts against the target's logits
     kv_commit_inplace       the accepted length; blocks past it go back to the free stack
 
