@@ -8,7 +8,8 @@ import torch
 import speculative_decoding_verification_sample_gb300 as sv
 from oracle import q8
 from tests import q8_helpers as h
-from tests.test_gpu_prefix import _run, _small, bound, check, grouped, plan_of, share  # noqa: F401
+from tests.test_gpu_prefix import (_run, _small, bound, check, grouped, plan_of, queries,
+                                   share)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +93,18 @@ def test_values_that_are_no_numbers(D, plain):
     rows = torch.empty_like(dq)
     sv.kv_q8_attention(dq, h.dev_pool(pool), h.dev_scales(scales), h.i32(bt), h.i32(L), rows)
     assert np.array_equal(torch.isnan(rows).cpu().numpy(), nan)
+
+
+def test_the_largest_lists():
+    """8192 rows in pairs, each pair with a tile in common, and one group of them all."""
+    rng = np.random.default_rng(24)
+    L, bt, starts, members, nb = grouped(rng, [(128, 2)] * 4096, (0, 20), 0, 16, 1)
+    pool, scales = h.cache(rng, nb, 1, 1, 16, 64, spread=1)
+    q, dq = queries(rng, len(L), 1, 2, 64)
+    some = rng.permutation(len(L))[:200]
+    for st in (starts, [0, len(L)]):
+        err = h.i32([0])
+        plan = plan_of(bt, L, st, members, 1, 2, 1, 16, nb, err=err)
+        out = _run(dq, pool, scales, bt, L, plan, err_flag=err)
+        assert int(err) == 0
+        check(out[torch.from_numpy(some).cuda()], q[some], pool, scales, bt[some], L[some])
