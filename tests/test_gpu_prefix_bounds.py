@@ -108,3 +108,14 @@ def test_the_largest_lists():
         out = _run(dq, pool, scales, bt, L, plan, err_flag=err)
         assert int(err) == 0
         check(out[torch.from_numpy(some).cuda()], q[some], pool, scales, bt[some], L[some])
+
+
+def test_tables_wider_than_their_rows():
+    """Entries that no row reaches change nothing, in whichever chunks of the tables they lie."""
+    _, L, bt, starts, members, nb, pool, scales, q, dq = _small(25, groups=((9000, 3), (300, 2)))
+    want = _run(dq, pool, scales, bt, L, plan_of(bt, L, starts, members, 4, 8, 2, 16, nb))
+    check(want, q, pool, scales, bt, L)
+    for more, fill in ((1, -1), (255, nb + 9), (70000, -1)):
+        wide = np.concatenate([bt, np.full((len(L), more), fill)], 1)
+        out = _run(dq, pool, scales, wide, L, plan_of(wide, L, starts, members, 4, 8, 2, 16, nb))
+        assert torch.equal(out, want)
