@@ -430,17 +430,19 @@ int kv_q8_append(const void* k, const void* v, int dtype, void* kv_pool, float* 
  *   interleaved  0: pair i is (i, i + num_pairs); else (2 i, 2 i + 1)
  *   rope_factor  position p turns pair i by p * inv_freq[i]: (a, b) -> rope_factor *
  *                (a cos - b sin, b cos + a sin). Scalings for long contexts are a choice of
- *                inv_freq and rope_factor. Angles are exact to 2^-54 turns a position and
- *                2^-25 of an eighth turn, however far the position; an |inv_freq| that is
- *                not finite counts as 0
- *   seq_lens     [B] int32: token t of row b is at position seq_lens[b] + t
+ *                inv_freq and rope_factor. Angles are exact to 2^-53 turns a position (times
+ *                |inv_freq| where that is above 1) and 2^-25 of an eighth turn, however far
+ *                the position; an |inv_freq| that is not finite, or above 2^55, counts as 0
+ *   seq_lens     [B] int32: token t of row b is at position seq_lens[b] + t (which may pass
+ *                2^31 - 1)
  *   positions    optional [B, T] int32 instead (a draft tree's: seq_lens[b] + depth);
  *                seq_lens may then be null
  *   num_new      optional [B] int32: tokens t >= num_new[b] are neither read nor written
  *   head_dim     even, up to 256
- * Everything is computed in fp32 and rounded once. Any strides and addresses that are
- * multiples of the element size do; 16-byte (else 8-byte) ones with num_pairs a multiple of a
- * vector's numbers take vector loads. Device errors: SPEC_DERR_BAD_LENGTH (a negative length,
+ * Everything is computed in fp32 and rounded once (the sum of squares too: numbers beyond 2^60
+ * make it infinite and their head zeros, numbers below 2^-75 count as 0 in it). Any strides and
+ * addresses that are multiples of the element size do; 16-byte (else 8-byte) ones with num_pairs
+ * a multiple of a vector's numbers take vector loads. Device errors: SPEC_DERR_BAD_LENGTH (a negative length,
  * num_new outside [0, T]: that row is not written).
  */
 int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int dtype,
@@ -460,6 +462,10 @@ int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_strid
  *   kv_pool, kv_scales, block_table, layer: as kv_q8_append. head_dim a multiple of 16
  *   seq_lens     [B] int32, not changed: the tokens' places in the cache, and their positions
  *                for the rotation unless `positions` is given
+ * A CTA holds the angles of a block's new tokens, up to 64 KB of them: with more than 8192 /
+ * num_pairs new tokens in a block (128 of a fully turned head of 128) the call takes the numbers
+ * one by one, about ten times as long (12 prompts of up to 4099 tokens: 0.17 ms with blocks of 16
+ * tokens, 0.38 with 128, 1.6 with 256).
  * Device errors: those of kv_q8_append; a row with invalid lengths is not written, q_out
  * included; a bad block concerns its keys and values only.
  */
@@ -533,8 +539,10 @@ size_t kv_q8_attention_workspace_bytes(int T, int num_q_heads, int num_kv_heads,
  * A group shares the blocks that the tables of its rows (those with new tokens) have in
  * common from the start, as kv_fork leaves them, as far as all of them have committed tokens
  * there, in whole tiles of 128 positions; a group that has nothing in common shares nothing.
- * So groups may be a guess: they change the time only, never the result. And it shares only
- * where that saves time by an estimate: long prefixes of many rows.
+ * So groups may be a guess: they change the time, and of the result no more than the roundings
+ * that kv_q8_prefix_attention tells of. And it shares only where that saves time by an estimate
+ * (with heads of 128: 16 rows of 5 tokens and 32 heads behind 13 thousand common tokens, 256 rows
+ * behind 2 thousand).
  * Device errors: SPEC_DERR_BAD_SLOT: a row out of range, or listed again (that entry is passed
  * over), or group_starts that are not ascending within [0, num_members] (nothing is shared).
  * B, num_groups, num_members <= 8192, T <= 32 (SPEC_ENOTSUP).
@@ -556,13 +564,17 @@ size_t kv_prefix_plan_bytes(int B, int num_groups, int num_members);
  *                size. A row whose lengths are not the plan's gets NaN and
  *                SPEC_DERR_BAD_LENGTH; with a plan of other sizes all do, and SPEC_DERR_BAD_SLOT
  *                (calls whose tables are too short to share anything do not look at it)
+ *   block_table  as wide as the rows may need, no wider: by its width the call sees whether
+ *                it can share at all, and is kv_q8_attention's where not. A plan that shares
+ *                nothing costs 6 to 30 us more than that
  *   workspace    kv_q8_prefix_attention_workspace_bytes bytes, 256-byte aligned, no
- *                initialisation; calls that share one must be ordered on the device
+ *                initialisation; calls that share one must be ordered on the device. Mostly
+ *                two fp32 parts of each output, whether anything is shared or not
  * Everything else is as in kv_q8_attention, which takes the rows' own keys. Shared keys: queries
  * as there in two e4m3 terms, against the keys' codes; probabilities are rounded to bf16
  * against values in bf16 (exact with scales that are powers of two between 2^-100 and 2^7;
  * others round code * scale to bf16); scores, maxima, sums and outputs up to the last rounding
- * are fp32. A value's NaN code counts as 480 there (kv_q8_append leaves none). Nothing is shared
+ * are fp32; values up to 2^103 cannot overflow the sums of 2^24 keys. Nothing is shared
  * with fp32 queries, head sizes but 64 and 128, and blocks that are not 16, 32, 64 or a multiple
  * of 128 tokens. The result does not depend on timing, but on the groups in its roundings.
  */

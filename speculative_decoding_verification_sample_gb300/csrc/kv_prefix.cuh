@@ -85,7 +85,7 @@ __host__ __device__ inline int64_t pf_alone(int64_t rows, int64_t tiles, int R) 
   const int blocks = (R + 63) / 64;
   return rows * tiles * blocks * pf_tile_price((R + blocks - 1) / blocks);
 }
-// The same shared: the units, 0.32 us each, and the parts and their join, 0.13 us a query.
+// The same shared: the units, 0.32 us each by the fit, the parts and their join 0.13 us a query.
 __host__ __device__ inline int64_t pf_shared(int64_t rows, int64_t many, int64_t tiles, int R) {
   return 32 * pf_units(many * R, tiles) + rows * R * 13;
 }

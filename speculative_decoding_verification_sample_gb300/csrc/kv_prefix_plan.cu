@@ -4,9 +4,9 @@
 // the list of members (the first, if one is listed twice), the groups' first rows and
 // shortest lengths, and compares its share of the tables with those of the first rows;
 // the first CTA takes the first differences from all and sums up the units. Where tables are too
-// short to share anything by the estimate it only looks at the lists. Bound by
-// latency, and for many long tables by reading them (B x max_blocks entries once): 9 us for 4
-// rows, 18 us for 256 rows that share 1000 blocks.
+// short to share anything by the estimate it only looks at the lists. Bound by latency, and for
+// many long tables by reading them (as far as the rows reach, once): in a graph 3.7 us for lists
+// alone, 8 us for 130 rows, 13 us for 256 rows that share 1000 blocks.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -62,8 +62,9 @@ __host__ __device__ inline PrefixLayout prefix_layout(int B, int NG, int NE) {
   return l;
 }
 // Whether a plan of `bytes` was made for such calls (at least a header). The header is read in
-// three loads that wait for nothing, and nothing waits for a part of the answer: one comparison
-// after the other took a plan that shares nothing from 90 to 107 us (130 rows, 8 kv heads).
+// three loads that wait for nothing, and nothing waits for a part of the answer. (One comparison
+// after the other, with a plan that shares nothing the kernel took 107 instead of 96 us for 130
+// rows of 8 kv heads; without a plan it takes 90.)
 __device__ __forceinline__ bool prefix_fits(const uint8_t* plan, size_t bytes, int B, int T, int G,
                                             int H, int bs, int MB) {
   const int4* h = reinterpret_cast<const int4*>(plan);
